@@ -15,14 +15,12 @@
 #include <unordered_map>
 #include <vector>
 
-#include "../../include/tok.h"
-#include "tok_common.cuh"
+#include "tok_handle.cuh"
 
 using namespace tokgb;
 
 namespace {
 
-constexpr int N_STAGES = 3;
 const char* kStageNames[N_STAGES] = {"k_boundaries", "k_bpe_engine", "k_emit"};
 
 thread_local std::string g_load_error;
@@ -33,69 +31,7 @@ struct ByteStringHash {
 
 }  // namespace
 
-constexpr unsigned long long kDefaultWaitNs = 4000000000ull;  // 4 s
-
-struct tok_handle {
-  int dev = 0;
-  int n_sms = 1;
-  int pattern = 0;
-  cudaStream_t stream = nullptr;
-  DevVocab v{};
-  // device allocations of the vocabulary
-  MergeEntry* d_table = nullptr;
-  int32_t* d_byte_id = nullptr;
-  uint16_t* d_tok_len = nullptr;
-  uint16_t* d_max_left = nullptr;
-  uint16_t* d_max_right = nullptr;
-  WholeEntry* d_whole = nullptr;
-  unsigned long long* d_whole_tail = nullptr;
-  uint64_t whole_tail_bytes = 0;
-  uint32_t* d_pair_bits = nullptr;
-  uint32_t n_whole = 0;
-  uint64_t hash = 0;
-  // workspace
-  Workspace ws{};
-  int32_t* d_out = nullptr;           // ids of host-side calls
-  long long* d_off = nullptr;         // token byte offsets of host-side calls (allocated on first use)
-  long long* d_items = nullptr;       // item starts of host-side batch calls
-  long long* d_item_off = nullptr;
-  uint64_t cap_items = 0;
-  DevStatus* h_status = nullptr;      // pinned
-  long long* h_ustatus = nullptr;     // pinned, written by the device: code, ids, UTF-8 error offset
-  long long* d_ustatus = nullptr;     // its device address
-  long long* h_items = nullptr;       // pinned
-  uint64_t cap_h_items = 0;
-  uint32_t epoch = 0;
-  std::string err;
-  int64_t err_off = -1;
-  uint32_t last_epoch = 0;            // epoch of the latest call
-  uint64_t launches = 0;
-  bool timing = false;
-  cudaEvent_t ev[N_STAGES + 1] = {};
-  float stage_ms[N_STAGES] = {};
-  bool have_times = false;
-  // test hook (tok_debug_fail_alloc): the allocation that fails, counted
-  // from 1 = the next one; 0 = none
-  uint32_t fail_alloc_in = 0;
-  // limit of a device-side wait (the grid barriers of the BPE kernel), and
-  // the test hook tok_debug_grid_wait: arrivals a grid barrier waits for
-  // beyond the CTAs that come
-  unsigned long long wait_ns = kDefaultWaitNs;
-  uint32_t grid_extra = 0;
-};
-
-namespace {
-
-struct DeviceGuard {
-  int prev = -1;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) == cudaSuccess && prev != dev) cudaSetDevice(dev);
-    else prev = -1;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
+namespace tokgb {
 
 int fail(tok_handle* h, int code, const std::string& msg) {
   if (h) h->err = msg;
@@ -106,6 +42,10 @@ int fail(tok_handle* h, int code, const std::string& msg) {
 int cuda_fail(tok_handle* h, cudaError_t e, const char* what) {
   return fail(h, TOK_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
+
+}  // namespace tokgb
+
+namespace {
 
 uint64_t fnv1a(uint64_t h, const void* p, size_t n) {
   const uint8_t* b = static_cast<const uint8_t*>(p);
@@ -118,37 +58,6 @@ uint64_t fnv1a(uint64_t h, const void* p, size_t n) {
 
 // group totals held for a workspace of nbch 512-byte chunks
 size_t gtot_cap(uint64_t nbch) { return (size_t)(nbch / CTOT_GROUP + 2); }
-
-template <class T>
-cudaError_t dalloc(T** p, size_t count) {
-  return cudaMalloc(reinterpret_cast<void**>(p), std::max<size_t>(count, 1) * sizeof(T));
-}
-
-// true when the handle's failure hook says this allocation is the one that
-// fails (it then stands in for a cudaMalloc that found the device full)
-bool injected_failure(tok_handle* h) {
-  return h->fail_alloc_in > 0 && --h->fail_alloc_in == 0;
-}
-
-// device allocation of a handle's buffers (workspace, items, offsets)
-template <class T>
-cudaError_t halloc(tok_handle* h, T** p, size_t count) {
-  if (injected_failure(h)) {
-    *p = nullptr;
-    return cudaErrorMemoryAllocation;
-  }
-  return dalloc(p, count);
-}
-
-// pinned host allocation of a handle's buffers
-template <class T>
-cudaError_t halloc_pinned(tok_handle* h, T** p, size_t count) {
-  if (injected_failure(h)) {
-    *p = nullptr;
-    return cudaErrorMemoryAllocation;
-  }
-  return cudaMallocHost(reinterpret_cast<void**>(p), std::max<size_t>(count, 1) * sizeof(T));
-}
 
 void free_workspace(tok_handle* h) {
   Workspace& w = h->ws;
@@ -551,6 +460,9 @@ int tok_load(const uint8_t* vocab_bytes, const uint64_t* vocab_off, uint32_t n_v
 
   tok_handle* h = new tok_handle();
   h->pattern = pattern;
+  h->vocab_bytes.assign(vocab_bytes + vocab_off[0], vocab_bytes + vocab_off[n_vocab]);
+  h->vocab_off.resize(n_vocab + 1);
+  for (uint32_t t = 0; t <= n_vocab; ++t) h->vocab_off[t] = vocab_off[t] - vocab_off[0];
   cudaError_t e = cudaGetDevice(&h->dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sms, cudaDevAttrMultiProcessorCount, h->dev);
   if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&h->stream, cudaStreamNonBlocking);
