@@ -38,7 +38,10 @@ SYMBOLS = ["tok_load", "tok_encode", "tok_encode_offsets", "tok_repair_append", 
            "tok_encode_offsets_device", "tok_encode_batch_device", "tok_pretokenize", "tok_pretokenize_batch",
            "tok_last_error", "tok_error_offset", "tok_content_hash", "tok_set_timing", "tok_stage_times",
            "tok_launch_count", "tok_free", "tok_pretokenize_device_noalloc", "tok_debug_fail_alloc",
-           "tok_debug_grid_wait"]
+           "tok_debug_grid_wait", "tok_paged_assign", "tok_paged_release", "tok_seen_bits", "tok_logits_process",
+           "tok_logits_backward", "tok_grammar_load", "tok_grammar_free", "tok_grammar_mask"]
+
+DTYPE_F32, DTYPE_F16, DTYPE_BF16 = 0, 1, 2   # tok.h TOK_F32, TOK_F16, TOK_BF16
 
 
 class TokError(RuntimeError):
@@ -46,6 +49,45 @@ class TokError(RuntimeError):
         super().__init__("%s: %s" % (_NAMES.get(code, code), msg))
         self.code = code
         self.offset = offset
+
+
+class _Args(ctypes.Structure):
+    """Arguments of one of the calls below: fields by keyword, device pointers
+    as ints (e.g. tensor.data_ptr()) or None.  A program may keep one and pass
+    it to every call; the buffers it names stay the caller's."""
+
+    def __init__(self, **fields):
+        super().__init__(**fields)
+        unknown = set(fields) - {n for n, _ in self._fields_}
+        if unknown:
+            raise TypeError("%s has no field %s" % (type(self).__name__, ", ".join(sorted(unknown))))
+        self._addr = ctypes.addressof(self)
+
+
+def _fields(text):
+    kinds = {"p": ctypes.c_void_p, "i64": ctypes.c_int64, "u64": ctypes.c_uint64, "u32": ctypes.c_uint32,
+             "i32": ctypes.c_int32}
+    return [(n, kinds[k]) for n, k in (f.split(":") for f in text.split())]
+
+
+class PagedArgs(_Args):
+    """tok_paged_args of include/tok.h."""
+    _fields_ = _fields("d_item_off:p d_ctx_len:p n:u32 block_size:u32 d_table:p table_stride:i64 max_blocks:u32 d_free:p "
+                       "d_n_free:p d_n_free_out:p d_slot:p d_pos:p d_req:p cap:u64 d_seq_len:p d_status:p")
+
+
+class LogitsArgs(_Args):
+    """tok_logits_args of include/tok.h."""
+    _fields_ = _fields("d_logits:p logits_stride:i64 d_out:p out_stride:i64 dtype:i32 rows:u32 n_logits:u32 d_seen:p "
+                       "seen_stride:i64 d_gen:p d_gen_start:p d_gen_len:p d_repetition:p d_frequency:p d_presence:p "
+                       "d_temperature:p d_bias_off:p d_bias_id:p d_bias:p d_mask:p mask_stride:i64 d_mask_row:p "
+                       "d_pick:p d_top:p d_lse:p d_logprob:p")
+
+
+class LogitsGradArgs(_Args):
+    """tok_logits_grad_args of include/tok.h."""
+    _fields_ = _fields("d_grad_out:p grad_out_stride:i64 d_grad_lse:p d_grad_logprob:p d_grad_logits:p "
+                       "grad_logits_stride:i64 d_grad_bias:p")
 
 
 _lib = None
@@ -93,9 +135,19 @@ def lib():
     L.tok_debug_grid_wait.restype = ctypes.c_int
     L.tok_free.argtypes = [P]
     L.tok_free.restype = None
+    L.tok_paged_assign.argtypes = [P, P, P]
+    L.tok_paged_release.argtypes = [P, P, P, U32, U32, P, ctypes.c_int64, U32, P, U64, P, P, P, P]
+    L.tok_seen_bits.argtypes = [P, P, P, U32, U32, P, ctypes.c_int64, ctypes.c_int, P]
+    L.tok_logits_process.argtypes = [P, P, P]
+    L.tok_logits_backward.argtypes = [P, P, P, P]
+    L.tok_grammar_load.argtypes = [P, I32P, U8P, U32, ctypes.POINTER(P)]
+    L.tok_grammar_mask.argtypes = [P, P, P, P, P, U32, ctypes.c_int32, P, U32, P, ctypes.c_int64, P]
+    L.tok_grammar_free.argtypes = [P]
+    L.tok_grammar_free.restype = None
     for fn in ("tok_load", "tok_encode", "tok_encode_offsets", "tok_repair_append", "tok_encode_batch", "tok_encode_device",
                "tok_encode_offsets_device", "tok_encode_batch_device", "tok_pretokenize", "tok_pretokenize_batch",
-               "tok_set_timing", "tok_stage_times"):
+               "tok_set_timing", "tok_stage_times", "tok_paged_assign", "tok_paged_release", "tok_seen_bits",
+               "tok_logits_process", "tok_logits_backward", "tok_grammar_load", "tok_grammar_mask"):
         getattr(L, fn).restype = ctypes.c_int
     _lib = L
     return L
@@ -294,6 +346,41 @@ class Tokenizer:
         self._check(self._L.tok_encode_batch_device(self._h, d_text, n_bytes, d_item_start, n_items, d_ids, cap,
                                                     d_item_off, d_status, stream or None))
 
+    # --- between the ids and a language model (device buffers) -----------
+    def paged_assign_device(self, args, stream=0):
+        """Blocks and slots of a batch's tokens in a paged cache (a PagedArgs)."""
+        rc = self._L.tok_paged_assign(self._h, args._addr, stream or None)
+        if rc:
+            self._check(rc)
+
+    def paged_release_device(self, d_seq_len, d_done, n, block_size, d_table, table_stride, max_blocks, d_free, free_cap,
+                             d_n_free, d_n_free_out, d_status, stream=0):
+        """The blocks of finished requests back on the stack of free blocks."""
+        rc = self._L.tok_paged_release(self._h, d_seq_len, d_done, n, block_size, d_table, table_stride, max_blocks,
+                                       d_free, free_cap, d_n_free, d_n_free_out, d_status, stream or None)
+        if rc:
+            self._check(rc)
+
+    def seen_bits_device(self, d_ids, d_item_off, n, n_logits, d_seen, seen_stride, keep=False, stream=0):
+        """The set of each item's ids, as rows of bits."""
+        rc = self._L.tok_seen_bits(self._h, d_ids, d_item_off, n, n_logits, d_seen, seen_stride, 1 if keep else 0,
+                                   stream or None)
+        if rc:
+            self._check(rc)
+
+    def process_logits_device(self, args, stream=0):
+        """Penalties, biases and masks on the next token's scores, with the
+        best token, the log-sum-exp and a log-probability (a LogitsArgs)."""
+        rc = self._L.tok_logits_process(self._h, args._addr, stream or None)
+        if rc:
+            self._check(rc)
+
+    def process_logits_backward_device(self, args, grad_args, stream=0):
+        """The gradient of process_logits_device (its LogitsArgs and a LogitsGradArgs)."""
+        rc = self._L.tok_logits_backward(self._h, args._addr, grad_args._addr, stream or None)
+        if rc:
+            self._check(rc)
+
     # --- introspection ---------------------------------------------------
     @property
     def content_hash(self):
@@ -313,3 +400,41 @@ class Tokenizer:
         if n < 0:
             self._check(n)
         return {names[k].decode(): float(ms[k]) for k in range(n)}
+
+
+class Grammar:
+    """A byte automaton over a tokenizer's vocabulary (a tok_grammar): next is
+    [n_states, 256], -1 where a byte is not allowed; accept is [n_states]."""
+
+    def __init__(self, tok, next_state, accept):
+        nxt = np.ascontiguousarray(next_state, dtype=np.int32)
+        acc = np.ascontiguousarray(accept, dtype=np.uint8)
+        if nxt.ndim != 2 or nxt.shape[1] != 256 or acc.shape != nxt.shape[:1]:
+            raise ValueError("next is [n_states, 256] and accept [n_states]")
+        g = ctypes.c_void_p()
+        self._tok, self._L, self._g = tok, tok._L, None   # (the tokenizer lives as long as its grammars)
+        tok._check(tok._L.tok_grammar_load(tok._h, nxt.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)),
+                                           acc.ctypes.data_as(ctypes.POINTER(ctypes.c_uint8)), nxt.shape[0],
+                                           ctypes.byref(g)))
+        self._g = g
+        self.n_states = nxt.shape[0]
+
+    def mask_device(self, d_state, d_ids, d_item_off, n, eos, d_state_out, n_logits, d_mask, mask_stride, stream=0):
+        """Walk rows' states over their tokens and write the masks of the
+        tokens that may follow (tok_grammar_mask)."""
+        rc = self._L.tok_grammar_mask(self._tok._h, self._g, d_state, d_ids, d_item_off, n, eos, d_state_out, n_logits,
+                                      d_mask, mask_stride, stream or None)
+        if rc:
+            self._tok._check(rc)
+
+    def close(self):
+        # (a tokenizer that was closed first has no device left to free on)
+        if self._g and getattr(self._tok, "_h", None):
+            self._L.tok_grammar_free(self._g)
+        self._g = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

@@ -475,6 +475,8 @@ int tok_load(const uint8_t* vocab_bytes, const uint64_t* vocab_off, uint32_t n_v
   if (e == cudaSuccess) e = dalloc(&h->d_whole_tail, tail.size());
   h->whole_tail_bytes = tail.size() * sizeof(unsigned long long);
   if (e == cudaSuccess) e = dalloc(&h->d_pair_bits, pair_bits.size());
+  if (e == cudaSuccess) e = dalloc(&h->d_done, 1);
+  if (e == cudaSuccess) e = cudaMemset(h->d_done, 0, sizeof(uint32_t));
   if (e == cudaSuccess)
     e = cudaMemcpy(h->d_pair_bits, pair_bits.data(), pair_bits.size() * sizeof(uint32_t), cudaMemcpyHostToDevice);
   if (e == cudaSuccess)
@@ -533,7 +535,7 @@ void tok_free(tok_handle* h) {
   if (h->stream) cudaStreamSynchronize(h->stream);
   free_workspace(h);
   void* ptrs[] = {h->d_table,  h->d_byte_id,     h->d_tok_len,   h->d_max_left, h->d_max_right, h->d_whole,
-                  h->d_whole_tail, h->d_pair_bits, h->d_items, h->d_item_off};
+                  h->d_whole_tail, h->d_pair_bits, h->d_items, h->d_item_off, h->d_done, h->d_tokens};
   for (void* p : ptrs)
     if (p) cudaFree(p);
   if (h->h_status) cudaFreeHost(h->h_status);

@@ -11,6 +11,17 @@
 #include "../../include/tok.h"
 #include "tok_common.cuh"
 
+namespace tokgb {
+
+// the vocabulary's bytes on the device: token t has bytes[off[t] .. off[t + 1])
+struct DevTokens {
+  const uint8_t* bytes;
+  const uint32_t* off;
+  uint32_t n;
+};
+
+}  // namespace tokgb
+
 constexpr int N_STAGES = 3;  // kernels of an encode
 
 constexpr unsigned long long kDefaultWaitNs = 4000000000ull;  // 4 s
@@ -36,6 +47,12 @@ struct tok_handle {
   // host copy of the tokens' bytes (token t: vocab_bytes[vocab_off[t] .. vocab_off[t + 1]))
   std::vector<uint8_t> vocab_bytes;
   std::vector<uint64_t> vocab_off;
+  // finished CTAs of a paged-cache call that completes in place; 0 between calls
+  uint32_t* d_done = nullptr;
+  // the tokens' bytes in the order the grammar kernels read them (laid out by
+  // the first tok_grammar_load)
+  tokgb::DevTokens tokens{};
+  void* d_tokens = nullptr;
   // workspace
   tokgb::Workspace ws{};
   int32_t* d_out = nullptr;           // ids of host-side calls

@@ -235,6 +235,202 @@ int tok_pretokenize_batch(tok_handle* h, const uint8_t* const* texts, const uint
 int tok_pretokenize_device_noalloc(int pattern_id, const uint8_t* d_text, uint64_t len,
                                    uint32_t* d_start_bits, int64_t* d_status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Between the ids and a language model.  The entry points below work on
+ * device buffers, are enqueued on `stream` (NULL = the CUDA default stream)
+ * without a host synchronisation or an allocation, and may be captured in a
+ * CUDA graph.  h gives the device, the error message and the launch count;
+ * TokTier describes none of them: they serve the steps before and after the
+ * model that read this library's ids, item offsets and vocabulary.
+ * Arguments are checked on the host (TOK_EINVAL, nothing enqueued); what only
+ * the device can see is checked there and reported in a device status.
+ * ------------------------------------------------------------------------- */
+
+/* tok_paged_assign -- where the tokens of a batch go in a paged cache.
+ * Request k has ctx_len[k] tokens in the cache, in the blocks
+ * table[k][0 .. ceil(ctx_len[k] / block_size)), and brings the tokens
+ * item_off[k] .. item_off[k+1) of the batch (as tok_encode_batch_device
+ * writes them; one token each in a decode step; none is fine).  Blocks it
+ * lacks are popped from a stack of free blocks, the top first, requests in
+ * order, and written behind its blocks in the table; entries beyond are left
+ * alone.  Token t of request k then has
+ *   pos[t]  = ctx_len[k] + t - item_off[k]
+ *   slot[t] = table[k][pos / block_size] * block_size + pos % block_size
+ *   req[t]  = k
+ * and entries from the batch's token count up to cap are -1 (a padded batch).
+ * status (device int64[4]): [0] = TOK_OK, TOK_EINVAL (item_off not from 0 or
+ *   decreasing, a negative length or free count, 2^31 tokens or more in a
+ *   request) or TOK_EBUF (cap below the token count, a row of the table too
+ *   narrow, too few free blocks); [1] = blocks taken (TOK_EBUF: needed);
+ *   [2] = tokens; [3] = the first request that does not fit, or -1.  On an
+ *   error no block is taken: the table stays, slot, pos and req are -1,
+ *   n_free_out = n_free, seq_len = ctx_len.
+ */
+typedef struct {
+  const int64_t* d_item_off; /* n + 1 */
+  const int64_t* d_ctx_len;  /* n; NULL: all 0 */
+  uint32_t n;
+  uint32_t block_size;       /* 1 .. 2^20 */
+  int32_t* d_table;          /* n rows of max_blocks entries, table_stride apart */
+  int64_t table_stride;
+  uint32_t max_blocks;
+  const int32_t* d_free;     /* the stack: entries 0 .. *d_n_free - 1, its top last */
+  const int64_t* d_n_free;
+  int64_t* d_n_free_out;     /* may be d_n_free itself */
+  int64_t* d_slot;           /* cap */
+  int32_t* d_pos;            /* cap; NULL: not wanted */
+  int32_t* d_req;            /* cap; NULL: not wanted */
+  uint64_t cap;
+  int64_t* d_seq_len;        /* n: ctx_len + new tokens; may be d_ctx_len itself; NULL: not wanted */
+  int64_t* d_status;         /* 4 */
+} tok_paged_args;
+
+/* Two calls on one handle must not overlap on the GPU (they share a counter).
+ * Errors: TOK_EINVAL (NULL buffers, n == 0, a block size or stride out of
+ * range), TOK_ECUDA. */
+int tok_paged_assign(tok_handle* h, const tok_paged_args* a, void* stream);
+
+/* tok_paged_release -- the blocks of finished requests go back on the stack.
+ * Request k with done[k] != 0 returns its ceil(seq_len[k] / block_size) blocks;
+ * they are appended to free[n_free ..), requests in order, a request's blocks
+ * in the table's order.  The table is not written.
+ * n_free_out may be d_n_free itself.  status (device int64[4]): [0] = TOK_OK,
+ * TOK_EINVAL (a negative length or free count, a length beyond the table's
+ * row) or TOK_EBUF (more than free_cap entries); [1] = blocks returned
+ * (TOK_EBUF: that would have been); [2] = 0; [3] = the first bad request, or
+ * -1.  On an error nothing is returned and n_free_out = n_free.
+ * Two calls on one handle must not overlap on the GPU.
+ * Errors: as tok_paged_assign. */
+int tok_paged_release(tok_handle* h, const int64_t* d_seq_len, const uint8_t* d_done, uint32_t n,
+                      uint32_t block_size, const int32_t* d_table, int64_t table_stride, uint32_t max_blocks,
+                      int32_t* d_free, uint64_t free_cap, const int64_t* d_n_free, int64_t* d_n_free_out,
+                      int64_t* d_status, void* stream);
+
+/* tok_seen_bits -- the set of the tokens of each item, as bits: bit v % 32 of
+ * word v / 32 of row k is set iff v is among ids[item_off[k] .. item_off[k+1])
+ * (as tok_encode_batch_device writes them).  A row has ceil(n_logits / 32)
+ * words, rows are seen_stride words apart; ids outside 0 .. n_logits - 1 are
+ * skipped.  keep != 0: bits that are set stay set (a prompt that comes in
+ * parts); 0: the rows are written whole.
+ * Errors: TOK_EINVAL (NULL buffers, n == 0, n_logits == 0 or above 2^20,
+ * seen_stride too small), TOK_ECUDA. */
+int tok_seen_bits(tok_handle* h, const int32_t* d_ids, const int64_t* d_item_off, uint32_t n, uint32_t n_logits,
+                  uint32_t* d_seen, int64_t seen_stride, int keep, void* stream);
+
+/* tok_logits_process -- the rules on the scores of the next token, and what a
+ * decoder asks of the result, in one pass.  For row b and token v, in 32-bit
+ * floating point:
+ *   c = how often v is among gen[gen_start[b] .. gen_start[b] + gen_len[b])
+ *   x = logits[b][v]
+ *   c > 0, or v's bit of seen row b set:  x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *   x = x - frequency[b] * c;  c > 0:  x = x - presence[b]
+ *   x = x + the bias values of v in row b, in the list's order
+ *   v's bit of the row's mask clear:  x = -inf (whatever the logit was, NaN too)
+ *   y = x / temperature[b]
+ * out[b][v] = y, in the logits' type; out may be the logits themselves (with
+ *   their stride).
+ * top[b] = the v of the largest x, the lowest one of equals; -1 if no x is
+ *   above -inf or one is NaN.
+ * lse[b] = log of the sum of exp(y) over the row (-inf for a row that the mask
+ *   leaves empty, NaN if a y is NaN).
+ * logprob[b] = y[pick[b]] - lse[b]; pick NULL or negative: of top[b]
+ *   (a row without one, or a pick beyond the row: -inf, NaN if lse is).
+ * Rows read mask row mask_row[b] (NULL: b): an index into a table of masks,
+ * for instance one for each state of a grammar; -1: nothing is allowed, less:
+ * everything is.  ids outside 0 .. n_logits - 1 in gen or bias_id are
+ * skipped.  Nothing is read of a score that the mask hides.
+ */
+enum { TOK_F32 = 0, TOK_F16 = 1, TOK_BF16 = 2 };
+
+typedef struct {
+  const void* d_logits;       /* rows of n_logits, logits_stride elements apart */
+  int64_t logits_stride;
+  void* d_out;                /* NULL: not wanted */
+  int64_t out_stride;
+  int32_t dtype;              /* TOK_F32, TOK_F16 or TOK_BF16, of logits and out */
+  uint32_t rows;
+  uint32_t n_logits;          /* 1 .. 2^20 */
+  const uint32_t* d_seen;     /* rows of bits as tok_seen_bits writes them; NULL: none */
+  int64_t seen_stride;
+  const int32_t* d_gen;       /* generated ids; NULL (with the next two): none */
+  const int64_t* d_gen_start; /* rows; rows may share ids */
+  const int32_t* d_gen_len;   /* rows */
+  const float* d_repetition;  /* rows, > 0; NULL: 1 */
+  const float* d_frequency;   /* rows; NULL: 0 */
+  const float* d_presence;    /* rows; NULL: 0 */
+  const float* d_temperature; /* rows, > 0; NULL: 1 */
+  const int64_t* d_bias_off;  /* rows + 1; NULL (with the next two): none */
+  const int32_t* d_bias_id;
+  const float* d_bias;
+  const uint32_t* d_mask;     /* rows of bits, a set bit allows the token; NULL: all allowed */
+  int64_t mask_stride;
+  const int32_t* d_mask_row;  /* rows; NULL: row b reads mask row b */
+  const int32_t* d_pick;      /* rows; NULL: none */
+  int32_t* d_top;             /* rows; NULL: not wanted (this and the next two) */
+  float* d_lse;
+  float* d_logprob;
+} tok_logits_args;
+
+/* Errors: TOK_EINVAL (NULL or missing buffers, an unknown type, n_logits out
+ * of range, a stride below a row), TOK_ECUDA.  rows == 0 does nothing. */
+int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream);
+
+/* tok_logits_backward -- the gradient of tok_logits_process.  a: the same
+ * arguments as the forward call; of its outputs d_lse is read, and d_top
+ * where a row's pick is negative (d_out and d_logprob are not used).  With
+ *   dy[v] = grad_out[v] + (grad_lse - grad_logprob) * exp(y[v] - lse) + (v == pick) * grad_logprob
+ * and 0 where the mask hides v,
+ *   grad_logits[v] = dy[v] / temperature * (the factor of the repetition penalty on v: 1, 1 / repetition or repetition)
+ *   grad_bias[i]   = dy[bias_id[i]] / temperature (0 for an id that was skipped)
+ * A row with an lse of -inf gets no gradient through it.
+ */
+typedef struct {
+  const void* d_grad_out;       /* as out, of the logits' type; NULL: 0 */
+  int64_t grad_out_stride;
+  const float* d_grad_lse;      /* rows; NULL: 0 */
+  const float* d_grad_logprob;  /* rows; NULL: 0 */
+  void* d_grad_logits;          /* of the logits' type; must not overlap the logits or grad_out */
+  int64_t grad_logits_stride;
+  float* d_grad_bias;           /* as d_bias; NULL: not wanted */
+} tok_logits_grad_args;
+
+/* Errors: as tok_logits_process; TOK_EINVAL if d_lse is missing where
+ * grad_lse or grad_logprob is given, or d_top where a pick may be the top. */
+int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logits_grad_args* g, void* stream);
+
+/* tok_grammar_load -- a byte automaton over the vocabulary of h, for token
+ * masks.  next (host): n_states rows of 256 int32, the state after each byte,
+ * -1 where the byte is not allowed.  accept (host, n_states): whether the text
+ * may end there.  n_states is 1 .. 65535.  The first call on a handle lays out the
+ * vocabulary's bytes on the device.  A grammar belongs to h: free it, with
+ * tok_grammar_free, before h.
+ * Errors: TOK_EINVAL (NULL, n_states or a next state out of range),
+ * TOK_ENOMEM, TOK_ECUDA. */
+typedef struct tok_grammar tok_grammar;
+int tok_grammar_load(tok_handle* h, const int32_t* next, const uint8_t* accept, uint32_t n_states,
+                     tok_grammar** out);
+void tok_grammar_free(tok_grammar* g);
+
+/* tok_grammar_mask -- walk the automaton over tokens, then say which tokens
+ * may follow.  Row k is in state[k] (-1: nothing may follow) and reads the
+ * tokens ids[item_off[k] .. item_off[k+1]), or ids[k] alone where item_off is
+ * NULL (negative ids are skipped; ids NULL: no tokens); state_out[k] is the
+ * state after their bytes, -1 once a byte is not allowed.  eos (-1: none) is
+ * the id of the end token: it is allowed in accepting states, and nothing
+ * may follow it.  Other ids from the vocabulary's size on are not allowed.
+ * Bit v of mask row k (n_logits bits in ceil(n_logits / 32) words, rows
+ * mask_stride words apart, the last word's other bits 0) is set iff token v's
+ * bytes can be walked from state_out[k].  d_mask NULL: only the states;
+ * d_state_out NULL: only the masks; state_out must not overlap state (rows
+ * look at one another's state: equal ones are walked once).
+ * States outside the automaton count as -1.
+ * Errors: TOK_EINVAL (NULL buffers, g of another handle, state_out == state,
+ * n_logits == 0 or above 2^20, mask_stride too small), TOK_ECUDA.  n == 0 does
+ * nothing. */
+int tok_grammar_mask(tok_handle* h, const tok_grammar* g, const int32_t* d_state, const int32_t* d_ids,
+                     const int64_t* d_item_off, uint32_t n, int32_t eos, int32_t* d_state_out, uint32_t n_logits,
+                     uint32_t* d_mask, int64_t mask_stride, void* stream);
+
 /* tok_last_error -- message of the last failure on h (or of the last failed
  * tok_load when h is NULL).  The string is owned by the library and valid
  * until the next call on h. */
