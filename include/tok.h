@@ -338,7 +338,7 @@ int tok_seen_bits(tok_handle* h, const int32_t* d_ids, const int64_t* d_item_off
  * Rows read mask row mask_row[b] (NULL: b): an index into a table of masks,
  * for instance one for each state of a grammar; -1: nothing is allowed, less:
  * everything is.  ids outside 0 .. n_logits - 1 in gen or bias_id are
- * skipped.  Nothing is read of a score that the mask hides.
+ * skipped.  A logit that the mask hides has no influence.
  */
 enum { TOK_F32 = 0, TOK_F16 = 1, TOK_BF16 = 2 };
 
@@ -382,7 +382,8 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream);
  * and 0 where the mask hides v,
  *   grad_logits[v] = dy[v] / temperature * (the factor of the repetition penalty on v: 1, 1 / repetition or repetition)
  *   grad_bias[i]   = dy[bias_id[i]] / temperature (0 for an id that was skipped)
- * A row with an lse of -inf gets no gradient through it.
+ * A row with an lse of -inf, or beyond 1e36 (nothing but a type's lowest
+ * values), gets no gradient through it.
  */
 typedef struct {
   const void* d_grad_out;       /* as out, of the logits' type; NULL: 0 */
