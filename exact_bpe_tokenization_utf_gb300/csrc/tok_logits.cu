@@ -24,10 +24,12 @@ namespace {
 constexpr uint32_t MAX_LOGITS = 1u << 20;
 constexpr int LG_THREADS = 256;
 constexpr int LG_WARPS = LG_THREADS / 32;
-constexpr int VEC = 8;            // scores per thread and step
+constexpr int PER = 16;           // scores per thread and step
+constexpr int STEP = LG_THREADS * PER;
 constexpr int EDGE = 16;          // places before a slice's first vector, for the scores that come before it (fewer)
-constexpr int SLOTS = 4096;       // of the table of tokens with entries
-constexpr int MOST_TOKENS = 3072; // tokens that it takes
+constexpr int TABLE = STEP + 64;  // slots of the table of tokens with entries
+constexpr int SLOTS = 4096;       // of them, where tokens are hashed
+constexpr int MOST_TOKENS = 3072; // tokens that it then takes
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float REF_MAX = 1e37f;  // references of a sum of exponentials stay within this
@@ -36,6 +38,7 @@ template <class T> struct Num;
 template <> struct Num<float> {
   static __device__ __forceinline__ float get(float x) { return x; }
   static __device__ __forceinline__ float put(float x) { return x; }
+  static constexpr int VEC = 4;  // scores of a vector: 16 bytes
   // scores 2 i and 2 i + 1 of a vector's words
   static __device__ __forceinline__ float2 pair(const uint32_t* w, int i) {
     return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
@@ -46,6 +49,7 @@ template <> struct Num<float> {
   }
 };
 template <> struct Num<__half> {
+  static constexpr int VEC = 8;
   static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
   static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
   static __device__ __forceinline__ float2 pair(const uint32_t* w, int i) {
@@ -56,6 +60,7 @@ template <> struct Num<__half> {
   }
 };
 template <> struct Num<__nv_bfloat16> {
+  static constexpr int VEC = 8;
   static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
   static __device__ __forceinline__ float2 pair(const uint32_t* w, int i) {
@@ -126,17 +131,19 @@ __device__ __forceinline__ Row load_row(const tok_logits_args& a, uint32_t b) {
   return r;
 }
 
-// How a row's scores fall into vectors of 8: vector i holds v0 + 8 i ..
-// v0 + 8 i + 7, at a 16-byte boundary of the array that is written (of the
-// logits where none is).  The scores before and after are taken one by one,
-// and where another array's rows lie differently so are the first and the
-// last vector: reading them takes whole 16-byte pieces around them.
+// How a row's scores fall into vectors of 16 bytes: vector i holds the VEC
+// scores from v0 + VEC i on, at a 16-byte boundary of the array that is
+// written (of the logits where none is).  The scores before and after are
+// taken one by one, and where another array's rows lie differently (SHIFTED)
+// so are the first and the last vector: reading them takes whole 16-byte
+// pieces around them.
 struct Grid {
   uint32_t v0, n_vec;
 };
 
 template <class T, bool SHIFTED>
 __device__ __forceinline__ Grid vectors(const void* row, uint32_t n_logits) {
+  constexpr uint32_t VEC = Num<T>::VEC;
   Grid g;
   g.v0 = (uint32_t)((16u - (reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / (uint32_t)sizeof(T);
   g.n_vec = n_logits > g.v0 ? (n_logits - g.v0) / VEC : 0;
@@ -152,64 +159,127 @@ __device__ __forceinline__ Grid vectors(const void* row, uint32_t n_logits) {
   return g;
 }
 
-// The words of one vector as they come from memory: whole 16-byte pieces, one
-// more where the row is shifted against the vectors.
-template <class T, bool SHIFTED> struct Raw {
-  static constexpr int WORDS = VEC * (int)sizeof(T) / 4;
-  static constexpr int PIECES = WORDS / 4 + (SHIFTED ? 1 : 0);
-  uint4 p[PIECES];
+// A row's vectors on their way from memory: each thread keeps its vectors of
+// the next steps in flight (cp.async into slots of its own warp), so that
+// about 24 KB per CTA are under way whatever the warps are doing.  Vector i of
+// a shifted row lies in the pieces i and i + 1.
+template <class T, bool SHIFTED> struct Stream {
+  static constexpr int VEC = Num<T>::VEC;
+  static constexpr int U = PER / VEC;                       // vectors per thread and step
+  static constexpr int DEPTH = sizeof(T) == 4 ? 3 : 4;      // steps in flight
+  static constexpr int SLOT = (SHIFTED ? 33 : 32) * 16;     // bytes of a warp's 32 vectors
+  static constexpr int STAGE = LG_WARPS * U * SLOT;         // bytes of a step
+  static constexpr size_t BYTES = (size_t)DEPTH * STAGE;
 
-  __device__ __forceinline__ void load(const T* row, uint32_t v) {
-    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row + v) & ~uintptr_t(SHIFTED ? 15 : 0));
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) p[i] = __ldcs(q + i);
+  const uint8_t* base;  // the piece of vector 0
+  uint32_t shift;       // bytes of the vectors past a 16-byte boundary
+  uint8_t* mine;        // this lane's slot of stage 0
+  uint32_t i_end;
+
+  __device__ __forceinline__ void open(const T* row, uint32_t v0, uint32_t end, uint8_t* mem) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + v0);
+    shift = (uint32_t)(at & 15u);
+    base = reinterpret_cast<const uint8_t*>(at - (SHIFTED ? shift : 0u));
+    mine = mem + (threadIdx.x >> 5) * U * SLOT + (threadIdx.x & 31u) * 16;
+    i_end = end;
   }
-  // the vector's own words; shift: the row's bytes past a 16-byte boundary at each vector
-  __device__ __forceinline__ void words(uint32_t* w, uint32_t shift) const {
-    uint32_t a[PIECES * 4];
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      a[4 * i] = p[i].x;
-      a[4 * i + 1] = p[i].y;
-      a[4 * i + 2] = p[i].z;
-      a[4 * i + 3] = p[i].w;
+  static __device__ __forceinline__ void copy(uint8_t* to, const uint8_t* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+                 : "memory");
+  }
+  // the thread's u-th vector, i; want: whether its scores matter (for a shifted row: any of the warp's)
+  __device__ __forceinline__ void issue(uint32_t stage, int u, uint32_t i, bool want) const {
+    uint8_t* to = mine + stage * STAGE + u * SLOT;
+    if (!SHIFTED) {
+      if (want && i < i_end) copy(to, base + (size_t)i * 16);
+    } else if (want) {
+      if (i <= i_end && i_end) copy(to, base + (size_t)i * 16);
+      if ((threadIdx.x & 31u) == 0 && i + 32 <= i_end) copy(to + 512, base + (size_t)(i + 32) * 16);
     }
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    if (SHIFTED) __syncwarp();
+  }
+  __device__ __forceinline__ void scores(uint32_t stage, int u, float* z) const {
+    const uint4* q = reinterpret_cast<const uint4*>(mine + stage * STAGE + u * SLOT);
+    uint32_t w[5];
+    const uint4 a = q[0];
     if constexpr (!SHIFTED) {
-#pragma unroll
-      for (int i = 0; i < WORDS; ++i) w[i] = a[i];
+      w[0] = a.x;
+      w[1] = a.y;
+      w[2] = a.z;
+      w[3] = a.w;
     } else {
+      const uint4 b = q[1];
       const bool two = shift & 8u, one = shift & 4u;
+      const uint32_t c0 = two ? a.z : a.x, c1 = two ? a.w : a.y, c2 = two ? b.x : a.z, c3 = two ? b.y : a.w,
+                     c4 = two ? b.z : b.x, c5 = two ? b.w : b.y;
+      w[0] = one ? c1 : c0;
+      w[1] = one ? c2 : c1;
+      w[2] = one ? c3 : c2;
+      w[3] = one ? c4 : c3;
+      w[4] = one ? c5 : c4;
+      if (sizeof(T) == 2) {
 #pragma unroll
-      for (int i = 0; i < WORDS + 2; ++i) a[i] = two ? a[i + 2] : a[i];
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 2u) * 8u);
+      }
+    }
 #pragma unroll
-      for (int i = 0; i < WORDS + 1; ++i) a[i] = one ? a[i + 1] : a[i];
-#pragma unroll
-      for (int i = 0; i < WORDS; ++i) w[i] = sizeof(T) == 4 ? a[i] : __funnelshift_r(a[i], a[i + 1], (shift & 2u) * 8u);
+    for (int e = 0; e < VEC / 2; ++e) {
+      const float2 f = Num<T>::pair(w, e);
+      z[2 * e] = f.x;
+      z[2 * e + 1] = f.y;
     }
   }
 };
 
-// the 8 bits from v on
-__device__ __forceinline__ uint32_t bits8(const uint32_t* words, uint32_t v) {
-  if ((v & 7u) == 0) return __ldg(reinterpret_cast<const uint8_t*>(words) + (v >> 3));
-  return __funnelshift_r(__ldg(words + (v >> 5)), __ldg(words + ((v + 7u) >> 5)), v & 31u) & 255u;
+template <class T>
+__device__ __forceinline__ void store_scores(T* to, const float* z, float factor) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < Num<T>::VEC / 2; ++e) Num<T>::put_pair(w, e, z[2 * e] * factor, z[2 * e + 1] * factor);
+  __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 __device__ __forceinline__ bool bit_of(const uint32_t* words, uint32_t v) { return (__ldg(words + (v >> 5)) >> (v & 31)) & 1u; }
 
+// A slice's bits in shared memory, moved so that the bits of a vector lie in
+// one byte: bit p is that of token lo + p (lo modulo 2^32: it may be negative).
+__host__ __device__ constexpr uint32_t bit_words(uint32_t tokens) { return (tokens + 48 + 31) / 32; }
+
+__device__ __forceinline__ void move_bits(uint32_t* to, const uint32_t* from, uint32_t n_logits, uint32_t lo, uint32_t n) {
+  const int n_words = (int)((n_logits + 31) / 32);
+  for (uint32_t j = threadIdx.x; j < n; j += LG_THREADS) {
+    const int first = (int)(lo + 32 * j) >> 5;
+    const uint32_t a = first >= 0 && first < n_words ? __ldg(from + first) : 0u;
+    const uint32_t b = first + 1 >= 0 && first + 1 < n_words ? __ldg(from + first + 1) : 0u;
+    to[j] = __funnelshift_r(a, b, lo & 31u);
+  }
+}
+
+// the bits of the slice's vector ii
+template <class T>
+__device__ __forceinline__ uint32_t vector_bits(const uint32_t* bits, uint32_t ii) {
+  const uint8_t* b = reinterpret_cast<const uint8_t*>(bits) + EDGE / 8;
+  if (Num<T>::VEC == 8) return b[ii];
+  return (uint32_t)b[ii >> 1] >> (4 * (ii & 1u)) & 15u;
+}
+
 // What the lists (generated ids, biases) say about the tokens of a slice, in
 // shared memory: a bit for each token with entries, and a table of these
-// tokens (linear probing from a multiplicative hash) with the number of
-// occurrences and the smallest index of the bias entries (its top bit: there
-// are more), or NO_BIAS.  Once all entries are in, the scores of the table's
-// tokens are computed, all loads in flight at once, and replace the counts;
-// whoever meets a token's bit looks its score up.  A table that would hold
-// more than MOST_TOKENS tokens is made for half of the range, and so on down
-// to a single step's 2,048 tokens, which always fit.
+// tokens with the number of occurrences and the smallest index of the bias
+// entries (its top bit: there are more), or NO_BIAS.  Once all entries are in,
+// the scores of the table's tokens are computed, all loads in flight at once,
+// and replace the counts; whoever meets a token's bit looks its score up.  A
+// range of at most TABLE tokens has a slot for each; a longer one is hashed
+// (linear probing).  A table that would hold more than MOST_TOKENS tokens is
+// made for half of the range, down to a single step's, which fits.
 constexpr uint32_t NO_BIAS = 0x7fffffffu;
 constexpr uint32_t NO_TOKEN = 0xffffffffu;
 constexpr uint32_t GENERATED = 0x80000000u;  // with a key: the token is among the generated ids
-static_assert(LG_THREADS * VEC <= MOST_TOKENS && MOST_TOKENS < SLOTS, "a step's tokens fit the table");
+static_assert(STEP + 2 * EDGE <= TABLE && SLOTS <= TABLE && MOST_TOKENS + LG_THREADS < SLOTS, "sizes of the table");
 
 struct Lists {
   uint32_t* bits;
@@ -219,33 +289,30 @@ struct Lists {
   uint16_t* used;   // the slots in use
   uint32_t* n_used;
   uint32_t lo;      // token of bit 0 (modulo 2^32)
-  uint32_t mask;    // slots - 1
+  uint32_t from;    // first token of the range
+  uint32_t mask;    // hashed: slots - 1; 0: a slot for each token
 };
 
-__host__ __device__ constexpr uint32_t bit_words(uint32_t per) { return (per * VEC + 48 + 31) / 32; }
-size_t lists_bytes(uint32_t per, bool bias) {
-  return (SLOTS * (bias ? 3 : 2) + 4 + bit_words(per)) * sizeof(uint32_t) + MOST_TOKENS * sizeof(uint16_t);
-}
+size_t lists_bytes(bool bias) { return (TABLE * (bias ? 3 : 2) + 4) * sizeof(uint32_t) + TABLE * sizeof(uint16_t); }
 
-__device__ __forceinline__ Lists place_lists(uint32_t* mem, bool bias, uint32_t n_entries) {
+__device__ __forceinline__ Lists place_lists(uint32_t* mem, bool bias, uint32_t* bits, uint32_t lo) {
   Lists l;
   l.key = mem;
-  l.val = mem + SLOTS;
-  l.first = bias ? mem + 2 * SLOTS : nullptr;
-  uint32_t* at = mem + SLOTS * (bias ? 3 : 2);
-  l.used = reinterpret_cast<uint16_t*>(at);
-  l.n_used = at + MOST_TOKENS / 2;
-  l.bits = l.n_used + 4;
-  l.lo = 0;
-  uint32_t slots = 256;
-  while (slots < SLOTS && slots / 2 < n_entries) slots *= 2;
-  l.mask = slots - 1;
+  l.val = mem + TABLE;
+  l.first = bias ? mem + 2 * TABLE : nullptr;
+  l.n_used = mem + TABLE * (bias ? 3 : 2);
+  l.used = reinterpret_cast<uint16_t*>(l.n_used + 4);
+  l.bits = bits;
+  l.lo = lo;
+  l.from = l.mask = 0;
   return l;
 }
 
 __device__ __forceinline__ uint32_t first_slot(const Lists& l, uint32_t v) { return (v * 0x9E3779B1u >> 16) & l.mask; }
 
+// the slot of a token that is in the table
 __device__ __forceinline__ uint32_t slot_of(const Lists& l, uint32_t v) {
+  if (l.mask == 0) return v - l.from;
   uint32_t s = first_slot(l, v);
   while ((l.key[s] & ~GENERATED) != v) s = (s + 1) & l.mask;
   return s;
@@ -253,14 +320,14 @@ __device__ __forceinline__ uint32_t slot_of(const Lists& l, uint32_t v) {
 
 // a token's slot, taken if it has none; NO_TOKEN: the table is full
 __device__ __forceinline__ uint32_t take_slot(const Lists& l, uint32_t v) {
-  uint32_t s = first_slot(l, v);
+  uint32_t s = l.mask ? first_slot(l, v) : v - l.from;
   for (;;) {
     uint32_t k = *static_cast<volatile uint32_t*>(l.key + s);
     if (k == NO_TOKEN) {
       k = atomicCAS(&l.key[s], NO_TOKEN, v);
       if (k == NO_TOKEN) {
         const uint32_t n = atomicAdd(l.n_used, 1u);
-        if (n >= MOST_TOKENS) return NO_TOKEN;  // (at most one per thread beyond: the table keeps free slots)
+        if (l.mask && n >= MOST_TOKENS) return NO_TOKEN;  // (at most one per thread beyond: slots stay free)
         l.used[n] = (uint16_t)s;
         const uint32_t at = v - l.lo;
         atomicOr(&l.bits[at >> 5], 1u << (at & 31));
@@ -294,8 +361,17 @@ __device__ __forceinline__ float score(const Row& r, uint32_t v, uint32_t c, uin
 // The table of the tokens from .. from + n - 1, with their scores.  False (in
 // every thread): it is too small for them.
 template <class T>
-__device__ __forceinline__ bool take_lists(const Row& r, const Lists& l, uint32_t from, uint32_t n, const T* x) {
-  for (uint32_t i = threadIdx.x; i <= l.mask; i += LG_THREADS) {
+__device__ __forceinline__ bool take_lists(const Row& r, Lists& l, uint32_t from, uint32_t n, const T* x) {
+  uint32_t slots = n;
+  l.from = from;
+  l.mask = 0;
+  if (n > TABLE) {
+    const uint32_t entries = (uint32_t)r.gen_len + (uint32_t)r.bias_n;
+    slots = 256;
+    while (slots < SLOTS && slots / 2 < entries) slots *= 2;
+    l.mask = slots - 1;
+  }
+  for (uint32_t i = threadIdx.x; i < slots; i += LG_THREADS) {
     l.key[i] = NO_TOKEN;
     l.val[i] = 0;
     if (l.first) l.first[i] = NO_BIAS;
@@ -343,28 +419,29 @@ __device__ __forceinline__ bool take_lists(const Row& r, const Lists& l, uint32_
   return true;
 }
 
-// The scores of a vector; special: its tokens with entries, generated (where
-// asked for): those among the generated ids.  The repetition penalty of the
-// others is a product with its reciprocal, within 2^-22 of the quotient:
-// where that can decide which score is the largest, they are taken again with
-// score().
-__device__ __forceinline__ void scores(const Row& r, const Lists& l, uint32_t v, uint32_t seen, uint32_t special,
-                                       float* z, uint32_t* generated) {
+// The scores of a thread's step, q-th at token v[q / VEC] + q % VEC; special:
+// those of tokens with entries, generated (where asked for): of these, the
+// generated ids.  The repetition penalty of the others is a product with its
+// reciprocal, within 2^-22 of the quotient: where that can decide which score
+// is the largest, they are taken again with score().
+template <int VEC>
+__device__ __forceinline__ void rules(const Row& r, const Lists& l, const uint32_t* v, uint32_t seen, uint32_t special,
+                                      float* z, uint32_t* generated) {
   if (seen) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float f = z[e] > 0.f ? r.inv_rep : r.rep;
-      if ((seen >> e) & 1u) z[e] *= f;
+    for (int q = 0; q < PER; ++q) {
+      const float f = z[q] > 0.f ? r.inv_rep : r.rep;
+      if ((seen >> q) & 1u) z[q] *= f;
     }
   }
   for (uint32_t m = special; m; m &= m - 1) {
     const int at = __ffs((int)m) - 1;
-    const uint32_t s = slot_of(l, v + at);
+    const uint32_t s = slot_of(l, v[0] + (uint32_t)(at / VEC) * (LG_THREADS * VEC) + (uint32_t)(at % VEC));
     const float zs = __uint_as_float(l.val[s]);
     if (generated) *generated |= (l.key[s] >> 31) << at;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      if (e == at) z[e] = zs;
+    for (int q = 0; q < PER; ++q)
+      if (q == at) z[q] = zs;
   }
 }
 
@@ -396,18 +473,21 @@ __device__ __forceinline__ void join_sum(float& ref, float& sum, float ref2, flo
 
 struct LogitsCall {
   tok_logits_args a;
-  uint32_t per;   // vectors per CTA
-  int lists;      // there are generated ids or biases
+  uint32_t per;    // vectors per CTA
+  uint32_t words;  // of a slice's bits
+  int lists;       // there are generated ids or biases
 };
 
 // Forward.  A row is cut into the slices of a cluster's CTAs (one CTA: the
-// whole row); each thread takes vectors of 8 scores, up to three of them in
-// flight, with the mask's, the seen tokens' and the lists' bits of a vector as
-// a byte each.  Scores that the mask hides are not read.
+// whole row); a step gives each thread 16 scores.  Scores that the mask hides
+// are not read.
 template <class T, bool SHIFTED>
-__global__ void __launch_bounds__(LG_THREADS, 3) k_logits(LogitsCall call) {
+__global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
   namespace cg = cooperative_groups;
-  extern __shared__ __align__(16) uint32_t s_lists[];
+  using S = Stream<T, SHIFTED>;
+  constexpr int VEC = S::VEC, U = S::U, DEPTH = S::DEPTH;
+  constexpr uint32_t FULL = (1u << PER) - 1u;
+  extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ Part s_part[16];
   __shared__ float s_ref[LG_WARPS], s_sum[LG_WARPS], s_z_pick;
   __shared__ unsigned long long s_key;
@@ -416,21 +496,34 @@ __global__ void __launch_bounds__(LG_THREADS, 3) k_logits(LogitsCall call) {
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t rank = cluster.block_rank(), n_ranks = cluster.num_blocks();
   const uint32_t b = blockIdx.x / n_ranks, tid = threadIdx.x, lane = tid & 31u;
-  const Row r = load_row(a, b);
   const T* x = static_cast<const T*>(a.d_logits) + (long long)b * a.logits_stride;
   T* out = a.d_out ? static_cast<T*>(a.d_out) + (long long)b * a.out_stride : nullptr;
+  const Grid g = vectors<T, SHIFTED>(out ? static_cast<const void*>(out) : x, a.n_logits);
+  const uint32_t i_begin = min(rank * call.per, g.n_vec), i_end = min(i_begin + call.per, g.n_vec);
+  S in;
+  in.open(x, g.v0, i_end, s_mem);
+  const Row r = load_row(a, b);
+  // the first steps' scores, before it is known which of them are hidden
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) in.issue(d, u, i_begin + (d * U + u) * LG_THREADS + tid, !r.none);
+    S::commit();
+  }
+  const bool lists = call.lists && (r.gen_len || r.bias_n);
+  const uint32_t lo = g.v0 + i_begin * VEC - EDGE;
+  uint32_t* words = reinterpret_cast<uint32_t*>(s_mem + S::BYTES);
+  uint32_t *m_bits = nullptr, *s_bits = nullptr, *l_bits = nullptr;
+  if (a.d_mask) m_bits = words, words += call.words;
+  if (a.d_seen) s_bits = words, words += call.words;
+  if (call.lists) l_bits = words, words += call.words;
+  if (r.mask) move_bits(m_bits, r.mask, a.n_logits, lo, call.words);
+  if (r.seen) move_bits(s_bits, r.seen, a.n_logits, lo, call.words);
+  Lists l = place_lists(words, a.d_bias_off != nullptr, l_bits, lo);
+  if (lists)
+    for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
   const uint32_t pick = a.d_pick ? (uint32_t)a.d_pick[b] : 0xffffffffu;
   const float k = r.inv_t * LOG2E;
-  const Grid g = vectors<T, SHIFTED>(out ? static_cast<const void*>(out) : x, a.n_logits);
-  const uint32_t shift = (uint32_t)(reinterpret_cast<uintptr_t>(x + g.v0) & 15u);
-  const uint32_t i_begin = min(rank * call.per, g.n_vec), i_end = min(i_begin + call.per, g.n_vec);
-  Lists l{};
-  const bool lists = call.lists && (r.gen_len || r.bias_n);
-  if (lists) {
-    l = place_lists(s_lists, a.d_bias_off != nullptr, (uint32_t)r.gen_len + (uint32_t)r.bias_n);
-    for (uint32_t i = tid; i < bit_words(call.per); i += LG_THREADS) l.bits[i] = 0;
-  }
-  l.lo = g.v0 + i_begin * VEC - EDGE;
   if (tid == 0) {
     s_key = 0;
     s_best = -INFINITY;
@@ -438,37 +531,36 @@ __global__ void __launch_bounds__(LG_THREADS, 3) k_logits(LogitsCall call) {
   }
   cluster.sync();  // (every CTA of the cluster runs before its shared memory is written)
 
-  float ref = -REF_MAX, sum = 0.f;
-  auto allowed8 = [&](uint32_t i) -> uint32_t {
-    if (i >= i_end || r.none) return 0u;
-    return r.mask ? bits8(r.mask, g.v0 + i * VEC) : 255u;
+  // the bits of a thread's vectors from i on
+  auto bits_at = [&](const uint32_t* bits, uint32_t i) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * LG_THREADS < i_end) m |= vector_bits<T>(bits, i - i_begin + u * LG_THREADS) << (u * VEC);
+    return m;
   };
-  auto seen8 = [&](uint32_t i) -> uint32_t { return r.seen && i < i_end ? bits8(r.seen, g.v0 + i * VEC) : 0u; };
-  // the next three vectors of this thread and their bits
-  constexpr int DEPTH = 3;
-  Raw<T, SHIFTED> raw[DEPTH];
-  uint32_t ok[DEPTH], sn[DEPTH];
+  auto inside = [&](uint32_t i) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int d = 0; d < DEPTH; ++d) {
-    ok[d] = allowed8(i_begin + tid + d * LG_THREADS);
-    sn[d] = seen8(i_begin + tid + d * LG_THREADS);
-  }
-#pragma unroll
-  for (int d = 0; d < DEPTH; ++d)
-    if (ok[d]) raw[d].load(x, g.v0 + (i_begin + tid + d * LG_THREADS) * VEC);
+    for (int u = 0; u < U; ++u)
+      if (i + u * LG_THREADS < i_end) m |= ((1u << VEC) - 1u) << (u * VEC);
+    return m;
+  };
+  auto allowed_at = [&](uint32_t i) { return r.none ? 0u : r.mask ? bits_at(m_bits, i) : inside(i); };
 
-  const uint32_t steps = max(1u, (i_end - i_begin + LG_THREADS - 1) / LG_THREADS);
+  float ref = -REF_MAX, sum = 0.f;
+  const uint32_t steps = max(1u, (i_end - i_begin + U * LG_THREADS - 1) / (U * LG_THREADS));
   uint32_t range = steps, next = 0;  // steps that the table is made for, and the step of the next table
+  uint32_t stage = 0;
 #pragma unroll 1
   for (uint32_t step = 0; step < steps; ++step) {
-    const uint32_t i = i_begin + step * LG_THREADS + tid, v = g.v0 + i * VEC;
+    const uint32_t ib = i_begin + step * (U * LG_THREADS), i = ib + tid;
     if (step == next) {
       // the scores of this range: its vectors, the first with those before all vectors, the last with those after
-      const uint32_t i0 = i_begin + step * LG_THREADS;
-      const uint32_t from = rank == 0 && step == 0 ? 0u : g.v0 + i0 * VEC;
+      const uint32_t from = rank == 0 && step == 0 ? 0u : g.v0 + ib * VEC;
       uint32_t i1, to;
       for (;;) {
-        i1 = min(i0 + range * LG_THREADS, i_end);
+        i1 = min(ib + range * (U * LG_THREADS), i_end);
         to = rank == n_ranks - 1 && i1 == i_end ? a.n_logits : g.v0 + i1 * VEC;
         if (!lists) break;
         __syncthreads();
@@ -477,75 +569,72 @@ __global__ void __launch_bounds__(LG_THREADS, 3) k_logits(LogitsCall call) {
       }
       next = step + range;
       if (tid < 32) {  // the scores outside the vectors
-        const uint32_t head = g.v0 + i0 * VEC - from, n = head + (to - (g.v0 + i1 * VEC));
+        const uint32_t head = g.v0 + ib * VEC - from, n = head + (to - (g.v0 + i1 * VEC));
         if (tid < n) {
-          const uint32_t u = tid < head ? from + tid : g.v0 + i1 * VEC + (tid - head);
+          const uint32_t t = tid < head ? from + tid : g.v0 + i1 * VEC + (tid - head);
           float z = -INFINITY;
-          if (!r.none && (!r.mask || bit_of(r.mask, u))) {
-            const uint32_t at = u - l.lo;
-            if (lists && (l.bits[at >> 5] >> (at & 31) & 1u)) z = __uint_as_float(l.val[slot_of(l, u)]);
-            else z = score(r, u, 0, NO_BIAS, r.seen && bit_of(r.seen, u), Num<T>::get(x[u]));
-            const float t = z * k;
-            if (t > ref + 24.f) {
-              const float m = fminf(t, REF_MAX);
+          if (!r.none && (!r.mask || bit_of(r.mask, t))) {
+            const uint32_t at = t - lo;
+            if (lists && (l_bits[at >> 5] >> (at & 31) & 1u)) z = __uint_as_float(l.val[slot_of(l, t)]);
+            else z = score(r, t, 0, NO_BIAS, r.seen && bit_of(r.seen, t), Num<T>::get(x[t]));
+            const float y = z * k;
+            if (y > ref + 24.f) {
+              const float m = fminf(y, REF_MAX);
               sum *= ex2(ref - m);
               ref = m;
             }
             sum += ex2(fmaf(z, k, -ref));
-            atomicMax(&s_key, top_key(z, u));
+            atomicMax(&s_key, top_key(z, t));
           }
-          if (out) out[u] = Num<T>::put(z * r.inv_t);
-          if (u == pick) s_z_pick = z;
+          if (out) out[t] = Num<T>::put(z * r.inv_t);
+          if (t == pick) s_z_pick = z;
         }
       }
     }
-    const uint32_t allowed = ok[0], seen = sn[0];
-    float z[VEC];
-    {
-      uint32_t w[Raw<T, SHIFTED>::WORDS];
-      raw[0].words(w, shift);
+    uint32_t v[U];
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        const float2 p = Num<T>::pair(w, e);
-        z[2 * e] = p.x;
-        z[2 * e + 1] = p.y;
-      }
-    }
-#pragma unroll
-    for (int d = 0; d + 1 < DEPTH; ++d) {
-      ok[d] = ok[d + 1];
-      sn[d] = sn[d + 1];
-      raw[d] = raw[d + 1];
-    }
-    ok[DEPTH - 1] = allowed8(i + DEPTH * LG_THREADS);
-    sn[DEPTH - 1] = seen8(i + DEPTH * LG_THREADS);
-    if (ok[DEPTH - 1]) raw[DEPTH - 1].load(x, v + DEPTH * LG_THREADS * VEC);
-
-    const bool mine = i < i_end;
+    for (int u = 0; u < U; ++u) v[u] = g.v0 + (i + u * LG_THREADS) * VEC;
+    const uint32_t allowed = allowed_at(i), seen = r.seen ? bits_at(s_bits, i) : 0u;
     uint32_t special = 0;
-    if (lists && mine) special = reinterpret_cast<const uint8_t*>(l.bits)[(v - l.lo) >> 3];
-    float vmax = -INFINITY;
+    if (lists) special = bits_at(l_bits, i);
+    S::wait();
+    float z[PER], vmax = -INFINITY;
     if (allowed) {
-      scores(r, l, v, seen, special, z, nullptr);
-      if (allowed != 255u) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (!((allowed >> e) & 1u)) z[e] = -INFINITY;
+      for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
+      rules<VEC>(r, l, v, seen & ~special, special, z, nullptr);
+      if (allowed != FULL) {
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+          if (!((allowed >> q) & 1u)) z[q] = -INFINITY;
       }
-      vmax = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
-      const float t = vmax * k;
-      if (t > ref + 24.f) {
-        const float m = fminf(t, REF_MAX);
+#pragma unroll
+      for (int q = 0; q < PER; q += 2) vmax = fmaxf(fmaxf(z[q], z[q + 1]), vmax);
+      const float y = vmax * k;
+      if (y > ref + 24.f) {
+        const float m = fminf(y, REF_MAX);
         sum *= ex2(ref - m);
         ref = m;
       }
-      float q[VEC];
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) q[e] = ex2(fmaf(z[e], k, -ref));
-      sum += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
+      for (int q = 0; q < PER; ++q) part[q & 3] += ex2(fmaf(z[q], k, -ref));
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
     } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) z[e] = -INFINITY;
+      for (int q = 0; q < PER; ++q) z[q] = -INFINITY;
+    }
+    // this stage's slots are free: the step DEPTH later
+    __syncwarp();
+    {
+      const uint32_t later = i + DEPTH * U * LG_THREADS;
+      uint32_t want = step + DEPTH < steps ? allowed_at(later) : 0u;
+      if (SHIFTED) want = __any_sync(0xffffffffu, want != 0) ? FULL : 0u;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        in.issue(stage, u, later + u * LG_THREADS, (want >> (u * VEC)) & ((1u << VEC) - 1u));
+      S::commit();
+      stage = stage + 1 == DEPTH ? 0 : stage + 1;
     }
     // scores that may be the largest, once more and exactly
     const float best = *static_cast<volatile float*>(&s_best);
@@ -557,34 +646,37 @@ __global__ void __launch_bounds__(LG_THREADS, 3) k_logits(LogitsCall call) {
       const float at_least = fmaxf(near, wmax - fabsf(wmax) * 0x1p-20f);
       if (vmax >= at_least) {
         unsigned long long key = 0;
+        uint32_t m = 0;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (z[e] >= at_least) {
-            float zx = z[e];
-            if (((seen & ~special) >> e) & 1u) zx = score(r, v + e, 0, NO_BIAS, true, Num<T>::get(x[v + e]));
-            key = max(key, top_key(zx, v + e));
-          }
+        for (int q = 0; q < PER; ++q) m |= (z[q] >= at_least && z[q] > -INFINITY ? 1u : 0u) << q;
+        for (; m; m &= m - 1) {
+          const uint32_t q = (uint32_t)__ffs((int)m) - 1u, t = v[0] + q / VEC * (LG_THREADS * VEC) + q % VEC;
+          float zx;
+          if ((special >> q) & 1u) zx = __uint_as_float(l.val[slot_of(l, t)]);
+          else zx = score(r, t, 0, NO_BIAS, (seen >> q) & 1u, Num<T>::get(x[t]));
+          key = max(key, top_key(zx, t));
+        }
         atomicMax(&s_key, key);
         const float zx = key_score(key);
         if (zx > best) s_best = zx;
       }
     }
-    if (mine && pick - v < (uint32_t)VEC) {
-      float zp = -INFINITY;
-      if ((allowed >> (pick - v)) & 1u) {
-        if ((special >> (pick - v)) & 1u) zp = __uint_as_float(l.val[slot_of(l, pick)]);
-        else zp = score(r, pick, 0, NO_BIAS, (seen >> (pick - v)) & 1u, Num<T>::get(x[pick]));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (pick - v[u] < (uint32_t)VEC && i + u * LG_THREADS < i_end) {
+        const uint32_t q = u * VEC + (pick - v[u]);
+        float zp = -INFINITY;
+        if ((allowed >> q) & 1u) {
+          if ((special >> q) & 1u) zp = __uint_as_float(l.val[slot_of(l, pick)]);
+          else zp = score(r, pick, 0, NO_BIAS, (seen >> q) & 1u, Num<T>::get(x[pick]));
+        }
+        s_z_pick = zp;
       }
-      s_z_pick = zp;
-    }
     // (last: out may be the logits, which the lines above read again)
-    if (out && mine) {
-      uint32_t w[Raw<T, false>::WORDS];
+    if (out) {
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) Num<T>::put_pair(w, e, z[2 * e] * r.inv_t, z[2 * e + 1] * r.inv_t);
-      uint4* q = reinterpret_cast<uint4*>(out + v);
-#pragma unroll
-      for (int j = 0; j < Raw<T, false>::PIECES; ++j) __stcs(q + j, make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+      for (int u = 0; u < U; ++u)
+        if (i + u * LG_THREADS < i_end) store_scores(out + v[u], z + u * VEC, r.inv_t);
     }
   }
 
@@ -616,7 +708,7 @@ __global__ void __launch_bounds__(LG_THREADS, 3) k_logits(LogitsCall call) {
     const bool nan = sum != sum;
     const float z_top = key_score(key), y_top = z_top * r.inv_t;
     // beyond the references' range all of the sum is its largest term
-    float lse = nan ? sum : fabsf(y_top) < 1e36f ? LN2 * (ref + log2f(sum)) : y_top;
+    const float lse = nan ? sum : fabsf(y_top) < 1e36f ? LN2 * (ref + log2f(sum)) : y_top;
     if (a.d_top) a.d_top[b] = nan || !key ? -1 : (int32_t)(0xffffffffu - (uint32_t)key);
     if (a.d_lse) a.d_lse[b] = lse;
     if (a.d_logprob) {
@@ -629,7 +721,7 @@ __global__ void __launch_bounds__(LG_THREADS, 3) k_logits(LogitsCall call) {
 struct GradCall {
   tok_logits_args a;
   Grad g;
-  uint32_t per, ranks;
+  uint32_t per, words, ranks;
   int lists;
 };
 
@@ -639,40 +731,60 @@ struct GradCall {
 // log2(e) are sums of two numbers each (their rounding would weigh |y| times
 // on the result) and nothing is added to the exponent.
 template <class T, bool SHIFTED>
-__global__ void __launch_bounds__(LG_THREADS, 3) k_logits_grad(GradCall call) {
-  extern __shared__ __align__(16) uint32_t s_lists[];
+__global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
+  using S = Stream<T, SHIFTED>;
+  constexpr int VEC = S::VEC, U = S::U, DEPTH = S::DEPTH;
+  constexpr uint32_t FULL = (1u << PER) - 1u;
+  extern __shared__ __align__(16) uint8_t s_mem[];
   const tok_logits_args& a = call.a;
   const Grad& gr = call.g;
   const uint32_t rank = blockIdx.x % call.ranks, b = blockIdx.x / call.ranks, tid = threadIdx.x;
-  const Row r = load_row(a, b);
   const T* x = static_cast<const T*>(a.d_logits) + (long long)b * a.logits_stride;
   const T* go = gr.out ? static_cast<const T*>(gr.out) + (long long)b * gr.out_stride : nullptr;
   T* gx = static_cast<T*>(gr.logits) + (long long)b * gr.logits_stride;
+  const Grid g = vectors<T, SHIFTED>(gx, a.n_logits);
+  const uint32_t i_begin = min(rank * call.per, g.n_vec), i_end = min(i_begin + call.per, g.n_vec);
+  S in, gin;
+  in.open(x, g.v0, i_end, s_mem);
+  if (go) gin.open(go, g.v0, i_end, s_mem + S::BYTES);
+  const Row r = load_row(a, b);
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = i_begin + (d * U + u) * LG_THREADS + tid;
+      in.issue(d, u, i, !r.none);
+      if (go) gin.issue(d, u, i, !r.none);
+    }
+    S::commit();
+  }
+  const bool lists = call.lists && (r.gen_len || r.bias_n);
+  const uint32_t lo = g.v0 + i_begin * VEC - EDGE;
+  uint32_t* words = reinterpret_cast<uint32_t*>(s_mem + S::BYTES * (go ? 2 : 1));
+  uint32_t *m_bits = nullptr, *s_bits = nullptr, *l_bits = nullptr;
+  if (a.d_mask) m_bits = words, words += call.words;
+  if (a.d_seen) s_bits = words, words += call.words;
+  if (call.lists) l_bits = words, words += call.words;
+  if (r.mask) move_bits(m_bits, r.mask, a.n_logits, lo, call.words);
+  if (r.seen) move_bits(s_bits, r.seen, a.n_logits, lo, call.words);
+  Lists l = place_lists(words, a.d_bias_off != nullptr, l_bits, lo);
+  if (lists)
+    for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
   const float glp = gr.logprob ? gr.logprob[b] : 0.f;
   float cp = (gr.lse ? gr.lse[b] : 0.f) - glp, lse = 0.f;
   if (gr.lse || gr.logprob) lse = a.d_lse[b];
   if (fabsf(lse) >= 1e36f) cp = lse = 0.f;  // (nothing but -inf or a type's lowest value)
   uint32_t pick = a.d_pick ? (uint32_t)a.d_pick[b] : 0xffffffffu;
   if ((int32_t)pick < 0 && gr.logprob) pick = (uint32_t)a.d_top[b];
-  const double kd = 1.4426950408889634 / (a.d_temperature ? (double)a.d_temperature[b] : 1.0);
   const float up = sizeof(T) == 4 ? 0.f : 24.f;
+  const double kd = 1.4426950408889634 / (a.d_temperature ? (double)a.d_temperature[b] : 1.0);
   const double ld = (double)lse * 1.4426950408889634 - (double)up;
   const float k = (float)kd, k_lo = (float)(kd - (double)k), lh = (float)ld, l_lo = (float)(ld - (double)lh);
   const float cpt = cp * r.inv_t * (sizeof(T) == 4 ? 1.f : 0x1p-24f);
-  const Grid g = vectors<T, SHIFTED>(gx, a.n_logits);
-  const uint32_t shift = (uint32_t)(reinterpret_cast<uintptr_t>(x + g.v0) & 15u);
-  const uint32_t go_shift = (uint32_t)(reinterpret_cast<uintptr_t>(go + g.v0) & 15u);
-  const uint32_t i_begin = min(rank * call.per, g.n_vec), i_end = min(i_begin + call.per, g.n_vec);
-  Lists l{};
-  const bool lists = call.lists && (r.gen_len || r.bias_n);
-  if (lists) {
-    l = place_lists(s_lists, a.d_bias_off != nullptr, (uint32_t)r.gen_len + (uint32_t)r.bias_n);
-    for (uint32_t i = tid; i < bit_words(call.per); i += LG_THREADS) l.bits[i] = 0;
-  }
-  l.lo = g.v0 + i_begin * VEC - EDGE;
   if (rank == 0 && gr.bias)
     for (int i = tid; i < r.bias_n; i += LG_THREADS)
       if ((uint32_t)r.bias_id[i] >= a.n_logits) gr.bias[(r.bias - a.d_bias) + i] = 0.f;
+  __syncthreads();
 
   // the gradient of a score before the temperature, from the score and grad_out
   auto d_score = [&](float z, float d) -> float {
@@ -688,47 +800,41 @@ __global__ void __launch_bounds__(LG_THREADS, 3) k_logits_grad(GradCall call) {
     return d;
   };
   // the gradients of a token's bias entries
-  auto bias_grad = [&](uint32_t v, uint32_t s, float dz) {
+  auto bias_grad = [&](uint32_t t, uint32_t s, float dz) {
     const uint32_t fb = l.first ? l.first[s] : NO_BIAS;
     if (!gr.bias || (fb & NO_BIAS) == NO_BIAS) return;
     float* to = gr.bias + (r.bias - a.d_bias);
     to[fb & NO_BIAS] = dz;
     if (fb >> 31)
       for (int i = (int)(fb & NO_BIAS) + 1; i < r.bias_n; ++i)
-        if ((uint32_t)r.bias_id[i] == v) to[i] = dz;
+        if ((uint32_t)r.bias_id[i] == t) to[i] = dz;
   };
-  auto allowed8 = [&](uint32_t i) -> uint32_t {
-    if (i >= i_end || r.none) return 0u;
-    return r.mask ? bits8(r.mask, g.v0 + i * VEC) : 255u;
+  auto bits_at = [&](const uint32_t* bits, uint32_t i) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * LG_THREADS < i_end) m |= vector_bits<T>(bits, i - i_begin + u * LG_THREADS) << (u * VEC);
+    return m;
   };
-  auto seen8 = [&](uint32_t i) -> uint32_t { return r.seen && i < i_end ? bits8(r.seen, g.v0 + i * VEC) : 0u; };
-  constexpr int DEPTH = 2;
-  Raw<T, SHIFTED> raw[DEPTH], graw[DEPTH];
-  uint32_t ok[DEPTH], sn[DEPTH];
+  auto inside = [&](uint32_t i) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int d = 0; d < DEPTH; ++d) {
-    ok[d] = allowed8(i_begin + tid + d * LG_THREADS);
-    sn[d] = seen8(i_begin + tid + d * LG_THREADS);
-  }
-#pragma unroll
-  for (int d = 0; d < DEPTH; ++d)
-    if (ok[d]) {
-      const uint32_t v = g.v0 + (i_begin + tid + d * LG_THREADS) * VEC;
-      raw[d].load(x, v);
-      if (go) graw[d].load(go, v);
-    }
+    for (int u = 0; u < U; ++u)
+      if (i + u * LG_THREADS < i_end) m |= ((1u << VEC) - 1u) << (u * VEC);
+    return m;
+  };
+  auto allowed_at = [&](uint32_t i) { return r.none ? 0u : r.mask ? bits_at(m_bits, i) : inside(i); };
 
-  const uint32_t steps = max(1u, (i_end - i_begin + LG_THREADS - 1) / LG_THREADS);
-  uint32_t range = steps, next = 0;
+  const uint32_t steps = max(1u, (i_end - i_begin + U * LG_THREADS - 1) / (U * LG_THREADS));
+  uint32_t range = steps, next = 0, stage = 0;
 #pragma unroll 1
   for (uint32_t step = 0; step < steps; ++step) {
-    const uint32_t i = i_begin + step * LG_THREADS + tid, v = g.v0 + i * VEC;
+    const uint32_t ib = i_begin + step * (U * LG_THREADS), i = ib + tid;
     if (step == next) {
-      const uint32_t i0 = i_begin + step * LG_THREADS;
-      const uint32_t from = rank == 0 && step == 0 ? 0u : g.v0 + i0 * VEC;
+      const uint32_t from = rank == 0 && step == 0 ? 0u : g.v0 + ib * VEC;
       uint32_t i1, to;
       for (;;) {
-        i1 = min(i0 + range * LG_THREADS, i_end);
+        i1 = min(ib + range * (U * LG_THREADS), i_end);
         to = rank == call.ranks - 1 && i1 == i_end ? a.n_logits : g.v0 + i1 * VEC;
         if (!lists) break;
         __syncthreads();
@@ -737,108 +843,99 @@ __global__ void __launch_bounds__(LG_THREADS, 3) k_logits_grad(GradCall call) {
       }
       next = step + range;
       if (tid < 32) {
-        const uint32_t head = g.v0 + i0 * VEC - from, n = head + (to - (g.v0 + i1 * VEC));
+        const uint32_t head = g.v0 + ib * VEC - from, n = head + (to - (g.v0 + i1 * VEC));
         if (tid < n) {
-          const uint32_t u = tid < head ? from + tid : g.v0 + i1 * VEC + (tid - head), at = u - l.lo;
-          const bool special = lists && (l.bits[at >> 5] >> (at & 31) & 1u);
-          const uint32_t s = special ? slot_of(l, u) : 0;
+          const uint32_t t = tid < head ? from + tid : g.v0 + i1 * VEC + (tid - head), at = t - lo;
+          const bool special = lists && (l_bits[at >> 5] >> (at & 31) & 1u);
+          const uint32_t s = special ? slot_of(l, t) : 0;
           float dz = 0.f, f = 1.f;
-          if (!r.none && (!r.mask || bit_of(r.mask, u))) {
-            const bool seen = r.seen && bit_of(r.seen, u);
-            const float xu = Num<T>::get(x[u]);
-            if (seen || (special && l.key[s] >> 31)) f = xu > 0.f ? r.inv_rep : r.rep;
-            dz = d_score(special ? __uint_as_float(l.val[s]) : score(r, u, 0, NO_BIAS, seen, xu), go ? Num<T>::get(go[u]) : 0.f);
-            if (u == pick) dz += glp * r.inv_t;
+          if (!r.none && (!r.mask || bit_of(r.mask, t))) {
+            const bool seen = r.seen && bit_of(r.seen, t);
+            const float xt = Num<T>::get(x[t]);
+            if (seen || (special && l.key[s] >> 31)) f = xt > 0.f ? r.inv_rep : r.rep;
+            dz = d_score(special ? __uint_as_float(l.val[s]) : score(r, t, 0, NO_BIAS, seen, xt), go ? Num<T>::get(go[t]) : 0.f);
+            if (t == pick) dz = fmaf(glp, r.inv_t, dz);
           }
-          gx[u] = Num<T>::put(dz * f);
-          if (special) bias_grad(u, s, dz);
+          gx[t] = Num<T>::put(dz * f);
+          if (special) bias_grad(t, s, dz);
         }
       }
     }
-    const uint32_t allowed = ok[0], seen = sn[0];
-    float z[VEC], d[VEC];
-    {
-      uint32_t w[Raw<T, SHIFTED>::WORDS];
-      raw[0].words(w, shift);
+    uint32_t v[U];
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        const float2 p = Num<T>::pair(w, e);
-        z[2 * e] = p.x;
-        z[2 * e + 1] = p.y;
-      }
+    for (int u = 0; u < U; ++u) v[u] = g.v0 + (i + u * LG_THREADS) * VEC;
+    const uint32_t allowed = allowed_at(i), seen = r.seen ? bits_at(s_bits, i) : 0u;
+    uint32_t special = 0;
+    if (lists) special = bits_at(l_bits, i);
+    S::wait();
+    float z[PER], d[PER];
+    uint32_t positive = 0, hit = 0;
+    if (allowed) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
       if (go) {
-        graw[0].words(w, go_shift);
 #pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) {
-          const float2 p = Num<T>::pair(w, e);
-          d[2 * e] = p.x;
-          d[2 * e + 1] = p.y;
-        }
+        for (int u = 0; u < U; ++u) gin.scores(stage, u, d + u * VEC);
       } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) d[e] = 0.f;
+        for (int q = 0; q < PER; ++q) d[q] = 0.f;
       }
-    }
-#pragma unroll
-    for (int q = 0; q + 1 < DEPTH; ++q) {
-      ok[q] = ok[q + 1];
-      sn[q] = sn[q + 1];
-      raw[q] = raw[q + 1];
-      if (go) graw[q] = graw[q + 1];
-    }
-    ok[DEPTH - 1] = allowed8(i + DEPTH * LG_THREADS);
-    sn[DEPTH - 1] = seen8(i + DEPTH * LG_THREADS);
-    if (ok[DEPTH - 1]) {
-      raw[DEPTH - 1].load(x, v + DEPTH * LG_THREADS * VEC);
-      if (go) graw[DEPTH - 1].load(go, v + DEPTH * LG_THREADS * VEC);
-    }
-    if (i >= i_end) continue;
-    uint32_t special = 0;
-    if (lists) special = reinterpret_cast<const uint8_t*>(l.bits)[(v - l.lo) >> 3];
-    if (allowed) {
-      uint32_t positive = 0, hit = seen;
+      hit = seen;
       if (seen | special) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) positive |= (z[e] > 0.f ? 1u : 0u) << e;
+        for (int q = 0; q < PER; ++q) positive |= (z[q] > 0.f ? 1u : 0u) << q;
       }
-      scores(r, l, v, seen, special, z, &hit);
+      rules<VEC>(r, l, v, seen & ~special, special, z, &hit);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) d[e] = d_score(z[e], d[e]);
-      if (pick - v < (uint32_t)VEC) {
+      for (int q = 0; q < PER; ++q) d[q] = d_score(z[q], d[q]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (v + e == pick) d[e] = fmaf(glp, r.inv_t, d[e]);
-      }
-      if (allowed != 255u) {
+      for (int u = 0; u < U; ++u)
+        if (pick - v[u] < (uint32_t)VEC) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (!((allowed >> e) & 1u)) d[e] = 0.f;
-      }
-      if (special && gr.bias) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if ((special >> e) & 1u) bias_grad(v + e, slot_of(l, v + e), d[e]);
-      }
-      if (hit) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float f = (positive >> e) & 1u ? r.inv_rep : r.rep;
-          if ((hit >> e) & 1u) d[e] *= f;
+          for (int e = 0; e < VEC; ++e)
+            if (v[u] + e == pick) d[u * VEC + e] = fmaf(glp, r.inv_t, d[u * VEC + e]);
         }
+      if (allowed != FULL) {
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+          if (!((allowed >> q) & 1u)) d[q] = 0.f;
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        d[e] = 0.f;
-        if (gr.bias && ((special >> e) & 1u)) bias_grad(v + e, slot_of(l, v + e), 0.f);
+      for (int q = 0; q < PER; ++q) d[q] = 0.f;
+    }
+    if (special && gr.bias) {
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if ((special >> q) & 1u) {
+          const uint32_t t = v[q / VEC] + q % VEC;
+          bias_grad(t, slot_of(l, t), d[q]);
+        }
+    }
+    if (hit) {
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const float f = (positive >> q) & 1u ? r.inv_rep : r.rep;
+        if ((hit >> q) & 1u) d[q] *= f;
       }
     }
-    uint32_t w[Raw<T, false>::WORDS];
+    __syncwarp();
+    {
+      const uint32_t later = i + DEPTH * U * LG_THREADS;
+      uint32_t want = step + DEPTH < steps ? allowed_at(later) : 0u;
+      if (SHIFTED) want = __any_sync(0xffffffffu, want != 0) ? FULL : 0u;
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) Num<T>::put_pair(w, e, d[2 * e], d[2 * e + 1]);
-    uint4* q = reinterpret_cast<uint4*>(gx + v);
+      for (int u = 0; u < U; ++u) {
+        const bool w = (want >> (u * VEC)) & ((1u << VEC) - 1u);
+        in.issue(stage, u, later + u * LG_THREADS, w);
+        if (go) gin.issue(stage, u, later + u * LG_THREADS, w);
+      }
+      S::commit();
+      stage = stage + 1 == DEPTH ? 0 : stage + 1;
+    }
 #pragma unroll
-    for (int j = 0; j < Raw<T, false>::PIECES; ++j) __stcs(q + j, make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+    for (int u = 0; u < U; ++u)
+      if (i + u * LG_THREADS < i_end) store_scores(gx + v[u], d + u * VEC, 1.f);
   }
 }
 
@@ -860,11 +957,25 @@ __global__ void __launch_bounds__(LG_THREADS) k_seen_bits(const int32_t* ids, co
 }
 
 // Slices of a row: enough CTAs to fill the GPU a few times over while a slice
-// keeps some thousand scores, at most the 16 CTAs of a cluster.
+// keeps some thousand scores, at most the 16 CTAs of a cluster; a slice's
+// bits stay within 16 KB each.
 uint32_t slices(const tok_handle* h, const tok_logits_args& a) {
   uint32_t s = 1;
-  while (s < 16 && (unsigned long long)a.rows * s < 4ull * (unsigned)h->n_sms && a.n_logits / (2 * s) >= 2048) s *= 2;
+  while (s < 16 && ((unsigned long long)a.rows * s < 4ull * (unsigned)h->n_sms || a.n_logits / s > (1u << 17)) &&
+         a.n_logits / (2 * s) >= 2048)
+    s *= 2;
   return s;
+}
+
+size_t stage_bytes(int dtype, bool shifted) {
+  if (dtype == TOK_F32) return shifted ? Stream<float, true>::BYTES : Stream<float, false>::BYTES;
+  return shifted ? Stream<__half, true>::BYTES : Stream<__half, false>::BYTES;
+}
+
+// shared memory of a CTA: the scores in flight, the bits, the table of tokens with entries
+size_t shared_bytes(const tok_logits_args& a, bool shifted, int arrays, uint32_t words, bool lists) {
+  const size_t bits = (size_t)((a.d_mask ? 1 : 0) + (a.d_seen ? 1 : 0) + (lists ? 1 : 0)) * words * sizeof(uint32_t);
+  return arrays * stage_bytes(a.dtype, shifted) + bits + (lists ? lists_bytes(a.d_bias_off != nullptr) : 0);
 }
 
 // whether rows of an array lie like those of another towards 16-byte boundaries
@@ -949,9 +1060,11 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream) tr
   c.a = *a;
   c.lists = a->d_gen || a->d_bias_off;
   const uint32_t n = slices(h, *a);
-  c.per = (a->n_logits / VEC + n - 1) / n;
-  const size_t smem = c.lists ? lists_bytes(c.per, a->d_bias_off != nullptr) : 0;
+  const uint32_t vec = 16 / (uint32_t)size_of(a->dtype);
+  c.per = (a->n_logits / vec + n - 1) / n;
+  c.words = bit_words(c.per * vec);
   const bool shifted = a->d_out && !alike(a->d_logits, a->logits_stride, a->d_out, a->out_stride, a->rows, size_of(a->dtype));
+  const size_t smem = shared_bytes(*a, shifted, 1, c.words, c.lists);
   const unsigned ctas = a->rows * n;
   const cudaError_t e = a->dtype == TOK_F32   ? launch_forward<float>(c, shifted, ctas, n, smem, s)
                         : a->dtype == TOK_F16 ? launch_forward<__half>(c, shifted, ctas, n, smem, s)
@@ -980,11 +1093,14 @@ int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logit
                ga->d_grad_logits, ga->grad_logits_stride, a->d_bias_off ? ga->d_grad_bias : nullptr};
   c.lists = a->d_gen || a->d_bias_off;
   c.ranks = slices(h, *a);
-  c.per = (a->n_logits / VEC + c.ranks - 1) / c.ranks;
-  const size_t smem = c.lists ? lists_bytes(c.per, a->d_bias_off != nullptr) : 0, size = size_of(a->dtype);
+  const size_t size = size_of(a->dtype);
+  const uint32_t vec = 16 / (uint32_t)size;
+  c.per = (a->n_logits / vec + c.ranks - 1) / c.ranks;
+  c.words = bit_words(c.per * vec);
   const bool shifted = !alike(a->d_logits, a->logits_stride, ga->d_grad_logits, ga->grad_logits_stride, a->rows, size) ||
                        (ga->d_grad_out && !alike(ga->d_grad_out, ga->grad_out_stride, ga->d_grad_logits,
                                                  ga->grad_logits_stride, a->rows, size));
+  const size_t smem = shared_bytes(*a, shifted, ga->d_grad_out ? 2 : 1, c.words, c.lists);
   const unsigned ctas = a->rows * c.ranks;
   const cudaError_t e = a->dtype == TOK_F32   ? launch_grad<float>(c, shifted, ctas, smem, s)
                         : a->dtype == TOK_F16 ? launch_grad<__half>(c, shifted, ctas, smem, s)
