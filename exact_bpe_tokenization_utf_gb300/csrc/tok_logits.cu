@@ -202,6 +202,8 @@ template <class T, bool SHIFTED> struct Stream {
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
     if (SHIFTED) __syncwarp();
   }
+  // before the slots serve as other memory
+  static __device__ __forceinline__ void close() { asm volatile("cp.async.wait_all;" ::: "memory"); }
   __device__ __forceinline__ void scores(uint32_t stage, int u, float* z) const {
     const uint4* q = reinterpret_cast<const uint4*>(mine + stage * STAGE + u * SLOT);
     uint32_t w[5];
@@ -267,70 +269,93 @@ __device__ __forceinline__ uint32_t vector_bits(const uint32_t* bits, uint32_t i
   return (uint32_t)b[ii >> 1] >> (4 * (ii & 1u)) & 15u;
 }
 
-// What the lists (generated ids, biases) say about the tokens of a slice, in
-// shared memory: a bit for each token with entries, and a table of these
-// tokens with the number of occurrences and the smallest index of the bias
-// entries (its top bit: there are more), or NO_BIAS.  Once all entries are in,
-// the scores of the table's tokens are computed, all loads in flight at once,
-// and replace the counts; whoever meets a token's bit looks its score up.  A
-// range of at most TABLE tokens has a slot for each; a longer one is hashed
-// (linear probing).  A table that would hold more than MOST_TOKENS tokens is
-// made for half of the range, down to a single step's, which fits.
+// The tokens of the lists (generated ids, biases).  A slice's main pass only
+// knows a bit for each and leaves them out; after it they are counted in a
+// table in shared memory (number of occurrences and the smallest index of the
+// bias entries, its top bit: there are more, or NO_BIAS) and scored one by one,
+// a thread each, all loads in flight at once.  A range of at most TABLE tokens
+// has a slot for each; a longer one is hashed (linear probing).  A table that
+// would hold more than MOST_TOKENS tokens is made for half of the range, and
+// so on down to a step's tokens, which fit.
 constexpr uint32_t NO_BIAS = 0x7fffffffu;
 constexpr uint32_t NO_TOKEN = 0xffffffffu;
-constexpr uint32_t GENERATED = 0x80000000u;  // with a key: the token is among the generated ids
-static_assert(STEP + 2 * EDGE <= TABLE && SLOTS <= TABLE && MOST_TOKENS + LG_THREADS < SLOTS, "sizes of the table");
+static_assert(SLOTS <= TABLE && MOST_TOKENS + LG_THREADS < SLOTS, "sizes of the table");
 
-struct Lists {
-  uint32_t* bits;
+struct Table {
   uint32_t* key;
   uint32_t* val;    // occurrences, then the score
   uint32_t* first;  // nullptr: no biases
   uint16_t* used;   // the slots in use
   uint32_t* n_used;
-  uint32_t lo;      // token of bit 0 (modulo 2^32)
-  uint32_t from;    // first token of the range
+  uint32_t from, n; // the range
   uint32_t mask;    // hashed: slots - 1; 0: a slot for each token
 };
 
-size_t lists_bytes(bool bias) { return (TABLE * (bias ? 3 : 2) + 4) * sizeof(uint32_t) + TABLE * sizeof(uint16_t); }
+size_t table_bytes(bool bias) { return (TABLE * (bias ? 3 : 2) + 4) * sizeof(uint32_t) + TABLE * sizeof(uint16_t); }
 
-__device__ __forceinline__ Lists place_lists(uint32_t* mem, bool bias, uint32_t* bits, uint32_t lo) {
-  Lists l;
-  l.key = mem;
-  l.val = mem + TABLE;
-  l.first = bias ? mem + 2 * TABLE : nullptr;
-  l.n_used = mem + TABLE * (bias ? 3 : 2);
+__device__ __forceinline__ Table place_table(void* mem, bool bias) {
+  Table l;
+  l.key = static_cast<uint32_t*>(mem);
+  l.val = l.key + TABLE;
+  l.first = bias ? l.key + 2 * TABLE : nullptr;
+  l.n_used = l.key + TABLE * (bias ? 3 : 2);
   l.used = reinterpret_cast<uint16_t*>(l.n_used + 4);
-  l.bits = bits;
-  l.lo = lo;
-  l.from = l.mask = 0;
+  l.from = l.n = l.mask = 0;
   return l;
 }
 
-__device__ __forceinline__ uint32_t first_slot(const Lists& l, uint32_t v) { return (v * 0x9E3779B1u >> 16) & l.mask; }
+// f(i, ids[i]) for this thread's entries of a list, eight loads at a time
+template <class F>
+__device__ __forceinline__ void each_id(const int32_t* ids, int n, F f) {
+  for (int i0 = (int)threadIdx.x; i0 < n; i0 += 8 * LG_THREADS) {
+    int32_t id[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) id[j] = i0 + j * LG_THREADS < n ? __ldg(ids + i0 + j * LG_THREADS) : -1;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+      // (rotated, so that the body stands here once)
+      const int32_t v = id[0];
+#pragma unroll
+      for (int q = 0; q < 7; ++q) id[q] = id[q + 1];
+      if (i0 + j * LG_THREADS < n) f(i0 + j * LG_THREADS, (uint32_t)v);
+    }
+  }
+}
+
+// the bits of the listed tokens among from .. from + n - 1; bit 0 is token lo
+__device__ __forceinline__ void list_bits(const Row& r, uint32_t* bits, uint32_t lo, uint32_t from, uint32_t n) {
+  auto one = [&](int, uint32_t v) {
+    if (v - from < n) atomicOr(&bits[(v - lo) >> 5], 1u << ((v - lo) & 31));
+  };
+  each_id(r.gen, r.gen_len, one);
+  each_id(r.bias_id, r.bias_n, one);
+}
+
+__device__ __forceinline__ uint32_t first_slot(const Table& l, uint32_t v) { return (v * 0x9E3779B1u >> 16) & l.mask; }
 
 // the slot of a token that is in the table
-__device__ __forceinline__ uint32_t slot_of(const Lists& l, uint32_t v) {
+__device__ __forceinline__ uint32_t slot_of(const Table& l, uint32_t v) {
   if (l.mask == 0) return v - l.from;
   uint32_t s = first_slot(l, v);
-  while ((l.key[s] & ~GENERATED) != v) s = (s + 1) & l.mask;
+  while (l.key[s] != v) s = (s + 1) & l.mask;
   return s;
 }
 
 // a token's slot, taken if it has none; NO_TOKEN: the table is full
-__device__ __forceinline__ uint32_t take_slot(const Lists& l, uint32_t v) {
+__device__ __forceinline__ uint32_t take_slot(const Table& l, uint32_t v) {
   uint32_t s = l.mask ? first_slot(l, v) : v - l.from;
   for (;;) {
     uint32_t k = *static_cast<volatile uint32_t*>(l.key + s);
     if (k == NO_TOKEN) {
       k = atomicCAS(&l.key[s], NO_TOKEN, v);
       if (k == NO_TOKEN) {
-        const uint32_t n = atomicAdd(l.n_used, 1u);
+        // one addition for all threads of the warp that are here
+        const uint32_t here = __activemask(), lane = threadIdx.x & 31u, first = (uint32_t)__ffs((int)here) - 1u;
+        uint32_t n = 0;
+        if (lane == first) n = atomicAdd(l.n_used, (uint32_t)__popc(here));
+        n = __shfl_sync(here, n, (int)first) + (uint32_t)__popc(here & ((1u << lane) - 1u));
         if (l.mask && n >= MOST_TOKENS) return NO_TOKEN;  // (at most one per thread beyond: slots stay free)
         l.used[n] = (uint16_t)s;
-        const uint32_t at = v - l.lo;
-        atomicOr(&l.bits[at >> 5], 1u << (at & 31));
         return s;
       }
     }
@@ -358,12 +383,12 @@ __device__ __forceinline__ float score(const Row& r, uint32_t v, uint32_t c, uin
   return x;
 }
 
-// The table of the tokens from .. from + n - 1, with their scores.  False (in
+// The table of the tokens from .. from + n - 1, entries counted.  False (in
 // every thread): it is too small for them.
-template <class T>
-__device__ __forceinline__ bool take_lists(const Row& r, Lists& l, uint32_t from, uint32_t n, const T* x) {
+__device__ __forceinline__ bool fill_table(const Row& r, Table& l, uint32_t from, uint32_t n) {
   uint32_t slots = n;
   l.from = from;
+  l.n = n;
   l.mask = 0;
   if (n > TABLE) {
     const uint32_t entries = (uint32_t)r.gen_len + (uint32_t)r.bias_n;
@@ -371,6 +396,7 @@ __device__ __forceinline__ bool take_lists(const Row& r, Lists& l, uint32_t from
     while (slots < SLOTS && slots / 2 < entries) slots *= 2;
     l.mask = slots - 1;
   }
+  __syncthreads();
   for (uint32_t i = threadIdx.x; i < slots; i += LG_THREADS) {
     l.key[i] = NO_TOKEN;
     l.val[i] = 0;
@@ -379,69 +405,57 @@ __device__ __forceinline__ bool take_lists(const Row& r, Lists& l, uint32_t from
   if (threadIdx.x == 0) *l.n_used = 0;
   __syncthreads();
   bool full = false;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < r.gen_len; i += LG_THREADS) {
-    const uint32_t v = (uint32_t)r.gen[i];
+  each_id(r.gen, r.gen_len, [&](int, uint32_t v) {
     if (v - from < n && !full) {
       const uint32_t s = take_slot(l, v);
       if (s == NO_TOKEN) full = true;
       else atomicAdd(&l.val[s], 1u);
     }
-  }
+  });
   if (l.first)
-    for (int i = threadIdx.x; i < r.bias_n; i += LG_THREADS) {
-      const uint32_t v = (uint32_t)r.bias_id[i];
+    each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
       if (v - from < n && !full) {
         const uint32_t s = take_slot(l, v);
         if (s == NO_TOKEN) full = true;
         else atomicMin(&l.first[s], (uint32_t)i);
       }
-    }
+    });
   if (__syncthreads_or(full)) return false;
   if (l.first && r.bias_n > 1) {
-    for (int i = threadIdx.x; i < r.bias_n; i += LG_THREADS) {
-      const uint32_t v = (uint32_t)r.bias_id[i];
+    each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
       if (v - from < n) {
         const uint32_t s = slot_of(l, v);
         if ((l.first[s] & NO_BIAS) != (uint32_t)i) atomicOr(&l.first[s], 0x80000000u);
       }
-    }
+    });
     __syncthreads();
   }
-  const uint32_t used = *l.n_used;
-  for (uint32_t j = threadIdx.x; j < used; j += LG_THREADS) {
-    const uint32_t s = l.used[j], v = l.key[s], c = l.val[s];
-    const float z = score(r, v, c, l.first ? l.first[s] : NO_BIAS, r.seen && bit_of(r.seen, v), Num<T>::get(x[v]));
-    l.val[s] = __float_as_uint(z);
-    if (c) l.key[s] = v | GENERATED;
-  }
-  __syncthreads();
   return true;
 }
 
-// The scores of a thread's step, q-th at token v[q / VEC] + q % VEC; special:
-// those of tokens with entries, generated (where asked for): of these, the
-// generated ids.  The repetition penalty of the others is a product with its
+// Calls per_table() with the table of each part of the tokens from .. from + n - 1.
+template <class F>
+__device__ __forceinline__ void each_table(const Row& r, Table& l, uint32_t from, uint32_t n, F per_table) {
+  uint32_t range = n;
+  for (uint32_t at = from; at - from < n;) {
+    const uint32_t m = min(range, n - (at - from));
+    if (!fill_table(r, l, at, m)) {
+      range = (m + 1) / 2;
+      continue;
+    }
+    per_table();
+    at += m;
+  }
+}
+
+// The repetition penalty of a thread's seen scores, as a product with its
 // reciprocal, within 2^-22 of the quotient: where that can decide which score
 // is the largest, they are taken again with score().
-template <int VEC>
-__device__ __forceinline__ void rules(const Row& r, const Lists& l, const uint32_t* v, uint32_t seen, uint32_t special,
-                                      float* z, uint32_t* generated) {
-  if (seen) {
+__device__ __forceinline__ void penalise(const Row& r, uint32_t seen, float* z) {
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const float f = z[q] > 0.f ? r.inv_rep : r.rep;
-      if ((seen >> q) & 1u) z[q] *= f;
-    }
-  }
-  for (uint32_t m = special; m; m &= m - 1) {
-    const int at = __ffs((int)m) - 1;
-    const uint32_t s = slot_of(l, v[0] + (uint32_t)(at / VEC) * (LG_THREADS * VEC) + (uint32_t)(at % VEC));
-    const float zs = __uint_as_float(l.val[s]);
-    if (generated) *generated |= (l.key[s] >> 31) << at;
-#pragma unroll
-    for (int q = 0; q < PER; ++q)
-      if (q == at) z[q] = zs;
+  for (int q = 0; q < PER; ++q) {
+    const float f = z[q] > 0.f ? r.inv_rep : r.rep;
+    if ((seen >> q) & 1u) z[q] *= f;
   }
 }
 
@@ -475,7 +489,9 @@ struct LogitsCall {
   tok_logits_args a;
   uint32_t per;    // vectors per CTA
   uint32_t words;  // of a slice's bits
+  uint32_t bits_at; // where they are in shared memory
   int lists;       // there are generated ids or biases
+  int in_place;    // out is logits
 };
 
 // Forward.  A row is cut into the slices of a cluster's CTAs (one CTA: the
@@ -490,7 +506,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
   extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ Part s_part[16];
   __shared__ float s_ref[LG_WARPS], s_sum[LG_WARPS], s_z_pick;
-  __shared__ unsigned long long s_key;
+  __shared__ unsigned long long s_key, s_list_key, s_total[LG_WARPS];
   __shared__ float s_best;  // a score that some token of this CTA has: what is below it is not the top
   const tok_logits_args& a = call.a;
   const cg::cluster_group cluster = cg::this_cluster();
@@ -512,16 +528,21 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
   }
   const bool lists = call.lists && (r.gen_len || r.bias_n);
   const uint32_t lo = g.v0 + i_begin * VEC - EDGE;
-  uint32_t* words = reinterpret_cast<uint32_t*>(s_mem + S::BYTES);
+  uint32_t* words = reinterpret_cast<uint32_t*>(s_mem + call.bits_at);
   uint32_t *m_bits = nullptr, *s_bits = nullptr, *l_bits = nullptr;
   if (a.d_mask) m_bits = words, words += call.words;
   if (a.d_seen) s_bits = words, words += call.words;
   if (call.lists) l_bits = words, words += call.words;
   if (r.mask) move_bits(m_bits, r.mask, a.n_logits, lo, call.words);
   if (r.seen) move_bits(s_bits, r.seen, a.n_logits, lo, call.words);
-  Lists l = place_lists(words, a.d_bias_off != nullptr, l_bits, lo);
-  if (lists)
+  // the slice's tokens: those of its vectors, the first slice's from the row's start, the last one's to its end
+  const uint32_t from = rank == 0 ? 0u : g.v0 + i_begin * VEC;
+  const uint32_t to = rank == n_ranks - 1 ? a.n_logits : g.v0 + i_end * VEC;
+  if (lists) {
     for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
+    __syncthreads();
+    list_bits(r, l_bits, lo, from, to - from);
+  }
   const uint32_t pick = a.d_pick ? (uint32_t)a.d_pick[b] : 0xffffffffu;
   const float k = r.inv_t * LOG2E;
   if (tid == 0) {
@@ -550,59 +571,42 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
 
   float ref = -REF_MAX, sum = 0.f;
   const uint32_t steps = max(1u, (i_end - i_begin + U * LG_THREADS - 1) / (U * LG_THREADS));
-  uint32_t range = steps, next = 0;  // steps that the table is made for, and the step of the next table
   uint32_t stage = 0;
-#pragma unroll 1
-  for (uint32_t step = 0; step < steps; ++step) {
-    const uint32_t ib = i_begin + step * (U * LG_THREADS), i = ib + tid;
-    if (step == next) {
-      // the scores of this range: its vectors, the first with those before all vectors, the last with those after
-      const uint32_t from = rank == 0 && step == 0 ? 0u : g.v0 + ib * VEC;
-      uint32_t i1, to;
-      for (;;) {
-        i1 = min(ib + range * (U * LG_THREADS), i_end);
-        to = rank == n_ranks - 1 && i1 == i_end ? a.n_logits : g.v0 + i1 * VEC;
-        if (!lists) break;
-        __syncthreads();
-        if (take_lists(r, l, from, to - from, x)) break;
-        range = (range + 1) / 2;
-      }
-      next = step + range;
-      if (tid < 32) {  // the scores outside the vectors
-        const uint32_t head = g.v0 + ib * VEC - from, n = head + (to - (g.v0 + i1 * VEC));
-        if (tid < n) {
-          const uint32_t t = tid < head ? from + tid : g.v0 + i1 * VEC + (tid - head);
-          float z = -INFINITY;
-          if (!r.none && (!r.mask || bit_of(r.mask, t))) {
-            const uint32_t at = t - lo;
-            if (lists && (l_bits[at >> 5] >> (at & 31) & 1u)) z = __uint_as_float(l.val[slot_of(l, t)]);
-            else z = score(r, t, 0, NO_BIAS, r.seen && bit_of(r.seen, t), Num<T>::get(x[t]));
-            const float y = z * k;
-            if (y > ref + 24.f) {
-              const float m = fminf(y, REF_MAX);
-              sum *= ex2(ref - m);
-              ref = m;
-            }
-            sum += ex2(fmaf(z, k, -ref));
-            atomicMax(&s_key, top_key(z, t));
+  if (tid < 32) {  // the scores outside the vectors
+    const uint32_t head = g.v0 + i_begin * VEC - from, n = head + (to - (g.v0 + i_end * VEC));
+    if (tid < n) {
+      const uint32_t t = tid < head ? from + tid : g.v0 + i_end * VEC + (tid - head), at = t - lo;
+      if (!lists || !(l_bits[at >> 5] >> (at & 31) & 1u)) {
+        float z = -INFINITY;
+        if (!r.none && (!r.mask || bit_of(r.mask, t))) {
+          z = score(r, t, 0, NO_BIAS, r.seen && bit_of(r.seen, t), Num<T>::get(x[t]));
+          const float y = z * k;
+          if (y > ref + 24.f) {
+            ref = fminf(y, REF_MAX);
+            sum = 0.f;
           }
-          if (out) out[t] = Num<T>::put(z * r.inv_t);
-          if (t == pick) s_z_pick = z;
+          sum += ex2(fmaf(z, k, -ref));
+          atomicMax(&s_key, top_key(z, t));
         }
+        if (out) out[t] = Num<T>::put(z * r.inv_t);
+        if (t == pick) s_z_pick = z;
       }
     }
+  }
+#pragma unroll 1
+  for (uint32_t step = 0; step < steps; ++step) {
+    const uint32_t i = i_begin + step * (U * LG_THREADS) + tid;
     uint32_t v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = g.v0 + (i + u * LG_THREADS) * VEC;
-    const uint32_t allowed = allowed_at(i), seen = r.seen ? bits_at(s_bits, i) : 0u;
-    uint32_t special = 0;
-    if (lists) special = bits_at(l_bits, i);
+    const uint32_t special = lists ? bits_at(l_bits, i) : 0u;
+    const uint32_t loaded = allowed_at(i), allowed = loaded & ~special, seen = r.seen ? bits_at(s_bits, i) : 0u;
     S::wait();
     float z[PER], vmax = -INFINITY;
     if (allowed) {
 #pragma unroll
       for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
-      rules<VEC>(r, l, v, seen & ~special, special, z, nullptr);
+      if (seen) penalise(r, seen, z);
       if (allowed != FULL) {
 #pragma unroll
         for (int q = 0; q < PER; ++q)
@@ -624,18 +628,6 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
 #pragma unroll
       for (int q = 0; q < PER; ++q) z[q] = -INFINITY;
     }
-    // this stage's slots are free: the step DEPTH later
-    __syncwarp();
-    {
-      const uint32_t later = i + DEPTH * U * LG_THREADS;
-      uint32_t want = step + DEPTH < steps ? allowed_at(later) : 0u;
-      if (SHIFTED) want = __any_sync(0xffffffffu, want != 0) ? FULL : 0u;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        in.issue(stage, u, later + u * LG_THREADS, (want >> (u * VEC)) & ((1u << VEC) - 1u));
-      S::commit();
-      stage = stage + 1 == DEPTH ? 0 : stage + 1;
-    }
     // scores that may be the largest, once more and exactly
     const float best = *static_cast<volatile float*>(&s_best);
     const float near = best < INFINITY ? best - fabsf(best) * 0x1p-20f : best;
@@ -651,9 +643,14 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
         for (int q = 0; q < PER; ++q) m |= (z[q] >= at_least && z[q] > -INFINITY ? 1u : 0u) << q;
         for (; m; m &= m - 1) {
           const uint32_t q = (uint32_t)__ffs((int)m) - 1u, t = v[0] + q / VEC * (LG_THREADS * VEC) + q % VEC;
-          float zx;
-          if ((special >> q) & 1u) zx = __uint_as_float(l.val[slot_of(l, t)]);
-          else zx = score(r, t, 0, NO_BIAS, (seen >> q) & 1u, Num<T>::get(x[t]));
+          float zx = 0.f;
+          if ((seen >> q) & 1u) {
+            zx = score(r, t, 0, NO_BIAS, true, Num<T>::get(x[t]));
+          } else {
+#pragma unroll
+            for (int p = 0; p < PER; ++p)
+              if (p == (int)q) zx = z[p];
+          }
           key = max(key, top_key(zx, t));
         }
         atomicMax(&s_key, key);
@@ -665,20 +662,40 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
     for (int u = 0; u < U; ++u)
       if (pick - v[u] < (uint32_t)VEC && i + u * LG_THREADS < i_end) {
         const uint32_t q = u * VEC + (pick - v[u]);
-        float zp = -INFINITY;
-        if ((allowed >> q) & 1u) {
-          if ((special >> q) & 1u) zp = __uint_as_float(l.val[slot_of(l, pick)]);
-          else zp = score(r, pick, 0, NO_BIAS, (seen >> q) & 1u, Num<T>::get(x[pick]));
-        }
-        s_z_pick = zp;
+        if ((allowed >> q) & 1u) s_z_pick = score(r, pick, 0, NO_BIAS, (seen >> q) & 1u, Num<T>::get(x[pick]));
       }
-    // (last: out may be the logits, which the lines above read again)
+    // (out may be the logits, which the lines above read again; those of listed tokens are still needed then)
     if (out) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i + u * LG_THREADS < i_end) store_scores(out + v[u], z + u * VEC, r.inv_t);
+        if (i + u * LG_THREADS < i_end) {
+          if (call.in_place && (special & loaded) >> (u * VEC) & ((1u << VEC) - 1u)) {
+            float xs[VEC];
+            in.scores(stage, u, xs);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+              if (!((special & loaded) >> (u * VEC + e) & 1u)) xs[e] = z[u * VEC + e] * r.inv_t;
+            store_scores(out + v[u], xs, 1.f);
+          } else {
+            store_scores(out + v[u], z + u * VEC, r.inv_t);
+          }
+        }
+    }
+    // this stage's slots are free: the step DEPTH later
+    __syncwarp();
+    {
+      const uint32_t later = i + DEPTH * U * LG_THREADS;
+      uint32_t want = step + DEPTH < steps ? allowed_at(later) : 0u;
+      if (SHIFTED) want = __any_sync(0xffffffffu, want != 0) ? FULL : 0u;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        in.issue(stage, u, later + u * LG_THREADS, (want >> (u * VEC)) & ((1u << VEC) - 1u));
+      S::commit();
+      stage = stage + 1 == DEPTH ? 0 : stage + 1;
     }
   }
+
+  S::close();
 
   // the CTA's sum, then the cluster's, and the row's results
 #pragma unroll
@@ -689,10 +706,49 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
     s_sum[tid >> 5] = sum;
   }
   __syncthreads();
-  if (tid == 0) {
+  if (tid == 0)
     for (int w = 1; w < LG_WARPS; ++w) join_sum(ref, sum, s_ref[w], s_sum[w]);
-    Part* to = n_ranks == 1 ? s_part : cluster.map_shared_rank(s_part, 0);
-    to[rank] = Part{s_key, ref, sum, s_z_pick};
+  // The listed tokens.  Which thread scores which of them depends on the order
+  // of the table's atomics, so their exponentials are added up as whole
+  // numbers, in units of 2^-40 of the largest one.
+  if (lists) {
+    Table l = place_table(s_mem, a.d_bias_off != nullptr);
+    each_table(r, l, from, to - from, [&] {
+      const uint32_t used = *l.n_used;
+      if (tid == 0) s_list_key = 0;
+      __syncthreads();
+      bool nan = false;
+      for (uint32_t j = tid; j < used; j += LG_THREADS) {
+        const uint32_t s = l.used[j], t = l.key[s], at = t - lo;
+        float z = -INFINITY;
+        if (!r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u)))
+          z = score(r, t, l.val[s], l.first ? l.first[s] : NO_BIAS, r.seen && (s_bits[at >> 5] >> (at & 31) & 1u),
+                    Num<T>::get(x[t]));
+        l.val[s] = __float_as_uint(z);
+        nan |= z != z;
+        atomicMax(&s_list_key, top_key(z, t));
+        if (t == pick) s_z_pick = z;
+        if (out) out[t] = Num<T>::put(z * r.inv_t);
+      }
+      nan = __syncthreads_or(nan);
+      const float m = fmaxf(fminf(key_score(s_list_key) * k, REF_MAX), -REF_MAX);
+      unsigned long long total = 0;
+      for (uint32_t j = tid; j < used; j += LG_THREADS)
+        total += (unsigned long long)(fminf(ex2(fmaf(__uint_as_float(l.val[l.used[j]]), k, -m)), 1.f) * 0x1p40f);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      if (lane == 0) s_total[tid >> 5] = total;
+      __syncthreads();
+      if (tid == 0) {
+        for (int w = 1; w < LG_WARPS; ++w) total += s_total[w];
+        join_sum(ref, sum, m, nan ? NAN : (float)total * 0x1p-40f);
+        s_key = max(s_key, s_list_key);
+      }
+    });
+  }
+  if (tid == 0) {
+    Part* parts = n_ranks == 1 ? s_part : cluster.map_shared_rank(s_part, 0);
+    parts[rank] = Part{s_key, ref, sum, s_z_pick};
   }
   if (n_ranks > 1) cluster.sync();
   if (rank == 0 && tid == 0) {
@@ -721,7 +777,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
 struct GradCall {
   tok_logits_args a;
   Grad g;
-  uint32_t per, words, ranks;
+  uint32_t per, words, bits_at, ranks;
   int lists;
 };
 
@@ -760,16 +816,20 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
   }
   const bool lists = call.lists && (r.gen_len || r.bias_n);
   const uint32_t lo = g.v0 + i_begin * VEC - EDGE;
-  uint32_t* words = reinterpret_cast<uint32_t*>(s_mem + S::BYTES * (go ? 2 : 1));
+  uint32_t* words = reinterpret_cast<uint32_t*>(s_mem + call.bits_at);
   uint32_t *m_bits = nullptr, *s_bits = nullptr, *l_bits = nullptr;
   if (a.d_mask) m_bits = words, words += call.words;
   if (a.d_seen) s_bits = words, words += call.words;
   if (call.lists) l_bits = words, words += call.words;
   if (r.mask) move_bits(m_bits, r.mask, a.n_logits, lo, call.words);
   if (r.seen) move_bits(s_bits, r.seen, a.n_logits, lo, call.words);
-  Lists l = place_lists(words, a.d_bias_off != nullptr, l_bits, lo);
-  if (lists)
+  const uint32_t from = rank == 0 ? 0u : g.v0 + i_begin * VEC;
+  const uint32_t to = rank == call.ranks - 1 ? a.n_logits : g.v0 + i_end * VEC;
+  if (lists) {
     for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
+    __syncthreads();
+    list_bits(r, l_bits, lo, from, to - from);
+  }
   const float glp = gr.logprob ? gr.logprob[b] : 0.f;
   float cp = (gr.lse ? gr.lse[b] : 0.f) - glp, lse = 0.f;
   if (gr.lse || gr.logprob) lse = a.d_lse[b];
@@ -799,16 +859,6 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
     }
     return d;
   };
-  // the gradients of a token's bias entries
-  auto bias_grad = [&](uint32_t t, uint32_t s, float dz) {
-    const uint32_t fb = l.first ? l.first[s] : NO_BIAS;
-    if (!gr.bias || (fb & NO_BIAS) == NO_BIAS) return;
-    float* to = gr.bias + (r.bias - a.d_bias);
-    to[fb & NO_BIAS] = dz;
-    if (fb >> 31)
-      for (int i = (int)(fb & NO_BIAS) + 1; i < r.bias_n; ++i)
-        if ((uint32_t)r.bias_id[i] == t) to[i] = dz;
-  };
   auto bits_at = [&](const uint32_t* bits, uint32_t i) {
     uint32_t m = 0;
 #pragma unroll
@@ -826,50 +876,38 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
   auto allowed_at = [&](uint32_t i) { return r.none ? 0u : r.mask ? bits_at(m_bits, i) : inside(i); };
 
   const uint32_t steps = max(1u, (i_end - i_begin + U * LG_THREADS - 1) / (U * LG_THREADS));
-  uint32_t range = steps, next = 0, stage = 0;
+  uint32_t stage = 0;
+  // one score's gradient; c, fb: its entries in the lists.  Returns that before the repetition penalty.
+  auto one = [&](uint32_t t, uint32_t c, uint32_t fb) {
+    float dz = 0.f, f = 1.f;
+    const uint32_t at = t - lo;
+    if (!r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u))) {
+      const bool seen = r.seen && (s_bits[at >> 5] >> (at & 31) & 1u);
+      const float xt = Num<T>::get(x[t]);
+      if (seen || c) f = xt > 0.f ? r.inv_rep : r.rep;
+      dz = d_score(score(r, t, c, fb, seen, xt), go ? Num<T>::get(go[t]) : 0.f);
+      if (t == pick) dz = fmaf(glp, r.inv_t, dz);
+    }
+    gx[t] = Num<T>::put(dz * f);
+    return dz;
+  };
+  if (tid < 32) {  // the scores outside the vectors
+    const uint32_t head = g.v0 + i_begin * VEC - from, n = head + (to - (g.v0 + i_end * VEC));
+    if (tid < n) {
+      const uint32_t t = tid < head ? from + tid : g.v0 + i_end * VEC + (tid - head), at = t - lo;
+      if (!lists || !(l_bits[at >> 5] >> (at & 31) & 1u)) one(t, 0, NO_BIAS);
+    }
+  }
 #pragma unroll 1
   for (uint32_t step = 0; step < steps; ++step) {
-    const uint32_t ib = i_begin + step * (U * LG_THREADS), i = ib + tid;
-    if (step == next) {
-      const uint32_t from = rank == 0 && step == 0 ? 0u : g.v0 + ib * VEC;
-      uint32_t i1, to;
-      for (;;) {
-        i1 = min(ib + range * (U * LG_THREADS), i_end);
-        to = rank == call.ranks - 1 && i1 == i_end ? a.n_logits : g.v0 + i1 * VEC;
-        if (!lists) break;
-        __syncthreads();
-        if (take_lists(r, l, from, to - from, x)) break;
-        range = (range + 1) / 2;
-      }
-      next = step + range;
-      if (tid < 32) {
-        const uint32_t head = g.v0 + ib * VEC - from, n = head + (to - (g.v0 + i1 * VEC));
-        if (tid < n) {
-          const uint32_t t = tid < head ? from + tid : g.v0 + i1 * VEC + (tid - head), at = t - lo;
-          const bool special = lists && (l_bits[at >> 5] >> (at & 31) & 1u);
-          const uint32_t s = special ? slot_of(l, t) : 0;
-          float dz = 0.f, f = 1.f;
-          if (!r.none && (!r.mask || bit_of(r.mask, t))) {
-            const bool seen = r.seen && bit_of(r.seen, t);
-            const float xt = Num<T>::get(x[t]);
-            if (seen || (special && l.key[s] >> 31)) f = xt > 0.f ? r.inv_rep : r.rep;
-            dz = d_score(special ? __uint_as_float(l.val[s]) : score(r, t, 0, NO_BIAS, seen, xt), go ? Num<T>::get(go[t]) : 0.f);
-            if (t == pick) dz = fmaf(glp, r.inv_t, dz);
-          }
-          gx[t] = Num<T>::put(dz * f);
-          if (special) bias_grad(t, s, dz);
-        }
-      }
-    }
+    const uint32_t i = i_begin + step * (U * LG_THREADS) + tid;
     uint32_t v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = g.v0 + (i + u * LG_THREADS) * VEC;
-    const uint32_t allowed = allowed_at(i), seen = r.seen ? bits_at(s_bits, i) : 0u;
-    uint32_t special = 0;
-    if (lists) special = bits_at(l_bits, i);
+    const uint32_t allowed = allowed_at(i) & ~(lists ? bits_at(l_bits, i) : 0u);
+    const uint32_t seen = r.seen ? bits_at(s_bits, i) : 0u;
     S::wait();
     float z[PER], d[PER];
-    uint32_t positive = 0, hit = 0;
     if (allowed) {
 #pragma unroll
       for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
@@ -880,12 +918,12 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
 #pragma unroll
         for (int q = 0; q < PER; ++q) d[q] = 0.f;
       }
-      hit = seen;
-      if (seen | special) {
+      uint32_t positive = 0;
+      if (seen) {
 #pragma unroll
         for (int q = 0; q < PER; ++q) positive |= (z[q] > 0.f ? 1u : 0u) << q;
+        penalise(r, seen, z);
       }
-      rules<VEC>(r, l, v, seen & ~special, special, z, &hit);
 #pragma unroll
       for (int q = 0; q < PER; ++q) d[q] = d_score(z[q], d[q]);
 #pragma unroll
@@ -900,24 +938,16 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
         for (int q = 0; q < PER; ++q)
           if (!((allowed >> q) & 1u)) d[q] = 0.f;
       }
+      if (seen) {
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+          const float f = (positive >> q) & 1u ? r.inv_rep : r.rep;
+          if ((seen >> q) & 1u) d[q] *= f;
+        }
+      }
     } else {
 #pragma unroll
       for (int q = 0; q < PER; ++q) d[q] = 0.f;
-    }
-    if (special && gr.bias) {
-#pragma unroll
-      for (int q = 0; q < PER; ++q)
-        if ((special >> q) & 1u) {
-          const uint32_t t = v[q / VEC] + q % VEC;
-          bias_grad(t, slot_of(l, t), d[q]);
-        }
-    }
-    if (hit) {
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        const float f = (positive >> q) & 1u ? r.inv_rep : r.rep;
-        if ((hit >> q) & 1u) d[q] *= f;
-      }
     }
     __syncwarp();
     {
@@ -936,6 +966,24 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (i + u * LG_THREADS < i_end) store_scores(gx + v[u], d + u * VEC, 1.f);
+  }
+  S::close();
+  if (lists) {  // the listed tokens
+    __syncthreads();
+    Table l = place_table(s_mem, a.d_bias_off != nullptr);
+    each_table(r, l, from, to - from, [&] {
+      const uint32_t used = *l.n_used;
+      for (uint32_t j = tid; j < used; j += LG_THREADS) {
+        const uint32_t s = l.used[j], t = l.key[s], fb = l.first ? l.first[s] : NO_BIAS;
+        const float dz = one(t, l.val[s], fb);
+        if (!gr.bias || (fb & NO_BIAS) == NO_BIAS) continue;
+        float* gb = gr.bias + (r.bias - a.d_bias);
+        gb[fb & NO_BIAS] = dz;
+        if (fb >> 31)
+          for (int e = (int)(fb & NO_BIAS) + 1; e < r.bias_n; ++e)
+            if ((uint32_t)r.bias_id[e] == t) gb[e] = dz;
+      }
+    });
   }
 }
 
@@ -972,10 +1020,13 @@ size_t stage_bytes(int dtype, bool shifted) {
   return shifted ? Stream<__half, true>::BYTES : Stream<__half, false>::BYTES;
 }
 
-// shared memory of a CTA: the scores in flight, the bits, the table of tokens with entries
-size_t shared_bytes(const tok_logits_args& a, bool shifted, int arrays, uint32_t words, bool lists) {
-  const size_t bits = (size_t)((a.d_mask ? 1 : 0) + (a.d_seen ? 1 : 0) + (lists ? 1 : 0)) * words * sizeof(uint32_t);
-  return arrays * stage_bytes(a.dtype, shifted) + bits + (lists ? lists_bytes(a.d_bias_off != nullptr) : 0);
+// bytes of shared memory for the scores in flight, later the table of listed tokens; the bits follow
+uint32_t front_bytes(const tok_logits_args& a, bool shifted, int arrays, bool lists) {
+  return (uint32_t)std::max(arrays * stage_bytes(a.dtype, shifted), lists ? table_bytes(a.d_bias_off != nullptr) : 0);
+}
+
+size_t bits_bytes(const tok_logits_args& a, uint32_t words, bool lists) {
+  return (size_t)((a.d_mask ? 1 : 0) + (a.d_seen ? 1 : 0) + (lists ? 1 : 0)) * words * sizeof(uint32_t);
 }
 
 // whether rows of an array lie like those of another towards 16-byte boundaries
@@ -1064,7 +1115,9 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream) tr
   c.per = (a->n_logits / vec + n - 1) / n;
   c.words = bit_words(c.per * vec);
   const bool shifted = a->d_out && !alike(a->d_logits, a->logits_stride, a->d_out, a->out_stride, a->rows, size_of(a->dtype));
-  const size_t smem = shared_bytes(*a, shifted, 1, c.words, c.lists);
+  c.in_place = a->d_out == a->d_logits;
+  c.bits_at = front_bytes(*a, shifted, 1, c.lists);
+  const size_t smem = c.bits_at + bits_bytes(*a, c.words, c.lists);
   const unsigned ctas = a->rows * n;
   const cudaError_t e = a->dtype == TOK_F32   ? launch_forward<float>(c, shifted, ctas, n, smem, s)
                         : a->dtype == TOK_F16 ? launch_forward<__half>(c, shifted, ctas, n, smem, s)
@@ -1100,7 +1153,8 @@ int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logit
   const bool shifted = !alike(a->d_logits, a->logits_stride, ga->d_grad_logits, ga->grad_logits_stride, a->rows, size) ||
                        (ga->d_grad_out && !alike(ga->d_grad_out, ga->grad_out_stride, ga->d_grad_logits,
                                                  ga->grad_logits_stride, a->rows, size));
-  const size_t smem = shared_bytes(*a, shifted, ga->d_grad_out ? 2 : 1, c.words, c.lists);
+  c.bits_at = front_bytes(*a, shifted, ga->d_grad_out ? 2 : 1, c.lists);
+  const size_t smem = c.bits_at + bits_bytes(*a, c.words, c.lists);
   const unsigned ctas = a->rows * c.ranks;
   const cudaError_t e = a->dtype == TOK_F32   ? launch_grad<float>(c, shifted, ctas, smem, s)
                         : a->dtype == TOK_F16 ? launch_grad<__half>(c, shifted, ctas, smem, s)
