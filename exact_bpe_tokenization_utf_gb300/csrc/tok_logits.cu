@@ -27,9 +27,7 @@ constexpr int LG_WARPS = LG_THREADS / 32;
 constexpr int PER = 16;           // scores per thread and step
 constexpr int STEP = LG_THREADS * PER;
 constexpr int EDGE = 16;          // places before a slice's first vector, for the scores that come before it (fewer)
-constexpr int TABLE = STEP + 64;  // slots of the table of tokens with entries
-constexpr int SLOTS = 4096;       // of them, where tokens are hashed
-constexpr int MOST_TOKENS = 3072; // tokens that it then takes
+constexpr int TABLE_STEP = STEP + 64;  // places of a table for one step: its scores and those outside the vectors
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float REF_MAX = 1e37f;  // references of a sum of exponentials stay within this
@@ -202,8 +200,10 @@ template <class T, bool SHIFTED> struct Stream {
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
     if (SHIFTED) __syncwarp();
   }
-  // before the slots serve as other memory
-  static __device__ __forceinline__ void close() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+  // score e of the u-th vector
+  __device__ __forceinline__ float score(uint32_t stage, uint32_t u, uint32_t e) const {
+    return Num<T>::get(*reinterpret_cast<const T*>(mine + stage * STAGE + u * SLOT + (SHIFTED ? shift : 0u) + e * sizeof(T)));
+  }
   __device__ __forceinline__ void scores(uint32_t stage, int u, float* z) const {
     const uint4* q = reinterpret_cast<const uint4*>(mine + stage * STAGE + u * SLOT);
     uint32_t w[5];
@@ -245,8 +245,6 @@ __device__ __forceinline__ void store_scores(T* to, const float* z, float factor
   __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-__device__ __forceinline__ bool bit_of(const uint32_t* words, uint32_t v) { return (__ldg(words + (v >> 5)) >> (v & 31)) & 1u; }
-
 // A slice's bits in shared memory, moved so that the bits of a vector lie in
 // one byte: bit p is that of token lo + p (lo modulo 2^32: it may be negative).
 __host__ __device__ constexpr uint32_t bit_words(uint32_t tokens) { return (tokens + 48 + 31) / 32; }
@@ -269,100 +267,85 @@ __device__ __forceinline__ uint32_t vector_bits(const uint32_t* bits, uint32_t i
   return (uint32_t)b[ii >> 1] >> (4 * (ii & 1u)) & 15u;
 }
 
-// The tokens of the lists (generated ids, biases).  A slice's main pass only
-// knows a bit for each and leaves them out; after it they are counted in a
-// table in shared memory (number of occurrences and the smallest index of the
-// bias entries, its top bit: there are more, or NO_BIAS) and scored one by one,
-// a thread each, all loads in flight at once.  A range of at most TABLE tokens
-// has a slot for each; a longer one is hashed (linear probing).  A table that
-// would hold more than MOST_TOKENS tokens is made for half of the range, and
-// so on down to a step's tokens, which fit.
+// The tokens of the lists (generated ids, biases).  For a range of steps a
+// table in shared memory has, for each token, the number of its occurrences
+// (16 bits where the row's list is no longer than they count) and the smallest
+// index of its bias entries (its top bit: there are more), or NO_BIAS; a bit
+// for each token says whether it has any.  A range is as many steps as the
+// table has room for; the lists are read once for each.
 constexpr uint32_t NO_BIAS = 0x7fffffffu;
-constexpr uint32_t NO_TOKEN = 0xffffffffu;
-static_assert(SLOTS <= TABLE && MOST_TOKENS + LG_THREADS < SLOTS, "sizes of the table");
 
 struct Table {
-  uint32_t* key;
-  uint32_t* val;    // occurrences, then the score
+  uint32_t* count;
   uint32_t* first;  // nullptr: no biases
-  uint16_t* used;   // the slots in use
-  uint32_t* n_used;
-  uint32_t from, n; // the range
-  uint32_t mask;    // hashed: slots - 1; 0: a slot for each token
+  uint32_t* bits;   // of the slice
+  uint32_t lo;      // token of bit 0 (modulo 2^32)
+  uint32_t base;    // token of the table's place 0 (modulo 2^32)
+  bool wide;        // counts of 32 bits
 };
 
-size_t table_bytes(bool bias) { return (TABLE * (bias ? 3 : 2) + 4) * sizeof(uint32_t) + TABLE * sizeof(uint16_t); }
+// bytes of a table: three steps of 16-bit counts, or two with biases (always room for one step of anything)
+constexpr uint32_t table_bytes(bool bias) { return TABLE_STEP * (bias ? 12u : 6u); }
 
-__device__ __forceinline__ Table place_table(void* mem, bool bias) {
-  Table l;
-  l.key = static_cast<uint32_t*>(mem);
-  l.val = l.key + TABLE;
-  l.first = bias ? l.key + 2 * TABLE : nullptr;
-  l.n_used = l.key + TABLE * (bias ? 3 : 2);
-  l.used = reinterpret_cast<uint16_t*>(l.n_used + 4);
-  l.from = l.n = l.mask = 0;
-  return l;
+__device__ __forceinline__ uint32_t range_steps(const Row& r, bool bias) {
+  const uint32_t per_token = (r.gen_len > 0xffff ? 4u : 2u) + (bias ? 4u : 0u);
+  return (table_bytes(bias) / per_token - 64) / STEP;
 }
 
-// f(i, ids[i]) for this thread's entries of a list, eight loads at a time
+// f(i, ids[i]) for this thread's entries of a list, four loads at a time
 template <class F>
 __device__ __forceinline__ void each_id(const int32_t* ids, int n, F f) {
-  for (int i0 = (int)threadIdx.x; i0 < n; i0 += 8 * LG_THREADS) {
-    int32_t id[8];
+  for (int i0 = (int)threadIdx.x; i0 < n; i0 += 4 * LG_THREADS) {
+    int32_t id[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) id[j] = i0 + j * LG_THREADS < n ? __ldg(ids + i0 + j * LG_THREADS) : -1;
-#pragma unroll 1
-    for (int j = 0; j < 8; ++j) {
-      // (rotated, so that the body stands here once)
-      const int32_t v = id[0];
+    for (int j = 0; j < 4; ++j) id[j] = i0 + j * LG_THREADS < n ? __ldg(ids + i0 + j * LG_THREADS) : -1;
 #pragma unroll
-      for (int q = 0; q < 7; ++q) id[q] = id[q + 1];
-      if (i0 + j * LG_THREADS < n) f(i0 + j * LG_THREADS, (uint32_t)v);
-    }
+    for (int j = 0; j < 4; ++j)
+      if (i0 + j * LG_THREADS < n) f(i0 + j * LG_THREADS, (uint32_t)id[j]);
   }
 }
 
-// the bits of the listed tokens among from .. from + n - 1; bit 0 is token lo
-__device__ __forceinline__ void list_bits(const Row& r, uint32_t* bits, uint32_t lo, uint32_t from, uint32_t n) {
-  auto one = [&](int, uint32_t v) {
-    if (v - from < n) atomicOr(&bits[(v - lo) >> 5], 1u << ((v - lo) & 31));
-  };
-  each_id(r.gen, r.gen_len, one);
-  each_id(r.bias_id, r.bias_n, one);
-}
-
-__device__ __forceinline__ uint32_t first_slot(const Table& l, uint32_t v) { return (v * 0x9E3779B1u >> 16) & l.mask; }
-
-// the slot of a token that is in the table
-__device__ __forceinline__ uint32_t slot_of(const Table& l, uint32_t v) {
-  if (l.mask == 0) return v - l.from;
-  uint32_t s = first_slot(l, v);
-  while (l.key[s] != v) s = (s + 1) & l.mask;
-  return s;
-}
-
-// a token's slot, taken if it has none; NO_TOKEN: the table is full
-__device__ __forceinline__ uint32_t take_slot(const Table& l, uint32_t v) {
-  uint32_t s = l.mask ? first_slot(l, v) : v - l.from;
-  for (;;) {
-    uint32_t k = *static_cast<volatile uint32_t*>(l.key + s);
-    if (k == NO_TOKEN) {
-      k = atomicCAS(&l.key[s], NO_TOKEN, v);
-      if (k == NO_TOKEN) {
-        // one addition for all threads of the warp that are here
-        const uint32_t here = __activemask(), lane = threadIdx.x & 31u, first = (uint32_t)__ffs((int)here) - 1u;
-        uint32_t n = 0;
-        if (lane == first) n = atomicAdd(l.n_used, (uint32_t)__popc(here));
-        n = __shfl_sync(here, n, (int)first) + (uint32_t)__popc(here & ((1u << lane) - 1u));
-        if (l.mask && n >= MOST_TOKENS) return NO_TOKEN;  // (at most one per thread beyond: slots stay free)
-        l.used[n] = (uint16_t)s;
-        return s;
+// The table of the tokens from .. from + n - 1 (n at most what it has room for).
+__device__ __forceinline__ void fill_table(const Row& r, Table& t, void* mem, bool bias, uint32_t base, uint32_t from,
+                                           uint32_t n) {
+  t.wide = r.gen_len > 0xffff;
+  t.base = base;
+  t.count = static_cast<uint32_t*>(mem);
+  const uint32_t places = from + n - base, words = t.wide ? places : (places + 1) / 2;
+  t.first = bias ? t.count + words : nullptr;
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < words; i += LG_THREADS) t.count[i] = 0;
+  if (bias)
+    for (uint32_t i = threadIdx.x; i < places; i += LG_THREADS) t.first[i] = NO_BIAS;
+  __syncthreads();
+  each_id(r.gen, r.gen_len, [&](int, uint32_t v) {
+    if (v - from < n) {
+      const uint32_t at = v - base, bit = v - t.lo;
+      atomicAdd(&t.count[t.wide ? at : at >> 1], t.wide ? 1u : 1u << (16 * (at & 1u)));
+      atomicOr(&t.bits[bit >> 5], 1u << (bit & 31));
+    }
+  });
+  if (bias && r.bias_n) {
+    each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
+      if (v - from < n) {
+        const uint32_t bit = v - t.lo;
+        atomicMin(&t.first[v - base], (uint32_t)i);
+        atomicOr(&t.bits[bit >> 5], 1u << (bit & 31));
       }
-    }
-    if (k == v) return s;
-    s = (s + 1) & l.mask;
+    });
+    __syncthreads();
+    each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
+      if (v - from < n && (t.first[v - base] & NO_BIAS) != (uint32_t)i) atomicOr(&t.first[v - base], 0x80000000u);
+    });
   }
+  __syncthreads();
 }
+
+__device__ __forceinline__ uint32_t count_of(const Table& t, uint32_t v) {
+  const uint32_t at = v - t.base;
+  return t.wide ? t.count[at] : t.count[at >> 1] >> (16 * (at & 1u)) & 0xffffu;
+}
+__device__ __forceinline__ uint32_t first_of(const Table& t, uint32_t v) { return t.first ? t.first[v - t.base] : NO_BIAS; }
 
 // The score of a token with c occurrences and bias entries from fb on, from
 // its logit; with the divisions and the order of the definition, so that equal
@@ -381,71 +364,6 @@ __device__ __forceinline__ float score(const Row& r, uint32_t v, uint32_t c, uin
     x = __fadd_rn(x, s);
   }
   return x;
-}
-
-// The table of the tokens from .. from + n - 1, entries counted.  False (in
-// every thread): it is too small for them.
-__device__ __forceinline__ bool fill_table(const Row& r, Table& l, uint32_t from, uint32_t n) {
-  uint32_t slots = n;
-  l.from = from;
-  l.n = n;
-  l.mask = 0;
-  if (n > TABLE) {
-    const uint32_t entries = (uint32_t)r.gen_len + (uint32_t)r.bias_n;
-    slots = 256;
-    while (slots < SLOTS && slots / 2 < entries) slots *= 2;
-    l.mask = slots - 1;
-  }
-  __syncthreads();
-  for (uint32_t i = threadIdx.x; i < slots; i += LG_THREADS) {
-    l.key[i] = NO_TOKEN;
-    l.val[i] = 0;
-    if (l.first) l.first[i] = NO_BIAS;
-  }
-  if (threadIdx.x == 0) *l.n_used = 0;
-  __syncthreads();
-  bool full = false;
-  each_id(r.gen, r.gen_len, [&](int, uint32_t v) {
-    if (v - from < n && !full) {
-      const uint32_t s = take_slot(l, v);
-      if (s == NO_TOKEN) full = true;
-      else atomicAdd(&l.val[s], 1u);
-    }
-  });
-  if (l.first)
-    each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
-      if (v - from < n && !full) {
-        const uint32_t s = take_slot(l, v);
-        if (s == NO_TOKEN) full = true;
-        else atomicMin(&l.first[s], (uint32_t)i);
-      }
-    });
-  if (__syncthreads_or(full)) return false;
-  if (l.first && r.bias_n > 1) {
-    each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
-      if (v - from < n) {
-        const uint32_t s = slot_of(l, v);
-        if ((l.first[s] & NO_BIAS) != (uint32_t)i) atomicOr(&l.first[s], 0x80000000u);
-      }
-    });
-    __syncthreads();
-  }
-  return true;
-}
-
-// Calls per_table() with the table of each part of the tokens from .. from + n - 1.
-template <class F>
-__device__ __forceinline__ void each_table(const Row& r, Table& l, uint32_t from, uint32_t n, F per_table) {
-  uint32_t range = n;
-  for (uint32_t at = from; at - from < n;) {
-    const uint32_t m = min(range, n - (at - from));
-    if (!fill_table(r, l, at, m)) {
-      range = (m + 1) / 2;
-      continue;
-    }
-    per_table();
-    at += m;
-  }
 }
 
 // The repetition penalty of a thread's seen scores, as a product with its
@@ -485,13 +403,16 @@ __device__ __forceinline__ void join_sum(float& ref, float& sum, float ref2, flo
   ref = m;
 }
 
+// the two halves of a cluster's barrier
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 struct LogitsCall {
   tok_logits_args a;
   uint32_t per;    // vectors per CTA
   uint32_t words;  // of a slice's bits
   uint32_t bits_at; // where they are in shared memory
   int lists;       // there are generated ids or biases
-  int in_place;    // out is logits
 };
 
 // Forward.  A row is cut into the slices of a cluster's CTAs (one CTA: the
@@ -506,11 +427,12 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
   extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ Part s_part[16];
   __shared__ float s_ref[LG_WARPS], s_sum[LG_WARPS], s_z_pick;
-  __shared__ unsigned long long s_key, s_list_key, s_total[LG_WARPS];
+  __shared__ unsigned long long s_key;
   __shared__ float s_best;  // a score that some token of this CTA has: what is below it is not the top
   const tok_logits_args& a = call.a;
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t rank = cluster.block_rank(), n_ranks = cluster.num_blocks();
+  if (n_ranks > 1) cluster_arrive();  // (waited for before another CTA's shared memory is written)
   const uint32_t b = blockIdx.x / n_ranks, tid = threadIdx.x, lane = tid & 31u;
   const T* x = static_cast<const T*>(a.d_logits) + (long long)b * a.logits_stride;
   T* out = a.d_out ? static_cast<T*>(a.d_out) + (long long)b * a.out_stride : nullptr;
@@ -538,11 +460,11 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
   // the slice's tokens: those of its vectors, the first slice's from the row's start, the last one's to its end
   const uint32_t from = rank == 0 ? 0u : g.v0 + i_begin * VEC;
   const uint32_t to = rank == n_ranks - 1 ? a.n_logits : g.v0 + i_end * VEC;
-  if (lists) {
+  if (lists)
     for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
-    __syncthreads();
-    list_bits(r, l_bits, lo, from, to - from);
-  }
+  Table table{};
+  table.bits = l_bits;
+  table.lo = lo;
   const uint32_t pick = a.d_pick ? (uint32_t)a.d_pick[b] : 0xffffffffu;
   const float k = r.inv_t * LOG2E;
   if (tid == 0) {
@@ -550,7 +472,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
     s_best = -INFINITY;
     s_z_pick = -INFINITY;
   }
-  cluster.sync();  // (every CTA of the cluster runs before its shared memory is written)
+  __syncthreads();
 
   // the bits of a thread's vectors from i on
   auto bits_at = [&](const uint32_t* bits, uint32_t i) {
@@ -571,31 +493,45 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
 
   float ref = -REF_MAX, sum = 0.f;
   const uint32_t steps = max(1u, (i_end - i_begin + U * LG_THREADS - 1) / (U * LG_THREADS));
-  uint32_t stage = 0;
-  if (tid < 32) {  // the scores outside the vectors
-    const uint32_t head = g.v0 + i_begin * VEC - from, n = head + (to - (g.v0 + i_end * VEC));
-    if (tid < n) {
-      const uint32_t t = tid < head ? from + tid : g.v0 + i_end * VEC + (tid - head), at = t - lo;
-      if (!lists || !(l_bits[at >> 5] >> (at & 31) & 1u)) {
-        float z = -INFINITY;
-        if (!r.none && (!r.mask || bit_of(r.mask, t))) {
-          z = score(r, t, 0, NO_BIAS, r.seen && bit_of(r.seen, t), Num<T>::get(x[t]));
-          const float y = z * k;
-          if (y > ref + 24.f) {
-            ref = fminf(y, REF_MAX);
-            sum = 0.f;
-          }
-          sum += ex2(fmaf(z, k, -ref));
-          atomicMax(&s_key, top_key(z, t));
-        }
-        if (out) out[t] = Num<T>::put(z * r.inv_t);
-        if (t == pick) s_z_pick = z;
-      }
+  const uint32_t range = lists ? range_steps(r, a.d_bias_off != nullptr) : steps;
+  uint32_t stage = 0, next = 0;
+  // one score outside the vectors or of a listed token, into the sum; the top is left to the caller
+  auto one = [&](float z) {
+    const float y = z * k;
+    if (y > ref + 24.f) {
+      const float m = fminf(y, REF_MAX);
+      sum *= ex2(ref - m);
+      ref = m;
     }
-  }
+    sum += ex2(fmaf(z, k, -ref));
+  };
 #pragma unroll 1
   for (uint32_t step = 0; step < steps; ++step) {
-    const uint32_t i = i_begin + step * (U * LG_THREADS) + tid;
+    const uint32_t ib = i_begin + step * (U * LG_THREADS), i = ib + tid;
+    if (step == next) {
+      // the scores of this range: its vectors, the first with those before all vectors, the last with those after
+      next = step + range;
+      const uint32_t i1 = next < steps ? ib + range * (U * LG_THREADS) : i_end;
+      const uint32_t from1 = step == 0 ? from : g.v0 + ib * VEC, to1 = next < steps ? g.v0 + i1 * VEC : to;
+      if (lists)
+        fill_table(r, table, s_mem + S::BYTES, a.d_bias_off != nullptr, g.v0 + ib * VEC - EDGE, from1, to1 - from1);
+      if (tid < 32) {  // the scores outside the vectors
+        const uint32_t head = g.v0 + ib * VEC - from1, n = head + (to1 - (g.v0 + i1 * VEC));
+        if (tid < n) {
+          const uint32_t t = tid < head ? from1 + tid : g.v0 + i1 * VEC + (tid - head), at = t - lo;
+          float z = -INFINITY;
+          if (!r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u))) {
+            const bool special = lists && (l_bits[at >> 5] >> (at & 31) & 1u);
+            z = score(r, t, special ? count_of(table, t) : 0, special ? first_of(table, t) : NO_BIAS,
+                      r.seen && (s_bits[at >> 5] >> (at & 31) & 1u), Num<T>::get(x[t]));
+            one(z);
+            atomicMax(&s_key, top_key(z, t));
+          }
+          if (out) out[t] = Num<T>::put(z * r.inv_t);
+          if (t == pick) s_z_pick = z;
+        }
+      }
+    }
     uint32_t v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = g.v0 + (i + u * LG_THREADS) * VEC;
@@ -628,59 +564,50 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
 #pragma unroll
       for (int q = 0; q < PER; ++q) z[q] = -INFINITY;
     }
+    if (out) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u * LG_THREADS < i_end) store_scores(out + v[u], z + u * VEC, r.inv_t);
+    }
     // scores that may be the largest, once more and exactly
     const float best = *static_cast<volatile float*>(&s_best);
     const float near = best < INFINITY ? best - fabsf(best) * 0x1p-20f : best;
+    unsigned long long key = 0;
     if (__any_sync(0xffffffffu, vmax > -INFINITY && vmax >= near)) {
       float wmax = vmax;
 #pragma unroll
       for (int o = 16; o; o >>= 1) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, o));
       const float at_least = fmaxf(near, wmax - fabsf(wmax) * 0x1p-20f);
       if (vmax >= at_least) {
-        unsigned long long key = 0;
         uint32_t m = 0;
 #pragma unroll
         for (int q = 0; q < PER; ++q) m |= (z[q] >= at_least && z[q] > -INFINITY ? 1u : 0u) << q;
         for (; m; m &= m - 1) {
           const uint32_t q = (uint32_t)__ffs((int)m) - 1u, t = v[0] + q / VEC * (LG_THREADS * VEC) + q % VEC;
-          float zx = 0.f;
-          if ((seen >> q) & 1u) {
-            zx = score(r, t, 0, NO_BIAS, true, Num<T>::get(x[t]));
-          } else {
-#pragma unroll
-            for (int p = 0; p < PER; ++p)
-              if (p == (int)q) zx = z[p];
-          }
-          key = max(key, top_key(zx, t));
+          key = max(key, top_key(score(r, t, 0, NO_BIAS, (seen >> q) & 1u, in.score(stage, q / VEC, q % VEC)), t));
         }
-        atomicMax(&s_key, key);
-        const float zx = key_score(key);
-        if (zx > best) s_best = zx;
       }
+    }
+    // the listed tokens
+    for (uint32_t m = special & loaded; m; m &= m - 1) {
+      const uint32_t q = (uint32_t)__ffs((int)m) - 1u, t = v[0] + q / VEC * (LG_THREADS * VEC) + q % VEC;
+      const float zs = score(r, t, count_of(table, t), first_of(table, t), (seen >> q) & 1u, in.score(stage, q / VEC, q % VEC));
+      one(zs);
+      if (zs >= best) key = max(key, top_key(zs, t));
+      if (out) out[t] = Num<T>::put(zs * r.inv_t);
+      if (t == pick) s_z_pick = zs;
+    }
+    if (key) {
+      atomicMax(&s_key, key);
+      const float zx = key_score(key);
+      if (zx > best) s_best = zx;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (pick - v[u] < (uint32_t)VEC && i + u * LG_THREADS < i_end) {
-        const uint32_t q = u * VEC + (pick - v[u]);
-        if ((allowed >> q) & 1u) s_z_pick = score(r, pick, 0, NO_BIAS, (seen >> q) & 1u, Num<T>::get(x[pick]));
+        const uint32_t e = pick - v[u], q = u * VEC + e;
+        if ((allowed >> q) & 1u) s_z_pick = score(r, pick, 0, NO_BIAS, (seen >> q) & 1u, in.score(stage, u, e));
       }
-    // (out may be the logits, which the lines above read again; those of listed tokens are still needed then)
-    if (out) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + u * LG_THREADS < i_end) {
-          if (call.in_place && (special & loaded) >> (u * VEC) & ((1u << VEC) - 1u)) {
-            float xs[VEC];
-            in.scores(stage, u, xs);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-              if (!((special & loaded) >> (u * VEC + e) & 1u)) xs[e] = z[u * VEC + e] * r.inv_t;
-            store_scores(out + v[u], xs, 1.f);
-          } else {
-            store_scores(out + v[u], z + u * VEC, r.inv_t);
-          }
-        }
-    }
     // this stage's slots are free: the step DEPTH later
     __syncwarp();
     {
@@ -695,8 +622,6 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
     }
   }
 
-  S::close();
-
   // the CTA's sum, then the cluster's, and the row's results
 #pragma unroll
   for (int o = 16; o; o >>= 1)
@@ -706,47 +631,9 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
     s_sum[tid >> 5] = sum;
   }
   __syncthreads();
-  if (tid == 0)
-    for (int w = 1; w < LG_WARPS; ++w) join_sum(ref, sum, s_ref[w], s_sum[w]);
-  // The listed tokens.  Which thread scores which of them depends on the order
-  // of the table's atomics, so their exponentials are added up as whole
-  // numbers, in units of 2^-40 of the largest one.
-  if (lists) {
-    Table l = place_table(s_mem, a.d_bias_off != nullptr);
-    each_table(r, l, from, to - from, [&] {
-      const uint32_t used = *l.n_used;
-      if (tid == 0) s_list_key = 0;
-      __syncthreads();
-      bool nan = false;
-      for (uint32_t j = tid; j < used; j += LG_THREADS) {
-        const uint32_t s = l.used[j], t = l.key[s], at = t - lo;
-        float z = -INFINITY;
-        if (!r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u)))
-          z = score(r, t, l.val[s], l.first ? l.first[s] : NO_BIAS, r.seen && (s_bits[at >> 5] >> (at & 31) & 1u),
-                    Num<T>::get(x[t]));
-        l.val[s] = __float_as_uint(z);
-        nan |= z != z;
-        atomicMax(&s_list_key, top_key(z, t));
-        if (t == pick) s_z_pick = z;
-        if (out) out[t] = Num<T>::put(z * r.inv_t);
-      }
-      nan = __syncthreads_or(nan);
-      const float m = fmaxf(fminf(key_score(s_list_key) * k, REF_MAX), -REF_MAX);
-      unsigned long long total = 0;
-      for (uint32_t j = tid; j < used; j += LG_THREADS)
-        total += (unsigned long long)(fminf(ex2(fmaf(__uint_as_float(l.val[l.used[j]]), k, -m)), 1.f) * 0x1p40f);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-      if (lane == 0) s_total[tid >> 5] = total;
-      __syncthreads();
-      if (tid == 0) {
-        for (int w = 1; w < LG_WARPS; ++w) total += s_total[w];
-        join_sum(ref, sum, m, nan ? NAN : (float)total * 0x1p-40f);
-        s_key = max(s_key, s_list_key);
-      }
-    });
-  }
+  if (n_ranks > 1) cluster_wait();
   if (tid == 0) {
+    for (int w = 1; w < LG_WARPS; ++w) join_sum(ref, sum, s_ref[w], s_sum[w]);
     Part* parts = n_ranks == 1 ? s_part : cluster.map_shared_rank(s_part, 0);
     parts[rank] = Part{s_key, ref, sum, s_z_pick};
   }
@@ -777,7 +664,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
 struct GradCall {
   tok_logits_args a;
   Grad g;
-  uint32_t per, words, bits_at, ranks;
+  uint32_t per, words, table_at, bits_at, ranks;
   int lists;
 };
 
@@ -825,11 +712,11 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
   if (r.seen) move_bits(s_bits, r.seen, a.n_logits, lo, call.words);
   const uint32_t from = rank == 0 ? 0u : g.v0 + i_begin * VEC;
   const uint32_t to = rank == call.ranks - 1 ? a.n_logits : g.v0 + i_end * VEC;
-  if (lists) {
+  if (lists)
     for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
-    __syncthreads();
-    list_bits(r, l_bits, lo, from, to - from);
-  }
+  Table table{};
+  table.bits = l_bits;
+  table.lo = lo;
   const float glp = gr.logprob ? gr.logprob[b] : 0.f;
   float cp = (gr.lse ? gr.lse[b] : 0.f) - glp, lse = 0.f;
   if (gr.lse || gr.logprob) lse = a.d_lse[b];
@@ -876,35 +763,48 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
   auto allowed_at = [&](uint32_t i) { return r.none ? 0u : r.mask ? bits_at(m_bits, i) : inside(i); };
 
   const uint32_t steps = max(1u, (i_end - i_begin + U * LG_THREADS - 1) / (U * LG_THREADS));
-  uint32_t stage = 0;
-  // one score's gradient; c, fb: its entries in the lists.  Returns that before the repetition penalty.
-  auto one = [&](uint32_t t, uint32_t c, uint32_t fb) {
+  const uint32_t range = lists ? range_steps(r, a.d_bias_off != nullptr) : steps;
+  uint32_t stage = 0, next = 0;
+  // the gradient of one score; special: with its entries in the lists, whose biases' gradients are written too
+  auto one = [&](uint32_t t, bool allowed, bool seen, bool special, float xt, float gt) {
+    const uint32_t c = special ? count_of(table, t) : 0, fb = special ? first_of(table, t) : NO_BIAS;
     float dz = 0.f, f = 1.f;
-    const uint32_t at = t - lo;
-    if (!r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u))) {
-      const bool seen = r.seen && (s_bits[at >> 5] >> (at & 31) & 1u);
-      const float xt = Num<T>::get(x[t]);
+    if (allowed) {
       if (seen || c) f = xt > 0.f ? r.inv_rep : r.rep;
-      dz = d_score(score(r, t, c, fb, seen, xt), go ? Num<T>::get(go[t]) : 0.f);
+      dz = d_score(score(r, t, c, fb, seen, xt), gt);
       if (t == pick) dz = fmaf(glp, r.inv_t, dz);
     }
     gx[t] = Num<T>::put(dz * f);
-    return dz;
-  };
-  if (tid < 32) {  // the scores outside the vectors
-    const uint32_t head = g.v0 + i_begin * VEC - from, n = head + (to - (g.v0 + i_end * VEC));
-    if (tid < n) {
-      const uint32_t t = tid < head ? from + tid : g.v0 + i_end * VEC + (tid - head), at = t - lo;
-      if (!lists || !(l_bits[at >> 5] >> (at & 31) & 1u)) one(t, 0, NO_BIAS);
+    if (gr.bias && (fb & NO_BIAS) != NO_BIAS) {
+      float* gb = gr.bias + (r.bias - a.d_bias);
+      gb[fb & NO_BIAS] = dz;
+      if (fb >> 31)
+        for (int e = (int)(fb & NO_BIAS) + 1; e < r.bias_n; ++e)
+          if ((uint32_t)r.bias_id[e] == t) gb[e] = dz;
     }
-  }
+  };
 #pragma unroll 1
   for (uint32_t step = 0; step < steps; ++step) {
-    const uint32_t i = i_begin + step * (U * LG_THREADS) + tid;
+    const uint32_t ib = i_begin + step * (U * LG_THREADS), i = ib + tid;
+    if (step == next) {
+      next = step + range;
+      const uint32_t i1 = next < steps ? ib + range * (U * LG_THREADS) : i_end;
+      const uint32_t from1 = step == 0 ? from : g.v0 + ib * VEC, to1 = next < steps ? g.v0 + i1 * VEC : to;
+      if (lists)
+        fill_table(r, table, s_mem + call.table_at, a.d_bias_off != nullptr, g.v0 + ib * VEC - EDGE, from1, to1 - from1);
+      if (tid < 32) {  // the scores outside the vectors
+        const uint32_t head = g.v0 + ib * VEC - from1, n = head + (to1 - (g.v0 + i1 * VEC));
+        if (tid < n) {
+          const uint32_t t = tid < head ? from1 + tid : g.v0 + i1 * VEC + (tid - head), at = t - lo;
+          one(t, !r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u)), r.seen && (s_bits[at >> 5] >> (at & 31) & 1u),
+              lists && (l_bits[at >> 5] >> (at & 31) & 1u), Num<T>::get(x[t]), go ? Num<T>::get(go[t]) : 0.f);
+        }
+      }
+    }
     uint32_t v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = g.v0 + (i + u * LG_THREADS) * VEC;
-    const uint32_t allowed = allowed_at(i) & ~(lists ? bits_at(l_bits, i) : 0u);
+    const uint32_t special = lists ? bits_at(l_bits, i) : 0u, loaded = allowed_at(i), allowed = loaded & ~special;
     const uint32_t seen = r.seen ? bits_at(s_bits, i) : 0u;
     S::wait();
     float z[PER], d[PER];
@@ -949,6 +849,16 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
 #pragma unroll
       for (int q = 0; q < PER; ++q) d[q] = 0.f;
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * LG_THREADS < i_end) store_scores(gx + v[u], d + u * VEC, 1.f);
+    // the listed tokens
+    for (uint32_t m = special; m; m &= m - 1) {
+      const uint32_t q = (uint32_t)__ffs((int)m) - 1u, u = q / VEC, e = q % VEC;
+      const bool ok = (loaded >> q) & 1u;
+      one(v[0] + u * (LG_THREADS * VEC) + e, ok, (seen >> q) & 1u, true, ok ? in.score(stage, u, e) : 0.f,
+          ok && go ? gin.score(stage, u, e) : 0.f);
+    }
     __syncwarp();
     {
       const uint32_t later = i + DEPTH * U * LG_THREADS;
@@ -963,27 +873,6 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
       S::commit();
       stage = stage + 1 == DEPTH ? 0 : stage + 1;
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * LG_THREADS < i_end) store_scores(gx + v[u], d + u * VEC, 1.f);
-  }
-  S::close();
-  if (lists) {  // the listed tokens
-    __syncthreads();
-    Table l = place_table(s_mem, a.d_bias_off != nullptr);
-    each_table(r, l, from, to - from, [&] {
-      const uint32_t used = *l.n_used;
-      for (uint32_t j = tid; j < used; j += LG_THREADS) {
-        const uint32_t s = l.used[j], t = l.key[s], fb = l.first ? l.first[s] : NO_BIAS;
-        const float dz = one(t, l.val[s], fb);
-        if (!gr.bias || (fb & NO_BIAS) == NO_BIAS) continue;
-        float* gb = gr.bias + (r.bias - a.d_bias);
-        gb[fb & NO_BIAS] = dz;
-        if (fb >> 31)
-          for (int e = (int)(fb & NO_BIAS) + 1; e < r.bias_n; ++e)
-            if ((uint32_t)r.bias_id[e] == t) gb[e] = dz;
-      }
-    });
   }
 }
 
@@ -1018,11 +907,6 @@ uint32_t slices(const tok_handle* h, const tok_logits_args& a) {
 size_t stage_bytes(int dtype, bool shifted) {
   if (dtype == TOK_F32) return shifted ? Stream<float, true>::BYTES : Stream<float, false>::BYTES;
   return shifted ? Stream<__half, true>::BYTES : Stream<__half, false>::BYTES;
-}
-
-// bytes of shared memory for the scores in flight, later the table of listed tokens; the bits follow
-uint32_t front_bytes(const tok_logits_args& a, bool shifted, int arrays, bool lists) {
-  return (uint32_t)std::max(arrays * stage_bytes(a.dtype, shifted), lists ? table_bytes(a.d_bias_off != nullptr) : 0);
 }
 
 size_t bits_bytes(const tok_logits_args& a, uint32_t words, bool lists) {
@@ -1115,8 +999,7 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream) tr
   c.per = (a->n_logits / vec + n - 1) / n;
   c.words = bit_words(c.per * vec);
   const bool shifted = a->d_out && !alike(a->d_logits, a->logits_stride, a->d_out, a->out_stride, a->rows, size_of(a->dtype));
-  c.in_place = a->d_out == a->d_logits;
-  c.bits_at = front_bytes(*a, shifted, 1, c.lists);
+  c.bits_at = (uint32_t)stage_bytes(a->dtype, shifted) + (c.lists ? table_bytes(a->d_bias_off != nullptr) : 0);
   const size_t smem = c.bits_at + bits_bytes(*a, c.words, c.lists);
   const unsigned ctas = a->rows * n;
   const cudaError_t e = a->dtype == TOK_F32   ? launch_forward<float>(c, shifted, ctas, n, smem, s)
@@ -1153,7 +1036,8 @@ int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logit
   const bool shifted = !alike(a->d_logits, a->logits_stride, ga->d_grad_logits, ga->grad_logits_stride, a->rows, size) ||
                        (ga->d_grad_out && !alike(ga->d_grad_out, ga->grad_out_stride, ga->d_grad_logits,
                                                  ga->grad_logits_stride, a->rows, size));
-  c.bits_at = front_bytes(*a, shifted, ga->d_grad_out ? 2 : 1, c.lists);
+  c.table_at = (uint32_t)stage_bytes(a->dtype, shifted) * (ga->d_grad_out ? 2 : 1);
+  c.bits_at = c.table_at + (c.lists ? table_bytes(a->d_bias_off != nullptr) : 0);
   const size_t smem = c.bits_at + bits_bytes(*a, c.words, c.lists);
   const unsigned ctas = a->rows * c.ranks;
   const cudaError_t e = a->dtype == TOK_F32   ? launch_grad<float>(c, shifted, ctas, smem, s)
