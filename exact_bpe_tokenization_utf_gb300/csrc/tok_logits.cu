@@ -17,6 +17,7 @@
 #include <cfloat>
 
 #include "tok_handle.cuh"
+#include "tok_scan.cuh"
 
 namespace tokgb {
 namespace {
@@ -27,7 +28,7 @@ constexpr int LG_WARPS = LG_THREADS / 32;
 constexpr int PER = 16;           // scores per thread and step
 constexpr int STEP = LG_THREADS * PER;
 constexpr int EDGE = 16;          // places before a slice's first vector, for the scores that come before it (fewer)
-constexpr int TABLE_STEP = STEP + 64;  // places of a table for one step: its scores and those outside the vectors
+constexpr int TABLE = STEP + 64;  // listed tokens of a table: at least as many as a step has scores
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float REF_MAX = 1e37f;  // references of a sum of exponentials stay within this
@@ -80,6 +81,36 @@ __device__ __forceinline__ float ex2_small(float x) {
   float y;
   asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// two 32-bit operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c;"
+      " mov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 struct Grad {
@@ -241,7 +272,10 @@ template <class T>
 __device__ __forceinline__ void store_scores(T* to, const float* z, float factor) {
   uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < Num<T>::VEC / 2; ++e) Num<T>::put_pair(w, e, z[2 * e] * factor, z[2 * e + 1] * factor);
+  for (int e = 0; e < Num<T>::VEC / 2; ++e) {
+    const float2 y = mul2(make_float2(z[2 * e], z[2 * e + 1]), make_float2(factor, factor));
+    Num<T>::put_pair(w, e, y.x, y.y);
+  }
   __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
@@ -267,30 +301,26 @@ __device__ __forceinline__ uint32_t vector_bits(const uint32_t* bits, uint32_t i
   return (uint32_t)b[ii >> 1] >> (4 * (ii & 1u)) & 15u;
 }
 
-// The tokens of the lists (generated ids, biases).  For a range of steps a
-// table in shared memory has, for each token, the number of its occurrences
-// (16 bits where the row's list is no longer than they count) and the smallest
-// index of its bias entries (its top bit: there are more), or NO_BIAS; a bit
-// for each token says whether it has any.  A range is as many steps as the
-// table has room for; the lists are read once for each.
+// The tokens of the lists (generated ids, biases) have a bit each in a slice;
+// the number of bits before a token's is its place in a table with the number
+// of its occurrences and the smallest index of its bias entries (its top bit:
+// there are more), or NO_BIAS.  The table holds TABLE tokens: where a slice
+// lists more, it is made for as many steps as it has room for, at least one.
+// The main pass leaves listed tokens out; each warp collects those that it
+// meets and scores 32 of them at a time.
 constexpr uint32_t NO_BIAS = 0x7fffffffu;
+constexpr int QUEUE = 64;  // collected tokens of a warp
 
 struct Table {
   uint32_t* count;
-  uint32_t* first;  // nullptr: no biases
-  uint32_t* bits;   // of the slice
-  uint32_t lo;      // token of bit 0 (modulo 2^32)
-  uint32_t base;    // token of the table's place 0 (modulo 2^32)
-  bool wide;        // counts of 32 bits
+  uint32_t* first;   // nullptr: no biases
+  uint32_t* bits;    // of the slice
+  uint32_t* before;  // bits before each word of them
+  uint32_t lo;       // token of bit 0 (modulo 2^32)
+  uint32_t base;     // place of the first token of the table
 };
 
-// bytes of a table: three steps of 16-bit counts, or two with biases (always room for one step of anything)
-constexpr uint32_t table_bytes(bool bias) { return TABLE_STEP * (bias ? 12u : 6u); }
-
-__device__ __forceinline__ uint32_t range_steps(const Row& r, bool bias) {
-  const uint32_t per_token = (r.gen_len > 0xffff ? 4u : 2u) + (bias ? 4u : 0u);
-  return (table_bytes(bias) / per_token - 64) / STEP;
-}
+constexpr uint32_t table_bytes(bool bias) { return TABLE * (bias ? 8u : 4u); }
 
 // f(i, ids[i]) for this thread's entries of a list, four loads at a time
 template <class F>
@@ -305,47 +335,82 @@ __device__ __forceinline__ void each_id(const int32_t* ids, int n, F f) {
   }
 }
 
-// The table of the tokens from .. from + n - 1 (n at most what it has room for).
-__device__ __forceinline__ void fill_table(const Row& r, Table& t, void* mem, bool bias, uint32_t base, uint32_t from,
-                                           uint32_t n) {
-  t.wide = r.gen_len > 0xffff;
-  t.base = base;
-  t.count = static_cast<uint32_t*>(mem);
-  const uint32_t places = from + n - base, words = t.wide ? places : (places + 1) / 2;
-  t.first = bias ? t.count + words : nullptr;
+// the bits of the slice's listed tokens, from .. from + n - 1, and their sums
+__device__ __forceinline__ void list_bits(const Row& r, const Table& t, uint32_t words, uint32_t from, uint32_t n,
+                                          uint32_t* sh) {
+  auto one = [&](int, uint32_t v) {
+    const uint32_t bit = v - t.lo;
+    if (v - from < n) atomicOr(&t.bits[bit >> 5], 1u << (bit & 31));
+  };
+  each_id(r.gen, r.gen_len, one);
+  each_id(r.bias_id, r.bias_n, one);
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < words; i += LG_THREADS) t.count[i] = 0;
-  if (bias)
-    for (uint32_t i = threadIdx.x; i < places; i += LG_THREADS) t.first[i] = NO_BIAS;
+  const uint32_t each = (words + LG_THREADS - 1) / LG_THREADS, w0 = min(threadIdx.x * each, words), w1 = min(w0 + each, words);
+  uint32_t sum = 0, total;
+  for (uint32_t w = w0; w < w1; ++w) sum += (uint32_t)__popc(t.bits[w]);
+  sum = block_excl_sum(sum, &total, sh);
+  for (uint32_t w = w0; w < w1; ++w) {
+    t.before[w] = sum;
+    sum += (uint32_t)__popc(t.bits[w]);
+  }
+  if (threadIdx.x == 0) t.before[words] = total;
+  __syncthreads();
+}
+
+// listed tokens before v
+__device__ __forceinline__ uint32_t place_of(const Table& t, uint32_t v) {
+  const uint32_t bit = v - t.lo;
+  return t.before[bit >> 5] + (uint32_t)__popc(t.bits[bit >> 5] & ((1u << (bit & 31)) - 1u));
+}
+
+// The table of the listed tokens from place t.base on, n of them.
+__device__ __forceinline__ void fill_table(const Row& r, const Table& t, uint32_t from, uint32_t n_tokens, uint32_t n) {
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < n; i += LG_THREADS) {
+    t.count[i] = 0;
+    if (t.first) t.first[i] = NO_BIAS;
+  }
   __syncthreads();
   each_id(r.gen, r.gen_len, [&](int, uint32_t v) {
-    if (v - from < n) {
-      const uint32_t at = v - base, bit = v - t.lo;
-      atomicAdd(&t.count[t.wide ? at : at >> 1], t.wide ? 1u : 1u << (16 * (at & 1u)));
-      atomicOr(&t.bits[bit >> 5], 1u << (bit & 31));
-    }
+    if (v - from < n_tokens) atomicAdd(&t.count[place_of(t, v) - t.base], 1u);
   });
-  if (bias && r.bias_n) {
+  if (t.first && r.bias_n) {
     each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
-      if (v - from < n) {
-        const uint32_t bit = v - t.lo;
-        atomicMin(&t.first[v - base], (uint32_t)i);
-        atomicOr(&t.bits[bit >> 5], 1u << (bit & 31));
-      }
+      if (v - from < n_tokens) atomicMin(&t.first[place_of(t, v) - t.base], (uint32_t)i);
     });
-    __syncthreads();
-    each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
-      if (v - from < n && (t.first[v - base] & NO_BIAS) != (uint32_t)i) atomicOr(&t.first[v - base], 0x80000000u);
-    });
+    if (r.bias_n > 1) {
+      __syncthreads();
+      each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
+        if (v - from >= n_tokens) return;
+        uint32_t* f = &t.first[place_of(t, v) - t.base];
+        if ((*f & NO_BIAS) != (uint32_t)i) atomicOr(f, 0x80000000u);
+      });
+    }
   }
   __syncthreads();
 }
 
-__device__ __forceinline__ uint32_t count_of(const Table& t, uint32_t v) {
-  const uint32_t at = v - t.base;
-  return t.wide ? t.count[at] : t.count[at >> 1] >> (16 * (at & 1u)) & 0xffffu;
+// the number of occurrences of a listed token, and its first bias entry
+__device__ __forceinline__ void entries_of(const Table& t, uint32_t v, uint32_t* c, uint32_t* fb) {
+  const uint32_t i = place_of(t, v) - t.base;
+  *c = t.count[i];
+  *fb = t.first ? t.first[i] : NO_BIAS;
 }
-__device__ __forceinline__ uint32_t first_of(const Table& t, uint32_t v) { return t.first ? t.first[v - t.base] : NO_BIAS; }
+
+// The range of steps from `step` on that a table has room for: its end, and the table.
+template <int VEC, int U>
+__device__ __forceinline__ uint32_t next_table(const Row& r, Table& t, uint32_t step, uint32_t steps, uint32_t v_begin,
+                                               uint32_t from, uint32_t to) {
+  // listed tokens before the vectors of a step (the first and the last step: before all, and all)
+  auto until = [&](uint32_t s) { return place_of(t, s == 0 ? from : s < steps ? v_begin + s * STEP : to); };
+  const uint32_t base = until(step);
+  uint32_t end = steps;
+  while (end > step + 1 && until(end) - base > TABLE) end = step + (end - step + 1) / 2;
+  t.base = base;
+  const uint32_t t0 = step == 0 ? from : v_begin + step * STEP, t1 = end < steps ? v_begin + end * STEP : to;
+  fill_table(r, t, t0, t1 - t0, until(end) - base);
+  return end;
+}
 
 // The score of a token with c occurrences and bias entries from fb on, from
 // its logit; with the divisions and the order of the definition, so that equal
@@ -428,6 +493,8 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
   __shared__ Part s_part[16];
   __shared__ float s_ref[LG_WARPS], s_sum[LG_WARPS], s_z_pick;
   __shared__ unsigned long long s_key;
+  __shared__ uint32_t s_scan[LG_WARPS];
+  __shared__ uint2 s_queue[LG_WARPS][QUEUE];
   __shared__ float s_best;  // a score that some token of this CTA has: what is below it is not the top
   const tok_logits_args& a = call.a;
   const cg::cluster_group cluster = cg::this_cluster();
@@ -460,11 +527,17 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
   // the slice's tokens: those of its vectors, the first slice's from the row's start, the last one's to its end
   const uint32_t from = rank == 0 ? 0u : g.v0 + i_begin * VEC;
   const uint32_t to = rank == n_ranks - 1 ? a.n_logits : g.v0 + i_end * VEC;
-  if (lists)
-    for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
   Table table{};
-  table.bits = l_bits;
   table.lo = lo;
+  if (lists) {
+    table.bits = l_bits;
+    table.before = words;
+    table.count = reinterpret_cast<uint32_t*>(s_mem + S::BYTES);
+    table.first = a.d_bias_off ? table.count + TABLE : nullptr;
+    for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
+    __syncthreads();
+    list_bits(r, table, call.words, from, to - from, s_scan);
+  }
   const uint32_t pick = a.d_pick ? (uint32_t)a.d_pick[b] : 0xffffffffu;
   const float k = r.inv_t * LOG2E;
   if (tid == 0) {
@@ -493,8 +566,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
 
   float ref = -REF_MAX, sum = 0.f;
   const uint32_t steps = max(1u, (i_end - i_begin + U * LG_THREADS - 1) / (U * LG_THREADS));
-  const uint32_t range = lists ? range_steps(r, a.d_bias_off != nullptr) : steps;
-  uint32_t stage = 0, next = 0;
+  uint32_t stage = 0, next = 0, queued = 0;
   // one score outside the vectors or of a listed token, into the sum; the top is left to the caller
   auto one = [&](float z) {
     const float y = z * k;
@@ -507,29 +579,24 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
   };
 #pragma unroll 1
   for (uint32_t step = 0; step < steps; ++step) {
-    const uint32_t ib = i_begin + step * (U * LG_THREADS), i = ib + tid;
-    if (step == next) {
-      // the scores of this range: its vectors, the first with those before all vectors, the last with those after
-      next = step + range;
-      const uint32_t i1 = next < steps ? ib + range * (U * LG_THREADS) : i_end;
-      const uint32_t from1 = step == 0 ? from : g.v0 + ib * VEC, to1 = next < steps ? g.v0 + i1 * VEC : to;
-      if (lists)
-        fill_table(r, table, s_mem + S::BYTES, a.d_bias_off != nullptr, g.v0 + ib * VEC - EDGE, from1, to1 - from1);
-      if (tid < 32) {  // the scores outside the vectors
-        const uint32_t head = g.v0 + ib * VEC - from1, n = head + (to1 - (g.v0 + i1 * VEC));
-        if (tid < n) {
-          const uint32_t t = tid < head ? from1 + tid : g.v0 + i1 * VEC + (tid - head), at = t - lo;
-          float z = -INFINITY;
-          if (!r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u))) {
-            const bool special = lists && (l_bits[at >> 5] >> (at & 31) & 1u);
-            z = score(r, t, special ? count_of(table, t) : 0, special ? first_of(table, t) : NO_BIAS,
-                      r.seen && (s_bits[at >> 5] >> (at & 31) & 1u), Num<T>::get(x[t]));
-            one(z);
-            atomicMax(&s_key, top_key(z, t));
-          }
-          if (out) out[t] = Num<T>::put(z * r.inv_t);
-          if (t == pick) s_z_pick = z;
+    const uint32_t i = i_begin + step * (U * LG_THREADS) + tid;
+    if (lists && step == next) next = next_table<VEC, U>(r, table, step, steps, g.v0 + i_begin * VEC, from, to);
+    // the scores outside the vectors: before the first step's, after the last one's
+    if ((step == 0 || step + 1 == steps) && tid < 32) {
+      const uint32_t head = step == 0 ? g.v0 + i_begin * VEC - from : 0u;
+      const uint32_t n = head + (step + 1 == steps ? to - (g.v0 + i_end * VEC) : 0u);
+      if (tid < n) {
+        const uint32_t t = tid < head ? from + tid : g.v0 + i_end * VEC + (tid - head), at = t - lo;
+        float z = -INFINITY;
+        if (!r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u))) {
+          uint32_t c = 0, fb = NO_BIAS;
+          if (lists && (l_bits[at >> 5] >> (at & 31) & 1u)) entries_of(table, t, &c, &fb);
+          z = score(r, t, c, fb, r.seen && (s_bits[at >> 5] >> (at & 31) & 1u), Num<T>::get(x[t]));
+          one(z);
+          atomicMax(&s_key, top_key(z, t));
         }
+        if (out) out[t] = Num<T>::put(z * r.inv_t);
+        if (t == pick) s_z_pick = z;
       }
     }
     uint32_t v[U];
@@ -549,17 +616,21 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
           if (!((allowed >> q) & 1u)) z[q] = -INFINITY;
       }
 #pragma unroll
-      for (int q = 0; q < PER; q += 2) vmax = fmaxf(fmaxf(z[q], z[q + 1]), vmax);
+      for (int q = 0; q < PER; q += 2) vmax = max3(z[q], z[q + 1], vmax);
       const float y = vmax * k;
       if (y > ref + 24.f) {
         const float m = fminf(y, REF_MAX);
         sum *= ex2(ref - m);
         ref = m;
       }
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int q = 0; q < PER; ++q) part[q & 3] += ex2(fmaf(z[q], k, -ref));
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      for (int q = 0; q < PER; q += 2) {
+        const float2 w = fma2(make_float2(z[q], z[q + 1]), make_float2(k, k), make_float2(-ref, -ref));
+        part[q / 2 & 1] = add2(part[q / 2 & 1], make_float2(ex2(w.x), ex2(w.y)));
+      }
+      part[0] = add2(part[0], part[1]);
+      sum += part[0].x + part[0].y;
     } else {
 #pragma unroll
       for (int q = 0; q < PER; ++q) z[q] = -INFINITY;
@@ -588,14 +659,39 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
         }
       }
     }
-    // the listed tokens
-    for (uint32_t m = special & loaded; m; m &= m - 1) {
-      const uint32_t q = (uint32_t)__ffs((int)m) - 1u, t = v[0] + q / VEC * (LG_THREADS * VEC) + q % VEC;
-      const float zs = score(r, t, count_of(table, t), first_of(table, t), (seen >> q) & 1u, in.score(stage, q / VEC, q % VEC));
-      one(zs);
-      if (zs >= best) key = max(key, top_key(zs, t));
-      if (out) out[t] = Num<T>::put(zs * r.inv_t);
-      if (t == pick) s_z_pick = zs;
+    // the listed tokens: collected, and scored as soon as there are 32 of them or the table changes
+    if (lists) {
+      const bool flush = step + 1 == next;
+      for (uint32_t m = special & loaded;;) {
+        const uint32_t with = __ballot_sync(0xffffffffu, m != 0);
+        if (with) {
+          if (m) {
+            const uint32_t q = (uint32_t)__ffs((int)m) - 1u, t = v[0] + q / VEC * (LG_THREADS * VEC) + q % VEC;
+            s_queue[tid >> 5][queued + __popc(with & ((1u << lane) - 1u))] =
+                make_uint2(t | ((seen >> q) & 1u) << 31, __float_as_uint(in.score(stage, q / VEC, q % VEC)));
+            m &= m - 1;
+          }
+          queued += __popc(with);
+        }
+        if (queued >= 32 || (!with && flush && queued)) {
+          __syncwarp();
+          const uint32_t n = min(queued, 32u);
+          if (lane < n) {
+            const uint2 e = s_queue[tid >> 5][queued - n + lane];
+            const uint32_t t = e.x & 0x7fffffffu;
+            uint32_t c, fb;
+            entries_of(table, t, &c, &fb);
+            const float zs = score(r, t, c, fb, e.x >> 31, __uint_as_float(e.y));
+            one(zs);
+            if (zs >= best) key = max(key, top_key(zs, t));
+            if (out) out[t] = Num<T>::put(zs * r.inv_t);
+            if (t == pick) s_z_pick = zs;
+          }
+          queued -= n;
+          __syncwarp();
+        }
+        if (!with) break;
+      }
     }
     if (key) {
       atomicMax(&s_key, key);
@@ -679,9 +775,12 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
   constexpr int VEC = S::VEC, U = S::U, DEPTH = S::DEPTH;
   constexpr uint32_t FULL = (1u << PER) - 1u;
   extern __shared__ __align__(16) uint8_t s_mem[];
+  __shared__ uint32_t s_scan[LG_WARPS];
+  __shared__ uint2 s_queue[LG_WARPS][QUEUE];
+  __shared__ float s_queue_grad[LG_WARPS][QUEUE];
   const tok_logits_args& a = call.a;
   const Grad& gr = call.g;
-  const uint32_t rank = blockIdx.x % call.ranks, b = blockIdx.x / call.ranks, tid = threadIdx.x;
+  const uint32_t rank = blockIdx.x % call.ranks, b = blockIdx.x / call.ranks, tid = threadIdx.x, lane = tid & 31u;
   const T* x = static_cast<const T*>(a.d_logits) + (long long)b * a.logits_stride;
   const T* go = gr.out ? static_cast<const T*>(gr.out) + (long long)b * gr.out_stride : nullptr;
   T* gx = static_cast<T*>(gr.logits) + (long long)b * gr.logits_stride;
@@ -712,11 +811,17 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
   if (r.seen) move_bits(s_bits, r.seen, a.n_logits, lo, call.words);
   const uint32_t from = rank == 0 ? 0u : g.v0 + i_begin * VEC;
   const uint32_t to = rank == call.ranks - 1 ? a.n_logits : g.v0 + i_end * VEC;
-  if (lists)
-    for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
   Table table{};
-  table.bits = l_bits;
   table.lo = lo;
+  if (lists) {
+    table.bits = l_bits;
+    table.before = words;
+    table.count = reinterpret_cast<uint32_t*>(s_mem + call.table_at);
+    table.first = a.d_bias_off ? table.count + TABLE : nullptr;
+    for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
+    __syncthreads();
+    list_bits(r, table, call.words, from, to - from, s_scan);
+  }
   const float glp = gr.logprob ? gr.logprob[b] : 0.f;
   float cp = (gr.lse ? gr.lse[b] : 0.f) - glp, lse = 0.f;
   if (gr.lse || gr.logprob) lse = a.d_lse[b];
@@ -763,11 +868,11 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
   auto allowed_at = [&](uint32_t i) { return r.none ? 0u : r.mask ? bits_at(m_bits, i) : inside(i); };
 
   const uint32_t steps = max(1u, (i_end - i_begin + U * LG_THREADS - 1) / (U * LG_THREADS));
-  const uint32_t range = lists ? range_steps(r, a.d_bias_off != nullptr) : steps;
-  uint32_t stage = 0, next = 0;
+  uint32_t stage = 0, next = 0, queued = 0;
   // the gradient of one score; special: with its entries in the lists, whose biases' gradients are written too
   auto one = [&](uint32_t t, bool allowed, bool seen, bool special, float xt, float gt) {
-    const uint32_t c = special ? count_of(table, t) : 0, fb = special ? first_of(table, t) : NO_BIAS;
+    uint32_t c = 0, fb = NO_BIAS;
+    if (special) entries_of(table, t, &c, &fb);
     float dz = 0.f, f = 1.f;
     if (allowed) {
       if (seen || c) f = xt > 0.f ? r.inv_rep : r.rep;
@@ -785,20 +890,15 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
   };
 #pragma unroll 1
   for (uint32_t step = 0; step < steps; ++step) {
-    const uint32_t ib = i_begin + step * (U * LG_THREADS), i = ib + tid;
-    if (step == next) {
-      next = step + range;
-      const uint32_t i1 = next < steps ? ib + range * (U * LG_THREADS) : i_end;
-      const uint32_t from1 = step == 0 ? from : g.v0 + ib * VEC, to1 = next < steps ? g.v0 + i1 * VEC : to;
-      if (lists)
-        fill_table(r, table, s_mem + call.table_at, a.d_bias_off != nullptr, g.v0 + ib * VEC - EDGE, from1, to1 - from1);
-      if (tid < 32) {  // the scores outside the vectors
-        const uint32_t head = g.v0 + ib * VEC - from1, n = head + (to1 - (g.v0 + i1 * VEC));
-        if (tid < n) {
-          const uint32_t t = tid < head ? from1 + tid : g.v0 + i1 * VEC + (tid - head), at = t - lo;
-          one(t, !r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u)), r.seen && (s_bits[at >> 5] >> (at & 31) & 1u),
-              lists && (l_bits[at >> 5] >> (at & 31) & 1u), Num<T>::get(x[t]), go ? Num<T>::get(go[t]) : 0.f);
-        }
+    const uint32_t i = i_begin + step * (U * LG_THREADS) + tid;
+    if (lists && step == next) next = next_table<VEC, U>(r, table, step, steps, g.v0 + i_begin * VEC, from, to);
+    if ((step == 0 || step + 1 == steps) && tid < 32) {  // the scores outside the vectors
+      const uint32_t head = step == 0 ? g.v0 + i_begin * VEC - from : 0u;
+      const uint32_t n = head + (step + 1 == steps ? to - (g.v0 + i_end * VEC) : 0u);
+      if (tid < n) {
+        const uint32_t t = tid < head ? from + tid : g.v0 + i_end * VEC + (tid - head), at = t - lo;
+        one(t, !r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u)), r.seen && (s_bits[at >> 5] >> (at & 31) & 1u),
+            lists && (l_bits[at >> 5] >> (at & 31) & 1u), Num<T>::get(x[t]), go ? Num<T>::get(go[t]) : 0.f);
       }
     }
     uint32_t v[U];
@@ -852,12 +952,35 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (i + u * LG_THREADS < i_end) store_scores(gx + v[u], d + u * VEC, 1.f);
-    // the listed tokens
-    for (uint32_t m = special; m; m &= m - 1) {
-      const uint32_t q = (uint32_t)__ffs((int)m) - 1u, u = q / VEC, e = q % VEC;
-      const bool ok = (loaded >> q) & 1u;
-      one(v[0] + u * (LG_THREADS * VEC) + e, ok, (seen >> q) & 1u, true, ok ? in.score(stage, u, e) : 0.f,
-          ok && go ? gin.score(stage, u, e) : 0.f);
+    // the listed tokens: collected, and taken as soon as there are 32 of them or the table changes
+    if (lists) {
+      const bool flush = step + 1 == next;
+      for (uint32_t m = special;;) {
+        const uint32_t with = __ballot_sync(0xffffffffu, m != 0);
+        if (with) {
+          if (m) {
+            const uint32_t q = (uint32_t)__ffs((int)m) - 1u, u = q / VEC, e = q % VEC;
+            const uint32_t at = queued + __popc(with & ((1u << lane) - 1u)), ok = (loaded >> q) & 1u;
+            s_queue[tid >> 5][at] = make_uint2(v[0] + u * (LG_THREADS * VEC) + e | ((seen >> q) & 1u) << 31 | ok << 30,
+                                               ok ? __float_as_uint(in.score(stage, u, e)) : 0u);
+            if (go) s_queue_grad[tid >> 5][at] = ok ? gin.score(stage, u, e) : 0.f;
+            m &= m - 1;
+          }
+          queued += __popc(with);
+        }
+        if (queued >= 32 || (!with && flush && queued)) {
+          __syncwarp();
+          const uint32_t n = min(queued, 32u);
+          if (lane < n) {
+            const uint2 e = s_queue[tid >> 5][queued - n + lane];
+            one(e.x & 0x3fffffffu, e.x >> 30 & 1u, e.x >> 31, true, __uint_as_float(e.y),
+                go ? s_queue_grad[tid >> 5][queued - n + lane] : 0.f);
+          }
+          queued -= n;
+          __syncwarp();
+        }
+        if (!with) break;
+      }
     }
     __syncwarp();
     {
@@ -910,7 +1033,7 @@ size_t stage_bytes(int dtype, bool shifted) {
 }
 
 size_t bits_bytes(const tok_logits_args& a, uint32_t words, bool lists) {
-  return (size_t)((a.d_mask ? 1 : 0) + (a.d_seen ? 1 : 0) + (lists ? 1 : 0)) * words * sizeof(uint32_t);
+  return (size_t)((a.d_mask ? words : 0) + (a.d_seen ? words : 0) + (lists ? 2 * words + 1 : 0)) * sizeof(uint32_t);
 }
 
 // whether rows of an array lie like those of another towards 16-byte boundaries
