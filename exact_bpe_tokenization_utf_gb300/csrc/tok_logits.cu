@@ -26,9 +26,7 @@ constexpr uint32_t MAX_LOGITS = 1u << 20;
 constexpr int LG_THREADS = 256;
 constexpr int LG_WARPS = LG_THREADS / 32;
 constexpr int PER = 16;           // scores per thread and step
-constexpr int STEP = LG_THREADS * PER;
 constexpr int EDGE = 16;          // places before a slice's first vector, for the scores that come before it (fewer)
-constexpr int TABLE = STEP + 64;  // listed tokens of a table: at least as many as a step has scores
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float REF_MAX = 1e37f;  // references of a sum of exponentials stay within this
@@ -89,29 +87,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
-// two 32-bit operations in one instruction
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c;"
-      " mov.b64 {%0, %1}, d;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
+// two 32-bit numbers, and operations on both in one instruction
+struct Two {
+  float2 v;
+  __device__ __forceinline__ Two() {}
+  __device__ __forceinline__ Two(float x, float y) : v(make_float2(x, y)) {}
+  __device__ __forceinline__ explicit Two(float2 x) : v(x) {}
+  __device__ __forceinline__ void get(float& x, float& y) const {
+    x = v.x;
+    y = v.y;
+  }
+};
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return Two(__ffma2_rn(a.v, b.v, c.v)); }
+__device__ __forceinline__ Two add2(Two a, Two b) { return Two(__fadd2_rn(a.v, b.v)); }
+__device__ __forceinline__ Two mul2(Two a, Two b) { return Two(__fmul2_rn(a.v, b.v)); }
 
 struct Grad {
   const void* out;
@@ -146,6 +135,8 @@ __device__ __forceinline__ Row load_row(const tok_logits_args& a, uint32_t b) {
   r.gen_len = a.d_gen ? max(a.d_gen_len[b], 0) : 0;
   r.gen = a.d_gen ? a.d_gen + a.d_gen_start[b] : nullptr;
   r.bias_n = 0;
+  r.bias_id = nullptr;
+  r.bias = nullptr;
   if (a.d_bias_off) {
     const long long o = a.d_bias_off[b], n = a.d_bias_off[b + 1] - o;
     r.bias_n = n > 0 ? (int)min(n, (long long)0x7fffffff) : 0;
@@ -200,37 +191,44 @@ template <class T, bool SHIFTED> struct Stream {
   static constexpr int STAGE = LG_WARPS * U * SLOT;         // bytes of a step
   static constexpr size_t BYTES = (size_t)DEPTH * STAGE;
 
-  const uint8_t* base;  // the piece of vector 0
+  const uint8_t* from;  // this lane's piece of the next step to be issued
+  uint32_t left;        // vectors from this thread's first one of that step on
   uint32_t shift;       // bytes of the vectors past a 16-byte boundary
   uint8_t* mine;        // this lane's slot of stage 0
-  uint32_t i_end;
 
-  __device__ __forceinline__ void open(const T* row, uint32_t v0, uint32_t end, uint8_t* mem) {
+  __device__ __forceinline__ void open(const T* row, uint32_t v0, uint32_t i_begin, uint32_t i_end, uint8_t* mem) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(row + v0);
     shift = (uint32_t)(at & 15u);
-    base = reinterpret_cast<const uint8_t*>(at - (SHIFTED ? shift : 0u));
+    from = reinterpret_cast<const uint8_t*>(at - (SHIFTED ? shift : 0u)) + ((size_t)i_begin + threadIdx.x) * 16;
     mine = mem + (threadIdx.x >> 5) * U * SLOT + (threadIdx.x & 31u) * 16;
-    i_end = end;
+    left = i_begin + threadIdx.x < i_end ? i_end - i_begin - threadIdx.x : 0u;
+    // (a shifted row's last piece belongs to the last vector, which another lane may hold)
+    if (SHIFTED && i_end > i_begin && i_begin + threadIdx.x <= i_end) left = i_end - i_begin - threadIdx.x + 1u;
   }
-  static __device__ __forceinline__ void copy(uint8_t* to, const uint8_t* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+  static __device__ __forceinline__ void copy(uint8_t* to, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(src)
                  : "memory");
   }
-  // the thread's u-th vector, i; want: whether its scores matter (for a shifted row: any of the warp's)
-  __device__ __forceinline__ void issue(uint32_t stage, int u, uint32_t i, bool want) const {
-    uint8_t* to = mine + stage * STAGE + u * SLOT;
-    if (!SHIFTED) {
-      if (want && i < i_end) copy(to, base + (size_t)i * 16);
-    } else if (want) {
-      if (i <= i_end && i_end) copy(to, base + (size_t)i * 16);
-      if ((threadIdx.x & 31u) == 0 && i + 32 <= i_end) copy(to + 512, base + (size_t)(i + 32) * 16);
+  // the next step into a stage; bit u of want: whether scores of the u-th vector matter (for a shifted row: any)
+  __device__ __forceinline__ void issue(uint32_t stage, uint32_t want) {
+    uint8_t* to = mine + stage * STAGE;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint8_t* src = from + u * (LG_THREADS * 16);
+      if ((want >> u & 1u) && left > (uint32_t)(u * LG_THREADS)) copy(to + u * SLOT, src);
+      if (SHIFTED && want && (threadIdx.x & 31u) == 0 && left > (uint32_t)(u * LG_THREADS + 32)) copy(to + u * SLOT + 512, src + 512);
     }
+    from += U * LG_THREADS * 16;
+    left = left > (uint32_t)(U * LG_THREADS) ? left - U * LG_THREADS : 0u;
   }
+  // the copies issued since the last call are a step
   static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   static __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
     if (SHIFTED) __syncwarp();
   }
+  // before the slots serve as other memory
+  static __device__ __forceinline__ void close() { asm volatile("cp.async.wait_all;" ::: "memory"); }
   // score e of the u-th vector
   __device__ __forceinline__ float score(uint32_t stage, uint32_t u, uint32_t e) const {
     return Num<T>::get(*reinterpret_cast<const T*>(mine + stage * STAGE + u * SLOT + (SHIFTED ? shift : 0u) + e * sizeof(T)));
@@ -270,13 +268,23 @@ template <class T, bool SHIFTED> struct Stream {
 
 template <class T>
 __device__ __forceinline__ void store_scores(T* to, const float* z, float factor) {
+  const Two f(factor, factor);
   uint32_t w[4];
 #pragma unroll
   for (int e = 0; e < Num<T>::VEC / 2; ++e) {
-    const float2 y = mul2(make_float2(z[2 * e], z[2 * e + 1]), make_float2(factor, factor));
-    Num<T>::put_pair(w, e, y.x, y.y);
+    float a, b;
+    mul2(Two(z[2 * e], z[2 * e + 1]), f).get(a, b);
+    Num<T>::put_pair(w, e, a, b);
   }
   __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// the vector of a masked place
+template <class T>
+__device__ __forceinline__ void store_all(T* to, float x) {
+  uint32_t w[1 + sizeof(T) / 4];
+  Num<T>::put_pair(w, 0, x, x);
+  __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[0], w[0], w[0]));
 }
 
 // A slice's bits in shared memory, moved so that the bits of a vector lie in
@@ -301,26 +309,29 @@ __device__ __forceinline__ uint32_t vector_bits(const uint32_t* bits, uint32_t i
   return (uint32_t)b[ii >> 1] >> (4 * (ii & 1u)) & 15u;
 }
 
-// The tokens of the lists (generated ids, biases) have a bit each in a slice;
-// the number of bits before a token's is its place in a table with the number
-// of its occurrences and the smallest index of its bias entries (its top bit:
-// there are more), or NO_BIAS.  The table holds TABLE tokens: where a slice
-// lists more, it is made for as many steps as it has room for, at least one.
-// The main pass leaves listed tokens out; each warp collects those that it
-// meets and scores 32 of them at a time.
+// The tokens of the lists (generated ids, biases) have a bit each in a slice,
+// and the main pass leaves them out.  The number of bits before a token's is
+// its place among them; after the main pass a table in shared memory takes,
+// by place, the token, the number of its occurrences and the smallest index of
+// its bias entries (its top bit: there are more), or NO_BIAS, and each thread
+// scores every LG_THREADS-th of them.  Where a slice lists more tokens than the
+// table holds, it is filled several times.
 constexpr uint32_t NO_BIAS = 0x7fffffffu;
-constexpr int QUEUE = 64;  // collected tokens of a warp
 
 struct Table {
+  uint32_t* token;
   uint32_t* count;
-  uint32_t* first;   // nullptr: no biases
+  uint32_t* first;   // where there are biases
   uint32_t* bits;    // of the slice
   uint32_t* before;  // bits before each word of them
   uint32_t lo;       // token of bit 0 (modulo 2^32)
-  uint32_t base;     // place of the first token of the table
+  uint32_t total;    // listed tokens
+  uint32_t room;     // of the table
 };
 
-constexpr uint32_t table_bytes(bool bias) { return TABLE * (bias ? 8u : 4u); }
+__device__ __forceinline__ bool listed(const Table& t, uint32_t v) {
+  return (t.bits[(v - t.lo) >> 5] >> ((v - t.lo) & 31)) & 1u;
+}
 
 // f(i, ids[i]) for this thread's entries of a list, four loads at a time
 template <class F>
@@ -336,8 +347,7 @@ __device__ __forceinline__ void each_id(const int32_t* ids, int n, F f) {
 }
 
 // the bits of the slice's listed tokens, from .. from + n - 1, and their sums
-__device__ __forceinline__ void list_bits(const Row& r, const Table& t, uint32_t words, uint32_t from, uint32_t n,
-                                          uint32_t* sh) {
+__device__ __forceinline__ void list_bits(const Row& r, Table& t, uint32_t words, uint32_t from, uint32_t n, uint32_t* sh) {
   auto one = [&](int, uint32_t v) {
     const uint32_t bit = v - t.lo;
     if (v - from < n) atomicOr(&t.bits[bit >> 5], 1u << (bit & 31));
@@ -346,70 +356,64 @@ __device__ __forceinline__ void list_bits(const Row& r, const Table& t, uint32_t
   each_id(r.bias_id, r.bias_n, one);
   __syncthreads();
   const uint32_t each = (words + LG_THREADS - 1) / LG_THREADS, w0 = min(threadIdx.x * each, words), w1 = min(w0 + each, words);
-  uint32_t sum = 0, total;
+  uint32_t sum = 0;
   for (uint32_t w = w0; w < w1; ++w) sum += (uint32_t)__popc(t.bits[w]);
-  sum = block_excl_sum(sum, &total, sh);
+  sum = block_excl_sum(sum, &t.total, sh);
   for (uint32_t w = w0; w < w1; ++w) {
     t.before[w] = sum;
     sum += (uint32_t)__popc(t.bits[w]);
   }
-  if (threadIdx.x == 0) t.before[words] = total;
-  __syncthreads();
 }
 
-// listed tokens before v
+// the place of a listed token
 __device__ __forceinline__ uint32_t place_of(const Table& t, uint32_t v) {
   const uint32_t bit = v - t.lo;
   return t.before[bit >> 5] + (uint32_t)__popc(t.bits[bit >> 5] & ((1u << (bit & 31)) - 1u));
 }
 
-// The table of the listed tokens from place t.base on, n of them.
-__device__ __forceinline__ void fill_table(const Row& r, const Table& t, uint32_t from, uint32_t n_tokens, uint32_t n) {
-  __syncthreads();
-  for (uint32_t i = threadIdx.x; i < n; i += LG_THREADS) {
-    t.count[i] = 0;
-    if (t.first) t.first[i] = NO_BIAS;
-  }
-  __syncthreads();
-  each_id(r.gen, r.gen_len, [&](int, uint32_t v) {
-    if (v - from < n_tokens) atomicAdd(&t.count[place_of(t, v) - t.base], 1u);
-  });
-  if (t.first && r.bias_n) {
-    each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
-      if (v - from < n_tokens) atomicMin(&t.first[place_of(t, v) - t.base], (uint32_t)i);
-    });
-    if (r.bias_n > 1) {
-      __syncthreads();
-      each_id(r.bias_id, r.bias_n, [&](int i, uint32_t v) {
-        if (v - from >= n_tokens) return;
-        uint32_t* f = &t.first[place_of(t, v) - t.base];
-        if ((*f & NO_BIAS) != (uint32_t)i) atomicOr(f, 0x80000000u);
-      });
+// one(token, occurrences, first bias entry) for this thread's listed tokens, in the order of the tokens
+template <class F>
+__device__ __forceinline__ void each_listed(const Row& r, Table& t, void* mem, uint32_t bytes, bool bias, uint32_t from,
+                                            uint32_t n_tokens, F one) {
+  t.room = bytes / (bias ? 12u : 8u);
+  t.token = static_cast<uint32_t*>(mem);
+  t.count = t.token + t.room;
+  t.first = bias ? t.count + t.room : t.count;  // (read with biases only)
+  for (uint32_t base = 0; base < t.total; base += t.room) {
+    const uint32_t n = min(t.room, t.total - base);
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < n; i += LG_THREADS) {
+      t.count[i] = 0;
+      if (bias) t.first[i] = NO_BIAS;
     }
+    __syncthreads();
+    each_id(r.gen, r.gen_len, [&](int, uint32_t v) {
+      if (v - from >= n_tokens) return;
+      const uint32_t i = place_of(t, v) - base;
+      if (i >= n) return;
+      t.token[i] = v;  // (the same from every occurrence)
+      atomicAdd(&t.count[i], 1u);
+    });
+    if (bias && r.bias_n) {
+      each_id(r.bias_id, r.bias_n, [&](int e, uint32_t v) {
+        if (v - from >= n_tokens) return;
+        const uint32_t i = place_of(t, v) - base;
+        if (i >= n) return;
+        t.token[i] = v;
+        atomicMin(&t.first[i], (uint32_t)e);
+      });
+      if (r.bias_n > 1) {
+        __syncthreads();
+        each_id(r.bias_id, r.bias_n, [&](int e, uint32_t v) {
+          if (v - from >= n_tokens) return;
+          const uint32_t i = place_of(t, v) - base;
+          if (i < n && (t.first[i] & NO_BIAS) != (uint32_t)e) atomicOr(&t.first[i], 0x80000000u);
+        });
+      }
+    }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < n; i += LG_THREADS) one(t.token[i], t.count[i], bias ? t.first[i] : NO_BIAS);
   }
-  __syncthreads();
-}
-
-// the number of occurrences of a listed token, and its first bias entry
-__device__ __forceinline__ void entries_of(const Table& t, uint32_t v, uint32_t* c, uint32_t* fb) {
-  const uint32_t i = place_of(t, v) - t.base;
-  *c = t.count[i];
-  *fb = t.first ? t.first[i] : NO_BIAS;
-}
-
-// The range of steps from `step` on that a table has room for: its end, and the table.
-template <int VEC, int U>
-__device__ __forceinline__ uint32_t next_table(const Row& r, Table& t, uint32_t step, uint32_t steps, uint32_t v_begin,
-                                               uint32_t from, uint32_t to) {
-  // listed tokens before the vectors of a step (the first and the last step: before all, and all)
-  auto until = [&](uint32_t s) { return place_of(t, s == 0 ? from : s < steps ? v_begin + s * STEP : to); };
-  const uint32_t base = until(step);
-  uint32_t end = steps;
-  while (end > step + 1 && until(end) - base > TABLE) end = step + (end - step + 1) / 2;
-  t.base = base;
-  const uint32_t t0 = step == 0 ? from : v_begin + step * STEP, t1 = end < steps ? v_begin + end * STEP : to;
-  fill_table(r, t, t0, t1 - t0, until(end) - base);
-  return end;
 }
 
 // The score of a token with c occurrences and bias entries from fb on, from
@@ -433,13 +437,22 @@ __device__ __forceinline__ float score(const Row& r, uint32_t v, uint32_t c, uin
 
 // The repetition penalty of a thread's seen scores, as a product with its
 // reciprocal, within 2^-22 of the quotient: where that can decide which score
-// is the largest, they are taken again with score().
-__device__ __forceinline__ void penalise(const Row& r, uint32_t seen, float* z) {
+// is the largest, they are taken again with score().  d: scaled alike.
+__device__ __forceinline__ void penalise(const Row& r, uint32_t seen, float* z, float* d) {
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const float f = z[q] > 0.f ? r.inv_rep : r.rep;
-    if ((seen >> q) & 1u) z[q] *= f;
+    if ((seen >> q) & 1u) {
+      z[q] *= f;
+      if (d) d[q] = f;
+    }
   }
+}
+
+__device__ __forceinline__ float max16(const float* z) {
+  const float a = max3(z[0], z[1], z[2]), b = max3(z[3], z[4], z[5]), c = max3(z[6], z[7], z[8]),
+              d = max3(z[9], z[10], z[11]), e = max3(z[12], z[13], z[14]);
+  return max3(max3(a, b, c), max3(d, e, z[15]), z[15]);
 }
 
 // the largest score and its token (the lowest of equals) as one word; 0: none above -inf
@@ -468,33 +481,128 @@ __device__ __forceinline__ void join_sum(float& ref, float& sum, float ref2, flo
   ref = m;
 }
 
+// A row's slice as a CTA takes it, for both kernels: its vectors, its bits in
+// shared memory and its listed tokens.
+struct Shape {
+  uint32_t per;      // vectors per CTA
+  uint32_t words;    // of a slice's bits
+  uint32_t front;    // bytes of shared memory for the scores in flight, later the table of listed tokens
+  int lists;         // there are generated ids or biases
+};
+
+template <class T> struct Slice {
+  static constexpr int VEC = Num<T>::VEC, U = PER / VEC;
+  static constexpr uint32_t FULL = (1u << PER) - 1u;
+  uint32_t v0, i_begin, i_end;  // the first vector's first token; the vectors
+  uint32_t from, to;            // the tokens
+  uint32_t *mask, *seen;        // bits, where there are any (pointers into the slice's memory in any case)
+  bool none, masked, marked, lists;
+  Table table;
+
+  __device__ __forceinline__ void open(const tok_logits_args& a, const Shape& sh, const Grid& g, uint32_t rank, uint32_t n_ranks) {
+    v0 = g.v0;
+    i_begin = min(rank * sh.per, g.n_vec);
+    i_end = min(i_begin + sh.per, g.n_vec);
+    // the first slice's tokens from the row's start, the last one's to its end
+    from = rank == 0 ? 0u : v0 + i_begin * VEC;
+    to = rank == n_ranks - 1 ? a.n_logits : v0 + i_end * VEC;
+    table.lo = v0 + i_begin * VEC - EDGE;
+  }
+  // (ends with a barrier)
+  __device__ __forceinline__ void fill(const tok_logits_args& a, const Shape& sh, const Row& r, uint8_t* mem, uint32_t* scan) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(mem + sh.front);
+    none = r.none;
+    masked = r.mask != nullptr;
+    marked = r.seen != nullptr;
+    lists = sh.lists && (r.gen_len || r.bias_n);
+    table.token = table.count = table.first = reinterpret_cast<uint32_t*>(mem);
+    table.bits = table.before = mask = seen = w;
+    table.total = table.room = 0;
+    if (lists) {
+      table.before = w + sh.words;
+      w += 2 * sh.words;
+      for (uint32_t i = threadIdx.x; i < sh.words; i += LG_THREADS) table.bits[i] = 0;
+    }
+    if (masked) {
+      mask = w;
+      w += sh.words;
+      move_bits(mask, r.mask, a.n_logits, table.lo, sh.words);
+    }
+    if (marked) {
+      seen = w;
+      move_bits(seen, r.seen, a.n_logits, table.lo, sh.words);
+    }
+    __syncthreads();
+    if (lists) list_bits(r, table, sh.words, from, to - from, scan);
+    __syncthreads();
+  }
+  // the bits of a thread's vectors, the first one ii after the slice's first (those outside: 0)
+  __device__ __forceinline__ uint32_t bits_at(const uint32_t* bits, uint32_t ii) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (ii + u * LG_THREADS < i_end - i_begin) m |= vector_bits<T>(bits, ii + u * LG_THREADS) << (u * VEC);
+    return m;
+  }
+  __device__ __forceinline__ uint32_t inside(uint32_t ii) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (ii + u * LG_THREADS < i_end - i_begin) m |= ((1u << VEC) - 1u) << (u * VEC);
+    return m;
+  }
+  __device__ __forceinline__ uint32_t allowed_at(uint32_t ii) const {
+    return none ? 0u : masked ? bits_at(mask, ii) : inside(ii);
+  }
+  // which of a thread's vectors have allowed scores; for a shifted row: whether any of the warp's has
+  template <bool SHIFTED>
+  __device__ __forceinline__ uint32_t wanted(uint32_t ii) const {
+    const uint32_t m = allowed_at(ii);
+    if (SHIFTED) return __any_sync(0xffffffffu, m != 0) ? 0xffu : 0u;
+    uint32_t w = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) w |= (m >> (u * VEC) & ((1u << VEC) - 1u) ? 1u : 0u) << u;
+    return w;
+  }
+  __device__ __forceinline__ bool allows(uint32_t t) const {
+    const uint32_t at = t - table.lo;
+    return !none && (!masked || (mask[at >> 5] >> (at & 31) & 1u));
+  }
+  __device__ __forceinline__ bool saw(uint32_t t) const {
+    const uint32_t at = t - table.lo;
+    return marked && (seen[at >> 5] >> (at & 31) & 1u);
+  }
+  // the tid-th score outside the vectors (fewer than 32), or NO_TOKEN
+  __device__ __forceinline__ uint32_t outside(uint32_t tid) const {
+    const uint32_t head = v0 + i_begin * VEC - from, n = head + (to - (v0 + i_end * VEC));
+    return tid < n ? (tid < head ? from + tid : v0 + i_end * VEC + (tid - head)) : 0xffffffffu;
+  }
+};
+
 // the two halves of a cluster's barrier
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 struct LogitsCall {
   tok_logits_args a;
-  uint32_t per;    // vectors per CTA
-  uint32_t words;  // of a slice's bits
-  uint32_t bits_at; // where they are in shared memory
-  int lists;       // there are generated ids or biases
+  Shape shape;
+  int in_place;  // out is logits
 };
 
 // Forward.  A row is cut into the slices of a cluster's CTAs (one CTA: the
 // whole row); a step gives each thread 16 scores.  Scores that the mask hides
 // are not read.
 template <class T, bool SHIFTED>
-__global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
+__global__ void __launch_bounds__(LG_THREADS, 3) k_logits(LogitsCall call) {
   namespace cg = cooperative_groups;
   using S = Stream<T, SHIFTED>;
   constexpr int VEC = S::VEC, U = S::U, DEPTH = S::DEPTH;
-  constexpr uint32_t FULL = (1u << PER) - 1u;
+  constexpr uint32_t FULL = Slice<T>::FULL, ALL = 0xffffffffu;
   extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ Part s_part[16];
   __shared__ float s_ref[LG_WARPS], s_sum[LG_WARPS], s_z_pick;
-  __shared__ unsigned long long s_key;
   __shared__ uint32_t s_scan[LG_WARPS];
-  __shared__ uint2 s_queue[LG_WARPS][QUEUE];
+  __shared__ unsigned long long s_key;
   __shared__ float s_best;  // a score that some token of this CTA has: what is below it is not the top
   const tok_logits_args& a = call.a;
   const cg::cluster_group cluster = cg::this_cluster();
@@ -503,228 +611,156 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
   const uint32_t b = blockIdx.x / n_ranks, tid = threadIdx.x, lane = tid & 31u;
   const T* x = static_cast<const T*>(a.d_logits) + (long long)b * a.logits_stride;
   T* out = a.d_out ? static_cast<T*>(a.d_out) + (long long)b * a.out_stride : nullptr;
-  const Grid g = vectors<T, SHIFTED>(out ? static_cast<const void*>(out) : x, a.n_logits);
-  const uint32_t i_begin = min(rank * call.per, g.n_vec), i_end = min(i_begin + call.per, g.n_vec);
+  Slice<T> c;
+  c.open(a, call.shape, vectors<T, SHIFTED>(out ? static_cast<const void*>(out) : x, a.n_logits), rank, n_ranks);
   S in;
-  in.open(x, g.v0, i_end, s_mem);
-  const Row r = load_row(a, b);
+  in.open(x, c.v0, c.i_begin, c.i_end, s_mem);
   // the first steps' scores, before it is known which of them are hidden
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) in.issue(d, u, i_begin + (d * U + u) * LG_THREADS + tid, !r.none);
+    in.issue(d, 0xffu);
     S::commit();
   }
-  const bool lists = call.lists && (r.gen_len || r.bias_n);
-  const uint32_t lo = g.v0 + i_begin * VEC - EDGE;
-  uint32_t* words = reinterpret_cast<uint32_t*>(s_mem + call.bits_at);
-  uint32_t *m_bits = nullptr, *s_bits = nullptr, *l_bits = nullptr;
-  if (a.d_mask) m_bits = words, words += call.words;
-  if (a.d_seen) s_bits = words, words += call.words;
-  if (call.lists) l_bits = words, words += call.words;
-  if (r.mask) move_bits(m_bits, r.mask, a.n_logits, lo, call.words);
-  if (r.seen) move_bits(s_bits, r.seen, a.n_logits, lo, call.words);
-  // the slice's tokens: those of its vectors, the first slice's from the row's start, the last one's to its end
-  const uint32_t from = rank == 0 ? 0u : g.v0 + i_begin * VEC;
-  const uint32_t to = rank == n_ranks - 1 ? a.n_logits : g.v0 + i_end * VEC;
-  Table table{};
-  table.lo = lo;
-  if (lists) {
-    table.bits = l_bits;
-    table.before = words;
-    table.count = reinterpret_cast<uint32_t*>(s_mem + S::BYTES);
-    table.first = a.d_bias_off ? table.count + TABLE : nullptr;
-    for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
-    __syncthreads();
-    list_bits(r, table, call.words, from, to - from, s_scan);
-  }
+  const Row r = load_row(a, b);
   const uint32_t pick = a.d_pick ? (uint32_t)a.d_pick[b] : 0xffffffffu;
-  const float k = r.inv_t * LOG2E;
+  const float x_pick = pick - c.from < c.to - c.from ? Num<T>::get(x[pick]) : 0.f;
   if (tid == 0) {
     s_key = 0;
     s_best = -INFINITY;
     s_z_pick = -INFINITY;
   }
-  __syncthreads();
+  c.fill(a, call.shape, r, s_mem, s_scan);
 
-  // the bits of a thread's vectors from i on
-  auto bits_at = [&](const uint32_t* bits, uint32_t i) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * LG_THREADS < i_end) m |= vector_bits<T>(bits, i - i_begin + u * LG_THREADS) << (u * VEC);
-    return m;
-  };
-  auto inside = [&](uint32_t i) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * LG_THREADS < i_end) m |= ((1u << VEC) - 1u) << (u * VEC);
-    return m;
-  };
-  auto allowed_at = [&](uint32_t i) { return r.none ? 0u : r.mask ? bits_at(m_bits, i) : inside(i); };
-
+  // ref is the same in all threads of a warp
+  const float k = r.inv_t * LOG2E;
+  const Two k2(k, k);
   float ref = -REF_MAX, sum = 0.f;
-  const uint32_t steps = max(1u, (i_end - i_begin + U * LG_THREADS - 1) / (U * LG_THREADS));
-  uint32_t stage = 0, next = 0, queued = 0;
-  // one score outside the vectors or of a listed token, into the sum; the top is left to the caller
-  auto one = [&](float z) {
-    const float y = z * k;
-    if (y > ref + 24.f) {
-      const float m = fminf(y, REF_MAX);
-      sum *= ex2(ref - m);
-      ref = m;
-    }
-    sum += ex2(fmaf(z, k, -ref));
+  unsigned long long key = 0;
+  auto raise = [&](float y) {  // ref to y or higher
+    const float m = fmaxf(ref, fminf(y, REF_MAX));
+    sum *= ex2(ref - m);
+    ref = m;
   };
-#pragma unroll 1
-  for (uint32_t step = 0; step < steps; ++step) {
-    const uint32_t i = i_begin + step * (U * LG_THREADS) + tid;
-    if (lists && step == next) next = next_table<VEC, U>(r, table, step, steps, g.v0 + i_begin * VEC, from, to);
-    // the scores outside the vectors: before the first step's, after the last one's
-    if ((step == 0 || step + 1 == steps) && tid < 32) {
-      const uint32_t head = step == 0 ? g.v0 + i_begin * VEC - from : 0u;
-      const uint32_t n = head + (step + 1 == steps ? to - (g.v0 + i_end * VEC) : 0u);
-      if (tid < n) {
-        const uint32_t t = tid < head ? from + tid : g.v0 + i_end * VEC + (tid - head), at = t - lo;
-        float z = -INFINITY;
-        if (!r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u))) {
-          uint32_t c = 0, fb = NO_BIAS;
-          if (lists && (l_bits[at >> 5] >> (at & 31) & 1u)) entries_of(table, t, &c, &fb);
-          z = score(r, t, c, fb, r.seen && (s_bits[at >> 5] >> (at & 31) & 1u), Num<T>::get(x[t]));
-          one(z);
-          atomicMax(&s_key, top_key(z, t));
-        }
-        if (out) out[t] = Num<T>::put(z * r.inv_t);
-        if (t == pick) s_z_pick = z;
-      }
+  if (tid == 0 && pick - c.from < c.to - c.from && c.allows(pick) && !(c.lists && listed(c.table, pick)))
+    s_z_pick = score(r, pick, 0, NO_BIAS, c.saw(pick), x_pick);
+  if (tid < 32) {  // the scores outside the vectors
+    const uint32_t t = c.outside(tid);
+    float z = -INFINITY;
+    if (t != 0xffffffffu && !(c.lists && listed(c.table, t))) {
+      if (c.allows(t)) z = score(r, t, 0, NO_BIAS, c.saw(t), Num<T>::get(x[t]));
+      if (out) out[t] = Num<T>::put(z * r.inv_t);
+      key = top_key(z, t);
     }
-    uint32_t v[U];
+    float y = z * k;
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = g.v0 + (i + u * LG_THREADS) * VEC;
-    const uint32_t special = lists ? bits_at(l_bits, i) : 0u;
-    const uint32_t loaded = allowed_at(i), allowed = loaded & ~special, seen = r.seen ? bits_at(s_bits, i) : 0u;
+    for (int o = 16; o; o >>= 1) y = fmaxf(y, __shfl_xor_sync(ALL, y, o));
+    raise(y);
+    sum = ex2(fmaf(z, k, -ref));
+  }
+  const uint32_t steps = (c.i_end - c.i_begin + U * LG_THREADS - 1) / (U * LG_THREADS);
+  T* to = out + c.v0 + (c.i_begin + tid) * VEC;
+  uint32_t stage = 0, ii = tid;
+#pragma unroll 1
+  for (uint32_t step = 0; step < steps; ++step, ii += U * LG_THREADS) {
+    const uint32_t special = c.lists ? c.bits_at(c.table.bits, ii) : 0u;
+    const uint32_t loaded = c.allowed_at(ii), allowed = loaded & ~special;
     S::wait();
-    float z[PER], vmax = -INFINITY;
-    if (allowed) {
+    if (__any_sync(ALL, allowed != 0)) {
+      const uint32_t seen = c.marked ? c.bits_at(c.seen, ii) : 0u;
+      float z[PER];
 #pragma unroll
       for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
-      if (seen) penalise(r, seen, z);
+      if (c.marked) penalise(r, seen, z, nullptr);
       if (allowed != FULL) {
 #pragma unroll
         for (int q = 0; q < PER; ++q)
           if (!((allowed >> q) & 1u)) z[q] = -INFINITY;
       }
+      const float vmax = max16(z);
+      // scores that may be the largest, once more and exactly; and ref where the scores leave its range
+      const float best = *static_cast<volatile float*>(&s_best);
+      const float near = best < INFINITY ? best - fabsf(best) * 0x1p-20f : best;
+      if (__any_sync(ALL, (vmax >= near && vmax > -INFINITY) || best * k > ref + 24.f)) {
+        float wmax = vmax;
 #pragma unroll
-      for (int q = 0; q < PER; q += 2) vmax = max3(z[q], z[q + 1], vmax);
-      const float y = vmax * k;
-      if (y > ref + 24.f) {
-        const float m = fminf(y, REF_MAX);
-        sum *= ex2(ref - m);
-        ref = m;
+        for (int o = 16; o; o >>= 1) wmax = fmaxf(wmax, __shfl_xor_sync(ALL, wmax, o));
+        raise(fmaxf(wmax, best) * k);
+        const float at_least = fmaxf(near, wmax - fabsf(wmax) * 0x1p-20f);
+        if (vmax >= at_least) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int q = 0; q < PER; ++q) m |= (z[q] >= at_least && z[q] > -INFINITY ? 1u : 0u) << q;
+          unsigned long long top = 0;
+          for (; m; m &= m - 1) {
+            const uint32_t q = (uint32_t)__ffs((int)m) - 1u;
+            const uint32_t t = c.v0 + (c.i_begin + ii + q / VEC * LG_THREADS) * VEC + q % VEC;
+            top = max(top, top_key(score(r, t, 0, NO_BIAS, (seen >> q) & 1u, in.score(stage, q / VEC, q % VEC)), t));
+          }
+          key = max(key, top);
+          const float zx = key_score(top);
+          if (zx > best) s_best = zx;
+        }
       }
-      float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      const Two ref2(-ref, -ref);
+      Two part[2] = {Two(0.f, 0.f), Two(0.f, 0.f)};
 #pragma unroll
       for (int q = 0; q < PER; q += 2) {
-        const float2 w = fma2(make_float2(z[q], z[q + 1]), make_float2(k, k), make_float2(-ref, -ref));
-        part[q / 2 & 1] = add2(part[q / 2 & 1], make_float2(ex2(w.x), ex2(w.y)));
+        float p0, p1;
+        fma2(Two(z[q], z[q + 1]), k2, ref2).get(p0, p1);
+        part[q / 2 & 1] = add2(part[q / 2 & 1], Two(ex2(p0), ex2(p1)));
       }
-      part[0] = add2(part[0], part[1]);
-      sum += part[0].x + part[0].y;
-    } else {
+      float p0, p1;
+      add2(part[0], part[1]).get(p0, p1);
+      sum += p0 + p1;
+      if (out) {
 #pragma unroll
-      for (int q = 0; q < PER; ++q) z[q] = -INFINITY;
+        for (int u = 0; u < U; ++u)
+          if (ii + u * LG_THREADS < c.i_end - c.i_begin) store_scores(to + u * (LG_THREADS * VEC), z + u * VEC, r.inv_t);
+      }
+    } else if (out) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (ii + u * LG_THREADS < c.i_end - c.i_begin) store_all(to + u * (LG_THREADS * VEC), -INFINITY);
     }
     if (out) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + u * LG_THREADS < i_end) store_scores(out + v[u], z + u * VEC, r.inv_t);
-    }
-    // scores that may be the largest, once more and exactly
-    const float best = *static_cast<volatile float*>(&s_best);
-    const float near = best < INFINITY ? best - fabsf(best) * 0x1p-20f : best;
-    unsigned long long key = 0;
-    if (__any_sync(0xffffffffu, vmax > -INFINITY && vmax >= near)) {
-      float wmax = vmax;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, o));
-      const float at_least = fmaxf(near, wmax - fabsf(wmax) * 0x1p-20f);
-      if (vmax >= at_least) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int q = 0; q < PER; ++q) m |= (z[q] >= at_least && z[q] > -INFINITY ? 1u : 0u) << q;
-        for (; m; m &= m - 1) {
-          const uint32_t q = (uint32_t)__ffs((int)m) - 1u, t = v[0] + q / VEC * (LG_THREADS * VEC) + q % VEC;
-          key = max(key, top_key(score(r, t, 0, NO_BIAS, (seen >> q) & 1u, in.score(stage, q / VEC, q % VEC)), t));
+      if (call.in_place)  // the logits of listed tokens are still needed
+        for (uint32_t m = special & loaded; m; m &= m - 1) {
+          const uint32_t q = (uint32_t)__ffs((int)m) - 1u;
+          to[q / VEC * (LG_THREADS * VEC) + q % VEC] = Num<T>::put(in.score(stage, q / VEC, q % VEC));
         }
-      }
+      to += U * LG_THREADS * VEC;
     }
-    // the listed tokens: collected, and scored as soon as there are 32 of them or the table changes
-    if (lists) {
-      const bool flush = step + 1 == next;
-      for (uint32_t m = special & loaded;;) {
-        const uint32_t with = __ballot_sync(0xffffffffu, m != 0);
-        if (with) {
-          if (m) {
-            const uint32_t q = (uint32_t)__ffs((int)m) - 1u, t = v[0] + q / VEC * (LG_THREADS * VEC) + q % VEC;
-            s_queue[tid >> 5][queued + __popc(with & ((1u << lane) - 1u))] =
-                make_uint2(t | ((seen >> q) & 1u) << 31, __float_as_uint(in.score(stage, q / VEC, q % VEC)));
-            m &= m - 1;
-          }
-          queued += __popc(with);
-        }
-        if (queued >= 32 || (!with && flush && queued)) {
-          __syncwarp();
-          const uint32_t n = min(queued, 32u);
-          if (lane < n) {
-            const uint2 e = s_queue[tid >> 5][queued - n + lane];
-            const uint32_t t = e.x & 0x7fffffffu;
-            uint32_t c, fb;
-            entries_of(table, t, &c, &fb);
-            const float zs = score(r, t, c, fb, e.x >> 31, __uint_as_float(e.y));
-            one(zs);
-            if (zs >= best) key = max(key, top_key(zs, t));
-            if (out) out[t] = Num<T>::put(zs * r.inv_t);
-            if (t == pick) s_z_pick = zs;
-          }
-          queued -= n;
-          __syncwarp();
-        }
-        if (!with) break;
-      }
-    }
-    if (key) {
-      atomicMax(&s_key, key);
-      const float zx = key_score(key);
-      if (zx > best) s_best = zx;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (pick - v[u] < (uint32_t)VEC && i + u * LG_THREADS < i_end) {
-        const uint32_t e = pick - v[u], q = u * VEC + e;
-        if ((allowed >> q) & 1u) s_z_pick = score(r, pick, 0, NO_BIAS, (seen >> q) & 1u, in.score(stage, u, e));
-      }
     // this stage's slots are free: the step DEPTH later
     __syncwarp();
-    {
-      const uint32_t later = i + DEPTH * U * LG_THREADS;
-      uint32_t want = step + DEPTH < steps ? allowed_at(later) : 0u;
-      if (SHIFTED) want = __any_sync(0xffffffffu, want != 0) ? FULL : 0u;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        in.issue(stage, u, later + u * LG_THREADS, (want >> (u * VEC)) & ((1u << VEC) - 1u));
-      S::commit();
-      stage = stage + 1 == DEPTH ? 0 : stage + 1;
-    }
+    in.issue(stage, step + DEPTH < steps ? c.template wanted<SHIFTED>(ii + DEPTH * U * LG_THREADS) : 0u);
+    S::commit();
+    stage = stage + 1 == DEPTH ? 0 : stage + 1;
   }
+  S::close();
+
+  // the listed tokens
+  if (c.lists)
+    each_listed(r, c.table, s_mem, call.shape.front, a.d_bias_off != nullptr, c.from, c.to - c.from,
+                [&](uint32_t t, uint32_t n, uint32_t fb) {
+                  float z = -INFINITY;
+                  if (c.allows(t)) z = score(r, t, n, fb, c.saw(t), Num<T>::get(x[t]));
+                  if (z * k > ref + 24.f) raise(z * k);
+                  sum += ex2(fmaf(z, k, -ref));
+                  key = max(key, top_key(z, t));
+                  if (t == pick) s_z_pick = z;
+                  if (out) out[t] = Num<T>::put(z * r.inv_t);
+                });
 
   // the CTA's sum, then the cluster's, and the row's results
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
-    join_sum(ref, sum, __shfl_xor_sync(0xffffffffu, ref, o), __shfl_xor_sync(0xffffffffu, sum, o));
+  for (int o = 16; o; o >>= 1) {
+    join_sum(ref, sum, __shfl_xor_sync(ALL, ref, o), __shfl_xor_sync(ALL, sum, o));
+    key = max(key, __shfl_xor_sync(ALL, key, o));
+  }
   if (lane == 0) {
     s_ref[tid >> 5] = ref;
     s_sum[tid >> 5] = sum;
+    atomicMax(&s_key, key);
   }
   __syncthreads();
   if (n_ranks > 1) cluster_wait();
@@ -735,7 +771,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
   }
   if (n_ranks > 1) cluster.sync();
   if (rank == 0 && tid == 0) {
-    unsigned long long key = s_part[0].key;
+    key = s_part[0].key;
     ref = s_part[0].ref;
     sum = s_part[0].sum;
     float z_pick = s_part[0].z_pick;
@@ -760,8 +796,8 @@ __global__ void __launch_bounds__(LG_THREADS, 2) k_logits(LogitsCall call) {
 struct GradCall {
   tok_logits_args a;
   Grad g;
-  uint32_t per, words, table_at, bits_at, ranks;
-  int lists;
+  Shape shape;
+  uint32_t ranks;
 };
 
 // Gradient: slices as in k_logits, but independent CTAs.  exp(y - lse) is
@@ -770,233 +806,143 @@ struct GradCall {
 // log2(e) are sums of two numbers each (their rounding would weigh |y| times
 // on the result) and nothing is added to the exponent.
 template <class T, bool SHIFTED>
-__global__ void __launch_bounds__(LG_THREADS, 2) k_logits_grad(GradCall call) {
+__global__ void __launch_bounds__(LG_THREADS, 3) k_logits_grad(GradCall call) {
   using S = Stream<T, SHIFTED>;
   constexpr int VEC = S::VEC, U = S::U, DEPTH = S::DEPTH;
-  constexpr uint32_t FULL = (1u << PER) - 1u;
+  constexpr uint32_t FULL = Slice<T>::FULL, ALL = 0xffffffffu;
   extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ uint32_t s_scan[LG_WARPS];
-  __shared__ uint2 s_queue[LG_WARPS][QUEUE];
-  __shared__ float s_queue_grad[LG_WARPS][QUEUE];
   const tok_logits_args& a = call.a;
   const Grad& gr = call.g;
-  const uint32_t rank = blockIdx.x % call.ranks, b = blockIdx.x / call.ranks, tid = threadIdx.x, lane = tid & 31u;
+  const uint32_t rank = blockIdx.x % call.ranks, b = blockIdx.x / call.ranks, tid = threadIdx.x;
   const T* x = static_cast<const T*>(a.d_logits) + (long long)b * a.logits_stride;
   const T* go = gr.out ? static_cast<const T*>(gr.out) + (long long)b * gr.out_stride : nullptr;
   T* gx = static_cast<T*>(gr.logits) + (long long)b * gr.logits_stride;
-  const Grid g = vectors<T, SHIFTED>(gx, a.n_logits);
-  const uint32_t i_begin = min(rank * call.per, g.n_vec), i_end = min(i_begin + call.per, g.n_vec);
+  Slice<T> c;
+  c.open(a, call.shape, vectors<T, SHIFTED>(gx, a.n_logits), rank, call.ranks);
   S in, gin;
-  in.open(x, g.v0, i_end, s_mem);
-  if (go) gin.open(go, g.v0, i_end, s_mem + S::BYTES);
-  const Row r = load_row(a, b);
+  in.open(x, c.v0, c.i_begin, c.i_end, s_mem);
+  gin.open(go ? go : x, c.v0, c.i_begin, c.i_end, s_mem + (go ? S::BYTES : 0));
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t i = i_begin + (d * U + u) * LG_THREADS + tid;
-      in.issue(d, u, i, !r.none);
-      if (go) gin.issue(d, u, i, !r.none);
-    }
+    in.issue(d, 0xffu);
+    if (go) gin.issue(d, 0xffu);
     S::commit();
   }
-  const bool lists = call.lists && (r.gen_len || r.bias_n);
-  const uint32_t lo = g.v0 + i_begin * VEC - EDGE;
-  uint32_t* words = reinterpret_cast<uint32_t*>(s_mem + call.bits_at);
-  uint32_t *m_bits = nullptr, *s_bits = nullptr, *l_bits = nullptr;
-  if (a.d_mask) m_bits = words, words += call.words;
-  if (a.d_seen) s_bits = words, words += call.words;
-  if (call.lists) l_bits = words, words += call.words;
-  if (r.mask) move_bits(m_bits, r.mask, a.n_logits, lo, call.words);
-  if (r.seen) move_bits(s_bits, r.seen, a.n_logits, lo, call.words);
-  const uint32_t from = rank == 0 ? 0u : g.v0 + i_begin * VEC;
-  const uint32_t to = rank == call.ranks - 1 ? a.n_logits : g.v0 + i_end * VEC;
-  Table table{};
-  table.lo = lo;
-  if (lists) {
-    table.bits = l_bits;
-    table.before = words;
-    table.count = reinterpret_cast<uint32_t*>(s_mem + call.table_at);
-    table.first = a.d_bias_off ? table.count + TABLE : nullptr;
-    for (uint32_t i = tid; i < call.words; i += LG_THREADS) l_bits[i] = 0;
-    __syncthreads();
-    list_bits(r, table, call.words, from, to - from, s_scan);
-  }
+  const Row r = load_row(a, b);
   const float glp = gr.logprob ? gr.logprob[b] : 0.f;
   float cp = (gr.lse ? gr.lse[b] : 0.f) - glp, lse = 0.f;
   if (gr.lse || gr.logprob) lse = a.d_lse[b];
   if (fabsf(lse) >= 1e36f) cp = lse = 0.f;  // (nothing but -inf or a type's lowest value)
   uint32_t pick = a.d_pick ? (uint32_t)a.d_pick[b] : 0xffffffffu;
   if ((int32_t)pick < 0 && gr.logprob) pick = (uint32_t)a.d_top[b];
-  const float up = sizeof(T) == 4 ? 0.f : 24.f;
   const double kd = 1.4426950408889634 / (a.d_temperature ? (double)a.d_temperature[b] : 1.0);
-  const double ld = (double)lse * 1.4426950408889634 - (double)up;
+  const double ld = (double)lse * 1.4426950408889634 - (sizeof(T) == 4 ? 0.0 : 24.0);
   const float k = (float)kd, k_lo = (float)(kd - (double)k), lh = (float)ld, l_lo = (float)(ld - (double)lh);
   const float cpt = cp * r.inv_t * (sizeof(T) == 4 ? 1.f : 0x1p-24f);
   if (rank == 0 && gr.bias)
     for (int i = tid; i < r.bias_n; i += LG_THREADS)
       if ((uint32_t)r.bias_id[i] >= a.n_logits) gr.bias[(r.bias - a.d_bias) + i] = 0.f;
-  __syncthreads();
+  c.fill(a, call.shape, r, s_mem, s_scan);
 
-  // the gradient of a score before the temperature, from the score and grad_out
-  auto d_score = [&](float z, float d) -> float {
-    d *= r.inv_t;
-    if (cpt != 0.f) {
-      if (sizeof(T) == 4) {
-        z = fmaxf(z, -FLT_MAX);  // (-inf times k_lo is no number)
-        d = fmaf(cpt, ex2_small(fmaf(z, k, -lh) + fmaf(z, k_lo, -l_lo)), d);
-      } else {
-        d = fmaf(cpt, ex2(fmaf(z, k, -lh)), d);
-      }
-    }
-    return d;
-  };
-  auto bits_at = [&](const uint32_t* bits, uint32_t i) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * LG_THREADS < i_end) m |= vector_bits<T>(bits, i - i_begin + u * LG_THREADS) << (u * VEC);
-    return m;
-  };
-  auto inside = [&](uint32_t i) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * LG_THREADS < i_end) m |= ((1u << VEC) - 1u) << (u * VEC);
-    return m;
-  };
-  auto allowed_at = [&](uint32_t i) { return r.none ? 0u : r.mask ? bits_at(m_bits, i) : inside(i); };
-
-  const uint32_t steps = max(1u, (i_end - i_begin + U * LG_THREADS - 1) / (U * LG_THREADS));
-  uint32_t stage = 0, next = 0, queued = 0;
-  // the gradient of one score; special: with its entries in the lists, whose biases' gradients are written too
-  auto one = [&](uint32_t t, bool allowed, bool seen, bool special, float xt, float gt) {
-    uint32_t c = 0, fb = NO_BIAS;
-    if (special) entries_of(table, t, &c, &fb);
+  // the gradient of one score and, returned, the one before the repetition penalty
+  auto one = [&](uint32_t t, uint32_t n, uint32_t fb) {
     float dz = 0.f, f = 1.f;
-    if (allowed) {
-      if (seen || c) f = xt > 0.f ? r.inv_rep : r.rep;
-      dz = d_score(score(r, t, c, fb, seen, xt), gt);
+    if (c.allows(t)) {
+      const bool seen = c.saw(t);
+      const float xt = Num<T>::get(x[t]);
+      if (seen || n) f = xt > 0.f ? r.inv_rep : r.rep;
+      if (go) dz = Num<T>::get(go[t]) * r.inv_t;
+      if (cpt != 0.f) {
+        const float z = fmaxf(score(r, t, n, fb, seen, xt), -FLT_MAX);  // (-inf times k_lo is no number)
+        dz = fmaf(cpt, sizeof(T) == 4 ? ex2_small(fmaf(z, k, -lh) + fmaf(z, k_lo, -l_lo)) : ex2(fmaf(z, k, -lh)), dz);
+      }
       if (t == pick) dz = fmaf(glp, r.inv_t, dz);
     }
     gx[t] = Num<T>::put(dz * f);
-    if (gr.bias && (fb & NO_BIAS) != NO_BIAS) {
-      float* gb = gr.bias + (r.bias - a.d_bias);
-      gb[fb & NO_BIAS] = dz;
-      if (fb >> 31)
-        for (int e = (int)(fb & NO_BIAS) + 1; e < r.bias_n; ++e)
-          if ((uint32_t)r.bias_id[e] == t) gb[e] = dz;
-    }
+    return dz;
   };
+  if (tid < 32) {  // the scores outside the vectors
+    const uint32_t t = c.outside(tid);
+    if (t != 0xffffffffu && !(c.lists && listed(c.table, t))) one(t, 0, NO_BIAS);
+  }
+  const Two k2(k, k), lh2(-lh, -lh), klo2(k_lo, k_lo), llo2(-l_lo, -l_lo), cpt2(cpt, cpt), inv_t2(r.inv_t, r.inv_t);
+  const uint32_t steps = (c.i_end - c.i_begin + U * LG_THREADS - 1) / (U * LG_THREADS);
+  T* to = gx + c.v0 + (c.i_begin + tid) * VEC;
+  uint32_t stage = 0, ii = tid;
 #pragma unroll 1
-  for (uint32_t step = 0; step < steps; ++step) {
-    const uint32_t i = i_begin + step * (U * LG_THREADS) + tid;
-    if (lists && step == next) next = next_table<VEC, U>(r, table, step, steps, g.v0 + i_begin * VEC, from, to);
-    if ((step == 0 || step + 1 == steps) && tid < 32) {  // the scores outside the vectors
-      const uint32_t head = step == 0 ? g.v0 + i_begin * VEC - from : 0u;
-      const uint32_t n = head + (step + 1 == steps ? to - (g.v0 + i_end * VEC) : 0u);
-      if (tid < n) {
-        const uint32_t t = tid < head ? from + tid : g.v0 + i_end * VEC + (tid - head), at = t - lo;
-        one(t, !r.none && (!r.mask || (m_bits[at >> 5] >> (at & 31) & 1u)), r.seen && (s_bits[at >> 5] >> (at & 31) & 1u),
-            lists && (l_bits[at >> 5] >> (at & 31) & 1u), Num<T>::get(x[t]), go ? Num<T>::get(go[t]) : 0.f);
-      }
-    }
-    uint32_t v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = g.v0 + (i + u * LG_THREADS) * VEC;
-    const uint32_t special = lists ? bits_at(l_bits, i) : 0u, loaded = allowed_at(i), allowed = loaded & ~special;
-    const uint32_t seen = r.seen ? bits_at(s_bits, i) : 0u;
+  for (uint32_t step = 0; step < steps; ++step, ii += U * LG_THREADS, to += U * LG_THREADS * VEC) {
+    const uint32_t allowed = c.allowed_at(ii) & ~(c.lists ? c.bits_at(c.table.bits, ii) : 0u);
     S::wait();
-    float z[PER], d[PER];
-    if (allowed) {
+    if (__any_sync(ALL, allowed != 0)) {
+      float z[PER], d[PER], f[PER];
 #pragma unroll
       for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
+      if (c.marked) {
+        const uint32_t seen = c.bits_at(c.seen, ii);
+#pragma unroll
+        for (int q = 0; q < PER; ++q) f[q] = 1.f;
+        penalise(r, seen, z, f);
+      }
       if (go) {
 #pragma unroll
         for (int u = 0; u < U; ++u) gin.scores(stage, u, d + u * VEC);
-      } else {
-#pragma unroll
-        for (int q = 0; q < PER; ++q) d[q] = 0.f;
-      }
-      uint32_t positive = 0;
-      if (seen) {
-#pragma unroll
-        for (int q = 0; q < PER; ++q) positive |= (z[q] > 0.f ? 1u : 0u) << q;
-        penalise(r, seen, z);
       }
 #pragma unroll
-      for (int q = 0; q < PER; ++q) d[q] = d_score(z[q], d[q]);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (pick - v[u] < (uint32_t)VEC) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (v[u] + e == pick) d[u * VEC + e] = fmaf(glp, r.inv_t, d[u * VEC + e]);
+      for (int q = 0; q < PER; q += 2) {
+        Two d2(0.f, 0.f);
+        if (go) d2 = mul2(Two(d[q], d[q + 1]), inv_t2);
+        if (cpt != 0.f) {
+          if (sizeof(T) == 4) {  // (-inf times k_lo is no number)
+            z[q] = fmaxf(z[q], -FLT_MAX);
+            z[q + 1] = fmaxf(z[q + 1], -FLT_MAX);
+          }
+          const Two z2(z[q], z[q + 1]);
+          Two e2 = fma2(z2, k2, lh2);
+          if (sizeof(T) == 4) e2 = add2(e2, fma2(z2, klo2, llo2));
+          float p0, p1;
+          e2.get(p0, p1);
+          d2 = fma2(cpt2, sizeof(T) == 4 ? Two(ex2_small(p0), ex2_small(p1)) : Two(ex2(p0), ex2(p1)), d2);
         }
+        if (c.marked) d2 = mul2(d2, Two(f[q], f[q + 1]));
+        d2.get(d[q], d[q + 1]);
+      }
       if (allowed != FULL) {
 #pragma unroll
         for (int q = 0; q < PER; ++q)
           if (!((allowed >> q) & 1u)) d[q] = 0.f;
       }
-      if (seen) {
 #pragma unroll
-        for (int q = 0; q < PER; ++q) {
-          const float f = (positive >> q) & 1u ? r.inv_rep : r.rep;
-          if ((seen >> q) & 1u) d[q] *= f;
-        }
-      }
+      for (int u = 0; u < U; ++u)
+        if (ii + u * LG_THREADS < c.i_end - c.i_begin) store_scores(to + u * (LG_THREADS * VEC), d + u * VEC, 1.f);
     } else {
 #pragma unroll
-      for (int q = 0; q < PER; ++q) d[q] = 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * LG_THREADS < i_end) store_scores(gx + v[u], d + u * VEC, 1.f);
-    // the listed tokens: collected, and taken as soon as there are 32 of them or the table changes
-    if (lists) {
-      const bool flush = step + 1 == next;
-      for (uint32_t m = special;;) {
-        const uint32_t with = __ballot_sync(0xffffffffu, m != 0);
-        if (with) {
-          if (m) {
-            const uint32_t q = (uint32_t)__ffs((int)m) - 1u, u = q / VEC, e = q % VEC;
-            const uint32_t at = queued + __popc(with & ((1u << lane) - 1u)), ok = (loaded >> q) & 1u;
-            s_queue[tid >> 5][at] = make_uint2(v[0] + u * (LG_THREADS * VEC) + e | ((seen >> q) & 1u) << 31 | ok << 30,
-                                               ok ? __float_as_uint(in.score(stage, u, e)) : 0u);
-            if (go) s_queue_grad[tid >> 5][at] = ok ? gin.score(stage, u, e) : 0.f;
-            m &= m - 1;
-          }
-          queued += __popc(with);
-        }
-        if (queued >= 32 || (!with && flush && queued)) {
-          __syncwarp();
-          const uint32_t n = min(queued, 32u);
-          if (lane < n) {
-            const uint2 e = s_queue[tid >> 5][queued - n + lane];
-            one(e.x & 0x3fffffffu, e.x >> 30 & 1u, e.x >> 31, true, __uint_as_float(e.y),
-                go ? s_queue_grad[tid >> 5][queued - n + lane] : 0.f);
-          }
-          queued -= n;
-          __syncwarp();
-        }
-        if (!with) break;
-      }
+      for (int u = 0; u < U; ++u)
+        if (ii + u * LG_THREADS < c.i_end - c.i_begin) store_all(to + u * (LG_THREADS * VEC), 0.f);
     }
     __syncwarp();
-    {
-      const uint32_t later = i + DEPTH * U * LG_THREADS;
-      uint32_t want = step + DEPTH < steps ? allowed_at(later) : 0u;
-      if (SHIFTED) want = __any_sync(0xffffffffu, want != 0) ? FULL : 0u;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool w = (want >> (u * VEC)) & ((1u << VEC) - 1u);
-        in.issue(stage, u, later + u * LG_THREADS, w);
-        if (go) gin.issue(stage, u, later + u * LG_THREADS, w);
-      }
-      S::commit();
-      stage = stage + 1 == DEPTH ? 0 : stage + 1;
-    }
+    const uint32_t want = step + DEPTH < steps ? c.template wanted<SHIFTED>(ii + DEPTH * U * LG_THREADS) : 0u;
+    in.issue(stage, want);
+    if (go) gin.issue(stage, want);
+    S::commit();
+    stage = stage + 1 == DEPTH ? 0 : stage + 1;
   }
+  S::close();
+  __syncthreads();
+  if (tid == 0 && pick - c.from < c.to - c.from && !(c.lists && listed(c.table, pick))) one(pick, 0, NO_BIAS);
+
+  // the listed tokens, with their biases' gradients
+  if (c.lists)
+    each_listed(r, c.table, s_mem, call.shape.front, a.d_bias_off != nullptr, c.from, c.to - c.from,
+                [&](uint32_t t, uint32_t n, uint32_t fb) {
+                  const float dz = one(t, n, fb);
+                  if (!gr.bias || (fb & NO_BIAS) == NO_BIAS) return;
+                  float* gb = gr.bias + (r.bias - a.d_bias);
+                  gb[fb & NO_BIAS] = dz;
+                  if (fb >> 31)
+                    for (int e = (int)(fb & NO_BIAS) + 1; e < r.bias_n; ++e)
+                      if ((uint32_t)r.bias_id[e] == t) gb[e] = dz;
+                });
 }
 
 // One CTA per row: the bits in shared memory, then the row.
@@ -1016,15 +962,25 @@ __global__ void __launch_bounds__(LG_THREADS) k_seen_bits(const int32_t* ids, co
   for (uint32_t w = threadIdx.x; w < words; w += LG_THREADS) row[w] = s_bits[w];
 }
 
-// Slices of a row: enough CTAs to fill the GPU a few times over while a slice
-// keeps some thousand scores, at most the 16 CTAs of a cluster; a slice's
-// bits stay within 16 KB each.
-uint32_t slices(const tok_handle* h, const tok_logits_args& a) {
-  uint32_t s = 1;
-  while (s < 16 && ((unsigned long long)a.rows * s < 4ull * (unsigned)h->n_sms || a.n_logits / s > (1u << 17)) &&
-         a.n_logits / (2 * s) >= 2048)
-    s *= 2;
-  return s;
+// Slices of a row, at most the 16 CTAs of a cluster: as few rounds of CTAs as
+// possible (three fit an SM), weighing a CTA's start and end like 48 KB of
+// scores.  A slice keeps 2,048 scores or more, and its bits 16 KB at most.
+uint32_t slices(const tok_handle* h, const tok_logits_args& a, size_t size) {
+  const unsigned long long room = 3ull * (unsigned)h->n_sms;
+  uint32_t best = 1;
+  double least = 0;
+  for (uint32_t s = 1; s <= 16; ++s) {
+    if (s > 1 && a.n_logits / s < 2048) break;
+    const unsigned long long rounds = ((unsigned long long)a.rows * s + room - 1) / room;
+    const double cost = (double)rounds * ((double)a.n_logits * (double)size / s + 49152.0);
+    if (a.n_logits / s > (1u << 17)) {
+      best = s + 1;
+    } else if (best == s || cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 size_t stage_bytes(int dtype, bool shifted) {
@@ -1033,7 +989,7 @@ size_t stage_bytes(int dtype, bool shifted) {
 }
 
 size_t bits_bytes(const tok_logits_args& a, uint32_t words, bool lists) {
-  return (size_t)((a.d_mask ? words : 0) + (a.d_seen ? words : 0) + (lists ? 2 * words + 1 : 0)) * sizeof(uint32_t);
+  return (size_t)((a.d_mask ? 1 : 0) + (a.d_seen ? 1 : 0) + (lists ? 2 : 0)) * words * sizeof(uint32_t);
 }
 
 // whether rows of an array lie like those of another towards 16-byte boundaries
@@ -1116,14 +1072,15 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream) tr
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   LogitsCall c{};
   c.a = *a;
-  c.lists = a->d_gen || a->d_bias_off;
-  const uint32_t n = slices(h, *a);
-  const uint32_t vec = 16 / (uint32_t)size_of(a->dtype);
-  c.per = (a->n_logits / vec + n - 1) / n;
-  c.words = bit_words(c.per * vec);
-  const bool shifted = a->d_out && !alike(a->d_logits, a->logits_stride, a->d_out, a->out_stride, a->rows, size_of(a->dtype));
-  c.bits_at = (uint32_t)stage_bytes(a->dtype, shifted) + (c.lists ? table_bytes(a->d_bias_off != nullptr) : 0);
-  const size_t smem = c.bits_at + bits_bytes(*a, c.words, c.lists);
+  const size_t size = size_of(a->dtype);
+  const uint32_t vec = 16 / (uint32_t)size, n = slices(h, *a, size);
+  const bool shifted = a->d_out && !alike(a->d_logits, a->logits_stride, a->d_out, a->out_stride, a->rows, size);
+  c.in_place = a->d_out == a->d_logits;
+  c.shape.lists = a->d_gen || a->d_bias_off;
+  c.shape.per = (a->n_logits / vec + n - 1) / n;
+  c.shape.words = bit_words(c.shape.per * vec);
+  c.shape.front = (uint32_t)stage_bytes(a->dtype, shifted);
+  const size_t smem = c.shape.front + bits_bytes(*a, c.shape.words, c.shape.lists);
   const unsigned ctas = a->rows * n;
   const cudaError_t e = a->dtype == TOK_F32   ? launch_forward<float>(c, shifted, ctas, n, smem, s)
                         : a->dtype == TOK_F16 ? launch_forward<__half>(c, shifted, ctas, n, smem, s)
@@ -1150,18 +1107,17 @@ int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logit
   c.a = *a;
   c.g = Grad{ga->d_grad_out, ga->grad_out_stride, ga->d_grad_lse,  ga->d_grad_logprob,
                ga->d_grad_logits, ga->grad_logits_stride, a->d_bias_off ? ga->d_grad_bias : nullptr};
-  c.lists = a->d_gen || a->d_bias_off;
-  c.ranks = slices(h, *a);
   const size_t size = size_of(a->dtype);
   const uint32_t vec = 16 / (uint32_t)size;
-  c.per = (a->n_logits / vec + c.ranks - 1) / c.ranks;
-  c.words = bit_words(c.per * vec);
   const bool shifted = !alike(a->d_logits, a->logits_stride, ga->d_grad_logits, ga->grad_logits_stride, a->rows, size) ||
                        (ga->d_grad_out && !alike(ga->d_grad_out, ga->grad_out_stride, ga->d_grad_logits,
                                                  ga->grad_logits_stride, a->rows, size));
-  c.table_at = (uint32_t)stage_bytes(a->dtype, shifted) * (ga->d_grad_out ? 2 : 1);
-  c.bits_at = c.table_at + (c.lists ? table_bytes(a->d_bias_off != nullptr) : 0);
-  const size_t smem = c.bits_at + bits_bytes(*a, c.words, c.lists);
+  c.ranks = slices(h, *a, size);
+  c.shape.lists = a->d_gen || a->d_bias_off;
+  c.shape.per = (a->n_logits / vec + c.ranks - 1) / c.ranks;
+  c.shape.words = bit_words(c.shape.per * vec);
+  c.shape.front = (uint32_t)stage_bytes(a->dtype, shifted) * (ga->d_grad_out ? 2 : 1);
+  const size_t smem = c.shape.front + bits_bytes(*a, c.shape.words, c.shape.lists);
   const unsigned ctas = a->rows * c.ranks;
   const cudaError_t e = a->dtype == TOK_F32   ? launch_grad<float>(c, shifted, ctas, smem, s)
                         : a->dtype == TOK_F16 ? launch_grad<__half>(c, shifted, ctas, smem, s)
