@@ -24,6 +24,8 @@ namespace {
 
 constexpr uint32_t MAX_LOGITS = 1u << 20;
 constexpr int LG_THREADS = 256;
+constexpr int LG_CTAS = 3;        // per SM, where shared memory has room for them
+constexpr int SB_THREADS = 256;   // of k_seen_bits
 constexpr int LG_WARPS = LG_THREADS / 32;
 constexpr int PER = 16;           // scores per thread and step
 constexpr int EDGE = 16;          // places before a slice's first vector, for the scores that come before it (fewer)
@@ -323,7 +325,7 @@ struct Table {
   uint32_t* count;
   uint32_t* first;   // where there are biases
   uint32_t* bits;    // of the slice
-  uint32_t* before;  // bits before each word of them
+  uint32_t* before;  // bits before every fourth word of them
   uint32_t lo;       // token of bit 0 (modulo 2^32)
   uint32_t total;    // listed tokens
   uint32_t room;     // of the table
@@ -355,20 +357,31 @@ __device__ __forceinline__ void list_bits(const Row& r, Table& t, uint32_t words
   each_id(r.gen, r.gen_len, one);
   each_id(r.bias_id, r.bias_n, one);
   __syncthreads();
-  const uint32_t each = (words + LG_THREADS - 1) / LG_THREADS, w0 = min(threadIdx.x * each, words), w1 = min(w0 + each, words);
+  const uint32_t groups = (words + 3) / 4, each = (groups + LG_THREADS - 1) / LG_THREADS;
+  const uint32_t g0 = min(threadIdx.x * each, groups), g1 = min(g0 + each, groups);
+  auto in_group = [&](uint32_t g) {
+    uint32_t c = 0;
+#pragma unroll
+    for (uint32_t w = 4 * g; w < 4 * g + 4; ++w) c += w < words ? (uint32_t)__popc(t.bits[w]) : 0u;
+    return c;
+  };
   uint32_t sum = 0;
-  for (uint32_t w = w0; w < w1; ++w) sum += (uint32_t)__popc(t.bits[w]);
+  for (uint32_t g = g0; g < g1; ++g) sum += in_group(g);
   sum = block_excl_sum(sum, &t.total, sh);
-  for (uint32_t w = w0; w < w1; ++w) {
-    t.before[w] = sum;
-    sum += (uint32_t)__popc(t.bits[w]);
+  for (uint32_t g = g0; g < g1; ++g) {
+    t.before[g] = sum;
+    sum += in_group(g);
   }
 }
 
 // the place of a listed token
 __device__ __forceinline__ uint32_t place_of(const Table& t, uint32_t v) {
-  const uint32_t bit = v - t.lo;
-  return t.before[bit >> 5] + (uint32_t)__popc(t.bits[bit >> 5] & ((1u << (bit & 31)) - 1u));
+  const uint32_t bit = v - t.lo, word = bit >> 5;
+  uint32_t n = t.before[bit >> 7] + (uint32_t)__popc(t.bits[word] & ((1u << (bit & 31)) - 1u));
+#pragma unroll
+  for (uint32_t back = 1; back < 4; ++back)
+    if ((word & 3u) >= back) n += (uint32_t)__popc(t.bits[word - back]);
+  return n;
 }
 
 // one(token, occurrences, first bias entry) for this thread's listed tokens, in the order of the tokens
@@ -520,7 +533,7 @@ template <class T> struct Slice {
     table.total = table.room = 0;
     if (lists) {
       table.before = w + sh.words;
-      w += 2 * sh.words;
+      w += sh.words + (sh.words + 3) / 4;
       for (uint32_t i = threadIdx.x; i < sh.words; i += LG_THREADS) table.bits[i] = 0;
     }
     if (masked) {
@@ -593,7 +606,7 @@ struct LogitsCall {
 // whole row); a step gives each thread 16 scores.  Scores that the mask hides
 // are not read.
 template <class T, bool SHIFTED>
-__global__ void __launch_bounds__(LG_THREADS, 3) k_logits(LogitsCall call) {
+__global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call) {
   namespace cg = cooperative_groups;
   using S = Stream<T, SHIFTED>;
   constexpr int VEC = S::VEC, U = S::U, DEPTH = S::DEPTH;
@@ -806,7 +819,7 @@ struct GradCall {
 // log2(e) are sums of two numbers each (their rounding would weigh |y| times
 // on the result) and nothing is added to the exponent.
 template <class T, bool SHIFTED>
-__global__ void __launch_bounds__(LG_THREADS, 3) k_logits_grad(GradCall call) {
+__global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall call) {
   using S = Stream<T, SHIFTED>;
   constexpr int VEC = S::VEC, U = S::U, DEPTH = S::DEPTH;
   constexpr uint32_t FULL = Slice<T>::FULL, ALL = 0xffffffffu;
@@ -946,41 +959,20 @@ __global__ void __launch_bounds__(LG_THREADS, 3) k_logits_grad(GradCall call) {
 }
 
 // One CTA per row: the bits in shared memory, then the row.
-__global__ void __launch_bounds__(LG_THREADS) k_seen_bits(const int32_t* ids, const long long* off, uint32_t n_logits,
+__global__ void __launch_bounds__(SB_THREADS) k_seen_bits(const int32_t* ids, const long long* off, uint32_t n_logits,
                                                           uint32_t* seen, long long stride, int keep) {
   extern __shared__ uint32_t s_bits[];
   const uint32_t words = (n_logits + 31) / 32;
   uint32_t* row = seen + (long long)blockIdx.x * stride;
-  for (uint32_t w = threadIdx.x; w < words; w += LG_THREADS) s_bits[w] = keep ? row[w] : 0u;
+  for (uint32_t w = threadIdx.x; w < words; w += SB_THREADS) s_bits[w] = keep ? row[w] : 0u;
   __syncthreads();
   const long long end = off[blockIdx.x + 1];
-  for (long long i = off[blockIdx.x] + threadIdx.x; i < end; i += LG_THREADS) {
+  for (long long i = off[blockIdx.x] + threadIdx.x; i < end; i += SB_THREADS) {
     const uint32_t v = (uint32_t)ids[i];
     if (v < n_logits) atomicOr(&s_bits[v >> 5], 1u << (v & 31));
   }
   __syncthreads();
-  for (uint32_t w = threadIdx.x; w < words; w += LG_THREADS) row[w] = s_bits[w];
-}
-
-// Slices of a row, at most the 16 CTAs of a cluster: as few rounds of CTAs as
-// possible (three fit an SM), weighing a CTA's start and end like 48 KB of
-// scores.  A slice keeps 2,048 scores or more, and its bits 16 KB at most.
-uint32_t slices(const tok_handle* h, const tok_logits_args& a, size_t size) {
-  const unsigned long long room = 3ull * (unsigned)h->n_sms;
-  uint32_t best = 1;
-  double least = 0;
-  for (uint32_t s = 1; s <= 16; ++s) {
-    if (s > 1 && a.n_logits / s < 2048) break;
-    const unsigned long long rounds = ((unsigned long long)a.rows * s + room - 1) / room;
-    const double cost = (double)rounds * ((double)a.n_logits * (double)size / s + 49152.0);
-    if (a.n_logits / s > (1u << 17)) {
-      best = s + 1;
-    } else if (best == s || cost < least) {
-      best = s;
-      least = cost;
-    }
-  }
-  return best;
+  for (uint32_t w = threadIdx.x; w < words; w += SB_THREADS) row[w] = s_bits[w];
 }
 
 size_t stage_bytes(int dtype, bool shifted) {
@@ -988,8 +980,42 @@ size_t stage_bytes(int dtype, bool shifted) {
   return shifted ? Stream<__half, true>::BYTES : Stream<__half, false>::BYTES;
 }
 
-size_t bits_bytes(const tok_logits_args& a, uint32_t words, bool lists) {
-  return (size_t)((a.d_mask ? 1 : 0) + (a.d_seen ? 1 : 0) + (lists ? 2 : 0)) * words * sizeof(uint32_t);
+size_t size_of(int dtype) { return dtype == TOK_F32 ? 4 : 2; }
+
+// A row in n slices; arrays: of scores that are read.
+Shape shape(const tok_logits_args& a, bool shifted, int arrays, uint32_t n, size_t* smem) {
+  const uint32_t vec = 16 / (uint32_t)size_of(a.dtype);
+  Shape s{};
+  s.lists = a.d_gen || a.d_bias_off;
+  s.per = (a.n_logits / vec + n - 1) / n;
+  s.words = bit_words(s.per * vec);
+  s.front = (uint32_t)stage_bytes(a.dtype, shifted) * arrays;
+  *smem = s.front + sizeof(uint32_t) * ((size_t)s.words * ((a.d_mask ? 1 : 0) + (a.d_seen ? 1 : 0) + (s.lists ? 1 : 0)) +
+                                        (s.lists ? (s.words + 3) / 4 : 0));
+  return s;
+}
+
+// The slices of a row, at most the 16 CTAs of a cluster: as few rounds of CTAs
+// as possible, weighing a CTA's start and end (about 8 us) like 64 KB of its
+// scores.  A slice keeps 2,048 scores or more.
+uint32_t slices(const tok_handle* h, const tok_logits_args& a, bool shifted, int arrays) {
+  uint32_t best = 0;
+  double least = 0;
+  for (uint32_t n = 1; n <= 16; ++n) {
+    if (best && a.n_logits / n < 2048) break;
+    size_t smem;
+    shape(a, shifted, arrays, n, &smem);
+    if (smem > 200 * 1024) continue;
+    const unsigned fit = (unsigned)std::min<size_t>(LG_CTAS, (228 * 1024) / (smem + 2048));
+    const unsigned long long room = (unsigned long long)fit * (unsigned)h->n_sms;
+    const unsigned long long rounds = ((unsigned long long)a.rows * n + room - 1) / room;
+    const double cost = (double)rounds * (fit * (double)a.n_logits * (double)size_of(a.dtype) / n + LG_CTAS * 65536.0);
+    if (!best || cost < least) {
+      best = n;
+      least = cost;
+    }
+  }
+  return best ? best : 16;
 }
 
 // whether rows of an array lie like those of another towards 16-byte boundaries
@@ -997,8 +1023,6 @@ bool alike(const void* p, int64_t stride, const void* q, int64_t q_stride, uint3
   if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15u) != 0) return false;
   return rows == 1 || ((uint64_t)(stride - q_stride) * size & 15u) == 0;
 }
-
-size_t size_of(int dtype) { return dtype == TOK_F32 ? 4 : 2; }
 
 template <class K, class C>
 cudaError_t launch(K kernel, const C& call, unsigned ctas, unsigned cluster, size_t smem, cudaStream_t s) {
@@ -1073,14 +1097,11 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream) tr
   LogitsCall c{};
   c.a = *a;
   const size_t size = size_of(a->dtype);
-  const uint32_t vec = 16 / (uint32_t)size, n = slices(h, *a, size);
   const bool shifted = a->d_out && !alike(a->d_logits, a->logits_stride, a->d_out, a->out_stride, a->rows, size);
+  const uint32_t n = slices(h, *a, shifted, 1);
+  size_t smem;
+  c.shape = shape(*a, shifted, 1, n, &smem);
   c.in_place = a->d_out == a->d_logits;
-  c.shape.lists = a->d_gen || a->d_bias_off;
-  c.shape.per = (a->n_logits / vec + n - 1) / n;
-  c.shape.words = bit_words(c.shape.per * vec);
-  c.shape.front = (uint32_t)stage_bytes(a->dtype, shifted);
-  const size_t smem = c.shape.front + bits_bytes(*a, c.shape.words, c.shape.lists);
   const unsigned ctas = a->rows * n;
   const cudaError_t e = a->dtype == TOK_F32   ? launch_forward<float>(c, shifted, ctas, n, smem, s)
                         : a->dtype == TOK_F16 ? launch_forward<__half>(c, shifted, ctas, n, smem, s)
@@ -1108,16 +1129,13 @@ int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logit
   c.g = Grad{ga->d_grad_out, ga->grad_out_stride, ga->d_grad_lse,  ga->d_grad_logprob,
                ga->d_grad_logits, ga->grad_logits_stride, a->d_bias_off ? ga->d_grad_bias : nullptr};
   const size_t size = size_of(a->dtype);
-  const uint32_t vec = 16 / (uint32_t)size;
   const bool shifted = !alike(a->d_logits, a->logits_stride, ga->d_grad_logits, ga->grad_logits_stride, a->rows, size) ||
                        (ga->d_grad_out && !alike(ga->d_grad_out, ga->grad_out_stride, ga->d_grad_logits,
                                                  ga->grad_logits_stride, a->rows, size));
-  c.ranks = slices(h, *a, size);
-  c.shape.lists = a->d_gen || a->d_bias_off;
-  c.shape.per = (a->n_logits / vec + c.ranks - 1) / c.ranks;
-  c.shape.words = bit_words(c.shape.per * vec);
-  c.shape.front = (uint32_t)stage_bytes(a->dtype, shifted) * (ga->d_grad_out ? 2 : 1);
-  const size_t smem = c.shape.front + bits_bytes(*a, c.shape.words, c.shape.lists);
+  const int arrays = ga->d_grad_out ? 2 : 1;
+  c.ranks = slices(h, *a, shifted, arrays);
+  size_t smem;
+  c.shape = shape(*a, shifted, arrays, c.ranks, &smem);
   const unsigned ctas = a->rows * c.ranks;
   const cudaError_t e = a->dtype == TOK_F32   ? launch_grad<float>(c, shifted, ctas, smem, s)
                         : a->dtype == TOK_F16 ? launch_grad<__half>(c, shifted, ctas, smem, s)
@@ -1140,7 +1158,7 @@ int tok_seen_bits(tok_handle* h, const int32_t* d_ids, const int64_t* d_item_off
     const cudaError_t e = cudaFuncSetAttribute(k_seen_bits, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return cuda_fail(h, e, "seen bits");
   }
-  k_seen_bits<<<n, LG_THREADS, bytes, static_cast<cudaStream_t>(stream)>>>(
+  k_seen_bits<<<n, SB_THREADS, bytes, static_cast<cudaStream_t>(stream)>>>(
       d_ids, reinterpret_cast<const long long*>(d_item_off), n_logits, d_seen, seen_stride, keep);
   return launched(h, cudaGetLastError());
 } catch (...) {
