@@ -3,6 +3,7 @@
 // the failure hook of tok_debug_fail_alloc).
 #pragma once
 #include <algorithm>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <string>
@@ -13,11 +14,26 @@
 
 namespace tokgb {
 
-// the vocabulary's bytes on the device: token t has bytes[off[t] .. off[t + 1])
+// The vocabulary's bytes on the device: token t has bytes[off[t] .. off[t + 1]),
+// and, for walking many tokens at once, the tokens sorted by their bytes in
+// groups of up to 32 that begin alike.  Group g: its first `prefix` bytes (at
+// most 8) are in head; lane i's token is id[32 g + i] (NO_TOKEN: none) with
+// rest[32 g + i] bytes more, four per word, words[at + 32 w + i].
+struct TokenGroup {
+  unsigned long long head;  // the first byte lowest
+  uint32_t shape;           // prefix | words per token << 4
+  uint32_t at;
+};
+
 struct DevTokens {
   const uint8_t* bytes;
   const uint32_t* off;
   uint32_t n;
+  uint32_t n_groups;
+  const TokenGroup* group;
+  const uint32_t* words;
+  const uint32_t* id;
+  const uint16_t* rest;
 };
 
 }  // namespace tokgb
@@ -131,6 +147,42 @@ cudaError_t halloc_pinned(tok_handle* h, T** p, size_t count) {
     return cudaErrorMemoryAllocation;
   }
   return cudaMallocHost(reinterpret_cast<void**>(p), std::max<size_t>(count, 1) * sizeof(T));
+}
+
+// Allow a kernel most of an SM's shared memory and clusters of 16 CTAs, once
+// per device (the two calls cost about as much as a launch).
+constexpr size_t MOST_SHARED = 200 * 1024;
+template <auto Kernel>
+cudaError_t allow_all(int dev) {
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MOST_SHARED);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+// Launch a kernel in clusters of `cluster` CTAs.
+template <auto Kernel, class... Args>
+cudaError_t launch_clusters(int dev, unsigned ctas, unsigned threads, unsigned cluster, size_t smem, cudaStream_t s,
+                            const Args&... args) {
+  const cudaError_t e = allow_all<Kernel>(dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (cluster > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, Kernel, args...);
 }
 
 }  // namespace tokgb

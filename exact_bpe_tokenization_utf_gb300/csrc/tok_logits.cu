@@ -25,7 +25,7 @@ namespace {
 constexpr uint32_t MAX_LOGITS = 1u << 20;
 constexpr int LG_THREADS = 256;
 constexpr int LG_CTAS = 3;        // per SM, where shared memory has room for them
-constexpr int SB_THREADS = 256;   // of k_seen_bits
+constexpr int SB_THREADS = 512;   // of k_seen_bits
 constexpr int LG_WARPS = LG_THREADS / 32;
 constexpr int PER = 16;           // scores per thread and step
 constexpr int EDGE = 16;          // places before a slice's first vector, for the scores that come before it (fewer)
@@ -958,21 +958,44 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
                 });
 }
 
-// One CTA per row: the bits in shared memory, then the row.
+// One cluster per row: each CTA sets the bits of its share of the ids in its
+// own shared memory; then each joins all CTAs' bits for its share of the row.
 __global__ void __launch_bounds__(SB_THREADS) k_seen_bits(const int32_t* ids, const long long* off, uint32_t n_logits,
                                                           uint32_t* seen, long long stride, int keep) {
-  extern __shared__ uint32_t s_bits[];
+  namespace cg = cooperative_groups;
+  extern __shared__ __align__(16) uint32_t s_bits[];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t rank = cluster.block_rank(), n_ranks = cluster.num_blocks(), b = blockIdx.x / n_ranks;
   const uint32_t words = (n_logits + 31) / 32;
-  uint32_t* row = seen + (long long)blockIdx.x * stride;
-  for (uint32_t w = threadIdx.x; w < words; w += SB_THREADS) s_bits[w] = keep ? row[w] : 0u;
+  const long long begin = off[b], n = off[b + 1] - begin, each = n > 0 ? (n + n_ranks - 1) / n_ranks : 0;
+  const long long i0 = min(each * rank, max(n, 0ll)), i1 = min(i0 + each, max(n, 0ll));
+  for (uint32_t w = threadIdx.x; w < words; w += SB_THREADS) s_bits[w] = 0;
   __syncthreads();
-  const long long end = off[blockIdx.x + 1];
-  for (long long i = off[blockIdx.x] + threadIdx.x; i < end; i += SB_THREADS) {
-    const uint32_t v = (uint32_t)ids[i];
-    if (v < n_logits) atomicOr(&s_bits[v >> 5], 1u << (v & 31));
+  constexpr int AHEAD = 8;  // loads of a thread in flight
+  for (long long i = i0 + threadIdx.x; i < i1; i += AHEAD * SB_THREADS) {
+    uint32_t v[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      v[j] = i + j * SB_THREADS < i1 ? (uint32_t)__ldcs(ids + begin + i + j * SB_THREADS) : 0xffffffffu;
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      // (text repeats its words: most bits are set already, and reading one is cheaper than setting it again)
+      const uint32_t bit = 1u << (v[j] & 31);
+      if (v[j] < n_logits && !(*static_cast<volatile uint32_t*>(s_bits + (v[j] >> 5)) & bit)) atomicOr(&s_bits[v[j] >> 5], bit);
+    }
   }
-  __syncthreads();
-  for (uint32_t w = threadIdx.x; w < words; w += SB_THREADS) row[w] = s_bits[w];
+  if (n_ranks > 1) cluster.sync();
+  else __syncthreads();
+  uint32_t* row = seen + (long long)b * stride;
+  const uint32_t share = (words + n_ranks - 1) / n_ranks, w1 = min((rank + 1) * share, words);
+  for (uint32_t w = rank * share + threadIdx.x; w < w1; w += SB_THREADS) {
+    uint32_t m = keep ? row[w] : 0u;
+    if (n_ranks == 1) m |= s_bits[w];
+    else
+      for (uint32_t q = 0; q < n_ranks; ++q) m |= cluster.map_shared_rank(s_bits, q)[w];
+    row[w] = m;
+  }
+  if (n_ranks > 1) cluster.sync();  // (until the others have read this CTA's bits)
 }
 
 size_t stage_bytes(int dtype, bool shifted) {
@@ -1005,7 +1028,7 @@ uint32_t slices(const tok_handle* h, const tok_logits_args& a, bool shifted, int
     if (best && a.n_logits / n < 2048) break;
     size_t smem;
     shape(a, shifted, arrays, n, &smem);
-    if (smem > 200 * 1024) continue;
+    if (smem > MOST_SHARED) continue;
     const unsigned fit = (unsigned)std::min<size_t>(LG_CTAS, (228 * 1024) / (smem + 2048));
     const unsigned long long room = (unsigned long long)fit * (unsigned)h->n_sms;
     const unsigned long long rounds = ((unsigned long long)a.rows * n + room - 1) / room;
@@ -1024,39 +1047,15 @@ bool alike(const void* p, int64_t stride, const void* q, int64_t q_stride, uint3
   return rows == 1 || ((uint64_t)(stride - q_stride) * size & 15u) == 0;
 }
 
-template <class K, class C>
-cudaError_t launch(K kernel, const C& call, unsigned ctas, unsigned cluster, size_t smem, cudaStream_t s) {
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(LG_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  if (cluster > 1) {
-    if (cluster > 8) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return e;
-    }
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-  return cudaLaunchKernelEx(&cfg, kernel, call);
-}
-
 template <class T>
-cudaError_t launch_forward(const LogitsCall& c, bool shifted, unsigned ctas, unsigned cluster, size_t smem, cudaStream_t s) {
-  return shifted ? launch(k_logits<T, true>, c, ctas, cluster, smem, s) : launch(k_logits<T, false>, c, ctas, cluster, smem, s);
+cudaError_t launch_forward(int dev, const LogitsCall& c, bool shifted, unsigned ctas, unsigned cluster, size_t smem, cudaStream_t s) {
+  return shifted ? launch_clusters<k_logits<T, true>>(dev, ctas, LG_THREADS, cluster, smem, s, c)
+                 : launch_clusters<k_logits<T, false>>(dev, ctas, LG_THREADS, cluster, smem, s, c);
 }
 template <class T>
-cudaError_t launch_grad(const GradCall& c, bool shifted, unsigned ctas, size_t smem, cudaStream_t s) {
-  return shifted ? launch(k_logits_grad<T, true>, c, ctas, 1, smem, s) : launch(k_logits_grad<T, false>, c, ctas, 1, smem, s);
+cudaError_t launch_grad(int dev, const GradCall& c, bool shifted, unsigned ctas, size_t smem, cudaStream_t s) {
+  return shifted ? launch_clusters<k_logits_grad<T, true>>(dev, ctas, LG_THREADS, 1, smem, s, c)
+                 : launch_clusters<k_logits_grad<T, false>>(dev, ctas, LG_THREADS, 1, smem, s, c);
 }
 
 int launched(tok_handle* h, cudaError_t e) {
@@ -1103,9 +1102,9 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream) tr
   c.shape = shape(*a, shifted, 1, n, &smem);
   c.in_place = a->d_out == a->d_logits;
   const unsigned ctas = a->rows * n;
-  const cudaError_t e = a->dtype == TOK_F32   ? launch_forward<float>(c, shifted, ctas, n, smem, s)
-                        : a->dtype == TOK_F16 ? launch_forward<__half>(c, shifted, ctas, n, smem, s)
-                                              : launch_forward<__nv_bfloat16>(c, shifted, ctas, n, smem, s);
+  const cudaError_t e = a->dtype == TOK_F32   ? launch_forward<float>(h->dev, c, shifted, ctas, n, smem, s)
+                        : a->dtype == TOK_F16 ? launch_forward<__half>(h->dev, c, shifted, ctas, n, smem, s)
+                                              : launch_forward<__nv_bfloat16>(h->dev, c, shifted, ctas, n, smem, s);
   return launched(h, e);
 } catch (...) {
   return TOK_ENOMEM;
@@ -1137,9 +1136,9 @@ int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logit
   size_t smem;
   c.shape = shape(*a, shifted, arrays, c.ranks, &smem);
   const unsigned ctas = a->rows * c.ranks;
-  const cudaError_t e = a->dtype == TOK_F32   ? launch_grad<float>(c, shifted, ctas, smem, s)
-                        : a->dtype == TOK_F16 ? launch_grad<__half>(c, shifted, ctas, smem, s)
-                                              : launch_grad<__nv_bfloat16>(c, shifted, ctas, smem, s);
+  const cudaError_t e = a->dtype == TOK_F32   ? launch_grad<float>(h->dev, c, shifted, ctas, smem, s)
+                        : a->dtype == TOK_F16 ? launch_grad<__half>(h->dev, c, shifted, ctas, smem, s)
+                                              : launch_grad<__nv_bfloat16>(h->dev, c, shifted, ctas, smem, s);
   return launched(h, e);
 } catch (...) {
   return TOK_ENOMEM;
@@ -1150,17 +1149,16 @@ int tok_seen_bits(tok_handle* h, const int32_t* d_ids, const int64_t* d_item_off
   if (!h) return TOK_EINVAL;
   if (!d_ids || !d_item_off || !d_seen || n == 0) return fail(h, TOK_EINVAL, "seen bits: a buffer is NULL, or n is 0");
   const uint32_t words = (n_logits + 31) / 32;
-  if (n > 0x7fffffffu || n_logits == 0 || n_logits > MAX_LOGITS || seen_stride < (int64_t)words)
+  if (n > 0x7ffffffu || n_logits == 0 || n_logits > MAX_LOGITS || seen_stride < (int64_t)words)
     return fail(h, TOK_EINVAL, "seen bits: n, n_logits or seen_stride is out of range");
   DeviceGuard g(h->dev);
-  const size_t bytes = words * sizeof(uint32_t);
-  if (bytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k_seen_bits, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return cuda_fail(h, e, "seen bits");
-  }
-  k_seen_bits<<<n, SB_THREADS, bytes, static_cast<cudaStream_t>(stream)>>>(
-      d_ids, reinterpret_cast<const long long*>(d_item_off), n_logits, d_seen, seen_stride, keep);
-  return launched(h, cudaGetLastError());
+  // few rows: more CTAs for each, up to a cluster of 16
+  uint32_t ranks = 16;
+  while (ranks > 1 && (unsigned long long)n * ranks > 4ull * (unsigned)h->n_sms) ranks /= 2;
+  return launched(h, launch_clusters<k_seen_bits>(h->dev, n * ranks, SB_THREADS, ranks, words * sizeof(uint32_t),
+                                                  static_cast<cudaStream_t>(stream), d_ids,
+                                                  reinterpret_cast<const long long*>(d_item_off), n_logits, d_seen,
+                                                  (long long)seen_stride, keep));
 } catch (...) {
   return TOK_ENOMEM;
 }

@@ -15,14 +15,13 @@
 namespace tokgb {
 namespace {
 
-constexpr int PG_THREADS = 256;
-constexpr int PG_PER = 4;                          // tokens per thread and tile
-constexpr int PG_TILE = PG_THREADS * PG_PER;       // tokens per tile
+constexpr int PG_THREADS = 1024;                   // most threads of a CTA
 constexpr int PG_MAX_LEN = 0x7fffffff;             // tokens of a request
 
 struct PagedCall {
   tok_paged_args a;
-  long long span;      // tokens per CTA, a multiple of PG_TILE
+  long long span;      // tokens per CTA, a multiple of its tile
+  int wide;            // slot, pos and req lie at 16-byte boundaries
   uint32_t* done;      // the handle's counter of finished CTAs (0 between calls), or nullptr: CTA 0 completes the call
 };
 
@@ -52,171 +51,201 @@ __device__ __forceinline__ Req load_req(const tok_paged_args& a, uint32_t k) {
   return r;
 }
 
-// One CTA takes a span of tokens.  It reads every request once: the blocks of
-// those that end before its span are its base, the sum over all of them and
-// their checks decide (alike in every CTA) whether the call goes through.
-__global__ void __launch_bounds__(PG_THREADS) k_paged_assign(PagedCall c) {
-  const tok_paged_args& a = c.a;
-  __shared__ long long sh[PG_THREADS / 32], sh_first;
-  __shared__ unsigned s_bad, s_kf, s_last;
-  __shared__ int s_req[PG_TILE], s_add[PG_TILE + 1];
-  __shared__ int s_w[PG_THREADS / 32], s_m[PG_THREADS / 32];
-  const int tid = threadIdx.x;
-  const long long n_free = *a.d_n_free;
-  const long long t_begin = (long long)blockIdx.x * c.span;
-  if (tid == 0) {
-    s_bad = s_kf = 0xffffffffu;
-    s_last = 0;
-    sh_first = 0;
+// sums of two numbers over the block, in every thread; sh: 2 * 32 words
+__device__ __forceinline__ void block_sums(long long& a, long long& b, long long* sh) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, n = blockDim.x >> 5;
+  if (lane == 0) {
+    sh[warp] = a;
+    sh[32 + warp] = b;
   }
   __syncthreads();
-  long long sum = 0, before = 0;
-  bool bad = false;
-  for (uint32_t k = tid; k < a.n; k += PG_THREADS) {
+  a = lane < n ? sh[lane] : 0;
+  b = lane < n ? sh[32 + lane] : 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+}
+
+// true in one CTA of the grid: the one that gets here last (done is 0 again
+// then), or without a counter the first one
+__device__ __forceinline__ bool completes(uint32_t* done, unsigned* sh) {
+  if (!done) return blockIdx.x == 0;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const bool last = atomicAdd(done, 1u) == gridDim.x - 1;
+    if (last) *done = 0;
+    *sh = last;
+  }
+  __syncthreads();
+  return *sh != 0;
+}
+
+// One CTA takes a span of tokens, PER a thread at a time.  It reads every
+// request once: the blocks of those that end before its span are its base,
+// the sum over all of them and their checks decide (alike in every CTA)
+// whether the call goes through.  This redundant pass over 20 bytes a request
+// costs less than a second launch, or a CTA's wait for another's sums.
+template <int PER>
+__global__ void __launch_bounds__(PG_THREADS, 1) k_paged_assign(PagedCall c) {
+  const tok_paged_args& a = c.a;
+  constexpr int MOST = PG_THREADS * PER;
+  __shared__ long long sh[64];
+  __shared__ unsigned s_bad, s_wide, s_kf, s_last;
+  __shared__ int s_req[MOST], s_add[MOST + 1];
+  __shared__ int s_w[32], s_m[32];
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int tile = nt * PER;
+  const long long n_free = *a.d_n_free, n_tok = a.d_item_off[a.n];
+  const long long t_begin = (long long)blockIdx.x * c.span;
+  if (tid == 0) s_bad = s_wide = s_kf = 0xffffffffu;
+  __syncthreads();
+  long long total = 0, carry = 0;
+#pragma unroll 4
+  for (uint32_t k = tid; k < a.n; k += nt) {
     const Req r = load_req(a, k);
-    if (r.bad || r.wide) {
-      atomicMin(&s_bad, k);
-      bad |= r.bad;
-      sum += r.extra;
-      continue;
-    }
-    sum += r.extra;
-    if (r.end <= t_begin) before += r.extra;
+    total += r.extra;
+    if (r.bad) atomicMin(&s_bad, k);
+    else if (r.wide) atomicMin(&s_wide, k);
+    else if (r.end <= t_begin) carry += r.extra;
     else if (r.off < r.end) atomicMin(&s_kf, k);
   }
-  const int any_bad = __syncthreads_or(bad);
-  long long total, carry;
-  block_excl_sum(sum, &total, sh);
-  block_excl_sum(before, &carry, sh);
-  const long long n_tok = a.d_item_off[a.n];
+  block_sums(total, carry, sh);  // (its barrier also completes the words above)
   int code = ST_OK;
-  if (any_bad || n_free < 0) code = TOK_EINVAL;
-  else if (s_bad != 0xffffffffu || (unsigned long long)n_tok > a.cap || total > n_free) code = TOK_EBUF;
+  if (s_bad != 0xffffffffu || n_free < 0) code = TOK_EINVAL;
+  else if (s_wide != 0xffffffffu || (unsigned long long)n_tok > a.cap || total > n_free) code = TOK_EBUF;
   const uint32_t bs = a.block_size;
   uint32_t kf = s_kf;
-  long long t_end = t_begin + c.span;
-  if (t_end > (long long)a.cap) t_end = (long long)a.cap;
-  for (long long t0 = t_begin; t0 < t_end; t0 += PG_TILE) {
-    if (code != ST_OK || t0 >= n_tok) {  // padding
-      for (int i = tid; i < PG_TILE && t0 + i < t_end; i += PG_THREADS) {
-        a.d_slot[t0 + i] = -1;
-        if (a.d_pos) a.d_pos[t0 + i] = -1;
-        if (a.d_req) a.d_req[t0 + i] = -1;
+  const long long t_end = min(t_begin + c.span, (long long)a.cap);
+  for (long long t0 = t_begin; t0 < t_end; t0 += tile) {
+    const long long mine = t0 + (long long)tid * PER;
+    long long slot[PER];
+    int pos[PER], req[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      slot[j] = -1;
+      pos[j] = req[j] = -1;
+    }
+    if (code == ST_OK && t0 < n_tok) {
+      // the requests with tokens in the tile mark their first one there, and
+      // add their blocks at the first token after them
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        s_req[j * nt + tid] = -1;
+        s_add[j * nt + tid] = 0;
       }
-      continue;
-    }
-    // the requests with tokens in the tile mark their first one there, and
-    // add their blocks at the first token after them
-    for (int i = tid; i <= PG_TILE; i += PG_THREADS) {
-      if (i < PG_TILE) s_req[i] = -1;
-      s_add[i] = 0;
-    }
-    __syncthreads();
-    const long long t1 = t0 + PG_TILE;
-    uint32_t k0 = kf;
-    for (; k0 < a.n && a.d_item_off[k0] < t1; k0 += PG_THREADS) {
-      const uint32_t k = k0 + tid;
-      if (k < a.n) {
-        const Req r = load_req(a, k);
-        if (r.off < r.end && r.off < t1 && r.end > t0) {
-          s_req[r.off > t0 ? (int)(r.off - t0) : 0] = (int)k;
-          if (r.end <= t1) s_add[(int)(r.end - t0)] = r.extra;
-          if (r.end >= t1) s_last = k;  // (one request covers the tile's last token)
+      if (tid == 0) s_add[tile] = 0;
+      __syncthreads();
+      const long long t1 = t0 + tile;
+      for (uint32_t k0 = kf; k0 < a.n && a.d_item_off[k0] < t1; k0 += nt) {
+        const uint32_t k = k0 + tid;
+        if (k < a.n) {
+          const Req r = load_req(a, k);
+          if (r.off < r.end && r.off < t1 && r.end > t0) {
+            s_req[r.off > t0 ? (int)(r.off - t0) : 0] = (int)k;
+            if (r.end <= t1) s_add[(int)(r.end - t0)] = r.extra;
+            if (r.end >= t1) s_last = k;  // (one request covers the tile's last token)
+          }
         }
       }
-    }
-    __syncthreads();
-    // each token's request (a running maximum) and base (a running sum)
-    int m[PG_PER], w[PG_PER];
-    int mm = -1, ww = 0;
+      __syncthreads();
+      // each token's request (a running maximum) and base (a running sum)
+      int m[PER], w[PER], mm = -1, ww = 0;
 #pragma unroll
-    for (int j = 0; j < PG_PER; ++j) {
-      mm = max(mm, s_req[tid * PG_PER + j]);
-      ww += s_add[tid * PG_PER + j];
-      m[j] = mm;
-      w[j] = ww;
-    }
-    const int lane = tid & 31, warp = tid >> 5;
-    int im = mm, iw = ww;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, im, o), y = __shfl_up_sync(0xffffffffu, iw, o);
-      if (lane >= o) {
-        im = max(im, x);
-        iw += y;
+      for (int j = 0; j < PER; ++j) {
+        mm = max(mm, s_req[tid * PER + j]);
+        ww += s_add[tid * PER + j];
+        m[j] = mm;
+        w[j] = ww;
       }
-    }
-    if (lane == 31) {
-      s_m[warp] = im;
-      s_w[warp] = iw;
-    }
-    int em = __shfl_up_sync(0xffffffffu, im, 1), ew = iw - ww;
-    if (lane == 0) em = -1;
-    __syncthreads();
-    int tot = 0;
+      int im = mm, iw = ww;
 #pragma unroll
-    for (int q = 0; q < PG_THREADS / 32; ++q) {
-      if (q < warp) {
-        em = max(em, s_m[q]);
-        ew += s_w[q];
-      }
-      tot += s_w[q];
-    }
-#pragma unroll
-    for (int j = 0; j < PG_PER; ++j) {
-      const long long t = t0 + tid * PG_PER + j;
-      if (t >= t_end) break;
-      long long slot = -1;
-      int pos = -1, req = -1;
-      if (t < n_tok) {
-        req = max(em, m[j]);
-        const Req r = load_req(a, (uint32_t)req);
-        pos = (int)(r.ctx + (t - r.off));
-        const uint32_t col = (uint32_t)pos / bs, in = (uint32_t)pos - col * bs;
-        int32_t* entry = a.d_table + (long long)req * a.table_stride + col;
-        int blk;
-        if ((int)col >= r.have) {
-          blk = a.d_free[n_free - 1 - (carry + ew + w[j] + ((int)col - r.have))];
-          if (in == 0) *entry = blk;
-        } else {
-          blk = *entry;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, im, o), y = __shfl_up_sync(0xffffffffu, iw, o);
+        if (lane >= o) {
+          im = max(im, x);
+          iw += y;
         }
-        slot = (long long)blk * bs + in;
       }
-      a.d_slot[t] = slot;
-      if (a.d_pos) a.d_pos[t] = pos;
-      if (a.d_req) a.d_req[t] = req;
+      if (lane == 31) {
+        s_m[warp] = im;
+        s_w[warp] = iw;
+      }
+      int em = __shfl_up_sync(0xffffffffu, im, 1), ew = iw - ww;
+      if (lane == 0) em = -1;
+      __syncthreads();
+      int tot = 0;
+      for (int q = 0; q < nt / 32; ++q) {
+        const int x = s_m[q], y = s_w[q];
+        if (q < warp) {
+          em = max(em, x);
+          ew += y;
+        }
+        tot += y;
+      }
+      Req r{};
+      int of = -1;  // r is this request's
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const long long t = mine + j;
+        if (t < n_tok) {
+          req[j] = max(em, m[j]);
+          if (req[j] != of) r = load_req(a, (uint32_t)(of = req[j]));
+          pos[j] = (int)(r.ctx + (t - r.off));
+          const uint32_t col = (uint32_t)pos[j] / bs, in = (uint32_t)pos[j] - col * bs;
+          int32_t* entry = a.d_table + (long long)req[j] * a.table_stride + col;
+          int blk;
+          if ((int)col >= r.have) {
+            blk = a.d_free[n_free - 1 - (carry + ew + w[j] + ((int)col - r.have))];
+            if (in == 0) *entry = blk;
+          } else {
+            blk = *entry;
+          }
+          slot[j] = (long long)blk * bs + in;
+        }
+      }
+      carry += tot + s_add[tile];
+      if (t1 < n_tok) kf = s_last;
+      __syncthreads();
     }
-    carry += tot + s_add[PG_TILE];
-    if (t1 < n_tok) kf = s_last;
-    __syncthreads();
+    if (PER == 4 && c.wide && mine + PER <= t_end) {
+      longlong2* q = reinterpret_cast<longlong2*>(a.d_slot + mine);
+      q[0] = make_longlong2(slot[0], slot[1 % PER]);
+      q[1] = make_longlong2(slot[2 % PER], slot[3 % PER]);
+      if (a.d_pos) *reinterpret_cast<int4*>(a.d_pos + mine) = make_int4(pos[0], pos[1 % PER], pos[2 % PER], pos[3 % PER]);
+      if (a.d_req) *reinterpret_cast<int4*>(a.d_req + mine) = make_int4(req[0], req[1 % PER], req[2 % PER], req[3 % PER]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (mine + j < t_end) {
+          a.d_slot[mine + j] = slot[j];
+          if (a.d_pos) a.d_pos[mine + j] = pos[j];
+          if (a.d_req) a.d_req[mine + j] = req[j];
+        }
+    }
   }
   // seq_len, n_free_out and the status: by the CTA that finishes last where
   // they may replace what the others still read, else by the first
-  if (c.done) {
-    __syncthreads();
-    if (tid == 0) {
-      __threadfence();
-      const uint32_t d = atomicAdd(c.done, 1u);
-      s_last = d == gridDim.x - 1;
-      if (s_last) *c.done = 0;
-    }
-    __syncthreads();
-    if (!s_last) return;
-  } else if (blockIdx.x != 0) {
-    return;
-  }
+  if (!completes(c.done, &s_last)) return;
   if (a.d_seq_len)
-    for (uint32_t k = tid; k < a.n; k += PG_THREADS) {
+    for (uint32_t k = tid; k < a.n; k += nt) {
       const long long ctx = a.d_ctx_len ? a.d_ctx_len[k] : 0;
       a.d_seq_len[k] = code == ST_OK ? ctx + (a.d_item_off[k + 1] - a.d_item_off[k]) : ctx;
     }
   if (tid == 0) {
+    const unsigned first = min(s_bad, s_wide);
     *a.d_n_free_out = code == ST_OK ? n_free - total : n_free;
     a.d_status[0] = code;
     a.d_status[1] = total;
     a.d_status[2] = n_tok;
-    a.d_status[3] = s_bad == 0xffffffffu ? -1 : (long long)s_bad;
+    a.d_status[3] = first == 0xffffffffu ? -1 : (long long)first;
   }
 }
 
@@ -246,62 +275,49 @@ __device__ __forceinline__ long long release_count(const ReleaseCall& c, uint32_
 }
 
 // One CTA takes a range of requests; as in k_paged_assign each CTA reads all
-// of them once for its base and for the checks.
-__global__ void __launch_bounds__(PG_THREADS) k_paged_release(ReleaseCall c) {
-  __shared__ long long sh[PG_THREADS / 32], s_cnt[PG_THREADS];
+// of them once for its base and for the checks.  A warp copies a request's
+// blocks.
+__global__ void __launch_bounds__(PG_THREADS, 1) k_paged_release(ReleaseCall c) {
+  __shared__ long long sh[64], s_base[PG_THREADS], s_scan[32];
   __shared__ unsigned s_bad, s_last;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const long long n_free = *c.n_free;
   const uint32_t k_begin = min(blockIdx.x * c.per, c.n), k_end = min(k_begin + c.per, c.n);
   if (tid == 0) s_bad = 0xffffffffu;
   __syncthreads();
-  long long sum = 0, before = 0;
-  for (uint32_t k = tid; k < c.n; k += PG_THREADS) {
+  long long total = 0, carry = 0;
+#pragma unroll 4
+  for (uint32_t k = tid; k < c.n; k += nt) {
     bool bad = false;
     const long long m = release_count(c, k, &bad);
     if (bad) atomicMin(&s_bad, k);
-    sum += m;
-    if (k < k_begin) before += m;
+    total += m;
+    if (k < k_begin) carry += m;
   }
-  long long total, carry;
-  block_excl_sum(sum, &total, sh);
-  block_excl_sum(before, &carry, sh);
+  block_sums(total, carry, sh);
   int code = ST_OK;
   if (s_bad != 0xffffffffu || n_free < 0) code = TOK_EINVAL;
   else if ((unsigned long long)(n_free + total) > c.free_cap) code = TOK_EBUF;
   if (code == ST_OK) {
-    for (uint32_t k0 = k_begin; k0 < k_end; k0 += PG_THREADS) {
+    for (uint32_t k0 = k_begin; k0 < k_end; k0 += nt) {
       const uint32_t k = k0 + tid;
       bool bad = false;
       const long long m = k < k_end ? release_count(c, k, &bad) : 0;
-      long long tile;
-      block_excl_sum(m, &tile, sh);
-      s_cnt[tid] = m;
+      long long sum;
+      s_base[tid] = n_free + carry + block_excl_sum(m, &sum, s_scan);
       __syncthreads();
-      long long base = n_free + carry;
-      for (uint32_t i = 0; i < PG_THREADS && k0 + i < k_end; ++i) {
-        const long long cnt = s_cnt[i];
+      for (uint32_t i = warp; i < (uint32_t)nt && k0 + i < k_end; i += nt / 32) {
+        const long long cnt = release_count(c, k0 + i, &bad);
         const int32_t* row = c.table + (long long)(k0 + i) * c.stride;
-        for (long long j = tid; j < cnt; j += PG_THREADS) c.free_stack[base + j] = row[j];
-        base += cnt;
+        int32_t* to = c.free_stack + s_base[i];
+#pragma unroll 4
+        for (long long j = lane; j < cnt; j += 32) to[j] = row[j];
       }
-      carry += tile;
+      carry += sum;
       __syncthreads();
     }
   }
-  if (c.done) {
-    __syncthreads();
-    if (tid == 0) {
-      __threadfence();
-      const uint32_t d = atomicAdd(c.done, 1u);
-      s_last = d == gridDim.x - 1;
-      if (s_last) *c.done = 0;
-    }
-    __syncthreads();
-    if (!s_last) return;
-  } else if (blockIdx.x != 0) {
-    return;
-  }
+  if (!completes(c.done, &s_last)) return;
   if (tid == 0) {
     *c.n_free_out = code == ST_OK ? n_free + total : n_free;
     c.status[0] = code;
@@ -309,6 +325,13 @@ __global__ void __launch_bounds__(PG_THREADS) k_paged_release(ReleaseCall c) {
     c.status[2] = 0;
     c.status[3] = s_bad == 0xffffffffu ? -1 : (long long)s_bad;
   }
+}
+
+// threads of a CTA for n things at a time: 128 to PG_THREADS
+unsigned threads_for(unsigned long long n) {
+  unsigned t = 128;
+  while (t < (unsigned)PG_THREADS && t < n) t *= 2;
+  return t;
 }
 
 }  // namespace
@@ -329,12 +352,21 @@ int tok_paged_assign(tok_handle* h, const tok_paged_args* a, void* stream) try {
   DeviceGuard g(h->dev);
   PagedCall c{};
   c.a = *a;
-  const long long tiles = std::max<long long>(1, ((long long)a->cap + PG_TILE - 1) / PG_TILE);
+  // one token a thread while all of them fit two CTAs per SM (a decode step's
+  // tokens are of as many requests: one's loads would wait for another's), else four
+  const unsigned threads = threads_for(std::max<unsigned long long>(a->n, a->cap));
+  const bool one = a->cap <= 2ull * (unsigned)h->n_sms * threads;
+  const long long tile = (long long)threads * (one ? 1 : 4);
+  const long long tiles = std::max<long long>(1, ((long long)a->cap + tile - 1) / tile);
   const long long ctas = std::min<long long>(tiles, 2ll * h->n_sms);
-  c.span = (tiles + ctas - 1) / ctas * PG_TILE;
+  c.span = (tiles + ctas - 1) / ctas * tile;
+  c.wide = ((reinterpret_cast<uintptr_t>(a->d_slot) | reinterpret_cast<uintptr_t>(a->d_pos) |
+             reinterpret_cast<uintptr_t>(a->d_req)) & 15u) == 0;
   const bool in_place = a->d_n_free_out == a->d_n_free || (a->d_seq_len && a->d_seq_len == a->d_ctx_len);
   c.done = in_place && ctas > 1 ? h->d_done : nullptr;
-  k_paged_assign<<<(unsigned)ctas, PG_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(c);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (one) k_paged_assign<1><<<(unsigned)ctas, threads, 0, s>>>(c);
+  else k_paged_assign<4><<<(unsigned)ctas, threads, 0, s>>>(c);
   h->launches += 1;
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TOK_OK : cuda_fail(h, e, "kernel launch");
@@ -366,10 +398,10 @@ int tok_paged_release(tok_handle* h, const int64_t* d_seq_len, const uint8_t* d_
   c.n_free = reinterpret_cast<const long long*>(d_n_free);
   c.n_free_out = reinterpret_cast<long long*>(d_n_free_out);
   c.status = reinterpret_cast<long long*>(d_status);
-  const uint32_t ctas = std::min<uint32_t>(n, 2u * (uint32_t)h->n_sms);
+  const uint32_t ctas = std::min<uint32_t>((n + 3) / 4, 2u * (uint32_t)h->n_sms);
   c.per = (n + ctas - 1) / ctas;
   c.done = d_n_free_out == d_n_free && ctas > 1 ? h->d_done : nullptr;
-  k_paged_release<<<ctas, PG_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(c);
+  k_paged_release<<<ctas, std::min(512u, threads_for(n)), 0, static_cast<cudaStream_t>(stream)>>>(c);
   h->launches += 1;
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TOK_OK : cuda_fail(h, e, "kernel launch");
