@@ -17,11 +17,13 @@ namespace {
 
 constexpr uint32_t MAX_LOGITS = 1u << 20;
 constexpr uint32_t DEAD = 0xffffu;
+constexpr uint32_t WHOLE = 0x80000000u;  // of a group: its tokens' other bytes do not change the state
 constexpr uint32_t NO_TOKEN = 0xffffffffu;
 constexpr int GR_THREADS = 512;
 
 struct DevGrammar {
   const uint16_t* next;   // n_states rows of 256
+  const uint32_t* leaves; // per state: the kinds of bytes of which some change the state
   const uint8_t* accept;
   uint32_t n_states;
 };
@@ -68,13 +70,33 @@ __global__ void __launch_bounds__(128) k_grammar_states(DevGrammar g, DevTokens 
   c.state_out[k] = s == DEAD ? -1 : (int32_t)s;
 }
 
+// read once: kept out of L1, where the automaton's rows are
+__device__ __forceinline__ uint32_t load_once(const uint32_t* p) {
+  uint32_t x;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint32_t load_once(const uint16_t* p) {
+  uint16_t x;
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(x) : "l"(p));
+  return x;
+}
+
+// a lane's token of a group whose common bytes lead to state s
+struct Item {
+  uint32_t s, id, rest, at, word;
+};
+
 // One cluster per row.  A thread walks a group's common first bytes, so that
-// one step decides over up to 32 tokens; where the state survives, a warp walks
-// the group's tokens, one per lane (sorted tokens read neighbouring bytes from
-// equal states).  Allowed tokens set their bits in the CTA's shared memory;
-// the cluster's CTAs then join their bits, a share of the row each, and write it.
-// Rows (of GR_THREADS at a time) in equal states are walked once, by the
-// first one's cluster, which writes all of them.
+// one step decides over up to 32 tokens; where the state survives, a warp
+// takes the group's tokens, one per lane.  Bytes of kinds that do not change
+// the state need no walk: inside a string that is most tokens, often a whole
+// group.  The others are walked (sorted tokens read neighbouring bytes from equal
+// states), two groups at a time with the next two on their way.  Allowed tokens
+// set their bits in the CTA's shared memory; the cluster's CTAs then join
+// their bits, a share of the row each, and write it.  Rows (of GR_THREADS at
+// a time) in equal states are walked once, by the first one's cluster, which
+// writes all of them.
 __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTokens v, MaskCall c) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint32_t s_mem[];
@@ -84,10 +106,16 @@ __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTo
   const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
   const uint32_t n_words = (c.n_logits + 31) / 32;
   uint32_t* bits = s_mem;                               // a row's
-  uint32_t* live = s_mem + ((n_words + 3) / 4) * 4;     // group | state << 16
+  uint2* live = reinterpret_cast<uint2*>(s_mem + ((n_words + 3) / 4) * 4);  // group | state << 16, words' place | WHOLE
   const uint32_t per = (v.n_groups + n_ranks - 1) / n_ranks;
-  // this thread's group, on its way while the states are walked
   const uint32_t g0 = min(rank * per, v.n_groups), g1 = min(g0 + per, v.n_groups);
+  // this thread's first group, on its way while the states are walked
+  uint4 r = make_uint4(0, 0, 0, 0);
+  uint32_t kinds = 0;
+  if (g0 + tid < g1) {
+    r = __ldg(reinterpret_cast<const uint4*>(v.group + g0 + tid));
+    kinds = __ldg(v.group_kinds + g0 + tid);
+  }
 
   // the states of this row's window, and the rows among them that equal it
   const uint32_t w0 = k / GR_THREADS * GR_THREADS, j = w0 + tid;
@@ -107,48 +135,69 @@ __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTo
   if (__syncthreads_or(same && j < k)) return;  // (in every CTA of the cluster alike)
 
   if (s0 != DEAD) {
-    for (uint32_t q = g0 + tid; q < g1; q += GR_THREADS) {
-      const uint4 r = __ldg(reinterpret_cast<const uint4*>(v.group + q));
+    for (uint32_t base = g0; base < g1; base += GR_THREADS) {
+      const uint32_t q = base + tid;
+      if (base != g0 && q < g1) {
+        r = __ldg(reinterpret_cast<const uint4*>(v.group + q));
+        kinds = __ldg(v.group_kinds + q);
+      }
       unsigned long long head = (unsigned long long)r.y << 32 | r.x;
-      uint32_t s = s0;
-      for (uint32_t i = r.z & 15u; i && s != DEAD; --i) {
+      uint32_t s = q < g1 ? s0 : DEAD;
+      for (uint32_t i = r.z; i && s != DEAD; --i) {
         s = __ldg(g.next + s * 256u + (uint32_t)(head & 255u));
         head >>= 8;
       }
-      if (s != DEAD) live[atomicAdd(&s_live, 1u)] = q | s << 16;
+      const uint32_t alive = __ballot_sync(0xffffffffu, s != DEAD);
+      uint32_t at = 0;
+      if (lane == 0 && alive) at = atomicAdd(&s_live, (uint32_t)__popc(alive));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(alive & ((1u << lane) - 1u));
+      if (s != DEAD) {
+        const uint32_t whole = (kinds & __ldg(g.leaves + s)) == 0 ? WHOLE : 0u;
+        live[at] = make_uint2(q | s << 16, r.w | whole);
+      }
     }
     __syncthreads();
     const uint32_t n_live = s_live;
-    // two groups at a time: their walks do not depend on one another
-    for (uint32_t e = warp; e < n_live; e += 2 * (GR_THREADS / 32)) {
-      uint32_t s[2], id[2], rest[2], at[2], words = 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t f = e + h * (GR_THREADS / 32);
-        const bool any = f < n_live;
-        const uint32_t x = live[any ? f : e], q = x & 0xffffu;
-        const TokenGroup* r = v.group + q;
-        s[h] = x >> 16;
-        id[h] = any ? __ldg(v.id + q * 32 + lane) : NO_TOKEN;
-        rest[h] = id[h] == NO_TOKEN ? 0u : __ldg(v.rest + q * 32 + lane);
-        at[h] = __ldg(&r->at) + lane;
-        words = max(words, any ? __ldg(&r->shape) >> 4 : 0u);
+    auto load = [&](uint32_t f) {
+      Item t{DEAD, NO_TOKEN, 0, 0, 0};
+      if (f < n_live) {
+        const uint2 e = live[f];
+        const uint32_t at = (e.x & 0xffffu) * 32 + lane;
+        t.id = load_once(v.id + at);
+        t.s = e.x >> 16;
+        if (!(e.y & WHOLE)) {
+          const uint32_t leaves = __ldg(g.leaves + t.s);
+          t.rest = load_once(v.kinds + at) & leaves ? load_once(v.rest + at) : 0u;
+          t.at = e.y + lane;
+          t.word = t.rest ? load_once(v.words + t.at) : 0u;
+        }
       }
-      for (uint32_t w = 0; w < words; ++w) {
-        uint32_t b[2];
+      return t;
+    };
+    constexpr uint32_t W = GR_THREADS / 32;
+    Item now[2] = {load(warp), load(warp + W)};
+    for (uint32_t e = warp; e < n_live; e += 2 * W) {
+      const Item next[2] = {load(e + 2 * W), load(e + 3 * W)};
+      for (uint32_t w = 0; __any_sync(0xffffffffu, (now[0].rest > w && now[0].s != DEAD) || (now[1].rest > w && now[1].s != DEAD));
+           w += 4) {
+        if (w) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) b[h] = rest[h] > 4 * w && s[h] != DEAD ? __ldg(v.words + at[h] + 32 * w) : 0u;
+          for (int h = 0; h < 2; ++h)
+            if (now[h].rest > w && now[h].s != DEAD) now[h].word = load_once(v.words + now[h].at + 8 * w);
+        }
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            if (4 * w + i < rest[h] && s[h] != DEAD) s[h] = __ldg(g.next + s[h] * 256u + (b[h] >> (8 * i) & 255u));
+            if (w + i < now[h].rest && now[h].s != DEAD)
+              now[h].s = __ldg(g.next + now[h].s * 256u + (now[h].word >> (8 * i) & 255u));
         }
-        if (!__any_sync(0xffffffffu, (rest[0] > 4 * w + 4 && s[0] != DEAD) || (rest[1] > 4 * w + 4 && s[1] != DEAD))) break;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (s[h] != DEAD && id[h] < c.n_logits) atomicOr(&bits[id[h] >> 5], 1u << (id[h] & 31));
+      for (int h = 0; h < 2; ++h) {
+        if (now[h].s != DEAD && now[h].id < c.n_logits) atomicOr(&bits[now[h].id >> 5], 1u << (now[h].id & 31));
+        now[h] = next[h];
+      }
     }
   }
   if (n_ranks > 1) cluster.sync();
@@ -170,11 +219,16 @@ __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTo
   if (n_ranks > 1) cluster.sync();  // (until the others have read this CTA's bits)
 }
 
+// bytes of shared memory of a CTA: a row's bits, and its groups' list
+size_t mask_bytes(const tok_handle* h, uint32_t n_logits, uint32_t ranks) {
+  return ((size_t)(n_logits + 31) / 32 + 3) / 4 * 16 + (size_t)(h->tokens.n_groups + ranks - 1) / ranks * sizeof(uint2);
+}
+
 // CTAs of a row's cluster: 16 while few rows leave SMs without work, 4 where
 // there are enough of them (their groups then keep a CTA's warps busy).
-uint32_t mask_ranks(const tok_handle* h, uint32_t n) {
+uint32_t mask_ranks(const tok_handle* h, uint32_t n, uint32_t n_logits) {
   uint32_t s = 16;
-  while (s > 4 && (unsigned long long)n * s > 4ull * (unsigned)h->n_sms) s /= 2;
+  while (s > 4 && (unsigned long long)n * s > 4ull * (unsigned)h->n_sms && mask_bytes(h, n_logits, s / 2) <= MOST_SHARED) s /= 2;
   return s;
 }
 
@@ -195,7 +249,7 @@ int ensure_tokens(tok_handle* h) {
     return d ? d < 0 : la < lb;
   });
   std::vector<TokenGroup> group;
-  std::vector<uint32_t> words, id;
+  std::vector<uint32_t> words, id, kinds, group_kinds;
   std::vector<uint16_t> rest;
   for (uint32_t i = 0; i < n;) {
     uint32_t m = 1;
@@ -208,14 +262,23 @@ int ensure_tokens(tok_handle* h) {
     for (uint32_t j = 0; j < p; ++j) r.head |= (unsigned long long)at(a)[j] << (8 * j);
     for (uint32_t q = 0; q < m; ++q) most = std::max(most, len(order[i + q]) - p);
     const uint32_t nw = (most + 3) / 4;
-    r.shape = p | nw << 4;
+    uint32_t all = 0;
+    r.prefix = p;
     words.resize(words.size() + (size_t)nw * 32, 0u);
     for (uint32_t q = 0; q < 32; ++q) {
       id.push_back(q < m ? order[i + q] : NO_TOKEN);
       const uint32_t l = q < m ? len(order[i + q]) - p : 0u;
       rest.push_back((uint16_t)l);
-      for (uint32_t j = 0; j < l; ++j) words[r.at + (size_t)(j / 4) * 32 + q] |= (uint32_t)at(order[i + q])[p + j] << (8 * (j & 3));
+      uint32_t some = 0;
+      for (uint32_t j = 0; j < l; ++j) {
+        const uint8_t x = at(order[i + q])[p + j];
+        words[r.at + (size_t)(j / 4) * 32 + q] |= (uint32_t)x << (8 * (j & 3));
+        some |= 1u << byte_kind(x);
+      }
+      kinds.push_back(some);
+      all |= some;
     }
+    group_kinds.push_back(all);
     group.push_back(r);
     i += m;
   }
@@ -224,17 +287,19 @@ int ensure_tokens(tok_handle* h) {
   std::vector<uint32_t> off(n + 1);
   for (uint32_t t = 0; t <= n; ++t) off[t] = (uint32_t)h->vocab_off[t];
   // one allocation; the parts by falling alignment
-  const void* part[6] = {group.data(), words.data(), id.data(), off.data(), rest.data(), bytes};
-  const size_t size[6] = {group.size() * sizeof(TokenGroup), words.size() * 4, id.size() * 4, off.size() * 4, rest.size() * 2, nb};
-  size_t place[7] = {0};
-  for (int i = 0; i < 6; ++i) place[i + 1] = place[i] + (size[i] + 15) / 16 * 16;
+  constexpr int PARTS = 8;
+  const void* part[PARTS] = {group.data(), words.data(), id.data(), kinds.data(), group_kinds.data(), off.data(), rest.data(), bytes};
+  const size_t size[PARTS] = {group.size() * sizeof(TokenGroup), words.size() * 4, id.size() * 4, kinds.size() * 4,
+                              group_kinds.size() * 4, off.size() * 4, rest.size() * 2, nb};
+  size_t place[PARTS + 1] = {0};
+  for (int i = 0; i < PARTS; ++i) place[i + 1] = place[i] + (size[i] + 15) / 16 * 16;
   uint8_t* p = nullptr;
-  cudaError_t e = halloc(h, &p, place[6]);
+  cudaError_t e = halloc(h, &p, place[PARTS]);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return fail(h, TOK_ENOMEM, "grammar: allocation failed");
   }
-  for (int i = 0; i < 6 && e == cudaSuccess; ++i)
+  for (int i = 0; i < PARTS && e == cudaSuccess; ++i)
     if (size[i]) e = cudaMemcpy(p + place[i], part[i], size[i], cudaMemcpyHostToDevice);
   if (e != cudaSuccess) {
     cudaFree(p);
@@ -244,9 +309,11 @@ int ensure_tokens(tok_handle* h) {
   h->tokens.group = reinterpret_cast<const TokenGroup*>(p + place[0]);
   h->tokens.words = reinterpret_cast<const uint32_t*>(p + place[1]);
   h->tokens.id = reinterpret_cast<const uint32_t*>(p + place[2]);
-  h->tokens.off = reinterpret_cast<const uint32_t*>(p + place[3]);
-  h->tokens.rest = reinterpret_cast<const uint16_t*>(p + place[4]);
-  h->tokens.bytes = p + place[5];
+  h->tokens.kinds = reinterpret_cast<const uint32_t*>(p + place[3]);
+  h->tokens.group_kinds = reinterpret_cast<const uint32_t*>(p + place[4]);
+  h->tokens.off = reinterpret_cast<const uint32_t*>(p + place[5]);
+  h->tokens.rest = reinterpret_cast<const uint16_t*>(p + place[6]);
+  h->tokens.bytes = p + place[7];
   h->tokens.n = n;
   h->tokens.n_groups = (uint32_t)group.size();
   return TOK_OK;
@@ -273,30 +340,34 @@ int tok_grammar_load(tok_handle* h, const int32_t* next, const uint8_t* accept, 
   if (!next || !accept) return fail(h, TOK_EINVAL, "grammar: next or accept is NULL");
   if (n_states == 0 || n_states > DEAD) return fail(h, TOK_EINVAL, "grammar: n_states is out of range");
   std::vector<uint16_t> t((size_t)n_states * 256);
+  std::vector<uint32_t> leaves(n_states, 0u);
   for (size_t i = 0; i < t.size(); ++i) {
     if (next[i] < -1 || next[i] >= (int32_t)n_states) return fail(h, TOK_EINVAL, "grammar: a next state is out of range");
     t[i] = next[i] < 0 ? (uint16_t)DEAD : (uint16_t)next[i];
+    if (next[i] != (int32_t)(i / 256)) leaves[i / 256] |= 1u << byte_kind((uint8_t)(i & 255));
   }
   DeviceGuard dg(h->dev);
   int rc = ensure_tokens(h);
   if (rc) return rc;
   tok_grammar* g = new tok_grammar();
-  const size_t tb = t.size() * sizeof(uint16_t);
-  cudaError_t e = halloc(h, &g->d_mem, tb + n_states);
+  const size_t tb = t.size() * sizeof(uint16_t), lb = n_states * sizeof(uint32_t);
+  cudaError_t e = halloc(h, &g->d_mem, tb + lb + n_states);
   if (e != cudaSuccess) {
     cudaGetLastError();
     delete g;
     return fail(h, TOK_ENOMEM, "grammar: allocation failed");
   }
   e = cudaMemcpy(g->d_mem, t.data(), tb, cudaMemcpyHostToDevice);
-  if (e == cudaSuccess) e = cudaMemcpy(g->d_mem + tb, accept, n_states, cudaMemcpyHostToDevice);
+  if (e == cudaSuccess) e = cudaMemcpy(g->d_mem + tb, leaves.data(), lb, cudaMemcpyHostToDevice);
+  if (e == cudaSuccess) e = cudaMemcpy(g->d_mem + tb + lb, accept, n_states, cudaMemcpyHostToDevice);
   if (e != cudaSuccess) {
     cudaFree(g->d_mem);
     delete g;
     return cuda_fail(h, e, "grammar: copy");
   }
   g->h = h;
-  g->g = DevGrammar{reinterpret_cast<const uint16_t*>(g->d_mem), g->d_mem + tb, n_states};
+  g->g = DevGrammar{reinterpret_cast<const uint16_t*>(g->d_mem), reinterpret_cast<const uint32_t*>(g->d_mem + tb),
+                    g->d_mem + tb + lb, n_states};
   *out = g;
   return TOK_OK;
 } catch (...) {
@@ -336,8 +407,8 @@ int tok_grammar_mask(tok_handle* h, const tok_grammar* g, const int32_t* d_state
     c.item_off = nullptr;
     c.state_out = nullptr;
   }
-  const uint32_t ranks = mask_ranks(h, n), groups = (h->tokens.n_groups + ranks - 1) / ranks;
-  const size_t smem = (((size_t)(n_logits + 31) / 32 + 3) / 4 * 4 + groups) * sizeof(uint32_t);
+  const uint32_t ranks = mask_ranks(h, n, n_logits);
+  const size_t smem = mask_bytes(h, n_logits, ranks);
   const cudaError_t e = launch_clusters<k_grammar_mask>(h->dev, n * ranks, GR_THREADS, ranks, smem, st, g->g, h->tokens, c);
   h->launches += 1;
   if (e != cudaSuccess) {

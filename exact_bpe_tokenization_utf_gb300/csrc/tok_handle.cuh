@@ -18,10 +18,12 @@ namespace tokgb {
 // and, for walking many tokens at once, the tokens sorted by their bytes in
 // groups of up to 32 that begin alike.  Group g: its first `prefix` bytes (at
 // most 8) are in head; lane i's token is id[32 g + i] (NO_TOKEN: none) with
-// rest[32 g + i] bytes more, four per word, words[at + 32 w + i].
+// rest[32 g + i] bytes more, four per word, words[at + 32 w + i].  kinds has a
+// bit for each kind of byte (byte_kind) among these, group_kinds for the
+// whole group.
 struct TokenGroup {
   unsigned long long head;  // the first byte lowest
-  uint32_t shape;           // prefix | words per token << 4
+  uint32_t prefix;
   uint32_t at;
 };
 
@@ -33,8 +35,44 @@ struct DevTokens {
   const TokenGroup* group;
   const uint32_t* words;
   const uint32_t* id;
+  const uint32_t* kinds;
+  const uint32_t* group_kinds;
   const uint16_t* rest;
 };
+
+// 32 kinds of bytes, such that what a grammar treats apart is often of different kinds
+inline uint32_t byte_kind(uint8_t b) {
+  if (b >= 0xf0) return 31;
+  if (b >= 0xe0) return 30;
+  if (b >= 0xc0) return 29;
+  if (b >= 0x80) return 28;
+  if (b == 0x7f) return 27;
+  if (b >= '0' && b <= '9') return b == '0' ? 8 : 9;
+  if (b >= 'a' && b <= 'z') return b <= 'f' ? 10 : 11;
+  if (b >= 'A' && b <= 'Z') return b <= 'F' ? 12 : 13;
+  switch (b) {
+    case '\t': return 1;
+    case '\n': return 2;
+    case '\r': return 3;
+    case ' ': return 4;
+    case '"': return 5;
+    case '\\': return 6;
+    case '\'': return 7;
+    case '_': return 14;
+    case '-': return 15;
+    case '.': return 16;
+    case ',': return 17;
+    case ':': return 18;
+    case ';': return 19;
+    case '/': return 20;
+    case '(': case ')': return 21;
+    case '[': case ']': return 22;
+    case '{': case '}': return 23;
+    case '<': case '=': case '>': return 24;
+    case '@': case '#': case '$': case '`': case '?': return 26;
+  }
+  return b < 0x20 ? 0 : 25;
+}
 
 }  // namespace tokgb
 

@@ -133,7 +133,24 @@ __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_assign(PagedCall c) {
       slot[j] = -1;
       pos[j] = req[j] = -1;
     }
+    // a request that covers the whole tile, as in a prefill: nothing to find
+    bool alone = false;
+    Req r{};
+    int of = -1;  // r is this request's
     if (code == ST_OK && t0 < n_tok) {
+      r = load_req(a, kf);
+      of = (int)kf;
+      alone = r.off <= t0 && r.end >= t0 + tile;
+    }
+    int m[PER], w[PER], em = -1, ew = 0;
+    long long next_carry = carry;
+    if (alone) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        m[j] = of;
+        w[j] = 0;
+      }
+    } else if (code == ST_OK && t0 < n_tok) {
       // the requests with tokens in the tile mark their first one there, and
       // add their blocks at the first token after them
 #pragma unroll
@@ -147,17 +164,17 @@ __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_assign(PagedCall c) {
       for (uint32_t k0 = kf; k0 < a.n && a.d_item_off[k0] < t1; k0 += nt) {
         const uint32_t k = k0 + tid;
         if (k < a.n) {
-          const Req r = load_req(a, k);
-          if (r.off < r.end && r.off < t1 && r.end > t0) {
-            s_req[r.off > t0 ? (int)(r.off - t0) : 0] = (int)k;
-            if (r.end <= t1) s_add[(int)(r.end - t0)] = r.extra;
-            if (r.end >= t1) s_last = k;  // (one request covers the tile's last token)
+          const Req x = load_req(a, k);
+          if (x.off < x.end && x.off < t1 && x.end > t0) {
+            s_req[x.off > t0 ? (int)(x.off - t0) : 0] = (int)k;
+            if (x.end <= t1) s_add[(int)(x.end - t0)] = x.extra;
+            if (x.end >= t1) s_last = k;  // (one request covers the tile's last token)
           }
         }
       }
       __syncthreads();
       // each token's request (a running maximum) and base (a running sum)
-      int m[PER], w[PER], mm = -1, ww = 0;
+      int mm = -1, ww = 0;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         mm = max(mm, s_req[tid * PER + j]);
@@ -178,20 +195,25 @@ __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_assign(PagedCall c) {
         s_m[warp] = im;
         s_w[warp] = iw;
       }
-      int em = __shfl_up_sync(0xffffffffu, im, 1), ew = iw - ww;
+      em = __shfl_up_sync(0xffffffffu, im, 1);
+      ew = iw - ww;
       if (lane == 0) em = -1;
       __syncthreads();
-      int tot = 0;
-      for (int q = 0; q < nt / 32; ++q) {
-        const int x = s_m[q], y = s_w[q];
-        if (q < warp) {
-          em = max(em, x);
-          ew += y;
-        }
-        tot += y;
+      // the warps before this one, and all
+      const bool in = lane < nt / 32, before = lane < warp;
+      int am = before ? s_m[lane] : -1, aw = before ? s_w[lane] : 0, tot = in ? s_w[lane] : 0;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+        aw += __shfl_xor_sync(0xffffffffu, aw, o);
+        tot += __shfl_xor_sync(0xffffffffu, tot, o);
       }
-      Req r{};
-      int of = -1;  // r is this request's
+      em = max(em, am);
+      ew += aw;
+      next_carry = carry + tot + s_add[tile];
+      if (t1 < n_tok) kf = s_last;
+    }
+    if (code == ST_OK && t0 < n_tok) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const long long t = mine + j;
@@ -211,9 +233,9 @@ __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_assign(PagedCall c) {
           slot[j] = (long long)blk * bs + in;
         }
       }
-      carry += tot + s_add[tile];
-      if (t1 < n_tok) kf = s_last;
-      __syncthreads();
+      if (alone && r.end == t0 + tile) next_carry += r.extra;
+      carry = next_carry;
+      if (!alone) __syncthreads();
     }
     if (PER == 4 && c.wide && mine + PER <= t_end) {
       longlong2* q = reinterpret_cast<longlong2*>(a.d_slot + mine);
@@ -271,16 +293,16 @@ __device__ __forceinline__ long long release_count(const ReleaseCall& c, uint32_
     *bad = true;
     return 0;
   }
+  if (len < 0x7fffffffll - c.block_size) return ((uint32_t)len + c.block_size - 1u) / c.block_size;
   return (len + c.block_size - 1) / c.block_size;
 }
 
 // One CTA takes a range of requests; as in k_paged_assign each CTA reads all
-// of them once for its base and for the checks.  A warp copies a request's
-// blocks.
+// of them once for its base and for the checks.
 __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_release(ReleaseCall c) {
-  __shared__ long long sh[64], s_base[PG_THREADS], s_scan[32];
+  __shared__ long long sh[64], s_cnt[PG_THREADS];
   __shared__ unsigned s_bad, s_last;
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, nt = blockDim.x;
   const long long n_free = *c.n_free;
   const uint32_t k_begin = min(blockIdx.x * c.per, c.n), k_end = min(k_begin + c.per, c.n);
   if (tid == 0) s_bad = 0xffffffffu;
@@ -299,22 +321,19 @@ __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_release(ReleaseCall c) 
   if (s_bad != 0xffffffffu || n_free < 0) code = TOK_EINVAL;
   else if ((unsigned long long)(n_free + total) > c.free_cap) code = TOK_EBUF;
   if (code == ST_OK) {
+    long long base = n_free + carry;
     for (uint32_t k0 = k_begin; k0 < k_end; k0 += nt) {
-      const uint32_t k = k0 + tid;
       bool bad = false;
-      const long long m = k < k_end ? release_count(c, k, &bad) : 0;
-      long long sum;
-      s_base[tid] = n_free + carry + block_excl_sum(m, &sum, s_scan);
       __syncthreads();
-      for (uint32_t i = warp; i < (uint32_t)nt && k0 + i < k_end; i += nt / 32) {
-        const long long cnt = release_count(c, k0 + i, &bad);
+      s_cnt[tid] = k0 + tid < k_end ? release_count(c, k0 + tid, &bad) : 0;
+      __syncthreads();
+      for (uint32_t i = 0; i < (uint32_t)nt && k0 + i < k_end; ++i) {
+        const long long cnt = s_cnt[i];
         const int32_t* row = c.table + (long long)(k0 + i) * c.stride;
-        int32_t* to = c.free_stack + s_base[i];
 #pragma unroll 4
-        for (long long j = lane; j < cnt; j += 32) to[j] = row[j];
+        for (long long j = tid; j < cnt; j += nt) c.free_stack[base + j] = row[j];
+        base += cnt;
       }
-      carry += sum;
-      __syncthreads();
     }
   }
   if (!completes(c.done, &s_last)) return;
