@@ -11,6 +11,7 @@
 #include <new>
 
 #include "tok_handle.cuh"
+#include "tok_scan.cuh"
 
 namespace tokgb {
 namespace {
@@ -93,10 +94,10 @@ struct Item {
 // the state need no walk: inside a string that is most tokens, often a whole
 // group.  The others are walked (sorted tokens read neighbouring bytes from equal
 // states), two groups at a time with the next two on their way.  Allowed tokens
-// set their bits in the CTA's shared memory; the cluster's CTAs then join
-// their bits, a share of the row each, and write it.  Rows (of GR_THREADS at
-// a time) in equal states are walked once, by the first one's cluster, which
-// writes all of them.
+// set their bits in the CTA's shared memory, which then sends the words that
+// are not empty to the CTAs that write them, a share of the row each.  Rows (of
+// GR_THREADS at a time) in equal states are walked once, by the first one's
+// cluster, which writes all of them.
 __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTokens v, MaskCall c) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint32_t s_mem[];
@@ -107,14 +108,15 @@ __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTo
   const uint32_t n_words = (c.n_logits + 31) / 32;
   uint32_t* bits = s_mem;                               // a row's
   uint2* live = reinterpret_cast<uint2*>(s_mem + ((n_words + 3) / 4) * 4);  // group | state << 16, words' place | WHOLE
-  const uint32_t per = (v.n_groups + n_ranks - 1) / n_ranks;
-  const uint32_t g0 = min(rank * per, v.n_groups), g1 = min(g0 + per, v.n_groups);
+  // the cluster's CTAs take 32 groups in turn: long tokens lie together
+  auto group_of = [&](uint32_t i) { return (i / 32 * n_ranks + rank) * 32 + i % 32; };
+  const uint32_t n_mine = ((v.n_groups + 31) / 32 + n_ranks - 1) / n_ranks * 32;
   // this thread's first group, on its way while the states are walked
   uint4 r = make_uint4(0, 0, 0, 0);
   uint32_t kinds = 0;
-  if (g0 + tid < g1) {
-    r = __ldg(reinterpret_cast<const uint4*>(v.group + g0 + tid));
-    kinds = __ldg(v.group_kinds + g0 + tid);
+  if (tid < n_mine && group_of(tid) < v.n_groups) {
+    r = __ldg(reinterpret_cast<const uint4*>(v.group + group_of(tid)));
+    kinds = __ldg(v.group_kinds + group_of(tid));
   }
 
   // the states of this row's window, and the rows among them that equal it
@@ -133,16 +135,17 @@ __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTo
   const uint32_t mine = __ballot_sync(0xffffffffu, same);
   if (lane == 0) s_row[warp] = mine;
   if (__syncthreads_or(same && j < k)) return;  // (in every CTA of the cluster alike)
+  cluster_arrive();  // (waited for before another CTA's bits are set)
 
   if (s0 != DEAD) {
-    for (uint32_t base = g0; base < g1; base += GR_THREADS) {
-      const uint32_t q = base + tid;
-      if (base != g0 && q < g1) {
+    for (uint32_t base = 0; base < n_mine; base += GR_THREADS) {
+      const uint32_t q = base + tid < n_mine ? group_of(base + tid) : v.n_groups;
+      if (base && q < v.n_groups) {
         r = __ldg(reinterpret_cast<const uint4*>(v.group + q));
         kinds = __ldg(v.group_kinds + q);
       }
       unsigned long long head = (unsigned long long)r.y << 32 | r.x;
-      uint32_t s = q < g1 ? s0 : DEAD;
+      uint32_t s = q < v.n_groups ? s0 : DEAD;
       for (uint32_t i = r.z; i && s != DEAD; --i) {
         s = __ldg(g.next + s * 256u + (uint32_t)(head & 255u));
         head >>= 8;
@@ -165,11 +168,11 @@ __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTo
         const uint32_t at = (e.x & 0xffffu) * 32 + lane;
         t.id = load_once(v.id + at);
         t.s = e.x >> 16;
-        if (!(e.y & WHOLE)) {
-          const uint32_t leaves = __ldg(g.leaves + t.s);
-          t.rest = load_once(v.kinds + at) & leaves ? load_once(v.rest + at) : 0u;
+        if (!(e.y & WHOLE)) {  // (every group has a first word, so that these loads need not wait for one another)
           t.at = e.y + lane;
-          t.word = t.rest ? load_once(v.words + t.at) : 0u;
+          t.word = load_once(v.words + t.at);
+          t.rest = load_once(v.rest + at);
+          if (!(load_once(v.kinds + at) & __ldg(g.leaves + t.s))) t.rest = 0;
         }
       }
       return t;
@@ -200,14 +203,16 @@ __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTo
       }
     }
   }
-  if (n_ranks > 1) cluster.sync();
-  else __syncthreads();
-  const uint32_t share = (n_words + n_ranks - 1) / n_ranks, b0 = min(rank * share, n_words), b1 = min(b0 + share, n_words);
-  for (uint32_t w = b0 + tid; w < b1; w += GR_THREADS) {
-    uint32_t m = 0;
-    if (n_ranks == 1) m = bits[w];
-    else
-      for (uint32_t q = 0; q < n_ranks; ++q) m |= cluster.map_shared_rank(bits, q)[w];
+  const uint32_t share = (n_words + n_ranks - 1) / n_ranks;
+  __syncthreads();
+  cluster_wait();
+  if (s0 != DEAD && s_live)
+    for (uint32_t w = tid; w < n_words; w += GR_THREADS)
+      if (bits[w] && w / share != rank) atomicOr(cluster.map_shared_rank(bits, w / share) + w, bits[w]);
+  cluster.sync();
+  const uint32_t b1 = min((rank + 1) * share, n_words);
+  for (uint32_t w = rank * share + tid; w < b1; w += GR_THREADS) {
+    uint32_t m = bits[w];
     if (c.eos >= 0 && (uint32_t)c.eos < c.n_logits && (uint32_t)c.eos / 32 == w) {
       m &= ~(1u << (c.eos & 31));
       if (s0 != DEAD && g.accept[s0]) m |= 1u << (c.eos & 31);
@@ -216,12 +221,11 @@ __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTo
       for (uint32_t x = s_row[i]; x; x &= x - 1)
         c.mask[(long long)(w0 + i * 32 + (uint32_t)__ffs((int)x) - 1u) * c.mask_stride + w] = m;
   }
-  if (n_ranks > 1) cluster.sync();  // (until the others have read this CTA's bits)
 }
 
 // bytes of shared memory of a CTA: a row's bits, and its groups' list
 size_t mask_bytes(const tok_handle* h, uint32_t n_logits, uint32_t ranks) {
-  return ((size_t)(n_logits + 31) / 32 + 3) / 4 * 16 + (size_t)(h->tokens.n_groups + ranks - 1) / ranks * sizeof(uint2);
+  return ((size_t)(n_logits + 31) / 32 + 3) / 4 * 16 + (size_t)((h->tokens.n_groups + 31) / 32 + ranks - 1) / ranks * 32 * sizeof(uint2);
 }
 
 // CTAs of a row's cluster: 16 while few rows leave SMs without work, 4 where
@@ -261,7 +265,7 @@ int ensure_tokens(tok_handle* h) {
     uint32_t most = 0;
     for (uint32_t j = 0; j < p; ++j) r.head |= (unsigned long long)at(a)[j] << (8 * j);
     for (uint32_t q = 0; q < m; ++q) most = std::max(most, len(order[i + q]) - p);
-    const uint32_t nw = (most + 3) / 4;
+    const uint32_t nw = std::max(1u, (most + 3) / 4);
     uint32_t all = 0;
     r.prefix = p;
     words.resize(words.size() + (size_t)nw * 32, 0u);

@@ -592,10 +592,6 @@ template <class T> struct Slice {
   }
 };
 
-// the two halves of a cluster's barrier
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
 struct LogitsCall {
   tok_logits_args a;
   Shape shape;

@@ -1,4 +1,4 @@
-// Block-wide sums shared by the kernels that turn lengths into places.
+// Block-wide sums, and the halves of a cluster's barrier.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -27,5 +27,9 @@ __device__ __forceinline__ T block_excl_sum(T v, T* total, T* sh) {
   __syncthreads();
   return pre + inc - v;
 }
+
+// the two halves of a cluster's barrier
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 }  // namespace tokgb
