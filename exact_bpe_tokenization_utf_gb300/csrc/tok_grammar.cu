@@ -88,151 +88,211 @@ struct Item {
   uint32_t s, id, rest, at, word;
 };
 
-// One cluster per row.  A thread walks a group's common first bytes, so that
-// one step decides over up to 32 tokens; where the state survives, a warp
-// takes the group's tokens, one per lane.  Bytes of kinds that do not change
-// the state need no walk: inside a string that is most tokens, often a whole
-// group.  The others are walked (sorted tokens read neighbouring bytes from equal
-// states), two groups at a time with the next two on their way.  Allowed tokens
-// set their bits in the CTA's shared memory, which then sends the words that
-// are not empty to the CTAs that write them, a share of the row each.  Rows (of
-// GR_THREADS at a time) in equal states are walked once, by the first one's
-// cluster, which writes all of them.
+// A row's window of GR_THREADS rows: its state, and the rows in equal states.
+// Each thread looks at one row.  sh holds GR_THREADS / 32 + 1 words.
+struct Window {
+  uint32_t state;
+  bool first;            // no earlier row of the window is in this state
+  const uint32_t* same;  // bits of the rows that are
+  uint32_t begin;
+};
+
+__device__ __forceinline__ Window look_around(const DevGrammar& g, const DevTokens& v, const MaskCall& c, uint32_t k, uint32_t* sh) {
+  Window w;
+  w.begin = k / GR_THREADS * GR_THREADS;
+  const uint32_t j = w.begin + threadIdx.x;
+  uint32_t sj = DEAD;
+  if (j < c.n) sj = row_state(g, v, c, j);
+  if (j == k) sh[GR_THREADS / 32] = sj;
+  __syncthreads();
+  w.state = sh[GR_THREADS / 32];
+  const bool same = j < c.n && sj == w.state;
+  const uint32_t b = __ballot_sync(0xffffffffu, same);
+  if ((threadIdx.x & 31u) == 0) sh[threadIdx.x >> 5] = b;
+  w.first = !__syncthreads_or(same && j < k);
+  w.same = sh;
+  return w;
+}
+
+// f(row's mask) for each row of a window that is in its state
+template <class F>
+__device__ __forceinline__ void each_same(const Window& win, const MaskCall& c, F f) {
+  for (uint32_t i = 0; i < GR_THREADS / 32; ++i)
+    for (uint32_t x = win.same[i]; x; x &= x - 1)
+      f(c.mask + (long long)(win.begin + i * 32 + (uint32_t)__ffs((int)x) - 1u) * c.mask_stride);
+}
+
+// A CTA's groups: 32 in turn with the others of its row (long tokens lie together).
+struct Share {
+  uint32_t rank, n_ranks;
+  __device__ __forceinline__ uint32_t group(uint32_t i) const { return (i / 32 * n_ranks + rank) * 32 + i % 32; }
+  __device__ __forceinline__ uint32_t count(const DevTokens& v) const { return ((v.n_groups + 31) / 32 + n_ranks - 1) / n_ranks * 32; }
+};
+
+// a thread's first group, on its way while the states are looked at
+struct First {
+  uint4 r;
+  uint32_t kinds;
+};
+__device__ __forceinline__ First first_group(const DevTokens& v, const Share& sh) {
+  First f{make_uint4(0, 0, 0, 0), 0};
+  if (threadIdx.x < sh.count(v) && sh.group(threadIdx.x) < v.n_groups) {
+    f.r = __ldg(reinterpret_cast<const uint4*>(v.group + sh.group(threadIdx.x)));
+    f.kinds = __ldg(v.group_kinds + sh.group(threadIdx.x));
+  }
+  return f;
+}
+
+// A thread walks a group's common first bytes, so that one step decides over up
+// to 32 tokens; the groups that survive are listed (the first `room` of them):
+// group | state << 16, place of its words | WHOLE.  n_live (0 before, behind a
+// barrier) receives their number.  Ends with a barrier.
+__device__ __forceinline__ void find_live(const DevGrammar& g, const DevTokens& v, const Share& sh, First f, uint32_t s0, uint2* live,
+                                          uint32_t room, uint32_t* n_live) {
+  const uint32_t tid = threadIdx.x, lane = tid & 31u, n = sh.count(v);
+  for (uint32_t base = 0; base < n; base += GR_THREADS) {
+    const uint32_t q = base + tid < n ? sh.group(base + tid) : v.n_groups;
+    unsigned long long head = (unsigned long long)f.r.y << 32 | f.r.x;
+    uint32_t s = q < v.n_groups ? s0 : DEAD;
+    const uint32_t kinds = f.kinds, words = f.r.w;
+    uint32_t i = f.r.z;
+    if (base + GR_THREADS + tid < n) {  // the next one
+      const uint32_t next = sh.group(base + GR_THREADS + tid);
+      if (next < v.n_groups) {
+        f.r = __ldg(reinterpret_cast<const uint4*>(v.group + next));
+        f.kinds = __ldg(v.group_kinds + next);
+      }
+    }
+    for (; i && s != DEAD; --i) {
+      s = __ldg(g.next + s * 256u + (uint32_t)(head & 255u));
+      head >>= 8;
+    }
+    const uint32_t alive = __ballot_sync(0xffffffffu, s != DEAD);
+    uint32_t at = 0;
+    if (lane == 0 && alive) at = atomicAdd(n_live, (uint32_t)__popc(alive));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(alive & ((1u << lane) - 1u));
+    if (s != DEAD && at < room) {
+      const uint32_t whole = (kinds & __ldg(g.leaves + s)) == 0 ? WHOLE : 0u;
+      live[at] = make_uint2(q | s << 16, words | whole);
+    }
+  }
+  __syncthreads();
+}
+
+// A warp takes a listed group's tokens, one per lane.  Bytes of kinds that do not
+// change the state need no walk: inside a string that is most tokens, often
+// a whole group.  The others are walked (sorted tokens read neighbouring bytes
+// from equal states), two groups at a time with the next two on their way.
+// Allowed tokens set their bits.
+__device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& v, const uint2* live, uint32_t n_live, uint32_t n_logits,
+                                          uint32_t* bits) {
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  auto load = [&](uint32_t f) {
+    Item t{DEAD, NO_TOKEN, 0, 0, 0};
+    if (f < n_live) {
+      const uint2 e = live[f];
+      const uint32_t at = (e.x & 0xffffu) * 32 + lane;
+      t.id = load_once(v.id + at);
+      t.s = e.x >> 16;
+      if (!(e.y & WHOLE)) {  // (every group has a first word, so that these loads need not wait for one another)
+        t.at = e.y + lane;
+        t.word = load_once(v.words + t.at);
+        t.rest = load_once(v.rest + at);
+        if (!(load_once(v.kinds + at) & __ldg(g.leaves + t.s))) t.rest = 0;
+      }
+    }
+    return t;
+  };
+  constexpr uint32_t W = GR_THREADS / 32;
+  Item now[2] = {load(warp), load(warp + W)};
+  for (uint32_t e = warp; e < n_live; e += 2 * W) {
+    const Item next[2] = {load(e + 2 * W), load(e + 3 * W)};
+    for (uint32_t w = 0; __any_sync(0xffffffffu, (now[0].rest > w && now[0].s != DEAD) || (now[1].rest > w && now[1].s != DEAD));
+         w += 4) {
+      uint32_t ahead[2];  // the tokens' next words
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        ahead[h] = now[h].rest > w + 4 && now[h].s != DEAD ? load_once(v.words + now[h].at + 8 * (w + 4)) : 0u;
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (w + i < now[h].rest && now[h].s != DEAD) now[h].s = __ldg(g.next + now[h].s * 256u + (now[h].word >> (8 * i) & 255u));
+      }
+      now[0].word = ahead[0];
+      now[1].word = ahead[1];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (now[h].s != DEAD && now[h].id < n_logits) atomicOr(&bits[now[h].id >> 5], 1u << (now[h].id & 31));
+      now[h] = next[h];
+    }
+  }
+}
+
+// word w of a mask with the end token's bit as the state has it (the token's own bytes do not count)
+__device__ __forceinline__ uint32_t with_eos(const DevGrammar& g, const MaskCall& c, uint32_t s, uint32_t w, uint32_t m) {
+  if (c.eos >= 0 && (uint32_t)c.eos < c.n_logits && (uint32_t)c.eos / 32 == w) {
+    m &= ~(1u << (c.eos & 31));
+    if (s != DEAD && g.accept[s]) m |= 1u << (c.eos & 31);
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint2* list_behind(uint32_t* bits, uint32_t n_words) {
+  return reinterpret_cast<uint2*>(bits + (n_words + 3) / 4 * 4);
+}
+
+// A cluster for each row.  The CTAs share the groups; then each sends its
+// words that are not empty to the CTAs that write them, a share of the row
+// each.  Rows in equal states are walked once, by the first one's cluster,
+// which writes all of them.
 __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTokens v, MaskCall c) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint32_t s_mem[];
-  __shared__ uint32_t s_live, s_row[GR_THREADS / 32], s_state;
+  __shared__ uint32_t s_live, s_row[GR_THREADS / 32 + 1];
   const cg::cluster_group cluster = cg::this_cluster();
-  const uint32_t rank = cluster.block_rank(), n_ranks = cluster.num_blocks(), k = blockIdx.x / n_ranks;
-  const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+  const uint32_t rank = cluster.block_rank(), n_ranks = cluster.num_blocks(), k = blockIdx.x / n_ranks, tid = threadIdx.x;
   const uint32_t n_words = (c.n_logits + 31) / 32;
-  uint32_t* bits = s_mem;                               // a row's
-  uint2* live = reinterpret_cast<uint2*>(s_mem + ((n_words + 3) / 4) * 4);  // group | state << 16, words' place | WHOLE
-  // the cluster's CTAs take 32 groups in turn: long tokens lie together
-  auto group_of = [&](uint32_t i) { return (i / 32 * n_ranks + rank) * 32 + i % 32; };
-  const uint32_t n_mine = ((v.n_groups + 31) / 32 + n_ranks - 1) / n_ranks * 32;
-  // this thread's first group, on its way while the states are walked
-  uint4 r = make_uint4(0, 0, 0, 0);
-  uint32_t kinds = 0;
-  if (tid < n_mine && group_of(tid) < v.n_groups) {
-    r = __ldg(reinterpret_cast<const uint4*>(v.group + group_of(tid)));
-    kinds = __ldg(v.group_kinds + group_of(tid));
-  }
-
-  // the states of this row's window, and the rows among them that equal it
-  const uint32_t w0 = k / GR_THREADS * GR_THREADS, j = w0 + tid;
-  uint32_t sj = DEAD;
-  if (j < c.n) sj = row_state(g, v, c, j);
-  if (j == k) {
-    s_state = sj;
-    s_live = 0;
-    if (rank == 0 && c.state_out) c.state_out[k] = sj == DEAD ? -1 : (int32_t)sj;
-  }
+  uint32_t* bits = s_mem;
+  uint2* live = list_behind(bits, n_words);
+  const Share share{rank, n_ranks};
+  const First f = first_group(v, share);
   for (uint32_t w = tid; w < n_words; w += GR_THREADS) bits[w] = 0;
-  __syncthreads();
-  const uint32_t s0 = s_state;
-  const bool same = j < c.n && sj == s0;
-  const uint32_t mine = __ballot_sync(0xffffffffu, same);
-  if (lane == 0) s_row[warp] = mine;
-  if (__syncthreads_or(same && j < k)) return;  // (in every CTA of the cluster alike)
-  cluster_arrive();  // (waited for before another CTA's bits are set)
-
-  if (s0 != DEAD) {
-    for (uint32_t base = 0; base < n_mine; base += GR_THREADS) {
-      const uint32_t q = base + tid < n_mine ? group_of(base + tid) : v.n_groups;
-      if (base && q < v.n_groups) {
-        r = __ldg(reinterpret_cast<const uint4*>(v.group + q));
-        kinds = __ldg(v.group_kinds + q);
-      }
-      unsigned long long head = (unsigned long long)r.y << 32 | r.x;
-      uint32_t s = q < v.n_groups ? s0 : DEAD;
-      for (uint32_t i = r.z; i && s != DEAD; --i) {
-        s = __ldg(g.next + s * 256u + (uint32_t)(head & 255u));
-        head >>= 8;
-      }
-      const uint32_t alive = __ballot_sync(0xffffffffu, s != DEAD);
-      uint32_t at = 0;
-      if (lane == 0 && alive) at = atomicAdd(&s_live, (uint32_t)__popc(alive));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(alive & ((1u << lane) - 1u));
-      if (s != DEAD) {
-        const uint32_t whole = (kinds & __ldg(g.leaves + s)) == 0 ? WHOLE : 0u;
-        live[at] = make_uint2(q | s << 16, r.w | whole);
-      }
-    }
-    __syncthreads();
-    const uint32_t n_live = s_live;
-    auto load = [&](uint32_t f) {
-      Item t{DEAD, NO_TOKEN, 0, 0, 0};
-      if (f < n_live) {
-        const uint2 e = live[f];
-        const uint32_t at = (e.x & 0xffffu) * 32 + lane;
-        t.id = load_once(v.id + at);
-        t.s = e.x >> 16;
-        if (!(e.y & WHOLE)) {  // (every group has a first word, so that these loads need not wait for one another)
-          t.at = e.y + lane;
-          t.word = load_once(v.words + t.at);
-          t.rest = load_once(v.rest + at);
-          if (!(load_once(v.kinds + at) & __ldg(g.leaves + t.s))) t.rest = 0;
-        }
-      }
-      return t;
-    };
-    constexpr uint32_t W = GR_THREADS / 32;
-    Item now[2] = {load(warp), load(warp + W)};
-    for (uint32_t e = warp; e < n_live; e += 2 * W) {
-      const Item next[2] = {load(e + 2 * W), load(e + 3 * W)};
-      for (uint32_t w = 0; __any_sync(0xffffffffu, (now[0].rest > w && now[0].s != DEAD) || (now[1].rest > w && now[1].s != DEAD));
-           w += 4) {
-        if (w) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (now[h].rest > w && now[h].s != DEAD) now[h].word = load_once(v.words + now[h].at + 8 * w);
-        }
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (w + i < now[h].rest && now[h].s != DEAD)
-              now[h].s = __ldg(g.next + now[h].s * 256u + (now[h].word >> (8 * i) & 255u));
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (now[h].s != DEAD && now[h].id < c.n_logits) atomicOr(&bits[now[h].id >> 5], 1u << (now[h].id & 31));
-        now[h] = next[h];
-      }
-    }
+  if (tid == 0) s_live = 0;
+  const Window win = look_around(g, v, c, k, s_row);
+  if (tid == 0 && rank == 0 && c.state_out) c.state_out[k] = win.state == DEAD ? -1 : (int32_t)win.state;
+  if (!win.first) return;  // (in every CTA of the cluster alike)
+  cluster_arrive();        // (waited for before another CTA's bits are set)
+  if (win.state != DEAD) {
+    find_live(g, v, share, f, win.state, live, share.count(v), &s_live);
+    walk_live(g, v, live, s_live, c.n_logits, bits);
   }
-  const uint32_t share = (n_words + n_ranks - 1) / n_ranks;
+  const uint32_t each = (n_words + n_ranks - 1) / n_ranks;
   __syncthreads();
   cluster_wait();
-  if (s0 != DEAD && s_live)
+  if (s_live)
     for (uint32_t w = tid; w < n_words; w += GR_THREADS)
-      if (bits[w] && w / share != rank) atomicOr(cluster.map_shared_rank(bits, w / share) + w, bits[w]);
+      if (bits[w] && w / each != rank) atomicOr(cluster.map_shared_rank(bits, w / each) + w, bits[w]);
   cluster.sync();
-  const uint32_t b1 = min((rank + 1) * share, n_words);
-  for (uint32_t w = rank * share + tid; w < b1; w += GR_THREADS) {
-    uint32_t m = bits[w];
-    if (c.eos >= 0 && (uint32_t)c.eos < c.n_logits && (uint32_t)c.eos / 32 == w) {
-      m &= ~(1u << (c.eos & 31));
-      if (s0 != DEAD && g.accept[s0]) m |= 1u << (c.eos & 31);
-    }
-    for (uint32_t i = 0; i < GR_THREADS / 32; ++i)
-      for (uint32_t x = s_row[i]; x; x &= x - 1)
-        c.mask[(long long)(w0 + i * 32 + (uint32_t)__ffs((int)x) - 1u) * c.mask_stride + w] = m;
+  const uint32_t w1 = min((rank + 1) * each, n_words);
+  for (uint32_t w = rank * each + tid; w < w1; w += GR_THREADS) {
+    const uint32_t m = with_eos(g, c, win.state, w, bits[w]);
+    each_same(win, c, [&](uint32_t* row) { row[w] = m; });
   }
 }
 
-// bytes of shared memory of a CTA: a row's bits, and its groups' list
-size_t mask_bytes(const tok_handle* h, uint32_t n_logits, uint32_t ranks) {
-  return ((size_t)(n_logits + 31) / 32 + 3) / 4 * 16 + (size_t)((h->tokens.n_groups + 31) / 32 + ranks - 1) / ranks * 32 * sizeof(uint2);
+// bytes of shared memory of a CTA: a row's bits, and a list of groups
+size_t mask_bytes(uint32_t n_logits, uint32_t groups) {
+  return ((size_t)(n_logits + 31) / 32 + 3) / 4 * 16 + groups * sizeof(uint2);
 }
+uint32_t share_of(const tok_handle* h, uint32_t ranks) { return ((h->tokens.n_groups + 31) / 32 + ranks - 1) / ranks * 32; }
 
-// CTAs of a row's cluster: 16 while few rows leave SMs without work, 4 where
-// there are enough of them (their groups then keep a CTA's warps busy).
+// CTAs of a row's cluster: as many as leave no SM without work, at least 4
 uint32_t mask_ranks(const tok_handle* h, uint32_t n, uint32_t n_logits) {
   uint32_t s = 16;
-  while (s > 4 && (unsigned long long)n * s > 4ull * (unsigned)h->n_sms && mask_bytes(h, n_logits, s / 2) <= MOST_SHARED) s /= 2;
+  while (s > 4 && (unsigned long long)n * s > 4ull * (unsigned)h->n_sms && mask_bytes(n_logits, share_of(h, s / 2)) <= MOST_SHARED)
+    s /= 2;
   return s;
 }
 
@@ -291,19 +351,19 @@ int ensure_tokens(tok_handle* h) {
   std::vector<uint32_t> off(n + 1);
   for (uint32_t t = 0; t <= n; ++t) off[t] = (uint32_t)h->vocab_off[t];
   // one allocation; the parts by falling alignment
-  constexpr int PARTS = 8;
-  const void* part[PARTS] = {group.data(), words.data(), id.data(), kinds.data(), group_kinds.data(), off.data(), rest.data(), bytes};
-  const size_t size[PARTS] = {group.size() * sizeof(TokenGroup), words.size() * 4, id.size() * 4, kinds.size() * 4,
+  constexpr int N_PARTS = 8;
+  const void* part[N_PARTS] = {group.data(), words.data(), id.data(), kinds.data(), group_kinds.data(), off.data(), rest.data(), bytes};
+  const size_t size[N_PARTS] = {group.size() * sizeof(TokenGroup), words.size() * 4, id.size() * 4, kinds.size() * 4,
                               group_kinds.size() * 4, off.size() * 4, rest.size() * 2, nb};
-  size_t place[PARTS + 1] = {0};
-  for (int i = 0; i < PARTS; ++i) place[i + 1] = place[i] + (size[i] + 15) / 16 * 16;
+  size_t place[N_PARTS + 1] = {0};
+  for (int i = 0; i < N_PARTS; ++i) place[i + 1] = place[i] + (size[i] + 15) / 16 * 16;
   uint8_t* p = nullptr;
-  cudaError_t e = halloc(h, &p, place[PARTS]);
+  cudaError_t e = halloc(h, &p, place[N_PARTS]);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return fail(h, TOK_ENOMEM, "grammar: allocation failed");
   }
-  for (int i = 0; i < PARTS && e == cudaSuccess; ++i)
+  for (int i = 0; i < N_PARTS && e == cudaSuccess; ++i)
     if (size[i]) e = cudaMemcpy(p + place[i], part[i], size[i], cudaMemcpyHostToDevice);
   if (e != cudaSuccess) {
     cudaFree(p);
@@ -412,8 +472,8 @@ int tok_grammar_mask(tok_handle* h, const tok_grammar* g, const int32_t* d_state
     c.state_out = nullptr;
   }
   const uint32_t ranks = mask_ranks(h, n, n_logits);
-  const size_t smem = mask_bytes(h, n_logits, ranks);
-  const cudaError_t e = launch_clusters<k_grammar_mask>(h->dev, n * ranks, GR_THREADS, ranks, smem, st, g->g, h->tokens, c);
+  const cudaError_t e = launch_clusters<k_grammar_mask>(h->dev, n * ranks, GR_THREADS, ranks, mask_bytes(n_logits, share_of(h, ranks)), st,
+                                                        g->g, h->tokens, c);
   h->launches += 1;
   if (e != cudaSuccess) {
     cudaGetLastError();
