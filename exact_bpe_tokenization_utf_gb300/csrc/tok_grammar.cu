@@ -41,9 +41,17 @@ struct MaskCall {
   long long mask_stride;
 };
 
+// (eight bytes at a time, whose loads need not wait for the states)
 __device__ __forceinline__ uint32_t walk(const DevGrammar& g, const DevTokens& v, uint32_t s, uint32_t t) {
-  const uint32_t end = v.off[t + 1];
-  for (uint32_t i = v.off[t]; i < end && s != DEAD; ++i) s = __ldg(g.next + s * 256u + __ldg(v.bytes + i));
+  const uint32_t begin = v.off[t], end = v.off[t + 1];
+  for (uint32_t i = begin; i < end && s != DEAD; i += 8) {
+    uint32_t b[8];
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) b[j] = i + j < end ? __ldg(v.bytes + i + j) : 0u;
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j)
+      if (i + j < end && s != DEAD) s = __ldg(g.next + s * 256u + b[j]);
+  }
   return s;
 }
 
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTo
   uint2* live = list_behind(bits, n_words);
   const Share share{rank, n_ranks};
   const First f = first_group(v, share);
-  for (uint32_t w = tid; w < n_words; w += GR_THREADS) bits[w] = 0;
+  for (uint32_t i = tid; i < (n_words + 3) / 4; i += GR_THREADS) reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) s_live = 0;
   const Window win = look_around(g, v, c, k, s_row);
   if (tid == 0 && rank == 0 && c.state_out) c.state_out[k] = win.state == DEAD ? -1 : (int32_t)win.state;
@@ -296,6 +304,54 @@ uint32_t mask_ranks(const tok_handle* h, uint32_t n, uint32_t n_logits) {
   return s;
 }
 
+// length of the well-formed UTF-8 sequence of two bytes or more (RFC 3629) at s[0..n), or 0
+uint32_t sequence(const uint8_t* s, uint32_t n) {
+  const uint8_t b = s[0];
+  const uint32_t len = b >= 0xc2 && b <= 0xdf ? 2 : b >= 0xe0 && b <= 0xef ? 3 : b >= 0xf0 && b <= 0xf4 ? 4 : 0;
+  if (len == 0 || len > n) return 0;
+  const uint8_t lo = b == 0xe0 ? 0xa0 : b == 0xf0 ? 0x90 : 0x80, hi = b == 0xed ? 0x9f : b == 0xf4 ? 0x8f : 0xbf;
+  if (s[1] < lo || s[1] > hi) return 0;
+  for (uint32_t i = 2; i < len; ++i)
+    if ((s[i] & 0xc0) != 0x80) return 0;
+  return len;
+}
+
+// the kinds of a token's bytes; well-formed sequences are a kind of their own
+uint32_t kinds_of(const uint8_t* s, uint32_t n) {
+  uint32_t k = 0;
+  for (uint32_t i = 0; i < n;) {
+    const uint32_t len = sequence(s + i, n - i);
+    k |= 1u << (len ? KIND_SEQUENCE : byte_kind(s[i]));
+    i += len ? len : 1;
+  }
+  return k;
+}
+
+// Whether every well-formed sequence of two bytes or more leads from state s
+// back to s.  (Answers no where more than a few states are on the way.)
+bool sequences_return(const int32_t* next, uint32_t s) {
+  for (uint32_t b = 0xc2; b <= 0xf4; ++b) {
+    std::vector<int32_t> at{next[(size_t)s * 256 + b]}, to;
+    const uint32_t len = b <= 0xdf ? 2 : b <= 0xef ? 3 : 4;
+    for (uint32_t i = 1; i < len; ++i) {
+      const uint32_t lo = i > 1 ? 0x80 : b == 0xe0 ? 0xa0 : b == 0xf0 ? 0x90 : 0x80;
+      const uint32_t hi = i > 1 ? 0xbf : b == 0xed ? 0x9f : b == 0xf4 ? 0x8f : 0xbf;
+      to.clear();
+      for (int32_t a : at) {
+        if (a < 0) return false;
+        for (uint32_t x = lo; x <= hi; ++x) {
+          const int32_t y = next[(size_t)a * 256 + x];
+          if (std::find(to.begin(), to.end(), y) == to.end()) to.push_back(y);
+        }
+        if (to.size() > 8) return false;
+      }
+      at.swap(to);
+    }
+    if (at.size() != 1 || at[0] != (int32_t)s) return false;
+  }
+  return true;
+}
+
 // the vocabulary's bytes on the device, once per handle
 int ensure_tokens(tok_handle* h) {
   if (h->d_tokens) return TOK_OK;
@@ -321,6 +377,13 @@ int ensure_tokens(tok_handle* h) {
     const uint32_t a = order[i], b = order[i + m - 1];
     uint32_t p = 0;
     while (p < 8 && p < len(a) && p < len(b) && at(a)[p] == at(b)[p]) ++p;  // (sorted: common to all between)
+    // not inside a code point, whose rest would have to be walked
+    auto splits = [&] {
+      for (uint32_t q = 0; q < m; ++q)
+        if (len(order[i + q]) > p && (at(order[i + q])[p] & 0xc0) == 0x80) return true;
+      return false;
+    };
+    while (p > 1 && splits()) --p;
     TokenGroup r{0, 0, (uint32_t)words.size()};
     uint32_t most = 0;
     for (uint32_t j = 0; j < p; ++j) r.head |= (unsigned long long)at(a)[j] << (8 * j);
@@ -333,12 +396,9 @@ int ensure_tokens(tok_handle* h) {
       id.push_back(q < m ? order[i + q] : NO_TOKEN);
       const uint32_t l = q < m ? len(order[i + q]) - p : 0u;
       rest.push_back((uint16_t)l);
-      uint32_t some = 0;
-      for (uint32_t j = 0; j < l; ++j) {
-        const uint8_t x = at(order[i + q])[p + j];
-        words[r.at + (size_t)(j / 4) * 32 + q] |= (uint32_t)x << (8 * (j & 3));
-        some |= 1u << byte_kind(x);
-      }
+      for (uint32_t j = 0; j < l; ++j)
+        words[r.at + (size_t)(j / 4) * 32 + q] |= (uint32_t)at(order[i + q])[p + j] << (8 * (j & 3));
+      const uint32_t some = q < m ? kinds_of(at(order[i + q]) + p, l) : 0u;
       kinds.push_back(some);
       all |= some;
     }
@@ -410,6 +470,8 @@ int tok_grammar_load(tok_handle* h, const int32_t* next, const uint8_t* accept, 
     t[i] = next[i] < 0 ? (uint16_t)DEAD : (uint16_t)next[i];
     if (next[i] != (int32_t)(i / 256)) leaves[i / 256] |= 1u << byte_kind((uint8_t)(i & 255));
   }
+  for (uint32_t s = 0; s < n_states; ++s)
+    if (!sequences_return(next, s)) leaves[s] |= 1u << KIND_SEQUENCE;
   DeviceGuard dg(h->dev);
   int rc = ensure_tokens(h);
   if (rc) return rc;

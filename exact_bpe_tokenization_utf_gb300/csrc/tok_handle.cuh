@@ -40,11 +40,10 @@ struct DevTokens {
   const uint16_t* rest;
 };
 
-// 32 kinds of bytes, such that what a grammar treats apart is often of different kinds
+// Kinds of bytes, such that what a grammar treats apart is often of different
+// kinds; well-formed UTF-8 sequences of several bytes are one of their own.
+constexpr uint32_t KIND_SEQUENCE = 29;
 inline uint32_t byte_kind(uint8_t b) {
-  if (b >= 0xf0) return 31;
-  if (b >= 0xe0) return 30;
-  if (b >= 0xc0) return 29;
   if (b >= 0x80) return 28;
   if (b == 0x7f) return 27;
   if (b >= '0' && b <= '9') return b == '0' ? 8 : 9;
