@@ -93,7 +93,7 @@ __device__ __forceinline__ uint32_t load_once(const uint16_t* p) {
 
 // a lane's token of a group whose common bytes lead to state s
 struct Item {
-  uint32_t s, id, rest, at, word;
+  uint32_t s, id, rest, at, word, kinds, leaves;
 };
 
 // A row's window of GR_THREADS rows: its state, and the rows in equal states.
@@ -171,6 +171,7 @@ __device__ __forceinline__ void find_live(const DevGrammar& g, const DevTokens& 
         f.kinds = __ldg(v.group_kinds + next);
       }
     }
+    if (i == 0 && s != DEAD && __ldg(g.next + s * 256u + (uint32_t)(head & 255u)) == DEAD) s = DEAD;
     for (; i && s != DEAD; --i) {
       s = __ldg(g.next + s * 256u + (uint32_t)(head & 255u));
       head >>= 8;
@@ -196,7 +197,7 @@ __device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& 
                                           uint32_t* bits) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   auto load = [&](uint32_t f) {
-    Item t{DEAD, NO_TOKEN, 0, 0, 0};
+    Item t{DEAD, NO_TOKEN, 0, 0, 0, 0, 0};
     if (f < n_live) {
       const uint2 e = live[f];
       const uint32_t at = (e.x & 0xffffu) * 32 + lane;
@@ -206,7 +207,8 @@ __device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& 
         t.at = e.y + lane;
         t.word = load_once(v.words + t.at);
         t.rest = load_once(v.rest + at);
-        if (!(load_once(v.kinds + at) & __ldg(g.leaves + t.s))) t.rest = 0;
+        t.kinds = load_once(v.kinds + at);
+        t.leaves = __ldg(g.leaves + t.s);
       }
     }
     return t;
@@ -214,7 +216,10 @@ __device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& 
   constexpr uint32_t W = GR_THREADS / 32;
   Item now[2] = {load(warp), load(warp + W)};
   for (uint32_t e = warp; e < n_live; e += 2 * W) {
-    const Item next[2] = {load(e + 2 * W), load(e + 3 * W)};
+    const Item next[2] = {load(e + 2 * W), load(e + 3 * W)};  // (used in the next turn: nothing waits for it here)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (!(now[h].kinds & now[h].leaves)) now[h].rest = 0;
     for (uint32_t w = 0; __any_sync(0xffffffffu, (now[0].rest > w && now[0].s != DEAD) || (now[1].rest > w && now[1].s != DEAD));
          w += 4) {
       uint32_t ahead[2];  // the tokens' next words
@@ -383,10 +388,10 @@ int ensure_tokens(tok_handle* h) {
         if (len(order[i + q]) > p && (at(order[i + q])[p] & 0xc0) == 0x80) return true;
       return false;
     };
-    while (p > 1 && splits()) --p;
+    while (p > 0 && splits()) --p;
     TokenGroup r{0, 0, (uint32_t)words.size()};
     uint32_t most = 0;
-    for (uint32_t j = 0; j < p; ++j) r.head |= (unsigned long long)at(a)[j] << (8 * j);
+    for (uint32_t j = 0; j < std::max(p, 1u); ++j) r.head |= (unsigned long long)at(a)[j] << (8 * j);
     for (uint32_t q = 0; q < m; ++q) most = std::max(most, len(order[i + q]) - p);
     const uint32_t nw = std::max(1u, (most + 3) / 4);
     uint32_t all = 0;

@@ -17,7 +17,8 @@ namespace tokgb {
 // The vocabulary's bytes on the device: token t has bytes[off[t] .. off[t + 1]),
 // and, for walking many tokens at once, the tokens sorted by their bytes in
 // groups of up to 32 that begin alike.  Group g: its first `prefix` bytes (at
-// most 8) are in head; lane i's token is id[32 g + i] (NO_TOKEN: none) with
+// most 8; none, but for a look at the first one, where they would end inside
+// a code point) are in head; lane i's token is id[32 g + i] (NO_TOKEN: none) with
 // rest[32 g + i] bytes more, four per word, words[at + 32 w + i].  kinds has a
 // bit for each kind of byte (byte_kind) among these, group_kinds for the
 // whole group.
