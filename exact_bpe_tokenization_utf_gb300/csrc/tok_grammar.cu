@@ -18,7 +18,6 @@ namespace {
 
 constexpr uint32_t MAX_LOGITS = 1u << 20;
 constexpr uint32_t DEAD = 0xffffu;
-constexpr uint32_t WHOLE = 0x80000000u;  // of a group: its tokens' other bytes do not change the state
 constexpr uint32_t NO_TOKEN = 0xffffffffu;
 constexpr int GR_THREADS = 512;
 
@@ -152,9 +151,11 @@ __device__ __forceinline__ First first_group(const DevTokens& v, const Share& sh
 }
 
 // A thread walks a group's common first bytes, so that one step decides over up
-// to 32 tokens; the groups that survive are listed (the first `room` of them):
-// group | state << 16, place of its words | WHOLE.  n_live (0 before, behind a
-// barrier) receives their number.  Ends with a barrier.
+// to 32 tokens.  The groups that survive are listed: from the front those whose
+// tokens have to be walked (group | state << 16, place of their words), from
+// the back those whose other bytes are all of kinds that do not change the
+// state.  n_live[0] and n_live[1] (0 before, behind a barrier) receive their
+// numbers.  Ends with a barrier.
 __device__ __forceinline__ void find_live(const DevGrammar& g, const DevTokens& v, const Share& sh, First f, uint32_t s0, uint2* live,
                                           uint32_t room, uint32_t* n_live) {
   const uint32_t tid = threadIdx.x, lane = tid & 31u, n = sh.count(v);
@@ -176,68 +177,93 @@ __device__ __forceinline__ void find_live(const DevGrammar& g, const DevTokens& 
       s = __ldg(g.next + s * 256u + (uint32_t)(head & 255u));
       head >>= 8;
     }
-    const uint32_t alive = __ballot_sync(0xffffffffu, s != DEAD);
-    uint32_t at = 0;
-    if (lane == 0 && alive) at = atomicAdd(n_live, (uint32_t)__popc(alive));
-    at = __shfl_sync(0xffffffffu, at, 0) + __popc(alive & ((1u << lane) - 1u));
-    if (s != DEAD && at < room) {
-      const uint32_t whole = (kinds & __ldg(g.leaves + s)) == 0 ? WHOLE : 0u;
-      live[at] = make_uint2(q | s << 16, words | whole);
+    const bool whole = s != DEAD && (kinds & __ldg(g.leaves + s)) == 0;
+#pragma unroll
+    for (uint32_t l = 0; l < 2; ++l) {
+      const uint32_t in = __ballot_sync(0xffffffffu, s != DEAD && whole == (l == 1));
+      uint32_t at = 0;
+      if (lane == 0 && in) at = atomicAdd(n_live + l, (uint32_t)__popc(in));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(in & ((1u << lane) - 1u));
+      if (in >> lane & 1u) live[l ? room - 1 - at : at] = make_uint2(q | s << 16, words);
     }
   }
   __syncthreads();
 }
 
-// A warp takes a listed group's tokens, one per lane.  Bytes of kinds that do not
-// change the state need no walk: inside a string that is most tokens, often
-// a whole group.  The others are walked (sorted tokens read neighbouring bytes
-// from equal states), two groups at a time with the next two on their way.
-// Allowed tokens set their bits.
-__device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& v, const uint2* live, uint32_t n_live, uint32_t n_logits,
-                                          uint32_t* bits) {
+// A warp takes a listed group's tokens, one per lane, and sets the allowed ones'
+// bits: at once where no byte changes the state (inside a string that is most
+// groups), the others by a walk, two groups at a time with the next two on
+// their way.  Four bytes are looked up at once, as if the state stayed; where it
+// changes, the lookups after that are done again.
+__device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& v, const uint2* live, uint32_t room,
+                                          const uint32_t* n_live, uint32_t n_logits, uint32_t* bits) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  constexpr uint32_t W = GR_THREADS / 32;
+  auto allow = [&](uint32_t id) {
+    if (id < n_logits) atomicOr(&bits[id >> 5], 1u << (id & 31));
+  };
+  const uint32_t n_whole = n_live[1], n_walk = n_live[0];
+  for (uint32_t e = warp; e < n_whole; e += 4 * W) {
+    uint32_t id[4];
+#pragma unroll
+    for (uint32_t h = 0; h < 4; ++h)
+      id[h] = e + h * W < n_whole ? load_once(v.id + (live[room - 1 - (e + h * W)].x & 0xffffu) * 32 + lane) : NO_TOKEN;
+#pragma unroll
+    for (uint32_t h = 0; h < 4; ++h) allow(id[h]);
+  }
   auto load = [&](uint32_t f) {
     Item t{DEAD, NO_TOKEN, 0, 0, 0, 0, 0};
-    if (f < n_live) {
+    if (f < n_walk) {  // (every group has a first word, so that these loads need not wait for one another)
       const uint2 e = live[f];
       const uint32_t at = (e.x & 0xffffu) * 32 + lane;
-      t.id = load_once(v.id + at);
       t.s = e.x >> 16;
-      if (!(e.y & WHOLE)) {  // (every group has a first word, so that these loads need not wait for one another)
-        t.at = e.y + lane;
-        t.word = load_once(v.words + t.at);
-        t.rest = load_once(v.rest + at);
-        t.kinds = load_once(v.kinds + at);
-        t.leaves = __ldg(g.leaves + t.s);
-      }
+      t.at = e.y + lane;
+      t.id = load_once(v.id + at);
+      t.word = load_once(v.words + t.at);
+      t.rest = load_once(v.rest + at);
+      t.kinds = load_once(v.kinds + at);
+      t.leaves = __ldg(g.leaves + t.s);
     }
     return t;
   };
-  constexpr uint32_t W = GR_THREADS / 32;
   Item now[2] = {load(warp), load(warp + W)};
-  for (uint32_t e = warp; e < n_live; e += 2 * W) {
+  for (uint32_t e = warp; e < n_walk; e += 2 * W) {
     const Item next[2] = {load(e + 2 * W), load(e + 3 * W)};  // (used in the next turn: nothing waits for it here)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       if (!(now[h].kinds & now[h].leaves)) now[h].rest = 0;
     for (uint32_t w = 0; __any_sync(0xffffffffu, (now[0].rest > w && now[0].s != DEAD) || (now[1].rest > w && now[1].s != DEAD));
          w += 4) {
-      uint32_t ahead[2];  // the tokens' next words
+      uint32_t ahead[2], from[2] = {0, 0}, to[2];  // the tokens' next words; the bytes of this word to be read
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        ahead[h] = now[h].rest > w + 4 && now[h].s != DEAD ? load_once(v.words + now[h].at + 8 * (w + 4)) : 0u;
+      for (int h = 0; h < 2; ++h) {
+        const bool on = now[h].rest > w && now[h].s != DEAD;
+        ahead[h] = on && now[h].rest > w + 4 ? load_once(v.words + now[h].at + 8 * (w + 4)) : 0u;
+        to[h] = on ? min(now[h].rest - w, 4u) : 0u;
+      }
+      while (__any_sync(0xffffffffu, from[0] < to[0] || from[1] < to[1])) {
+        uint32_t t[2][4];
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
+        for (uint32_t i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (w + i < now[h].rest && now[h].s != DEAD) now[h].s = __ldg(g.next + now[h].s * 256u + (now[h].word >> (8 * i) & 255u));
+          for (int h = 0; h < 2; ++h)
+            t[h][i] = i >= from[h] && i < to[h] ? (uint32_t)__ldg(g.next + now[h].s * 256u + (now[h].word >> (8 * i) & 255u)) : now[h].s;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t s = now[h].s;
+          // the first byte that changes the state is the last one that counts
+          const uint32_t stop = t[h][0] != s ? 0 : t[h][1] != s ? 1 : t[h][2] != s ? 2 : 3;
+          now[h].s = stop == 0 ? t[h][0] : stop == 1 ? t[h][1] : stop == 2 ? t[h][2] : t[h][3];
+          from[h] = now[h].s == DEAD ? to[h] : stop + 1;
+        }
       }
       now[0].word = ahead[0];
       now[1].word = ahead[1];
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (now[h].s != DEAD && now[h].id < n_logits) atomicOr(&bits[now[h].id >> 5], 1u << (now[h].id & 31));
+      if (now[h].s != DEAD) allow(now[h].id);
       now[h] = next[h];
     }
   }
@@ -260,10 +286,10 @@ __device__ __forceinline__ uint2* list_behind(uint32_t* bits, uint32_t n_words) 
 // words that are not empty to the CTAs that write them, a share of the row
 // each.  Rows in equal states are walked once, by the first one's cluster,
 // which writes all of them.
-__global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTokens v, MaskCall c) {
+__global__ void __launch_bounds__(GR_THREADS, 3) k_grammar_mask(DevGrammar g, DevTokens v, MaskCall c) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint32_t s_mem[];
-  __shared__ uint32_t s_live, s_row[GR_THREADS / 32 + 1];
+  __shared__ uint32_t s_live[2], s_row[GR_THREADS / 32 + 1];
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t rank = cluster.block_rank(), n_ranks = cluster.num_blocks(), k = blockIdx.x / n_ranks, tid = threadIdx.x;
   const uint32_t n_words = (c.n_logits + 31) / 32;
@@ -272,19 +298,19 @@ __global__ void __launch_bounds__(GR_THREADS) k_grammar_mask(DevGrammar g, DevTo
   const Share share{rank, n_ranks};
   const First f = first_group(v, share);
   for (uint32_t i = tid; i < (n_words + 3) / 4; i += GR_THREADS) reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
-  if (tid == 0) s_live = 0;
+  if (tid < 2) s_live[tid] = 0;
   const Window win = look_around(g, v, c, k, s_row);
   if (tid == 0 && rank == 0 && c.state_out) c.state_out[k] = win.state == DEAD ? -1 : (int32_t)win.state;
   if (!win.first) return;  // (in every CTA of the cluster alike)
   cluster_arrive();        // (waited for before another CTA's bits are set)
   if (win.state != DEAD) {
-    find_live(g, v, share, f, win.state, live, share.count(v), &s_live);
-    walk_live(g, v, live, s_live, c.n_logits, bits);
+    find_live(g, v, share, f, win.state, live, share.count(v), s_live);
+    walk_live(g, v, live, share.count(v), s_live, c.n_logits, bits);
   }
   const uint32_t each = (n_words + n_ranks - 1) / n_ranks;
   __syncthreads();
   cluster_wait();
-  if (s_live)
+  if (s_live[0] | s_live[1])
     for (uint32_t w = tid; w < n_words; w += GR_THREADS)
       if (bits[w] && w / each != rank) atomicOr(cluster.map_shared_rank(bits, w / each) + w, bits[w]);
   cluster.sync();
