@@ -289,12 +289,16 @@ __device__ __forceinline__ void store_all(T* to, float x) {
   __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[0], w[0], w[0]));
 }
 
+// the sums of a slice's words, four words each, in whole 16 bytes
+__host__ __device__ constexpr uint32_t fours_of(uint32_t words) { return (words / 4 + 3) / 4 * 4; }
+
 // A slice's bits in shared memory, moved so that the bits of a vector lie in
 // one byte: bit p is that of token lo + p (lo modulo 2^32: it may be negative).
-__host__ __device__ constexpr uint32_t bit_words(uint32_t tokens) { return (tokens + 48 + 31) / 32; }
+__host__ __device__ constexpr uint32_t bit_words(uint32_t tokens) { return ((tokens + 48 + 31) / 32 + 3) / 4 * 4; }
 
 __device__ __forceinline__ void move_bits(uint32_t* to, const uint32_t* from, uint32_t n_logits, uint32_t lo, uint32_t n) {
   const int n_words = (int)((n_logits + 31) / 32);
+#pragma unroll 4
   for (uint32_t j = threadIdx.x; j < n; j += LG_THREADS) {
     const int first = (int)(lo + 32 * j) >> 5;
     const uint32_t a = first >= 0 && first < n_words ? __ldg(from + first) : 0u;
@@ -357,21 +361,27 @@ __device__ __forceinline__ void list_bits(const Row& r, Table& t, uint32_t words
   each_id(r.gen, r.gen_len, one);
   each_id(r.bias_id, r.bias_n, one);
   __syncthreads();
-  const uint32_t groups = (words + 3) / 4, each = (groups + LG_THREADS - 1) / LG_THREADS;
-  const uint32_t g0 = min(threadIdx.x * each, groups), g1 = min(g0 + each, groups);
-  auto in_group = [&](uint32_t g) {
-    uint32_t c = 0;
-#pragma unroll
-    for (uint32_t w = 4 * g; w < 4 * g + 4; ++w) c += w < words ? (uint32_t)__popc(t.bits[w]) : 0u;
-    return c;
-  };
-  uint32_t sum = 0;
-  for (uint32_t g = g0; g < g1; ++g) sum += in_group(g);
-  sum = block_excl_sum(sum, &t.total, sh);
-  for (uint32_t g = g0; g < g1; ++g) {
-    t.before[g] = sum;
-    sum += in_group(g);
+  // sums of four words each (16 bytes a thread, side by side), then their scan, four sums a thread
+  const uint32_t fours = (words + 3) / 4;
+  for (uint32_t f = threadIdx.x; f < fours; f += LG_THREADS) {
+    const uint4 b = reinterpret_cast<const uint4*>(t.bits)[f];
+    t.before[f] = (uint32_t)(__popc(b.x) + __popc(b.y) + __popc(b.z) + __popc(b.w));
   }
+  __syncthreads();
+  uint32_t carry = 0;
+  for (uint32_t f0 = 0; f0 < fours; f0 += 4 * LG_THREADS) {
+    const uint32_t f = f0 + 4 * threadIdx.x;
+    uint4 n = make_uint4(0, 0, 0, 0);
+    if (f < fours) n = reinterpret_cast<const uint4*>(t.before)[f / 4];
+    if (f + 1 >= fours) n.y = 0;
+    if (f + 2 >= fours) n.z = 0;
+    if (f + 3 >= fours) n.w = 0;
+    uint32_t all;
+    const uint32_t at = carry + block_excl_sum(n.x + n.y + n.z + n.w, &all, sh);
+    if (f < fours) reinterpret_cast<uint4*>(t.before)[f / 4] = make_uint4(at, at + n.x, at + n.x + n.y, at + n.x + n.y + n.z);
+    carry += all;
+  }
+  t.total = carry;
 }
 
 // the place of a listed token
@@ -384,10 +394,11 @@ __device__ __forceinline__ uint32_t place_of(const Table& t, uint32_t v) {
   return n;
 }
 
-// one(token, occurrences, first bias entry) for this thread's listed tokens, in the order of the tokens
-template <class F>
+// one(token, occurrences, first bias entry, load(token)) for this thread's
+// listed tokens, in the order of the tokens, four loads at a time
+template <class L, class F>
 __device__ __forceinline__ void each_listed(const Row& r, Table& t, void* mem, uint32_t bytes, bool bias, uint32_t from,
-                                            uint32_t n_tokens, F one) {
+                                            uint32_t n_tokens, L load, F one) {
   t.room = bytes / (bias ? 12u : 8u);
   t.token = static_cast<uint32_t*>(mem);
   t.count = t.token + t.room;
@@ -425,7 +436,27 @@ __device__ __forceinline__ void each_listed(const Row& r, Table& t, void* mem, u
       }
     }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < n; i += LG_THREADS) one(t.token[i], t.count[i], bias ? t.first[i] : NO_BIAS);
+    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += 4 * LG_THREADS) {
+      uint32_t v[4];
+      float2 x[4];
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) {
+        v[j] = i0 + j * LG_THREADS < n ? t.token[i0 + j * LG_THREADS] : 0xffffffffu;
+        x[j] = make_float2(0.f, 0.f);
+        if (v[j] != 0xffffffffu) x[j] = load(v[j]);
+      }
+#pragma unroll 1
+      for (uint32_t i = i0; i < n && i < i0 + 4 * LG_THREADS; i += LG_THREADS) {
+        one(v[0], t.count[i], bias ? t.first[i] : NO_BIAS, x[0]);
+        // (moved up, so that the body stands here once)
+        v[0] = v[1];
+        v[1] = v[2];
+        v[2] = v[3];
+        x[0] = x[1];
+        x[1] = x[2];
+        x[2] = x[3];
+      }
+    }
   }
 }
 
@@ -533,7 +564,7 @@ template <class T> struct Slice {
     table.total = table.room = 0;
     if (lists) {
       table.before = w + sh.words;
-      w += sh.words + (sh.words + 3) / 4;
+      w += sh.words + fours_of(sh.words);
       for (uint32_t i = threadIdx.x; i < sh.words; i += LG_THREADS) table.bits[i] = 0;
     }
     if (masked) {
@@ -750,9 +781,10 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
   // the listed tokens
   if (c.lists)
     each_listed(r, c.table, s_mem, call.shape.front, a.d_bias_off != nullptr, c.from, c.to - c.from,
-                [&](uint32_t t, uint32_t n, uint32_t fb) {
+                [&](uint32_t t) { return make_float2(Num<T>::get(x[t]), 0.f); },
+                [&](uint32_t t, uint32_t n, uint32_t fb, float2 xt) {
                   float z = -INFINITY;
-                  if (c.allows(t)) z = score(r, t, n, fb, c.saw(t), Num<T>::get(x[t]));
+                  if (c.allows(t)) z = score(r, t, n, fb, c.saw(t), xt.x);
                   if (z * k > ref + 24.f) raise(z * k);
                   sum += ex2(fmaf(z, k, -ref));
                   key = max(key, top_key(z, t));
@@ -855,13 +887,14 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   c.fill(a, call.shape, r, s_mem, s_scan);
 
   // the gradient of one score and, returned, the one before the repetition penalty
-  auto one = [&](uint32_t t, uint32_t n, uint32_t fb) {
+  auto load = [&](uint32_t t) { return make_float2(Num<T>::get(x[t]), go ? Num<T>::get(go[t]) : 0.f); };
+  auto one = [&](uint32_t t, uint32_t n, uint32_t fb, float2 in) {
     float dz = 0.f, f = 1.f;
     if (c.allows(t)) {
       const bool seen = c.saw(t);
-      const float xt = Num<T>::get(x[t]);
+      const float xt = in.x;
       if (seen || n) f = xt > 0.f ? r.inv_rep : r.rep;
-      if (go) dz = Num<T>::get(go[t]) * r.inv_t;
+      dz = in.y * r.inv_t;
       if (cpt != 0.f) {
         const float z = fmaxf(score(r, t, n, fb, seen, xt), -FLT_MAX);  // (-inf times k_lo is no number)
         dz = fmaf(cpt, sizeof(T) == 4 ? ex2_small(fmaf(z, k, -lh) + fmaf(z, k_lo, -l_lo)) : ex2(fmaf(z, k, -lh)), dz);
@@ -873,7 +906,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   };
   if (tid < 32) {  // the scores outside the vectors
     const uint32_t t = c.outside(tid);
-    if (t != 0xffffffffu && !(c.lists && listed(c.table, t))) one(t, 0, NO_BIAS);
+    if (t != 0xffffffffu && !(c.lists && listed(c.table, t))) one(t, 0, NO_BIAS, load(t));
   }
   const Two k2(k, k), lh2(-lh, -lh), klo2(k_lo, k_lo), llo2(-l_lo, -l_lo), cpt2(cpt, cpt), inv_t2(r.inv_t, r.inv_t);
   const uint32_t steps = (c.i_end - c.i_begin + U * LG_THREADS - 1) / (U * LG_THREADS);
@@ -938,13 +971,13 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   }
   S::close();
   __syncthreads();
-  if (tid == 0 && pick - c.from < c.to - c.from && !(c.lists && listed(c.table, pick))) one(pick, 0, NO_BIAS);
+  if (tid == 0 && pick - c.from < c.to - c.from && !(c.lists && listed(c.table, pick))) one(pick, 0, NO_BIAS, load(pick));
 
   // the listed tokens, with their biases' gradients
   if (c.lists)
     each_listed(r, c.table, s_mem, call.shape.front, a.d_bias_off != nullptr, c.from, c.to - c.from,
-                [&](uint32_t t, uint32_t n, uint32_t fb) {
-                  const float dz = one(t, n, fb);
+                load, [&](uint32_t t, uint32_t n, uint32_t fb, float2 in) {
+                  const float dz = one(t, n, fb, in);
                   if (!gr.bias || (fb & NO_BIAS) == NO_BIAS) return;
                   float* gb = gr.bias + (r.bias - a.d_bias);
                   gb[fb & NO_BIAS] = dz;
@@ -1010,7 +1043,7 @@ Shape shape(const tok_logits_args& a, bool shifted, int arrays, uint32_t n, size
   s.words = bit_words(s.per * vec);
   s.front = (uint32_t)stage_bytes(a.dtype, shifted) * arrays;
   *smem = s.front + sizeof(uint32_t) * ((size_t)s.words * ((a.d_mask ? 1 : 0) + (a.d_seen ? 1 : 0) + (s.lists ? 1 : 0)) +
-                                        (s.lists ? (s.words + 3) / 4 : 0));
+                                        (s.lists ? fours_of(s.words) : 0));
   return s;
 }
 
@@ -1020,7 +1053,7 @@ Shape shape(const tok_logits_args& a, bool shifted, int arrays, uint32_t n, size
 uint32_t slices(const tok_handle* h, const tok_logits_args& a, bool shifted, int arrays) {
   uint32_t best = 0;
   double least = 0;
-  for (uint32_t n = 1; n <= 16; ++n) {
+  for (uint32_t n = 1; n <= 16; n *= 2) {  // (clusters of other sizes leave slots of an SM group empty)
     if (best && a.n_logits / n < 2048) break;
     size_t smem;
     shape(a, shifted, arrays, n, &smem);
