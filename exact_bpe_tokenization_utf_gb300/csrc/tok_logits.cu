@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 
 #include <cfloat>
+#include <type_traits>
 
 #include "tok_handle.cuh"
 #include "tok_scan.cuh"
@@ -194,34 +195,43 @@ template <class T, bool SHIFTED> struct Stream {
   static constexpr size_t BYTES = (size_t)DEPTH * STAGE;
 
   const uint8_t* from;  // this lane's piece of the next step to be issued
-  uint32_t left;        // vectors from this thread's first one of that step on
   uint32_t shift;       // bytes of the vectors past a 16-byte boundary
   uint8_t* mine;        // this lane's slot of stage 0
+  uint32_t slot;        // the same as a shared address
 
-  __device__ __forceinline__ void open(const T* row, uint32_t v0, uint32_t i_begin, uint32_t i_end, uint8_t* mem) {
+  __device__ __forceinline__ void open(const T* row, uint32_t v0, uint32_t i_begin, uint8_t* mem) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(row + v0);
     shift = (uint32_t)(at & 15u);
     from = reinterpret_cast<const uint8_t*>(at - (SHIFTED ? shift : 0u)) + ((size_t)i_begin + threadIdx.x) * 16;
     mine = mem + (threadIdx.x >> 5) * U * SLOT + (threadIdx.x & 31u) * 16;
-    left = i_begin + threadIdx.x < i_end ? i_end - i_begin - threadIdx.x : 0u;
-    // (a shifted row's last piece belongs to the last vector, which another lane may hold)
-    if (SHIFTED && i_end > i_begin && i_begin + threadIdx.x <= i_end) left = i_end - i_begin - threadIdx.x + 1u;
+    slot = (uint32_t)__cvta_generic_to_shared(mine);
   }
-  static __device__ __forceinline__ void copy(uint8_t* to, const uint8_t* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(src)
-                 : "memory");
+  static __device__ __forceinline__ void copy(uint32_t to, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
   }
-  // the next step into a stage; bit u of want: whether scores of the u-th vector matter (for a shifted row: any)
+  // The next step into a stage, all of whose vectors exist; bit u of want:
+  // whether scores of the u-th vector matter (for a shifted row: any).
   __device__ __forceinline__ void issue(uint32_t stage, uint32_t want) {
-    uint8_t* to = mine + stage * STAGE;
+    const uint32_t to = slot + stage * STAGE;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint8_t* src = from + u * (LG_THREADS * 16);
-      if ((want >> u & 1u) && left > (uint32_t)(u * LG_THREADS)) copy(to + u * SLOT, src);
-      if (SHIFTED && want && (threadIdx.x & 31u) == 0 && left > (uint32_t)(u * LG_THREADS + 32)) copy(to + u * SLOT + 512, src + 512);
+      if (want >> u & 1u) copy(to + u * SLOT, from + u * (LG_THREADS * 16));
+      if (SHIFTED && (want & 1u) && (threadIdx.x & 31u) == 0) copy(to + u * SLOT + 512, from + u * (LG_THREADS * 16) + 512);
     }
     from += U * LG_THREADS * 16;
-    left = left > (uint32_t)(U * LG_THREADS) ? left - U * LG_THREADS : 0u;
+  }
+  // The same of a slice's last steps: only what lies within its n vectors, the
+  // thread's first one being ii.  (A shifted row's last piece belongs to the
+  // last vector, which another lane may hold.)
+  __device__ __forceinline__ void issue_end(uint32_t stage, uint32_t want, uint32_t ii, uint32_t n) {
+    const uint32_t to = slot + stage * STAGE, end = n ? n + (SHIFTED ? 1u : 0u) : 0u;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = ii + u * LG_THREADS;
+      if ((want >> u & 1u) && i < end) copy(to + u * SLOT, from + u * (LG_THREADS * 16));
+      if (SHIFTED && (want & 1u) && (threadIdx.x & 31u) == 0 && i + 32 < end) copy(to + u * SLOT + 512, from + u * (LG_THREADS * 16) + 512);
+    }
+    from += U * LG_THREADS * 16;
   }
   // the copies issued since the last call are a step
   static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -278,6 +288,14 @@ __device__ __forceinline__ void store_scores(T* to, const float* z, float factor
     mul2(Two(z[2 * e], z[2 * e + 1]), f).get(a, b);
     Num<T>::put_pair(w, e, a, b);
   }
+  __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+template <class T>
+__device__ __forceinline__ void store_vector(T* to, const float* z) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < Num<T>::VEC / 2; ++e) Num<T>::put_pair(w, e, z[2 * e], z[2 * e + 1]);
   __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
@@ -481,15 +499,12 @@ __device__ __forceinline__ float score(const Row& r, uint32_t v, uint32_t c, uin
 
 // The repetition penalty of a thread's seen scores, as a product with its
 // reciprocal, within 2^-22 of the quotient: where that can decide which score
-// is the largest, they are taken again with score().  d: scaled alike.
-__device__ __forceinline__ void penalise(const Row& r, uint32_t seen, float* z, float* d) {
+// is the largest, they are taken again with score().
+__device__ __forceinline__ void penalise(const Row& r, uint32_t seen, float* z) {
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const float f = z[q] > 0.f ? r.inv_rep : r.rep;
-    if ((seen >> q) & 1u) {
-      z[q] *= f;
-      if (d) d[q] = f;
-    }
+    if ((seen >> q) & 1u) z[q] *= f;
   }
 }
 
@@ -527,6 +542,7 @@ __device__ __forceinline__ void join_sum(float& ref, float& sum, float ref2, flo
 
 // A row's slice as a CTA takes it, for both kernels: its vectors, its bits in
 // shared memory and its listed tokens.
+constexpr size_t BITS_ROOM = 16 * LG_THREADS / 8 + 64;  // read, not used, behind a slice's last bits: a step's
 struct Shape {
   uint32_t per;      // vectors per CTA
   uint32_t words;    // of a slice's bits
@@ -580,28 +596,34 @@ template <class T> struct Slice {
     if (lists) list_bits(r, table, sh.words, from, to - from, scan);
     __syncthreads();
   }
-  // the bits of a thread's vectors, the first one ii after the slice's first (those outside: 0)
+  __device__ __forceinline__ uint32_t n_vec() const { return i_end - i_begin; }
+  // the bits of a thread's vectors, the first one ii after the slice's first
+  // (beyond the slice: of what follows in memory)
   __device__ __forceinline__ uint32_t bits_at(const uint32_t* bits, uint32_t ii) const {
     uint32_t m = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (ii + u * LG_THREADS < i_end - i_begin) m |= vector_bits<T>(bits, ii + u * LG_THREADS) << (u * VEC);
+    for (int u = 0; u < U; ++u) m |= vector_bits<T>(bits, ii + u * LG_THREADS) << (u * VEC);
     return m;
   }
+  // the scores of a thread's vectors that are the slice's
   __device__ __forceinline__ uint32_t inside(uint32_t ii) const {
     uint32_t m = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (ii + u * LG_THREADS < i_end - i_begin) m |= ((1u << VEC) - 1u) << (u * VEC);
+      if (ii + u * LG_THREADS < n_vec()) m |= ((1u << VEC) - 1u) << (u * VEC);
     return m;
   }
-  __device__ __forceinline__ uint32_t allowed_at(uint32_t ii) const {
-    return none ? 0u : masked ? bits_at(mask, ii) : inside(ii);
+  // those that the mask allows; whole: the slice has all of the step's vectors
+  __device__ __forceinline__ uint32_t allowed_at(uint32_t ii, bool whole) const {
+    uint32_t m = masked ? bits_at(mask, ii) : none ? 0u : FULL;
+    if (!whole) m &= inside(ii);
+    return m;
   }
   // which of a thread's vectors have allowed scores; for a shifted row: whether any of the warp's has
   template <bool SHIFTED>
-  __device__ __forceinline__ uint32_t wanted(uint32_t ii) const {
-    const uint32_t m = allowed_at(ii);
+  __device__ __forceinline__ uint32_t wanted(uint32_t ii, bool whole) const {
+    if (!masked) return none ? 0u : 0xffu;
+    const uint32_t m = allowed_at(ii, whole);
     if (SHIFTED) return __any_sync(0xffffffffu, m != 0) ? 0xffu : 0u;
     uint32_t w = 0;
 #pragma unroll
@@ -654,11 +676,11 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
   Slice<T> c;
   c.open(a, call.shape, vectors<T, SHIFTED>(out ? static_cast<const void*>(out) : x, a.n_logits), rank, n_ranks);
   S in;
-  in.open(x, c.v0, c.i_begin, c.i_end, s_mem);
+  in.open(x, c.v0, c.i_begin, s_mem);
   // the first steps' scores, before it is known which of them are hidden
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) {
-    in.issue(d, 0xffu);
+    in.issue_end(d, 0xffu, tid + d * U * LG_THREADS, c.n_vec());
     S::commit();
   }
   const Row r = load_row(a, b);
@@ -697,20 +719,20 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
     raise(y);
     sum = ex2(fmaf(z, k, -ref));
   }
-  const uint32_t steps = (c.i_end - c.i_begin + U * LG_THREADS - 1) / (U * LG_THREADS);
+  const uint32_t n = c.n_vec(), steps = (n + U * LG_THREADS - 1) / (U * LG_THREADS), whole = n / (U * LG_THREADS);
   T* to = out + c.v0 + (c.i_begin + tid) * VEC;
   uint32_t stage = 0, ii = tid;
 #pragma unroll 1
   for (uint32_t step = 0; step < steps; ++step, ii += U * LG_THREADS) {
     const uint32_t special = c.lists ? c.bits_at(c.table.bits, ii) : 0u;
-    const uint32_t loaded = c.allowed_at(ii), allowed = loaded & ~special;
+    const uint32_t loaded = c.allowed_at(ii, step < whole), allowed = loaded & ~special;
     S::wait();
     if (__any_sync(ALL, allowed != 0)) {
       const uint32_t seen = c.marked ? c.bits_at(c.seen, ii) : 0u;
       float z[PER];
 #pragma unroll
       for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
-      if (c.marked) penalise(r, seen, z, nullptr);
+      if (c.marked) penalise(r, seen, z);
       if (allowed != FULL) {
 #pragma unroll
         for (int q = 0; q < PER; ++q)
@@ -755,12 +777,12 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
       if (out) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (ii + u * LG_THREADS < c.i_end - c.i_begin) store_scores(to + u * (LG_THREADS * VEC), z + u * VEC, r.inv_t);
+          if (step < whole || ii + u * LG_THREADS < n) store_scores(to + u * (LG_THREADS * VEC), z + u * VEC, r.inv_t);
       }
     } else if (out) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (ii + u * LG_THREADS < c.i_end - c.i_begin) store_all(to + u * (LG_THREADS * VEC), -INFINITY);
+        if (step < whole || ii + u * LG_THREADS < n) store_all(to + u * (LG_THREADS * VEC), -INFINITY);
     }
     if (out) {
       if (call.in_place)  // the logits of listed tokens are still needed
@@ -772,8 +794,12 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
     }
     // this stage's slots are free: the step DEPTH later
     __syncwarp();
-    in.issue(stage, step + DEPTH < steps ? c.template wanted<SHIFTED>(ii + DEPTH * U * LG_THREADS) : 0u);
-    S::commit();
+    {
+      const uint32_t later = step + DEPTH, i_later = ii + DEPTH * U * LG_THREADS;
+      if (later < whole) in.issue(stage, c.template wanted<SHIFTED>(i_later, true));
+      else if (later < steps) in.issue_end(stage, c.template wanted<SHIFTED>(i_later, false), i_later, n);
+      S::commit();
+    }
     stage = stage + 1 == DEPTH ? 0 : stage + 1;
   }
   S::close();
@@ -782,9 +808,9 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
   if (c.lists)
     each_listed(r, c.table, s_mem, call.shape.front, a.d_bias_off != nullptr, c.from, c.to - c.from,
                 [&](uint32_t t) { return make_float2(Num<T>::get(x[t]), 0.f); },
-                [&](uint32_t t, uint32_t n, uint32_t fb, float2 xt) {
+                [&](uint32_t t, uint32_t times, uint32_t fb, float2 xt) {
                   float z = -INFINITY;
-                  if (c.allows(t)) z = score(r, t, n, fb, c.saw(t), xt.x);
+                  if (c.allows(t)) z = score(r, t, times, fb, c.saw(t), xt.x);
                   if (z * k > ref + 24.f) raise(z * k);
                   sum += ex2(fmaf(z, k, -ref));
                   key = max(key, top_key(z, t));
@@ -862,12 +888,12 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   Slice<T> c;
   c.open(a, call.shape, vectors<T, SHIFTED>(gx, a.n_logits), rank, call.ranks);
   S in, gin;
-  in.open(x, c.v0, c.i_begin, c.i_end, s_mem);
-  gin.open(go ? go : x, c.v0, c.i_begin, c.i_end, s_mem + (go ? S::BYTES : 0));
+  in.open(x, c.v0, c.i_begin, s_mem);
+  gin.open(go ? go : x, c.v0, c.i_begin, s_mem + (go ? S::BYTES : 0));
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) {
-    in.issue(d, 0xffu);
-    if (go) gin.issue(d, 0xffu);
+    in.issue_end(d, 0xffu, tid + d * U * LG_THREADS, c.n_vec());
+    if (go) gin.issue_end(d, 0xffu, tid + d * U * LG_THREADS, c.n_vec());
     S::commit();
   }
   const Row r = load_row(a, b);
@@ -888,15 +914,15 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
 
   // the gradient of one score and, returned, the one before the repetition penalty
   auto load = [&](uint32_t t) { return make_float2(Num<T>::get(x[t]), go ? Num<T>::get(go[t]) : 0.f); };
-  auto one = [&](uint32_t t, uint32_t n, uint32_t fb, float2 in) {
+  auto one = [&](uint32_t t, uint32_t times, uint32_t fb, float2 in) {
     float dz = 0.f, f = 1.f;
     if (c.allows(t)) {
       const bool seen = c.saw(t);
       const float xt = in.x;
-      if (seen || n) f = xt > 0.f ? r.inv_rep : r.rep;
+      if (seen || times) f = xt > 0.f ? r.inv_rep : r.rep;
       dz = in.y * r.inv_t;
       if (cpt != 0.f) {
-        const float z = fmaxf(score(r, t, n, fb, seen, xt), -FLT_MAX);  // (-inf times k_lo is no number)
+        const float z = fmaxf(score(r, t, times, fb, seen, xt), -FLT_MAX);  // (-inf times k_lo is no number)
         dz = fmaf(cpt, sizeof(T) == 4 ? ex2_small(fmaf(z, k, -lh) + fmaf(z, k_lo, -l_lo)) : ex2(fmaf(z, k, -lh)), dz);
       }
       if (t == pick) dz = fmaf(glp, r.inv_t, dz);
@@ -908,47 +934,62 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
     const uint32_t t = c.outside(tid);
     if (t != 0xffffffffu && !(c.lists && listed(c.table, t))) one(t, 0, NO_BIAS, load(t));
   }
-  const Two k2(k, k), lh2(-lh, -lh), klo2(k_lo, k_lo), llo2(-l_lo, -l_lo), cpt2(cpt, cpt), inv_t2(r.inv_t, r.inv_t);
-  const uint32_t steps = (c.i_end - c.i_begin + U * LG_THREADS - 1) / (U * LG_THREADS);
+  const Two k2(k, k), lh2(-lh, -lh), klo2(k_lo, k_lo), llo2(-l_lo, -l_lo), cpt2(cpt, cpt);
+  const uint32_t n = c.n_vec(), steps = (n + U * LG_THREADS - 1) / (U * LG_THREADS), whole = n / (U * LG_THREADS);
   T* to = gx + c.v0 + (c.i_begin + tid) * VEC;
   uint32_t stage = 0, ii = tid;
 #pragma unroll 1
   for (uint32_t step = 0; step < steps; ++step, ii += U * LG_THREADS, to += U * LG_THREADS * VEC) {
-    const uint32_t allowed = c.allowed_at(ii) & ~(c.lists ? c.bits_at(c.table.bits, ii) : 0u);
+    const uint32_t allowed = c.allowed_at(ii, step < whole) & ~(c.lists ? c.bits_at(c.table.bits, ii) : 0u);
     S::wait();
     if (__any_sync(ALL, allowed != 0)) {
-      float z[PER], d[PER], f[PER];
+      float z[PER], d[PER];
 #pragma unroll
       for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
-      if (c.marked) {
-        const uint32_t seen = c.bits_at(c.seen, ii);
-#pragma unroll
-        for (int q = 0; q < PER; ++q) f[q] = 1.f;
-        penalise(r, seen, z, f);
-      }
       if (go) {
 #pragma unroll
         for (int u = 0; u < U; ++u) gin.scores(stage, u, d + u * VEC);
-      }
 #pragma unroll
-      for (int q = 0; q < PER; q += 2) {
-        Two d2(0.f, 0.f);
-        if (go) d2 = mul2(Two(d[q], d[q + 1]), inv_t2);
-        if (cpt != 0.f) {
-          if (sizeof(T) == 4) {  // (-inf times k_lo is no number)
-            z[q] = fmaxf(z[q], -FLT_MAX);
-            z[q + 1] = fmaxf(z[q + 1], -FLT_MAX);
-          }
-          const Two z2(z[q], z[q + 1]);
-          Two e2 = fma2(z2, k2, lh2);
-          if (sizeof(T) == 4) e2 = add2(e2, fma2(z2, klo2, llo2));
-          float p0, p1;
-          e2.get(p0, p1);
-          d2 = fma2(cpt2, sizeof(T) == 4 ? Two(ex2_small(p0), ex2_small(p1)) : Two(ex2(p0), ex2(p1)), d2);
-        }
-        if (c.marked) d2 = mul2(d2, Two(f[q], f[q + 1]));
-        d2.get(d[q], d[q + 1]);
+        for (int q = 0; q < PER; ++q) d[q] *= r.inv_t;
+      } else {
+#pragma unroll
+        for (int q = 0; q < PER; ++q) d[q] = 0.f;
       }
+      // (in two versions: rows without seen tokens carry no factors)
+      auto slope = [&](auto factors) {
+        float f[PER];
+        if constexpr (factors) {
+          const uint32_t seen = c.bits_at(c.seen, ii);
+#pragma unroll
+          for (int q = 0; q < PER; ++q) {
+            f[q] = (seen >> q) & 1u ? (z[q] > 0.f ? r.inv_rep : r.rep) : 1.f;
+          }
+#pragma unroll
+          for (int q = 0; q < PER; q += 2) mul2(Two(z[q], z[q + 1]), Two(f[q], f[q + 1])).get(z[q], z[q + 1]);
+        }
+        if (cpt != 0.f) {
+#pragma unroll
+          for (int q = 0; q < PER; q += 2) {
+            if (sizeof(T) == 4) {  // (-inf times k_lo is no number)
+              z[q] = fmaxf(z[q], -FLT_MAX);
+              z[q + 1] = fmaxf(z[q + 1], -FLT_MAX);
+            }
+            const Two z2(z[q], z[q + 1]);
+            Two e2 = fma2(z2, k2, lh2);
+            if (sizeof(T) == 4) e2 = add2(e2, fma2(z2, klo2, llo2));
+            float p0, p1;
+            e2.get(p0, p1);
+            const Two p2 = sizeof(T) == 4 ? Two(ex2_small(p0), ex2_small(p1)) : Two(ex2(p0), ex2(p1));
+            fma2(cpt2, p2, Two(d[q], d[q + 1])).get(d[q], d[q + 1]);
+          }
+        }
+        if constexpr (factors) {
+#pragma unroll
+          for (int q = 0; q < PER; q += 2) mul2(Two(d[q], d[q + 1]), Two(f[q], f[q + 1])).get(d[q], d[q + 1]);
+        }
+      };
+      if (c.marked) slope(std::true_type());
+      else slope(std::false_type());
       if (allowed != FULL) {
 #pragma unroll
         for (int q = 0; q < PER; ++q)
@@ -956,16 +997,23 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (ii + u * LG_THREADS < c.i_end - c.i_begin) store_scores(to + u * (LG_THREADS * VEC), d + u * VEC, 1.f);
+        if (step < whole || ii + u * LG_THREADS < n) store_vector(to + u * (LG_THREADS * VEC), d + u * VEC);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (ii + u * LG_THREADS < c.i_end - c.i_begin) store_all(to + u * (LG_THREADS * VEC), 0.f);
+        if (step < whole || ii + u * LG_THREADS < n) store_all(to + u * (LG_THREADS * VEC), 0.f);
     }
     __syncwarp();
-    const uint32_t want = step + DEPTH < steps ? c.template wanted<SHIFTED>(ii + DEPTH * U * LG_THREADS) : 0u;
-    in.issue(stage, want);
-    if (go) gin.issue(stage, want);
+    const uint32_t later = step + DEPTH, i_later = ii + DEPTH * U * LG_THREADS;
+    if (later < whole) {
+      const uint32_t want = c.template wanted<SHIFTED>(i_later, true);
+      in.issue(stage, want);
+      if (go) gin.issue(stage, want);
+    } else if (later < steps) {
+      const uint32_t want = c.template wanted<SHIFTED>(i_later, false);
+      in.issue_end(stage, want, i_later, n);
+      if (go) gin.issue_end(stage, want, i_later, n);
+    }
     S::commit();
     stage = stage + 1 == DEPTH ? 0 : stage + 1;
   }
@@ -976,8 +1024,8 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   // the listed tokens, with their biases' gradients
   if (c.lists)
     each_listed(r, c.table, s_mem, call.shape.front, a.d_bias_off != nullptr, c.from, c.to - c.from,
-                load, [&](uint32_t t, uint32_t n, uint32_t fb, float2 in) {
-                  const float dz = one(t, n, fb, in);
+                load, [&](uint32_t t, uint32_t times, uint32_t fb, float2 in) {
+                  const float dz = one(t, times, fb, in);
                   if (!gr.bias || (fb & NO_BIAS) == NO_BIAS) return;
                   float* gb = gr.bias + (r.bias - a.d_bias);
                   gb[fb & NO_BIAS] = dz;
@@ -1042,7 +1090,7 @@ Shape shape(const tok_logits_args& a, bool shifted, int arrays, uint32_t n, size
   s.per = (a.n_logits / vec + n - 1) / n;
   s.words = bit_words(s.per * vec);
   s.front = (uint32_t)stage_bytes(a.dtype, shifted) * arrays;
-  *smem = s.front + sizeof(uint32_t) * ((size_t)s.words * ((a.d_mask ? 1 : 0) + (a.d_seen ? 1 : 0) + (s.lists ? 1 : 0)) +
+  *smem = s.front + BITS_ROOM + sizeof(uint32_t) * ((size_t)s.words * ((a.d_mask ? 1 : 0) + (a.d_seen ? 1 : 0) + (s.lists ? 1 : 0)) +
                                         (s.lists ? fours_of(s.words) : 0));
   return s;
 }
