@@ -648,13 +648,13 @@ template <class T> struct Slice {
 struct LogitsCall {
   tok_logits_args a;
   Shape shape;
-  int in_place;  // out is logits
 };
 
 // Forward.  A row is cut into the slices of a cluster's CTAs (one CTA: the
 // whole row); a step gives each thread 16 scores.  Scores that the mask hides
 // are not read.
-template <class T, bool SHIFTED>
+// IN_PLACE: out is logits.
+template <class T, bool SHIFTED, bool IN_PLACE>
 __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call) {
   namespace cg = cooperative_groups;
   using S = Stream<T, SHIFTED>;
@@ -727,12 +727,14 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
     const uint32_t special = c.lists ? c.bits_at(c.table.bits, ii) : 0u;
     const uint32_t loaded = c.allowed_at(ii, step < whole), allowed = loaded & ~special;
     S::wait();
-    if (__any_sync(ALL, allowed != 0)) {
-      const uint32_t seen = c.marked ? c.bits_at(c.seen, ii) : 0u;
+    // (in two versions: rows without seen tokens do not pay for the penalty)
+    auto take = [&](auto marked) {
+      uint32_t seen = 0;
+      if constexpr (marked) seen = c.bits_at(c.seen, ii);
       float z[PER];
 #pragma unroll
       for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
-      if (c.marked) penalise(r, seen, z);
+      if constexpr (marked) penalise(r, seen, z);
       if (allowed != FULL) {
 #pragma unroll
         for (int q = 0; q < PER; ++q)
@@ -779,13 +781,17 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
         for (int u = 0; u < U; ++u)
           if (step < whole || ii + u * LG_THREADS < n) store_scores(to + u * (LG_THREADS * VEC), z + u * VEC, r.inv_t);
       }
+    };
+    if (__any_sync(ALL, allowed != 0)) {
+      if (c.marked) take(std::true_type());
+      else take(std::false_type());
     } else if (out) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (step < whole || ii + u * LG_THREADS < n) store_all(to + u * (LG_THREADS * VEC), -INFINITY);
     }
     if (out) {
-      if (call.in_place)  // the logits of listed tokens are still needed
+      if constexpr (IN_PLACE)  // the logits of listed tokens are still needed
         for (uint32_t m = special & loaded; m; m &= m - 1) {
           const uint32_t q = (uint32_t)__ffs((int)m) - 1u;
           to[q / VEC * (LG_THREADS * VEC) + q % VEC] = Num<T>::put(in.score(stage, q / VEC, q % VEC));
@@ -1125,9 +1131,11 @@ bool alike(const void* p, int64_t stride, const void* q, int64_t q_stride, uint3
 }
 
 template <class T>
-cudaError_t launch_forward(int dev, const LogitsCall& c, bool shifted, unsigned ctas, unsigned cluster, size_t smem, cudaStream_t s) {
-  return shifted ? launch_clusters<k_logits<T, true>>(dev, ctas, LG_THREADS, cluster, smem, s, c)
-                 : launch_clusters<k_logits<T, false>>(dev, ctas, LG_THREADS, cluster, smem, s, c);
+cudaError_t launch_forward(int dev, const LogitsCall& c, bool shifted, bool in_place, unsigned ctas, unsigned cluster, size_t smem,
+                           cudaStream_t s) {
+  if (in_place) return launch_clusters<k_logits<T, false, true>>(dev, ctas, LG_THREADS, cluster, smem, s, c);
+  return shifted ? launch_clusters<k_logits<T, true, false>>(dev, ctas, LG_THREADS, cluster, smem, s, c)
+                 : launch_clusters<k_logits<T, false, false>>(dev, ctas, LG_THREADS, cluster, smem, s, c);
 }
 template <class T>
 cudaError_t launch_grad(int dev, const GradCall& c, bool shifted, unsigned ctas, size_t smem, cudaStream_t s) {
@@ -1154,6 +1162,8 @@ const char* check_logits(const tok_logits_args* a) {
   if ((a->d_gen && (!a->d_gen_start || !a->d_gen_len)) || (a->d_bias_off && (!a->d_bias_id || !a->d_bias)))
     return "logits: generated ids need their starts and lengths, bias offsets their ids and values";
   if (a->d_mask_row && !a->d_mask) return "logits: mask rows without masks";
+  if (a->d_out == a->d_logits && a->out_stride != a->logits_stride && a->rows > 1)
+    return "logits: out is the logits with another stride";
   return nullptr;
 }
 
@@ -1177,11 +1187,11 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream) tr
   const uint32_t n = slices(h, *a, shifted, 1);
   size_t smem;
   c.shape = shape(*a, shifted, 1, n, &smem);
-  c.in_place = a->d_out == a->d_logits;
+  const bool in_place = a->d_out == a->d_logits;
   const unsigned ctas = a->rows * n;
-  const cudaError_t e = a->dtype == TOK_F32   ? launch_forward<float>(h->dev, c, shifted, ctas, n, smem, s)
-                        : a->dtype == TOK_F16 ? launch_forward<__half>(h->dev, c, shifted, ctas, n, smem, s)
-                                              : launch_forward<__nv_bfloat16>(h->dev, c, shifted, ctas, n, smem, s);
+  const cudaError_t e = a->dtype == TOK_F32   ? launch_forward<float>(h->dev, c, shifted, in_place, ctas, n, smem, s)
+                        : a->dtype == TOK_F16 ? launch_forward<__half>(h->dev, c, shifted, in_place, ctas, n, smem, s)
+                                              : launch_forward<__nv_bfloat16>(h->dev, c, shifted, in_place, ctas, n, smem, s);
   return launched(h, e);
 } catch (...) {
   return TOK_ENOMEM;

@@ -372,7 +372,8 @@ typedef struct {
 } tok_logits_args;
 
 /* Errors: TOK_EINVAL (NULL or missing buffers, an unknown type, n_logits out
- * of range, a stride below a row), TOK_ECUDA.  rows == 0 does nothing. */
+ * of range, a stride below a row, out the logits with another stride),
+ * TOK_ECUDA.  rows == 0 does nothing. */
 int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream);
 
 /* tok_logits_backward -- the gradient of tok_logits_process.  a: the same

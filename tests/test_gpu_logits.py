@@ -538,6 +538,22 @@ def test_gradient_against_differences(env):
         at += len(ids)
 
 
+@pytest.mark.parametrize("rows", [0, 1, 2])
+def test_in_place_with_another_stride(env, rows):
+    """Rows of out that begin inside other rows of the logits: refused; a single row has no stride."""
+    torch, pkg, tok = env
+    c = _Case(torch, 2, 100, "f32", 1)
+    args = c.args(pkg, d_out=c.p("logits"), out_stride=101, logits_stride=100, rows=rows)
+    if rows < 2:
+        tok.process_logits_device(args)
+    else:
+        with pytest.raises(pkg.TokError) as e:
+            tok.process_logits_device(args)
+        assert e.value.code == pkg.TOK_EINVAL and "stride" in str(e.value)
+        torch.cuda.synchronize()
+        assert np.array_equal(c.d["logits"].cpu().numpy(), c.x)
+
+
 # --- refusals, seen bits -----------------------------------------------------
 
 def test_refusals(env):
