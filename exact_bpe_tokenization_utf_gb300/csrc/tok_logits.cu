@@ -741,14 +741,16 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
           if (!((allowed >> q) & 1u)) z[q] = -INFINITY;
       }
       const float vmax = max16(z);
-      // scores that may be the largest, once more and exactly; and ref where the scores leave its range
+      // scores that may be the largest, once more and exactly (which those are
+      // depends on the order of the warps, the largest does not); and ref where
+      // the warp's own scores leave its range: the sum has the same bits each time
       const float best = *static_cast<volatile float*>(&s_best);
       const float near = best < INFINITY ? best - fabsf(best) * 0x1p-20f : best;
-      if (__any_sync(ALL, (vmax >= near && vmax > -INFINITY) || best * k > ref + 24.f)) {
+      if (__any_sync(ALL, (vmax >= near && vmax > -INFINITY) || vmax * k > ref + 24.f)) {
         float wmax = vmax;
 #pragma unroll
         for (int o = 16; o; o >>= 1) wmax = fmaxf(wmax, __shfl_xor_sync(ALL, wmax, o));
-        raise(fmaxf(wmax, best) * k);
+        if (wmax * k > ref + 24.f) raise(wmax * k);
         const float at_least = fmaxf(near, wmax - fabsf(wmax) * 0x1p-20f);
         if (vmax >= at_least) {
           uint32_t m = 0;

@@ -538,6 +538,19 @@ def test_gradient_against_differences(env):
         at += len(ids)
 
 
+@pytest.mark.parametrize("rows,kind", [(3, "bf16"), (200, "f32")])
+def test_same_bits_each_time(env, rows, kind):
+    torch, pkg, tok = env
+    c = _Case(torch, rows, 50_001, kind, 12, gen=200, bias=30, mask=[0.9, 0.1, 1.0], seen=True, strengths=True)
+    first = None
+    for _ in range(20):
+        _run(env, c)
+        torch.cuda.synchronize()
+        got = [c.d[k].clone().view(torch.int16 if k == "out" and kind != "f32" else torch.int32) for k in ("out", "top", "lse", "logprob")]
+        assert first is None or all(torch.equal(g, f) for g, f in zip(got, first))
+        first = first or got
+
+
 @pytest.mark.parametrize("rows", [0, 1, 2])
 def test_in_place_with_another_stride(env, rows):
     """Rows of out that begin inside other rows of the logits: refused; a single row has no stride."""
