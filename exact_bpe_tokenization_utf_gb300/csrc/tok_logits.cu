@@ -39,6 +39,7 @@ template <> struct Num<float> {
   static __device__ __forceinline__ float get(float x) { return x; }
   static __device__ __forceinline__ float put(float x) { return x; }
   static constexpr int VEC = 4;  // scores of a vector: 16 bytes
+  static constexpr uint32_t MINUS_INF = 0xff800000u;  // in all of a word's scores
   // scores 2 i and 2 i + 1 of a vector's words
   static __device__ __forceinline__ float2 pair(const uint32_t* w, int i) {
     return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
@@ -50,6 +51,7 @@ template <> struct Num<float> {
 };
 template <> struct Num<__half> {
   static constexpr int VEC = 8;
+  static constexpr uint32_t MINUS_INF = 0xfc00fc00u;
   static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
   static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
   static __device__ __forceinline__ float2 pair(const uint32_t* w, int i) {
@@ -61,6 +63,7 @@ template <> struct Num<__half> {
 };
 template <> struct Num<__nv_bfloat16> {
   static constexpr int VEC = 8;
+  static constexpr uint32_t MINUS_INF = 0xff80ff80u;
   static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
   static __device__ __forceinline__ float2 pair(const uint32_t* w, int i) {
@@ -70,6 +73,24 @@ template <> struct Num<__nv_bfloat16> {
     *reinterpret_cast<__nv_bfloat162*>(w + i) = __floats2bfloat162_rn(a, b);
   }
 };
+
+// Of the words of a thread's u-th vector (scores u VEC on), the scores whose
+// bit of m is clear become those of fill.  For 16-bit scores the bits of two
+// neighbours are moved to the tops of bytes and prmt spreads them: six
+// instructions for four scores, where a test and a choice each take eight.
+template <class T>
+__device__ __forceinline__ void hide(uint32_t* w, uint32_t m, int u, uint32_t fill) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (sizeof(T) == 4) {
+      if (!((m >> (u * 4 + e)) & 1u)) w[e] = fill;
+    } else {
+      uint32_t keep;
+      asm("prmt.b32 %0, %1, %2, %3;" : "=r"(keep) : "r"(m << (7 - 2 * e)), "r"(m << (6 - 2 * e)), "r"(u == 0 ? 0xcc88 : 0xdd99));
+      w[e] = (w[e] & keep) | (fill & ~keep);
+    }
+  }
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -245,16 +266,17 @@ template <class T, bool SHIFTED> struct Stream {
   __device__ __forceinline__ float score(uint32_t stage, uint32_t u, uint32_t e) const {
     return Num<T>::get(*reinterpret_cast<const T*>(mine + stage * STAGE + u * SLOT + (SHIFTED ? shift : 0u) + e * sizeof(T)));
   }
-  __device__ __forceinline__ void scores(uint32_t stage, int u, float* z) const {
+  // the four words of the u-th vector
+  __device__ __forceinline__ void words(uint32_t stage, int u, uint32_t* to) const {
     const uint4* q = reinterpret_cast<const uint4*>(mine + stage * STAGE + u * SLOT);
-    uint32_t w[5];
     const uint4 a = q[0];
     if constexpr (!SHIFTED) {
-      w[0] = a.x;
-      w[1] = a.y;
-      w[2] = a.z;
-      w[3] = a.w;
+      to[0] = a.x;
+      to[1] = a.y;
+      to[2] = a.z;
+      to[3] = a.w;
     } else {
+      uint32_t w[5];
       const uint4 b = q[1];
       const bool two = shift & 8u, one = shift & 4u;
       const uint32_t c0 = two ? a.z : a.x, c1 = two ? a.w : a.y, c2 = two ? b.x : a.z, c3 = two ? b.y : a.w,
@@ -268,12 +290,25 @@ template <class T, bool SHIFTED> struct Stream {
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 2u) * 8u);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to[i] = w[i];
+    }
+  }
+  // the thread's scores, those without a bit in m as -inf (HIDE)
+  template <bool HIDE>
+  __device__ __forceinline__ void scores(uint32_t stage, float* z, uint32_t m) const {
+    uint32_t w[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) words(stage, u, w[u]);
+    if (HIDE && m != (1u << PER) - 1u) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) hide<T>(w[u], m, u, Num<T>::MINUS_INF);
     }
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) {
-      const float2 f = Num<T>::pair(w, e);
-      z[2 * e] = f.x;
-      z[2 * e + 1] = f.y;
+    for (int q = 0; q < PER; q += 2) {
+      const float2 f = Num<T>::pair(w[q / VEC], q % VEC / 2);
+      z[q] = f.x;
+      z[q + 1] = f.y;
     }
   }
 };
@@ -288,14 +323,6 @@ __device__ __forceinline__ void store_scores(T* to, const float* z, float factor
     mul2(Two(z[2 * e], z[2 * e + 1]), f).get(a, b);
     Num<T>::put_pair(w, e, a, b);
   }
-  __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
-}
-
-template <class T>
-__device__ __forceinline__ void store_vector(T* to, const float* z) {
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < Num<T>::VEC / 2; ++e) Num<T>::put_pair(w, e, z[2 * e], z[2 * e + 1]);
   __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
@@ -659,7 +686,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
   namespace cg = cooperative_groups;
   using S = Stream<T, SHIFTED>;
   constexpr int VEC = S::VEC, U = S::U, DEPTH = S::DEPTH;
-  constexpr uint32_t FULL = Slice<T>::FULL, ALL = 0xffffffffu;
+  constexpr uint32_t ALL = 0xffffffffu;
   extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ Part s_part[16];
   __shared__ float s_ref[LG_WARPS], s_sum[LG_WARPS], s_z_pick;
@@ -732,14 +759,8 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
       uint32_t seen = 0;
       if constexpr (marked) seen = c.bits_at(c.seen, ii);
       float z[PER];
-#pragma unroll
-      for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
-      if constexpr (marked) penalise(r, seen, z);
-      if (allowed != FULL) {
-#pragma unroll
-        for (int q = 0; q < PER; ++q)
-          if (!((allowed >> q) & 1u)) z[q] = -INFINITY;
-      }
+      in.template scores<true>(stage, z, allowed);
+      if constexpr (marked) penalise(r, seen, z);  // (-inf stays)
       const float vmax = max16(z);
       // scores that may be the largest, once more and exactly (which those are
       // depends on the order of the warps, the largest does not); and ref where
@@ -880,7 +901,8 @@ struct GradCall {
 // temperature is not lost below 2^-126.  For 32-bit gradients k and lse
 // log2(e) are sums of two numbers each (their rounding would weigh |y| times
 // on the result) and nothing is added to the exponent.
-template <class T, bool SHIFTED>
+// DENSE: out has a gradient.
+template <class T, bool SHIFTED, bool DENSE>
 __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall call) {
   using S = Stream<T, SHIFTED>;
   constexpr int VEC = S::VEC, U = S::U, DEPTH = S::DEPTH;
@@ -891,17 +913,17 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   const Grad& gr = call.g;
   const uint32_t rank = blockIdx.x % call.ranks, b = blockIdx.x / call.ranks, tid = threadIdx.x;
   const T* x = static_cast<const T*>(a.d_logits) + (long long)b * a.logits_stride;
-  const T* go = gr.out ? static_cast<const T*>(gr.out) + (long long)b * gr.out_stride : nullptr;
+  const T* go = DENSE ? static_cast<const T*>(gr.out) + (long long)b * gr.out_stride : x;
   T* gx = static_cast<T*>(gr.logits) + (long long)b * gr.logits_stride;
   Slice<T> c;
   c.open(a, call.shape, vectors<T, SHIFTED>(gx, a.n_logits), rank, call.ranks);
   S in, gin;
   in.open(x, c.v0, c.i_begin, s_mem);
-  gin.open(go ? go : x, c.v0, c.i_begin, s_mem + (go ? S::BYTES : 0));
+  gin.open(go, c.v0, c.i_begin, s_mem + (DENSE ? S::BYTES : 0));
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) {
     in.issue_end(d, 0xffu, tid + d * U * LG_THREADS, c.n_vec());
-    if (go) gin.issue_end(d, 0xffu, tid + d * U * LG_THREADS, c.n_vec());
+    if (DENSE) gin.issue_end(d, 0xffu, tid + d * U * LG_THREADS, c.n_vec());
     S::commit();
   }
   const Row r = load_row(a, b);
@@ -921,7 +943,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   c.fill(a, call.shape, r, s_mem, s_scan);
 
   // the gradient of one score and, returned, the one before the repetition penalty
-  auto load = [&](uint32_t t) { return make_float2(Num<T>::get(x[t]), go ? Num<T>::get(go[t]) : 0.f); };
+  auto load = [&](uint32_t t) { return make_float2(Num<T>::get(x[t]), DENSE ? Num<T>::get(go[t]) : 0.f); };
   auto one = [&](uint32_t t, uint32_t times, uint32_t fb, float2 in) {
     float dz = 0.f, f = 1.f;
     if (c.allows(t)) {
@@ -952,11 +974,9 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
     S::wait();
     if (__any_sync(ALL, allowed != 0)) {
       float z[PER], d[PER];
-#pragma unroll
-      for (int u = 0; u < U; ++u) in.scores(stage, u, z + u * VEC);
-      if (go) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) gin.scores(stage, u, d + u * VEC);
+      in.template scores<false>(stage, z, 0);
+      if constexpr (DENSE) {
+        gin.template scores<false>(stage, d, 0);
 #pragma unroll
         for (int q = 0; q < PER; ++q) d[q] *= r.inv_t;
       } else {
@@ -988,7 +1008,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
             float p0, p1;
             e2.get(p0, p1);
             const Two p2 = sizeof(T) == 4 ? Two(ex2_small(p0), ex2_small(p1)) : Two(ex2(p0), ex2(p1));
-            fma2(cpt2, p2, Two(d[q], d[q + 1])).get(d[q], d[q + 1]);
+            (DENSE ? fma2(cpt2, p2, Two(d[q], d[q + 1])) : mul2(cpt2, p2)).get(d[q], d[q + 1]);
           }
         }
         if constexpr (factors) {
@@ -998,14 +1018,17 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
       };
       if (c.marked) slope(std::true_type());
       else slope(std::false_type());
+      uint32_t w[U][4];
+#pragma unroll
+      for (int q = 0; q < PER; q += 2) Num<T>::put_pair(w[q / VEC], q % VEC / 2, d[q], d[q + 1]);
       if (allowed != FULL) {
 #pragma unroll
-        for (int q = 0; q < PER; ++q)
-          if (!((allowed >> q) & 1u)) d[q] = 0.f;
+        for (int u = 0; u < U; ++u) hide<T>(w[u], allowed, u, 0u);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (step < whole || ii + u * LG_THREADS < n) store_vector(to + u * (LG_THREADS * VEC), d + u * VEC);
+        if (step < whole || ii + u * LG_THREADS < n)
+          __stcs(reinterpret_cast<uint4*>(to + u * (LG_THREADS * VEC)), make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]));
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -1016,11 +1039,11 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
     if (later < whole) {
       const uint32_t want = c.template wanted<SHIFTED>(i_later, true);
       in.issue(stage, want);
-      if (go) gin.issue(stage, want);
+      if (DENSE) gin.issue(stage, want);
     } else if (later < steps) {
       const uint32_t want = c.template wanted<SHIFTED>(i_later, false);
       in.issue_end(stage, want, i_later, n);
-      if (go) gin.issue_end(stage, want, i_later, n);
+      if (DENSE) gin.issue_end(stage, want, i_later, n);
     }
     S::commit();
     stage = stage + 1 == DEPTH ? 0 : stage + 1;
@@ -1141,8 +1164,11 @@ cudaError_t launch_forward(int dev, const LogitsCall& c, bool shifted, bool in_p
 }
 template <class T>
 cudaError_t launch_grad(int dev, const GradCall& c, bool shifted, unsigned ctas, size_t smem, cudaStream_t s) {
-  return shifted ? launch_clusters<k_logits_grad<T, true>>(dev, ctas, LG_THREADS, 1, smem, s, c)
-                 : launch_clusters<k_logits_grad<T, false>>(dev, ctas, LG_THREADS, 1, smem, s, c);
+  if (c.g.out)
+    return shifted ? launch_clusters<k_logits_grad<T, true, true>>(dev, ctas, LG_THREADS, 1, smem, s, c)
+                   : launch_clusters<k_logits_grad<T, false, true>>(dev, ctas, LG_THREADS, 1, smem, s, c);
+  return shifted ? launch_clusters<k_logits_grad<T, true, false>>(dev, ctas, LG_THREADS, 1, smem, s, c)
+                 : launch_clusters<k_logits_grad<T, false, false>>(dev, ctas, LG_THREADS, 1, smem, s, c);
 }
 
 int launched(tok_handle* h, cudaError_t e) {
