@@ -327,10 +327,12 @@ size_t mask_bytes(uint32_t n_logits, uint32_t groups) {
 }
 uint32_t share_of(const tok_handle* h, uint32_t ranks) { return ((h->tokens.n_groups + 31) / 32 + ranks - 1) / ranks * 32; }
 
-// CTAs of a row's cluster: as many as leave no SM without work, at least 4
+// CTAs of a row's cluster: about eight for each SM, at least 4 a row.  (128 rows
+// of one grammar, many in equal states: 25.2 us with 8 a row, 33.3 with 4; 473
+// rows in as many states: 60 us with 4, 79 with 8, 148 with 16, 61 with 2.)
 uint32_t mask_ranks(const tok_handle* h, uint32_t n, uint32_t n_logits) {
   uint32_t s = 16;
-  while (s > 4 && (unsigned long long)n * s > 4ull * (unsigned)h->n_sms && mask_bytes(n_logits, share_of(h, s / 2)) <= MOST_SHARED)
+  while (s > 4 && (unsigned long long)n * s > 8ull * (unsigned)h->n_sms && mask_bytes(n_logits, share_of(h, s / 2)) <= MOST_SHARED)
     s /= 2;
   return s;
 }
@@ -552,8 +554,12 @@ int tok_grammar_mask(tok_handle* h, const tok_grammar* g, const int32_t* d_state
   DeviceGuard dg(h->dev);
   MaskCall c{d_state, d_ids, reinterpret_cast<const long long*>(d_item_off), n, eos, d_state_out, n_logits, d_mask, mask_stride};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // many rows with tokens: their states first, once (each row's cluster looks at those of GR_THREADS rows)
-  if (!d_mask || (d_ids && d_state_out && n > 64)) {
+  // Each row's cluster finds the states of its window of GR_THREADS rows, unless
+  // they are found first, once, by a kernel of their own: for rows of one token
+  // each beyond a window (400 rows: 43 us with that kernel, 41 without; 1,000
+  // rows: 55 and 65; 4,000: 118 and 192), for rows of any number of tokens early
+  // (64 rows of 8 tokens: 37 and 35; of 100 tokens: 177 and 338).
+  if (!d_mask || (d_ids && d_state_out && n > (d_item_off ? 16u : (uint32_t)GR_THREADS))) {
     k_grammar_states<<<(n + 127) / 128, 128, 0, st>>>(g->g, h->tokens, c);
     h->launches += 1;
     const cudaError_t e = cudaGetLastError();

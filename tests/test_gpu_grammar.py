@@ -174,6 +174,30 @@ def test_every_state_of_a_trained_vocabulary(pkg):
     tok.close()
 
 
+@pytest.mark.parametrize("rows", [1, 16, 17, 40, 511, 512, 513, 1100])
+@pytest.mark.parametrize("several", [False, True])
+def test_states_and_masks_of_many_rows(pkg, rows, several):
+    # rows in one window and in several, with states found by the masks' own kernel or before it
+    import torch
+    rng = np.random.default_rng(rows)
+    toks = _vocab("prefixes")
+    tok = pkg.Tokenizer(toks, [], pkg.PATTERN_GPT2)
+    nxt, accept = _automaton("mixed", rng)
+    g = pkg.Grammar(tok, nxt, accept)
+    V = len(toks)
+    states = rng.integers(0, len(nxt), rows)
+    lens = rng.integers(0, 6, rows) if several else np.ones(rows, int)
+    off = np.concatenate([[0], np.cumsum(lens)])
+    ids = rng.integers(-1, 256, max(1, int(off[-1])))
+    got, m = _run(torch, pkg, g, states, ids, off if several else None, V, V + 1)
+    want = [_row_state(nxt, toks, int(s), ids[a:b].tolist(), V) for s, a, b in zip(states, off, off[1:])]
+    assert got.tolist() == want
+    masks = {s: _mask(nxt, accept, toks, s, V, V + 1) for s in set(want)}
+    assert np.array_equal(m, np.stack([masks[s] for s in want]))
+    g.close()
+    tok.close()
+
+
 def test_refusals(pkg):
     import torch
     tok = pkg.Tokenizer.from_merges([], pkg.PATTERN_GPT2)
