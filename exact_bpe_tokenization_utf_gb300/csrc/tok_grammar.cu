@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t row_state(const DevGrammar& g, const DevToke
   return s;
 }
 
-// The rows' states alone.
+// The rows' states alone: a thread walks a row, one load after another.
 __global__ void __launch_bounds__(128) k_grammar_states(DevGrammar g, DevTokens v, MaskCall c) {
   const uint32_t k = blockIdx.x * 128 + threadIdx.x;
   if (k >= c.n) return;
@@ -286,6 +286,13 @@ __device__ __forceinline__ uint2* list_behind(uint32_t* bits, uint32_t n_words) 
 // words that are not empty to the CTAs that write them, a share of the row
 // each.  Rows in equal states are walked once, by the first one's cluster,
 // which writes all of them.
+//
+// Bound by instructions and by the chains of lookups: 473 states of a grammar
+// over 100,257 tokens (47M decisions) in 57 us, issuing in 35% of all cycles,
+// of which the masks' 6 MB are 1 us; one row in 8.7 us, the launch 7 of them.  A
+// CTA per row, with rows that have many live groups finished in 16 parts by a
+// second kernel, took 49 us for those 473 states (clusters then 62) but 122
+// instead of 42 for 400 rows that share states.
 __global__ void __launch_bounds__(GR_THREADS, 3) k_grammar_mask(DevGrammar g, DevTokens v, MaskCall c) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint32_t s_mem[];

@@ -93,6 +93,11 @@ __device__ __forceinline__ bool completes(uint32_t* done, unsigned* sh) {
 // the sum over all of them and their checks decide (alike in every CTA)
 // whether the call goes through.  This redundant pass over 20 bytes a request
 // costs less than a second launch, or a CTA's wait for another's sums.
+//
+// Bound by the chain offsets - sums - table or stack entry - store, and in a
+// small call by the launch (7 us with its host side).  Measured: a decode step of
+// 64 requests 6.8 us, of 4,096 requests 10.3 us; a prefill of 64 requests with
+// 0.9M tokens 14.4 us (15 MB, 1.1 TB/s).
 template <int PER>
 __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_assign(PagedCall c) {
   const tok_paged_args& a = c.a;
@@ -298,7 +303,8 @@ __device__ __forceinline__ long long release_count(const ReleaseCall& c, uint32_
 }
 
 // One CTA takes a range of requests; as in k_paged_assign each CTA reads all
-// of them once for its base and for the checks.
+// of them once for its base and for the checks.  Bound like it; a quarter of
+// 1,000 requests of up to 20,011 tokens in blocks of 16 in 9.3 us.
 __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_release(ReleaseCall c) {
   __shared__ long long sh[64], s_cnt[PG_THREADS];
   __shared__ unsigned s_bad, s_last;
@@ -372,7 +378,9 @@ int tok_paged_assign(tok_handle* h, const tok_paged_args* a, void* stream) try {
   PagedCall c{};
   c.a = *a;
   // one token a thread while all of them fit two CTAs per SM (a decode step's
-  // tokens are of as many requests: one's loads would wait for another's), else four
+  // tokens are of as many requests: one's loads would wait for another's), else
+  // four.  4,096 requests of a token 10.8 us with one, 16.8 with four; prefills of
+  // 64 requests of up to 20,001 tokens 7.5 and 10.8, of up to 180,001 16.9 and 15.1.
   const unsigned threads = threads_for(std::max<unsigned long long>(a->n, a->cap));
   const bool one = a->cap <= 2ull * (unsigned)h->n_sms * threads;
   const long long tile = (long long)threads * (one ? 1 : 4);
