@@ -16,6 +16,8 @@ namespace tokgb {
 namespace {
 
 constexpr int PG_THREADS = 1024;                   // most threads of a CTA
+constexpr int PG_THREADS_4 = 256;                  // of one that takes four tokens a thread,
+constexpr int PG_CTAS_4 = 4;                       // and how many of those an SM runs at once (56 registers)
 constexpr int PG_MAX_LEN = 0x7fffffff;             // tokens of a request
 
 struct PagedCall {
@@ -96,12 +98,12 @@ __device__ __forceinline__ bool completes(uint32_t* done, unsigned* sh) {
 //
 // Bound by the chain offsets - sums - table or stack entry - store, and in a
 // small call by the launch (7 us with its host side).  Measured: a decode step of
-// 64 requests 6.8 us, of 4,096 requests 10.3 us; a prefill of 64 requests with
-// 0.9M tokens 14.4 us (15 MB, 1.1 TB/s).
+// 64 requests 6.6 us, of 4,096 requests 10.2 us; a prefill of 64 requests with
+// 0.9M tokens 10.8 us (15 MB, 1.4 TB/s).
 template <int PER>
-__global__ void __launch_bounds__(PG_THREADS, 1) k_paged_assign(PagedCall c) {
+__global__ void __launch_bounds__(PER == 1 ? PG_THREADS : PG_THREADS_4, PER == 1 ? 1 : PG_CTAS_4) k_paged_assign(PagedCall c) {
   const tok_paged_args& a = c.a;
-  constexpr int MOST = PG_THREADS * PER;
+  constexpr int MOST = (PER == 1 ? PG_THREADS : PG_THREADS_4) * PER;
   __shared__ long long sh[64];
   __shared__ unsigned s_bad, s_wide, s_kf, s_last;
   __shared__ int s_req[MOST], s_add[MOST + 1];
@@ -352,10 +354,10 @@ __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_release(ReleaseCall c) 
   }
 }
 
-// threads of a CTA for n things at a time: 128 to PG_THREADS
-unsigned threads_for(unsigned long long n) {
+// threads of a CTA for n things at a time: 128 to most
+unsigned threads_for(unsigned long long n, int most) {
   unsigned t = 128;
-  while (t < (unsigned)PG_THREADS && t < n) t *= 2;
+  while (t < (unsigned)most && t < n) t *= 2;
   return t;
 }
 
@@ -381,11 +383,17 @@ int tok_paged_assign(tok_handle* h, const tok_paged_args* a, void* stream) try {
   // tokens are of as many requests: one's loads would wait for another's), else
   // four.  4,096 requests of a token 10.8 us with one, 16.8 with four; prefills of
   // 64 requests of up to 20,001 tokens 7.5 and 10.8, of up to 180,001 16.9 and 15.1.
-  const unsigned threads = threads_for(std::max<unsigned long long>(a->n, a->cap));
+  // Threads of a CTA: many CTAs hide one another's latencies, but each reads every
+  // request.  One token a thread, 512 and 1,024 threads: 1,000 requests 7.5 and
+  // 8.5 us, 4,096 10.5 and 10.8, 15,000 25.0 and 18.9.  Four, 128, 256, 512 and
+  // 1,024: 64 long requests 10.8, 12.7, 13.8 and 15.1, 4,096 requests with 3.9M
+  // tokens 28.3 and 22.7 with the first two.
+  unsigned threads = threads_for(std::max<unsigned long long>(a->n, a->cap), a->n > 4096 ? PG_THREADS : 512);
   const bool one = a->cap <= 2ull * (unsigned)h->n_sms * threads;
+  if (!one) threads = a->n > 512 ? PG_THREADS_4 : 128;
   const long long tile = (long long)threads * (one ? 1 : 4);
   const long long tiles = std::max<long long>(1, ((long long)a->cap + tile - 1) / tile);
-  const long long ctas = std::min<long long>(tiles, 2ll * h->n_sms);
+  const long long ctas = std::min<long long>(tiles, (one ? 2u : PG_CTAS_4 * PG_THREADS_4 / threads) * (long long)h->n_sms);
   c.span = (tiles + ctas - 1) / ctas * tile;
   c.wide = ((reinterpret_cast<uintptr_t>(a->d_slot) | reinterpret_cast<uintptr_t>(a->d_pos) |
              reinterpret_cast<uintptr_t>(a->d_req)) & 15u) == 0;
@@ -428,7 +436,7 @@ int tok_paged_release(tok_handle* h, const int64_t* d_seq_len, const uint8_t* d_
   const uint32_t ctas = std::min<uint32_t>((n + 3) / 4, 2u * (uint32_t)h->n_sms);
   c.per = (n + ctas - 1) / ctas;
   c.done = d_n_free_out == d_n_free && ctas > 1 ? h->d_done : nullptr;
-  k_paged_release<<<ctas, std::min(512u, threads_for(n)), 0, static_cast<cudaStream_t>(stream)>>>(c);
+  k_paged_release<<<ctas, threads_for(n, 512), 0, static_cast<cudaStream_t>(stream)>>>(c);
   h->launches += 1;
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TOK_OK : cuda_fail(h, e, "kernel launch");
