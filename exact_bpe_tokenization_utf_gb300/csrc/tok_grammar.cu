@@ -84,11 +84,6 @@ __device__ __forceinline__ uint32_t load_once(const uint32_t* p) {
   asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(x) : "l"(p));
   return x;
 }
-__device__ __forceinline__ uint32_t load_once(const uint16_t* p) {
-  uint16_t x;
-  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(x) : "l"(p));
-  return x;
-}
 
 // a lane's token of a group whose common bytes lead to state s
 struct Item {
@@ -194,7 +189,9 @@ __device__ __forceinline__ void find_live(const DevGrammar& g, const DevTokens& 
 // bits: at once where no byte changes the state (inside a string that is most
 // groups), the others by a walk, two groups at a time with the next two on
 // their way.  Four bytes are looked up at once, as if the state stayed; where it
-// changes, the lookups after that are done again.
+// changes, the lookups after that are done again.  A token's leading bytes of one
+// kind are passed over where that kind does not change the state: the longest
+// tokens are runs, and a warp that walked them kept its CTA waiting.
 __device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& v, const uint2* live, uint32_t room,
                                           const uint32_t* n_live, uint32_t n_logits, uint32_t* bits) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
@@ -229,17 +226,22 @@ __device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& 
   Item now[2] = {load(warp), load(warp + W)};
   for (uint32_t e = warp; e < n_walk; e += 2 * W) {
     const Item next[2] = {load(e + 2 * W), load(e + 3 * W)};  // (used in the next turn: nothing waits for it here)
+    uint32_t from[2];  // the bytes of a word to be read: from here
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (!(now[h].kinds & now[h].leaves)) now[h].rest = 0;
-    for (uint32_t w = 0; __any_sync(0xffffffffu, (now[0].rest > w && now[0].s != DEAD) || (now[1].rest > w && now[1].s != DEAD));
-         w += 4) {
-      uint32_t ahead[2], from[2] = {0, 0}, to[2];  // the tokens' next words; the bytes of this word to be read
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t r = now[h].rest, skip = now[h].leaves >> (r >> 16 & 31u) & 1u ? 0u : r >> 21;
+      from[h] = skip & 3u;
+      now[h].rest = now[h].kinds & now[h].leaves ? (r & 0xffffu) - (skip & ~3u) : 0u;
+      now[h].at += 8 * (skip & ~3u);
+      if (skip > 3 && now[h].rest) now[h].word = load_once(v.words + now[h].at);
+    }
+    while (__any_sync(0xffffffffu, now[0].rest | now[1].rest)) {
+      uint32_t ahead[2], to[2];  // the tokens' next words; to here
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bool on = now[h].rest > w && now[h].s != DEAD;
-        ahead[h] = on && now[h].rest > w + 4 ? load_once(v.words + now[h].at + 8 * (w + 4)) : 0u;
-        to[h] = on ? min(now[h].rest - w, 4u) : 0u;
+        now[h].at += 32;
+        ahead[h] = now[h].rest > 4 ? load_once(v.words + now[h].at) : 0u;
+        to[h] = min(now[h].rest, 4u);
       }
       while (__any_sync(0xffffffffu, from[0] < to[0] || from[1] < to[1])) {
         uint32_t t[2][4];
@@ -258,8 +260,12 @@ __device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& 
           from[h] = now[h].s == DEAD ? to[h] : stop + 1;
         }
       }
-      now[0].word = ahead[0];
-      now[1].word = ahead[1];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        now[h].word = ahead[h];
+        now[h].rest = now[h].s == DEAD ? 0u : now[h].rest - to[h];
+        from[h] = 0;
+      }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -288,7 +294,7 @@ __device__ __forceinline__ uint2* list_behind(uint32_t* bits, uint32_t n_words) 
 // which writes all of them.
 //
 // Bound by instructions and by the chains of lookups: 473 states of a grammar
-// over 100,257 tokens (47M decisions) in 57 us, issuing in 35% of all cycles,
+// over 100,257 tokens (47M decisions) in 52 us, issuing in 35% of all cycles,
 // of which the masks' 6 MB are 1 us; one row in 8.7 us, the launch 7 of them.  A
 // CTA per row, with rows that have many live groups finished in 16 parts by a
 // second kernel, took 49 us for those 473 states (clusters then 62) but 122
@@ -367,6 +373,21 @@ uint32_t kinds_of(const uint8_t* s, uint32_t n) {
   return k;
 }
 
+// the bytes of one kind that a text begins with, sequences whole
+struct Run {
+  uint32_t kind, bytes;
+};
+Run first_run(const uint8_t* s, uint32_t n) {
+  Run r{0, 0};
+  while (r.bytes < n) {
+    const uint32_t seq = sequence(s + r.bytes, n - r.bytes), len = seq ? seq : 1, k = seq ? KIND_SEQUENCE : byte_kind(s[r.bytes]);
+    if ((r.bytes && k != r.kind) || r.bytes + len > MOST_RUN) break;
+    r.kind = k;
+    r.bytes += len;
+  }
+  return r;
+}
+
 // Whether every well-formed sequence of two bytes or more leads from state s
 // back to s.  (Answers no where more than a few states are on the way.)
 bool sequences_return(const int32_t* next, uint32_t s) {
@@ -409,8 +430,7 @@ int ensure_tokens(tok_handle* h) {
     return d ? d < 0 : la < lb;
   });
   std::vector<TokenGroup> group;
-  std::vector<uint32_t> words, id, kinds, group_kinds;
-  std::vector<uint16_t> rest;
+  std::vector<uint32_t> words, id, kinds, group_kinds, rest;
   for (uint32_t i = 0; i < n;) {
     uint32_t m = 1;
     while (m < 32 && i + m < n && *at(order[i + m]) == *at(order[i])) ++m;
@@ -435,7 +455,8 @@ int ensure_tokens(tok_handle* h) {
     for (uint32_t q = 0; q < 32; ++q) {
       id.push_back(q < m ? order[i + q] : NO_TOKEN);
       const uint32_t l = q < m ? len(order[i + q]) - p : 0u;
-      rest.push_back((uint16_t)l);
+      const Run run = q < m ? first_run(at(order[i + q]) + p, l) : Run{0, 0};
+      rest.push_back(l | run.kind << 16 | run.bytes << 21);
       for (uint32_t j = 0; j < l; ++j)
         words[r.at + (size_t)(j / 4) * 32 + q] |= (uint32_t)at(order[i + q])[p + j] << (8 * (j & 3));
       const uint32_t some = q < m ? kinds_of(at(order[i + q]) + p, l) : 0u;
@@ -454,7 +475,7 @@ int ensure_tokens(tok_handle* h) {
   constexpr int N_PARTS = 8;
   const void* part[N_PARTS] = {group.data(), words.data(), id.data(), kinds.data(), group_kinds.data(), off.data(), rest.data(), bytes};
   const size_t size[N_PARTS] = {group.size() * sizeof(TokenGroup), words.size() * 4, id.size() * 4, kinds.size() * 4,
-                              group_kinds.size() * 4, off.size() * 4, rest.size() * 2, nb};
+                              group_kinds.size() * 4, off.size() * 4, rest.size() * 4, nb};
   size_t place[N_PARTS + 1] = {0};
   for (int i = 0; i < N_PARTS; ++i) place[i + 1] = place[i] + (size[i] + 15) / 16 * 16;
   uint8_t* p = nullptr;
@@ -476,7 +497,7 @@ int ensure_tokens(tok_handle* h) {
   h->tokens.kinds = reinterpret_cast<const uint32_t*>(p + place[3]);
   h->tokens.group_kinds = reinterpret_cast<const uint32_t*>(p + place[4]);
   h->tokens.off = reinterpret_cast<const uint32_t*>(p + place[5]);
-  h->tokens.rest = reinterpret_cast<const uint16_t*>(p + place[6]);
+  h->tokens.rest = reinterpret_cast<const uint32_t*>(p + place[6]);
   h->tokens.bytes = p + place[7];
   h->tokens.n = n;
   h->tokens.n_groups = (uint32_t)group.size();

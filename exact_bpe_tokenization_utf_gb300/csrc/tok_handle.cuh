@@ -38,8 +38,9 @@ struct DevTokens {
   const uint32_t* id;
   const uint32_t* kinds;
   const uint32_t* group_kinds;
-  const uint16_t* rest;
+  const uint32_t* rest;   // bytes | kind of the first one << 16 | how many of that kind it begins with << 21
 };
+constexpr uint32_t MOST_RUN = 2047;  // of those
 
 // Kinds of bytes, such that what a grammar treats apart is often of different
 // kinds; well-formed UTF-8 sequences of several bytes are one of their own.
