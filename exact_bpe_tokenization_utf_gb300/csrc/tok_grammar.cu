@@ -87,7 +87,7 @@ __device__ __forceinline__ uint32_t load_once(const uint32_t* p) {
 
 // a lane's token of a group whose common bytes lead to state s
 struct Item {
-  uint32_t s, id, rest, at, word, kinds, leaves;
+  uint32_t s, place, rest, at, word, kinds;
 };
 
 // A row's window of GR_THREADS rows: its state, and the rows in equal states.
@@ -209,29 +209,29 @@ __device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& 
     for (uint32_t h = 0; h < 4; ++h) allow(id[h]);
   }
   auto load = [&](uint32_t f) {
-    Item t{DEAD, NO_TOKEN, 0, 0, 0, 0, 0};
+    Item t{DEAD, 0, 0, 0, 0, 0};
     if (f < n_walk) {  // (every group has a first word, so that these loads need not wait for one another)
       const uint2 e = live[f];
-      const uint32_t at = (e.x & 0xffffu) * 32 + lane;
       t.s = e.x >> 16;
+      t.place = (e.x & 0xffffu) * 32 + lane;
       t.at = e.y + lane;
-      t.id = load_once(v.id + at);
       t.word = load_once(v.words + t.at);
-      t.rest = load_once(v.rest + at);
-      t.kinds = load_once(v.kinds + at);
-      t.leaves = __ldg(g.leaves + t.s);
+      t.rest = load_once(v.rest + t.place);
+      t.kinds = load_once(v.kinds + t.place);
     }
     return t;
   };
   Item now[2] = {load(warp), load(warp + W)};
   for (uint32_t e = warp; e < n_walk; e += 2 * W) {
     const Item next[2] = {load(e + 2 * W), load(e + 3 * W)};  // (used in the next turn: nothing waits for it here)
-    uint32_t from[2];  // the bytes of a word to be read: from here
+    uint32_t id[2], from[2];  // the bytes of a word to be read: from here
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t r = now[h].rest, skip = now[h].leaves >> (r >> 16 & 31u) & 1u ? 0u : r >> 21;
+      id[h] = now[h].s != DEAD ? load_once(v.id + now[h].place) : NO_TOKEN;
+      const uint32_t leaves = now[h].s != DEAD ? __ldg(g.leaves + now[h].s) : 0u;
+      const uint32_t r = now[h].rest, skip = leaves >> (r >> 16 & 31u) & 1u ? 0u : r >> 21;
       from[h] = skip & 3u;
-      now[h].rest = now[h].kinds & now[h].leaves ? (r & 0xffffu) - (skip & ~3u) : 0u;
+      now[h].rest = now[h].kinds & leaves ? (r & 0xffffu) - (skip & ~3u) : 0u;
       now[h].at += 8 * (skip & ~3u);
       if (skip > 3 && now[h].rest) now[h].word = load_once(v.words + now[h].at);
     }
@@ -269,7 +269,7 @@ __device__ __forceinline__ void walk_live(const DevGrammar& g, const DevTokens& 
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (now[h].s != DEAD) allow(now[h].id);
+      if (now[h].s != DEAD) allow(id[h]);
       now[h] = next[h];
     }
   }
