@@ -340,12 +340,17 @@ size_t mask_bytes(uint32_t n_logits, uint32_t groups) {
 }
 uint32_t share_of(const tok_handle* h, uint32_t ranks) { return ((h->tokens.n_groups + 31) / 32 + ranks - 1) / ranks * 32; }
 
-// CTAs of a row's cluster: about eight for each SM, at least 4 a row.  (128 rows
-// of one grammar, many in equal states: 25.2 us with 8 a row, 33.3 with 4; 473
-// rows in as many states: 60 us with 4, 79 with 8, 148 with 16, 61 with 2.)
+// CTAs of a row's cluster, for the times of a vocabulary of 100,257 tokens with
+// 16, 8 and 4: 16 while that makes no more than four for each SM (32 rows of one
+// grammar 15.6, 16.5 and 16.5 us; 76 rows 22.7, 16.8 and 22.8), 8 while those
+// are no more than eight (120 rows, 8 and 4: 18.7 and 24.5), else 4 (473 rows in
+// as many states 51 us; with 8 about 75, with 16 about 140, with 2 61).  And 32
+// groups for each CTA (1,257 tokens, 60 rows: 16.5 us with 16, 10.2 with 4).
 uint32_t mask_ranks(const tok_handle* h, uint32_t n, uint32_t n_logits) {
+  const unsigned long long sms = (unsigned)h->n_sms;
   uint32_t s = 16;
-  while (s > 4 && (unsigned long long)n * s > 8ull * (unsigned)h->n_sms && mask_bytes(n_logits, share_of(h, s / 2)) <= MOST_SHARED)
+  while (s > 4 && ((unsigned long long)n * s > (s == 16 ? 4 : 8) * sms || h->tokens.n_groups < 32 * s) &&
+         mask_bytes(n_logits, share_of(h, s / 2)) <= MOST_SHARED)
     s /= 2;
   return s;
 }
