@@ -344,12 +344,13 @@ uint32_t share_of(const tok_handle* h, uint32_t ranks) { return ((h->tokens.n_gr
 // 16, 8 and 4: 16 while that makes no more than four for each SM (32 rows of one
 // grammar 15.6, 16.5 and 16.5 us; 76 rows 22.7, 16.8 and 22.8), 8 while those
 // are no more than eight (120 rows, 8 and 4: 18.7 and 24.5), else 4 (473 rows in
-// as many states 51 us; with 8 about 75, with 16 about 140, with 2 61).  And 32
-// groups for each CTA (1,257 tokens, 60 rows: 16.5 us with 16, 10.2 with 4).
+// as many states 51 us; before runs were passed over 60, and 79 with 8, 148 with
+// 16, 61 with 2).  And 64 groups for each CTA (1,257 tokens, us with 16, 8 and 4:
+// 60 rows 16.5, 10.5, 10.2; 120 rows 15.0 with 8, 10.4 with 4).
 uint32_t mask_ranks(const tok_handle* h, uint32_t n, uint32_t n_logits) {
   const unsigned long long sms = (unsigned)h->n_sms;
   uint32_t s = 16;
-  while (s > 4 && ((unsigned long long)n * s > (s == 16 ? 4 : 8) * sms || h->tokens.n_groups < 32 * s) &&
+  while (s > 4 && ((unsigned long long)n * s > (s == 16 ? 4 : 8) * sms || h->tokens.n_groups < 64 * s) &&
          mask_bytes(n_logits, share_of(h, s / 2)) <= MOST_SHARED)
     s /= 2;
   return s;
