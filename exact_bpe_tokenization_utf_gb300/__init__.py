@@ -56,11 +56,14 @@ class _Args(ctypes.Structure):
     as ints (e.g. tensor.data_ptr()) or None.  A program may keep one and pass
     it to every call; the buffers it names stay the caller's."""
 
+    def __init_subclass__(cls, **kw):
+        super().__init_subclass__(**kw)
+        cls._names = frozenset(n for n, _ in cls._fields_)
+
     def __init__(self, **fields):
+        if not self._names.issuperset(fields):
+            raise TypeError("%s has no field %s" % (type(self).__name__, ", ".join(sorted(set(fields) - self._names))))
         super().__init__(**fields)
-        unknown = set(fields) - {n for n, _ in self._fields_}
-        if unknown:
-            raise TypeError("%s has no field %s" % (type(self).__name__, ", ".join(sorted(unknown))))
         self._addr = ctypes.addressof(self)
 
 
