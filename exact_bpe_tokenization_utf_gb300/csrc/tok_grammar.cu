@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(GR_THREADS, 3) k_grammar_mask(DevGrammar g, De
   const Window win = look_around(g, v, c, k, s_row);
   if (tid == 0 && rank == 0 && c.state_out) c.state_out[k] = win.state == DEAD ? -1 : (int32_t)win.state;
   if (!win.first) return;  // (in every CTA of the cluster alike)
-  cluster_arrive();        // (waited for before another CTA's bits are set)
+  cluster_arrive();        // (waited for before another CTA's bits are set; they are 0 since the window's barriers)
   if (win.state != DEAD) {
     find_live(g, v, share, f, win.state, live, share.count(v), s_live);
     walk_live(g, v, live, share.count(v), s_live, c.n_logits, bits);
@@ -326,7 +326,9 @@ __global__ void __launch_bounds__(GR_THREADS, 3) k_grammar_mask(DevGrammar g, De
   if (s_live[0] | s_live[1])
     for (uint32_t w = tid; w < n_words; w += GR_THREADS)
       if (bits[w] && w / each != rank) atomicOr(cluster.map_shared_rank(bits, w / each) + w, bits[w]);
-  cluster.sync();
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
   const uint32_t w1 = min((rank + 1) * each, n_words);
   for (uint32_t w = rank * each + tid; w < w1; w += GR_THREADS) {
     const uint32_t m = with_eos(g, c, win.state, w, bits[w]);

@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
   const tok_logits_args& a = call.a;
   const cg::cluster_group cluster = cg::this_cluster();
   const uint32_t rank = cluster.block_rank(), n_ranks = cluster.num_blocks();
-  if (n_ranks > 1) cluster_arrive();  // (waited for before another CTA's shared memory is written)
+  if (n_ranks > 1) cluster_arrive_only();  // (waited for before another CTA's shared memory is written)
   const uint32_t b = blockIdx.x / n_ranks, tid = threadIdx.x, lane = tid & 31u;
   const T* x = static_cast<const T*>(a.d_logits) + (long long)b * a.logits_stride;
   T* out = a.d_out ? static_cast<T*>(a.d_out) + (long long)b * a.out_stride : nullptr;
@@ -1118,8 +1118,11 @@ __global__ void __launch_bounds__(SB_THREADS) k_seen_bits(const int32_t* ids, co
       if (v[j] < n_logits && !(*static_cast<volatile uint32_t*>(s_bits + (v[j] >> 5)) & bit)) atomicOr(&s_bits[v[j] >> 5], bit);
     }
   }
-  if (n_ranks > 1) cluster.sync();
-  else __syncthreads();
+  __syncthreads();
+  if (n_ranks > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
   uint32_t* row = seen + (long long)b * stride;
   const uint32_t share = (words + n_ranks - 1) / n_ranks, w1 = min((rank + 1) * share, words);
   for (uint32_t w = rank * share + threadIdx.x; w < w1; w += SB_THREADS) {
@@ -1129,7 +1132,10 @@ __global__ void __launch_bounds__(SB_THREADS) k_seen_bits(const int32_t* ids, co
       for (uint32_t q = 0; q < n_ranks; ++q) m |= cluster.map_shared_rank(s_bits, q)[w];
     row[w] = m;
   }
-  if (n_ranks > 1) cluster.sync();  // (until the others have read this CTA's bits)
+  if (n_ranks > 1) {  // until the others have read this CTA's bits
+    cluster_arrive_only();
+    cluster_wait();
+  }
 }
 
 size_t stage_bytes(int dtype, bool shifted) {

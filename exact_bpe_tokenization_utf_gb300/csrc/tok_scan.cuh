@@ -28,8 +28,16 @@ __device__ __forceinline__ T block_excl_sum(T v, T* total, T* sh) {
   return pre + inc - v;
 }
 
-// the two halves of a cluster's barrier
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// The two halves of a cluster's barrier.  Only the first warp releases: what it
+// wrote, and what the other warps wrote before a barrier of the CTA that lies
+// between, is seen by the cluster; a release in each warp would wait for the
+// warp's own stores, results that no other CTA reads among them.
+__device__ __forceinline__ void cluster_arrive() {
+  if (threadIdx.x < 32) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+// without what anyone wrote: others' reads and their start are waited for
+__device__ __forceinline__ void cluster_arrive_only() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 }  // namespace tokgb
