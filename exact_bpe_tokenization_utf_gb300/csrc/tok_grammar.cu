@@ -294,7 +294,7 @@ __device__ __forceinline__ uint2* list_behind(uint32_t* bits, uint32_t n_words) 
 // which writes all of them.
 //
 // Bound by instructions and by the chains of lookups: 473 states of a grammar
-// over 100,257 tokens (47M decisions) in 50 us, issuing in 40% of all cycles,
+// over 100,257 tokens (47M decisions) in 49 us, issuing in 43% of all cycles,
 // of which the masks' 6 MB are 1 us; one row in 8 to 12 us, the launch 7 of them.  A
 // CTA per row, with rows that have many live groups finished in 16 parts by a
 // second kernel, took 49 us for those 473 states (clusters then 62) but 122

@@ -14,10 +14,10 @@
 // Both directions are one pass over the scores, which reads and writes each
 // once.  What bounds it is not the bytes but the issue of instructions and what
 // a CTA does besides: for 512 rows of 100,257 bf16 scores with seen sets and
-// lists of 2,000 ids on a GB300, 31 us of bytes, 49.7M warp instructions (39 us
+// lists of 2,000 ids on a GB300, 31 us of bytes, 48.7M warp instructions (39 us
 // if one were issued in every cycle) and 74 us measured.  Without rules a score
 // takes 13 instructions of its thread; a seen set adds 6, rows of the input and
-// the output that lie differently towards 16 bytes add 3.  The row's scalars,
+// the output that lie differently towards 16 bytes add 3 or fewer.  The row's scalars,
 // bits and listed tokens take a CTA 8 to 15 us before its first step and after
 // its last, which the SM's other CTAs overlap in part.
 #include <cooperative_groups.h>
