@@ -76,10 +76,11 @@ __device__ __forceinline__ void block_sums(long long& a, long long& b, long long
 }
 
 // true in one CTA of the grid: the one that gets here last (done is 0 again
-// then), or without a counter the first one
+// then), or without a counter the first one.  Either way all of its threads are
+// here: in place, what is written next is what the others of them read.
 __device__ __forceinline__ bool completes(uint32_t* done, unsigned* sh) {
-  if (!done) return blockIdx.x == 0;
   __syncthreads();
+  if (!done) return blockIdx.x == 0;
   if (threadIdx.x == 0) {
     __threadfence();
     const bool last = atomicAdd(done, 1u) == gridDim.x - 1;

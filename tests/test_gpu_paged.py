@@ -160,6 +160,18 @@ def test_assign_in_place_repeats(env):
     assert np.array_equal(c.host("ctx"), ctx) and tok._L.tok_last_error(tok._h) is not None
 
 
+@pytest.mark.parametrize("tokens,empty", [(128, 0), (256, 0), (512, 0), (128, 2), (512, 400), (1024, 4500)])
+def test_assign_in_place_by_one_cta(env, tokens, empty):
+    # one request brings all the tokens of a call that a single CTA takes, with no padding (a chunk of a
+    # prefill), and its length is replaced by the same CTA
+    torch, pkg, tok = env
+    for seed in range(20):
+        new, ctx = [0] * empty + [tokens] + [0] * empty, [1] * empty + [17 + seed] + [5] * empty
+        c = _Call(torch, pkg, new, ctx, 16, spare=0, pad=0, seed=seed)
+        tok.paged_assign_device(c.args(d_n_free_out=c.d["n_free"].data_ptr(), d_seq_len=c.d["ctx"].data_ptr()))
+        c.check(n_free="n_free", seq="ctx")
+
+
 @pytest.mark.parametrize("n", [3, 2000])
 def test_assign_refuses_on_the_device(env, n):
     torch, pkg, tok = env
