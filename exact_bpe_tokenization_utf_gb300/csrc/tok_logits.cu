@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   if (gr.lse || gr.logprob) lse = a.d_lse[b];
   if (fabsf(lse) >= 1e36f) cp = lse = 0.f;  // (nothing but -inf or a type's lowest value)
   uint32_t pick = a.d_pick ? (uint32_t)a.d_pick[b] : 0xffffffffu;
-  if ((int32_t)pick < 0 && gr.logprob) pick = (uint32_t)a.d_top[b];
+  if ((int32_t)pick < 0 && gr.logprob) pick = a.d_top ? (uint32_t)a.d_top[b] : 0xffffffffu;
   const double kd = 1.4426950408889634 / (a.d_temperature ? (double)a.d_temperature[b] : 1.0);
   const double ld = (double)lse * 1.4426950408889634 - (sizeof(T) == 4 ? 0.0 : 24.0);
   const float k = (float)kd, k_lo = (float)(kd - (double)k), lh = (float)ld, l_lo = (float)(ld - (double)lh);

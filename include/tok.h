@@ -378,7 +378,8 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream);
 
 /* tok_logits_backward -- the gradient of tok_logits_process.  a: the same
  * arguments as the forward call; of its outputs d_lse is read, and d_top
- * where a row's pick is negative (d_out and d_logprob are not used).  With
+ * where a row's pick is negative (d_top NULL: no v is such a row's pick; d_out
+ * and d_logprob are not used).  With
  *   dy[v] = grad_out[v] + (grad_lse - grad_logprob) * exp(y[v] - lse) + (v == pick) * grad_logprob
  * and 0 where the mask hides v,
  *   grad_logits[v] = dy[v] / temperature * (the factor of the repetition penalty on v: 1, 1 / repetition or repetition)
@@ -397,7 +398,8 @@ typedef struct {
 } tok_logits_grad_args;
 
 /* Errors: as tok_logits_process; TOK_EINVAL if d_lse is missing where
- * grad_lse or grad_logprob is given, or d_top where a pick may be the top. */
+ * grad_lse or grad_logprob is given, or both d_pick and d_top where
+ * grad_logprob is. */
 int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logits_grad_args* g, void* stream);
 
 /* tok_grammar_load -- a byte automaton over the vocabulary of h, for token

@@ -485,6 +485,27 @@ def test_gradient_ignores_what_the_mask_hides(env):
     _check_grad(c)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [33, 1000, 50_257])
+def test_gradient_of_negative_picks_without_a_top(env, V, kind):
+    # padded rows: a pick of -1 and no d_top, so that no token is the row's pick
+    torch, pkg, tok = env
+    for dense in (True, False):
+        c = _Case(torch, 5, V, kind, 13, gen=20, mask=[0.9, 1.0], seen=True)
+        c.pick[[0, 1, 3]] = [-1, -1, -2**31]
+        c._put(pick=c.pick)
+        _grad_inputs(c, 14, dense)
+        args = c.args(pkg, out=False)
+        tok.process_logits_device(args)
+        args.d_top = None
+        c.d["gx"] = torch.full((c.rows, c.V), 7.0, dtype=c.type, device="cuda")
+        tok.process_logits_backward_device(args, pkg.LogitsGradArgs(
+            d_grad_out=c.p("go") if dense else None, grad_out_stride=V, d_grad_lse=c.p("glse"), d_grad_logprob=c.p("glp"),
+            d_grad_logits=c.p("gx"), grad_logits_stride=V))
+        c.d["top"].fill_(-1)
+        _check_grad(c)
+
+
 def test_gradient_against_differences(env):
     # L = sum(grad_out * y) + grad_lse * lse + grad_logprob * logprob in 64 bits, central differences of step h:
     # the error is h^2 times a third derivative (at most about 10 / T^3) and 2^-52 |L| / h
