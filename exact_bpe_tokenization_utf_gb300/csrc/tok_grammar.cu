@@ -555,6 +555,9 @@ int tok_grammar_load(tok_handle* h, const int32_t* next, const uint8_t* accept, 
   e = cudaMemcpy(g->d_mem, t.data(), tb, cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemcpy(g->d_mem + tb, leaves.data(), lb, cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemcpy(g->d_mem + tb + lb, accept, n_states, cudaMemcpyHostToDevice);
+  // (a copy from pageable memory may return with its last part still on its way, the vocabulary's copies above
+  // too, and a caller's stream need not wait for the default one)
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
   if (e != cudaSuccess) {
     cudaFree(g->d_mem);
     delete g;

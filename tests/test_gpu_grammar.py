@@ -198,6 +198,31 @@ def test_states_and_masks_of_many_rows(pkg, rows, several):
     tok.close()
 
 
+def test_masks_right_after_the_load(pkg):
+    # on a stream that does not wait for the default one, with work queued there: the tables are complete all the same
+    import torch
+    toks = _vocab("prefixes")
+    V = len(toks)
+    s = torch.cuda.Stream()
+    states = torch.arange(700, dtype=torch.int32, device="cuda")
+    words = -(-V // 32)
+    busy = torch.zeros(1 << 26, device="cuda")
+    for seed in range(6):
+        nxt, accept = _automaton("many", np.random.default_rng(seed))
+        m = torch.full((700, words), -9, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        tok = pkg.Tokenizer(toks, [], pkg.PATTERN_GPT2)
+        busy.add_(1.0)
+        g = pkg.Grammar(tok, nxt, accept)
+        g.mask_device(states.data_ptr(), None, None, 700, -1, None, V, m.data_ptr(), words, s.cuda_stream)
+        s.synchronize()
+        got = m.cpu().numpy()
+        for k in range(seed, 700, 97):
+            assert np.array_equal(got[k], _mask(nxt, accept, toks, k, -1, V)), (seed, k)
+        g.close()
+        tok.close()
+
+
 def test_refusals(pkg):
     import torch
     tok = pkg.Tokenizer.from_merges([], pkg.PATTERN_GPT2)
