@@ -489,6 +489,8 @@ int tok_load(const uint8_t* vocab_bytes, const uint64_t* vocab_off, uint32_t n_v
   if (e == cudaSuccess) e = cudaMemcpy(h->d_tok_len, tok_len.data(), n_vocab * 2, cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemcpy(h->d_max_left, max_left.data(), n_vocab * 2, cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemcpy(h->d_max_right, max_right.data(), n_vocab * 2, cudaMemcpyHostToDevice);
+  // (the counter's zero and the last of the copies may still be on their way, and no other stream waits for them)
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
   if (e == cudaSuccess) e = cudaMallocHost(reinterpret_cast<void**>(&h->h_status), sizeof(DevStatus));
   if (e == cudaSuccess) e = cudaMallocHost(reinterpret_cast<void**>(&h->h_ustatus), 4 * sizeof(long long));
   if (e == cudaSuccess) e = cudaHostGetDevicePointer(reinterpret_cast<void**>(&h->d_ustatus), h->h_ustatus, 0);

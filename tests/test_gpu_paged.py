@@ -172,6 +172,23 @@ def test_assign_in_place_by_one_cta(env, tokens, empty):
         c.check(n_free="n_free", seq="ctx")
 
 
+def test_in_place_right_after_the_load(env):
+    # a handle's counter of finished CTAs is 0 for the first call, on a stream that does not wait for the default one
+    torch, pkg, _ = env
+    s = torch.cuda.Stream()
+    busy = torch.zeros(1 << 26, device="cuda")
+    n = 1500
+    for seed in range(6):
+        c = _Call(torch, pkg, [1] * n, [7] * n, 4, seed=seed)
+        torch.cuda.synchronize()
+        busy.add_(1.0)
+        tok = pkg.Tokenizer.from_merges([], pkg.PATTERN_GPT2)
+        tok.paged_assign_device(c.args(d_n_free_out=c.d["n_free"].data_ptr(), d_seq_len=c.d["ctx"].data_ptr()), s.cuda_stream)
+        s.synchronize()
+        c.check(n_free="n_free", seq="ctx")
+        tok.close()
+
+
 @pytest.mark.parametrize("n", [3, 2000])
 def test_assign_refuses_on_the_device(env, n):
     torch, pkg, tok = env
