@@ -528,11 +528,10 @@ __device__ __forceinline__ float score(const Row& r, uint32_t v, uint32_t c, uin
     x = __fsub_rn(x, r.pres);
   }
   if ((fb & NO_BIAS) != NO_BIAS) {
-    float s = r.bias[fb & NO_BIAS];
-    if (fb >> 31)  // more than one entry: their sum in the list's order
+    x = __fadd_rn(x, r.bias[fb & NO_BIAS]);
+    if (fb >> 31)  // more than one entry: one after another, in the list's order
       for (int i = (int)(fb & NO_BIAS) + 1; i < r.bias_n; ++i)
-        if ((uint32_t)r.bias_id[i] == v) s = __fadd_rn(s, r.bias[i]);
-    x = __fadd_rn(x, s);
+        if ((uint32_t)r.bias_id[i] == v) x = __fadd_rn(x, r.bias[i]);
   }
   return x;
 }

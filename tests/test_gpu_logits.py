@@ -273,6 +273,30 @@ def test_bias_over_the_whole_row(env):
     _run(env, c).check()
 
 
+@pytest.mark.parametrize("V", [50, 5000])
+def test_biases_are_added_in_the_lists_order(env, V):
+    # ((x + b1) + b2) + ... in 32 bits, bit for bit: large values of both signs on the same few tokens
+    torch = env[0]
+    c = _Case(torch, 3, V, "f32", 15, bias=120, strengths=False)
+    rng = np.random.default_rng(15)
+    for b in range(3):
+        ids, vals = c.bias[b]
+        few = rng.random(len(ids)) < 0.7
+        ids[few] = rng.integers(0, 5, int(few.sum()))
+        vals[:] = (vals * 2.0 ** rng.integers(0, 26, len(vals))).astype(np.float32)
+    c.bias[0][0][:3], c.bias[0][1][:3] = [7, 7, 7], [2.0 ** 24, -2.0 ** 24, 3.0]
+    c.d["logits"][0, 7] = c.x[0, 7] = 1.0
+    want = c.x.copy()
+    for b in range(3):
+        for i, v in zip(*c.bias[b]):
+            if 0 <= i < V:
+                want[b, i] += v
+    c._put(bias_id=np.concatenate([i for i, _ in c.bias]).astype(np.int32), bias=np.concatenate([v for _, v in c.bias]))
+    _run(env, c)
+    assert np.array_equal(c.d["out"].cpu().numpy(), want)
+    assert c.d["top"].cpu().tolist() == want.argmax(1).tolist()
+
+
 def test_masked_places_are_not_looked_at(env):
     torch = env[0]
     for kind in ("f32", "f16", "bf16"):
