@@ -44,7 +44,13 @@ constexpr int PER = 16;           // scores per thread and step
 constexpr int EDGE = 16;          // places before a slice's first vector, for the scores that come before it (fewer)
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float REF_MAX = 1e37f;  // references of a sum of exponentials stay within this
+// References of a sum of exponentials stay within this: up to there z k lies no
+// more than half a spacing (32) above a reference that was rounded from it, and
+// no sum overflows below the largest reference.  Y_MAX: from here on (in natural
+// units, well within REF_MAX) scores are 32 apart or more, and so is what 32 bits
+// tell apart of their log-sum-exp: the largest score is all of it.
+constexpr float REF_MAX = 0x1p30f;
+constexpr float Y_MAX = 0x1p29f;
 
 template <class T> struct Num;
 template <> struct Num<float> {
@@ -898,8 +904,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
     }
     const bool nan = sum != sum;
     const float z_top = key_score(key), y_top = z_top * r.inv_t;
-    // beyond the references' range all of the sum is its largest term
-    const float lse = nan ? sum : fabsf(y_top) < 1e36f ? LN2 * (ref + log2f(sum)) : y_top;
+    const float lse = nan ? sum : fabsf(y_top) < Y_MAX ? LN2 * (ref + log2f(sum)) : y_top;
     if (a.d_top) a.d_top[b] = nan || !key ? -1 : (int32_t)(0xffffffffu - (uint32_t)key);
     if (a.d_lse) a.d_lse[b] = lse;
     if (a.d_logprob) {

@@ -328,6 +328,46 @@ def test_special_logits(env, value):
             _run(env, c, out=False).check(out=False)
 
 
+@pytest.mark.parametrize("temp", [1.0, 1e-9, 1e-3])
+@pytest.mark.parametrize("value", [-1e35, -1e30, -1e15, -1e10, -3e9, -7e8, -4e8, 4e8, 7e8, 3e9, 1e10, 1e20, 1.0])
+def test_scores_far_from_0(env, value, temp):
+    # rows of one large value (a mask that was added to the scores), of large ones that differ, and ordinary ones
+    # over a small temperature.  The bounds are the module's, with the errors of those scores alone that carry weight
+    # (within 60 of the largest: a row has fewer than 2^20 others)
+    torch, pkg, tok = env
+    for kind in ("f32", "bf16"):
+        for V in (5, 70, 9000, 60_000):
+            rng = np.random.default_rng(2)
+            x = rng.normal(0, 1, (5, V)).astype(np.float32)
+            x[0, V // 2] = value
+            x[1] = value
+            x[2] = value
+            x[2, V - 1] = 1.5
+            x[3] *= np.float32(value)
+            c = _Case(torch, 5, V, kind, 6, logits=x, strengths=False)
+            c.temp[:] = temp
+            c.pick[:] = [V - 1, 0, 0, -1, -1]
+            c._put(pick=c.pick, temperature=c.temp)
+            _run(env, c)
+            top, lse, logprob = (c.d[k].cpu().numpy() for k in ("top", "lse", "logprob"))
+            for b in range(5):
+                z, _, S = c.row(b)
+                y, E = z / float(c.temp[b]), 10 * U * S / float(c.temp[b])
+                assert top[b] == int(np.argmax(c.row(b, np.float32)[0]))
+                m = y.max()
+                want = m + math.log(np.exp(y - m).sum())
+                tol = E[y >= m - 60].max() + 21 * 2.0 ** -22 + (V / 128 + 40) * U + 2 * U * abs(want)
+                at = int(c.pick[b]) if c.pick[b] >= 0 else int(top[b])
+                with np.errstate(all="ignore"):  # (what 32 bits do not hold is infinite)
+                    y32, want32 = np.float32(y[at]), np.float32(want)
+                if np.isinf(y32) or np.isinf(want32):
+                    assert np.isfinite(want32) or lse[b] == want32, (kind, V, b)
+                    assert logprob[b] == -np.inf if y32 < np.inf else np.isnan(logprob[b]), (kind, V, b)
+                    continue
+                assert abs(lse[b] - want) <= tol, (kind, V, b, lse[b], want)
+                assert abs(logprob[b] - (y[at] - want)) <= 2 * tol + E[at] + 2 * U * (abs(y[at]) + abs(want)), (kind, V, b)
+
+
 def test_ties_go_to_the_lowest_token(env):
     torch = env[0]
     for V in (100, 6001, 100_257):
