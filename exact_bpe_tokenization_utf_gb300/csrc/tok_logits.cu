@@ -964,6 +964,9 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   const double ld = (double)lse * 1.4426950408889634 - (sizeof(T) == 4 ? 0.0 : 24.0);
   const float k = (float)kd, k_lo = (float)(kd - (double)k), lh = (float)ld, l_lo = (float)(ld - (double)lh);
   const float cpt = cp * r.inv_t * (sizeof(T) == 4 ? 1.f : 0x1p-24f);
+  // the second part of a 32-bit exponent; where z is -inf or z k overflows, the first part is -inf and this one
+  // may be +inf or no number: it is kept finite
+  auto second = [](float x) { return fminf(x, FLT_MAX); };
   if (rank == 0 && gr.bias)
     for (int i = tid; i < r.bias_n; i += LG_THREADS)
       if ((uint32_t)r.bias_id[i] >= a.n_logits) gr.bias[(r.bias - a.d_bias) + i] = 0.f;
@@ -979,8 +982,8 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
       if (seen || times) f = xt > 0.f ? r.inv_rep : r.rep;
       dz = in.y * r.inv_t;
       if (cpt != 0.f) {
-        const float z = fmaxf(score(r, t, times, fb, seen, xt), -FLT_MAX);  // (-inf times k_lo is no number)
-        dz = fmaf(cpt, sizeof(T) == 4 ? ex2_small(fmaf(z, k, -lh) + fmaf(z, k_lo, -l_lo)) : ex2(fmaf(z, k, -lh)), dz);
+        const float z = score(r, t, times, fb, seen, xt);
+        dz = fmaf(cpt, sizeof(T) == 4 ? ex2_small(fmaf(z, k, -lh) + second(fmaf(z, k_lo, -l_lo))) : ex2(fmaf(z, k, -lh)), dz);
       }
       if (t == pick) dz = fmaf(glp, r.inv_t, dz);
     }
@@ -1025,14 +1028,13 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
         if (cpt != 0.f) {
 #pragma unroll
           for (int q = 0; q < PER; q += 2) {
-            if (sizeof(T) == 4) {  // (-inf times k_lo is no number)
-              z[q] = fmaxf(z[q], -FLT_MAX);
-              z[q + 1] = fmaxf(z[q + 1], -FLT_MAX);
-            }
             const Two z2(z[q], z[q + 1]);
             Two e2 = fma2(z2, k2, lh2);
-            if (sizeof(T) == 4) e2 = add2(e2, fma2(z2, klo2, llo2));
             float p0, p1;
+            if (sizeof(T) == 4) {
+              fma2(z2, klo2, llo2).get(p0, p1);
+              e2 = add2(e2, Two(second(p0), second(p1)));
+            }
             e2.get(p0, p1);
             const Two p2 = sizeof(T) == 4 ? Two(ex2_small(p0), ex2_small(p1)) : Two(ex2(p0), ex2(p1));
             (DENSE ? fma2(cpt2, p2, Two(d[q], d[q + 1])) : mul2(cpt2, p2)).get(d[q], d[q + 1]);

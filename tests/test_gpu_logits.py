@@ -570,6 +570,24 @@ def test_gradient_of_negative_picks_without_a_top(env, V, kind):
         _check_grad(c)
 
 
+@pytest.mark.parametrize("temp", [1.1e-8, 1.3e-8, 1e30, 1e37])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_gradient_of_the_lowest_scores_at_any_temperature(env, kind, temp):
+    # scores of -inf and of a type's lowest value next to a single 0: no NaN, whatever they are multiplied by
+    torch = env[0]
+    for V in (5, 40, 9001):
+        x = np.full((2, V), -np.inf, np.float32)
+        x[:, 1::3] = -3.38e38
+        x[0, V // 2] = x[1, V - 1] = 0
+        c = _Case(torch, 2, V, kind, 16, logits=x, strengths=False, gen=4)
+        c.temp[:] = temp
+        c._put(temperature=c.temp)
+        for dense in (True, False):
+            _grad_inputs(c, 17, dense)
+            _backward(env, c, dense)
+            _check_grad(c)
+
+
 def test_gradient_against_differences(env):
     # L = sum(grad_out * y) + grad_lse * lse + grad_logprob * logprob in 64 bits, central differences of step h:
     # the error is h^2 times a third derivative (at most about 10 / T^3) and 2^-52 |L| / h
