@@ -51,6 +51,9 @@ constexpr float LN2 = 0.6931471805599453f;
 // tell apart of their log-sum-exp: the largest score is all of it.
 constexpr float REF_MAX = 0x1p30f;
 constexpr float Y_MAX = 0x1p29f;
+// From here on the rounding of an lse is 2^-4 or more, and exp(y - lse) only makes
+// sense with the y that lse was formed from, rounded alike.
+constexpr float Y_FAR = 0x1p20f;
 
 template <class T> struct Num;
 template <> struct Num<float> {
@@ -903,8 +906,8 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call)
       z_pick = fmaxf(z_pick, s_part[q].z_pick);
     }
     const bool nan = sum != sum;
-    const float z_top = key_score(key), y_top = z_top * r.inv_t;
-    const float lse = nan ? sum : fabsf(y_top) < Y_MAX ? LN2 * (ref + log2f(sum)) : y_top;
+    const float z_top = key_score(key), y_top = __fmul_rn(z_top, r.inv_t);
+    const float lse = nan ? sum : fabsf(y_top) < Y_MAX ? __fadd_rn(y_top, LN2 * (log2f(sum) - fmaf(z_top, k, -ref))) : y_top;
     if (a.d_top) a.d_top[b] = nan || !key ? -1 : (int32_t)(0xffffffffu - (uint32_t)key);
     if (a.d_lse) a.d_lse[b] = lse;
     if (a.d_logprob) {
@@ -958,6 +961,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   float cp = (gr.lse ? gr.lse[b] : 0.f) - glp, lse = 0.f;
   if (gr.lse || gr.logprob) lse = a.d_lse[b];
   if (fabsf(lse) >= 1e36f) cp = lse = 0.f;  // (nothing but -inf or a type's lowest value)
+  const bool far = fabsf(lse) >= Y_FAR;     // (a masked row, or next to no temperature: every score is taken one by one)
   uint32_t pick = a.d_pick ? (uint32_t)a.d_pick[b] : 0xffffffffu;
   if ((int32_t)pick < 0 && gr.logprob) pick = a.d_top ? (uint32_t)a.d_top[b] : 0xffffffffu;
   const double kd = 1.4426950408889634 / (a.d_temperature ? (double)a.d_temperature[b] : 1.0);
@@ -983,19 +987,23 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
       dz = in.y * r.inv_t;
       if (cpt != 0.f) {
         const float z = score(r, t, times, fb, seen, xt);
-        dz = fmaf(cpt, sizeof(T) == 4 ? ex2_small(fmaf(z, k, -lh) + second(fmaf(z, k_lo, -l_lo))) : ex2(fmaf(z, k, -lh)), dz);
+        float e;
+        if (far) e = fmaf(fminf(__fsub_rn(__fmul_rn(z, r.inv_t), lse), 0.f), LOG2E, sizeof(T) == 4 ? 0.f : 24.f);
+        else e = sizeof(T) == 4 ? fmaf(z, k, -lh) + second(fmaf(z, k_lo, -l_lo)) : fmaf(z, k, -lh);
+        dz = fmaf(cpt, sizeof(T) == 4 ? ex2_small(e) : ex2(e), dz);
       }
       if (t == pick) dz = fmaf(glp, r.inv_t, dz);
     }
     gx[t] = Num<T>::put(dz * f);
     return dz;
   };
-  if (tid < 32) {  // the scores outside the vectors
-    const uint32_t t = c.outside(tid);
+  // the scores outside the vectors (fewer than 32), or all of them
+  for (uint32_t i = tid, some = far ? c.to - c.from : 32u; i < some; i += LG_THREADS) {
+    const uint32_t t = far ? c.from + i : c.outside(i);
     if (t != 0xffffffffu && !(c.lists && listed(c.table, t))) one(t, 0, NO_BIAS, load(t));
   }
   const Two k2(k, k), lh2(-lh, -lh), klo2(k_lo, k_lo), llo2(-l_lo, -l_lo), cpt2(cpt, cpt);
-  const uint32_t n = c.n_vec(), steps = (n + U * LG_THREADS - 1) / (U * LG_THREADS), whole = n / (U * LG_THREADS);
+  const uint32_t n = far ? 0u : c.n_vec(), steps = (n + U * LG_THREADS - 1) / (U * LG_THREADS), whole = n / (U * LG_THREADS);
   T* to = gx + c.v0 + (c.i_begin + tid) * VEC;
   uint32_t stage = 0, ii = tid;
 #pragma unroll 1

@@ -385,7 +385,9 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream);
  *   grad_logits[v] = dy[v] / temperature * (the factor of the repetition penalty on v: 1, 1 / repetition or repetition)
  *   grad_bias[i]   = dy[bias_id[i]] / temperature (0 for an id that was skipped)
  * A row with an lse of -inf, or beyond 1e36 (nothing but a type's lowest
- * values), gets no gradient through it.
+ * values), gets no gradient through it.  From 2^20 on, where an lse is rounded
+ * by 2^-4 or more, y is rounded as in the forward pass and exp(y - lse) is at
+ * most 1.
  */
 typedef struct {
   const void* d_grad_out;       /* as out, of the logits' type; NULL: 0 */

@@ -588,6 +588,60 @@ def test_gradient_of_the_lowest_scores_at_any_temperature(env, kind, temp):
             _check_grad(c)
 
 
+@pytest.mark.parametrize("value", [-1e35, -1e30, -1e15, -1e10, -3e9, -1e8, -2e7, 4e6, 1e8, 1e10, 1e20])
+def test_gradient_of_scores_far_from_0(env, value):
+    # At a temperature of 1 y is the logit itself.  exp(y - lse) is off by the roundings of the difference and of its
+    # product with log2(e) (3 u |d|) and by ex2's 2^-22; it is at most 1 where lse, rounded, lies below the largest y.
+    # The sum of the terms and its product are 6 roundings more, then the type's own.
+    torch = env[0]
+    for kind in ("f32", "bf16"):
+        unit, tiny = ROUND[kind]
+        for V in (5, 70, 9000, 60_000):
+            rng = np.random.default_rng(2)
+            x = rng.normal(0, 1, (4, V)).astype(np.float32)
+            x[0] = value
+            x[1, V // 2] = abs(value)
+            x[2, 1:] = value
+            x[3] *= np.float32(value)
+            c = _Case(torch, 4, V, kind, 6, logits=x, strengths=False)
+            for dense in (True, False):
+                _grad_inputs(c, 18, dense)
+                _backward(env, c, dense)
+                gx, lse, top = (c.d[k].double().cpu().numpy() for k in ("gx", "lse", "top"))
+                for b in range(4):
+                    d = np.minimum(c.x[b].astype(np.float64) - lse[b], 0.0)
+                    p, hit = np.exp(d), np.zeros(V)
+                    hit[int(c.pick[b] if c.pick[b] >= 0 else top[b])] = float(c.glp[b])
+                    cp = float(np.float32(c.glse[b]) - np.float32(c.glp[b]))
+                    want = c.go[b] + cp * p + hit
+                    size = np.abs(c.go[b]) + np.abs(cp) * p + np.abs(hit)
+                    rel = 3 * U * np.abs(d) + 2.0 ** -22
+                    if abs(lse[b]) < 2**20:
+                        rel += 2 * U * (abs(lse[b]) + np.abs(c.x[b]))
+                    err = np.abs(cp) * p * np.minimum(rel, 1.0) + 6 * U * size
+                    assert (np.abs(gx[b] - want) <= err + unit * np.abs(want) * 1.01 + tiny + 2.0 ** -126).all(), (kind, V, b)
+
+
+@pytest.mark.parametrize("temp", [1e-9, 1e-7])
+def test_gradient_at_next_to_no_temperature(env, temp):
+    # the largest score, and each one equal to it, has a weight of 1: lse is its y, rounded as exp's argument is
+    torch, pkg, tok = env
+    for kind in ("f32", "f16", "bf16"):
+        for V in (33, 9000, 60_000):
+            c = _Case(torch, 4, V, kind, 19, gen=20, bias=5, seen=True)
+            c.temp[:] = temp
+            c.rep[:] = 1.25 if temp < 1e-8 else 1.0
+            c._put(temperature=c.temp, repetition=c.rep)
+            _grad_inputs(c, 20, False)
+            c._put(glp=0 * c.glp, glse=np.full(4, temp, np.float32))
+            _backward(env, c, False)
+            gx, top = c.d["gx"].double().cpu().numpy(), c.d["top"].cpu().numpy()
+            for b in range(4):
+                z32 = c.row(b, np.float32)[0]
+                want = np.where(z32 == z32[top[b]], c.row(b)[1], 0.0)
+                assert (np.abs(gx[b] - want) <= 2.0 ** -7 * want + 2.0 ** -24).all(), (kind, V, b)
+
+
 def test_gradient_against_differences(env):
     # L = sum(grad_out * y) + grad_lse * lse + grad_logprob * logprob in 64 bits, central differences of step h:
     # the error is h^2 times a third derivative (at most about 10 / T^3) and 2^-52 |L| / h
