@@ -431,8 +431,7 @@ class Grammar:
             self._tok._check(rc)
 
     def close(self):
-        # (a tokenizer that was closed first has no device left to free on)
-        if self._g and getattr(self._tok, "_h", None):
+        if self._g:   # (its tokenizer may have been closed before it)
             self._L.tok_grammar_free(self._g)
         self._g = None
 

@@ -518,7 +518,8 @@ int ensure_tokens(tok_handle* h) {
 using namespace tokgb;
 
 struct tok_grammar {
-  tok_handle* h = nullptr;
+  const tok_handle* h = nullptr;  // compared, not read: the grammar may outlive it
+  int dev = 0;
   DevGrammar g{};
   uint8_t* d_mem = nullptr;
 };
@@ -564,6 +565,7 @@ int tok_grammar_load(tok_handle* h, const int32_t* next, const uint8_t* accept, 
     return cuda_fail(h, e, "grammar: copy");
   }
   g->h = h;
+  g->dev = h->dev;
   g->g = DevGrammar{reinterpret_cast<const uint16_t*>(g->d_mem), reinterpret_cast<const uint32_t*>(g->d_mem + tb),
                     g->d_mem + tb + lb, n_states};
   *out = g;
@@ -574,7 +576,7 @@ int tok_grammar_load(tok_handle* h, const int32_t* next, const uint8_t* accept, 
 
 void tok_grammar_free(tok_grammar* g) {
   if (!g) return;
-  DeviceGuard dg(g->h->dev);
+  DeviceGuard dg(g->dev);
   cudaFree(g->d_mem);
   delete g;
 }

@@ -408,8 +408,8 @@ int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logit
  * masks.  next (host): n_states rows of 256 int32, the state after each byte,
  * -1 where the byte is not allowed.  accept (host, n_states): whether the text
  * may end there.  n_states is 1 .. 65535.  The first call on a handle lays out the
- * vocabulary's bytes on the device.  A grammar belongs to h: free it, with
- * tok_grammar_free, before h.
+ * vocabulary's bytes on the device.  A grammar is used with h alone; free it,
+ * with tok_grammar_free, before h or after it.
  * Errors: TOK_EINVAL (NULL, n_states or a next state out of range),
  * TOK_ENOMEM, TOK_ECUDA. */
 typedef struct tok_grammar tok_grammar;

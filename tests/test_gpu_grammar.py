@@ -223,6 +223,22 @@ def test_masks_right_after_the_load(pkg):
         tok.close()
 
 
+def test_a_grammar_may_outlive_its_tokenizer(pkg):
+    # closed in either order, none keeps its automaton (31 MB here) on the device
+    import torch
+    nxt, acc = np.zeros((60_000, 256), np.int32), np.ones(60_000, np.uint8)
+    free = []
+    for k in range(8):
+        tok = pkg.Tokenizer.from_merges([], pkg.PATTERN_GPT2)
+        g = pkg.Grammar(tok, nxt, acc)
+        for x in (tok, g) if k % 2 else (g, tok):
+            x.close()
+        g.close()
+        torch.cuda.synchronize()
+        free.append(torch.cuda.mem_get_info()[0])
+    assert free[-1] > free[1] - (15 << 20), free
+
+
 def test_refusals(pkg):
     import torch
     tok = pkg.Tokenizer.from_merges([], pkg.PATTERN_GPT2)
