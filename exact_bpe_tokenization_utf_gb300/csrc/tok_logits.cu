@@ -1254,8 +1254,8 @@ extern "C" {
 
 int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream) try {
   if (!h) return TOK_EINVAL;
+  if (a && a->rows == 0) return TOK_OK;  // (an empty batch's buffers are often NULL)
   if (const char* w = check_logits(a)) return fail(h, TOK_EINVAL, w);
-  if (a->rows == 0) return TOK_OK;
   DeviceGuard g(h->dev);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   LogitsCall c{};
@@ -1277,6 +1277,7 @@ int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream) tr
 
 int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logits_grad_args* ga, void* stream) try {
   if (!h) return TOK_EINVAL;
+  if (a && a->rows == 0) return TOK_OK;
   if (const char* w = check_logits(a)) return fail(h, TOK_EINVAL, w);
   if (!ga || !ga->d_grad_logits) return fail(h, TOK_EINVAL, "logits: the gradient's arguments or buffer are NULL");
   if (ga->grad_logits_stride < (int64_t)a->n_logits || (ga->d_grad_out && ga->grad_out_stride < (int64_t)a->n_logits))
@@ -1285,7 +1286,6 @@ int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logit
     return fail(h, TOK_EINVAL, "logits: the gradient of lse or logprob needs the forward pass's lse");
   if (ga->d_grad_logprob && !a->d_top && !a->d_pick)
     return fail(h, TOK_EINVAL, "logits: the gradient of logprob needs the picks or the forward pass's top");
-  if (a->rows == 0) return TOK_OK;
   DeviceGuard gd(h->dev);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   GradCall c{};

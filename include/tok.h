@@ -373,7 +373,7 @@ typedef struct {
 
 /* Errors: TOK_EINVAL (NULL or missing buffers, an unknown type, n_logits out
  * of range, a stride below a row, out the logits with another stride),
- * TOK_ECUDA.  rows == 0 does nothing. */
+ * TOK_ECUDA.  rows == 0 does nothing, whatever the buffers. */
 int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream);
 
 /* tok_logits_backward -- the gradient of tok_logits_process.  a: the same

@@ -724,6 +724,23 @@ def test_in_place_with_another_stride(env, rows):
         assert np.array_equal(c.d["logits"].cpu().numpy(), c.x)
 
 
+def test_no_rows(env):
+    # a batch of no rows as tensors have it: their addresses are NULL
+    torch, pkg, tok = env
+    f = torch.empty((0, 100), device="cuda")
+    none = torch.empty(0, dtype=torch.int64, device="cuda")
+    off = torch.zeros(1, dtype=torch.int64, device="cuda")
+    shared = torch.zeros(5, dtype=torch.int32, device="cuda")
+    assert f.data_ptr() == none.data_ptr() == 0
+    before = tok.launch_count
+    args = pkg.LogitsArgs(d_logits=f.data_ptr(), logits_stride=100, d_out=f.data_ptr(), out_stride=100, rows=0, n_logits=100,
+                          d_gen=shared.data_ptr(), d_gen_start=none.data_ptr(), d_gen_len=none.data_ptr(),
+                          d_bias_off=off.data_ptr(), d_bias_id=none.data_ptr(), d_bias=f.data_ptr())
+    tok.process_logits_device(args)
+    tok.process_logits_backward_device(args, pkg.LogitsGradArgs(d_grad_logits=f.data_ptr(), grad_logits_stride=100))
+    assert tok.launch_count == before
+
+
 # --- refusals, seen bits -----------------------------------------------------
 
 def test_refusals(env):
