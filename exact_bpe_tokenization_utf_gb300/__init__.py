@@ -407,11 +407,16 @@ class Tokenizer:
 
 class Grammar:
     """A byte automaton over a tokenizer's vocabulary (a tok_grammar): next is
-    [n_states, 256], -1 where a byte is not allowed; accept is [n_states]."""
+    [n_states, 256], -1 where a byte is not allowed; accept is [n_states],
+    0 or not."""
 
     def __init__(self, tok, next_state, accept):
-        nxt = np.ascontiguousarray(next_state, dtype=np.int32)
-        acc = np.ascontiguousarray(accept, dtype=np.uint8)
+        given = np.asarray(next_state)
+        with np.errstate(invalid="ignore"):
+            nxt = np.ascontiguousarray(given, dtype=np.int32)
+        if given.dtype != np.int32 and not np.array_equal(nxt, given):
+            raise ValueError("next holds 32-bit whole numbers")
+        acc = np.ascontiguousarray(np.asarray(accept) != 0, dtype=np.uint8)
         if nxt.ndim != 2 or nxt.shape[1] != 256 or acc.shape != nxt.shape[:1]:
             raise ValueError("next is [n_states, 256] and accept [n_states]")
         g = ctypes.c_void_p()
