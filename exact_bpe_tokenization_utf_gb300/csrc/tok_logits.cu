@@ -1227,12 +1227,17 @@ int launched(tok_handle* h, cudaError_t e) {
   return e == cudaSuccess ? TOK_OK : cuda_fail(h, e, "kernel launch");
 }
 
+// (addresses come without a type: one that no score can have would fault on the device)
+bool lies_at_scores(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % size_of(dtype) == 0; }
+
 // nullptr, or what is wrong with the arguments
 const char* check_logits(const tok_logits_args* a) {
   if (!a || !a->d_logits) return "logits: the arguments or the logits are NULL";
   if (a->dtype != TOK_F32 && a->dtype != TOK_F16 && a->dtype != TOK_BF16) return "logits: unknown type";
   if (a->n_logits == 0 || a->n_logits > MAX_LOGITS) return "logits: n_logits is out of range";
   if (a->rows > 0x7ffffffu) return "logits: too many rows";
+  if (!lies_at_scores(a->d_logits, a->dtype) || !lies_at_scores(a->d_out, a->dtype))
+    return "logits: an array does not lie at a multiple of its type's size";
   const int64_t n = a->n_logits, words = (n + 31) / 32;
   if (a->logits_stride < n || (a->d_out && a->out_stride < n)) return "logits: a row stride is below n_logits";
   if ((a->d_seen && a->seen_stride < words) || (a->d_mask && a->mask_stride < words))
@@ -1280,6 +1285,8 @@ int tok_logits_backward(tok_handle* h, const tok_logits_args* a, const tok_logit
   if (a && a->rows == 0) return TOK_OK;
   if (const char* w = check_logits(a)) return fail(h, TOK_EINVAL, w);
   if (!ga || !ga->d_grad_logits) return fail(h, TOK_EINVAL, "logits: the gradient's arguments or buffer are NULL");
+  if (!lies_at_scores(ga->d_grad_logits, a->dtype) || !lies_at_scores(ga->d_grad_out, a->dtype))
+    return fail(h, TOK_EINVAL, "logits: an array does not lie at a multiple of its type's size");
   if (ga->grad_logits_stride < (int64_t)a->n_logits || (ga->d_grad_out && ga->grad_out_stride < (int64_t)a->n_logits))
     return fail(h, TOK_EINVAL, "logits: a row stride is below n_logits");
   if ((ga->d_grad_lse || ga->d_grad_logprob) && !a->d_lse)

@@ -371,8 +371,9 @@ typedef struct {
   float* d_logprob;
 } tok_logits_args;
 
-/* Errors: TOK_EINVAL (NULL or missing buffers, an unknown type, n_logits out
- * of range, a stride below a row, out the logits with another stride),
+/* Errors: TOK_EINVAL (NULL or missing buffers, an unknown type, scores that do
+ * not lie at a multiple of their type's size, n_logits out of range, a stride
+ * below a row, out the logits with another stride),
  * TOK_ECUDA.  rows == 0 does nothing, whatever the buffers. */
 int tok_logits_process(tok_handle* h, const tok_logits_args* a, void* stream);
 

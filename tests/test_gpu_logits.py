@@ -724,6 +724,24 @@ def test_in_place_with_another_stride(env, rows):
         assert np.array_equal(c.d["logits"].cpu().numpy(), c.x)
 
 
+@pytest.mark.parametrize("kind,by", [("f32", 1), ("f32", 2), ("f32", 3), ("f16", 1), ("bf16", 1)])
+def test_scores_between_two_places_are_refused(env, kind, by):
+    torch, pkg, tok = env
+    c = _Case(torch, 3, 100, kind, 1)
+    args = c.args(pkg)
+    ga = dict(d_grad_out=c.p("logits"), grad_out_stride=100, d_grad_logits=c.p("out"), grad_logits_stride=100)
+    calls = [lambda: tok.process_logits_device(c.args(pkg, d_logits=c.p("logits") + by)),
+             lambda: tok.process_logits_device(c.args(pkg, d_out=c.p("out") + by))]
+    for k in ("d_grad_out", "d_grad_logits"):
+        calls.append(lambda k=k: tok.process_logits_backward_device(args, pkg.LogitsGradArgs(**{**ga, k: ga[k] + by})))
+    for call in calls:
+        with pytest.raises(pkg.TokError) as e:
+            call()
+        assert e.value.code == pkg.TOK_EINVAL and "multiple" in str(e.value)
+    torch.cuda.synchronize()
+    assert (c.d["out"] == 7.0).all()
+
+
 def test_no_rows(env):
     # a batch of no rows as tensors have it: their addresses are NULL
     torch, pkg, tok = env
