@@ -124,14 +124,15 @@ def _peaks():
 
 
 def _sources_hash():
-    """SHA-256 of the sources of the encode kernels, comments and whitespace
-    removed (their DRAM counters stay valid across comment edits, not across
-    code changes; host code and other kernels do not touch them)."""
+    """SHA-256 of the sources that an encode runs (its kernels, and the host
+    code that sets their grids), comments and whitespace removed: the DRAM
+    counters stay valid across comment edits, not across code changes.  Only
+    the operators beside the encode are left out."""
     import re
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "exact_bpe_tokenization_utf_gb300", "csrc")
     for f in sorted(os.listdir(csrc)):
-        if f.endswith(".inc") or f in ("tok_common.cuh", "tok_pretok.cu", "tok_bpe.cu", "tok_emit.cu"):
+        if f.endswith((".cu", ".cuh", ".inc")) and f not in ("tok_paged.cu", "tok_logits.cu", "tok_grammar.cu", "tok_scan.cuh"):
             with open(os.path.join(csrc, f), encoding="utf-8", errors="replace") as fh:
                 text = fh.read()
             text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
