@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(PER == 1 ? PG_THREADS : PG_THREADS_4, PER == 1
     const unsigned first = min(s_bad, s_wide);
     *a.d_n_free_out = code == ST_OK ? n_free - total : n_free;
     a.d_status[0] = code;
-    a.d_status[1] = total;
+    a.d_status[1] = code == TOK_EINVAL ? 0 : total;
     a.d_status[2] = n_tok;
     a.d_status[3] = first == 0xffffffffu ? -1 : (long long)first;
   }
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_release(ReleaseCall c) 
   if (tid == 0) {
     *c.n_free_out = code == ST_OK ? n_free + total : n_free;
     c.status[0] = code;
-    c.status[1] = total;
+    c.status[1] = code == TOK_EINVAL ? 0 : total;
     c.status[2] = 0;
     c.status[3] = s_bad == 0xffffffffu ? -1 : (long long)s_bad;
   }

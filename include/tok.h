@@ -261,10 +261,10 @@ int tok_pretokenize_device_noalloc(int pattern_id, const uint8_t* d_text, uint64
  * status (device int64[4]): [0] = TOK_OK, TOK_EINVAL (item_off not from 0 or
  *   decreasing, a negative length or free count, 2^31 tokens or more in a
  *   request) or TOK_EBUF (cap below the token count, a row of the table too
- *   narrow, too few free blocks); [1] = blocks taken (TOK_EBUF: needed);
- *   [2] = tokens; [3] = the first request that does not fit, or -1.  On an
- *   error no block is taken: the table stays, slot, pos and req are -1,
- *   n_free_out = n_free, seq_len = ctx_len.
+ *   narrow, too few free blocks); [1] = blocks taken (TOK_EBUF: needed,
+ *   TOK_EINVAL: 0); [2] = tokens; [3] = the first request that does not fit, or
+ *   -1.  On an error no block is taken: the table stays, slot, pos and req are
+ *   -1, n_free_out = n_free, seq_len = ctx_len.
  */
 typedef struct {
   const int64_t* d_item_off; /* n + 1 */
@@ -297,8 +297,8 @@ int tok_paged_assign(tok_handle* h, const tok_paged_args* a, void* stream);
  * n_free_out may be d_n_free itself.  status (device int64[4]): [0] = TOK_OK,
  * TOK_EINVAL (a negative length or free count, a length beyond the table's
  * row) or TOK_EBUF (more than free_cap entries); [1] = blocks returned
- * (TOK_EBUF: that would have been); [2] = 0; [3] = the first bad request, or
- * -1.  On an error nothing is returned and n_free_out = n_free.
+ * (TOK_EBUF: that would have been, TOK_EINVAL: 0); [2] = 0; [3] = the first
+ * bad request, or -1.  On an error nothing is returned and n_free_out = n_free.
  * Two calls on one handle must not overlap on the GPU.
  * Errors: as tok_paged_assign. */
 int tok_paged_release(tok_handle* h, const int64_t* d_seq_len, const uint8_t* d_done, uint32_t n,

@@ -283,6 +283,25 @@ def test_release(env, n, most, bs, share, in_place):
         assert d["n_free" if in_place else "out"].cpu().tolist() == [10]
 
 
+@pytest.mark.parametrize("n", [3, 2000])
+def test_bad_numbers_count_no_blocks(env, n):
+    # status[1] is what was taken or returned, and what is lacking only where that is the error
+    torch, pkg, tok = env
+    c = _Call(torch, pkg, [2] * n, [3] * n, 4)
+    c.d["ctx"][1] = c.ctx[1] = -1
+    tok.paged_assign_device(c.args())
+    assert c.check_refused(pkg.TOK_EINVAL, 1)[1] == 0
+    d = {k: torch.full((m,), v, dtype=t, device="cuda") for k, m, v, t in (
+        ("lens", n, 5, torch.int64), ("done", n, 1, torch.uint8), ("free", 4 * n, -9, torch.int32), ("n_free", 1, 0, torch.int64),
+        ("out", 1, -7, torch.int64), ("status", 4, -7, torch.int64))}
+    d["lens"][2] = -1
+    tok.paged_release_device(d["lens"].data_ptr(), d["done"].data_ptr(), n, 4, c.d["table"].data_ptr(), c.table.shape[1],
+                             c.max_blocks, d["free"].data_ptr(), 4 * n, d["n_free"].data_ptr(), d["out"].data_ptr(),
+                             d["status"].data_ptr())
+    assert d["status"].cpu().tolist() == [pkg.TOK_EINVAL, 0, 0, 2]
+    assert d["out"].cpu().tolist() == [0] and bool((d["free"] == -9).all())
+
+
 def test_refusals_on_the_host(env):
     torch, pkg, tok = env
     c = _Call(torch, pkg, [2, 3], [1, 1], 4)
