@@ -293,9 +293,10 @@ __device__ __forceinline__ uint2* list_behind(uint32_t* bits, uint32_t n_words) 
 // each.  Rows in equal states are walked once, by the first one's cluster,
 // which writes all of them.
 //
-// Bound by instructions and by the chains of lookups: 473 states of a grammar
-// over 100,257 tokens (47M decisions) in 49 us, issuing in 43% of all cycles,
-// of which the masks' 6 MB are 1 us; one row in 8 to 12 us, the launch 7 of them.  A
+// Bound by barriers and by the chains of lookups (every row's cluster looks at
+// all groups, whatever its state allows): 473 states of a grammar over 100,257
+// tokens (47M decisions) in 49 us, issuing in 43% of all cycles, of which the
+// masks' 6 MB are 1 us; one row in 8 to 12 us, the launch 7 of them.  A
 // CTA per row, with rows that have many live groups finished in 16 parts by a
 // second kernel, took 49 us for those 473 states (clusters then 62) but 122
 // instead of 42 for 400 rows that share states.
@@ -343,12 +344,13 @@ size_t mask_bytes(uint32_t n_logits, uint32_t groups) {
 uint32_t share_of(const tok_handle* h, uint32_t ranks) { return ((h->tokens.n_groups + 31) / 32 + ranks - 1) / ranks * 32; }
 
 // CTAs of a row's cluster, for the times of a vocabulary of 100,257 tokens with
-// 16, 8 and 4: 16 while that makes no more than four for each SM (32 rows of one
-// grammar 15.6, 16.5 and 16.5 us; 76 rows 22.7, 16.8 and 22.8), 8 while those
-// are no more than eight (120 rows, 8 and 4: 18.7 and 24.5), else 4 (473 rows in
-// as many states 51 us; before runs were passed over 60, and 79 with 8, 148 with
-// 16, 61 with 2).  And 64 groups for each CTA (1,257 tokens, us with 16, 8 and 4:
-// 60 rows 16.5, 10.5, 10.2; 120 rows 15.0 with 8, 10.4 with 4).
+// 16, 8 and 4: 16 while that makes no more than four for each SM (a row 10.3, 10.4
+// and 10.4 us; 32 rows of one grammar 15.6, 16.5 and 16.5 or, of another, 22.7,
+// 18.5 and 22.7; 76 rows 32.2, 21.6 and 26.7), 8 while those are no more than
+// eight (120 rows 40.3, 23.6 and 22.7), else 4 (400 rows 101, 50 and 33, with two
+// 41; 473 rows in as many states 138, 69 and 50.6, with two 50.2).  And 64 groups
+// for each CTA (1,257 tokens: 60 rows 20.6, 12.3 and 10.3; 120 rows 32.1, 16.8 and
+// 11.6).
 uint32_t mask_ranks(const tok_handle* h, uint32_t n, uint32_t n_logits) {
   const unsigned long long sms = (unsigned)h->n_sms;
   uint32_t s = 16;
@@ -597,9 +599,10 @@ int tok_grammar_mask(tok_handle* h, const tok_grammar* g, const int32_t* d_state
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Each row's cluster finds the states of its window of GR_THREADS rows, unless
   // they are found first, once, by a kernel of their own: for rows of one token
-  // each beyond a window (400 rows: 43 us with that kernel, 41 without; 1,000
-  // rows: 55 and 65; 4,000: 118 and 192), for rows of any number of tokens early
-  // (64 rows of 8 tokens: 37 and 35; of 100 tokens: 177 and 338).
+  // each beyond a window (1,000 rows: 50 us with that kernel, 66 without; 4,000:
+  // 158 and 245; 400 rows, which are one window, 43 and 41 in one grammar, 29 and
+  // 33 in another), for rows of any number of tokens early (64 rows of 8 tokens:
+  // 35 and 34; of 100 tokens: 176 and 341).
   if (!d_mask || (d_ids && d_state_out && n > (d_item_off ? 16u : (uint32_t)GR_THREADS))) {
     k_grammar_states<<<(n + 127) / 128, 128, 0, st>>>(g->g, h->tokens, c);
     h->launches += 1;

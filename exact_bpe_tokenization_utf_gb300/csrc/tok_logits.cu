@@ -12,14 +12,16 @@
 // type once, when it is written.
 //
 // Both directions are one pass over the scores, which reads and writes each
-// once.  What bounds it is not the bytes but the issue of instructions and what
-// a CTA does besides: for 512 rows of 100,257 bf16 scores with seen sets and
-// lists of 2,000 ids on a GB300, 31 us of bytes, 48.7M warp instructions (39 us
-// if one were issued in every cycle) and 74 us measured.  Without rules a score
-// takes 13 instructions of its thread; a seen set adds 6, rows of the input and
-// the output that lie differently towards 16 bytes add 3 or fewer.  The row's scalars,
-// bits and listed tokens take a CTA 8 to 15 us before its first step and after
-// its last, which the SM's other CTAs overlap in part.
+// once.  What bounds it is neither the bytes nor the issue of instructions alone:
+// for 512 rows of 100,257 bf16 scores with seen sets and lists of 2,000 ids on a
+// GB300, 32 us of bytes, 48.7M warp instructions (39 us if one were issued in
+// every cycle) and 74 us measured, with instructions issued in 54% of all cycles
+// and DRAM at 29%.  The row's scalars, bits and listed tokens take a CTA 8 to 15
+// us before its first step and after its last, which do not overlap its own
+// scores, and the SM's other CTAs' only in part.  Of those 30 instructions of a
+// thread for each score the main pass has 22 or fewer: 13 without rules, 6 for a
+// seen set, up to 3 where the input's rows and the output's lie differently
+// towards 16 bytes.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -35,7 +37,7 @@ namespace {
 
 constexpr uint32_t MAX_LOGITS = 1u << 20;
 // 256 threads, 3 CTAs per SM (80 registers).  Six CTAs of 128 threads: one row
-// 13.7 us against 11.6, 512 rows 90 against 86, 2,048 rows' gradient 163 against 160.
+// 12.0 us against 10.3, 64 rows 21.3 against 18.4, 512 rows 75.2 against 73.6.
 constexpr int LG_THREADS = 256;
 constexpr int LG_CTAS = 3;        // per SM, where shared memory has room for them
 constexpr int SB_THREADS = 512;   // of k_seen_bits
@@ -706,10 +708,10 @@ struct LogitsCall {
 // definition's divisions, so that the choice is exact.  IN_PLACE: out is logits.
 //
 // Measured, with all rules on unless stated: one row of 100,257 bf16 scores
-// 10.6 us (the launch is 7); 64 rows of 50,257 f16 scores 18.4 us; 200 rows of
+// 10.3 us (the launch is 7); 64 rows of 50,257 f16 scores 18.4 us; 200 rows of
 // 100,257 f32 scores, half of them masked and nothing written, 28.1 us (2.9 TB/s of
 // logits); 512 rows of 100,257 bf16 scores, no mask, 74 us (2.9 TB/s read and
-// written), issuing in 54% of all cycles.
+// written).
 template <class T, bool SHIFTED, bool IN_PLACE>
 __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits(LogitsCall call) {
   namespace cg = cooperative_groups;
@@ -925,8 +927,8 @@ struct GradCall {
 };
 
 // Gradient: slices as in k_logits, but independent CTAs.  Measured: 2,048 rows of
-// 50,257 bf16 scores with masks, seen sets and lists of 2,047 ids in 129 us (3.4
-// TB/s read and written), issuing in 53% of all cycles.  exp(y - lse) is
+// 50,257 bf16 scores with masks, seen sets and lists of 2,047 ids in 130 us (3.4
+// TB/s read and written), issuing in 53% of all cycles, DRAM at 37%.  exp(y - lse) is
 // 2^-24 exp2(z k - lse log2(e) + 24): what is scaled by the gradient and the
 // temperature is not lost below 2^-126.  For 32-bit gradients k and lse
 // log2(e) are sums of two numbers each (their rounding would weigh |y| times

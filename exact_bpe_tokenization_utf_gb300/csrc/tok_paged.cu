@@ -99,8 +99,9 @@ __device__ __forceinline__ bool completes(uint32_t* done, unsigned* sh) {
 //
 // Bound by the chain offsets - sums - table or stack entry - store, and in a
 // small call by the launch (7 us with its host side).  Measured: a decode step of
-// 64 requests 6.6 us, of 4,096 requests 10.2 us; a prefill of 64 requests with
-// 0.9M tokens 10.8 us (15 MB, 1.4 TB/s).
+// 64 requests 6.5 us, of 4,096 requests 10.2 us (in place, with the counter of
+// finished CTAs, 12.4); a prefill of 64 requests with 0.9M tokens 10.3 to 11.2 us
+// (15 MB, 1.4 TB/s).
 template <int PER>
 __global__ void __launch_bounds__(PER == 1 ? PG_THREADS : PG_THREADS_4, PER == 1 ? 1 : PG_CTAS_4) k_paged_assign(PagedCall c) {
   const tok_paged_args& a = c.a;
@@ -306,8 +307,9 @@ __device__ __forceinline__ long long release_count(const ReleaseCall& c, uint32_
 }
 
 // One CTA takes a range of requests; as in k_paged_assign each CTA reads all
-// of them once for its base and for the checks.  Bound like it; a quarter of
-// 1,000 requests of up to 20,011 tokens in blocks of 16 in 9.3 us.
+// of them once for its base and for the checks.  Bound like it, and by a CTA's
+// requests being copied one after another; a quarter of 1,000 requests of up to
+// 20,011 tokens in blocks of 16 in 8.7 to 12.6 us, in place the same.
 __global__ void __launch_bounds__(PG_THREADS, 1) k_paged_release(ReleaseCall c) {
   __shared__ long long sh[64], s_cnt[PG_THREADS];
   __shared__ unsigned s_bad, s_last;
@@ -382,13 +384,12 @@ int tok_paged_assign(tok_handle* h, const tok_paged_args* a, void* stream) try {
   c.a = *a;
   // one token a thread while all of them fit two CTAs per SM (a decode step's
   // tokens are of as many requests: one's loads would wait for another's), else
-  // four.  4,096 requests of a token 10.8 us with one, 16.8 with four; prefills of
-  // 64 requests of up to 20,001 tokens 7.5 and 10.8, of up to 180,001 16.9 and 15.1.
+  // four.  4,096 requests of a token 10.3 us with one, 16.5 with four; prefills of
+  // 64 requests of up to 20,001 tokens 6.2 and 6.7, of up to 180,001 16.4 and 10.3.
   // Threads of a CTA: many CTAs hide one another's latencies, but each reads every
-  // request.  One token a thread, 512 and 1,024 threads: 1,000 requests 7.5 and
-  // 8.5 us, 4,096 10.5 and 10.8, 15,000 25.0 and 18.9.  Four, 128, 256, 512 and
-  // 1,024: 64 long requests 10.8, 12.7, 13.8 and 15.1, 4,096 requests with 3.9M
-  // tokens 28.3 and 22.7 with the first two.
+  // request.  One token a thread, 512 and 1,024 threads: 1,000 requests 7.2 and
+  // 8.3 us, 4,096 10.3 both, 15,000 24.7 and 18.5.  Four, 128 and 256: 64 long
+  // requests 10.3 and 12.5, 4,096 requests with 3.1M tokens 38.8 and 34.9.
   unsigned threads = threads_for(std::max<unsigned long long>(a->n, a->cap), a->n > 4096 ? PG_THREADS : 512);
   const bool one = a->cap <= 2ull * (unsigned)h->n_sms * threads;
   if (!one) threads = a->n > 512 ? PG_THREADS_4 : 128;

@@ -239,7 +239,8 @@ int tok_pretokenize_device_noalloc(int pattern_id, const uint8_t* d_text, uint64
  * Between the ids and a language model.  The entry points below work on
  * device buffers, are enqueued on `stream` (NULL = the CUDA default stream)
  * without a host synchronisation or an allocation, and may be captured in a
- * CUDA graph.  h gives the device, the error message and the launch count;
+ * CUDA graph (but for tok_grammar_load and tok_grammar_free, which allocate,
+ * free and wait).  h gives the device, the error message and the launch count;
  * TokTier describes none of them: they serve the steps before and after the
  * model that read this library's ids, item offsets and vocabulary.
  * Arguments are checked on the host (TOK_EINVAL, nothing enqueued); what only
