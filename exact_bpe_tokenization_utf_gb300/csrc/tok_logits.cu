@@ -963,7 +963,8 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) k_logits_grad(GradCall ca
   float cp = (gr.lse ? gr.lse[b] : 0.f) - glp, lse = 0.f;
   if (gr.lse || gr.logprob) lse = a.d_lse[b];
   if (fabsf(lse) >= 1e36f) cp = lse = 0.f;  // (nothing but -inf or a type's lowest value)
-  const bool far = fabsf(lse) >= Y_FAR;     // (a masked row, or next to no temperature: every score is taken one by one)
+  // a masked row, or next to no temperature: every score is taken one by one
+  const bool far = fabsf(lse) >= Y_FAR && cp != 0.f;
   uint32_t pick = a.d_pick ? (uint32_t)a.d_pick[b] : 0xffffffffu;
   if ((int32_t)pick < 0 && gr.logprob) pick = a.d_top ? (uint32_t)a.d_top[b] : 0xffffffffu;
   const double kd = 1.4426950408889634 / (a.d_temperature ? (double)a.d_temperature[b] : 1.0);
