@@ -316,7 +316,7 @@ uint64_t last_cut(const uint8_t* old, uint64_t n, uint64_t limit) {
 extern "C" {
 
 int tok_load(const uint8_t* vocab_bytes, const uint64_t* vocab_off, uint32_t n_vocab, const uint32_t* merges,
-             uint32_t n_merges, int pattern_id, tok_handle** out) {
+             uint32_t n_merges, int pattern_id, tok_handle** out) try {
   if (!out) return fail(nullptr, TOK_EINVAL, "out is NULL");
   *out = nullptr;
   const bool ignore_merges = (pattern_id & TOK_IGNORE_MERGES) != 0;
@@ -458,11 +458,13 @@ int tok_load(const uint8_t* vocab_bytes, const uint64_t* vocab_off, uint32_t n_v
     whole[slot] = WholeEntry{head, t, ((uint32_t)first << 8) | len};
   }
 
-  tok_handle* h = new tok_handle();
+  std::vector<uint8_t> bytes(vocab_bytes + vocab_off[0], vocab_bytes + vocab_off[n_vocab]);
+  std::vector<uint64_t> offsets(vocab_off, vocab_off + n_vocab + 1);
+  for (uint64_t& o : offsets) o -= vocab_off[0];
+  tok_handle* h = new tok_handle();  // (nothing below throws while it is held)
   h->pattern = pattern;
-  h->vocab_bytes.assign(vocab_bytes + vocab_off[0], vocab_bytes + vocab_off[n_vocab]);
-  h->vocab_off.resize(n_vocab + 1);
-  for (uint32_t t = 0; t <= n_vocab; ++t) h->vocab_off[t] = vocab_off[t] - vocab_off[0];
+  h->vocab_bytes.swap(bytes);
+  h->vocab_off.swap(offsets);
   cudaError_t e = cudaGetDevice(&h->dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sms, cudaDevAttrMultiProcessorCount, h->dev);
   if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&h->stream, cudaStreamNonBlocking);
@@ -497,10 +499,9 @@ int tok_load(const uint8_t* vocab_bytes, const uint64_t* vocab_off, uint32_t n_v
   for (int k = 0; k <= N_STAGES && e == cudaSuccess; ++k) e = cudaEventCreate(&h->ev[k]);
   if (e != cudaSuccess) {
     const int code = (e == cudaErrorMemoryAllocation) ? TOK_ENOMEM : TOK_ECUDA;
-    std::string msg = std::string("tok_load: ") + cudaGetErrorString(e);
     cudaGetLastError();
     tok_free(h);
-    return fail(nullptr, code, msg);
+    return fail(nullptr, code, std::string("tok_load: ") + cudaGetErrorString(e));
   }
   h->v.table = h->d_table;
   h->v.bits = bits;
@@ -529,6 +530,8 @@ int tok_load(const uint8_t* vocab_bytes, const uint64_t* vocab_off, uint32_t n_v
   h->hash = hh;
   *out = h;
   return TOK_OK;
+} catch (...) {
+  return fail(nullptr, TOK_ENOMEM, "out of memory");  // (short enough to need none)
 }
 
 void tok_free(tok_handle* h) {
