@@ -36,7 +36,7 @@ print("rc", rc, bool(h.value))
 def test_a_load_without_memory_is_an_error_code():
     import torch
     if torch.cuda.is_available():
-        pytest.skip("the driver's own memory is not limited here")
+        pytest.skip("with a GPU the limit would be that of CUDA itself too")
     from exact_bpe_tokenization_utf_gb300 import TOK_ECUDA, TOK_ENOMEM, _build
     _build.build()
     codes = []
