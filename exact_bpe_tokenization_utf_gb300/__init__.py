@@ -39,7 +39,9 @@ SYMBOLS = ["tok_load", "tok_encode", "tok_encode_offsets", "tok_repair_append", 
            "tok_last_error", "tok_error_offset", "tok_content_hash", "tok_set_timing", "tok_stage_times",
            "tok_launch_count", "tok_free", "tok_pretokenize_device_noalloc", "tok_debug_fail_alloc",
            "tok_debug_grid_wait", "tok_paged_assign", "tok_paged_release", "tok_seen_bits", "tok_logits_process",
-           "tok_logits_backward", "tok_grammar_load", "tok_grammar_free", "tok_grammar_mask"]
+           "tok_logits_backward", "tok_grammar_load", "tok_grammar_free", "tok_grammar_mask", "tok_embed",
+           "tok_embed_backward", "tok_embed_work_bytes", "tok_sample", "tok_paged_store", "tok_paged_attend",
+           "tok_paged_attend_work_bytes"]
 
 DTYPE_F32, DTYPE_F16, DTYPE_BF16 = 0, 1, 2   # tok.h TOK_F32, TOK_F16, TOK_BF16
 
@@ -69,7 +71,7 @@ class _Args(ctypes.Structure):
 
 def _fields(text):
     kinds = {"p": ctypes.c_void_p, "i64": ctypes.c_int64, "u64": ctypes.c_uint64, "u32": ctypes.c_uint32,
-             "i32": ctypes.c_int32}
+             "i32": ctypes.c_int32, "f32": ctypes.c_float}
     return [(n, kinds[k]) for n, k in (f.split(":") for f in text.split())]
 
 
@@ -91,6 +93,43 @@ class LogitsGradArgs(_Args):
     """tok_logits_grad_args of include/tok.h."""
     _fields_ = _fields("d_grad_out:p grad_out_stride:i64 d_grad_lse:p d_grad_logprob:p d_grad_logits:p "
                        "grad_logits_stride:i64 d_grad_bias:p")
+
+
+class EmbedArgs(_Args):
+    """tok_embed_args of include/tok.h."""
+    _fields_ = _fields("d_ids:p n:u64 d_n:p d_weight:p weight_stride:i64 weight_dtype:i32 n_rows:u32 dim:u32 scale:f32 "
+                       "d_out:p out_stride:i64 out_dtype:i32")
+
+
+class EmbedGradArgs(_Args):
+    """tok_embed_grad_args of include/tok.h."""
+    _fields_ = _fields("d_ids:p n:u64 d_n:p n_rows:u32 dim:u32 scale:f32 d_grad_out:p grad_out_stride:i64 "
+                       "grad_out_dtype:i32 d_grad_weight:p grad_weight_stride:i64 grad_weight_dtype:i32 accumulate:i32 "
+                       "d_work:p work_bytes:u64")
+
+
+class SampleArgs(_Args):
+    """tok_sample_args of include/tok.h."""
+    _fields_ = _fields("d_scores:p scores_stride:i64 dtype:i32 rows:u32 n_logits:u32 d_temperature:p d_min_p:p d_top_k:p "
+                       "d_top_p:p d_random:p d_pick:p d_kept:p d_logprob:p")
+
+
+class KVCache(_Args):
+    """tok_kv_cache of include/tok.h."""
+    _fields_ = _fields("d_k:p d_v:p block_stride:i64 token_stride:i64 head_stride:i64 dtype:i32 n_blocks:u32 "
+                       "block_size:u32 kv_heads:u32 head_dim:u32")
+
+
+class StoreArgs(_Args):
+    """tok_store_args of include/tok.h."""
+    _fields_ = _fields("d_k:p d_v:p token_stride:i64 head_stride:i64 d_slot:p n:u64")
+
+
+class AttendArgs(_Args):
+    """tok_attend_args of include/tok.h."""
+    _fields_ = _fields("d_q:p q_stride:i64 q_head_stride:i64 d_out:p out_stride:i64 out_head_stride:i64 d_lse:p n:u32 "
+                       "heads:u32 scale:f32 window:u32 d_table:p table_stride:i64 max_blocks:u32 d_seq_len:p d_work:p "
+                       "work_bytes:u64")
 
 
 _lib = None
@@ -147,10 +186,20 @@ def lib():
     L.tok_grammar_mask.argtypes = [P, P, P, P, P, U32, ctypes.c_int32, P, U32, P, ctypes.c_int64, P]
     L.tok_grammar_free.argtypes = [P]
     L.tok_grammar_free.restype = None
+    L.tok_embed.argtypes = [P, P, P]
+    L.tok_embed_backward.argtypes = [P, P, P]
+    L.tok_embed_work_bytes.argtypes = [U64, U32, U32]
+    L.tok_embed_work_bytes.restype = U64
+    L.tok_sample.argtypes = [P, P, P]
+    L.tok_paged_store.argtypes = [P, P, P, P]
+    L.tok_paged_attend.argtypes = [P, P, P, P]
+    L.tok_paged_attend_work_bytes.argtypes = [P, U32, U32, U32, U32]
+    L.tok_paged_attend_work_bytes.restype = U64
     for fn in ("tok_load", "tok_encode", "tok_encode_offsets", "tok_repair_append", "tok_encode_batch", "tok_encode_device",
                "tok_encode_offsets_device", "tok_encode_batch_device", "tok_pretokenize", "tok_pretokenize_batch",
                "tok_set_timing", "tok_stage_times", "tok_paged_assign", "tok_paged_release", "tok_seen_bits",
-               "tok_logits_process", "tok_logits_backward", "tok_grammar_load", "tok_grammar_mask"):
+               "tok_logits_process", "tok_logits_backward", "tok_grammar_load", "tok_grammar_mask", "tok_embed",
+               "tok_embed_backward", "tok_sample", "tok_paged_store", "tok_paged_attend"):
         getattr(L, fn).restype = ctypes.c_int
     _lib = L
     return L
@@ -383,6 +432,47 @@ class Tokenizer:
         rc = self._L.tok_logits_backward(self._h, args._addr, grad_args._addr, stream or None)
         if rc:
             self._check(rc)
+
+    # --- at the model's two ends and at its cache (device buffers) --------
+    def embed_device(self, args, stream=0):
+        """The rows of a batch's ids, scaled (an EmbedArgs)."""
+        rc = self._L.tok_embed(self._h, args._addr, stream or None)
+        if rc:
+            self._check(rc)
+
+    def embed_backward_device(self, args, stream=0):
+        """The gradient of embed_device with respect to the weights (an EmbedGradArgs)."""
+        rc = self._L.tok_embed_backward(self._h, args._addr, stream or None)
+        if rc:
+            self._check(rc)
+
+    def embed_work_bytes(self, n, n_rows, dim):
+        """Bytes of the buffer that embed_backward_device works in."""
+        return int(self._L.tok_embed_work_bytes(n, n_rows, dim))
+
+    def sample_device(self, args, stream=0):
+        """A token for each row of scores, by temperature, min-p, top-k, top-p
+        and a random number (a SampleArgs)."""
+        rc = self._L.tok_sample(self._h, args._addr, stream or None)
+        if rc:
+            self._check(rc)
+
+    def paged_store_device(self, cache, args, stream=0):
+        """New tokens' keys and values into the paged cache (a KVCache and a StoreArgs)."""
+        rc = self._L.tok_paged_store(self._h, cache._addr, args._addr, stream or None)
+        if rc:
+            self._check(rc)
+
+    def paged_attend_device(self, cache, args, stream=0):
+        """One new token's attention of each request over the paged cache (a
+        KVCache and an AttendArgs)."""
+        rc = self._L.tok_paged_attend(self._h, cache._addr, args._addr, stream or None)
+        if rc:
+            self._check(rc)
+
+    def attend_work_bytes(self, n, heads, kv_heads, head_dim):
+        """Bytes of the buffer that paged_attend_device works in."""
+        return int(self._L.tok_paged_attend_work_bytes(self._h, n, heads, kv_heads, head_dim))
 
     # --- introspection ---------------------------------------------------
     @property

@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libtokgb.so")
 SOURCES = ["tok_pretok.cu", "tok_bpe.cu", "tok_emit.cu", "tok_api.cu", "tok_noalloc.cu",
-           "tok_paged.cu", "tok_logits.cu", "tok_grammar.cu"]
+           "tok_paged.cu", "tok_logits.cu", "tok_grammar.cu",
+           "model/embed.cu", "model/sample.cu", "model/paged_attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]
 
@@ -34,7 +35,8 @@ def _newer(target, deps):
 
 def build(verbose=False, force=False):
     os.makedirs(OUT_DIR, exist_ok=True)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".inc"))]
+    deps = [os.path.join(d, f) for d in (CSRC, os.path.join(CSRC, "model")) for f in os.listdir(d)
+            if f.endswith((".cu", ".cuh", ".inc"))]
     deps.append(os.path.join(HERE, "..", "include", "tok.h"))
     if not force and _newer(LIB, deps + [__file__]):
         return LIB
@@ -42,7 +44,7 @@ def build(verbose=False, force=False):
     objs = []
 
     def compile_one(src):
-        obj = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
+        obj = os.path.join(OUT_DIR, os.path.basename(src).replace(".cu", ".o"))
         cmd = [cc] + ARCH + FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:

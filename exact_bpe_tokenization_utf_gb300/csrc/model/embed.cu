@@ -1,0 +1,603 @@
+// The rows of a batch's ids (tok_embed) and the gradient of the weights
+// (tok_embed_backward).
+//
+//   out[t] = scale * W[ids[t]],   dW[v] = scale * sum of dout[t] over ids[t] == v
+//
+// Both are bound by the bytes: the rows that ids name and what is written; the
+// gradients that come in and the rows of dW.
+//
+// The gradient sorts the tokens by their ids (a stable radix sort in two passes
+// of up to 11 bits, one where the ids have no more), so that a row's tokens lie
+// side by side and are added in their order: sums in 32 bits, the same bits each
+// time, without atomics on them.  The sorted tokens are cut into chunks of equal
+// length; a warp adds a chunk's rows over 256 columns.  A run of equal ids inside
+// a chunk is a finished row of dW; what a chunk's first and last run share with
+// the neighbours goes to d_work, and a second kernel adds those parts in order.
+#include "types.cuh"
+
+namespace tokgb {
+namespace {
+
+constexpr uint32_t MOST_ROWS = 1u << 20, MOST_DIM = 1u << 20;
+constexpr int EM_THREADS = 256;
+constexpr int COLS = 256;            // columns of a warp's step: eight a lane
+constexpr uint32_t ALL = 0xffffffffu;
+
+// --- the rows ------------------------------------------------------------------
+
+struct EmbedCall {
+  const int32_t* ids;
+  const long long* n_dev;
+  uint32_t n, n_rows, dim, segs;  // segs: warps of a row
+  const void* weight;
+  long long weight_stride;
+  void* out;
+  long long out_stride;
+  float scale;
+};
+
+constexpr int EM_U = 4;              // steps of a warp, all of whose loads are under way at once
+
+template <class TI, class TO>
+__global__ void __launch_bounds__(EM_THREADS) k_embed(EmbedCall c) {
+  const uint32_t n = count_of(c.n_dev, c.n);
+  const uint64_t unit = (uint64_t)blockIdx.x * (EM_THREADS / 32) + (threadIdx.x >> 5);
+  const uint32_t t = (uint32_t)(unit / c.segs), seg = (uint32_t)(unit % c.segs), lane = threadIdx.x & 31u;
+  if (t >= n) return;
+  const int32_t id = c.ids[t];
+  const bool there = (uint32_t)id < c.n_rows;
+  const TI* row = static_cast<const TI*>(c.weight) + (there ? (long long)id * c.weight_stride : 0);
+  TO* to = static_cast<TO*>(c.out) + (long long)t * c.out_stride;
+  const uint32_t col = seg * (EM_U * COLS) + lane * 8;
+  Eight<TI> x[EM_U];
+#pragma unroll
+  for (int u = 0; u < EM_U; ++u) {
+    if (there && col + u * COLS < c.dim) x[u].load(row + col + u * COLS);
+    else x[u].zero();
+  }
+#pragma unroll
+  for (int u = 0; u < EM_U; ++u) {
+    if (col + u * COLS >= c.dim) break;
+    Eight<TO> y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.put_pair(i, x[u].get(2 * i) * c.scale, x[u].get(2 * i + 1) * c.scale);
+    if (!there) y.zero();  // (0 times an infinite scale)
+    y.store(to + col + u * COLS);
+  }
+}
+
+// rows that do not lie at 16-byte boundaries, or of a width that is no multiple of eight
+template <class TI, class TO>
+__global__ void __launch_bounds__(EM_THREADS) k_embed_any(EmbedCall c) {
+  const uint32_t n = count_of(c.n_dev, c.n);
+  const uint64_t unit = (uint64_t)blockIdx.x * (EM_THREADS / 32) + (threadIdx.x >> 5);
+  const uint32_t t = (uint32_t)(unit / c.segs), seg = (uint32_t)(unit % c.segs), lane = threadIdx.x & 31u;
+  if (t >= n) return;
+  const int32_t id = c.ids[t];
+  const bool there = (uint32_t)id < c.n_rows;
+  const TI* row = static_cast<const TI*>(c.weight) + (there ? (long long)id * c.weight_stride : 0);
+  TO* to = static_cast<TO*>(c.out) + (long long)t * c.out_stride;
+  const uint32_t col = seg * (EM_U * COLS) + lane;
+#pragma unroll
+  for (int u = 0; u < EM_U; ++u) {
+    TI x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (there && col + u * COLS + i * 32 < c.dim) x[i] = row[col + u * COLS + i * 32];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + u * COLS + i * 32 < c.dim) to[col + u * COLS + i * 32] = from_f32<TO>(there ? to_f32(x[i]) * c.scale : 0.f);
+  }
+}
+
+// --- the tokens sorted by their ids ----------------------------------------------
+
+// A pass of the sort: every CTA takes a span of the tokens, in tiles.  A tile's
+// warps take 256 tokens each, 32 at a time, so that a token's place among those
+// of its digit is their order; counts of the digits by CTA (the table `counts`,
+// a row of n_digits for each CTA) give the places of the spans.
+constexpr int ST_THREADS = 512, ST_WARPS = ST_THREADS / 32, ST_PER = 8;
+constexpr int ST_TILE = ST_THREADS * ST_PER;
+constexpr int MOST_BITS = 11, MOST_DIGITS = 1 << MOST_BITS;
+constexpr uint32_t MOST_SPANS = 152;
+
+struct SortCall {
+  const int32_t* ids;
+  const long long* n_dev;
+  uint32_t n, n_rows;
+  uint32_t span;       // tokens of a CTA, a multiple of a tile
+  uint32_t spans;      // CTAs
+  uint32_t bits0, bits1;
+  uint32_t* counts0;   // spans rows of 2^bits0
+  uint32_t* counts1;   // spans rows of 2^bits1
+  uint2* half;         // (key, token) after the first pass of two
+  uint2* sorted;       // and at the end
+};
+
+// an id's key: ids without a row come last
+__device__ __forceinline__ uint32_t key_of(int32_t id, uint32_t n_rows) { return min((uint32_t)id, n_rows); }
+
+// lanes with the same digit
+template <int BITS_MOST>
+__device__ __forceinline__ uint32_t alike(uint32_t d, bool in, uint32_t bits) {
+  uint32_t m = __ballot_sync(ALL, in);
+#pragma unroll
+  for (int b = 0; b < BITS_MOST; ++b) {
+    if (b >= (int)bits) break;
+    const uint32_t one = __ballot_sync(ALL, d >> b & 1u);
+    m &= d >> b & 1u ? one : ~one;
+  }
+  return in ? m : 0u;
+}
+
+// counts of the first digit in each span; the second's counts are set to 0
+__global__ void __launch_bounds__(ST_THREADS) k_sort_count(SortCall c) {
+  __shared__ uint32_t s_count[MOST_DIGITS];
+  const uint32_t n = count_of(c.n_dev, c.n), digits = 1u << c.bits0, tid = threadIdx.x;
+  for (uint32_t d = tid; d < digits; d += ST_THREADS) s_count[d] = 0;
+  __syncthreads();
+  const uint32_t begin = min(blockIdx.x * c.span, n), end = min(begin + c.span, n);
+  for (uint32_t t = begin + tid; t < end; t += ST_THREADS) atomicAdd(&s_count[key_of(c.ids[t], c.n_rows) & (digits - 1)], 1u);
+  __syncthreads();
+  for (uint32_t d = tid; d < digits; d += ST_THREADS) c.counts0[(size_t)blockIdx.x * digits + d] = s_count[d];
+  if (c.bits1)
+    for (uint32_t d = tid; d < (1u << c.bits1); d += ST_THREADS) c.counts1[((size_t)blockIdx.x << c.bits1) + d] = 0;
+}
+
+template <int PASS>
+__global__ void __launch_bounds__(ST_THREADS) k_sort_place(SortCall c) {
+  extern __shared__ __align__(16) uint8_t mem[];
+  const uint32_t bits = PASS == 0 ? c.bits0 : c.bits1, digits = 1u << bits, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+  uint32_t* base = reinterpret_cast<uint32_t*>(mem);                    // [digits] where a digit's next token goes
+  uint16_t* count = reinterpret_cast<uint16_t*>(base + digits);         // [ST_WARPS][digits]
+  __shared__ uint32_t s_sum[ST_WARPS];
+  const uint32_t n = count_of(c.n_dev, c.n);
+  const uint32_t* counts = PASS == 0 ? c.counts0 : c.counts1;
+  const uint32_t begin = min(blockIdx.x * c.span, n), end = min(begin + c.span, n);
+  // places: all tokens of lower digits, then those of the digit in earlier spans.  A
+  // thread has up to four digits side by side.
+  constexpr int PER = MOST_DIGITS / ST_THREADS;
+  uint32_t before[PER], all = 0, mine[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    before[i] = mine[i] = 0;
+    const uint32_t d = tid * PER + i;
+    if (d < digits) {
+#pragma unroll 8
+      for (uint32_t s = 0; s < c.spans; ++s) {
+        const uint32_t m = counts[(size_t)s * digits + d];
+        mine[i] += m;
+        if (s < blockIdx.x) before[i] += m;
+      }
+    }
+    all += mine[i];
+  }
+  uint32_t inc = all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(ALL, inc, o);
+    if (lane >= (uint32_t)o) inc += v;
+  }
+  if (lane == 31) s_sum[warp] = inc;
+  __syncthreads();
+  uint32_t lower = inc - all;
+  for (uint32_t w = 0; w < warp; ++w) lower += s_sum[w];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t d = tid * PER + i;
+    if (d < digits) base[d] = lower + before[i];
+    lower += mine[i];
+  }
+  for (uint32_t t0 = begin; t0 < end; t0 += ST_TILE) {
+    __syncthreads();
+    for (uint32_t i = tid; i < ST_WARPS * digits / 2; i += ST_THREADS) reinterpret_cast<uint32_t*>(count)[i] = 0;
+    __syncthreads();
+    uint32_t key[ST_PER], tok[ST_PER], rank[ST_PER];
+    uint16_t* my = count + warp * digits;
+#pragma unroll
+    for (int j = 0; j < ST_PER; ++j) {
+      const uint32_t t = t0 + warp * (ST_PER * 32) + j * 32 + lane;
+      key[j] = tok[j] = 0;
+      if (t < end) {
+        if (PASS == 0) {
+          key[j] = key_of(c.ids[t], c.n_rows);
+          tok[j] = t;
+        } else {
+          const uint2 kt = c.half[t];
+          key[j] = kt.x;
+          tok[j] = kt.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < ST_PER; ++j) {
+      const bool in = t0 + warp * (ST_PER * 32) + j * 32 + lane < end;
+      const uint32_t d = PASS == 0 ? key[j] & (digits - 1) : key[j] >> c.bits0;
+      const uint32_t same = alike<MOST_BITS>(d, in, bits), below = __popc(same & ((1u << lane) - 1u));
+      uint32_t at = in ? my[d] : 0;
+      __syncwarp();
+      if (in && below == 0) my[d] = (uint16_t)(at + __popc(same));
+      __syncwarp();
+      rank[j] = at + below;
+    }
+    __syncthreads();
+    // a digit's counts by warp become places, its base moves on
+    for (uint32_t d = tid; d < digits; d += ST_THREADS) {
+      uint32_t run = 0;
+#pragma unroll
+      for (int w = 0; w < ST_WARPS; ++w) {
+        const uint32_t m = count[w * digits + d];
+        count[w * digits + d] = (uint16_t)run;
+        run += m;
+      }
+      // (kept in the place of a 17th warp's: the base without this tile's)
+      base[d] += run;
+      count[ST_WARPS * digits + d] = (uint16_t)run;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ST_PER; ++j) {
+      const bool in = t0 + warp * (ST_PER * 32) + j * 32 + lane < end;
+      const uint32_t d = PASS == 0 ? key[j] & (digits - 1) : key[j] >> c.bits0;
+      uint32_t to = 0;
+      if (in) {
+        to = base[d] - count[ST_WARPS * digits + d] + count[warp * digits + d] + rank[j];
+        const uint2 kt = make_uint2(key[j], tok[j]);
+        if (PASS == 0 && c.bits1) c.half[to] = kt;
+        else c.sorted[to] = kt;
+      }
+      if (PASS == 0 && c.bits1) {
+        // the next pass's counts; equal keys of a warp lie side by side (but where a
+        // span ends between them)
+        const uint32_t slot = in ? ((to / c.span) << c.bits1) + (key[j] >> c.bits0) : ALL;
+        const uint32_t same = __match_any_sync(ALL, slot);
+        if (in && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&c.counts1[slot], (uint32_t)__popc(same));
+      }
+    }
+  }
+}
+
+// --- the rows' sums ----------------------------------------------------------------
+
+struct SumCall {
+  const uint2* sorted;
+  const long long* n_dev;
+  uint32_t n, n_rows, dim, segs;  // segs: warps of a row
+  uint32_t chunk;                 // sorted tokens of a warp, a multiple of 32
+  uint32_t chunks;
+  float scale;
+  const void* grad_out;
+  long long grad_out_stride;
+  void* grad_weight;
+  long long grad_weight_stride;
+  float* parts;                   // [chunks][2][dim rounded up to COLS]: first and last run of a chunk
+  uint32_t sum_ctas;              // CTAs that add; the others write the rows without tokens
+};
+
+// a lane's eight columns: side by side (VEC), or 32 apart
+template <bool VEC> __device__ __forceinline__ uint32_t column(uint32_t seg, uint32_t lane, int i) {
+  return seg * COLS + (VEC ? lane * 8 + i : lane + i * 32);
+}
+
+template <class TG, class TW, bool VEC>
+__device__ __forceinline__ void write_row(const SumCall& c, uint32_t v, uint32_t seg, uint32_t lane, const float* s, bool add) {
+  TW* to = static_cast<TW*>(c.grad_weight) + (long long)v * c.grad_weight_stride;
+  if (VEC) {
+    const uint32_t col = column<true>(seg, lane, 0);
+    if (col >= c.dim) return;
+    Eight<TW> y;
+    if (add) {
+      Eight<TW> old;
+#pragma unroll
+      for (int i = 0; i < Eight<TW>::WORDS / 4; ++i) {
+        const uint4 q = reinterpret_cast<const uint4*>(to + col)[i];
+        old.w[4 * i] = q.x;
+        old.w[4 * i + 1] = q.y;
+        old.w[4 * i + 2] = q.z;
+        old.w[4 * i + 3] = q.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        y.put_pair(i, fmaf(s[2 * i], c.scale, old.get(2 * i)), fmaf(s[2 * i + 1], c.scale, old.get(2 * i + 1)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y.put_pair(i, s[2 * i] * c.scale, s[2 * i + 1] * c.scale);
+    }
+    y.store(to + col);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t col = column<false>(seg, lane, i);
+      if (col < c.dim) to[col] = from_f32<TW>(add ? fmaf(s[i], c.scale, to_f32(to[col])) : s[i] * c.scale);
+    }
+  }
+}
+
+__device__ __forceinline__ float* part_of(const SumCall& c, uint32_t chunk, int last, uint32_t seg, uint32_t lane) {
+  return c.parts + (((size_t)chunk * 2 + last) * c.segs + seg) * COLS + lane * 8;
+}
+__device__ __forceinline__ void put_part(float* p, const float* s) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(s[0], s[1], s[2], s[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(s[4], s[5], s[6], s[7]);
+}
+
+// first place from which on keys are at least v
+__device__ __forceinline__ uint32_t first_at(const uint2* sorted, uint32_t n, uint32_t v) {
+  uint32_t lo = 0, hi = n;
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi) >> 1;
+    if (sorted[mid].x < v) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+constexpr int AHEAD = 8;  // rows whose loads are under way
+
+template <class TG, class TW, bool VEC, bool ADD>
+__global__ void __launch_bounds__(EM_THREADS) k_embed_sum(SumCall c) {
+  const uint32_t n = count_of(c.n_dev, c.n), lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  if (blockIdx.x >= c.sum_ctas) {
+    // rows that no token names: 32 of them for each warp, found by their lanes
+    const uint32_t v0 = ((blockIdx.x - c.sum_ctas) * (EM_THREADS / 32) + warp) * 32;
+    if (v0 >= c.n_rows) return;
+    const uint32_t v = v0 + lane, at = first_at(c.sorted, n, v);
+    uint32_t empty = __ballot_sync(ALL, v < c.n_rows && (at >= n || c.sorted[at].x != v));
+    const float none[8] = {};
+    while (empty) {
+      const uint32_t k = __ffs(empty) - 1;
+      empty &= empty - 1;
+      for (uint32_t seg = 0; seg < c.segs; ++seg) write_row<TG, TW, VEC>(c, v0 + k, seg, lane, none, false);
+    }
+    return;
+  }
+  const uint64_t unit = (uint64_t)blockIdx.x * (EM_THREADS / 32) + warp;
+  const uint32_t chunk = (uint32_t)(unit / c.segs), seg = (uint32_t)(unit % c.segs);
+  const uint32_t begin = chunk * c.chunk, end = min(begin + c.chunk, n);
+  if (chunk >= c.chunks || begin >= n) return;
+  uint32_t run_key = begin ? c.sorted[begin - 1].x : ALL;  // the key of the tokens before
+  bool first = true;                                       // the run began before the chunk
+  const uint32_t next_key = end < n ? c.sorted[end].x : ALL;
+  float s[8] = {};
+  for (uint32_t b = begin; b < end; b += 32) {
+    const uint2 kt = b + lane < end ? c.sorted[b + lane] : make_uint2(ALL, 0);
+    const uint32_t m = min(32u, end - b);
+    for (uint32_t j0 = 0; j0 < m; j0 += AHEAD) {
+      Eight<TG> x[AHEAD];
+      float xs[VEC ? 1 : AHEAD][8];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const uint32_t t = __shfl_sync(ALL, kt.y, (j0 + j) & 31u), k = __shfl_sync(ALL, kt.x, (j0 + j) & 31u);
+        const bool in = j0 + j < m && k < c.n_rows;
+        const TG* row = static_cast<const TG*>(c.grad_out) + (long long)t * c.grad_out_stride;
+        if (VEC) {
+          const uint32_t col = column<true>(seg, lane, 0);
+          if (in && col < c.dim) x[j].load_once(row + col);
+          else x[j].zero();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t col = column<false>(seg, lane, i);
+            xs[VEC ? 0 : j][i] = in && col < c.dim ? to_f32(row[col]) : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (j0 + j >= m) break;
+        const uint32_t k = __shfl_sync(ALL, kt.x, (j0 + j) & 31u);
+        if (k != run_key) {  // (the same in all lanes)
+          if (run_key != ALL && run_key < c.n_rows) {
+            if (!first) write_row<TG, TW, VEC>(c, run_key, seg, lane, s, ADD);
+            else if (b + j0 + j > begin) put_part(part_of(c, chunk, 0, seg, lane), s);
+          }
+          first = false;
+          run_key = k;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += VEC ? x[j].get(i) : xs[VEC ? 0 : j][i];
+      }
+    }
+  }
+  if (run_key >= c.n_rows) return;
+  if (first) put_part(part_of(c, chunk, 0, seg, lane), s);
+  else if (next_key == run_key) put_part(part_of(c, chunk, 1, seg, lane), s);
+  else write_row<TG, TW, VEC>(c, run_key, seg, lane, s, ADD);
+}
+
+// Runs that reach over chunks: the CTA of the chunk in which one begins adds its
+// parts, each warp a share of them in order, then the shares in order.
+template <class TG, class TW, bool VEC, bool ADD>
+__global__ void __launch_bounds__(EM_THREADS) k_embed_join(SumCall c) {
+  __shared__ __align__(16) float s_part[EM_THREADS / 32][COLS];
+  const uint32_t n = count_of(c.n_dev, c.n), lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  const uint32_t chunk = blockIdx.x / c.segs, seg = blockIdx.x % c.segs;
+  const uint64_t last = (uint64_t)(chunk + 1) * c.chunk;
+  if (last >= n) return;
+  const uint32_t key = c.sorted[last].x;
+  if (key >= c.n_rows || c.sorted[last - 1].x != key) return;
+  const uint32_t begin = chunk * c.chunk;
+  // (a run that began earlier is another CTA's: its key is that of the token before the chunk)
+  if (c.sorted[begin].x == key && begin && c.sorted[begin - 1].x == key) return;
+  const uint32_t stop = first_at(c.sorted, n, key + 1);        // the run's end
+  const uint32_t to = (stop - 1) / c.chunk;                    // its last chunk
+  const uint32_t m = to - chunk + 1, per = (m + EM_THREADS / 32 - 1) / (EM_THREADS / 32);
+  float s[8] = {};
+  const uint32_t i_end = min((warp + 1) * per, m);
+#pragma unroll 4
+  for (uint32_t i = warp * per; i < i_end; ++i) {
+    const float4* p = reinterpret_cast<const float4*>(part_of(c, chunk + i, i == 0, seg, lane));
+    const float4 a = p[0], b = p[1];
+    s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+    s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+  }
+  put_part(&s_part[warp][lane * 8], s);
+  __syncthreads();
+  if (warp) return;
+  for (int w = 1; w < EM_THREADS / 32; ++w)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] += s_part[w][lane * 8 + i];
+  write_row<TG, TW, VEC>(c, key, seg, lane, s, ADD);
+}
+
+// --- the host's side -----------------------------------------------------------------
+
+uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
+
+struct Plan {
+  uint32_t bits0, bits1, span, spans, chunk, chunks, segs;
+  uint64_t counts0, counts1, half, sorted, parts, bytes;  // places in d_work
+};
+
+Plan plan_of(uint64_t n, uint32_t n_rows, uint32_t dim) {
+  Plan p{};
+  uint32_t bits = 1;
+  while (bits < 21 && (n_rows >> bits)) ++bits;  // keys are 0 .. n_rows
+  p.bits0 = bits <= (uint32_t)MOST_BITS ? bits : (bits + 1) / 2;
+  p.bits1 = bits - p.bits0;
+  const uint64_t tiles = std::max<uint64_t>(1, (n + ST_TILE - 1) / ST_TILE);
+  const uint64_t per = (tiles + MOST_SPANS - 1) / MOST_SPANS;
+  p.span = (uint32_t)(per * ST_TILE);
+  p.spans = (uint32_t)((tiles + per - 1) / per);
+  p.segs = (dim + COLS - 1) / COLS;
+  p.chunk = 32;
+  while (p.chunk < 128 && n / p.chunk * p.segs > 8192) p.chunk *= 2;
+  p.chunks = (uint32_t)((n + p.chunk - 1) / p.chunk);
+  uint64_t at = 0;
+  auto take = [&](uint64_t bytes) { const uint64_t here = at; at = up(at + bytes, 256); return here; };
+  p.counts0 = take((uint64_t)p.spans * 4 << p.bits0);
+  p.counts1 = take(p.bits1 ? (uint64_t)p.spans * 4 << p.bits1 : 0);
+  p.half = take(p.bits1 ? n * 8 : 0);
+  p.sorted = take(n * 8);
+  p.parts = take((uint64_t)p.chunks * 2 * p.segs * COLS * 4);
+  p.bytes = std::max<uint64_t>(at, 256);
+  return p;
+}
+
+bool sizes_ok(uint64_t n, uint32_t n_rows, uint32_t dim) {
+  return n < (1ull << 31) && n_rows && n_rows <= MOST_ROWS && dim && dim <= MOST_DIM;
+}
+
+int finish(tok_handle* h, unsigned launches) {
+  h->launches += launches;
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? TOK_OK : cuda_fail(h, e, "kernel launch");
+}
+
+// f(T{}) for an element type
+template <class F> void with_type(int dtype, F f) {
+  if (dtype == TOK_F32) f(float{});
+  else if (dtype == TOK_F16) f(__half{});
+  else f(__nv_bfloat16{});
+}
+
+// whether rows can be taken eight elements at a time
+bool in_eights(const void* p, int64_t stride, int dtype, uint32_t dim) {
+  return lies_at(p, 16) && (uint64_t)stride * element_size(dtype) % 16 == 0 && dim % 8 == 0;
+}
+
+}  // namespace
+}  // namespace tokgb
+
+using namespace tokgb;
+
+extern "C" {
+
+int tok_embed(tok_handle* h, const tok_embed_args* a, void* stream) try {
+  if (!h) return TOK_EINVAL;
+  if (a && a->n == 0) return TOK_OK;
+  if (!a || !a->d_ids || !a->d_weight || !a->d_out) return fail(h, TOK_EINVAL, "embed: a buffer is NULL");
+  if (!element_size(a->weight_dtype) || !element_size(a->out_dtype)) return fail(h, TOK_EINVAL, "embed: unknown type");
+  if (!sizes_ok(a->n, a->n_rows, a->dim) || a->weight_stride < (int64_t)a->dim || a->out_stride < (int64_t)a->dim)
+    return fail(h, TOK_EINVAL, "embed: n, n_rows, dim or a stride is out of range");
+  if (!lies_at(a->d_ids, 4) || !lies_at(a->d_n, 8) || !lies_at(a->d_weight, element_size(a->weight_dtype)) ||
+      !lies_at(a->d_out, element_size(a->out_dtype)))
+    return fail(h, TOK_EINVAL, "embed: an array does not lie at a multiple of its type's size");
+  DeviceGuard g(h->dev);
+  EmbedCall c{a->d_ids, reinterpret_cast<const long long*>(a->d_n), (uint32_t)a->n, a->n_rows, a->dim,
+              (a->dim + EM_U * COLS - 1) / (EM_U * COLS), a->d_weight, a->weight_stride, a->d_out, a->out_stride, a->scale};
+  const uint64_t ctas = (a->n * c.segs + EM_THREADS / 32 - 1) / (EM_THREADS / 32);
+  if (ctas > 0x7fffffffull) return fail(h, TOK_EINVAL, "embed: n times dim is out of range");
+  const bool eights = in_eights(a->d_weight, a->weight_stride, a->weight_dtype, a->dim) &&
+                      in_eights(a->d_out, a->out_stride, a->out_dtype, a->dim);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  with_type(a->weight_dtype, [&](auto ti) {
+    with_type(a->out_dtype, [&](auto to) {
+      if (eights) k_embed<decltype(ti), decltype(to)><<<(unsigned)ctas, EM_THREADS, 0, s>>>(c);
+      else k_embed_any<decltype(ti), decltype(to)><<<(unsigned)ctas, EM_THREADS, 0, s>>>(c);
+    });
+  });
+  return finish(h, 1);
+} catch (...) {
+  return TOK_ENOMEM;
+}
+
+uint64_t tok_embed_work_bytes(uint64_t n, uint32_t n_rows, uint32_t dim) {
+  return sizes_ok(n, n_rows, dim) ? plan_of(n, n_rows, dim).bytes : 0;
+}
+
+int tok_embed_backward(tok_handle* h, const tok_embed_grad_args* a, void* stream) try {
+  if (!h) return TOK_EINVAL;
+  if (a && a->n == 0 && a->accumulate) return TOK_OK;
+  if (!a || !a->d_grad_weight || (a->n && (!a->d_ids || !a->d_grad_out)))
+    return fail(h, TOK_EINVAL, "embed gradient: a buffer is NULL");
+  if (!element_size(a->grad_weight_dtype) || !element_size(a->grad_out_dtype))
+    return fail(h, TOK_EINVAL, "embed gradient: unknown type");
+  if (!sizes_ok(a->n, a->n_rows, a->dim) || a->grad_weight_stride < (int64_t)a->dim ||
+      (a->n && a->grad_out_stride < (int64_t)a->dim))
+    return fail(h, TOK_EINVAL, "embed gradient: n, n_rows, dim or a stride is out of range");
+  if (!lies_at(a->d_ids, 4) || !lies_at(a->d_n, 8) || !lies_at(a->d_grad_weight, element_size(a->grad_weight_dtype)) ||
+      !lies_at(a->d_grad_out, element_size(a->grad_out_dtype)))
+    return fail(h, TOK_EINVAL, "embed gradient: an array does not lie at a multiple of its type's size");
+  const Plan p = plan_of(a->n, a->n_rows, a->dim);
+  if (!a->d_work || !lies_at(a->d_work, 256) || a->work_bytes < p.bytes)
+    return fail(h, TOK_EINVAL, "embed gradient: d_work is NULL, not at a multiple of 256 bytes or too small");
+  DeviceGuard g(h->dev);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* work = static_cast<uint8_t*>(a->d_work);
+  const long long* n_dev = reinterpret_cast<const long long*>(a->d_n);
+  SortCall sc{a->d_ids, n_dev, (uint32_t)a->n, a->n_rows, p.span, p.spans, p.bits0, p.bits1,
+              reinterpret_cast<uint32_t*>(work + p.counts0), reinterpret_cast<uint32_t*>(work + p.counts1),
+              reinterpret_cast<uint2*>(work + p.half), reinterpret_cast<uint2*>(work + p.sorted)};
+  SumCall c{sc.sorted, n_dev, (uint32_t)a->n, a->n_rows, a->dim, p.segs, p.chunk, p.chunks, a->scale, a->d_grad_out,
+            a->grad_out_stride, a->d_grad_weight, a->grad_weight_stride, reinterpret_cast<float*>(work + p.parts), 0};
+  unsigned launches = 0;
+  if (a->n) {
+    auto room = [](uint32_t bits) { return ((size_t)4 << bits) + ((size_t)2 * (ST_WARPS + 1) << bits); };
+    cudaError_t e = allow_all<k_sort_place<0>>(h->dev);
+    if (e == cudaSuccess) e = allow_all<k_sort_place<1>>(h->dev);
+    if (e != cudaSuccess) return cuda_fail(h, e, "shared memory of a kernel");
+    k_sort_count<<<p.spans, ST_THREADS, 0, s>>>(sc);
+    k_sort_place<0><<<p.spans, ST_THREADS, room(p.bits0), s>>>(sc);
+    if (p.bits1) k_sort_place<1><<<p.spans, ST_THREADS, room(p.bits1), s>>>(sc);
+    launches += p.bits1 ? 3 : 2;
+  }
+  constexpr uint64_t WARPS = EM_THREADS / 32;
+  c.sum_ctas = (uint32_t)(((uint64_t)p.chunks * p.segs + WARPS - 1) / WARPS);
+  const uint32_t empty_ctas = a->accumulate ? 0 : (a->n_rows + 32 * WARPS - 1) / (32 * WARPS);
+  const uint64_t join_ctas = p.chunks > 1 ? (uint64_t)(p.chunks - 1) * p.segs : 0;
+  if ((uint64_t)p.chunks * p.segs > 0x7fffffffull) return fail(h, TOK_EINVAL, "embed gradient: n times dim is out of range");
+  const bool eights = in_eights(a->d_grad_out, a->grad_out_stride, a->grad_out_dtype, a->dim) &&
+                      in_eights(a->d_grad_weight, a->grad_weight_stride, a->grad_weight_dtype, a->dim);
+  with_type(a->grad_out_dtype, [&](auto tg) {
+    with_type(a->grad_weight_dtype, [&](auto tw) {
+      using TG = decltype(tg);
+      using TW = decltype(tw);
+      auto both = [&](auto vec, auto add) {
+        k_embed_sum<TG, TW, vec.value, add.value><<<c.sum_ctas + empty_ctas, EM_THREADS, 0, s>>>(c);
+        if (join_ctas) k_embed_join<TG, TW, vec.value, add.value><<<(unsigned)join_ctas, EM_THREADS, 0, s>>>(c);
+      };
+      if (eights && a->accumulate) both(std::true_type{}, std::true_type{});
+      else if (eights) both(std::true_type{}, std::false_type{});
+      else if (a->accumulate) both(std::false_type{}, std::true_type{});
+      else both(std::false_type{}, std::false_type{});
+    });
+  });
+  return finish(h, launches + (join_ctas ? 2 : 1));
+} catch (...) {
+  return TOK_ENOMEM;
+}
+
+}  // extern "C"

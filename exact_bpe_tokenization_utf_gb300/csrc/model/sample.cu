@@ -1,0 +1,722 @@
+// The choice of a token for each row of scores (tok_sample).
+//
+// With M = the largest score and T = the temperature, w(v) = exp((x(v) - M) / T).  The
+// tokens in the order of falling scores, equal ones by their ids, form a list from
+// which min-p keeps those with w >= m, top-k the first k of these, top-p the shortest
+// beginning whose sum reaches p times the whole; the choice is the first at which
+// the running sum exceeds u times the sum of what is left.
+//
+// Every border lies where a running sum reaches a number, so that two sums formed
+// differently could disagree about it.  Weights are therefore 43-bit fixed-point
+// numbers, formed with 38 bits or more, and sums are whole numbers: they do not depend
+// on the order in which threads add.
+//
+// A row is read once: a cluster of CTAs holds it in shared memory.  After the
+// maximum, each token is counted in one of 1,024 bins of equal width of log w, with
+// its weight.  The bins' sums say in which bin a border lies; the tokens of that bin
+// (a few hundred at most, as a rule) go to the cluster's first CTA, which sorts them.
+// Where there are more, bins of keys (scores as whole numbers of the same order) come
+// in between, until a bin holds few tokens or a single score.
+#include "types.cuh"
+
+#include <cooperative_groups.h>
+
+namespace tokgb {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr uint32_t ALL = 0xffffffffu;
+constexpr uint32_t MOST_LOGITS = 1u << 20;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int BINS = 1024;                    // of 2^-4 in log2 w each, the last one for all below
+constexpr int BIN_SHIFT = 12;                 // from 2^-16 in log2 w
+constexpr int PER_BIN = BINS / THREADS;
+constexpr uint32_t LIST = 1024;               // most tokens that are sorted
+constexpr double ONE = 8796093022208.0;       // the largest weight, 2^43; 2^20 of them fit 64 bits
+constexpr int MOST_COMMANDS = 64;             // three goals of at most 8 each; a limit, so that the kernel ends
+constexpr float LOWEST = -62.f;               // log2 of weights that count (below 2^-43 they are 0 anyway)
+constexpr int LOWEST_K = -(BINS << BIN_SHIFT);
+
+// --- weights ---------------------------------------------------------------------
+
+// 2^(i / 256) and 2^(i / 65536) - 1 by their series, evaluated by the compiler
+struct Pow { unsigned long long whole; uint32_t top; float near; };   // 2^39, 2^31 times, and as it is
+struct Fine { uint32_t less; float near; };                          // 2^40 times, and as it is
+struct Powers { Pow a[256]; Fine b[256]; };
+constexpr double exp_less_1(double x) {   // |x| < 0.7
+  double term = x, sum = 0;
+  for (int i = 2; i < 30; ++i) {
+    sum += term;
+    term = term * x / i;
+  }
+  return sum;
+}
+constexpr Powers make_powers() {
+  Powers p{};
+  constexpr double ln2 = 0.693147180559945309417;
+  for (int i = 0; i < 256; ++i) {
+    const double x = 1.0 + exp_less_1(i * ln2 / 256), y = exp_less_1(i * ln2 / 65536);
+    p.a[i] = Pow{(unsigned long long)(x * 549755813888.0 + 0.5), (uint32_t)(x * 2147483648.0 + 0.5), (float)x};
+    p.b[i] = Fine{(uint32_t)(y * 1099511627776.0 + 0.5), (float)y};
+  }
+  return p;
+}
+__device__ const Powers g_powers = make_powers();
+
+// a row's temperature and maximum, for weights
+struct Rule {
+  float c_hi, c_lo;     // log2(e) / T
+  float p_max, e_max;   // the largest score's c x, in two parts
+  float x_max;
+  bool only_max;        // no other weight is above 0
+};
+
+__device__ __forceinline__ void times_c(const Rule& r, float x, float& p, float& e) {
+  p = __fmul_rn(x, r.c_hi);   // (not to be joined with the subtraction after it)
+  e = fmaf(x, r.c_hi, -p);
+  e = fmaf(x, r.c_lo, e);
+}
+
+// log2 w in two parts: hi rounded to 32 bits (it never rises where x falls), and the rest
+__device__ __forceinline__ void log2_weight(const Rule& r, float x, float& hi, float& lo) {
+  float p, e;
+  times_c(r, x, p, e);
+  const float d = p - r.p_max;                       // exact with err
+  const float back = d - p;
+  const float err = (p - (d - back)) + (-r.p_max - back);
+  e = (e - r.e_max) + err;
+  hi = d + e;
+  lo = e - (hi - d);
+  if (r.only_max || !(d > -1e4f)) {
+    hi = x == r.x_max ? 0.f : -1e4f;
+    lo = 0.f;
+  }
+}
+
+// log2 w in units of 2^-16 (at most 0), and what is left of it
+__device__ __forceinline__ int fixed_log2(float hi, float lo, float& rest) {
+  if (hi < LOWEST) return LOWEST_K;
+  constexpr float MAGIC = 192.f;                     // 1.5 * 2^7: its last place is 2^-16
+  const float m = hi + MAGIC;
+  rest = (hi - (m - MAGIC)) + lo;
+  return min(__float_as_int(m) - __float_as_int(MAGIC), 0);
+}
+__device__ __forceinline__ uint32_t bin_of(int k) { return min((uint32_t)-k >> BIN_SHIFT, (uint32_t)BINS - 1u); }
+
+// 2^43 times w: 2^(k / 65536 + rest) is a whole power of 2, two factors from the
+// tables and 1 + q for the rest (below 2^-17), so that 32-bit arithmetic on q is enough.
+__device__ __forceinline__ unsigned long long weight(const Pow* a, const Fine* b, int k, float rest) {
+  if (k == LOWEST_K) return 0;
+  const Pow x = a[(k >> 8) & 255];
+  const Fine y = b[k & 255];
+  constexpr float L1 = 0.693147180559945f, L2 = 0.240226506959101f;   // ln 2, (ln 2)^2 / 2
+  const float q = rest * fmaf(rest, L2, L1);
+  const int v = __float2int_rn(fmaf(x.near, y.near, x.near) * 549755813888.f * q);
+  const unsigned long long s = x.whole + __umulhi(x.top, y.less) + (long long)v;   // 2^39 times
+  return (((s << 5) >> -(k >> 16)) + 1) >> 1;
+}
+
+__device__ __forceinline__ uint32_t key_of(float x) {   // whole numbers of the same order
+  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);   // (-0 is 0)
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+
+// --- the kernel --------------------------------------------------------------------
+
+enum Op { OP_DONE, OP_BINS, OP_GATHER, OP_NTH };
+
+struct Command {
+  int op;
+  uint32_t lo, hi;      // keys: the tokens that it is about
+  uint32_t shift;       // OP_BINS: bin = (hi - key) >> shift
+  uint32_t nth;         // OP_NTH: which of the tokens of key lo, in the order of ids
+  int by_bin;           // the tokens of a bin of log w instead (its keys' range comes back), or -1
+};
+
+struct Shared {
+  Pow pow[256];
+  Fine fine[256];
+  uint32_t cnt[BINS], low[BINS], high[BINS];         // this CTA's bins
+  // the first CTA's: sums over all bins up to each
+  unsigned long long mass[BINS];
+  uint32_t upto[BINS];
+  union {
+    struct { unsigned long long mass[BINS]; uint32_t upto[BINS]; } sub;   // of bins of keys
+    unsigned long long list[LIST];                                        // (~key, id)
+  };
+  unsigned long long scan_m[WARPS];
+  uint32_t scan_c[WARPS];
+  float part_max[16];
+  uint32_t part_cnt[16], part_lo[16], part_hi[16];
+  Rule rule;
+  float log_min_p;                                   // T ln(min_p), for the threshold
+  double t_ln_m;
+  float least;                                       // scores below are not kept
+  uint32_t listed;
+  Command cmd;
+  uint32_t found;
+  unsigned long long answer_mass;
+  uint32_t answer_cnt;
+};
+
+struct Slice {
+  const void* at;        // element `from` (in shared memory, or the row's)
+  uint32_t from, to;
+};
+
+// By all threads: one(place, element) for the elements before and after the 16-byte
+// pieces that the slice has, piece(place, its elements) for these.
+template <class T, class F, class G>
+__device__ __forceinline__ void for_vectors(const Slice& s, F one, G piece) {
+  const T* x = static_cast<const T*>(s.at);
+  const uint32_t n = s.to - s.from;
+  constexpr uint32_t VEC = 16 / sizeof(T);
+  const uint32_t head = min(n, (uint32_t)((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / (uint32_t)sizeof(T));
+  const uint32_t vecs = (n - head) / VEC, tail = head + vecs * VEC;
+  for (uint32_t i = threadIdx.x; i < head + (n - tail); i += THREADS) {
+    const uint32_t e = i < head ? i : tail + (i - head);
+    one(e, x[e]);
+  }
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < vecs; i += THREADS) piece(head + i * VEC, reinterpret_cast<const uint4*>(x + head)[i]);
+}
+// f(score, id) for every element
+template <class T, class F>
+__device__ __forceinline__ void for_each(const Slice& s, F f) {
+  for_vectors<T>(s, [&](uint32_t e, T x) { f(to_f32(x), s.from + e); }, [&](uint32_t e, uint4 q) {
+    const T* y = reinterpret_cast<const T*>(&q);
+#pragma unroll
+    for (uint32_t i = 0; i < 16 / sizeof(T); ++i) f(to_f32(y[i]), s.from + e + i);
+  });
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+struct SampleCall {
+  tok_sample_args a;
+  uint32_t ranks;     // CTAs of a row
+  uint32_t per;       // elements of a CTA
+  int resident;       // its elements are kept in shared memory
+};
+
+// sums over the threads before, and of all (in every thread)
+__device__ __forceinline__ void block_scan(Shared& sh, uint32_t& c, unsigned long long& m, uint32_t& all_c, unsigned long long& all_m) {
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  uint32_t ic = c;
+  unsigned long long im = m;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t pc = __shfl_up_sync(ALL, ic, o);
+    const unsigned long long pm = __shfl_up_sync(ALL, im, o);
+    if (lane >= (uint32_t)o) {
+      ic += pc;
+      im += pm;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    sh.scan_c[warp] = ic;
+    sh.scan_m[warp] = im;
+  }
+  __syncthreads();
+  uint32_t bc = 0;
+  unsigned long long bm = 0;
+  all_c = 0;
+  all_m = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < (int)warp) {
+      bc += sh.scan_c[w];
+      bm += sh.scan_m[w];
+    }
+    all_c += sh.scan_c[w];
+    all_m += sh.scan_m[w];
+  }
+  c = bc + ic - c;
+  m = bm + im - m;
+}
+
+template <class T>
+__global__ void __launch_bounds__(THREADS) k_sample(SampleCall c) {
+  extern __shared__ __align__(16) uint8_t mem[];
+  Shared& sh = *reinterpret_cast<Shared*>(mem);
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t rank = cluster.block_rank(), row = blockIdx.x / c.ranks, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+  const uint32_t V = c.a.n_logits;
+  Slice s;
+  s.from = min(rank * c.per, V);
+  s.to = min(s.from + c.per, V);
+  const T* src = static_cast<const T*>(c.a.d_scores) + (long long)row * c.a.scores_stride + s.from;
+  const float temp = c.a.d_temperature ? c.a.d_temperature[row] : 1.f;
+  const float min_p = c.a.d_min_p ? c.a.d_min_p[row] : 0.f;
+
+  // the largest score; the slice into shared memory, lying towards 16 bytes as it does in the row
+  float most = -INFINITY;
+  s.at = src;
+  if (c.resident) {
+    T* keep = reinterpret_cast<T*>(mem + ((sizeof(Shared) + 15) & ~size_t(15)) + (reinterpret_cast<uintptr_t>(src) & 15u));
+    for_vectors<T>(s, [&](uint32_t e, T x) {
+      most = max_nan(most, to_f32(x));
+      keep[e] = x;
+    }, [&](uint32_t e, uint4 q) {
+      *reinterpret_cast<uint4*>(keep + e) = q;
+      const T* y = reinterpret_cast<const T*>(&q);
+#pragma unroll
+      for (uint32_t i = 0; i < 16 / sizeof(T); ++i) most = max_nan(most, to_f32(y[i]));
+    });
+    s.at = keep;
+  } else {
+    for_each<T>(s, [&](float x, uint32_t) { most = max_nan(most, x); });
+  }
+  for (uint32_t i = tid; i < 256; i += THREADS) {
+    sh.pow[i] = g_powers.a[i];
+    sh.fine[i] = g_powers.b[i];
+  }
+  for (uint32_t i = tid; i < BINS; i += THREADS) sh.cnt[i] = sh.low[i] = sh.high[i] = 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) most = max_nan(most, __shfl_xor_sync(ALL, most, o));
+  if (lane == 0) sh.scan_c[warp] = __float_as_uint(most);
+  if (tid == 32) {
+    const double t = temp >= 0x1p-100f ? fmin((double)temp, 3e38) : 1.0, k = 1.4426950408889634074 / t;
+    sh.rule.c_hi = (float)k;
+    sh.rule.c_lo = (float)(k - (double)(float)k);
+    sh.t_ln_m = min_p > 0.f ? t * log((double)min_p) : 0.0;
+  }
+  __syncthreads();
+  most = __uint_as_float(sh.scan_c[lane % WARPS]);
+#pragma unroll
+  for (int o = WARPS / 2; o; o >>= 1) most = max_nan(most, __shfl_xor_sync(ALL, most, o));
+  if (tid < c.ranks) cluster.map_shared_rank(&sh, tid)->part_max[rank] = most;
+  cluster.sync();
+  most = -INFINITY;
+  for (uint32_t i = 0; i < c.ranks; ++i) most = max_nan(most, sh.part_max[i]);
+  if (!(temp >= 0.f) || !(most > -INFINITY && most < INFINITY)) {   // (all CTAs of the row)
+    if (rank == 0 && tid == 0) {
+      c.a.d_pick[row] = -1;
+      if (c.a.d_kept) c.a.d_kept[row] = 0;
+      if (c.a.d_logprob) c.a.d_logprob[row] = -INFINITY;
+    }
+    return;
+  }
+  Rule r = sh.rule;
+  r.x_max = most;
+  r.p_max = r.e_max = 0.f;
+  times_c(r, most, r.p_max, r.e_max);
+  r.only_max = temp < 0x1p-100f || !(fabsf(r.p_max) < INFINITY);
+  float least = -INFINITY;
+  if (min_p > 0.f) {
+    // the scores from M + T ln(min_p) on (T = 0: M)
+    const double d = temp >= 0x1p-100f ? (double)most + sh.t_ln_m : (double)most;
+    least = __double2float_ru(fmin(d, 3.402823466e38));
+    if (min_p > 1.f) least = INFINITY;
+  }
+  // what a token of the row is counted as; false: it is not kept
+  auto look = [&](float x, int& k, float& rest) {
+    if (!(x >= least) || x == -INFINITY) return false;
+    float hi, lo;
+    log2_weight(r, x, hi, lo);
+    k = fixed_log2(hi, lo, rest);
+    return true;
+  };
+  auto count_in = [&](uint32_t bin, unsigned long long w) {
+    atomicAdd(&sh.cnt[bin], 1u);
+    const uint32_t w_lo = (uint32_t)w, old = atomicAdd(&sh.low[bin], w_lo);
+    const uint32_t carry = (uint32_t)(w >> 32) + (old + w_lo < old ? 1u : 0u);
+    if (carry) atomicAdd(&sh.high[bin], carry);
+  };
+  for_each<T>(s, [&](float x, uint32_t) {
+    int k;
+    float rest = 0.f;
+    if (look(x, k, rest)) count_in(bin_of(k), weight(sh.pow, sh.fine, k, rest));
+  });
+  cluster.sync();
+  // the row's bins: each CTA adds a share of them, for the first one
+  auto add_up = [&](bool sub) {
+    Shared* first = cluster.map_shared_rank(&sh, 0);
+    const uint32_t share = (BINS + c.ranks - 1) / c.ranks, b0 = min(rank * share, (uint32_t)BINS), b1 = min(b0 + share, (uint32_t)BINS);
+    for (uint32_t b = b0 + tid; b < b1; b += THREADS) {
+      uint32_t n = 0;
+      unsigned long long m = 0;
+      for (uint32_t i = 0; i < c.ranks; ++i) {
+        const Shared* o = cluster.map_shared_rank(&sh, i);
+        n += o->cnt[b];
+        m += o->low[b] + ((unsigned long long)o->high[b] << 32);
+      }
+      (sub ? first->sub.upto : first->upto)[b] = n;
+      (sub ? first->sub.mass : first->mass)[b] = m;
+    }
+  };
+  add_up(false);
+  cluster.sync();
+
+  // sums of the bins up to each (in the first CTA)
+  uint32_t all_c = 0;
+  unsigned long long all_m = 0;
+  auto run_up = [&](uint32_t* upto, unsigned long long* mass) {
+    uint32_t n[PER_BIN], bc = 0;
+    unsigned long long m[PER_BIN], bm = 0;
+#pragma unroll
+    for (int i = 0; i < PER_BIN; ++i) {
+      n[i] = upto[tid * PER_BIN + i];
+      m[i] = mass[tid * PER_BIN + i];
+      bc += n[i];
+      bm += m[i];
+    }
+    block_scan(sh, bc, bm, all_c, all_m);
+#pragma unroll
+    for (int i = 0; i < PER_BIN; ++i) {
+      bc += n[i];
+      bm += m[i];
+      upto[tid * PER_BIN + i] = bc;
+      mass[tid * PER_BIN + i] = bm;
+    }
+    __syncthreads();
+  };
+  // the first bin at which a sum reaches a number
+  auto bin_at = [&](const uint32_t* upto, const unsigned long long* mass, bool by_count, unsigned long long target) {
+    uint32_t lo = 0, hi = BINS - 1;
+    while (lo < hi) {
+      const uint32_t mid = (lo + hi) / 2;
+      if ((by_count ? (unsigned long long)upto[mid] : mass[mid]) >= target) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo;
+  };
+
+  // The goals in turn: the last token of top-k (by count), of top-p (by mass), the
+  // choice (by mass).  The first CTA decides, all CTAs carry out.
+  enum { GOAL_K, GOAL_P, GOAL_U, GOAL_END };
+  int goal = GOAL_K;
+  bool started = false;                    // a goal's bin is being looked into
+  uint32_t kept = 0;                       // tokens kept so far
+  unsigned long long kept_m = 0;           // and their mass
+  unsigned long long target = 0;           // of the goal
+  uint32_t before_c = 0;                   // tokens before the range that is looked into
+  unsigned long long before_m = 0;
+  uint32_t pick_key = 0;
+  float top_p = 1.f, u = 0.f;
+  if (rank == 0) {
+    run_up(sh.upto, sh.mass);
+    kept = all_c;
+    kept_m = all_m;
+    top_p = c.a.d_top_p ? c.a.d_top_p[row] : 1.f;
+    u = c.a.d_random[row];
+  }
+  // The state after an answer: the first at which the goal's sum is reached is the
+  // cnt-th token, the sum up to it mass.
+  auto answered = [&](uint32_t cnt, unsigned long long mass) {
+    if (goal != GOAL_U) {
+      kept = cnt;
+      kept_m = mass;
+    }
+    ++goal;
+    started = false;
+  };
+  for (int commands = 0;; ++commands) {
+    if (rank == 0) {
+      Command cmd{};
+      cmd.by_bin = -1;
+      // (all threads of the first CTA come to the same decision)
+      while (goal != GOAL_END && !started) {
+        if (goal == GOAL_K) {
+          const int k = c.a.d_top_k ? c.a.d_top_k[row] : 0;
+          if (k <= 0 || (uint32_t)k >= kept) {
+            ++goal;
+            continue;
+          }
+          target = (uint32_t)k;
+        } else if (goal == GOAL_P) {
+          if (!(top_p < 1.f) || kept == 0) {
+            ++goal;
+            continue;
+          }
+          // ceil(p * mass), p's 24 bits exactly
+          const float p = fmaxf(top_p, 0.f);
+          const unsigned long long f = __double2ull_rd((double)p * 18446744073709551616.0);
+          target = __umul64hi(f, kept_m) + (f * kept_m != 0 ? 1 : 0);
+          if (target == 0) target = 1;
+        } else {
+          if (kept == 0) break;
+          const float v = u >= 0.f ? u : 0.f;
+          target = v < 1.f ? __umul64hi(__double2ull_rd((double)v * 18446744073709551616.0), kept_m) + 1 : kept_m;
+        }
+        const uint32_t b = bin_at(sh.upto, sh.mass, goal == GOAL_K, target);
+        before_c = b ? sh.upto[b - 1] : 0;
+        before_m = b ? sh.mass[b - 1] : 0;
+        const uint32_t n = sh.upto[b] - before_c;
+        if (goal != GOAL_U && (goal == GOAL_K ? target == sh.upto[b] : n == 1)) {
+          answered(sh.upto[b], sh.mass[b]);
+          continue;
+        }
+        started = true;
+        cmd.by_bin = (int)b;
+        cmd.op = n <= LIST ? OP_GATHER : OP_BINS;   // (OP_BINS with by_bin: only the range of its keys)
+      }
+      if (goal != GOAL_END && kept && cmd.by_bin < 0 && started) cmd = sh.cmd;   // set by the last answer
+      if (commands >= MOST_COMMANDS) cmd.op = OP_DONE;
+      if (tid < c.ranks) cluster.map_shared_rank(&sh, tid)->cmd = cmd;
+      if (tid == 0) {
+        sh.listed = 0;
+        sh.found = ALL;
+      }
+    }
+    cluster.sync();
+    const Command cmd = sh.cmd;
+    if (cmd.op == OP_DONE) break;
+    auto wanted = [&](float x, int& k, float& rest) {
+      if (cmd.by_bin >= 0) return look(x, k, rest) && bin_of(k) == (uint32_t)cmd.by_bin;
+      const uint32_t key = key_of(x);
+      if (key < cmd.lo || key > cmd.hi) return false;
+      return look(x, k, rest);
+    };
+    if (cmd.op == OP_GATHER) {
+      Shared* first = cluster.map_shared_rank(&sh, 0);
+      for_each<T>(s, [&](float x, uint32_t id) {
+        int k;
+        float rest;
+        if (wanted(x, k, rest)) {
+          const uint32_t at = atomicAdd(&first->listed, 1u);
+          if (at < LIST) first->list[at] = (unsigned long long)(~key_of(x)) << 32 | id;
+        }
+      });
+      cluster.sync();
+      if (rank == 0) {
+        const uint32_t n = min(sh.listed, LIST);
+        uint32_t size = 32;
+        while (size < n) size *= 2;
+        for (uint32_t i = n + tid; i < size; i += THREADS) sh.list[i] = ~0ull;
+        __syncthreads();
+        for (uint32_t k = 2; k <= size; k *= 2)
+          for (uint32_t j = k / 2; j; j /= 2) {
+            for (uint32_t i = tid; i < size / 2; i += THREADS) {
+              const uint32_t a = 2 * i - (i & (j - 1)), b = a + j;
+              const unsigned long long x = sh.list[a], y = sh.list[b];
+              if ((x > y) == ((a & k) == 0)) {
+                sh.list[a] = y;
+                sh.list[b] = x;
+              }
+            }
+            __syncthreads();
+          }
+        // sums up to each token, and the first that reaches the target
+        unsigned long long w[2], sum = 0;
+        uint32_t cnt = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          w[i] = 0;
+          if (tid * 2 + i < n) {
+            int k;
+            float rest = 0.f;
+            look(of_key(~(uint32_t)(sh.list[tid * 2 + i] >> 32)), k, rest);
+            w[i] = weight(sh.pow, sh.fine, k, rest);
+            ++cnt;
+          }
+          sum += w[i];
+        }
+        uint32_t ac;
+        unsigned long long am;
+        block_scan(sh, cnt, sum, ac, am);
+        unsigned long long m = before_m + sum;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (tid * 2 + i < n) {
+            const unsigned long long next = m + w[i];
+            const uint32_t at = before_c + tid * 2 + i + 1;
+            if (goal == GOAL_K ? at == target : m < target && next >= target) {
+              sh.answer_cnt = at;
+              sh.answer_mass = next;
+              sh.found = (uint32_t)sh.list[tid * 2 + i];
+              pick_key = ~(uint32_t)(sh.list[tid * 2 + i] >> 32);
+              sh.cmd.lo = pick_key;
+            }
+            m = next;
+          }
+        __syncthreads();
+        pick_key = sh.cmd.lo;
+        answered(sh.answer_cnt, sh.answer_mass);
+        if (goal == GOAL_END) {
+          __syncthreads();
+        }
+      }
+    } else if (cmd.op == OP_BINS && cmd.by_bin >= 0) {
+      // the range of the bin's keys
+      uint32_t lo = ALL, hi = 0;
+      for_each<T>(s, [&](float x, uint32_t) {
+        int k;
+        float rest;
+        if (wanted(x, k, rest)) {
+          lo = min(lo, key_of(x));
+          hi = max(hi, key_of(x));
+        }
+      });
+      lo = __reduce_min_sync(ALL, lo);
+      hi = __reduce_max_sync(ALL, hi);
+      if (tid == 0) {
+        sh.scan_c[0] = ALL;
+        sh.scan_c[1] = 0;
+      }
+      __syncthreads();
+      if (lane == 0) {
+        atomicMin(&sh.scan_c[0], lo);
+        atomicMax(&sh.scan_c[1], hi);
+      }
+      __syncthreads();
+      if (tid == 0) {
+        cluster.map_shared_rank(&sh, 0)->part_lo[rank] = sh.scan_c[0];
+        cluster.map_shared_rank(&sh, 0)->part_hi[rank] = sh.scan_c[1];
+      }
+      cluster.sync();
+      if (rank == 0) {
+        Command next{};
+        next.by_bin = -1;
+        next.op = OP_BINS;
+        next.lo = ALL;
+        for (uint32_t i = 0; i < c.ranks; ++i) {
+          next.lo = min(next.lo, sh.part_lo[i]);
+          next.hi = max(next.hi, sh.part_hi[i]);
+        }
+        while ((next.hi - next.lo) >> next.shift >= BINS) ++next.shift;
+        __syncthreads();
+        if (tid == 0) sh.cmd = next;
+        __syncthreads();
+      }
+    } else if (cmd.op == OP_BINS) {
+      for (uint32_t i = tid; i < BINS; i += THREADS) sh.cnt[i] = sh.low[i] = sh.high[i] = 0;
+      __syncthreads();
+      for_each<T>(s, [&](float x, uint32_t) {
+        int k;
+        float rest = 0.f;
+        if (wanted(x, k, rest)) count_in((cmd.hi - key_of(x)) >> cmd.shift, weight(sh.pow, sh.fine, k, rest));
+      });
+      cluster.sync();
+      add_up(true);
+      cluster.sync();
+      if (rank == 0) {
+        uint32_t keep_c = all_c;
+        const unsigned long long keep_m = all_m;
+        run_up(sh.sub.upto, sh.sub.mass);
+        all_c = keep_c;
+        all_m = keep_m;
+        const unsigned long long rest = target - (goal == GOAL_K ? (unsigned long long)before_c : before_m);
+        const uint32_t b = bin_at(sh.sub.upto, sh.sub.mass, goal == GOAL_K, rest);
+        const uint32_t bc = b ? sh.sub.upto[b - 1] : 0, n = sh.sub.upto[b] - bc;
+        const unsigned long long bm = b ? sh.sub.mass[b - 1] : 0, m = sh.sub.mass[b] - bm;
+        Command next{};
+        next.by_bin = -1;
+        next.hi = cmd.hi - (b << cmd.shift);
+        const uint32_t down = (1u << cmd.shift) - 1u;
+        next.lo = next.hi - cmd.lo > down ? next.hi - down : cmd.lo;
+        before_c += bc;
+        before_m += bm;
+        __syncthreads();
+        if (n <= LIST) {
+          next.op = OP_GATHER;
+        } else if (cmd.shift) {
+          next.op = OP_BINS;
+          while ((next.hi - next.lo) >> next.shift >= BINS) ++next.shift;
+        } else {
+          // tokens of one score, all of the same weight: by their number
+          const unsigned long long one = m / n, left = target - (goal == GOAL_K ? (unsigned long long)before_c : before_m);
+          const uint32_t nth = goal == GOAL_K ? (uint32_t)left : one ? (uint32_t)((left + one - 1) / one) : 1u;
+          pick_key = next.lo;
+          if (goal == GOAL_U) {
+            next.op = OP_NTH;
+            next.nth = nth;
+          } else {
+            answered(before_c + nth, before_m + nth * one);
+          }
+        }
+        if (tid == 0) sh.cmd = next;
+        __syncthreads();
+      }
+    } else {
+      // the nth token of one score, in the order of ids: each thread counts its run of elements
+      const T* x = static_cast<const T*>(s.at);
+      const uint32_t n = s.to - s.from, per = (n + THREADS - 1) / THREADS, e0 = min(tid * per, n), e1 = min(e0 + per, n);
+      uint32_t mine = 0;
+      for (uint32_t e = e0; e < e1; ++e) mine += key_of(to_f32(x[e])) == cmd.lo;
+      uint32_t at = mine, all;
+      unsigned long long zero = 0, zeros;
+      block_scan(sh, at, zero, all, zeros);
+      if (tid < c.ranks) cluster.map_shared_rank(&sh, tid)->part_cnt[rank] = all;
+      cluster.sync();
+      for (uint32_t i = 0; i < rank; ++i) at += sh.part_cnt[i];
+      if (at < cmd.nth && cmd.nth <= at + mine) {
+        for (uint32_t e = e0; e < e1; ++e)
+          if (key_of(to_f32(x[e])) == cmd.lo && ++at == cmd.nth) cluster.map_shared_rank(&sh, 0)->found = s.from + e;
+      }
+      cluster.sync();
+      if (rank == 0) answered(0, 0);
+    }
+    if (rank == 0 && goal == GOAL_END) {
+      __syncthreads();
+      if (tid == 0) {
+        c.a.d_pick[row] = (int32_t)sh.found;
+        if (c.a.d_kept) c.a.d_kept[row] = (int32_t)kept;
+        if (c.a.d_logprob) {
+          float hi, lo;
+          log2_weight(r, of_key(pick_key), hi, lo);
+          c.a.d_logprob[row] = (float)(((double)hi + lo) * 0.693147180559945309417 - log((double)kept_m / ONE));
+        }
+      }
+      __syncthreads();
+    }
+  }
+  // (min-p above 1 keeps nothing)
+  if (rank == 0 && tid == 0 && kept == 0) {
+    c.a.d_pick[row] = -1;
+    if (c.a.d_kept) c.a.d_kept[row] = 0;
+    if (c.a.d_logprob) c.a.d_logprob[row] = -INFINITY;
+  }
+}
+
+template <class T>
+cudaError_t launch(tok_handle* h, const tok_sample_args* a, cudaStream_t s) {
+  SampleCall c{};
+  c.a = *a;
+  uint32_t n = 1;
+  while (n < 16 && (a->n_logits / n > 65536 || (a->n_logits / n > 4096 && (uint64_t)a->rows * n * 2 <= 2ull * (uint32_t)h->n_sms))) n *= 2;
+  c.ranks = n;
+  c.per = (a->n_logits + n - 1) / n;
+  c.per = (c.per + 7) / 8 * 8;
+  const size_t base = (sizeof(Shared) + 15) & ~size_t(15), slice = (size_t)c.per * sizeof(T) + 16;
+  c.resident = base + slice <= MOST_SHARED;
+  return launch_clusters<k_sample<T>>(h->dev, a->rows * n, THREADS, n, base + (c.resident ? slice : 0), s, c);
+}
+
+}  // namespace
+}  // namespace tokgb
+
+using namespace tokgb;
+
+extern "C" {
+
+int tok_sample(tok_handle* h, const tok_sample_args* a, void* stream) try {
+  if (!h) return TOK_EINVAL;
+  if (a && a->rows == 0) return TOK_OK;
+  if (!a || !a->d_scores || !a->d_random || !a->d_pick) return fail(h, TOK_EINVAL, "sample: a buffer is NULL");
+  if (!element_size(a->dtype)) return fail(h, TOK_EINVAL, "sample: unknown type");
+  if (a->n_logits == 0 || a->n_logits > MOST_LOGITS || a->rows > 0x7ffffffu || a->scores_stride < (int64_t)a->n_logits)
+    return fail(h, TOK_EINVAL, "sample: rows, n_logits or scores_stride is out of range");
+  if (!lies_at(a->d_scores, element_size(a->dtype)) || !lies_at(a->d_temperature, 4) || !lies_at(a->d_min_p, 4) ||
+      !lies_at(a->d_top_k, 4) || !lies_at(a->d_top_p, 4) || !lies_at(a->d_random, 4) || !lies_at(a->d_pick, 4) ||
+      !lies_at(a->d_kept, 4) || !lies_at(a->d_logprob, 4))
+    return fail(h, TOK_EINVAL, "sample: an array does not lie at a multiple of its type's size");
+  DeviceGuard g(h->dev);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a->dtype == TOK_F32 ? launch<float>(h, a, s) : a->dtype == TOK_F16 ? launch<__half>(h, a, s)
+                                                                                             : launch<__nv_bfloat16>(h, a, s);
+  h->launches += 1;
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? TOK_OK : cuda_fail(h, e, "kernel launch");
+} catch (...) {
+  return TOK_ENOMEM;
+}
+
+}  // extern "C"

@@ -439,6 +439,190 @@ int tok_grammar_mask(tok_handle* h, const tok_grammar* g, const int32_t* d_state
                      const int64_t* d_item_off, uint32_t n, int32_t eos, int32_t* d_state_out, uint32_t n_logits,
                      uint32_t* d_mask, int64_t mask_stride, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * At the model's two ends and at its cache.  Like the entry points above:
+ * device buffers, no host synchronisation, no allocation, CUDA graphs.  What a
+ * call needs beside its inputs and outputs is a buffer of the caller's (d_work,
+ * at a multiple of 256 bytes); its contents need not survive the call, and two
+ * calls that may overlap on the GPU (two captured graphs, say) need one each.
+ * ------------------------------------------------------------------------- */
+
+/* tok_embed -- the rows of a batch's ids.  With n' = min(n, *d_n) (d_n NULL: n;
+ * tok_encode_batch_device writes such a count at d_item_off + its n),
+ *   out[t][j] = scale * weight[ids[t]][j]   for t < n', j < dim
+ * in 32 bits, rounded once; zeros for an id outside 0 .. n_rows - 1.  Rows of
+ * out from n' on are left as they were.
+ */
+typedef struct {
+  const int32_t* d_ids;      /* n */
+  uint64_t n;                /* below 2^31 */
+  const int64_t* d_n;        /* NULL: n ids; a count below 0 is 0 */
+  const void* d_weight;      /* rows of dim, weight_stride elements apart */
+  int64_t weight_stride;
+  int32_t weight_dtype;      /* TOK_F32, TOK_F16 or TOK_BF16, as out_dtype */
+  uint32_t n_rows;           /* 1 .. 2^20 */
+  uint32_t dim;              /* 1 .. 2^20 */
+  float scale;
+  void* d_out;
+  int64_t out_stride;
+  int32_t out_dtype;
+} tok_embed_args;
+
+/* Errors: TOK_EINVAL (NULL buffers, an unknown type, n, n_rows or dim out of
+ * range, a stride below a row, an array that does not lie at a multiple of its
+ * type's size), TOK_ECUDA.  n == 0 does nothing, whatever the buffers. */
+int tok_embed(tok_handle* h, const tok_embed_args* a, void* stream);
+
+/* tok_embed_backward -- the gradient of tok_embed with respect to the weights:
+ *   grad_weight[v][j] = scale * sum of grad_out[t][j] over t < n' with ids[t] == v
+ * Tokens are sorted by their ids; a row's sum is in 32 bits, in an order that
+ * n, d_n's value, the types and the strides fix alone: the same bits each time.
+ * accumulate == 0: the n_rows rows are written whole (zeros where no id is v).
+ * accumulate != 0: the sum is added, in 32 bits, to the rows that ids name, and
+ * the others are neither read nor written.
+ */
+typedef struct {
+  const int32_t* d_ids;      /* as in tok_embed_args */
+  uint64_t n;
+  const int64_t* d_n;
+  uint32_t n_rows;
+  uint32_t dim;
+  float scale;
+  const void* d_grad_out;    /* rows of dim; from n' on they are not read */
+  int64_t grad_out_stride;
+  int32_t grad_out_dtype;
+  void* d_grad_weight;       /* must not overlap grad_out */
+  int64_t grad_weight_stride;
+  int32_t grad_weight_dtype;
+  int32_t accumulate;
+  void* d_work;              /* tok_embed_work_bytes(n, n_rows, dim) */
+  uint64_t work_bytes;
+} tok_embed_grad_args;
+
+/* Errors: as tok_embed; TOK_EINVAL for a d_work that is NULL, not at a multiple
+ * of 256 bytes or too small.  n == 0 with accumulate != 0 does nothing. */
+int tok_embed_backward(tok_handle* h, const tok_embed_grad_args* a, void* stream);
+
+/* Bytes of d_work that are enough for n ids or fewer (0 if n, n_rows or dim is out of range). */
+uint64_t tok_embed_work_bytes(uint64_t n, uint32_t n_rows, uint32_t dim);
+
+/* tok_sample -- one token for each row of scores (logits, or what
+ * tok_logits_process left of them), by the row's rules and a random number.
+ * With M = the row's largest score and T = temperature[b], in exact arithmetic,
+ *   w(v) = exp((scores[b][v] - M) / T)          (T == 0: 1 for M, 0 below)
+ * and the tokens above -inf in the order of falling scores, equal ones by
+ * their ids,
+ *   min_p > 0:  only tokens with w >= min_p are kept
+ *   top_k > 0:  of these the first top_k
+ *   top_p < 1:  of these the shortest beginning whose sum of w is at least
+ *               top_p times that of all of them (top_p <= 0: the first one)
+ * What is kept, in that order, is the list that the choice is from: pick[b] is its
+ * first token at which the running sum of w exceeds random[b] times the whole
+ * sum (random below 0 or NaN: 0; from 1 on: the last of the list whose w is not
+ * below 2^-40), kept[b] the list's length, logprob[b] = log(w(pick) / the sum).
+ * The weights are formed to within 2^-36 of the largest one and summed exactly,
+ * so a border of top_p or random is met unless it lies closer than that, and
+ * results are the same bits each time.  A NaN in min_p or top_p is no rule.
+ * A row in which nothing is above -inf, with a score of NaN or +inf, or with a
+ * temperature below 0 or NaN has pick -1, kept 0 and logprob -inf.
+ */
+typedef struct {
+  const void* d_scores;       /* rows of n_logits, scores_stride elements apart */
+  int64_t scores_stride;
+  int32_t dtype;              /* TOK_F32, TOK_F16 or TOK_BF16 */
+  uint32_t rows;
+  uint32_t n_logits;          /* 1 .. 2^20 */
+  const float* d_temperature; /* rows; NULL: 1 (this and the next three: no rule where NULL) */
+  const float* d_min_p;       /* rows */
+  const int32_t* d_top_k;     /* rows; 0 or less: no rule */
+  const float* d_top_p;       /* rows */
+  const float* d_random;      /* rows, in [0, 1) */
+  int32_t* d_pick;            /* rows */
+  int32_t* d_kept;            /* rows; NULL: not wanted (this and the next) */
+  float* d_logprob;           /* rows */
+} tok_sample_args;
+
+/* Errors: TOK_EINVAL (NULL buffers, an unknown type, scores that do not lie at
+ * a multiple of their type's size, rows or n_logits out of range, a stride below
+ * a row), TOK_ECUDA.  rows == 0 does nothing, whatever the buffers. */
+int tok_sample(tok_handle* h, const tok_sample_args* a, void* stream);
+
+/* A paged cache of keys and values: token place p of block b has, for key head
+ * h, the head_dim elements from b * block_stride + p * token_stride + h *
+ * head_stride on, in both arrays.  Slots and tables are those of
+ * tok_paged_assign: slot = block * block_size + place.
+ * The arrays lie at multiples of 16 bytes and the strides are multiples of 8. */
+typedef struct {
+  void* d_k;
+  void* d_v;
+  int64_t block_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t dtype;        /* TOK_F16 or TOK_BF16 */
+  uint32_t n_blocks;
+  uint32_t block_size;  /* 1 .. 2^20 */
+  uint32_t kv_heads;    /* 1 .. 1024 */
+  uint32_t head_dim;    /* a multiple of 8, 8 .. 256 */
+} tok_kv_cache;
+
+/* tok_paged_store -- new tokens' keys and values into the cache, at the slots
+ * that tok_paged_assign gave them.  Tokens whose slot is outside
+ * 0 .. n_blocks * block_size - 1 are skipped (-1: a padded batch).  Slots are
+ * distinct; where two tokens name one, each 16 bytes there are either's.
+ */
+typedef struct {
+  const void* d_k;       /* token t, head h: from t * token_stride + h * head_stride on, in the cache's type */
+  const void* d_v;       /* the same; both at multiples of 16 bytes, the strides multiples of 8 */
+  int64_t token_stride;
+  int64_t head_stride;
+  const int64_t* d_slot; /* n */
+  uint64_t n;            /* below 2^31 */
+} tok_store_args;
+
+/* Errors: TOK_EINVAL (NULL buffers, an unknown type, sizes, strides or
+ * addresses out of range), TOK_ECUDA.  n == 0 does nothing. */
+int tok_paged_store(tok_handle* h, const tok_kv_cache* c, const tok_store_args* a, void* stream);
+
+/* tok_paged_attend -- the attention of one new token of each request over the
+ * request's tokens in the cache.  Request k has L = seq_len[k] of them (the new
+ * one among them, as tok_paged_assign's d_seq_len counts; below 0: 0, beyond
+ * the table's row: what the row holds), token p in block table[k][p / block_size].
+ * Query head j reads key head j / (heads / kv_heads).  With
+ *   s(p) = scale * (q[k][j] . key(p))   for max(0, L - window) <= p < L (window 0: all),
+ *   out[k][j] = sum of exp(s(p)) value(p) / sum of exp(s(p)),   lse[k][j] = log sum of exp(s(p))
+ * Sums and the softmax are in 32 bits; the weights that the values are
+ * multiplied by are two 16-bit numbers each, out is rounded once.  A table
+ * entry outside 0 .. n_blocks - 1 hides its block's tokens; their memory is not
+ * read.  A request without a token to read has out 0 and lse -inf.
+ */
+typedef struct {
+  const void* d_q;        /* request k, head j: from k * q_stride + j * q_head_stride on, in the cache's type */
+  int64_t q_stride;
+  int64_t q_head_stride;
+  void* d_out;            /* the same with its strides; must not overlap the cache */
+  int64_t out_stride;
+  int64_t out_head_stride;
+  float* d_lse;           /* n rows of heads, back to back; NULL: not wanted */
+  uint32_t n;             /* up to 2^20 */
+  uint32_t heads;         /* a multiple of kv_heads, at most 64 times as many */
+  float scale;
+  uint32_t window;        /* 0: none */
+  const int32_t* d_table; /* n rows of max_blocks entries, table_stride apart */
+  int64_t table_stride;
+  uint32_t max_blocks;
+  const int64_t* d_seq_len; /* n */
+  void* d_work;           /* tok_paged_attend_work_bytes(h, n, heads, kv_heads, head_dim) */
+  uint64_t work_bytes;
+} tok_attend_args;
+
+/* Errors: TOK_EINVAL (NULL buffers, an unknown type, sizes, strides or
+ * addresses out of range: queries and out lie as the cache does), TOK_ECUDA.
+ * n == 0 does nothing. */
+int tok_paged_attend(tok_handle* h, const tok_kv_cache* c, const tok_attend_args* a, void* stream);
+
+/* Bytes of d_work that are enough for n requests or fewer (0 if a number is out of range). */
+uint64_t tok_paged_attend_work_bytes(tok_handle* h, uint32_t n, uint32_t heads, uint32_t kv_heads, uint32_t head_dim);
+
 /* tok_last_error -- message of the last failure on h (or of the last failed
  * tok_load when h is NULL).  The string is owned by the library and valid
  * until the next call on h. */
