@@ -123,6 +123,25 @@ __device__ __forceinline__ uint32_t key_of(float x) {   // whole numbers of the 
 }
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
+// scores below this are not kept: M + T ln(min_p) (T = 0: M)
+__device__ __forceinline__ float least_of(const Rule& r, float temp, float min_p, double t_ln_m) {
+  if (!(min_p > 0.f)) return -INFINITY;
+  if (min_p > 1.f) return INFINITY;
+  return __double2float_ru(temp >= 0x1p-100f ? (double)r.x_max + t_ln_m : (double)r.x_max);
+}
+
+// The sums that top-p's list and the choice have to reach, with all bits of p (below
+// 1) and u: the least whole number from p times the mass on, and above u times it.
+__device__ __forceinline__ unsigned long long enough(float p, unsigned long long mass) {
+  const unsigned long long f = __double2ull_rd((double)fmaxf(p, 0.f) * 18446744073709551616.0);
+  const unsigned long long m = __umul64hi(f, mass) + (f * mass != 0 ? 1 : 0);
+  return m ? m : 1;
+}
+__device__ __forceinline__ unsigned long long chosen_at(float u, unsigned long long mass) {
+  const float v = u >= 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f;
+  return __umul64hi(__double2ull_rd((double)v * 18446744073709551616.0), mass) + 1;
+}
+
 // --- the kernel --------------------------------------------------------------------
 
 enum Op { OP_DONE, OP_BINS, OP_GATHER, OP_NTH };
@@ -132,7 +151,8 @@ struct Command {
   uint32_t lo, hi;      // keys: the tokens that it is about
   uint32_t shift;       // OP_BINS: bin = (hi - key) >> shift
   uint32_t nth;         // OP_NTH: which of the tokens of key lo, in the order of ids
-  int by_bin;           // the tokens of a bin of log w instead (its keys' range comes back), or -1
+  int by_bin;           // the tokens of a bin of log w instead, or -1
+  int through;          // OP_GATHER: of all bins up to it
 };
 
 struct Shared {
@@ -151,14 +171,12 @@ struct Shared {
   float part_max[16];
   uint32_t part_cnt[16], part_lo[16], part_hi[16];
   Rule rule;
-  float log_min_p;                                   // T ln(min_p), for the threshold
-  double t_ln_m;
-  float least;                                       // scores below are not kept
+  double t_ln_m;                                     // T ln(min_p), for the threshold
   uint32_t listed;
   Command cmd;
   uint32_t found;
   unsigned long long answer_mass;
-  uint32_t answer_cnt;
+  uint32_t answer_cnt, answer_key;
 };
 
 struct Slice {
@@ -243,8 +261,7 @@ __device__ __forceinline__ void block_scan(Shared& sh, uint32_t& c, unsigned lon
 }
 
 template <class T>
-__global__ void __launch_bounds__(THREADS) k_sample(SampleCall c) {
-  extern __shared__ __align__(16) uint8_t mem[];
+__device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   Shared& sh = *reinterpret_cast<Shared*>(mem);
   cg::cluster_group cluster = cg::this_cluster();
   const uint32_t rank = cluster.block_rank(), row = blockIdx.x / c.ranks, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
@@ -309,13 +326,7 @@ __global__ void __launch_bounds__(THREADS) k_sample(SampleCall c) {
   r.p_max = r.e_max = 0.f;
   times_c(r, most, r.p_max, r.e_max);
   r.only_max = temp < 0x1p-100f || !(fabsf(r.p_max) < INFINITY);
-  float least = -INFINITY;
-  if (min_p > 0.f) {
-    // the scores from M + T ln(min_p) on (T = 0: M)
-    const double d = temp >= 0x1p-100f ? (double)most + sh.t_ln_m : (double)most;
-    least = __double2float_ru(fmin(d, 3.402823466e38));
-    if (min_p > 1.f) least = INFINITY;
-  }
+  const float least = least_of(r, temp, min_p, sh.t_ln_m);
   // what a token of the row is counted as; false: it is not kept
   auto look = [&](float x, int& k, float& rest) {
     if (!(x >= least) || x == -INFINITY) return false;
@@ -394,6 +405,7 @@ __global__ void __launch_bounds__(THREADS) k_sample(SampleCall c) {
   enum { GOAL_K, GOAL_P, GOAL_U, GOAL_END };
   int goal = GOAL_K;
   bool started = false;                    // a goal's bin is being looked into
+  bool listed = false;                     // all goals' tokens have been listed
   uint32_t kept = 0;                       // tokens kept so far
   unsigned long long kept_m = 0;           // and their mass
   unsigned long long target = 0;           // of the goal
@@ -401,13 +413,28 @@ __global__ void __launch_bounds__(THREADS) k_sample(SampleCall c) {
   unsigned long long before_m = 0;
   uint32_t pick_key = 0;
   float top_p = 1.f, u = 0.f;
+  int top_k = 0;
   if (rank == 0) {
     run_up(sh.upto, sh.mass);
     kept = all_c;
     kept_m = all_m;
+    top_k = c.a.d_top_k ? c.a.d_top_k[row] : 0;
     top_p = c.a.d_top_p ? c.a.d_top_p[row] : 1.f;
     u = c.a.d_random[row];
   }
+  // The number that the goal's sum has to reach; false: there is no such rule.
+  auto aim = [&]() {
+    if (goal == GOAL_K) {
+      target = (unsigned long long)max(top_k, 0);
+      return target != 0 && target < kept;
+    }
+    if (goal == GOAL_P) {
+      target = enough(top_p, kept_m);
+      return top_p < 1.f;
+    }
+    target = chosen_at(u, kept_m);
+    return true;
+  };
   // The state after an answer: the first at which the goal's sum is reached is the
   // cnt-th token, the sum up to it mass.
   auto answered = [&](uint32_t cnt, unsigned long long mass) {
@@ -423,30 +450,23 @@ __global__ void __launch_bounds__(THREADS) k_sample(SampleCall c) {
       Command cmd{};
       cmd.by_bin = -1;
       // (all threads of the first CTA come to the same decision)
-      while (goal != GOAL_END && !started) {
-        if (goal == GOAL_K) {
-          const int k = c.a.d_top_k ? c.a.d_top_k[row] : 0;
-          if (k <= 0 || (uint32_t)k >= kept) {
-            ++goal;
-            continue;
-          }
-          target = (uint32_t)k;
-        } else if (goal == GOAL_P) {
-          if (!(top_p < 1.f) || kept == 0) {
-            ++goal;
-            continue;
-          }
-          // ceil(p * mass), p's 24 bits exactly
-          const float p = fmaxf(top_p, 0.f);
-          const unsigned long long f = __double2ull_rd((double)p * 18446744073709551616.0);
-          target = __umul64hi(f, kept_m) + (f * kept_m != 0 ? 1 : 0);
-          if (target == 0) target = 1;
-        } else {
-          if (kept == 0) break;
-          const float v = u >= 0.f ? u : 0.f;
-          target = v < 1.f ? __umul64hi(__double2ull_rd((double)v * 18446744073709551616.0), kept_m) + 1 : kept_m;
+      while (goal != GOAL_END && kept && !started) {
+        if (!aim()) {
+          ++goal;
+          continue;
         }
         const uint32_t b = bin_at(sh.upto, sh.mass, goal == GOAL_K, target);
+        // where everything up to the first goal's bin fits the list, the goals after it
+        // lie there too: one list for all
+        if (!listed && sh.upto[b] <= LIST) {
+          listed = started = true;
+          before_c = 0;
+          before_m = 0;
+          cmd.by_bin = (int)b;
+          cmd.through = 1;
+          cmd.op = OP_GATHER;
+          continue;
+        }
         before_c = b ? sh.upto[b - 1] : 0;
         before_m = b ? sh.mass[b - 1] : 0;
         const uint32_t n = sh.upto[b] - before_c;
@@ -470,7 +490,11 @@ __global__ void __launch_bounds__(THREADS) k_sample(SampleCall c) {
     const Command cmd = sh.cmd;
     if (cmd.op == OP_DONE) break;
     auto wanted = [&](float x, int& k, float& rest) {
-      if (cmd.by_bin >= 0) return look(x, k, rest) && bin_of(k) == (uint32_t)cmd.by_bin;
+      if (cmd.by_bin >= 0) {
+        if (!look(x, k, rest)) return false;
+        const uint32_t b = bin_of(k);
+        return b == (uint32_t)cmd.by_bin || (cmd.through && b < (uint32_t)cmd.by_bin);
+      }
       const uint32_t key = key_of(x);
       if (key < cmd.lo || key > cmd.hi) return false;
       return look(x, k, rest);
@@ -522,27 +546,29 @@ __global__ void __launch_bounds__(THREADS) k_sample(SampleCall c) {
         uint32_t ac;
         unsigned long long am;
         block_scan(sh, cnt, sum, ac, am);
-        unsigned long long m = before_m + sum;
+        do {
+          unsigned long long m = before_m + sum;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (tid * 2 + i < n) {
-            const unsigned long long next = m + w[i];
-            const uint32_t at = before_c + tid * 2 + i + 1;
-            if (goal == GOAL_K ? at == target : m < target && next >= target) {
-              sh.answer_cnt = at;
-              sh.answer_mass = next;
-              sh.found = (uint32_t)sh.list[tid * 2 + i];
-              pick_key = ~(uint32_t)(sh.list[tid * 2 + i] >> 32);
-              sh.cmd.lo = pick_key;
+          for (int i = 0; i < 2; ++i)
+            if (tid * 2 + i < n) {
+              const unsigned long long next = m + w[i];
+              const uint32_t at = before_c + tid * 2 + i + 1;
+              if (goal == GOAL_K ? at == target : m < target && next >= target) {
+                sh.answer_cnt = at;
+                sh.answer_mass = next;
+                sh.found = (uint32_t)sh.list[tid * 2 + i];
+                sh.answer_key = ~(uint32_t)(sh.list[tid * 2 + i] >> 32);
+              }
+              m = next;
             }
-            m = next;
-          }
-        __syncthreads();
-        pick_key = sh.cmd.lo;
-        answered(sh.answer_cnt, sh.answer_mass);
-        if (goal == GOAL_END) {
           __syncthreads();
-        }
+          pick_key = sh.answer_key;
+          answered(sh.answer_cnt, sh.answer_mass);
+          __syncthreads();
+          // (a list of all tokens that matter serves the next goals)
+          if (listed)
+            while (goal < GOAL_U && !aim()) ++goal;
+        } while (listed && goal != GOAL_END && aim());
       }
     } else if (cmd.op == OP_BINS && cmd.by_bin >= 0) {
       // the range of the bin's keys
@@ -677,17 +703,426 @@ __global__ void __launch_bounds__(THREADS) k_sample(SampleCall c) {
 }
 
 template <class T>
+__global__ void __launch_bounds__(THREADS, 2) k_sample(SampleCall c) {
+  extern __shared__ __align__(16) uint8_t mem[];
+  choose<T>(c, mem);
+}
+
+// --- 16-bit scores -------------------------------------------------------------------
+
+// A row of 16-bit scores has few different ones: they are counted, score by score, and
+// a weight is formed once for each.  Places in the order of falling scores: positive
+// scores below 2^12, zero, negative ones above -2^12; what lies further down is only
+// counted, and must have no weight.  A row with other scores (2^12 or more, below
+// 2^-27 in bf16, NaN) takes the way above.
+template <class T> struct Places;
+template <> struct Places<__nv_bfloat16> {
+  static constexpr uint32_t LOW = 100u << 7, HIGH = 139u << 7, INF = 0x7f80;   // 2^-27, 2^12
+  using Count = uint32_t;
+};
+template <> struct Places<__half> {
+  static constexpr uint32_t LOW = 1, HIGH = 27u << 10, INF = 0x7c00;           // all, 2^12
+  using Count = uint16_t;                                                      // (as words they would not fit)
+};
+constexpr float FAR = -4096.f;
+constexpr int GROUP = 256;                 // places of a warp's step
+
+template <class T> struct Counts {
+  static constexpr uint32_t RANGE = Places<T>::HIGH - Places<T>::LOW;
+  static constexpr uint32_t N = 2 * RANGE + 1, GROUPS = (N + GROUP - 1) / GROUP;
+  using Count = typename Places<T>::Count;
+  Pow pow[256];
+  Fine fine[256];
+  __align__(16) Count at[GROUPS * GROUP];
+  // the first CTA's: of each group, then up to each
+  unsigned long long mass[GROUPS];
+  uint32_t upto[GROUPS];
+  uint32_t part_best[16], part_far[16], part_odd[16], part_cnt[16];
+  uint32_t best, far, odd;
+  uint32_t warp_cnt[WARPS];
+  Rule rule;
+  double t_ln_m;
+  uint32_t pick_bits, nth, found;          // the choice is the nth of this score (nth 0: there is none)
+
+  // the place of a score that has one
+  static __device__ __forceinline__ float score(uint32_t place) {
+    const uint32_t bits = place < RANGE ? Places<T>::HIGH - 1 - place : place == RANGE ? 0u : 0x8000u | (place - RANGE - 1 + Places<T>::LOW);
+    if (sizeof(Count) == 4) return __uint_as_float(bits << 16);
+    return __half2float(__ushort_as_half((unsigned short)bits));
+  }
+  __device__ __forceinline__ void add(uint32_t place, uint32_t n) {
+    if (sizeof(Count) == 4) atomicAdd(reinterpret_cast<uint32_t*>(at) + place, n);
+    else atomicAdd(reinterpret_cast<uint32_t*>(at) + (place >> 1), n << (place & 1u) * 16);
+  }
+};
+
+// sums over the lanes before, and up to this one
+__device__ __forceinline__ void warp_scan(uint32_t& c, unsigned long long& m) {
+  const uint32_t lane = threadIdx.x & 31u;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t pc = __shfl_up_sync(ALL, c, o);
+    const unsigned long long pm = __shfl_up_sync(ALL, m, o);
+    if (lane >= (uint32_t)o) {
+      c += pc;
+      m += pm;
+    }
+  }
+}
+
+// true: the row is done; false: it has scores that this way does not take (in all CTAs alike)
+template <class T>
+__device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem) {
+  using C = Counts<T>;
+  constexpr uint32_t RANGE = C::RANGE, LOW = Places<T>::LOW;
+  C& sh = *reinterpret_cast<C*>(mem);
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t rank = cluster.block_rank(), row = blockIdx.x / c.ranks, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+  const uint32_t V = c.a.n_logits;
+  Slice s;
+  s.from = min(rank * c.per, V);
+  s.to = min(s.from + c.per, V);
+  const uint16_t* src = static_cast<const uint16_t*>(c.a.d_scores) + (long long)row * c.a.scores_stride + s.from;
+  s.at = src;
+  const float temp = c.a.d_temperature ? c.a.d_temperature[row] : 1.f;
+  const float min_p = c.a.d_min_p ? c.a.d_min_p[row] : 0.f;
+  for (uint32_t i = tid; i < sizeof(sh.at) / 16; i += THREADS) reinterpret_cast<uint4*>(sh.at)[i] = make_uint4(0, 0, 0, 0);
+  for (uint32_t i = tid; i < 256; i += THREADS) {
+    sh.pow[i] = g_powers.a[i];
+    sh.fine[i] = g_powers.b[i];
+  }
+  if (tid == 32) {
+    const double t = temp >= 0x1p-100f ? fmin((double)temp, 3e38) : 1.0, k = 1.4426950408889634074 / t;
+    sh.rule.c_hi = (float)k;
+    sh.rule.c_lo = (float)(k - (double)(float)k);
+    sh.t_ln_m = min_p > 0.f ? t * log((double)min_p) : 0.0;
+  }
+  if (tid == 0) {
+    sh.best = ALL;
+    sh.far = sh.odd = 0;
+  }
+  __syncthreads();
+
+  // the scores are counted
+  uint32_t best = ALL, far = 0, odd = 0;
+  auto count = [&](uint32_t u) {
+    const uint32_t m = u & 0x7fffu, q = m - LOW;
+    if (q < RANGE) {
+      const uint32_t neg = u >> 15;
+      const uint32_t place = neg ? RANGE + 1 + q : RANGE - 1 - q;
+      best = min(best, place);
+      sh.add(place, 1);
+    } else if (m == 0) {
+      best = min(best, RANGE);
+      sh.add(RANGE, 1);
+    } else if ((u >> 15) && m > LOW && m <= Places<T>::INF) {
+      far += m < Places<T>::INF;   // (-inf is no token)
+    } else {
+      odd = 1;
+    }
+  };
+  for_vectors<uint16_t>(s, [&](uint32_t, uint16_t x) { count(x); }, [&](uint32_t, uint4 q) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      count(w[i] & 0xffffu);
+      count(w[i] >> 16);
+    }
+  });
+  best = __reduce_min_sync(ALL, best);
+  far = __reduce_add_sync(ALL, far);
+  odd = __any_sync(ALL, odd);
+  if (lane == 0) {
+    atomicMin(&sh.best, best);
+    if (far) atomicAdd(&sh.far, far);
+    if (odd) sh.odd = 1;
+  }
+  __syncthreads();
+  if (tid < c.ranks) {
+    C* o = cluster.map_shared_rank(&sh, tid);
+    o->part_best[rank] = sh.best;
+    o->part_far[rank] = sh.far;
+    o->part_odd[rank] = sh.odd;
+  }
+  cluster.sync();
+  best = ALL;
+  far = odd = 0;
+  for (uint32_t i = 0; i < c.ranks; ++i) {
+    best = min(best, sh.part_best[i]);
+    far += sh.part_far[i];
+    odd |= sh.part_odd[i];
+  }
+  if (odd || (best == ALL && far) || !(temp >= 0.f)) {
+    cluster.sync();
+    return false;
+  }
+  if (best == ALL) {
+    if (rank == 0 && tid == 0) {
+      c.a.d_pick[row] = -1;
+      if (c.a.d_kept) c.a.d_kept[row] = 0;
+      if (c.a.d_logprob) c.a.d_logprob[row] = -INFINITY;
+    }
+    return true;
+  }
+  Rule r = sh.rule;
+  r.x_max = C::score(best);
+  times_c(r, r.x_max, r.p_max, r.e_max);
+  r.only_max = temp < 0x1p-100f || !(fabsf(r.p_max) < INFINITY);
+  const float least = least_of(r, temp, min_p, sh.t_ln_m);
+  const int top_k = c.a.d_top_k ? c.a.d_top_k[row] : 0;
+  if (far) {
+    // the scores far down have no weight, and no rule reaches in among them
+    float hi, lo;
+    log2_weight(r, FAR, hi, lo);
+    if (hi >= LOWEST || (min_p > 0.f && least <= FAR)) {
+      cluster.sync();
+      return false;
+    }
+    if (min_p > 0.f) far = 0;
+  }
+  auto count_at = [&](uint32_t place) {   // in all CTAs
+    uint32_t n = 0;
+    for (uint32_t i = 0; i < c.ranks; ++i) n += cluster.map_shared_rank(&sh, i)->at[place];
+    return n;
+  };
+  // a lane's eight places of a group: how many tokens, and each one's weight
+  auto look = [&](uint32_t g, uint32_t* n, unsigned long long* w) {
+    const uint32_t place = g * GROUP + lane * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n[i] = 0;
+    for (uint32_t k = 0; k < c.ranks; ++k) {
+      const uint4* p = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&sh, k)->at + place);
+      const uint4 a = p[0];
+      if (sizeof(typename C::Count) == 4) {
+        const uint4 b = p[1];
+        n[0] += a.x; n[1] += a.y; n[2] += a.z; n[3] += a.w;
+        n[4] += b.x; n[5] += b.y; n[6] += b.z; n[7] += b.w;
+      } else {
+        n[0] += a.x & 0xffffu; n[1] += a.x >> 16; n[2] += a.y & 0xffffu; n[3] += a.y >> 16;
+        n[4] += a.z & 0xffffu; n[5] += a.z >> 16; n[6] += a.w & 0xffffu; n[7] += a.w >> 16;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] = 0;
+      if (n[i]) {
+        const float x = C::score(place + i);
+        if (x >= least) {
+          float hi, lo, rest = 0.f;
+          log2_weight(r, x, hi, lo);
+          const int k = fixed_log2(hi, lo, rest);
+          w[i] = weight(sh.pow, sh.fine, k, rest);
+        } else {
+          n[i] = 0;
+        }
+      }
+    }
+  };
+  C* first = cluster.map_shared_rank(&sh, 0);
+  for (uint32_t g = warp * c.ranks + rank; g < C::GROUPS; g += WARPS * c.ranks) {
+    uint32_t n[8], all = 0;
+    unsigned long long w[8], m = 0;
+    look(g, n, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      all += n[i];
+      m += n[i] * w[i];
+    }
+    all = __reduce_add_sync(ALL, all);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m += __shfl_xor_sync(ALL, m, o);
+    if (lane == 0) {
+      first->upto[g] = all;
+      first->mass[g] = m;
+    }
+  }
+  cluster.sync();
+
+  // the first CTA's first warp finds the borders
+  uint32_t kept = 0;
+  unsigned long long kept_m = 0;
+  if (rank == 0 && warp == 0) {
+    for (uint32_t g0 = 0; g0 < C::GROUPS; g0 += 32) {
+      uint32_t n = g0 + lane < C::GROUPS ? sh.upto[g0 + lane] : 0;
+      unsigned long long m = g0 + lane < C::GROUPS ? sh.mass[g0 + lane] : 0;
+      warp_scan(n, m);
+      n += kept;
+      m += kept_m;
+      if (g0 + lane < C::GROUPS) {
+        sh.upto[g0 + lane] = n;
+        sh.mass[g0 + lane] = m;
+      }
+      kept = __shfl_sync(ALL, n, 31);
+      kept_m = __shfl_sync(ALL, m, 31);
+    }
+    __syncwarp();
+    const uint32_t near = kept;
+    uint32_t place = 0, nth = 0;
+    // the token at which a sum reaches the target: its place, its number among that
+    // score's, how many tokens and what mass there are up to it
+    auto reach = [&](bool by_count, unsigned long long target, uint32_t& cnt, unsigned long long& mass) {
+      uint32_t g = 0;
+      for (uint32_t g0 = 0; g0 < C::GROUPS; g0 += 32) {
+        const bool below = g0 + lane < C::GROUPS && (by_count ? (unsigned long long)sh.upto[g0 + lane] : sh.mass[g0 + lane]) < target;
+        g += __popc(__ballot_sync(ALL, below));
+      }
+      g = min(g, C::GROUPS - 1);
+      uint32_t n[8], lane_n = 0;
+      unsigned long long w[8], lane_m = 0;
+      look(g, n, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lane_n += n[i];
+        lane_m += n[i] * w[i];
+      }
+      uint32_t upto_n = lane_n;
+      unsigned long long upto_m = lane_m;
+      warp_scan(upto_n, upto_m);
+      uint32_t at_n = upto_n - lane_n + (g ? sh.upto[g - 1] : 0);
+      unsigned long long at_m = upto_m - lane_m + (g ? sh.mass[g - 1] : 0);
+      uint32_t hit = ALL, hit_nth = 0, hit_n = 0;
+      unsigned long long hit_m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t next_n = at_n + n[i];
+        const unsigned long long next_m = at_m + n[i] * w[i];
+        if (by_count ? at_n < target && next_n >= target : at_m < target && next_m >= target) {
+          hit = g * GROUP + lane * 8 + i;
+          hit_nth = by_count ? (uint32_t)(target - at_n) : (uint32_t)((target - at_m + w[i] - 1) / w[i]);
+          hit_n = at_n + hit_nth;
+          hit_m = at_m + hit_nth * w[i];
+        }
+        at_n = next_n;
+        at_m = next_m;
+      }
+      const uint32_t who = __ffs(__ballot_sync(ALL, hit != ALL)) - 1;
+      place = __shfl_sync(ALL, hit, who);
+      nth = __shfl_sync(ALL, hit_nth, who);
+      cnt = __shfl_sync(ALL, hit_n, who);
+      mass = __shfl_sync(ALL, hit_m, who);
+    };
+    kept += far;
+    if (top_k > 0 && (uint32_t)top_k < kept) {
+      if ((uint32_t)top_k > near) kept = (uint32_t)top_k;   // (among those without weight)
+      else reach(true, (uint32_t)top_k, kept, kept_m);
+    }
+    const float top_p = c.a.d_top_p ? c.a.d_top_p[row] : 1.f;
+    if (kept && top_p < 1.f) {
+      reach(false, enough(top_p, kept_m), kept, kept_m);
+    }
+    uint32_t bits = 0;
+    if (kept) {
+      uint32_t n;
+      unsigned long long m;
+      reach(false, chosen_at(c.a.d_random[row], kept_m), n, m);
+      bits = place < RANGE ? Places<T>::HIGH - 1 - place : place == RANGE ? 0u : 0x8000u | (place - RANGE - 1 + LOW);
+    }
+    if (lane < c.ranks) {
+      C* o = cluster.map_shared_rank(&sh, lane);
+      o->pick_bits = bits;
+      o->nth = kept ? nth : 0;
+    }
+    if (lane == 0) {
+      if (c.a.d_kept) c.a.d_kept[row] = (int32_t)kept;
+      if (c.a.d_logprob) {
+        float hi, lo;
+        log2_weight(r, C::score(place), hi, lo);
+        c.a.d_logprob[row] = kept ? (float)(((double)hi + lo) * 0.693147180559945309417 - log((double)kept_m / ONE)) : -INFINITY;
+      }
+      if (!kept) c.a.d_pick[row] = -1;
+    }
+  }
+  cluster.sync();
+  const uint32_t nth = sh.nth;
+  if (nth == 0) return true;
+  // the nth token of that score in the order of ids: a warp has a run of the slice
+  const uint32_t want = sh.pick_bits, n = s.to - s.from;
+  const uint32_t head = min(n, (uint32_t)((16u - (reinterpret_cast<uintptr_t>(src) & 15u)) & 15u) / 2u), vecs = (n - head) / 8, tail = head + vecs * 8;
+  const uint32_t run = (vecs + WARPS - 1) / WARPS, v0 = min(warp * run, vecs), v1 = min(v0 + run, vecs);
+  auto same = [&](uint32_t u) { return u == want || (want == 0 && u == 0x8000u); };
+  auto match = [&](uint32_t v) {   // of the eight scores of a piece, as bits
+    const uint4 q = reinterpret_cast<const uint4*>(src + head)[v];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m |= (same(w[i] & 0xffffu) ? 1u : 0u) << (2 * i) | (same(w[i] >> 16) ? 2u : 0u) << (2 * i);
+    return m;
+  };
+  const bool has_head = warp == 0 && lane < head && same(src[lane]), has_tail = warp == WARPS - 1 && lane < n - tail && same(src[tail + lane]);
+  uint32_t mine = (has_head ? 1 : 0) + (has_tail ? 1 : 0);
+#pragma unroll 4
+  for (uint32_t v = v0 + lane; v < v1; v += 32) mine += __popc(match(v));
+  const uint32_t here = __reduce_add_sync(ALL, mine);
+  if (lane == 0) sh.warp_cnt[warp] = here;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < (int)warp) before += sh.warp_cnt[w];
+    all += sh.warp_cnt[w];
+  }
+  if (tid < c.ranks) cluster.map_shared_rank(&sh, tid)->part_cnt[rank] = all;
+  cluster.sync();
+  for (uint32_t i = 0; i < rank; ++i) before += sh.part_cnt[i];
+  if (before < nth && nth <= before + here) {   // (a warp as a whole)
+    uint32_t left = nth - before;               // the left-th of the warp's
+    auto among = [&](uint32_t ballot, uint32_t base) {
+      const uint32_t k = __popc(ballot);
+      if (left && left <= k) {
+        c.a.d_pick[row] = (int32_t)(s.from + base + __fns(ballot, 0, (int)left));
+        left = 0;
+      } else if (left) {
+        left -= k;
+      }
+    };
+    if (warp == 0) among(__ballot_sync(ALL, has_head), 0);
+    for (uint32_t v = v0; v < v1 && left; v += 32) {
+      const uint32_t m = v + lane < v1 ? match(v + lane) : 0;
+      uint32_t upto = __popc(m);
+      const uint32_t cnt = upto;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t p = __shfl_up_sync(ALL, upto, o);
+        if (lane >= (uint32_t)o) upto += p;
+      }
+      const uint32_t total = __shfl_sync(ALL, upto, 31);
+      if (upto - cnt < left && left <= upto)
+        c.a.d_pick[row] = (int32_t)(s.from + head + (v + lane) * 8 + __fns(m, 0, (int)(left - (upto - cnt))));
+      left = total >= left ? 0 : left - total;
+    }
+    if (warp == WARPS - 1) among(__ballot_sync(ALL, has_tail), tail);
+  }
+  return true;
+}
+
+template <class T>
+__device__ __noinline__ void choose_any(const SampleCall& c, uint8_t* mem) { choose<T>(c, mem); }
+
+template <class T>
+__global__ void __launch_bounds__(THREADS, 2) k_sample_counted(const __grid_constant__ SampleCall c) {
+  extern __shared__ __align__(16) uint8_t mem[];
+  if (!choose_counted<T>(c, mem)) choose_any<T>(c, mem);
+}
+
+template <class T>
 cudaError_t launch(tok_handle* h, const tok_sample_args* a, cudaStream_t s) {
   SampleCall c{};
   c.a = *a;
+  const size_t base = (sizeof(Shared) + 15) & ~size_t(15);
   uint32_t n = 1;
-  while (n < 16 && (a->n_logits / n > 65536 || (a->n_logits / n > 4096 && (uint64_t)a->rows * n * 2 <= 2ull * (uint32_t)h->n_sms))) n *= 2;
+  while (n < 16 && (a->n_logits / n > 65000 || (a->n_logits / n > 4096 && (uint64_t)a->rows * n * 2 <= 2ull * (uint32_t)h->n_sms))) n *= 2;
   c.ranks = n;
   c.per = (a->n_logits + n - 1) / n;
   c.per = (c.per + 7) / 8 * 8;
-  const size_t base = (sizeof(Shared) + 15) & ~size_t(15), slice = (size_t)c.per * sizeof(T) + 16;
-  c.resident = base + slice <= MOST_SHARED;
-  return launch_clusters<k_sample<T>>(h->dev, a->rows * n, THREADS, n, base + (c.resident ? slice : 0), s, c);
+  if constexpr (sizeof(T) == 2) {
+    // (a CTA's count of a score has to fit; 2^20 scores are too many for 16 CTAs)
+    if (sizeof(typename Places<T>::Count) == 4 || c.per < 65536)
+      return launch_clusters<k_sample_counted<T>>(h->dev, a->rows * n, THREADS, n, std::max(base, sizeof(Counts<T>)), s, c);
+  }
+  {
+    const size_t slice = (size_t)c.per * sizeof(T) + 16;
+    c.resident = base + slice <= MOST_SHARED;
+    return launch_clusters<k_sample<T>>(h->dev, a->rows * n, THREADS, n, base + (c.resident ? slice : 0), s, c);
+  }
 }
 
 }  // namespace

@@ -509,7 +509,7 @@ uint64_t tok_embed_work_bytes(uint64_t n, uint32_t n_rows, uint32_t dim);
 /* tok_sample -- one token for each row of scores (logits, or what
  * tok_logits_process left of them), by the row's rules and a random number.
  * With M = the row's largest score and T = temperature[b], in exact arithmetic,
- *   w(v) = exp((scores[b][v] - M) / T)          (T == 0: 1 for M, 0 below)
+ *   w(v) = exp((scores[b][v] - M) / T)          (T below 2^-100: 1 for M, 0 below)
  * and the tokens above -inf in the order of falling scores, equal ones by
  * their ids,
  *   min_p > 0:  only tokens with w >= min_p are kept
@@ -518,11 +518,10 @@ uint64_t tok_embed_work_bytes(uint64_t n, uint32_t n_rows, uint32_t dim);
  *               top_p times that of all of them (top_p <= 0: the first one)
  * What is kept, in that order, is the list that the choice is from: pick[b] is its
  * first token at which the running sum of w exceeds random[b] times the whole
- * sum (random below 0 or NaN: 0; from 1 on: the last of the list whose w is not
- * below 2^-40), kept[b] the list's length, logprob[b] = log(w(pick) / the sum).
- * The weights are formed to within 2^-36 of the largest one and summed exactly,
- * so a border of top_p or random is met unless it lies closer than that, and
- * results are the same bits each time.  A NaN in min_p or top_p is no rule.
+ * sum (random below 0 or NaN: 0; from 1 on: 1 - 2^-24), kept[b] the list's length, logprob[b] = log(w(pick) / the sum).
+ * The weights are formed to within 2^-36 of their size, in steps of 2^-43 of the
+ * largest one, and summed exactly: a border of top_p or random is met unless it
+ * lies closer than that, and results are the same bits each time.  A NaN in min_p or top_p is no rule.
  * A row in which nothing is above -inf, with a score of NaN or +inf, or with a
  * temperature below 0 or NaN has pick -1, kept 0 and logprob -inf.
  */
