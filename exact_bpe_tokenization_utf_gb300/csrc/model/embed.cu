@@ -13,6 +13,10 @@
 // length; a warp adds a chunk's rows over 256 columns.  A run of equal ids inside
 // a chunk is a finished row of dW; what a chunk's first and last run share with
 // the neighbours goes to d_work, and a second kernel adds those parts in order.
+//
+// The rows that no token names are written as zeros: most of a small batch's bytes.
+// Which these are is known from the first kernel on (a bit for each row), so that the
+// sort's kernels, a few CTAs that wait for chains of latencies, write a part of them.
 #include "types.cuh"
 
 namespace tokgb {
@@ -100,6 +104,7 @@ constexpr int ST_THREADS = 512, ST_WARPS = ST_THREADS / 32, ST_PER = 8;
 constexpr int ST_TILE = ST_THREADS * ST_PER;
 constexpr int MOST_BITS = 11, MOST_DIGITS = 1 << MOST_BITS;
 constexpr uint32_t MOST_SPANS = 152;
+constexpr uint64_t SORT_BYTES = 48u << 20;   // zeros that are written beside a pass of the sort (about 8 us)
 
 struct SortCall {
   const int32_t* ids;
@@ -110,6 +115,7 @@ struct SortCall {
   uint32_t bits0, bits1;
   uint32_t* counts0;   // spans rows of 2^bits0
   uint32_t* counts1;   // spans rows of 2^bits1
+  uint32_t* named;     // spans rows of a bit for each row of the weights: whether the span's ids name it; or nullptr
   uint2* half;         // (key, token) after the first pass of two
   uint2* sorted;       // and at the end
 };
@@ -130,23 +136,79 @@ __device__ __forceinline__ uint32_t alike(uint32_t d, bool in, uint32_t bits) {
   return in ? m : 0u;
 }
 
-// counts of the first digit in each span; the second's counts are set to 0
+// rows of the weights that get zeros, in blocks of 32
+struct Empty {
+  const uint32_t* named;
+  uint32_t spans, n_rows, words;
+  uint8_t* rows;
+  long long stride;       // bytes
+  unsigned long long row; // bytes
+  int eights;             // rows are multiples of 16 bytes and lie at such
+  uint32_t element;       // bytes
+};
+
+// block b's rows by all threads of the CTA (up to 1,024)
+__device__ __forceinline__ void write_empty(const Empty& e, uint32_t b) {
+  __shared__ uint32_t s_named;
+  if (threadIdx.x < 32) {
+    uint32_t m = 0;
+    for (uint32_t s = threadIdx.x; s < e.spans; s += 32) m |= e.named[(size_t)s * e.words + b];
+    m = __reduce_or_sync(ALL, m);
+    if (threadIdx.x == 0) s_named = m;
+  }
+  __syncthreads();
+  uint32_t left = ~s_named;
+  const uint32_t rows = min(32u, e.n_rows - b * 32);
+  if (rows < 32) left &= (1u << rows) - 1u;
+  // each warp takes rows in turn
+  for (uint32_t k = 0; left; left &= left - 1, ++k) {
+    if (k % (blockDim.x >> 5) != threadIdx.x >> 5) continue;
+    uint8_t* to = e.rows + (long long)(b * 32 + __ffs(left) - 1) * e.stride;
+    const uint32_t lane = threadIdx.x & 31u;
+    if (e.eights) {
+      for (unsigned long long i = lane * 16; i < e.row; i += 512) *reinterpret_cast<uint4*>(to + i) = make_uint4(0, 0, 0, 0);
+    } else if (e.element == 4) {
+      for (unsigned long long i = lane * 4; i < e.row; i += 128) *reinterpret_cast<uint32_t*>(to + i) = 0;
+    } else {
+      for (unsigned long long i = lane * 2; i < e.row; i += 64) *reinterpret_cast<uint16_t*>(to + i) = 0;
+    }
+  }
+}
+
+// counts of the first digit in each span, and the rows that it names; the second
+// digit's counts are set to 0
 __global__ void __launch_bounds__(ST_THREADS) k_sort_count(SortCall c) {
-  __shared__ uint32_t s_count[MOST_DIGITS];
-  const uint32_t n = count_of(c.n_dev, c.n), digits = 1u << c.bits0, tid = threadIdx.x;
-  for (uint32_t d = tid; d < digits; d += ST_THREADS) s_count[d] = 0;
+  extern __shared__ __align__(16) uint8_t mem[];
+  uint32_t* s_count = reinterpret_cast<uint32_t*>(mem);
+  uint32_t* s_named = s_count + (1u << c.bits0);
+  let_next_start();
+  const uint32_t n = count_of(c.n_dev, c.n), digits = 1u << c.bits0, words = (c.n_rows + 31) / 32, tid = threadIdx.x;
+  for (uint32_t d = tid; d < digits + (c.named ? words : 0u); d += ST_THREADS) s_count[d] = 0;
   __syncthreads();
   const uint32_t begin = min(blockIdx.x * c.span, n), end = min(begin + c.span, n);
-  for (uint32_t t = begin + tid; t < end; t += ST_THREADS) atomicAdd(&s_count[key_of(c.ids[t], c.n_rows) & (digits - 1)], 1u);
+#pragma unroll 4
+  for (uint32_t t = begin + tid; t < end; t += ST_THREADS) {
+    const uint32_t k = key_of(c.ids[t], c.n_rows);
+    atomicAdd(&s_count[k & (digits - 1)], 1u);
+    if (c.named && k < c.n_rows) atomicOr(&s_named[k >> 5], 1u << (k & 31u));
+  }
   __syncthreads();
   for (uint32_t d = tid; d < digits; d += ST_THREADS) c.counts0[(size_t)blockIdx.x * digits + d] = s_count[d];
+  if (c.named)
+    for (uint32_t w = tid; w < words; w += ST_THREADS) c.named[(size_t)blockIdx.x * words + w] = s_named[w];
   if (c.bits1)
     for (uint32_t d = tid; d < (1u << c.bits1); d += ST_THREADS) c.counts1[((size_t)blockIdx.x << c.bits1) + d] = 0;
 }
 
 template <int PASS>
-__global__ void __launch_bounds__(ST_THREADS) k_sort_place(SortCall c) {
+__global__ void __launch_bounds__(ST_THREADS) k_sort_place(SortCall c, Empty empty, uint32_t empty_from) {
   extern __shared__ __align__(16) uint8_t mem[];
+  wait_for_previous();
+  let_next_start();
+  if (blockIdx.x >= c.spans) {
+    write_empty(empty, empty_from + blockIdx.x - c.spans);
+    return;
+  }
   const uint32_t bits = PASS == 0 ? c.bits0 : c.bits1, digits = 1u << bits, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
   uint32_t* base = reinterpret_cast<uint32_t*>(mem);                    // [digits] where a digit's next token goes
   uint16_t* count = reinterpret_cast<uint16_t*>(base + digits);         // [ST_WARPS][digits]
@@ -271,7 +333,7 @@ struct SumCall {
   void* grad_weight;
   long long grad_weight_stride;
   float* parts;                   // [chunks][2][dim rounded up to COLS]: first and last run of a chunk
-  uint32_t sum_ctas;              // CTAs that add; the others write the rows without tokens
+  uint32_t sum_ctas;              // CTAs that add; the others write rows without tokens
 };
 
 // a lane's eight columns: side by side (VEC), or 32 apart
@@ -321,36 +383,17 @@ __device__ __forceinline__ void put_part(float* p, const float* s) {
   reinterpret_cast<float4*>(p)[1] = make_float4(s[4], s[5], s[6], s[7]);
 }
 
-// first place from which on keys are at least v
-__device__ __forceinline__ uint32_t first_at(const uint2* sorted, uint32_t n, uint32_t v) {
-  uint32_t lo = 0, hi = n;
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi) >> 1;
-    if (sorted[mid].x < v) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
-}
-
 constexpr int AHEAD = 8;  // rows whose loads are under way
 
 template <class TG, class TW, bool VEC, bool ADD>
-__global__ void __launch_bounds__(EM_THREADS) k_embed_sum(SumCall c) {
-  const uint32_t n = count_of(c.n_dev, c.n), lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(EM_THREADS) k_embed_sum(SumCall c, Empty empty, uint32_t empty_from) {
+  wait_for_previous();
+  let_next_start();
   if (blockIdx.x >= c.sum_ctas) {
-    // rows that no token names: 32 of them for each warp, found by their lanes
-    const uint32_t v0 = ((blockIdx.x - c.sum_ctas) * (EM_THREADS / 32) + warp) * 32;
-    if (v0 >= c.n_rows) return;
-    const uint32_t v = v0 + lane, at = first_at(c.sorted, n, v);
-    uint32_t empty = __ballot_sync(ALL, v < c.n_rows && (at >= n || c.sorted[at].x != v));
-    const float none[8] = {};
-    while (empty) {
-      const uint32_t k = __ffs(empty) - 1;
-      empty &= empty - 1;
-      for (uint32_t seg = 0; seg < c.segs; ++seg) write_row<TG, TW, VEC>(c, v0 + k, seg, lane, none, false);
-    }
+    write_empty(empty, empty_from + blockIdx.x - c.sum_ctas);
     return;
   }
+  const uint32_t n = count_of(c.n_dev, c.n), lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint64_t unit = (uint64_t)blockIdx.x * (EM_THREADS / 32) + warp;
   const uint32_t chunk = (uint32_t)(unit / c.segs), seg = (uint32_t)(unit % c.segs);
   const uint32_t begin = chunk * c.chunk, end = min(begin + c.chunk, n);
@@ -412,18 +455,25 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed_sum(SumCall c) {
 template <class TG, class TW, bool VEC, bool ADD>
 __global__ void __launch_bounds__(EM_THREADS) k_embed_join(SumCall c) {
   __shared__ __align__(16) float s_part[EM_THREADS / 32][COLS];
+  wait_for_previous();
   const uint32_t n = count_of(c.n_dev, c.n), lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t chunk = blockIdx.x / c.segs, seg = blockIdx.x % c.segs;
   const uint64_t last = (uint64_t)(chunk + 1) * c.chunk;
   if (last >= n) return;
-  const uint32_t key = c.sorted[last].x;
-  if (key >= c.n_rows || c.sorted[last - 1].x != key) return;
-  const uint32_t begin = chunk * c.chunk;
-  // (a run that began earlier is another CTA's: its key is that of the token before the chunk)
-  if (c.sorted[begin].x == key && begin && c.sorted[begin - 1].x == key) return;
-  const uint32_t stop = first_at(c.sorted, n, key + 1);        // the run's end
-  const uint32_t to = (stop - 1) / c.chunk;                    // its last chunk
-  const uint32_t m = to - chunk + 1, per = (m + EM_THREADS / 32 - 1) / (EM_THREADS / 32);
+  const uint32_t begin = chunk * c.chunk, key = c.sorted[last].x, end_key = c.sorted[last - 1].x, begin_key = c.sorted[begin].x;
+  const uint32_t before_key = begin ? c.sorted[begin - 1].x : ALL;
+  if (key >= c.n_rows || end_key != key) return;
+  // (a run that began earlier is another CTA's)
+  if (begin_key == key && before_key == key) return;
+  // parts of it: this chunk's, and those of the chunks after it that begin with the key
+  uint32_t m = 1;
+  for (uint64_t k0 = chunk + 1;; k0 += 32) {
+    const uint64_t at = (k0 + lane) * c.chunk;
+    const uint32_t same = __ballot_sync(ALL, at < n && c.sorted[at].x == key);
+    m += same == ALL ? 32 : __ffs(~same) - 1;
+    if (same != ALL) break;
+  }
+  const uint32_t per = (m + EM_THREADS / 32 - 1) / (EM_THREADS / 32);
   float s[8] = {};
   const uint32_t i_end = min((warp + 1) * per, m);
 #pragma unroll 4
@@ -448,7 +498,7 @@ uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
 struct Plan {
   uint32_t bits0, bits1, span, spans, chunk, chunks, segs;
-  uint64_t counts0, counts1, half, sorted, parts, bytes;  // places in d_work
+  uint64_t counts0, counts1, named, half, sorted, parts, bytes;  // places in d_work
 };
 
 Plan plan_of(uint64_t n, uint32_t n_rows, uint32_t dim) {
@@ -469,6 +519,7 @@ Plan plan_of(uint64_t n, uint32_t n_rows, uint32_t dim) {
   auto take = [&](uint64_t bytes) { const uint64_t here = at; at = up(at + bytes, 256); return here; };
   p.counts0 = take((uint64_t)p.spans * 4 << p.bits0);
   p.counts1 = take(p.bits1 ? (uint64_t)p.spans * 4 << p.bits1 : 0);
+  p.named = take((uint64_t)p.spans * ((n_rows + 31) / 32) * 4);
   p.half = take(p.bits1 ? n * 8 : 0);
   p.sorted = take(n * 8);
   p.parts = take((uint64_t)p.chunks * 2 * p.segs * COLS * 4);
@@ -560,34 +611,60 @@ int tok_embed_backward(tok_handle* h, const tok_embed_grad_args* a, void* stream
   const long long* n_dev = reinterpret_cast<const long long*>(a->d_n);
   SortCall sc{a->d_ids, n_dev, (uint32_t)a->n, a->n_rows, p.span, p.spans, p.bits0, p.bits1,
               reinterpret_cast<uint32_t*>(work + p.counts0), reinterpret_cast<uint32_t*>(work + p.counts1),
+              a->accumulate ? nullptr : reinterpret_cast<uint32_t*>(work + p.named),
               reinterpret_cast<uint2*>(work + p.half), reinterpret_cast<uint2*>(work + p.sorted)};
   SumCall c{sc.sorted, n_dev, (uint32_t)a->n, a->n_rows, a->dim, p.segs, p.chunk, p.chunks, a->scale, a->d_grad_out,
             a->grad_out_stride, a->d_grad_weight, a->grad_weight_stride, reinterpret_cast<float*>(work + p.parts), 0};
-  unsigned launches = 0;
-  if (a->n) {
-    auto room = [](uint32_t bits) { return ((size_t)4 << bits) + ((size_t)2 * (ST_WARPS + 1) << bits); };
-    cudaError_t e = allow_all<k_sort_place<0>>(h->dev);
-    if (e == cudaSuccess) e = allow_all<k_sort_place<1>>(h->dev);
-    if (e != cudaSuccess) return cuda_fail(h, e, "shared memory of a kernel");
-    k_sort_count<<<p.spans, ST_THREADS, 0, s>>>(sc);
-    k_sort_place<0><<<p.spans, ST_THREADS, room(p.bits0), s>>>(sc);
-    if (p.bits1) k_sort_place<1><<<p.spans, ST_THREADS, room(p.bits1), s>>>(sc);
-    launches += p.bits1 ? 3 : 2;
-  }
   constexpr uint64_t WARPS = EM_THREADS / 32;
+  if ((uint64_t)p.chunks * p.segs > 0x7fffffffull / 2) return fail(h, TOK_EINVAL, "embed gradient: n times dim is out of range");
   c.sum_ctas = (uint32_t)(((uint64_t)p.chunks * p.segs + WARPS - 1) / WARPS);
-  const uint32_t empty_ctas = a->accumulate ? 0 : (a->n_rows + 32 * WARPS - 1) / (32 * WARPS);
   const uint64_t join_ctas = p.chunks > 1 ? (uint64_t)(p.chunks - 1) * p.segs : 0;
-  if ((uint64_t)p.chunks * p.segs > 0x7fffffffull) return fail(h, TOK_EINVAL, "embed gradient: n times dim is out of range");
+  const size_t size = element_size(a->grad_weight_dtype);
   const bool eights = in_eights(a->d_grad_out, a->grad_out_stride, a->grad_out_dtype, a->dim) &&
                       in_eights(a->d_grad_weight, a->grad_weight_stride, a->grad_weight_dtype, a->dim);
+  const Empty em{sc.named, p.spans, a->n_rows, (a->n_rows + 31) / 32, static_cast<uint8_t*>(a->d_grad_weight),
+                 (long long)(a->grad_weight_stride * (int64_t)size), (unsigned long long)a->dim * size,
+                 in_eights(a->d_grad_weight, a->grad_weight_stride, a->grad_weight_dtype, a->dim), (uint32_t)size};
+  // blocks of rows that the sort's kernels look after: what the memory takes while they run
+  uint32_t left = a->accumulate ? 0 : em.words, from = 0;
+  const uint32_t some = (uint32_t)std::min<uint64_t>(left, SORT_BYTES / (32 * em.row) + 1);
+  auto share = [&](uint32_t most) {
+    const uint32_t m = std::min(left, most);
+    left -= m;
+    from += m;
+    return m;
+  };
+  cudaError_t e = allow_all<k_sort_count>(h->dev);
+  if (e == cudaSuccess) e = allow_all<k_sort_place<0>>(h->dev);
+  if (e == cudaSuccess) e = allow_all<k_sort_place<1>>(h->dev);
+  if (e != cudaSuccess) return cuda_fail(h, e, "shared memory of a kernel");
+  auto room = [](uint32_t bits) { return ((size_t)4 << bits) + ((size_t)2 * (ST_WARPS + 1) << bits); };
+  k_sort_count<<<p.spans, ST_THREADS, ((size_t)4 << p.bits0) + (sc.named ? (size_t)em.words * 4 : 0), s>>>(sc);
+  unsigned launches = 1;
+  uint32_t at = from, m = share(some);
+  launch_behind(k_sort_place<0>, p.spans + m, ST_THREADS, room(p.bits0), s, sc, em, at);
+  ++launches;
+  if (p.bits1) {
+    at = from;
+    m = share(some);
+    launch_behind(k_sort_place<1>, p.spans + m, ST_THREADS, room(p.bits1), s, sc, em, at);
+    ++launches;
+  }
+  at = from;
+  m = share(left);
   with_type(a->grad_out_dtype, [&](auto tg) {
     with_type(a->grad_weight_dtype, [&](auto tw) {
       using TG = decltype(tg);
       using TW = decltype(tw);
       auto both = [&](auto vec, auto add) {
-        k_embed_sum<TG, TW, vec.value, add.value><<<c.sum_ctas + empty_ctas, EM_THREADS, 0, s>>>(c);
-        if (join_ctas) k_embed_join<TG, TW, vec.value, add.value><<<(unsigned)join_ctas, EM_THREADS, 0, s>>>(c);
+        if (c.sum_ctas + m) {
+          launch_behind(k_embed_sum<TG, TW, vec.value, add.value>, c.sum_ctas + m, EM_THREADS, 0, s, c, em, at);
+          ++launches;
+        }
+        if (join_ctas) {
+          launch_behind(k_embed_join<TG, TW, vec.value, add.value>, (unsigned)join_ctas, EM_THREADS, 0, s, c);
+          ++launches;
+        }
       };
       if (eights && a->accumulate) both(std::true_type{}, std::true_type{});
       else if (eights) both(std::true_type{}, std::false_type{});
@@ -595,7 +672,7 @@ int tok_embed_backward(tok_handle* h, const tok_embed_grad_args* a, void* stream
       else both(std::false_type{}, std::false_type{});
     });
   });
-  return finish(h, launches + (join_ctas ? 2 : 1));
+  return finish(h, launches);
 } catch (...) {
   return TOK_ENOMEM;
 }

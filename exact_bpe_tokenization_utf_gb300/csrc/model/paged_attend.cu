@@ -14,6 +14,8 @@
 // the maximum, the sum and the output of its tokens, and the CTA joins its warps'
 // when the piece of a request and head ends.  What a CTA has only a part of goes to
 // d_work and a second kernel joins the parts, in order: the same bits each time.
+// A piece's start costs about as much as two of its tiles (its first tokens' places
+// and copies, the queries, the join of the warps): pieces are cut by that measure.
 //
 // The products are on mma.sync (m16n8k16): 16 tokens by 8 query heads, so that
 // groups of eight fill it; S^T = K Q^T and O^T = V^T P^T both read the cache's rows
@@ -32,6 +34,7 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int WARPS = 4, THREADS = WARPS * 32;
 constexpr int STEP = 16;                // tokens of a warp's step
 constexpr int TILE = STEP * WARPS;      // tokens of a CTA's step, the unit that pieces are cut at
+constexpr uint32_t START = 2;           // what the start of a request and head counts, in tiles
 constexpr uint32_t MOST_REQUESTS = 1u << 20, MOST_GROUP = 64;
 // A weight's exponent is relative to a reference that is replaced once a score lies
 // more than this above it (in powers of 2): weights stay below 2^8.
@@ -64,7 +67,7 @@ struct AttendCall {
   long long table_stride;
   long long most_len;               // tokens that a row of the table has room for
   const long long* seq_len;
-  unsigned long long* base;         // [n + 1]: units of the requests before each, and of all
+  uint4* splits;                    // [ctas]: what a CTA began and others end: request, key head and share, last CTA, 1
   float* sums;                      // [ctas][2][16][2]: reference and sum of a part
   float* outs;                      // [ctas][2][16][D]
   uint32_t ctas;
@@ -76,13 +79,10 @@ __device__ __forceinline__ Span span_of(const AttendCall& c, uint32_t r) {
   m = m < 0 ? 0 : m > c.most_len ? c.most_len : m;
   return Span{c.window && m > (long long)c.window ? m - (long long)c.window : 0, m};
 }
-__device__ __forceinline__ unsigned long long units_of(const AttendCall& c, uint32_t r) {
-  const Span s = span_of(c, r);
-  return (unsigned long long)((s.end - s.begin + TILE - 1) / TILE) * c.kv_heads * c.parts;
-}
-// the first unit of a CTA's piece of all units
-__device__ __forceinline__ unsigned long long piece(unsigned long long total, uint32_t cta, uint32_t ctas) {
-  return total / ctas * cta + total % ctas * cta / ctas;
+__device__ __forceinline__ uint32_t tiles_of(const Span& s) { return (uint32_t)((s.end - s.begin + TILE - 1) / TILE); }
+// of all its key heads and shares
+__device__ __forceinline__ unsigned long long cost_of(const AttendCall& c, const Span& s) {
+  return s.end > s.begin ? (unsigned long long)(tiles_of(s) + START) * (c.kv_heads * c.parts) : 0ull;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -182,10 +182,11 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
   using S = Shape<D>;
   const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, g = lane >> 2, t = lane & 3u;
 
-  // the units of all requests, and the request in which this CTA's piece begins
+  let_next_start();
+  // the cost of all requests, and the request in which this CTA's piece begins
   const uint32_t per = (c.n + THREADS - 1) / THREADS, r0 = min(tid * per, c.n), r1 = min(r0 + per, c.n);
   unsigned long long mine = 0;
-  for (uint32_t r = r0; r < r1; ++r) mine += units_of(c, r);
+  for (uint32_t r = r0; r < r1; ++r) mine += cost_of(c, span_of(c, r));
   unsigned long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
     if (lane >= (uint32_t)o) inc += x;
   }
   if (lane == 31) s_sum[warp] = inc;
+  if (tid == 0) s_req = c.n;
   __syncthreads();
   unsigned long long total = 0, at = inc - mine;
 #pragma unroll
@@ -200,17 +202,25 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
     if (w < (int)warp) at += s_sum[w];
     total += s_sum[w];
   }
-  const unsigned long long begin = piece(total, blockIdx.x, c.ctas), stop = piece(total, blockIdx.x + 1, c.ctas);
+  const unsigned long long share = (total + c.ctas - 1) / c.ctas;
+  const unsigned long long begin = min(share * blockIdx.x, total), stop = min(begin + share, total);
   for (uint32_t r = r0; r < r1; ++r) {
-    if (blockIdx.x == 0) c.base[r] = at;
-    const unsigned long long m = units_of(c, r);
+    const unsigned long long m = cost_of(c, span_of(c, r));
     if (begin >= at && begin < at + m) {
       s_req = r;
       s_base = at;
     }
     at += m;
+    if (m == 0 && r % c.ctas == blockIdx.x) {
+      // a request without tokens
+      for (uint32_t j = 0; j < c.heads; ++j) {
+        T* to = static_cast<T*>(c.out) + (long long)r * c.out_stride + (long long)j * c.out_head_stride;
+        for (uint32_t d = 0; d < c.head_dim; d += 8) *reinterpret_cast<uint4*>(to + d) = make_uint4(0, 0, 0, 0);
+        if (c.lse) c.lse[(size_t)r * c.heads + j] = -INFINITY;
+      }
+    }
   }
-  if (blockIdx.x == 0 && tid == 0) c.base[c.n] = total;
+  if (tid == 0) c.splits[blockIdx.x] = make_uint4(0, 0, 0, 0);
   if (begin >= stop) return;  // (all threads: nothing in this piece)
   __syncthreads();
   uint32_t r = s_req;
@@ -220,17 +230,26 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
   while (u < stop) {
     // the piece's part of one request, key head and share of the group
     Span sp = span_of(c, r);
-    while (sp.end == sp.begin) sp = span_of(c, ++r);   // (u < total: a request with units follows)
-    const unsigned long long tiles = (unsigned long long)(sp.end - sp.begin + TILE - 1) / TILE;
-    const unsigned long long which = (u - r_base) / tiles, tile0 = (u - r_base) % tiles;
-    const unsigned long long tile1 = tile0 + (stop - u) < tiles ? tile0 + (stop - u) : tiles;
-    const uint32_t part = (uint32_t)(which % c.parts), head = (uint32_t)(which / c.parts);
+    while (sp.end == sp.begin) sp = span_of(c, ++r);   // (u < total: a request with tokens follows)
+    const uint32_t tiles = tiles_of(sp), cost = tiles + START;
+    const uint32_t which = (uint32_t)((u - r_base) / cost), off = (uint32_t)((u - r_base) % cost);
+    const uint32_t until = (uint32_t)min((unsigned long long)cost, off + (stop - u));
+    const uint32_t tile0 = off > START ? off - START : 0u, tile1 = until > START ? until - START : 0u;
+    u += until - off;
+    const unsigned long long next_base = r_base + (unsigned long long)cost * (c.kv_heads * c.parts);
+    const uint32_t r_now = r;
+    if (u == next_base) {
+      r_base = next_base;
+      ++r;
+    }
+    if (tile0 == tile1) continue;   // (only the start's share)
+    const uint32_t part = which % c.parts, head = which / c.parts;
     const uint32_t j0 = head * c.group + part * c.gt, heads = min(c.gt, c.group - part * c.gt);  // query heads
     const long long p0 = sp.begin + (long long)tile0 * TILE, p1 = min(sp.end, sp.begin + (long long)tile1 * TILE);
-    in.row = c.table + (long long)r * c.table_stride;
+    in.row = c.table + (long long)r_now * c.table_stride;
     in.end = p1;
     in.head_off = (long long)head * c.head_stride;
-    const uint32_t tiles_here = (uint32_t)(tile1 - tile0);
+    const uint32_t tiles_here = tile1 - tile0;
 
     // the first steps' copies; the place of each step's tokens is looked up a step early
     long long p = p0 + warp * STEP + (lane & 15u);
@@ -249,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const uint32_t j = nt * 8 + g;
-      const T* from = static_cast<const T*>(c.q) + (long long)r * c.q_stride + (long long)(j0 + (j < heads ? j : 0)) * c.q_head_stride;
+      const T* from = static_cast<const T*>(c.q) + (long long)r_now * c.q_stride + (long long)(j0 + (j < heads ? j : 0)) * c.q_head_stride;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -404,75 +423,79 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
       if (whole) {
         if (d < c.head_dim) {
           const float inv = tot == 0.f ? 0.f : 1.f / tot;
-          T* to = static_cast<T*>(c.out) + (long long)r * c.out_stride + (long long)(j0 + j) * c.out_head_stride + d;
+          T* to = static_cast<T*>(c.out) + (long long)r_now * c.out_stride + (long long)(j0 + j) * c.out_head_stride + d;
           *reinterpret_cast<uint32_t*>(to) = Mma<T>::pack(x * inv, y * inv);
         }
-        if (d == 0 && c.lse) c.lse[(size_t)r * c.heads + j0 + j] = tot == 0.f ? -INFINITY : (m + log2f(tot)) * LN2;
+        if (d == 0 && c.lse) c.lse[(size_t)r_now * c.heads + j0 + j] = tot == 0.f ? -INFINITY : (m + log2f(tot)) * LN2;
       } else {
         *reinterpret_cast<float2*>(c.outs + (part_at * 16 + j) * D + d) = make_float2(x, y);
         if (d == 0) *reinterpret_cast<float2*>(c.sums + (part_at * 16 + j) * 2) = make_float2(m, tot);
       }
     }
-    __syncthreads();
-    u += tile1 - tile0;
-    if (u == r_base + tiles * c.kv_heads * c.parts) {
-      r_base = u;
-      ++r;
+    if (tid == 0 && tile0 == 0 && !whole) {
+      // who ends it: the CTA that has its last tile
+      const unsigned long long end = (u - until) + cost;
+      c.splits[blockIdx.x] = make_uint4(r_now, which, (uint32_t)((end - 1) / share), 1);
     }
+    __syncthreads();
   }
 }
 
-// A CTA for each request, key head and share of the group: what several CTAs
-// have parts of is joined, what has no tokens is set.
+// A CTA for each query head of what a CTA above began and others end: their parts
+// joined in order (every GROUPS-th one by the same threads, then these).
 template <class T, int D>
 __global__ void __launch_bounds__(THREADS) k_attend_join(AttendCall c) {
-  const uint32_t shares = c.kv_heads * c.parts, r = blockIdx.x / shares, which = blockIdx.x % shares, tid = threadIdx.x;
-  const uint32_t head = which / c.parts, part = which % c.parts;
+  constexpr int LANES = D / 2, GROUPS = THREADS / LANES, MOST = 1024;
+  __shared__ float s_f[MOST], s_x[GROUPS][D], s_m[THREADS / 32], s_t[GROUPS];
+  const uint32_t first = blockIdx.x / c.gt, j = blockIdx.x % c.gt, tid = threadIdx.x, group = tid / LANES, d = tid % LANES * 2;
+  wait_for_previous();
+  const uint4 split = c.splits[first];
+  if (!split.w) return;
+  const uint32_t r = split.x, part = split.y % c.parts, head = split.y / c.parts, n = split.z - first + 1;
   const uint32_t j0 = head * c.group + part * c.gt, heads = min(c.gt, c.group - part * c.gt);
-  const unsigned long long total = c.base[c.n], tiles = (c.base[r + 1] - c.base[r]) / shares;
-  const unsigned long long u0 = c.base[r] + tiles * which, u1 = u0 + tiles;
-  uint32_t first = 0, last = 0;
-  if (tiles) {
-    // the CTAs whose pieces hold the first and the last unit
-    auto owner = [&](unsigned long long u) {
-      uint32_t lo = 0, hi = c.ctas - 1;
-      while (lo < hi) {
-        const uint32_t mid = (lo + hi + 1) / 2;
-        if (piece(total, mid, c.ctas) <= u) lo = mid;
-        else hi = mid - 1;
-      }
-      return lo;
-    };
-    first = owner(u0);
-    last = owner(u1 - 1);
-    if (first == last) return;
-  }
-  for (uint32_t i = tid; i < heads * (D / 2); i += THREADS) {
-    const uint32_t j = i / (D / 2), d = i % (D / 2) * 2;
-    float m = -FLT_MAX, x = 0.f, y = 0.f, tot = 0.f;
-    if (tiles) {
-      for (uint32_t k = first; k <= last; ++k) {
-        const size_t at = ((size_t)k * 2 + (k == first ? 1 : 0)) * 16 + j;
-        m = fmaxf(m, c.sums[at * 2]);
-      }
-#pragma unroll 4
-      for (uint32_t k = first; k <= last; ++k) {
-        const size_t at = ((size_t)k * 2 + (k == first ? 1 : 0)) * 16 + j;
-        const float2 s = *reinterpret_cast<const float2*>(c.sums + at * 2);
-        const float2 v = *reinterpret_cast<const float2*>(c.outs + at * D + d);
-        const float f = ex2(s.x - m);
-        x = fmaf(v.x, f, x);
-        y = fmaf(v.y, f, y);
-        tot = fmaf(s.y, f, tot);
-      }
+  if (j >= heads) return;
+  // part k is the second of CTA `first`, or the first of a CTA after it
+  auto place = [&](uint32_t k) { return ((size_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * 16 + j; };
+  float m = -FLT_MAX;
+  for (uint32_t k = tid; k < n; k += THREADS) m = fmaxf(m, c.sums[place(k) * 2]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(ALL, m, o));
+  if ((tid & 31u) == 0) s_m[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) m = fmaxf(m, s_m[w]);
+  float x = 0.f, y = 0.f, tot = 0.f;
+  for (uint32_t k0 = 0; k0 < n; k0 += MOST) {   // (as many CTAs as the GPU holds at once: a few hundred)
+    const uint32_t some = min(n - k0, (uint32_t)MOST);
+    __syncthreads();
+    for (uint32_t k = tid; k < some; k += THREADS) s_f[k] = ex2(c.sums[place(k0 + k) * 2] - m);
+    __syncthreads();
+#pragma unroll 8
+    for (uint32_t k = group; k < some; k += GROUPS) {
+      const size_t at = place(k0 + k);
+      const float2 v = *reinterpret_cast<const float2*>(c.outs + at * D + d);
+      const float f = s_f[k];
+      x = fmaf(v.x, f, x);
+      y = fmaf(v.y, f, y);
+      tot = fmaf(c.sums[at * 2 + 1], f, tot);
     }
-    if (d < c.head_dim) {
-      const float inv = tot == 0.f ? 0.f : 1.f / tot;
-      T* to = static_cast<T*>(c.out) + (long long)r * c.out_stride + (long long)(j0 + j) * c.out_head_stride + d;
-      *reinterpret_cast<uint32_t*>(to) = Mma<T>::pack(x * inv, y * inv);
-    }
-    if (d == 0 && c.lse) c.lse[(size_t)r * c.heads + j0 + j] = tot == 0.f ? -INFINITY : (m + log2f(tot)) * LN2;
   }
+  s_x[group][d] = x;
+  s_x[group][d + 1] = y;
+  if (d == 0) s_t[group] = tot;
+  __syncthreads();
+  if (group) return;
+  for (int g = 1; g < GROUPS; ++g) {
+    x += s_x[g][d];
+    y += s_x[g][d + 1];
+    tot += s_t[g];
+  }
+  if (d < c.head_dim) {
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;
+    T* to = static_cast<T*>(c.out) + (long long)r * c.out_stride + (long long)(j0 + j) * c.out_head_stride + d;
+    *reinterpret_cast<uint32_t*>(to) = Mma<T>::pack(x * inv, y * inv);
+  }
+  if (d == 0 && c.lse) c.lse[(size_t)r * c.heads + j0 + j] = tot == 0.f ? -INFINITY : (m + log2f(tot)) * LN2;
 }
 
 struct StoreCall {
@@ -521,7 +544,7 @@ const char* check_cache(const tok_kv_cache* c) {
 struct Sizes {
   int d;              // width that kernels are made for
   uint32_t gt, parts, ctas;
-  uint64_t base, sums, outs, bytes;
+  uint64_t splits, sums, outs, bytes;
 };
 
 bool sizes_of(const tok_handle* h, uint32_t n, uint32_t heads, uint32_t kv_heads, uint32_t head_dim, Sizes* s) {
@@ -536,7 +559,7 @@ bool sizes_of(const tok_handle* h, uint32_t n, uint32_t heads, uint32_t kv_heads
   s->ctas = (uint32_t)h->n_sms * (s->d == 256 ? 1 : 2);
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) { const uint64_t here = at; at = (at + bytes + 255) / 256 * 256; return here; };
-  s->base = take((uint64_t)(n + 1) * 8);
+  s->splits = take((uint64_t)s->ctas * 16);
   s->sums = take((uint64_t)s->ctas * 2 * 16 * 2 * 4);
   s->outs = take((uint64_t)s->ctas * 2 * 16 * (uint64_t)s->d * 4);
   s->bytes = at;
@@ -547,7 +570,7 @@ template <class T, int D, int NT>
 cudaError_t launch_attend(int dev, const AttendCall& c, cudaStream_t s) {
   cudaError_t e = launch_clusters<k_attend<T, D, NT>>(dev, c.ctas, THREADS, 1, Shape<D>::BYTES, s, c);
   if (e != cudaSuccess) return e;
-  return launch_clusters<k_attend_join<T, D>>(dev, c.n * c.kv_heads * c.parts, THREADS, 1, 0, s, c);
+  return launch_behind(k_attend_join<T, D>, c.ctas * c.gt, THREADS, 0, s, c);
 }
 
 template <class T>
@@ -599,7 +622,7 @@ int tok_paged_attend(tok_handle* h, const tok_kv_cache* c, const tok_attend_args
   if (!a || !a->d_q || !a->d_out || !a->d_table || !a->d_seq_len) return fail(h, TOK_EINVAL, "paged attend: a buffer is NULL");
   Sizes z;
   if (!sizes_of(h, a->n, a->heads, c->kv_heads, c->head_dim, &z) || a->max_blocks > 0x7fffffffu ||
-      a->table_stride < (int64_t)a->max_blocks || (uint64_t)a->n * c->kv_heads * z.parts > 0x7fffffffull)
+      a->table_stride < (int64_t)a->max_blocks)
     return fail(h, TOK_EINVAL, "paged attend: n, heads, max_blocks or table_stride is out of range");
   if (!lies_at(a->d_q, 16) || !lies_at(a->d_out, 16) || a->q_stride % 8 || a->q_head_stride % 8 || a->out_stride % 8 ||
       a->out_head_stride % 8 || !lies_at(a->d_lse, 4) || !lies_at(a->d_table, 4) || !lies_at(a->d_seq_len, 8))
@@ -637,7 +660,7 @@ int tok_paged_attend(tok_handle* h, const tok_kv_cache* c, const tok_attend_args
   // (a token's place in its row is a 32-bit number)
   k.most_len = std::min<long long>((long long)a->max_blocks * c->block_size, 0x7fffffffll);
   k.seq_len = reinterpret_cast<const long long*>(a->d_seq_len);
-  k.base = reinterpret_cast<unsigned long long*>(work + z.base);
+  k.splits = reinterpret_cast<uint4*>(work + z.splits);
   k.sums = reinterpret_cast<float*>(work + z.sums);
   k.outs = reinterpret_cast<float*>(work + z.outs);
   k.ctas = z.ctas;

@@ -28,10 +28,9 @@ namespace cg = cooperative_groups;
 
 constexpr uint32_t ALL = 0xffffffffu;
 constexpr uint32_t MOST_LOGITS = 1u << 20;
-constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int MOST_WARPS = 16;                // of a CTA
 constexpr int BINS = 1024;                    // of 2^-4 in log2 w each, the last one for all below
 constexpr int BIN_SHIFT = 12;                 // from 2^-16 in log2 w
-constexpr int PER_BIN = BINS / THREADS;
 constexpr uint32_t LIST = 1024;               // most tokens that are sorted
 constexpr double ONE = 8796093022208.0;       // the largest weight, 2^43; 2^20 of them fit 64 bits
 constexpr int MOST_COMMANDS = 64;             // three goals of at most 8 each; a limit, so that the kernel ends
@@ -166,8 +165,8 @@ struct Shared {
     struct { unsigned long long mass[BINS]; uint32_t upto[BINS]; } sub;   // of bins of keys
     unsigned long long list[LIST];                                        // (~key, id)
   };
-  unsigned long long scan_m[WARPS];
-  uint32_t scan_c[WARPS];
+  unsigned long long scan_m[MOST_WARPS];
+  uint32_t scan_c[MOST_WARPS];
   float part_max[16];
   uint32_t part_cnt[16], part_lo[16], part_hi[16];
   Rule rule;
@@ -186,24 +185,24 @@ struct Slice {
 
 // By all threads: one(place, element) for the elements before and after the 16-byte
 // pieces that the slice has, piece(place, its elements) for these.
-template <class T, class F, class G>
+template <class T, int N, class F, class G>
 __device__ __forceinline__ void for_vectors(const Slice& s, F one, G piece) {
   const T* x = static_cast<const T*>(s.at);
   const uint32_t n = s.to - s.from;
   constexpr uint32_t VEC = 16 / sizeof(T);
   const uint32_t head = min(n, (uint32_t)((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / (uint32_t)sizeof(T));
   const uint32_t vecs = (n - head) / VEC, tail = head + vecs * VEC;
-  for (uint32_t i = threadIdx.x; i < head + (n - tail); i += THREADS) {
+  for (uint32_t i = threadIdx.x; i < head + (n - tail); i += N) {
     const uint32_t e = i < head ? i : tail + (i - head);
     one(e, x[e]);
   }
 #pragma unroll 4
-  for (uint32_t i = threadIdx.x; i < vecs; i += THREADS) piece(head + i * VEC, reinterpret_cast<const uint4*>(x + head)[i]);
+  for (uint32_t i = threadIdx.x; i < vecs; i += N) piece(head + i * VEC, reinterpret_cast<const uint4*>(x + head)[i]);
 }
 // f(score, id) for every element
-template <class T, class F>
+template <class T, int N, class F>
 __device__ __forceinline__ void for_each(const Slice& s, F f) {
-  for_vectors<T>(s, [&](uint32_t e, T x) { f(to_f32(x), s.from + e); }, [&](uint32_t e, uint4 q) {
+  for_vectors<T, N>(s, [&](uint32_t e, T x) { f(to_f32(x), s.from + e); }, [&](uint32_t e, uint4 q) {
     const T* y = reinterpret_cast<const T*>(&q);
 #pragma unroll
     for (uint32_t i = 0; i < 16 / sizeof(T); ++i) f(to_f32(y[i]), s.from + e + i);
@@ -224,6 +223,7 @@ struct SampleCall {
 };
 
 // sums over the threads before, and of all (in every thread)
+template <int WARPS>
 __device__ __forceinline__ void block_scan(Shared& sh, uint32_t& c, unsigned long long& m, uint32_t& all_c, unsigned long long& all_m) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   uint32_t ic = c;
@@ -260,8 +260,9 @@ __device__ __forceinline__ void block_scan(Shared& sh, uint32_t& c, unsigned lon
   m = bm + im - m;
 }
 
-template <class T>
+template <class T, int THREADS>
 __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
+  constexpr int WARPS = THREADS / 32, PER_BIN = BINS / THREADS, PER_LIST = LIST / THREADS;
   Shared& sh = *reinterpret_cast<Shared*>(mem);
   cg::cluster_group cluster = cg::this_cluster();
   const uint32_t rank = cluster.block_rank(), row = blockIdx.x / c.ranks, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
@@ -278,7 +279,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   s.at = src;
   if (c.resident) {
     T* keep = reinterpret_cast<T*>(mem + ((sizeof(Shared) + 15) & ~size_t(15)) + (reinterpret_cast<uintptr_t>(src) & 15u));
-    for_vectors<T>(s, [&](uint32_t e, T x) {
+    for_vectors<T, THREADS>(s, [&](uint32_t e, T x) {
       most = max_nan(most, to_f32(x));
       keep[e] = x;
     }, [&](uint32_t e, uint4 q) {
@@ -289,7 +290,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
     });
     s.at = keep;
   } else {
-    for_each<T>(s, [&](float x, uint32_t) { most = max_nan(most, x); });
+    for_each<T, THREADS>(s, [&](float x, uint32_t) { most = max_nan(most, x); });
   }
   for (uint32_t i = tid; i < 256; i += THREADS) {
     sh.pow[i] = g_powers.a[i];
@@ -341,7 +342,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
     const uint32_t carry = (uint32_t)(w >> 32) + (old + w_lo < old ? 1u : 0u);
     if (carry) atomicAdd(&sh.high[bin], carry);
   };
-  for_each<T>(s, [&](float x, uint32_t) {
+  for_each<T, THREADS>(s, [&](float x, uint32_t) {
     int k;
     float rest = 0.f;
     if (look(x, k, rest)) count_in(bin_of(k), weight(sh.pow, sh.fine, k, rest));
@@ -350,17 +351,20 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   // the row's bins: each CTA adds a share of them, for the first one
   auto add_up = [&](bool sub) {
     Shared* first = cluster.map_shared_rank(&sh, 0);
-    const uint32_t share = (BINS + c.ranks - 1) / c.ranks, b0 = min(rank * share, (uint32_t)BINS), b1 = min(b0 + share, (uint32_t)BINS);
-    for (uint32_t b = b0 + tid; b < b1; b += THREADS) {
-      uint32_t n = 0;
-      unsigned long long m = 0;
-      for (uint32_t i = 0; i < c.ranks; ++i) {
-        const Shared* o = cluster.map_shared_rank(&sh, i);
-        n += o->cnt[b];
-        m += o->low[b] + ((unsigned long long)o->high[b] << 32);
+    // (ranks lanes side by side read a bin of a CTA each)
+    const uint32_t i = tid & (c.ranks - 1), b0 = rank * (BINS / c.ranks);
+    const Shared* o = cluster.map_shared_rank(&sh, i);
+    for (uint32_t b = b0 + tid / c.ranks; b < b0 + BINS / c.ranks; b += THREADS / c.ranks) {
+      uint32_t n = o->cnt[b];
+      unsigned long long m = o->low[b] + ((unsigned long long)o->high[b] << 32);
+      for (uint32_t d = 1; d < c.ranks; d *= 2) {
+        n += __shfl_xor_sync(ALL, n, d);
+        m += __shfl_xor_sync(ALL, m, d);
       }
-      (sub ? first->sub.upto : first->upto)[b] = n;
-      (sub ? first->sub.mass : first->mass)[b] = m;
+      if (i == 0) {
+        (sub ? first->sub.upto : first->upto)[b] = n;
+        (sub ? first->sub.mass : first->mass)[b] = m;
+      }
     }
   };
   add_up(false);
@@ -379,7 +383,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
       bc += n[i];
       bm += m[i];
     }
-    block_scan(sh, bc, bm, all_c, all_m);
+    block_scan<WARPS>(sh, bc, bm, all_c, all_m);
 #pragma unroll
     for (int i = 0; i < PER_BIN; ++i) {
       bc += n[i];
@@ -501,7 +505,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
     };
     if (cmd.op == OP_GATHER) {
       Shared* first = cluster.map_shared_rank(&sh, 0);
-      for_each<T>(s, [&](float x, uint32_t id) {
+      for_each<T, THREADS>(s, [&](float x, uint32_t id) {
         int k;
         float rest;
         if (wanted(x, k, rest)) {
@@ -529,15 +533,15 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
             __syncthreads();
           }
         // sums up to each token, and the first that reaches the target
-        unsigned long long w[2], sum = 0;
+        unsigned long long w[PER_LIST], sum = 0;
         uint32_t cnt = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < PER_LIST; ++i) {
           w[i] = 0;
-          if (tid * 2 + i < n) {
+          if (tid * PER_LIST + i < n) {
             int k;
             float rest = 0.f;
-            look(of_key(~(uint32_t)(sh.list[tid * 2 + i] >> 32)), k, rest);
+            look(of_key(~(uint32_t)(sh.list[tid * PER_LIST + i] >> 32)), k, rest);
             w[i] = weight(sh.pow, sh.fine, k, rest);
             ++cnt;
           }
@@ -545,19 +549,19 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
         }
         uint32_t ac;
         unsigned long long am;
-        block_scan(sh, cnt, sum, ac, am);
+        block_scan<WARPS>(sh, cnt, sum, ac, am);
         do {
           unsigned long long m = before_m + sum;
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (tid * 2 + i < n) {
+          for (int i = 0; i < PER_LIST; ++i)
+            if (tid * PER_LIST + i < n) {
               const unsigned long long next = m + w[i];
-              const uint32_t at = before_c + tid * 2 + i + 1;
+              const uint32_t at = before_c + tid * PER_LIST + i + 1;
               if (goal == GOAL_K ? at == target : m < target && next >= target) {
                 sh.answer_cnt = at;
                 sh.answer_mass = next;
-                sh.found = (uint32_t)sh.list[tid * 2 + i];
-                sh.answer_key = ~(uint32_t)(sh.list[tid * 2 + i] >> 32);
+                sh.found = (uint32_t)sh.list[tid * PER_LIST + i];
+                sh.answer_key = ~(uint32_t)(sh.list[tid * PER_LIST + i] >> 32);
               }
               m = next;
             }
@@ -573,7 +577,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
     } else if (cmd.op == OP_BINS && cmd.by_bin >= 0) {
       // the range of the bin's keys
       uint32_t lo = ALL, hi = 0;
-      for_each<T>(s, [&](float x, uint32_t) {
+      for_each<T, THREADS>(s, [&](float x, uint32_t) {
         int k;
         float rest;
         if (wanted(x, k, rest)) {
@@ -615,7 +619,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
     } else if (cmd.op == OP_BINS) {
       for (uint32_t i = tid; i < BINS; i += THREADS) sh.cnt[i] = sh.low[i] = sh.high[i] = 0;
       __syncthreads();
-      for_each<T>(s, [&](float x, uint32_t) {
+      for_each<T, THREADS>(s, [&](float x, uint32_t) {
         int k;
         float rest = 0.f;
         if (wanted(x, k, rest)) count_in((cmd.hi - key_of(x)) >> cmd.shift, weight(sh.pow, sh.fine, k, rest));
@@ -669,7 +673,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
       for (uint32_t e = e0; e < e1; ++e) mine += key_of(to_f32(x[e])) == cmd.lo;
       uint32_t at = mine, all;
       unsigned long long zero = 0, zeros;
-      block_scan(sh, at, zero, all, zeros);
+      block_scan<WARPS>(sh, at, zero, all, zeros);
       if (tid < c.ranks) cluster.map_shared_rank(&sh, tid)->part_cnt[rank] = all;
       cluster.sync();
       for (uint32_t i = 0; i < rank; ++i) at += sh.part_cnt[i];
@@ -702,57 +706,88 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   }
 }
 
+constexpr int SAMPLE_THREADS = 512;
 template <class T>
-__global__ void __launch_bounds__(THREADS, 2) k_sample(SampleCall c) {
+__global__ void __launch_bounds__(SAMPLE_THREADS, 2) k_sample(const __grid_constant__ SampleCall c) {
   extern __shared__ __align__(16) uint8_t mem[];
-  choose<T>(c, mem);
+  choose<T, SAMPLE_THREADS>(c, mem);
 }
 
 // --- 16-bit scores -------------------------------------------------------------------
 
 // A row of 16-bit scores has few different ones: they are counted, score by score, and
-// a weight is formed once for each.  Places in the order of falling scores: positive
-// scores below 2^12, zero, negative ones above -2^12; what lies further down is only
-// counted, and must have no weight.  A row with other scores (2^12 or more, below
-// 2^-27 in bf16, NaN) takes the way above.
-template <class T> struct Places;
+// a weight is formed once for each.  What lies below -2^11 is only counted, and must have
+// no weight; a row with other scores (2^11 or more, below 2^-27 in bf16, NaN) takes the
+// way above.
+template <class T> struct Places { static constexpr uint32_t LOW = 0, HIGH = 256; using Count = uint16_t; };   // (not used)
 template <> struct Places<__nv_bfloat16> {
-  static constexpr uint32_t LOW = 100u << 7, HIGH = 139u << 7, INF = 0x7f80;   // 2^-27, 2^12
+  static constexpr uint32_t LOW = 100u << 7, HIGH = 138u << 7, INF = 0x7f80;   // the bits of 2^-27, 2^11
   using Count = uint32_t;
 };
 template <> struct Places<__half> {
-  static constexpr uint32_t LOW = 1, HIGH = 27u << 10, INF = 0x7c00;           // all, 2^12
+  static constexpr uint32_t LOW = 0, HIGH = 26u << 10, INF = 0x7c00;           // all but 0, 2^11
   using Count = uint16_t;                                                      // (as words they would not fit)
 };
-constexpr float FAR = -4096.f;
+constexpr float FAR = -2048.f;
 constexpr int GROUP = 256;                 // places of a warp's step
+constexpr int COUNT_THREADS = 256, COUNT_WARPS = COUNT_THREADS / 32;
+constexpr uint32_t ROUNDS = 8;              // most of the search for the choice, of 256 pieces a warp
 
+// Counts lie by size, positive scores first, then negative ones, then 0.  In the order
+// of falling scores (places): the positive ones backwards, a group with 0, the others.
 template <class T> struct Counts {
-  static constexpr uint32_t RANGE = Places<T>::HIGH - Places<T>::LOW;
-  static constexpr uint32_t N = 2 * RANGE + 1, GROUPS = (N + GROUP - 1) / GROUP;
+  static constexpr uint32_t RANGE = Places<T>::HIGH - Places<T>::LOW, N = 2 * RANGE + GROUP, GROUPS = N / GROUP;
+  static_assert(RANGE % GROUP == 0);
   using Count = typename Places<T>::Count;
+  static constexpr bool WORDS = sizeof(Count) == 4;
   Pow pow[256];
   Fine fine[256];
-  __align__(16) Count at[GROUPS * GROUP];
-  // the first CTA's: of each group, then up to each
-  unsigned long long mass[GROUPS];
+  __align__(16) Count at[N];
+  // the first CTA's: of eight places each (up to them in the group), and of each group, then up to each
+  unsigned long long lane_mass[GROUPS * 32], mass[GROUPS];
   uint32_t upto[GROUPS];
   uint32_t part_best[16], part_far[16], part_odd[16], part_cnt[16];
-  uint32_t best, far, odd;
-  uint32_t warp_cnt[WARPS];
+  uint32_t part_some[16][(GROUPS + 31) / 32];   // which groups have tokens in each CTA
+  uint32_t best, far, odd, some[(GROUPS + 31) / 32];
+  uint32_t cell[64];                       // of the search
   Rule rule;
   double t_ln_m;
-  uint32_t pick_bits, nth, found;          // the choice is the nth of this score (nth 0: there is none)
+  uint32_t pick_bits, nth;                 // the choice is the nth of this score (nth 0: there is none)
 
-  // the place of a score that has one
-  static __device__ __forceinline__ float score(uint32_t place) {
-    const uint32_t bits = place < RANGE ? Places<T>::HIGH - 1 - place : place == RANGE ? 0u : 0x8000u | (place - RANGE - 1 + Places<T>::LOW);
-    if (sizeof(Count) == 4) return __uint_as_float(bits << 16);
-    return __half2float(__ushort_as_half((unsigned short)bits));
+  // a place's score, and where its count lies
+  static __device__ __forceinline__ uint32_t bits(uint32_t place) {
+    return place < RANGE ? Places<T>::HIGH - 1 - place : place < RANGE + GROUP ? 0u : 0x8000u | (place - RANGE - GROUP + Places<T>::LOW);
   }
-  __device__ __forceinline__ void add(uint32_t place, uint32_t n) {
-    if (sizeof(Count) == 4) atomicAdd(reinterpret_cast<uint32_t*>(at) + place, n);
-    else atomicAdd(reinterpret_cast<uint32_t*>(at) + (place >> 1), n << (place & 1u) * 16);
+  static __device__ __forceinline__ float score(uint32_t place) {
+    if (WORDS) return __uint_as_float(bits(place) << 16);
+    return __half2float(__ushort_as_half((unsigned short)bits(place)));
+  }
+  static __device__ __forceinline__ uint32_t lies(uint32_t place) {
+    return place < RANGE ? RANGE - 1 - place : place < RANGE + GROUP ? place + RANGE : place - GROUP;
+  }
+  __device__ __forceinline__ void add(uint32_t lies, uint32_t n) {
+    if (WORDS) atomicAdd(reinterpret_cast<uint32_t*>(at) + lies, n);
+    else atomicAdd(reinterpret_cast<uint32_t*>(at) + (lies >> 1), n << (lies & 1u) * 16);
+  }
+  // one more, without a branch (from: the shared address of at)
+  static __device__ __forceinline__ void add_if(uint32_t from, uint32_t lies, bool really) {
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; @p red.shared.add.u32 [%0], %1; }" ::
+                 "r"(WORDS ? from + lies * 4 : from + (lies >> 1) * 4), "r"(WORDS ? 1u : 1u << (lies & 1u) * 16), "r"((uint32_t)really) : "memory");
+  }
+  // the counts of eight places side by side are added to n (place: a multiple of 8)
+  __device__ __forceinline__ void eight(uint32_t place, uint32_t* n) const {
+    const uint4* p = reinterpret_cast<const uint4*>(at + (place < RANGE ? RANGE - 8 - place : lies(place)));
+    const uint4 a = p[0], b = WORDS ? p[1] : a;
+    uint32_t v[8];
+    if (WORDS) {
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      v[0] = a.x & 0xffffu; v[1] = a.x >> 16; v[2] = a.y & 0xffffu; v[3] = a.y >> 16;
+      v[4] = a.z & 0xffffu; v[5] = a.z >> 16; v[6] = a.w & 0xffffu; v[7] = a.w >> 16;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n[i] += place < RANGE ? v[7 - i] : v[i];
   }
 };
 
@@ -786,8 +821,8 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
   s.at = src;
   const float temp = c.a.d_temperature ? c.a.d_temperature[row] : 1.f;
   const float min_p = c.a.d_min_p ? c.a.d_min_p[row] : 0.f;
-  for (uint32_t i = tid; i < sizeof(sh.at) / 16; i += THREADS) reinterpret_cast<uint4*>(sh.at)[i] = make_uint4(0, 0, 0, 0);
-  for (uint32_t i = tid; i < 256; i += THREADS) {
+  for (uint32_t i = tid; i < sizeof(sh.at) / 16; i += COUNT_THREADS) reinterpret_cast<uint4*>(sh.at)[i] = make_uint4(0, 0, 0, 0);
+  for (uint32_t i = tid; i < 256; i += COUNT_THREADS) {
     sh.pow[i] = g_powers.a[i];
     sh.fine[i] = g_powers.b[i];
   }
@@ -800,35 +835,95 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
   if (tid == 0) {
     sh.best = ALL;
     sh.far = sh.odd = 0;
+    for (uint32_t& x : sh.some) x = 0;
   }
+  if (tid < 64) sh.cell[tid] = 0;
   __syncthreads();
 
   // the scores are counted
-  uint32_t best = ALL, far = 0, odd = 0;
+  uint32_t best = ALL, far = 0, odd = 0, zero = 0;
   auto count = [&](uint32_t u) {
-    const uint32_t m = u & 0x7fffu, q = m - LOW;
-    if (q < RANGE) {
-      const uint32_t neg = u >> 15;
-      const uint32_t place = neg ? RANGE + 1 + q : RANGE - 1 - q;
-      best = min(best, place);
-      sh.add(place, 1);
-    } else if (m == 0) {
-      best = min(best, RANGE);
-      sh.add(RANGE, 1);
-    } else if ((u >> 15) && m > LOW && m <= Places<T>::INF) {
+    const uint32_t m = u & 0x7fffu, q = m - LOW, neg = u >> 15;
+    if (m == 0) {
+      ++zero;
+    } else if (q < RANGE) {
+      sh.add(q + neg * RANGE, 1);
+    } else if (neg && m > LOW && m <= Places<T>::INF) {
       far += m < Places<T>::INF;   // (-inf is no token)
     } else {
       odd = 1;
     }
   };
-  for_vectors<uint16_t>(s, [&](uint32_t, uint16_t x) { count(x); }, [&](uint32_t, uint4 q) {
+  const uint32_t n_mine = s.to - s.from;
+  const uint32_t head = min(n_mine, (uint32_t)((16u - (reinterpret_cast<uintptr_t>(src) & 15u)) & 15u) / 2u);
+  const uint32_t vecs = (n_mine - head) / 8, tail = head + vecs * 8;
+  const uint4* pieces = reinterpret_cast<const uint4*>(src + head);
+  if (tid < head + (n_mine - tail)) count(src[tid < head ? tid : tail + (tid - head)]);   // (14 at most)
+  const uint32_t counts = (uint32_t)__cvta_generic_to_shared(sh.at);
+  auto count_piece = [&](const uint4& q) {
+    // two scores in each operation: their sizes' range, their places, an atomic for each
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t m[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      count(w[i] & 0xffffu);
-      count(w[i] >> 16);
+    for (int i = 0; i < 4; ++i) m[i] = w[i] & 0x7fff7fffu;
+    const uint32_t hi = __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3]));
+    const uint32_t lo = __vminu2(__vminu2(m[0], m[1]), __vminu2(m[2], m[3]));
+    if (max(hi & 0xffffu, hi >> 16) < Places<T>::HIGH && min(lo & 0xffffu, lo >> 16) >= max(LOW, 1u)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t at2 = m[i] + (w[i] >> 15 & 0x00010001u) * RANGE;
+        sh.add((at2 & 0xffffu) - LOW, 1);
+        sh.add((at2 >> 16) - LOW, 1);
+      }
+    } else {
+      // (masked rows: what is -inf is passed over, what else has no place comes after)
+      uint32_t left = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu, x = u & 0x7fffu;
+        const bool in = x - LOW < RANGE && x;
+        C::add_if(counts, x - LOW + (u >> 15) * RANGE, in);
+        left |= (in || u == (0x8000u | Places<T>::INF) ? 0u : 1u) << i;
+      }
+      for (; left; left &= left - 1) {
+        const uint32_t i = __ffs(left) - 1;
+        const uint32_t x = i & 4u ? (i & 2u ? w[3] : w[2]) : (i & 2u ? w[1] : w[0]);
+        count(i & 1u ? x >> 16 : x & 0xffffu);
+      }
     }
-  });
+  };
+  constexpr int AHEAD = 3;   // pieces under way while as many are counted
+  uint4 q[AHEAD];
+  auto fetch = [&](uint32_t i) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (i + u * COUNT_THREADS < vecs) q[u] = __ldg(pieces + i + u * COUNT_THREADS);
+  };
+  fetch(tid);
+  for (uint32_t i = tid; i < vecs; i += AHEAD * COUNT_THREADS) {
+    uint4 now[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) now[u] = q[u];
+    fetch(i + AHEAD * COUNT_THREADS);
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (i + u * COUNT_THREADS < vecs) count_piece(now[u]);
+  }
+  zero = __reduce_add_sync(ALL, zero);
+  if (lane == 0 && zero) sh.add(2 * RANGE, zero);
+  __syncthreads();
+  // the groups that have tokens, and the largest score: the first place that has one
+  for (uint32_t g = warp; g < C::GROUPS; g += COUNT_WARPS) {
+    uint32_t n[8] = {};
+    sh.eight(g * GROUP + lane * 8, n);
+    uint32_t mine = ALL;
+#pragma unroll
+    for (int i = 7; i >= 0; --i)
+      if (n[i]) mine = g * GROUP + lane * 8 + i;
+    const bool any = __any_sync(ALL, mine != ALL);
+    if (any && lane == 0) atomicOr(&sh.some[g >> 5], 1u << (g & 31u));
+    best = min(best, mine);
+  }
   best = __reduce_min_sync(ALL, best);
   far = __reduce_add_sync(ALL, far);
   odd = __any_sync(ALL, odd);
@@ -843,6 +938,7 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
     o->part_best[rank] = sh.best;
     o->part_far[rank] = sh.far;
     o->part_odd[rank] = sh.odd;
+    for (uint32_t i = 0; i < (C::GROUPS + 31) / 32; ++i) o->part_some[rank][i] = sh.some[i];
   }
   cluster.sync();
   best = ALL;
@@ -880,58 +976,43 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
     }
     if (min_p > 0.f) far = 0;
   }
-  auto count_at = [&](uint32_t place) {   // in all CTAs
-    uint32_t n = 0;
-    for (uint32_t i = 0; i < c.ranks; ++i) n += cluster.map_shared_rank(&sh, i)->at[place];
-    return n;
+  auto weight_of = [&](uint32_t place, uint32_t& n) {   // (n 0: below min-p's scores)
+    const float x = C::score(place);
+    if (!(x >= least)) n = 0;
+    float hi, lo, rest = 0.f;
+    log2_weight(r, x, hi, lo);
+    const int k = fixed_log2(hi, lo, rest);
+    return weight(sh.pow, sh.fine, k, rest);
   };
-  // a lane's eight places of a group: how many tokens, and each one's weight
-  auto look = [&](uint32_t g, uint32_t* n, unsigned long long* w) {
+  C* first = cluster.map_shared_rank(&sh, 0);
+  C* second = cluster.map_shared_rank(&sh, c.ranks > 1 ? 1 : 0);
+  for (uint32_t g = warp * c.ranks + rank; g < C::GROUPS; g += COUNT_WARPS * c.ranks) {
     const uint32_t place = g * GROUP + lane * 8;
+    uint32_t n[8] = {}, all = 0;
+    unsigned long long m = 0;
+#pragma unroll 4
+    for (uint32_t k = 0; k < c.ranks; ++k)   // (reading another CTA's memory is slow: only where it has tokens)
+      if (sh.part_some[k][g >> 5] >> (g & 31u) & 1u) cluster.map_shared_rank(&sh, k)->eight(place, n);
+    if (__any_sync(ALL, n[0] | n[1] | n[2] | n[3] | n[4] | n[5] | n[6] | n[7])) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n[i] = 0;
-    for (uint32_t k = 0; k < c.ranks; ++k) {
-      const uint4* p = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&sh, k)->at + place);
-      const uint4 a = p[0];
-      if (sizeof(typename C::Count) == 4) {
-        const uint4 b = p[1];
-        n[0] += a.x; n[1] += a.y; n[2] += a.z; n[3] += a.w;
-        n[4] += b.x; n[5] += b.y; n[6] += b.z; n[7] += b.w;
-      } else {
-        n[0] += a.x & 0xffffu; n[1] += a.x >> 16; n[2] += a.y & 0xffffu; n[3] += a.y >> 16;
-        n[4] += a.z & 0xffffu; n[5] += a.z >> 16; n[6] += a.w & 0xffffu; n[7] += a.w >> 16;
+      for (int i = 0; i < 8; ++i) {
+        if (!__any_sync(ALL, n[i])) continue;
+        const unsigned long long w = weight_of(place + i, n[i]);
+        all += n[i];
+        m += n[i] * w;
       }
-    }
+      // the row's counts stay with the first CTA (or 16 bits of them, the others with the second)
+      if (c.ranks > 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] = 0;
-      if (n[i]) {
-        const float x = C::score(place + i);
-        if (x >= least) {
-          float hi, lo, rest = 0.f;
-          log2_weight(r, x, hi, lo);
-          const int k = fixed_log2(hi, lo, rest);
-          w[i] = weight(sh.pow, sh.fine, k, rest);
-        } else {
-          n[i] = 0;
+        for (int i = 0; i < 8; ++i) {
+          first->at[C::lies(place + i)] = (typename C::Count)n[i];
+          if (!C::WORDS) second->at[C::lies(place + i)] = (typename C::Count)(n[i] >> 16);
         }
       }
     }
-  };
-  C* first = cluster.map_shared_rank(&sh, 0);
-  for (uint32_t g = warp * c.ranks + rank; g < C::GROUPS; g += WARPS * c.ranks) {
-    uint32_t n[8], all = 0;
-    unsigned long long w[8], m = 0;
-    look(g, n, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      all += n[i];
-      m += n[i] * w[i];
-    }
-    all = __reduce_add_sync(ALL, all);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m += __shfl_xor_sync(ALL, m, o);
-    if (lane == 0) {
+    warp_scan(all, m);
+    first->lane_mass[g * 32 + lane] = m;
+    if (lane == 31) {
       first->upto[g] = all;
       first->mass[g] = m;
     }
@@ -939,7 +1020,7 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
   cluster.sync();
 
   // the first CTA's first warp finds the borders
-  uint32_t kept = 0;
+  uint32_t kept = 0, pick_place = 0;
   unsigned long long kept_m = 0;
   if (rank == 0 && warp == 0) {
     for (uint32_t g0 = 0; g0 < C::GROUPS; g0 += 32) {
@@ -967,39 +1048,48 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
         g += __popc(__ballot_sync(ALL, below));
       }
       g = min(g, C::GROUPS - 1);
-      uint32_t n[8], lane_n = 0;
-      unsigned long long w[8], lane_m = 0;
-      look(g, n, w);
+      uint32_t at_n = g ? sh.upto[g - 1] : 0;
+      unsigned long long at_m = g ? sh.mass[g - 1] : 0;
+      // the eight places, then the place, by a lane for each
+      uint32_t n8[8] = {}, lane_n = 0;
+      sh.eight(g * GROUP + lane * 8, n8);
+      if (!C::WORDS && c.ranks > 1) {
+        uint32_t top[8] = {};
+        second->eight(g * GROUP + lane * 8, top);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        lane_n += n[i];
-        lane_m += n[i] * w[i];
+        for (int i = 0; i < 8; ++i) n8[i] |= top[i] << 16;
       }
-      uint32_t upto_n = lane_n;
-      unsigned long long upto_m = lane_m;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (C::score(g * GROUP + lane * 8 + i) >= least) lane_n += n8[i];
+      unsigned long long no_mass = 0;
+      warp_scan(lane_n, no_mass);
+      lane_n += at_n;
+      const unsigned long long lane_m = at_m + sh.lane_mass[g * 32 + lane];
+      const uint32_t e = min((uint32_t)__popc(__ballot_sync(ALL, (by_count ? (unsigned long long)lane_n : lane_m) < target)), 31u);
+      if (e) {
+        at_n = __shfl_sync(ALL, lane_n, e - 1);
+        at_m = __shfl_sync(ALL, lane_m, e - 1);
+      }
+      const uint32_t p = g * GROUP + e * 8 + (lane & 7u);
+      uint32_t n = sh.at[C::lies(p)];
+      if (!C::WORDS && c.ranks > 1) n |= (uint32_t)second->at[C::lies(p)] << 16;
+      if (lane >= 8) n = 0;
+      const unsigned long long w = weight_of(p, n);
+      uint32_t upto_n = n;
+      unsigned long long upto_m = n * w;
       warp_scan(upto_n, upto_m);
-      uint32_t at_n = upto_n - lane_n + (g ? sh.upto[g - 1] : 0);
-      unsigned long long at_m = upto_m - lane_m + (g ? sh.mass[g - 1] : 0);
-      uint32_t hit = ALL, hit_nth = 0, hit_n = 0;
-      unsigned long long hit_m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t next_n = at_n + n[i];
-        const unsigned long long next_m = at_m + n[i] * w[i];
-        if (by_count ? at_n < target && next_n >= target : at_m < target && next_m >= target) {
-          hit = g * GROUP + lane * 8 + i;
-          hit_nth = by_count ? (uint32_t)(target - at_n) : (uint32_t)((target - at_m + w[i] - 1) / w[i]);
-          hit_n = at_n + hit_nth;
-          hit_m = at_m + hit_nth * w[i];
-        }
-        at_n = next_n;
-        at_m = next_m;
-      }
-      const uint32_t who = __ffs(__ballot_sync(ALL, hit != ALL)) - 1;
-      place = __shfl_sync(ALL, hit, who);
-      nth = __shfl_sync(ALL, hit_nth, who);
-      cnt = __shfl_sync(ALL, hit_n, who);
-      mass = __shfl_sync(ALL, hit_m, who);
+      upto_n += at_n - n;
+      upto_m += at_m - n * w;
+      // (the place's first token's sums are above upto, without it)
+      const bool in = n && (by_count ? upto_n < target && upto_n + n >= target : upto_m < target && upto_m + n * w >= target);
+      uint32_t nth_here = 0;
+      if (in) nth_here = by_count ? (uint32_t)(target - upto_n) : (uint32_t)((target - upto_m + w - 1) / w);
+      const uint32_t who = __ffs(__ballot_sync(ALL, in)) - 1;
+      place = __shfl_sync(ALL, p, who);
+      nth = __shfl_sync(ALL, nth_here, who);
+      cnt = __shfl_sync(ALL, upto_n + nth_here, who);
+      mass = __shfl_sync(ALL, upto_m + nth_here * w, who);
     };
     kept += far;
     if (top_k > 0 && (uint32_t)top_k < kept) {
@@ -1015,90 +1105,146 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
       uint32_t n;
       unsigned long long m;
       reach(false, chosen_at(c.a.d_random[row], kept_m), n, m);
-      bits = place < RANGE ? Places<T>::HIGH - 1 - place : place == RANGE ? 0u : 0x8000u | (place - RANGE - 1 + LOW);
+      bits = C::bits(place);
     }
     if (lane < c.ranks) {
       C* o = cluster.map_shared_rank(&sh, lane);
       o->pick_bits = bits;
       o->nth = kept ? nth : 0;
     }
-    if (lane == 0) {
-      if (c.a.d_kept) c.a.d_kept[row] = (int32_t)kept;
-      if (c.a.d_logprob) {
-        float hi, lo;
-        log2_weight(r, C::score(place), hi, lo);
-        c.a.d_logprob[row] = kept ? (float)(((double)hi + lo) * 0.693147180559945309417 - log((double)kept_m / ONE)) : -INFINITY;
-      }
-      if (!kept) c.a.d_pick[row] = -1;
-    }
+    pick_place = place;
   }
   cluster.sync();
   const uint32_t nth = sh.nth;
-  if (nth == 0) return true;
-  // the nth token of that score in the order of ids: a warp has a run of the slice
-  const uint32_t want = sh.pick_bits, n = s.to - s.from;
-  const uint32_t head = min(n, (uint32_t)((16u - (reinterpret_cast<uintptr_t>(src) & 15u)) & 15u) / 2u), vecs = (n - head) / 8, tail = head + vecs * 8;
-  const uint32_t run = (vecs + WARPS - 1) / WARPS, v0 = min(warp * run, vecs), v1 = min(v0 + run, vecs);
-  auto same = [&](uint32_t u) { return u == want || (want == 0 && u == 0x8000u); };
-  auto match = [&](uint32_t v) {   // of the eight scores of a piece, as bits
-    const uint4 q = reinterpret_cast<const uint4*>(src + head)[v];
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  auto finish = [&] {   // (by the first warp, which has no part in the search below)
+    if (rank || tid) return;
+    if (c.a.d_kept) c.a.d_kept[row] = (int32_t)kept;
+    if (c.a.d_logprob) {
+      float hi, lo;
+      log2_weight(r, C::score(pick_place), hi, lo);
+      c.a.d_logprob[row] = kept ? (float)(((double)hi + lo) * 0.693147180559945309417 - log((double)kept_m / ONE)) : -INFINITY;
+    }
+    if (!kept) c.a.d_pick[row] = -1;
+  };
+  if (nth == 0) {
+    finish();
+    return true;
+  }
+  // The nth token of that score in the order of ids.  The slice is searched in rounds,
+  // in each of which a warp has a run of 256 pieces; a row that one CTA has is searched
+  // no further than needed.  Cells, in order: the scores before the first piece, each
+  // round's warps, the scores after the last piece.
+  const uint32_t want = sh.pick_bits, mask = want ? 0xffffu : 0x7fffu, want2 = want | want << 16, mask2 = mask | mask << 16;
+  auto same = [&](uint32_t u) { return (u & mask) == want; };
+  auto match = [&](const uint4& q) {   // of the eight scores of a piece, as bits
+    const uint32_t x[4] = {(q.x & mask2) ^ want2, (q.y & mask2) ^ want2, (q.z & mask2) ^ want2, (q.w & mask2) ^ want2};
+    const uint32_t least = __vminu2(__vminu2(x[0], x[1]), __vminu2(x[2], x[3]));
     uint32_t m = 0;
+    if (!(least & 0xffffu) || !(least >> 16)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m |= (same(w[i] & 0xffffu) ? 1u : 0u) << (2 * i) | (same(w[i] >> 16) ? 2u : 0u) << (2 * i);
+      for (int i = 0; i < 4; ++i) m |= (x[i] & 0xffffu ? 0u : 1u) << (2 * i) | (x[i] >> 16 ? 0u : 2u) << (2 * i);
+    }
     return m;
   };
-  const bool has_head = warp == 0 && lane < head && same(src[lane]), has_tail = warp == WARPS - 1 && lane < n - tail && same(src[tail + lane]);
-  uint32_t mine = (has_head ? 1 : 0) + (has_tail ? 1 : 0);
-#pragma unroll 4
-  for (uint32_t v = v0 + lane; v < v1; v += 32) mine += __popc(match(v));
-  const uint32_t here = __reduce_add_sync(ALL, mine);
-  if (lane == 0) sh.warp_cnt[warp] = here;
-  __syncthreads();
-  uint32_t before = 0, all = 0;
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < (int)warp) before += sh.warp_cnt[w];
-    all += sh.warp_cnt[w];
-  }
-  if (tid < c.ranks) cluster.map_shared_rank(&sh, tid)->part_cnt[rank] = all;
-  cluster.sync();
-  for (uint32_t i = 0; i < rank; ++i) before += sh.part_cnt[i];
-  if (before < nth && nth <= before + here) {   // (a warp as a whole)
-    uint32_t left = nth - before;               // the left-th of the warp's
-    auto among = [&](uint32_t ballot, uint32_t base) {
-      const uint32_t k = __popc(ballot);
-      if (left && left <= k) {
-        c.a.d_pick[row] = (int32_t)(s.from + base + __fns(ballot, 0, (int)left));
-        left = 0;
-      } else if (left) {
-        left -= k;
-      }
-    };
-    if (warp == 0) among(__ballot_sync(ALL, has_head), 0);
-    for (uint32_t v = v0; v < v1 && left; v += 32) {
-      const uint32_t m = v + lane < v1 ? match(v + lane) : 0;
-      uint32_t upto = __popc(m);
-      const uint32_t cnt = upto;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t p = __shfl_up_sync(ALL, upto, o);
-        if (lane >= (uint32_t)o) upto += p;
-      }
-      const uint32_t total = __shfl_sync(ALL, upto, 31);
-      if (upto - cnt < left && left <= upto)
-        c.a.d_pick[row] = (int32_t)(s.from + head + (v + lane) * 8 + __fns(m, 0, (int)(left - (upto - cnt))));
-      left = total >= left ? 0 : left - total;
+  constexpr uint32_t SEARCH = COUNT_WARPS - 1, LAST = 1 + ROUNDS * SEARCH;
+  const bool has_head = warp == 1 && lane < head && same(src[lane]);
+  const bool has_tail = warp == 1 && lane < n_mine - tail && same(src[tail + lane]);
+  if (warp == 1) {
+    const uint32_t h = __popc(__ballot_sync(ALL, has_head)), t = __popc(__ballot_sync(ALL, has_tail));
+    if (lane == 0) {
+      sh.cell[0] = h;
+      sh.cell[LAST] = t;
     }
-    if (warp == WARPS - 1) among(__ballot_sync(ALL, has_tail), tail);
+  }
+  unsigned long long steps = 0;   // in which the lane found some
+  uint4 p[8];                     // the pieces of the next round
+  auto get = [&](uint32_t k) {
+    const uint32_t v0 = (k * SEARCH + warp - 1) * 256 + lane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (warp && v0 + i * 32 < vecs) p[i] = __ldg(pieces + v0 + i * 32);
+  };
+  get(0);
+  for (uint32_t k = 0; k * SEARCH * 256 < vecs; ++k) {
+    uint32_t mine = 0;
+    if (warp) {
+      const uint32_t v0 = (k * SEARCH + warp - 1) * 256 + lane;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t m = v0 + i * 32 < vecs ? match(p[i]) : 0u;
+        mine += __popc(m);
+        if (m) steps |= 1ull << (k * 8 + i);
+      }
+      get(k + 1);
+      mine = __reduce_add_sync(ALL, mine);
+      if (lane == 0) sh.cell[1 + k * SEARCH + warp - 1] = mine;
+    }
+    if (c.ranks == 1) {
+      __syncthreads();
+      uint32_t found = lane <= (k + 1) * SEARCH ? sh.cell[lane] : 0;
+      if (lane + 32 <= (k + 1) * SEARCH) found += sh.cell[lane + 32];
+      if (__reduce_add_sync(ALL, found) >= nth) break;   // (all warps alike)
+    }
+  }
+  __syncthreads();
+  const uint32_t c0 = sh.cell[lane], c1 = sh.cell[lane + 32];
+  uint32_t before = 0;
+  if (c.ranks > 1) {
+    const uint32_t all = __reduce_add_sync(ALL, c0 + c1);
+    if (tid < c.ranks) cluster.map_shared_rank(&sh, tid)->part_cnt[rank] = all;
+    cluster.sync();
+    for (uint32_t i = 0; i < rank; ++i) before += sh.part_cnt[i];
+  }
+  // sums up to each cell: in which one it is, and as which of its tokens
+  uint32_t s0 = c0, s1 = c1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t p0 = __shfl_up_sync(ALL, s0, o), p1 = __shfl_up_sync(ALL, s1, o);
+    if (lane >= (uint32_t)o) {
+      s0 += p0;
+      s1 += p1;
+    }
+  }
+  s0 += before;
+  s1 += __shfl_sync(ALL, s0, 31);
+  const uint32_t in0 = __ballot_sync(ALL, s0 - c0 < nth && nth <= s0), in1 = __ballot_sync(ALL, s1 - c1 < nth && nth <= s1);
+  finish();
+  if (!(in0 | in1)) return true;   // (another CTA's)
+  const uint32_t cell = in0 ? __ffs(in0) - 1 : 31 + __ffs(in1);
+  uint32_t left = nth - (in0 ? __shfl_sync(ALL, s0 - c0, cell) : __shfl_sync(ALL, s1 - c1, cell - 32));
+  if (cell == 0 || cell == LAST) {
+    if (warp == 1) {
+      const uint32_t m = __ballot_sync(ALL, cell ? has_tail : has_head);
+      if (lane == 0) c.a.d_pick[row] = (int32_t)(s.from + (cell ? tail : 0u) + __fns(m, 0, (int)left));
+    }
+    return true;
+  }
+  const uint32_t k = (cell - 1) / SEARCH;
+  if (warp != 1 + (cell - 1) % SEARCH) return true;
+  for (uint32_t i = 0; i < 8; ++i) {
+    const bool some = steps >> (k * 8 + i) & 1;
+    if (!__any_sync(ALL, some)) continue;
+    const uint32_t v = (cell - 1) * 256 + i * 32 + lane, m = some ? match(__ldg(pieces + v)) : 0u, mine = __popc(m);
+    uint32_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t p = __shfl_up_sync(ALL, upto, o);
+      if (lane >= (uint32_t)o) upto += p;
+    }
+    if (upto - mine < left && left <= upto)
+      c.a.d_pick[row] = (int32_t)(s.from + head + v * 8 + __fns(m, 0, (int)(left - (upto - mine))));
+    const uint32_t total = __shfl_sync(ALL, upto, 31);
+    if (total >= left) break;
+    left -= total;
   }
   return true;
 }
 
 template <class T>
-__device__ __noinline__ void choose_any(const SampleCall& c, uint8_t* mem) { choose<T>(c, mem); }
+__device__ __noinline__ void choose_any(const SampleCall& c, uint8_t* mem) { choose<T, COUNT_THREADS>(c, mem); }
 
 template <class T>
-__global__ void __launch_bounds__(THREADS, 2) k_sample_counted(const __grid_constant__ SampleCall c) {
+__global__ void __launch_bounds__(COUNT_THREADS, 4) k_sample_counted(const __grid_constant__ SampleCall c) {
   extern __shared__ __align__(16) uint8_t mem[];
   if (!choose_counted<T>(c, mem)) choose_any<T>(c, mem);
 }
@@ -1108,21 +1254,26 @@ cudaError_t launch(tok_handle* h, const tok_sample_args* a, cudaStream_t s) {
   SampleCall c{};
   c.a = *a;
   const size_t base = (sizeof(Shared) + 15) & ~size_t(15);
+  // CTAs at once: as many as an SM's threads' registers (64 each) and shared memory have room for
+  const uint32_t fit = sizeof(T) == 2 ? (uint32_t)std::min<size_t>(4, 228 * 1024 / (std::max(base, sizeof(Counts<T>)) + 1024)) : 2u;
+  const uint32_t room = fit * (uint32_t)h->n_sms;
+  // counts of 16 bits have to hold a CTA's, and the search its slice
+  const uint32_t most = sizeof(T) == 2 && sizeof(typename Places<T>::Count) == 4 ? (COUNT_WARPS - 1) * ROUNDS * 2048 - 8 : 65000u;
   uint32_t n = 1;
-  while (n < 16 && (a->n_logits / n > 65000 || (a->n_logits / n > 4096 && (uint64_t)a->rows * n * 2 <= 2ull * (uint32_t)h->n_sms))) n *= 2;
+  while (n < 16 && (a->n_logits / n > most || (a->n_logits / n > (sizeof(T) == 2 ? 16384u : 4096u) && (uint64_t)a->rows * n * 2 <= room))) n *= 2;
   c.ranks = n;
-  c.per = (a->n_logits + n - 1) / n;
-  c.per = (c.per + 7) / 8 * 8;
+  c.per = ((a->n_logits + n - 1) / n + 7) / 8 * 8;
   if constexpr (sizeof(T) == 2) {
     // (a CTA's count of a score has to fit; 2^20 scores are too many for 16 CTAs)
     if (sizeof(typename Places<T>::Count) == 4 || c.per < 65536)
-      return launch_clusters<k_sample_counted<T>>(h->dev, a->rows * n, THREADS, n, std::max(base, sizeof(Counts<T>)), s, c);
+      return launch_clusters<k_sample_counted<T>>(h->dev, a->rows * n, COUNT_THREADS, n, std::max(base, sizeof(Counts<T>)), s, c);
   }
-  {
+  if constexpr (sizeof(typename Places<T>::Count) != 4) {
     const size_t slice = (size_t)c.per * sizeof(T) + 16;
     c.resident = base + slice <= MOST_SHARED;
-    return launch_clusters<k_sample<T>>(h->dev, a->rows * n, THREADS, n, base + (c.resident ? slice : 0), s, c);
+    return launch_clusters<k_sample<T>>(h->dev, a->rows * n, SAMPLE_THREADS, n, base + (c.resident ? slice : 0), s, c);
   }
+  return cudaErrorInvalidValue;   // (not reached)
 }
 
 }  // namespace

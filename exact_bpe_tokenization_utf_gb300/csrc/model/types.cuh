@@ -78,6 +78,25 @@ template <> __device__ __forceinline__ void Eight<__nv_bfloat16>::put_pair(int i
   w[i] = *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A kernel that launch_behind launched starts while the one before it in the stream
+// ends, if that one lets it, and waits here until its results are there.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <class... Args>
+cudaError_t launch_behind(void (*kernel)(Args...), unsigned ctas, unsigned threads, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // count of a batch of at most n whose number the device knows (p may be nullptr)
 __device__ __forceinline__ uint32_t count_of(const long long* p, uint32_t n) {
   if (!p) return n;
