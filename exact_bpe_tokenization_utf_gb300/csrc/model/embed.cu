@@ -14,9 +14,10 @@
 // a chunk is a finished row of dW; what a chunk's first and last run share with
 // the neighbours goes to d_work, and a second kernel adds those parts in order.
 //
-// The rows that no token names are written as zeros: most of a small batch's bytes.
-// Which these are is known from the first kernel on (a bit for each row), so that the
-// sort's kernels, a few CTAs that wait for chains of latencies, write a part of them.
+// The rows that no token names are written as zeros by CTAs of their own (which rows
+// these are, the first kernel of the sort says with a bit for each).  Zeros written
+// beside the sort's kernels, whose few CTAs wait for chains of latencies, gained
+// nothing: 131,057 tokens by 2,048 columns 211 us with 48 to 128 MB there, 209 without.
 #include "types.cuh"
 
 namespace tokgb {
@@ -100,11 +101,10 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed_any(EmbedCall c) {
 // warps take 256 tokens each, 32 at a time, so that a token's place among those
 // of its digit is their order; counts of the digits by CTA (the table `counts`,
 // a row of n_digits for each CTA) give the places of the spans.
-constexpr int ST_THREADS = 512, ST_WARPS = ST_THREADS / 32, ST_PER = 8;
+constexpr int ST_THREADS = 512, ST_WARPS = ST_THREADS / 32, ST_PER = 4;
 constexpr int ST_TILE = ST_THREADS * ST_PER;
 constexpr int MOST_BITS = 11, MOST_DIGITS = 1 << MOST_BITS;
 constexpr uint32_t MOST_SPANS = 152;
-constexpr uint64_t SORT_BYTES = 48u << 20;   // zeros that are written beside a pass of the sort (about 8 us)
 
 struct SortCall {
   const int32_t* ids;
@@ -118,6 +118,7 @@ struct SortCall {
   uint32_t* named;     // spans rows of a bit for each row of the weights: whether the span's ids name it; or nullptr
   uint2* half;         // (key, token) after the first pass of two
   uint2* sorted;       // and at the end
+  uint32_t* n_runs;    // set to 0 for the sums
 };
 
 // an id's key: ids without a row come last
@@ -166,11 +167,14 @@ __device__ __forceinline__ void write_empty(const Empty& e, uint32_t b) {
     uint8_t* to = e.rows + (long long)(b * 32 + __ffs(left) - 1) * e.stride;
     const uint32_t lane = threadIdx.x & 31u;
     if (e.eights) {
-      for (unsigned long long i = lane * 16; i < e.row; i += 512) *reinterpret_cast<uint4*>(to + i) = make_uint4(0, 0, 0, 0);
+      uint4* q = reinterpret_cast<uint4*>(to);
+      const uint32_t n = (uint32_t)(e.row / 16);
+#pragma unroll 8
+      for (uint32_t i = lane; i < n; i += 32) q[i] = make_uint4(0, 0, 0, 0);
     } else if (e.element == 4) {
-      for (unsigned long long i = lane * 4; i < e.row; i += 128) *reinterpret_cast<uint32_t*>(to + i) = 0;
+      for (uint32_t i = lane; i < (uint32_t)(e.row / 4); i += 32) reinterpret_cast<uint32_t*>(to)[i] = 0;
     } else {
-      for (unsigned long long i = lane * 2; i < e.row; i += 64) *reinterpret_cast<uint16_t*>(to + i) = 0;
+      for (uint32_t i = lane; i < (uint32_t)(e.row / 2); i += 32) reinterpret_cast<uint16_t*>(to)[i] = 0;
     }
   }
 }
@@ -182,6 +186,7 @@ __global__ void __launch_bounds__(ST_THREADS) k_sort_count(SortCall c) {
   uint32_t* s_count = reinterpret_cast<uint32_t*>(mem);
   uint32_t* s_named = s_count + (1u << c.bits0);
   let_next_start();
+  if (blockIdx.x == 0 && threadIdx.x < 2) c.n_runs[threadIdx.x] = 0;
   const uint32_t n = count_of(c.n_dev, c.n), digits = 1u << c.bits0, words = (c.n_rows + 31) / 32, tid = threadIdx.x;
   for (uint32_t d = tid; d < digits + (c.named ? words : 0u); d += ST_THREADS) s_count[d] = 0;
   __syncthreads();
@@ -201,14 +206,10 @@ __global__ void __launch_bounds__(ST_THREADS) k_sort_count(SortCall c) {
 }
 
 template <int PASS>
-__global__ void __launch_bounds__(ST_THREADS) k_sort_place(SortCall c, Empty empty, uint32_t empty_from) {
+__global__ void __launch_bounds__(ST_THREADS) k_sort_place(SortCall c) {
   extern __shared__ __align__(16) uint8_t mem[];
   wait_for_previous();
   let_next_start();
-  if (blockIdx.x >= c.spans) {
-    write_empty(empty, empty_from + blockIdx.x - c.spans);
-    return;
-  }
   const uint32_t bits = PASS == 0 ? c.bits0 : c.bits1, digits = 1u << bits, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
   uint32_t* base = reinterpret_cast<uint32_t*>(mem);                    // [digits] where a digit's next token goes
   uint16_t* count = reinterpret_cast<uint16_t*>(base + digits);         // [ST_WARPS][digits]
@@ -216,24 +217,26 @@ __global__ void __launch_bounds__(ST_THREADS) k_sort_place(SortCall c, Empty emp
   const uint32_t n = count_of(c.n_dev, c.n);
   const uint32_t* counts = PASS == 0 ? c.counts0 : c.counts1;
   const uint32_t begin = min(blockIdx.x * c.span, n), end = min(begin + c.span, n);
-  // places: all tokens of lower digits, then those of the digit in earlier spans.  A
-  // thread has up to four digits side by side.
-  constexpr int PER = MOST_DIGITS / ST_THREADS;
-  uint32_t before[PER], all = 0, mine[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    before[i] = mine[i] = 0;
-    const uint32_t d = tid * PER + i;
-    if (d < digits) {
-#pragma unroll 8
-      for (uint32_t s = 0; s < c.spans; ++s) {
-        const uint32_t m = counts[(size_t)s * digits + d];
-        mine[i] += m;
-        if (s < blockIdx.x) before[i] += m;
-      }
+  // places: all tokens of lower digits, then those of the digit in earlier spans
+  uint32_t* total = reinterpret_cast<uint32_t*>(count);                 // [digits][2], before the counts of tiles
+  for (uint32_t d = tid; d < digits; d += ST_THREADS) {
+    uint32_t mine = 0, before = 0;
+#pragma unroll 16
+    for (uint32_t s = 0; s < c.spans; ++s) {
+      const uint32_t m = counts[(size_t)s * digits + d];
+      mine += m;
+      before += s < blockIdx.x ? m : 0u;
     }
-    all += mine[i];
+    total[2 * d] = mine;
+    total[2 * d + 1] = before;
   }
+  __syncthreads();
+  // (up to four digits of a thread side by side)
+  constexpr int PER = MOST_DIGITS / ST_THREADS;
+  uint32_t all = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (tid * PER + i < digits) all += total[2 * (tid * PER + i)];
   uint32_t inc = all;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -247,8 +250,10 @@ __global__ void __launch_bounds__(ST_THREADS) k_sort_place(SortCall c, Empty emp
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const uint32_t d = tid * PER + i;
-    if (d < digits) base[d] = lower + before[i];
-    lower += mine[i];
+    if (d < digits) {
+      base[d] = lower + total[2 * d + 1];
+      lower += total[2 * d];
+    }
   }
   for (uint32_t t0 = begin; t0 < end; t0 += ST_TILE) {
     __syncthreads();
@@ -333,6 +338,8 @@ struct SumCall {
   void* grad_weight;
   long long grad_weight_stride;
   float* parts;                   // [chunks][2][dim rounded up to COLS]: first and last run of a chunk
+  uint32_t* runs;                 // [chunks]: chunks in which a run begins that others end; from the end, long ones
+  uint32_t* n_runs;               // how many of both
   uint32_t sum_ctas;              // CTAs that add; the others write rows without tokens
 };
 
@@ -384,13 +391,14 @@ __device__ __forceinline__ void put_part(float* p, const float* s) {
 }
 
 constexpr int AHEAD = 8;  // rows whose loads are under way
+constexpr uint32_t LONG_RUN = 8;  // chunks of a run that a whole CTA adds
 
 template <class TG, class TW, bool VEC, bool ADD>
-__global__ void __launch_bounds__(EM_THREADS) k_embed_sum(SumCall c, Empty empty, uint32_t empty_from) {
+__global__ void __launch_bounds__(EM_THREADS) k_embed_sum(SumCall c, Empty empty) {
   wait_for_previous();
   let_next_start();
   if (blockIdx.x >= c.sum_ctas) {
-    write_empty(empty, empty_from + blockIdx.x - c.sum_ctas);
+    write_empty(empty, blockIdx.x - c.sum_ctas);
     return;
   }
   const uint32_t n = count_of(c.n_dev, c.n), lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
@@ -445,51 +453,73 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed_sum(SumCall c, Empty empty
     }
   }
   if (run_key >= c.n_rows) return;
-  if (first) put_part(part_of(c, chunk, 0, seg, lane), s);
-  else if (next_key == run_key) put_part(part_of(c, chunk, 1, seg, lane), s);
-  else write_row<TG, TW, VEC>(c, run_key, seg, lane, s, ADD);
+  if (first) {
+    put_part(part_of(c, chunk, 0, seg, lane), s);
+  } else if (next_key == run_key) {
+    put_part(part_of(c, chunk, 1, seg, lane), s);
+    if (seg == 0 && lane == 0) {
+      const uint64_t far = (uint64_t)begin + (uint64_t)c.chunk * LONG_RUN;
+      if (far < n && c.sorted[far].x == run_key) c.runs[c.chunks - 1 - atomicAdd(c.n_runs + 1, 1u)] = chunk;
+      else c.runs[atomicAdd(c.n_runs, 1u)] = chunk;
+    }
+  } else {
+    write_row<TG, TW, VEC>(c, run_key, seg, lane, s, ADD);
+  }
 }
 
-// Runs that reach over chunks: the CTA of the chunk in which one begins adds its
-// parts, each warp a share of them in order, then the shares in order.
+// Runs that reach over chunks, as the chunks in which they begin (in any order: each
+// is a row of its own).  A warp adds a run's parts over 256 columns in order; of a
+// long run each warp of a CTA takes a share, and the shares are added in order.
 template <class TG, class TW, bool VEC, bool ADD>
 __global__ void __launch_bounds__(EM_THREADS) k_embed_join(SumCall c) {
   __shared__ __align__(16) float s_part[EM_THREADS / 32][COLS];
   wait_for_previous();
+  constexpr uint32_t WARPS = EM_THREADS / 32;
   const uint32_t n = count_of(c.n_dev, c.n), lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-  const uint32_t chunk = blockIdx.x / c.segs, seg = blockIdx.x % c.segs;
-  const uint64_t last = (uint64_t)(chunk + 1) * c.chunk;
-  if (last >= n) return;
-  const uint32_t begin = chunk * c.chunk, key = c.sorted[last].x, end_key = c.sorted[last - 1].x, begin_key = c.sorted[begin].x;
-  const uint32_t before_key = begin ? c.sorted[begin - 1].x : ALL;
-  if (key >= c.n_rows || end_key != key) return;
-  // (a run that began earlier is another CTA's)
-  if (begin_key == key && before_key == key) return;
-  // parts of it: this chunk's, and those of the chunks after it that begin with the key
-  uint32_t m = 1;
-  for (uint64_t k0 = chunk + 1;; k0 += 32) {
-    const uint64_t at = (k0 + lane) * c.chunk;
-    const uint32_t same = __ballot_sync(ALL, at < n && c.sorted[at].x == key);
-    m += same == ALL ? 32 : __ffs(~same) - 1;
-    if (same != ALL) break;
-  }
-  const uint32_t per = (m + EM_THREADS / 32 - 1) / (EM_THREADS / 32);
-  float s[8] = {};
-  const uint32_t i_end = min((warp + 1) * per, m);
-#pragma unroll 4
-  for (uint32_t i = warp * per; i < i_end; ++i) {
-    const float4* p = reinterpret_cast<const float4*>(part_of(c, chunk + i, i == 0, seg, lane));
-    const float4 a = p[0], b = p[1];
-    s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
-    s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
-  }
-  put_part(&s_part[warp][lane * 8], s);
-  __syncthreads();
-  if (warp) return;
-  for (int w = 1; w < EM_THREADS / 32; ++w)
+  // parts of the run that begins in a chunk: its own, and those of the chunks after it that begin with the key
+  auto parts_of = [&](uint32_t chunk, uint32_t key) {
+    uint32_t m = 1;
+    for (uint64_t k0 = chunk + 1;; k0 += 32) {
+      const uint64_t at = (k0 + lane) * c.chunk;
+      const uint32_t same = __ballot_sync(ALL, at < n && c.sorted[at].x == key);
+      m += same == ALL ? 32 : __ffs(~same) - 1;
+      if (same != ALL) return m;
+    }
+  };
+  auto sum = [&](uint32_t chunk, uint32_t seg, uint32_t from, uint32_t to, float* s) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] += s_part[w][lane * 8 + i];
-  write_row<TG, TW, VEC>(c, key, seg, lane, s, ADD);
+    for (int i = 0; i < 8; ++i) s[i] = 0.f;
+#pragma unroll 4
+    for (uint32_t i = from; i < to; ++i) {
+      const float4* p = reinterpret_cast<const float4*>(part_of(c, chunk + i, i == 0, seg, lane));
+      const float4 a = p[0], b = p[1];
+      s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+      s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+    }
+  };
+  float s[8];
+  const uint64_t short_items = (uint64_t)c.n_runs[0] * c.segs, long_items = (uint64_t)c.n_runs[1] * c.segs;
+  for (uint64_t item = (uint64_t)blockIdx.x * WARPS + warp; item < short_items; item += (uint64_t)gridDim.x * WARPS) {
+    const uint32_t chunk = c.runs[item / c.segs], seg = (uint32_t)(item % c.segs);
+    const uint32_t key = c.sorted[(uint64_t)(chunk + 1) * c.chunk].x;
+    sum(chunk, seg, 0, parts_of(chunk, key), s);
+    write_row<TG, TW, VEC>(c, key, seg, lane, s, ADD);
+  }
+  for (uint64_t item = blockIdx.x; item < long_items; item += gridDim.x) {
+    const uint32_t chunk = c.runs[c.chunks - 1 - item / c.segs], seg = (uint32_t)(item % c.segs);
+    const uint32_t key = c.sorted[(uint64_t)(chunk + 1) * c.chunk].x;
+    const uint32_t m = parts_of(chunk, key), per = (m + WARPS - 1) / WARPS;
+    sum(chunk, seg, min(warp * per, m), min((warp + 1) * per, m), s);
+    put_part(&s_part[warp][lane * 8], s);
+    __syncthreads();
+    if (warp == 0) {
+      for (uint32_t w = 1; w < WARPS; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += s_part[w][lane * 8 + i];
+      write_row<TG, TW, VEC>(c, key, seg, lane, s, ADD);
+    }
+    __syncthreads();
+  }
 }
 
 // --- the host's side -----------------------------------------------------------------
@@ -498,7 +528,7 @@ uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
 struct Plan {
   uint32_t bits0, bits1, span, spans, chunk, chunks, segs;
-  uint64_t counts0, counts1, named, half, sorted, parts, bytes;  // places in d_work
+  uint64_t counts0, counts1, named, half, sorted, parts, runs, bytes;  // places in d_work
 };
 
 Plan plan_of(uint64_t n, uint32_t n_rows, uint32_t dim) {
@@ -523,7 +553,8 @@ Plan plan_of(uint64_t n, uint32_t n_rows, uint32_t dim) {
   p.half = take(p.bits1 ? n * 8 : 0);
   p.sorted = take(n * 8);
   p.parts = take((uint64_t)p.chunks * 2 * p.segs * COLS * 4);
-  p.bytes = std::max<uint64_t>(at, 256);
+  p.runs = take((uint64_t)p.chunks * 4 + 8);
+  p.bytes = at;
   return p;
 }
 
@@ -612,28 +643,21 @@ int tok_embed_backward(tok_handle* h, const tok_embed_grad_args* a, void* stream
   SortCall sc{a->d_ids, n_dev, (uint32_t)a->n, a->n_rows, p.span, p.spans, p.bits0, p.bits1,
               reinterpret_cast<uint32_t*>(work + p.counts0), reinterpret_cast<uint32_t*>(work + p.counts1),
               a->accumulate ? nullptr : reinterpret_cast<uint32_t*>(work + p.named),
-              reinterpret_cast<uint2*>(work + p.half), reinterpret_cast<uint2*>(work + p.sorted)};
+              reinterpret_cast<uint2*>(work + p.half), reinterpret_cast<uint2*>(work + p.sorted),
+              reinterpret_cast<uint32_t*>(work + p.runs)};
   SumCall c{sc.sorted, n_dev, (uint32_t)a->n, a->n_rows, a->dim, p.segs, p.chunk, p.chunks, a->scale, a->d_grad_out,
-            a->grad_out_stride, a->d_grad_weight, a->grad_weight_stride, reinterpret_cast<float*>(work + p.parts), 0};
+            a->grad_out_stride, a->d_grad_weight, a->grad_weight_stride, reinterpret_cast<float*>(work + p.parts), sc.n_runs + 2, sc.n_runs, 0};
   constexpr uint64_t WARPS = EM_THREADS / 32;
   if ((uint64_t)p.chunks * p.segs > 0x7fffffffull / 2) return fail(h, TOK_EINVAL, "embed gradient: n times dim is out of range");
   c.sum_ctas = (uint32_t)(((uint64_t)p.chunks * p.segs + WARPS - 1) / WARPS);
-  const uint64_t join_ctas = p.chunks > 1 ? (uint64_t)(p.chunks - 1) * p.segs : 0;
+  const uint64_t join_ctas = p.chunks > 1 ? std::min<uint64_t>((uint64_t)(p.chunks - 1) * p.segs, 6ull * (uint32_t)h->n_sms) : 0;
   const size_t size = element_size(a->grad_weight_dtype);
   const bool eights = in_eights(a->d_grad_out, a->grad_out_stride, a->grad_out_dtype, a->dim) &&
                       in_eights(a->d_grad_weight, a->grad_weight_stride, a->grad_weight_dtype, a->dim);
   const Empty em{sc.named, p.spans, a->n_rows, (a->n_rows + 31) / 32, static_cast<uint8_t*>(a->d_grad_weight),
                  (long long)(a->grad_weight_stride * (int64_t)size), (unsigned long long)a->dim * size,
                  in_eights(a->d_grad_weight, a->grad_weight_stride, a->grad_weight_dtype, a->dim), (uint32_t)size};
-  // blocks of rows that the sort's kernels look after: what the memory takes while they run
-  uint32_t left = a->accumulate ? 0 : em.words, from = 0;
-  const uint32_t some = (uint32_t)std::min<uint64_t>(left, SORT_BYTES / (32 * em.row) + 1);
-  auto share = [&](uint32_t most) {
-    const uint32_t m = std::min(left, most);
-    left -= m;
-    from += m;
-    return m;
-  };
+  const uint32_t m = a->accumulate ? 0 : em.words;   // blocks of rows
   cudaError_t e = allow_all<k_sort_count>(h->dev);
   if (e == cudaSuccess) e = allow_all<k_sort_place<0>>(h->dev);
   if (e == cudaSuccess) e = allow_all<k_sort_place<1>>(h->dev);
@@ -641,24 +665,19 @@ int tok_embed_backward(tok_handle* h, const tok_embed_grad_args* a, void* stream
   auto room = [](uint32_t bits) { return ((size_t)4 << bits) + ((size_t)2 * (ST_WARPS + 1) << bits); };
   k_sort_count<<<p.spans, ST_THREADS, ((size_t)4 << p.bits0) + (sc.named ? (size_t)em.words * 4 : 0), s>>>(sc);
   unsigned launches = 1;
-  uint32_t at = from, m = share(some);
-  launch_behind(k_sort_place<0>, p.spans + m, ST_THREADS, room(p.bits0), s, sc, em, at);
+  launch_behind(k_sort_place<0>, p.spans, ST_THREADS, room(p.bits0), s, sc);
   ++launches;
   if (p.bits1) {
-    at = from;
-    m = share(some);
-    launch_behind(k_sort_place<1>, p.spans + m, ST_THREADS, room(p.bits1), s, sc, em, at);
+    launch_behind(k_sort_place<1>, p.spans, ST_THREADS, room(p.bits1), s, sc);
     ++launches;
   }
-  at = from;
-  m = share(left);
   with_type(a->grad_out_dtype, [&](auto tg) {
     with_type(a->grad_weight_dtype, [&](auto tw) {
       using TG = decltype(tg);
       using TW = decltype(tw);
       auto both = [&](auto vec, auto add) {
         if (c.sum_ctas + m) {
-          launch_behind(k_embed_sum<TG, TW, vec.value, add.value>, c.sum_ctas + m, EM_THREADS, 0, s, c, em, at);
+          launch_behind(k_embed_sum<TG, TW, vec.value, add.value>, c.sum_ctas + m, EM_THREADS, 0, s, c, em);
           ++launches;
         }
         if (join_ctas) {

@@ -342,12 +342,13 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
     const uint32_t carry = (uint32_t)(w >> 32) + (old + w_lo < old ? 1u : 0u);
     if (carry) atomicAdd(&sh.high[bin], carry);
   };
-  for_each<T, THREADS>(s, [&](float x, uint32_t) {
-    int k;
-    float rest = 0.f;
-    if (look(x, k, rest)) count_in(bin_of(k), weight(sh.pow, sh.fine, k, rest));
-  });
-  cluster.sync();
+  // a bin of the same width without the care that weights take: off by one at most (but
+  // for the last ones), and it never falls where x falls either
+  const float bin_scale = 16.f * r.c_hi;
+  auto rough_bin = [&](float x) {
+    if (r.only_max) return x == r.x_max ? 0u : (uint32_t)BINS - 1u;
+    return (uint32_t)min((int)((r.x_max - x) * bin_scale), BINS - 1);
+  };
   // the row's bins: each CTA adds a share of them, for the first one
   auto add_up = [&](bool sub) {
     Shared* first = cluster.map_shared_rank(&sh, 0);
@@ -367,9 +368,6 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
       }
     }
   };
-  add_up(false);
-  cluster.sync();
-
   // sums of the bins up to each (in the first CTA)
   uint32_t all_c = 0;
   unsigned long long all_m = 0;
@@ -419,12 +417,50 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   float top_p = 1.f, u = 0.f;
   int top_k = 0;
   if (rank == 0) {
-    run_up(sh.upto, sh.mass);
-    kept = all_c;
-    kept_m = all_m;
     top_k = c.a.d_top_k ? c.a.d_top_k[row] : 0;
     top_p = c.a.d_top_p ? c.a.d_top_p[row] : 1.f;
     u = c.a.d_random[row];
+  }
+  // Where top-k or min-p leave few tokens, their number is enough to list them; no
+  // other token's weight is formed.
+  bool brief = false;
+  if (min_p > 0.f || (c.a.d_top_k && c.a.d_top_k[row] > 0)) {
+    for_each<T, THREADS>(s, [&](float x, uint32_t) {
+      if (x >= least && x > -INFINITY) atomicAdd(&sh.cnt[rough_bin(x)], 1u);
+    });
+    cluster.sync();
+    add_up(false);
+    cluster.sync();
+    if (rank == 0) {
+      run_up(sh.upto, sh.mass);
+      kept = all_c;
+      const uint32_t b = bin_at(sh.upto, sh.mass, true, top_k > 0 ? min((uint32_t)top_k, kept) : kept);
+      Command next{};
+      next.by_bin = (int)b;
+      next.op = sh.upto[b] <= LIST ? OP_GATHER : OP_BINS;
+      __syncthreads();
+      if (tid < c.ranks) cluster.map_shared_rank(&sh, tid)->cmd = next;
+    }
+    cluster.sync();
+    brief = sh.cmd.op == OP_GATHER;
+    if (!brief)
+      for (uint32_t i = tid; i < BINS; i += THREADS) sh.cnt[i] = 0;
+    __syncthreads();
+  }
+  if (!brief) {
+    for_each<T, THREADS>(s, [&](float x, uint32_t) {
+      int k;
+      float rest = 0.f;
+      if (look(x, k, rest)) count_in(bin_of(k), weight(sh.pow, sh.fine, k, rest));
+    });
+    cluster.sync();
+    add_up(false);
+    cluster.sync();
+    if (rank == 0) {
+      run_up(sh.upto, sh.mass);
+      kept = all_c;
+      kept_m = all_m;
+    }
   }
   // The number that the goal's sum has to reach; false: there is no such rule.
   auto aim = [&]() {
@@ -455,6 +491,10 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
       cmd.by_bin = -1;
       // (all threads of the first CTA come to the same decision)
       while (goal != GOAL_END && kept && !started) {
+        if (brief) {   // (the list's command is set; its goals are aimed at when its weights are known)
+          listed = started = true;
+          break;
+        }
         if (!aim()) {
           ++goal;
           continue;
@@ -495,6 +535,9 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
     if (cmd.op == OP_DONE) break;
     auto wanted = [&](float x, int& k, float& rest) {
       if (cmd.by_bin >= 0) {
+        const int rough = (int)rough_bin(x);
+        if (brief) return rough <= cmd.by_bin && look(x, k, rest);
+        if (cmd.by_bin < BINS - 64 && (rough > cmd.by_bin + 1 || (!cmd.through && rough < cmd.by_bin - 1))) return false;
         if (!look(x, k, rest)) return false;
         const uint32_t b = bin_of(k);
         return b == (uint32_t)cmd.by_bin || (cmd.through && b < (uint32_t)cmd.by_bin);
@@ -550,6 +593,11 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
         uint32_t ac;
         unsigned long long am;
         block_scan<WARPS>(sh, cnt, sum, ac, am);
+        if (listed) {
+          if (brief && !(goal == GOAL_K && aim())) kept_m = am;   // (the list is all that is kept)
+          while (goal < GOAL_U && !aim()) ++goal;
+          aim();
+        }
         do {
           unsigned long long m = before_m + sum;
 #pragma unroll

@@ -57,7 +57,7 @@ class _Call:
     def __init__(self, env, ids, rows, dim, w_kind, o_kind, scale=1.0, count=None, w_pad=0, o_pad=0, shift=0, seed=0, cap=None):
         self.torch, self.pkg, self.tok = env
         torch = self.torch
-        self.ids, self.rows, self.dim, self.scale = np.asarray(ids), rows, dim, scale
+        self.ids, self.rows, self.dim, self.scale = np.asarray(ids, np.int64), rows, dim, scale
         self.n = len(self.ids)
         self.count = count
         self.used = self.n if count is None else max(0, min(self.n, count))
@@ -97,12 +97,12 @@ class _Call:
         spare[self.shift:self.shift + self.n * (self.dim + self.o_pad)].view(self.n, -1)[:, :self.dim] = False
         assert bool((store[spare] == 9).all())
 
-    def backward(self, accumulate=False, start=3.0, work=None, grad=None, **other):
+    def backward(self, accumulate=False, start=3.0, work=None, grad=None, into=None, **other):
         torch = self.torch
         if grad is None:
             grad, _ = _array(torch, self.o_kind, max(self.n, 1), self.dim, self.o_pad, self.shift, seed=self.seed + 1)
             grad[self.used:] = float("nan")   # not read
-        gw, store = _array(torch, self.w_kind, self.rows, self.dim, self.w_pad, self.shift, fill=start)
+        gw, store = into or _array(torch, self.w_kind, self.rows, self.dim, self.w_pad, self.shift, fill=start)
         size = self.tok.embed_work_bytes(self.n, self.rows, self.dim)
         work = torch.full((size,), 0xee, dtype=torch.uint8, device="cuda") if work is None else work
         f = dict(d_ids=self.d_ids.data_ptr(), n=self.n, d_n=None if self.d_n is None else self.d_n.data_ptr(),
@@ -263,10 +263,13 @@ def test_streams_and_graphs(env):
     size = tok.embed_work_bytes(c.n, c.rows, c.dim)
     works = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
     graphs, outs = [], []
+    grad = c.backward()[0]
     for w in works:
+        into = _array(torch, "bf16", c.rows, c.dim, 0, 0, fill=3.0)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            outs.append(c.backward(work=w)[1])
+            c.backward(work=w, grad=grad, into=into)
+        outs.append(into[0])
         graphs.append(g)
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
