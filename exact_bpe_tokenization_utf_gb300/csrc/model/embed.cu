@@ -14,10 +14,11 @@
 // a chunk is a finished row of dW; what a chunk's first and last run share with
 // the neighbours goes to d_work, and a second kernel adds those parts in order.
 //
-// The rows that no token names are written as zeros by CTAs of their own (which rows
-// these are, the first kernel of the sort says with a bit for each).  Zeros written
-// beside the sort's kernels, whose few CTAs wait for chains of latencies, gained
-// nothing: 131,057 tokens by 2,048 columns 211 us with 48 to 128 MB there, 209 without.
+// The rows that no token names are written as zeros by CTAs of their own, as bulk
+// copies out of shared memory (131,057 tokens by 2,048 columns 185 us, with stores 201);
+// which rows these are the first kernel of the sort says, with a bit for each.  A part
+// of them beside the sort's kernels: 4,096 tokens 52 us instead of 56, but 1,000,000
+// tokens 330 instead of 311.
 #include "types.cuh"
 
 namespace tokgb {
@@ -148,30 +149,46 @@ struct Empty {
   uint32_t element;       // bytes
 };
 
-// block b's rows by all threads of the CTA (up to 1,024)
+// block b's rows by all threads of the CTA.  Rows of whole 16-byte pieces are bulk
+// copies of zeros in shared memory: a lane issues a row's, no thread waits for a store.
+constexpr uint32_t ZEROS = 8192;
 __device__ __forceinline__ void write_empty(const Empty& e, uint32_t b) {
   __shared__ uint32_t s_named;
+  __shared__ __align__(128) uint4 s_zero[ZEROS / 16];
   if (threadIdx.x < 32) {
     uint32_t m = 0;
     for (uint32_t s = threadIdx.x; s < e.spans; s += 32) m |= e.named[(size_t)s * e.words + b];
     m = __reduce_or_sync(ALL, m);
     if (threadIdx.x == 0) s_named = m;
   }
+  if (e.eights) {
+    for (uint32_t i = threadIdx.x; i < ZEROS / 16; i += blockDim.x) s_zero[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   __syncthreads();
   uint32_t left = ~s_named;
   const uint32_t rows = min(32u, e.n_rows - b * 32);
   if (rows < 32) left &= (1u << rows) - 1u;
+  if (e.eights) {
+    if (threadIdx.x < 32) {
+      if (left >> threadIdx.x & 1u) {
+        uint8_t* to = e.rows + (long long)(b * 32 + threadIdx.x) * e.stride;
+        const uint32_t from = (uint32_t)__cvta_generic_to_shared(s_zero);
+        for (uint32_t i = 0; i < (uint32_t)e.row; i += ZEROS)
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to + i), "r"(from),
+                       "r"(min(ZEROS, (uint32_t)e.row - i)) : "memory");
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    return;
+  }
   // each warp takes rows in turn
   for (uint32_t k = 0; left; left &= left - 1, ++k) {
     if (k % (blockDim.x >> 5) != threadIdx.x >> 5) continue;
     uint8_t* to = e.rows + (long long)(b * 32 + __ffs(left) - 1) * e.stride;
     const uint32_t lane = threadIdx.x & 31u;
-    if (e.eights) {
-      uint4* q = reinterpret_cast<uint4*>(to);
-      const uint32_t n = (uint32_t)(e.row / 16);
-#pragma unroll 8
-      for (uint32_t i = lane; i < n; i += 32) q[i] = make_uint4(0, 0, 0, 0);
-    } else if (e.element == 4) {
+    if (e.element == 4) {
       for (uint32_t i = lane; i < (uint32_t)(e.row / 4); i += 32) reinterpret_cast<uint32_t*>(to)[i] = 0;
     } else {
       for (uint32_t i = lane; i < (uint32_t)(e.row / 2); i += 32) reinterpret_cast<uint16_t*>(to)[i] = 0;
@@ -657,7 +674,7 @@ int tok_embed_backward(tok_handle* h, const tok_embed_grad_args* a, void* stream
   const Empty em{sc.named, p.spans, a->n_rows, (a->n_rows + 31) / 32, static_cast<uint8_t*>(a->d_grad_weight),
                  (long long)(a->grad_weight_stride * (int64_t)size), (unsigned long long)a->dim * size,
                  in_eights(a->d_grad_weight, a->grad_weight_stride, a->grad_weight_dtype, a->dim), (uint32_t)size};
-  const uint32_t m = a->accumulate ? 0 : em.words;   // blocks of rows
+  const uint32_t m = a->accumulate ? 0 : em.words;   // blocks of 32 rows
   cudaError_t e = allow_all<k_sort_count>(h->dev);
   if (e == cudaSuccess) e = allow_all<k_sort_place<0>>(h->dev);
   if (e == cudaSuccess) e = allow_all<k_sort_place<1>>(h->dev);

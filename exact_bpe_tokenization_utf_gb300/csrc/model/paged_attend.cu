@@ -251,18 +251,20 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
     in.head_off = (long long)head * c.head_stride;
     const uint32_t tiles_here = tile1 - tile0;
 
-    // the first steps' copies; the place of each step's tokens is looked up a step early
-    long long p = p0 + warp * STEP + (lane & 15u);
-    long long next = in.place(p);
+    // the first steps' copies, their places looked up together; then the place of each
+    // step's tokens is looked up a step early
+    long long p = p0 + warp * STEP + (lane & 15u), next[S::DEPTH];
     uint32_t ring[S::DEPTH - 1];   // which tokens of the steps under way are there
 #pragma unroll
+    for (int i = 0; i < S::DEPTH; ++i) next[i] = in.place(p + i * TILE);
+#pragma unroll
     for (int i = 0; i < S::DEPTH - 1; ++i) {
-      ring[i] = __ballot_sync(ALL, next >= 0) & 0xffffu;
-      if ((uint32_t)i < tiles_here) in.issue(i, next);
+      ring[i] = __ballot_sync(ALL, next[i] >= 0) & 0xffffu;
+      if ((uint32_t)i < tiles_here) in.issue(i, next[i]);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      p += TILE;
-      next = in.place(p);
     }
+    long long ahead_at = next[S::DEPTH - 1];
+    p += (S::DEPTH - 1) * TILE;
     // the queries, as the matrices' second operand
     uint32_t q[NT][D / 16][2];
 #pragma unroll
@@ -292,11 +294,11 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
       // the copies DEPTH - 1 steps ahead, into the stage that was read last
       const uint32_t ahead = stage == 0 ? S::DEPTH - 1 : stage - 1;
       __syncwarp();
-      const uint32_t seen = __ballot_sync(ALL, next >= 0) & 0xffffu;
+      const uint32_t seen = __ballot_sync(ALL, ahead_at >= 0) & 0xffffu;
       if (step + S::DEPTH - 1 < tiles_here) {
-        in.issue(ahead, next);
+        in.issue(ahead, ahead_at);
         p += TILE;
-        next = in.place(p);
+        ahead_at = in.place(p);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       uint32_t live = ring[0];
