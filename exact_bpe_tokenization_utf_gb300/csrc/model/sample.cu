@@ -11,12 +11,21 @@
 // numbers, formed with 38 bits or more, and sums are whole numbers: they do not depend
 // on the order in which threads add.
 //
-// A row is read once: a cluster of CTAs holds it in shared memory.  After the
-// maximum, each token is counted in one of 1,024 bins of equal width of log w, with
-// its weight.  The bins' sums say in which bin a border lies; the tokens of that bin
-// (a few hundred at most, as a rule) go to the cluster's first CTA, which sorts them.
-// Where there are more, bins of keys (scores as whole numbers of the same order) come
-// in between, until a bin holds few tokens or a single score.
+// Rows of 32-bit scores: a cluster of CTAs holds the row in shared memory, so that it
+// is read once.  After the maximum, each token is counted in one of 2,048 bins of equal
+// width of log w, with its weight.  The bins' sums say in which bin a border lies; the
+// tokens of that bin (a few hundred, as a rule) go to the cluster's first CTA, which
+// sorts them.  Where there are more, bins of keys (scores as whole numbers of the same
+// order) come in between, until a bin holds few tokens or a single score.  Where top-k or
+// min-p leave few tokens, their number is found without weights and they go there at once.
+// Bound by instructions: a weight takes about 45.
+//
+// Rows of 16-bit scores have few different scores.  They are counted score by score, with
+// an atomic on shared memory for each token and two tokens in each operation before it; a
+// weight is formed once for a score, and a border is met by counts alone.  The choice's
+// id is then searched in the row, which is read again from L2.  512 rows of 100,257 bf16
+// scores 70 us on a GB300 (the bytes: 15 us): 25 to 50 of counting (bound by the atomics,
+// 3 cycles for a warp's 32), 8 of weights, 3 of borders, 6 to 14 of the search.
 #include "types.cuh"
 
 #include <cooperative_groups.h>
@@ -28,14 +37,12 @@ namespace cg = cooperative_groups;
 
 constexpr uint32_t ALL = 0xffffffffu;
 constexpr uint32_t MOST_LOGITS = 1u << 20;
-constexpr int MOST_WARPS = 16;                // of a CTA
-constexpr int BINS = 1024;                    // of 2^-4 in log2 w each, the last one for all below
-constexpr int BIN_SHIFT = 12;                 // from 2^-16 in log2 w
+constexpr int MOST_WARPS = 32;                // of a CTA
 constexpr uint32_t LIST = 1024;               // most tokens that are sorted
 constexpr double ONE = 8796093022208.0;       // the largest weight, 2^43; 2^20 of them fit 64 bits
 constexpr int MOST_COMMANDS = 64;             // three goals of at most 8 each; a limit, so that the kernel ends
 constexpr float LOWEST = -62.f;               // log2 of weights that count (below 2^-43 they are 0 anyway)
-constexpr int LOWEST_K = -(BINS << BIN_SHIFT);
+constexpr int LOWEST_K = -(1 << 22);          // of log2 w in units of 2^-16
 
 // --- weights ---------------------------------------------------------------------
 
@@ -101,7 +108,6 @@ __device__ __forceinline__ int fixed_log2(float hi, float lo, float& rest) {
   rest = (hi - (m - MAGIC)) + lo;
   return min(__float_as_int(m) - __float_as_int(MAGIC), 0);
 }
-__device__ __forceinline__ uint32_t bin_of(int k) { return min((uint32_t)-k >> BIN_SHIFT, (uint32_t)BINS - 1u); }
 
 // 2^43 times w: 2^(k / 65536 + rest) is a whole power of 2, two factors from the
 // tables and 1 + q for the rest (below 2^-17), so that 32-bit arithmetic on q is enough.
@@ -154,7 +160,9 @@ struct Command {
   int through;          // OP_GATHER: of all bins up to it
 };
 
-struct Shared {
+// Bins are of 2^BIN_SHIFT units of log2 w, to 2^-64; the last one is for all below, too.
+template <int BIN_SHIFT> struct Shared {
+  static constexpr int BINS = 1 << (22 - BIN_SHIFT);
   Pow pow[256];
   Fine fine[256];
   uint32_t cnt[BINS], low[BINS], high[BINS];         // this CTA's bins
@@ -223,8 +231,8 @@ struct SampleCall {
 };
 
 // sums over the threads before, and of all (in every thread)
-template <int WARPS>
-__device__ __forceinline__ void block_scan(Shared& sh, uint32_t& c, unsigned long long& m, uint32_t& all_c, unsigned long long& all_m) {
+template <int WARPS, class S>
+__device__ __forceinline__ void block_scan(S& sh, uint32_t& c, unsigned long long& m, uint32_t& all_c, unsigned long long& all_m) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   uint32_t ic = c;
   unsigned long long im = m;
@@ -260,9 +268,10 @@ __device__ __forceinline__ void block_scan(Shared& sh, uint32_t& c, unsigned lon
   m = bm + im - m;
 }
 
-template <class T, int THREADS>
+template <class T, int THREADS, int BIN_SHIFT>
 __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
-  constexpr int WARPS = THREADS / 32, PER_BIN = BINS / THREADS, PER_LIST = LIST / THREADS;
+  using Shared = tokgb::Shared<BIN_SHIFT>;
+  constexpr int BINS = Shared::BINS, WARPS = THREADS / 32, PER_BIN = BINS / THREADS, PER_LIST = LIST / THREADS;
   Shared& sh = *reinterpret_cast<Shared*>(mem);
   cg::cluster_group cluster = cg::this_cluster();
   const uint32_t rank = cluster.block_rank(), row = blockIdx.x / c.ranks, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
@@ -328,6 +337,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   times_c(r, most, r.p_max, r.e_max);
   r.only_max = temp < 0x1p-100f || !(fabsf(r.p_max) < INFINITY);
   const float least = least_of(r, temp, min_p, sh.t_ln_m);
+  auto bin_of = [](int k) { return min((uint32_t)-k >> BIN_SHIFT, (uint32_t)BINS - 1u); };
   // what a token of the row is counted as; false: it is not kept
   auto look = [&](float x, int& k, float& rest) {
     if (!(x >= least) || x == -INFINITY) return false;
@@ -344,30 +354,39 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   };
   // a bin of the same width without the care that weights take: off by one at most (but
   // for the last ones), and it never falls where x falls either
-  const float bin_scale = 16.f * r.c_hi;
+  const float bin_scale = (float)(65536 >> BIN_SHIFT) * r.c_hi;
   auto rough_bin = [&](float x) {
     if (r.only_max) return x == r.x_max ? 0u : (uint32_t)BINS - 1u;
     return (uint32_t)min((int)((r.x_max - x) * bin_scale), BINS - 1);
   };
   // the row's bins: each CTA adds a share of them, for the first one
-  auto add_up = [&](bool sub) {
+  auto add_up = [&](bool sub, bool weights) {
     Shared* first = cluster.map_shared_rank(&sh, 0);
     // (ranks lanes side by side read a bin of a CTA each)
-    const uint32_t i = tid & (c.ranks - 1), b0 = rank * (BINS / c.ranks);
+    const uint32_t i = tid & (c.ranks - 1), b0 = rank * (BINS / c.ranks) + tid / c.ranks;
     const Shared* o = cluster.map_shared_rank(&sh, i);
-    for (uint32_t b = b0 + tid / c.ranks; b < b0 + BINS / c.ranks; b += THREADS / c.ranks) {
-      uint32_t n = o->cnt[b];
-      unsigned long long m = o->low[b] + ((unsigned long long)o->high[b] << 32);
+    uint32_t n[PER_BIN];
+    unsigned long long m[PER_BIN];
+#pragma unroll
+    for (int k = 0; k < PER_BIN; ++k) {
+      const uint32_t b = b0 + k * (THREADS / c.ranks);
+      n[k] = o->cnt[b];
+      m[k] = weights ? o->low[b] + ((unsigned long long)o->high[b] << 32) : 0ull;
+    }
+#pragma unroll
+    for (int k = 0; k < PER_BIN; ++k) {
       for (uint32_t d = 1; d < c.ranks; d *= 2) {
-        n += __shfl_xor_sync(ALL, n, d);
-        m += __shfl_xor_sync(ALL, m, d);
+        n[k] += __shfl_xor_sync(ALL, n[k], d);
+        if (weights) m[k] += __shfl_xor_sync(ALL, m[k], d);
       }
+      const uint32_t b = b0 + k * (THREADS / c.ranks);
       if (i == 0) {
-        (sub ? first->sub.upto : first->upto)[b] = n;
-        (sub ? first->sub.mass : first->mass)[b] = m;
+        (sub ? first->sub.upto : first->upto)[b] = n[k];
+        (sub ? first->sub.mass : first->mass)[b] = m[k];
       }
     }
   };
+
   // sums of the bins up to each (in the first CTA)
   uint32_t all_c = 0;
   unsigned long long all_m = 0;
@@ -429,7 +448,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
       if (x >= least && x > -INFINITY) atomicAdd(&sh.cnt[rough_bin(x)], 1u);
     });
     cluster.sync();
-    add_up(false);
+    add_up(false, false);
     cluster.sync();
     if (rank == 0) {
       run_up(sh.upto, sh.mass);
@@ -454,7 +473,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
       if (look(x, k, rest)) count_in(bin_of(k), weight(sh.pow, sh.fine, k, rest));
     });
     cluster.sync();
-    add_up(false);
+    add_up(false, true);
     cluster.sync();
     if (rank == 0) {
       run_up(sh.upto, sh.mass);
@@ -673,7 +692,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
         if (wanted(x, k, rest)) count_in((cmd.hi - key_of(x)) >> cmd.shift, weight(sh.pow, sh.fine, k, rest));
       });
       cluster.sync();
-      add_up(true);
+      add_up(true, true);
       cluster.sync();
       if (rank == 0) {
         uint32_t keep_c = all_c;
@@ -746,19 +765,19 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
       __syncthreads();
     }
   }
-  // (min-p above 1 keeps nothing)
-  if (rank == 0 && tid == 0 && kept == 0) {
+  // (min-p above 1 keeps nothing; commands do not run out)
+  if (rank == 0 && tid == 0 && (kept == 0 || goal != GOAL_END)) {
     c.a.d_pick[row] = -1;
     if (c.a.d_kept) c.a.d_kept[row] = 0;
     if (c.a.d_logprob) c.a.d_logprob[row] = -INFINITY;
   }
 }
 
-constexpr int SAMPLE_THREADS = 512;
+constexpr int SAMPLE_THREADS = 512, SAMPLE_BINS = 11, FEW_BINS = 12;   // (BIN_SHIFT; fewer where counts share the memory)
 template <class T>
 __global__ void __launch_bounds__(SAMPLE_THREADS, 2) k_sample(const __grid_constant__ SampleCall c) {
   extern __shared__ __align__(16) uint8_t mem[];
-  choose<T, SAMPLE_THREADS>(c, mem);
+  choose<T, SAMPLE_THREADS, SAMPLE_BINS>(c, mem);
 }
 
 // --- 16-bit scores -------------------------------------------------------------------
@@ -767,19 +786,19 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) k_sample(const __grid_const
 // a weight is formed once for each.  What lies below -2^11 is only counted, and must have
 // no weight; a row with other scores (2^11 or more, below 2^-27 in bf16, NaN) takes the
 // way above.
-template <class T> struct Places { static constexpr uint32_t LOW = 0, HIGH = 256; using Count = uint16_t; };   // (not used)
+template <class T> struct Places { static constexpr uint32_t LOW = 0, HIGH = 256; static constexpr int THREADS = 256; using Count = uint16_t; };   // (not used)
 template <> struct Places<__nv_bfloat16> {
   static constexpr uint32_t LOW = 100u << 7, HIGH = 138u << 7, INF = 0x7f80;   // the bits of 2^-27, 2^11
+  static constexpr int THREADS = 256, ROUNDS = 8;                              // four CTAs per SM
   using Count = uint32_t;
 };
 template <> struct Places<__half> {
   static constexpr uint32_t LOW = 0, HIGH = 26u << 10, INF = 0x7c00;           // all but 0, 2^11
+  static constexpr int THREADS = 1024, ROUNDS = 2;                             // one
   using Count = uint16_t;                                                      // (as words they would not fit)
 };
 constexpr float FAR = -2048.f;
 constexpr int GROUP = 256;                 // places of a warp's step
-constexpr int COUNT_THREADS = 256, COUNT_WARPS = COUNT_THREADS / 32;
-constexpr uint32_t ROUNDS = 8;              // most of the search for the choice, of 256 pieces a warp
 
 // Counts lie by size, positive scores first, then negative ones, then 0.  In the order
 // of falling scores (places): the positive ones backwards, a group with 0, the others.
@@ -857,6 +876,8 @@ __device__ __forceinline__ void warp_scan(uint32_t& c, unsigned long long& m) {
 template <class T>
 __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem) {
   using C = Counts<T>;
+  constexpr int COUNT_THREADS = Places<T>::THREADS, COUNT_WARPS = COUNT_THREADS / 32;
+  constexpr uint32_t ROUNDS = Places<T>::ROUNDS;   // of the search for the choice, of 256 pieces a warp, at most
   constexpr uint32_t RANGE = C::RANGE, LOW = Places<T>::LOW;
   C& sh = *reinterpret_cast<C*>(mem);
   cg::cluster_group cluster = cg::this_cluster();
@@ -1289,10 +1310,10 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
 }
 
 template <class T>
-__device__ __noinline__ void choose_any(const SampleCall& c, uint8_t* mem) { choose<T, COUNT_THREADS>(c, mem); }
+__device__ __noinline__ void choose_any(const SampleCall& c, uint8_t* mem) { choose<T, Places<T>::THREADS, FEW_BINS>(c, mem); }
 
 template <class T>
-__global__ void __launch_bounds__(COUNT_THREADS, 4) k_sample_counted(const __grid_constant__ SampleCall c) {
+__global__ void __launch_bounds__(Places<T>::THREADS, 1024 / Places<T>::THREADS) k_sample_counted(const __grid_constant__ SampleCall c) {
   extern __shared__ __align__(16) uint8_t mem[];
   if (!choose_counted<T>(c, mem)) choose_any<T>(c, mem);
 }
@@ -1301,24 +1322,24 @@ template <class T>
 cudaError_t launch(tok_handle* h, const tok_sample_args* a, cudaStream_t s) {
   SampleCall c{};
   c.a = *a;
-  const size_t base = (sizeof(Shared) + 15) & ~size_t(15);
+  const size_t base = (sizeof(Shared<SAMPLE_BINS>) + 15) & ~size_t(15);
   // CTAs at once: as many as an SM's threads' registers (64 each) and shared memory have room for
-  const uint32_t fit = sizeof(T) == 2 ? (uint32_t)std::min<size_t>(4, 228 * 1024 / (std::max(base, sizeof(Counts<T>)) + 1024)) : 2u;
+  const uint32_t fit = sizeof(T) == 2 ? (uint32_t)std::min<size_t>(4, 228 * 1024 / (std::max(sizeof(Shared<FEW_BINS>), sizeof(Counts<T>)) + 1024)) : 2u;
   const uint32_t room = fit * (uint32_t)h->n_sms;
   // counts of 16 bits have to hold a CTA's, and the search its slice
-  const uint32_t most = sizeof(T) == 2 && sizeof(typename Places<T>::Count) == 4 ? (COUNT_WARPS - 1) * ROUNDS * 2048 - 8 : 65000u;
+  const uint32_t most = sizeof(T) == 2 && sizeof(typename Places<T>::Count) == 4 ? (256 / 32 - 1) * 8 * 2048 - 8 : 63000u;
   uint32_t n = 1;
   while (n < 16 && (a->n_logits / n > most || (a->n_logits / n > (sizeof(T) == 2 ? 16384u : 4096u) && (uint64_t)a->rows * n * 2 <= room))) n *= 2;
   c.ranks = n;
   c.per = ((a->n_logits + n - 1) / n + 7) / 8 * 8;
   if constexpr (sizeof(T) == 2) {
     // (a CTA's count of a score has to fit; 2^20 scores are too many for 16 CTAs)
-    if (sizeof(typename Places<T>::Count) == 4 || c.per < 65536)
-      return launch_clusters<k_sample_counted<T>>(h->dev, a->rows * n, COUNT_THREADS, n, std::max(base, sizeof(Counts<T>)), s, c);
+    if (sizeof(typename Places<T>::Count) == 4 || c.per <= 63488)
+      return launch_clusters<k_sample_counted<T>>(h->dev, a->rows * n, Places<T>::THREADS, n, std::max(sizeof(Shared<FEW_BINS>), sizeof(Counts<T>)), s, c);
   }
   if constexpr (sizeof(typename Places<T>::Count) != 4) {
     const size_t slice = (size_t)c.per * sizeof(T) + 16;
-    c.resident = base + slice <= MOST_SHARED;
+    c.resident = base + slice <= 112 * 1024;   // (two CTAs per SM: 256 rows of 100,257 scores 226 us, with one that keeps them 330)
     return launch_clusters<k_sample<T>>(h->dev, a->rows * n, SAMPLE_THREADS, n, base + (c.resident ? slice : 0), s, c);
   }
   return cudaErrorInvalidValue;   // (not reached)
