@@ -127,6 +127,9 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed_any(EmbedCall c) {
 
 // --- the tokens sorted by their ids ----------------------------------------------
 
+// Bound by latencies: 131,057 tokens over 100,257 rows in 6 us of counting and 13 and 12
+// us of placing (64 CTAs; tiles of 4,096 tokens, 32 CTAs: 2 us more for both, of 1,024
+// tokens: the gradient 242 us instead of 222), 4,096 tokens in 4, 9 and 8.
 // A pass of the sort: every CTA takes a span of the tokens, in tiles.  A tile's
 // warps take 256 tokens each, 32 at a time, so that a token's place among those
 // of its digit is their order; counts of the digits by CTA (the table `counts`,
@@ -436,6 +439,9 @@ __device__ __forceinline__ void put_part(float* p, const float* s) {
   reinterpret_cast<float4*>(p)[1] = make_float4(s[4], s[5], s[6], s[7]);
 }
 
+// Bound by the bytes: 131,057 rows of 2,048 bf16 columns in, 100,257 rows out, in 145 us
+// (6.5 TB/s); chunks of 32 tokens while a warp's columns and chunks are 8,192 or fewer,
+// then longer ones, up to 128: parts that go to d_work are two rows of 32 bits a chunk.
 constexpr int AHEAD = 8;  // rows whose loads are under way
 constexpr uint32_t LONG_RUN = 8;  // chunks of a run that a whole CTA adds
 

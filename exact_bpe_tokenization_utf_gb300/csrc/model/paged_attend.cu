@@ -9,8 +9,8 @@
 // Tokens are taken in tiles of 64 of one request and key head.  All tiles of all
 // requests form one row; each CTA (as many as the SMs hold at once) takes an equal
 // piece of it, so that long and short requests share the GPU evenly.  A warp takes
-// 16 tokens at a time, which it copies into shared memory of its own (cp.async,
-// three steps ahead or more), so that warps never wait for one another; it keeps
+// 16 tokens at a time, which it copies into shared memory of its own (cp.async, two
+// steps ahead, five for widths of 64), so that warps never wait for one another; it keeps
 // the maximum, the sum and the output of its tokens, and the CTA joins its warps'
 // when the piece of a request and head ends.  What a CTA has only a part of goes to
 // d_work and a second kernel joins the parts, in order: the same bits each time.
@@ -22,6 +22,12 @@
 // as they lie (ldmatrix, transposed for the values), and P^T comes from S^T by
 // movmatrix.  The matrix work is a small part of the time that the bytes take: at
 // group 8 and width 128, 24 instructions of 2,048 multiply-adds for 8 KB.
+//
+// Measured on a GB300 (6.7 TB/s of plain copying): 256 requests of up to 4,801 tokens, 8
+// key heads of 128, group 8, in 390 us (6.5 TB/s); 64 requests of 0 to 16,381 tokens in 81
+// us (5.5); one of 32,749 in 36 us (3.7): of these 2 are the way to the first copies, 24
+// the bytes, 4 the warps' and CTAs' joins, the rest the second kernel, which the first lets
+// start early.  Without the starts' share in the pieces the 64 requests took 133 us.
 #include "types.cuh"
 
 #include <cfloat>
@@ -514,7 +520,8 @@ struct StoreCall {
 };
 
 // A copy of 2 * row units a head and token; a thread takes one of the keys and one of
-// the values.
+// the values.  Bound by the bytes: 16,381 tokens of 8 heads of 128 in 19 us (7.1 TB/s, the
+// writes in part still in L2).
 __global__ void __launch_bounds__(256) k_store(StoreCall c) {
   const uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const uint32_t per = c.kv_heads * c.row;

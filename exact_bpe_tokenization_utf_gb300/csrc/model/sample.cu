@@ -1326,6 +1326,10 @@ cudaError_t launch(tok_handle* h, const tok_sample_args* a, cudaStream_t s) {
   // CTAs at once: as many as an SM's threads' registers (64 each) and shared memory have room for
   const uint32_t fit = sizeof(T) == 2 ? (uint32_t)std::min<size_t>(4, 228 * 1024 / (std::max(sizeof(Shared<FEW_BINS>), sizeof(Counts<T>)) + 1024)) : 2u;
   const uint32_t room = fit * (uint32_t)h->n_sms;
+  // More CTAs for a row while all CTAs run at once and a CTA keeps 16,384 scores (32 bits:
+  // 4,096): adding up bins over a cluster costs more than it gains from there.  us with 1,
+  // 2, 4 and 8 CTAs for a row of bf16: 64 rows of 50,257 27, 23, 25, 32; 512 of 100,257
+  // 70, 78, 119, 192; one of 100,257 27, 25, 23, 21; 150 39, 33, 47, 70.
   // counts of 16 bits have to hold a CTA's, and the search its slice
   const uint32_t most = sizeof(T) == 2 && sizeof(typename Places<T>::Count) == 4 ? (256 / 32 - 1) * 8 * 2048 - 8 : 63000u;
   uint32_t n = 1;
