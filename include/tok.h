@@ -476,7 +476,7 @@ int tok_embed(tok_handle* h, const tok_embed_args* a, void* stream);
 /* tok_embed_backward -- the gradient of tok_embed with respect to the weights:
  *   grad_weight[v][j] = scale * sum of grad_out[t][j] over t < n' with ids[t] == v
  * Tokens are sorted by their ids; a row's sum is in 32 bits, in an order that
- * n, d_n's value, the types and the strides fix alone: the same bits each time.
+ * n, dim and d_n's value fix alone: the same bits each time.
  * accumulate == 0: the n_rows rows are written whole (zeros where no id is v).
  * accumulate != 0: the sum is added, in 32 bits, to the rows that ids name, and
  * the others are neither read nor written.
