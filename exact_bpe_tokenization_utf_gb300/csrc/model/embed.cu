@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed_any(EmbedCall c) {
 
 // Bound by latencies: 131,057 tokens over 100,257 rows in 6 us of counting and 13 and 12
 // us of placing (64 CTAs; tiles of 4,096 tokens, 32 CTAs: 2 us more for both, of 1,024
-// tokens: the gradient 242 us instead of 222), 4,096 tokens in 4, 9 and 8.
+// tokens: the gradient 242 us instead of 222), 4,096 tokens in 4, 9 and 8 (all of it by one
+// CTA in its shared memory: the gradient 54 us instead of 55).
 // A pass of the sort: every CTA takes a span of the tokens, in tiles.  A tile's
 // warps take 256 tokens each, 32 at a time, so that a token's place among those
 // of its digit is their order; counts of the digits by CTA (the table `counts`,
@@ -576,6 +577,8 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed_join(SumCall c) {
 
 // --- the host's side -----------------------------------------------------------------
 
+constexpr uint64_t MOST_SHORT = 8192;   // chunks times warps of a row, with chunks below 128 tokens
+
 uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
 struct Plan {
@@ -595,17 +598,20 @@ Plan plan_of(uint64_t n, uint32_t n_rows, uint32_t dim) {
   p.spans = (uint32_t)((tiles + per - 1) / per);
   p.segs = (dim + COLS - 1) / COLS;
   p.chunk = 32;
-  while (p.chunk < 128 && n / p.chunk * p.segs > 8192) p.chunk *= 2;
+  while (p.chunk < 128 && n / p.chunk * p.segs > MOST_SHORT) p.chunk *= 2;
   p.chunks = (uint32_t)((n + p.chunk - 1) / p.chunk);
+  // room for fewer ids, too, of which there may be more spans or chunks
+  const uint64_t spans = std::min<uint64_t>(tiles, MOST_SPANS);
+  const uint64_t chunks = std::min<uint64_t>((n + 31) / 32, std::max<uint64_t>(MOST_SHORT / p.segs + 1, (n + 127) / 128));
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) { const uint64_t here = at; at = up(at + bytes, 256); return here; };
-  p.counts0 = take((uint64_t)p.spans * 4 << p.bits0);
-  p.counts1 = take(p.bits1 ? (uint64_t)p.spans * 4 << p.bits1 : 0);
-  p.named = take((uint64_t)p.spans * ((n_rows + 31) / 32) * 4);
+  p.counts0 = take(spans * 4 << p.bits0);
+  p.counts1 = take(p.bits1 ? spans * 4 << p.bits1 : 0);
+  p.named = take(spans * ((n_rows + 31) / 32) * 4);
   p.half = take(p.bits1 ? n * 8 : 0);
   p.sorted = take(n * 8);
-  p.parts = take((uint64_t)p.chunks * 2 * p.segs * COLS * 4);
-  p.runs = take((uint64_t)p.chunks * 4 + 8);
+  p.parts = take(chunks * 2 * p.segs * COLS * 4);
+  p.runs = take(chunks * 4 + 8);
   p.bytes = at;
   return p;
 }
@@ -714,9 +720,10 @@ int tok_embed_backward(tok_handle* h, const tok_embed_grad_args* a, void* stream
   if (e == cudaSuccess) e = allow_all<k_sort_place<0>>(h->dev);
   if (e == cudaSuccess) e = allow_all<k_sort_place<1>>(h->dev);
   if (e != cudaSuccess) return cuda_fail(h, e, "shared memory of a kernel");
-  auto room = [](uint32_t bits) { return ((size_t)4 << bits) + ((size_t)2 * (ST_WARPS + 1) << bits); };
-  k_sort_count<<<p.spans, ST_THREADS, ((size_t)4 << p.bits0) + (sc.named ? (size_t)em.words * 4 : 0), s>>>(sc);
   unsigned launches = 1;
+  const size_t bitmap = sc.named ? (size_t)em.words * 4 : 0;
+  auto room = [](uint32_t bits) { return ((size_t)4 << bits) + ((size_t)2 * (ST_WARPS + 1) << bits); };
+  k_sort_count<<<p.spans, ST_THREADS, ((size_t)4 << p.bits0) + bitmap, s>>>(sc);
   launch_behind(k_sort_place<0>, p.spans, ST_THREADS, room(p.bits0), s, sc);
   ++launches;
   if (p.bits1) {

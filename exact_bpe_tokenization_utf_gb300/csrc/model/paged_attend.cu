@@ -46,6 +46,10 @@ constexpr uint32_t MOST_REQUESTS = 1u << 20, MOST_GROUP = 64;
 // more than this above it (in powers of 2): weights stay below 2^8.
 constexpr float SLACK = 8.f;
 
+// Kernels are made for widths of 64, 128 and 256; others take the next one's, with zeros
+// in shared memory (256 requests of up to 4,000 tokens, 8 key heads of 80: 317 us, and 331
+// with kernels for 96 and 192, too: what bounds it is that 160 bytes of a token lie in
+// three or four of the 64-byte pieces that DRAM is read in).
 template <int D> struct Shape {
   static constexpr int ROW = D * 2;                    // bytes of a token in shared memory
   static constexpr int STAGE = 2 * STEP * ROW;         // keys and values of a step

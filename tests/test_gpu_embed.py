@@ -281,6 +281,23 @@ def test_streams_and_graphs(env):
     assert all(torch.equal(o, want) for o in outs)
 
 
+def test_a_buffer_serves_fewer_ids(env):
+    torch, pkg, tok = env
+    for rows, dim in ((700, 8), (100257, 2048), (1 << 20, 256), (5000, 1031)):
+        sizes = [tok.embed_work_bytes(n, rows, dim) for n in
+                 (0, 1, 31, 32, 4095, 4096, 4097, 6144, 8192, 16384, 32767, 32768, 32769, 65536, 65537, 262143, 311296, 311297, 1 << 20,
+                  1 << 22)]
+        assert sizes == sorted(sizes)
+        steps = [tok.embed_work_bytes(n, rows, dim) for n in range(0, 400000, 997)]
+        assert steps == sorted(steps)
+    big = tok.embed_work_bytes(40000, 300, 2048)
+    work = torch.full((big,), 0xee, dtype=torch.uint8, device="cuda")
+    for n in (1, 4096, 4097, 32768, 40000):
+        c = _Call(env, _ids(n, n, 300), 300, 2048, "bf16", "bf16")
+        grad, gw, _ = c.backward(work=work, work_bytes=big)
+        assert torch.equal(gw, c.backward(grad=grad)[1])
+
+
 def test_refusals(env):
     torch, pkg, tok = env
     c = _Call(env, _ids(1, 10, 20), 20, 8, "f32", "f32")
