@@ -193,7 +193,7 @@ struct Slice {
 
 // By all threads: one(place, element) for the elements before and after the 16-byte
 // pieces that the slice has, piece(place, its elements) for these.
-template <class T, int N, class F, class G>
+template <class T, int N, int UNROLL, class F, class G>
 __device__ __forceinline__ void for_vectors(const Slice& s, F one, G piece) {
   const T* x = static_cast<const T*>(s.at);
   const uint32_t n = s.to - s.from;
@@ -204,13 +204,13 @@ __device__ __forceinline__ void for_vectors(const Slice& s, F one, G piece) {
     const uint32_t e = i < head ? i : tail + (i - head);
     one(e, x[e]);
   }
-#pragma unroll 4
+#pragma unroll UNROLL
   for (uint32_t i = threadIdx.x; i < vecs; i += N) piece(head + i * VEC, reinterpret_cast<const uint4*>(x + head)[i]);
 }
 // f(score, id) for every element
 template <class T, int N, class F>
 __device__ __forceinline__ void for_each(const Slice& s, F f) {
-  for_vectors<T, N>(s, [&](uint32_t e, T x) { f(to_f32(x), s.from + e); }, [&](uint32_t e, uint4 q) {
+  for_vectors<T, N, sizeof(T) == 4 ? 2 : 1>(s, [&](uint32_t e, T x) { f(to_f32(x), s.from + e); }, [&](uint32_t e, uint4 q) {
     const T* y = reinterpret_cast<const T*>(&q);
 #pragma unroll
     for (uint32_t i = 0; i < 16 / sizeof(T); ++i) f(to_f32(y[i]), s.from + e + i);
@@ -288,7 +288,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   s.at = src;
   if (c.resident) {
     T* keep = reinterpret_cast<T*>(mem + ((sizeof(Shared) + 15) & ~size_t(15)) + (reinterpret_cast<uintptr_t>(src) & 15u));
-    for_vectors<T, THREADS>(s, [&](uint32_t e, T x) {
+    for_vectors<T, THREADS, 4>(s, [&](uint32_t e, T x) {
       most = max_nan(most, to_f32(x));
       keep[e] = x;
     }, [&](uint32_t e, uint4 q) {
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) k_sample(const __grid_const
 // a weight is formed once for each.  What lies below -2^11 is only counted, and must have
 // no weight; a row with other scores (2^11 or more, below 2^-27 in bf16, NaN) takes the
 // way above.
-template <class T> struct Places { static constexpr uint32_t LOW = 0, HIGH = 256; static constexpr int THREADS = 256; using Count = uint16_t; };   // (not used)
+template <class T> struct Places;
 template <> struct Places<__nv_bfloat16> {
   static constexpr uint32_t LOW = 100u << 7, HIGH = 138u << 7, INF = 0x7f80;   // the bits of 2^-27, 2^11
   static constexpr int THREADS = 256, ROUNDS = 8;                              // four CTAs per SM
@@ -1318,33 +1318,37 @@ __global__ void __launch_bounds__(Places<T>::THREADS, 1024 / Places<T>::THREADS)
   if (!choose_counted<T>(c, mem)) choose_any<T>(c, mem);
 }
 
+// More CTAs for a row while all of them run at once (fit: on an SM) and each keeps `few`
+// scores: adding up bins over a cluster costs more than it gains from there.  us with 1,
+// 2, 4 and 8 CTAs for a row of bf16 (16,384 scores): 64 rows of 50,257 27, 23, 25, 32; 512
+// of 100,257 70, 78, 119, 192; one of 100,257 27, 25, 23, 21; 150 39, 33, 47, 70.
+void split(const tok_handle* h, uint32_t fit, uint32_t most, uint32_t few, SampleCall& c) {
+  const uint32_t V = c.a.n_logits;
+  uint32_t n = 1;
+  while (n < 16 && (V / n > most || (V / n > few && (uint64_t)c.a.rows * n * 2 <= (uint64_t)fit * (uint32_t)h->n_sms))) n *= 2;
+  c.ranks = n;
+  c.per = ((V + n - 1) / n + 7) / 8 * 8;
+}
+
 template <class T>
 cudaError_t launch(tok_handle* h, const tok_sample_args* a, cudaStream_t s) {
   SampleCall c{};
   c.a = *a;
-  const size_t base = (sizeof(Shared<SAMPLE_BINS>) + 15) & ~size_t(15);
-  // CTAs at once: as many as an SM's threads' registers (64 each) and shared memory have room for
-  const uint32_t fit = sizeof(T) == 2 ? (uint32_t)std::min<size_t>(4, 228 * 1024 / (std::max(sizeof(Shared<FEW_BINS>), sizeof(Counts<T>)) + 1024)) : 2u;
-  const uint32_t room = fit * (uint32_t)h->n_sms;
-  // More CTAs for a row while all CTAs run at once and a CTA keeps 16,384 scores (32 bits:
-  // 4,096): adding up bins over a cluster costs more than it gains from there.  us with 1,
-  // 2, 4 and 8 CTAs for a row of bf16: 64 rows of 50,257 27, 23, 25, 32; 512 of 100,257
-  // 70, 78, 119, 192; one of 100,257 27, 25, 23, 21; 150 39, 33, 47, 70.
-  // counts of 16 bits have to hold a CTA's, and the search its slice
-  const uint32_t most = sizeof(T) == 2 && sizeof(typename Places<T>::Count) == 4 ? (256 / 32 - 1) * 8 * 2048 - 8 : 63000u;
-  uint32_t n = 1;
-  while (n < 16 && (a->n_logits / n > most || (a->n_logits / n > (sizeof(T) == 2 ? 16384u : 4096u) && (uint64_t)a->rows * n * 2 <= room))) n *= 2;
-  c.ranks = n;
-  c.per = ((a->n_logits + n - 1) / n + 7) / 8 * 8;
   if constexpr (sizeof(T) == 2) {
-    // (a CTA's count of a score has to fit; 2^20 scores are too many for 16 CTAs)
-    if (sizeof(typename Places<T>::Count) == 4 || c.per <= 63488)
-      return launch_clusters<k_sample_counted<T>>(h->dev, a->rows * n, Places<T>::THREADS, n, std::max(sizeof(Shared<FEW_BINS>), sizeof(Counts<T>)), s, c);
+    // a CTA's counts have to fit their type, and its slice the search for the choice
+    constexpr bool WORDS = Counts<T>::WORDS;
+    constexpr uint32_t most = std::min<uint32_t>(WORDS ? MOST_LOGITS : 63000u, (Places<T>::THREADS / 32 - 1) * Places<T>::ROUNDS * 2048 - 8);
+    const size_t room = std::max(sizeof(Shared<FEW_BINS>), sizeof(Counts<T>));
+    split(h, (uint32_t)std::min<size_t>(1024 / Places<T>::THREADS, 228 * 1024 / (room + 1024)), most, 16384, c);
+    // (2^20 f16 scores are too many for 16 CTAs)
+    if (WORDS || c.per <= most + 8)
+      return launch_clusters<k_sample_counted<T>>(h->dev, a->rows * c.ranks, Places<T>::THREADS, c.ranks, room, s, c);
   }
-  if constexpr (sizeof(typename Places<T>::Count) != 4) {
-    const size_t slice = (size_t)c.per * sizeof(T) + 16;
+  if constexpr (!std::is_same_v<T, __nv_bfloat16>) {
+    split(h, 2, 65536, 4096, c);
+    const size_t base = (sizeof(Shared<SAMPLE_BINS>) + 15) & ~size_t(15), slice = (size_t)c.per * sizeof(T) + 16;
     c.resident = base + slice <= 112 * 1024;   // (two CTAs per SM: 256 rows of 100,257 scores 226 us, with one that keeps them 330)
-    return launch_clusters<k_sample<T>>(h->dev, a->rows * n, SAMPLE_THREADS, n, base + (c.resident ? slice : 0), s, c);
+    return launch_clusters<k_sample<T>>(h->dev, a->rows * c.ranks, SAMPLE_THREADS, c.ranks, base + (c.resident ? slice : 0), s, c);
   }
   return cudaErrorInvalidValue;   // (not reached)
 }
