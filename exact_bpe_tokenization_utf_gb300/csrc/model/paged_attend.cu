@@ -21,7 +21,7 @@
 // groups of eight fill it; S^T = K Q^T and O^T = V^T P^T both read the cache's rows
 // as they lie (ldmatrix, transposed for the values), and P^T comes from S^T by
 // movmatrix.  The matrix work is a small part of the time that the bytes take: at
-// group 8 and width 128, 24 instructions of 2,048 multiply-adds for 8 KB.
+// group 8 and width 128, 32 instructions (bf16; f16: 24) of 2,048 multiply-adds for 8 KB.
 //
 // Measured on a GB300 (6.7 TB/s of plain copying): 256 requests of up to 4,801 tokens, 8
 // key heads of 128, group 8, in 390 us (6.5 TB/s); 64 requests of 0 to 16,381 tokens in 81
@@ -101,8 +101,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The products of a type, and a weight as PARTS numbers of the type that add up to it:
+// three of bf16 hold its 24 bits, two of f16 22 of them.
 template <class T> struct Mma;
 template <> struct Mma<__nv_bfloat16> {
+  static constexpr int PARTS = 3;
   static __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -112,11 +115,18 @@ template <> struct Mma<__nv_bfloat16> {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
-  static __device__ __forceinline__ float2 unpack(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  // two weights' parts, x's in the lower halves; each is the rest's upper half
+  static __device__ __forceinline__ void split(float x, float y, uint32_t* part) {
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      part[p] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+      x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+      y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+    }
   }
 };
 template <> struct Mma<__half> {
+  static constexpr int PARTS = 2;
   static __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -126,7 +136,11 @@ template <> struct Mma<__half> {
     const __half2 h = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
-  static __device__ __forceinline__ float2 unpack(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+  static __device__ __forceinline__ void split(float x, float y, uint32_t* part) {
+    part[0] = pack(x, y);
+    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&part[0]));
+    part[1] = pack(x - back.x, y - back.y);
+  }
 };
 
 __device__ __forceinline__ void ldmatrix(uint32_t* r, uint32_t at) {
@@ -362,9 +376,10 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
             }
           }
       }
-      // weights, as two 16-bit numbers each: with one alone they would be off by half
-      // a step of the type, as much as the rounding of out
-      uint32_t hi[NT][2], lo[NT][2];
+      // weights, in parts: with one alone they would be off by half a step of the type, as
+      // much as the rounding of out
+      constexpr int PARTS = Mma<T>::PARTS;
+      uint32_t w[NT][PARTS][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -372,10 +387,10 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
           const float x = ex2(s[nt][2 * e] - ref[nt][0]), y = ex2(s[nt][2 * e + 1] - ref[nt][1]);
           sum[nt][0] += x;
           sum[nt][1] += y;
-          const uint32_t h = Mma<T>::pack(x, y);
-          const float2 back = Mma<T>::unpack(h);
-          hi[nt][e] = transposed(h);
-          lo[nt][e] = transposed(Mma<T>::pack(x - back.x, y - back.y));
+          uint32_t part[PARTS];
+          Mma<T>::split(x, y, part);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) w[nt][p][e] = transposed(part[p]);
         }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -384,8 +399,8 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
         ldmatrix_trans(a, vs + row * S::ROW + (chunk ^ (row & 7u)) * 16);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          Mma<T>::mma(o[nt][i], a, hi[nt][0], hi[nt][1]);
-          Mma<T>::mma(o[nt][i], a, lo[nt][0], lo[nt][1]);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) Mma<T>::mma(o[nt][i], a, w[nt][p][0], w[nt][p][1]);
         }
       }
     }

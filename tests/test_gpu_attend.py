@@ -404,3 +404,52 @@ def test_refusals(env):
     assert bool((a.out == 7).all())
     assert tok.attend_work_bytes(1, 7, 2, 64) == 0 and tok.attend_work_bytes(1, 8, 2, 60) == 0
     assert tok.attend_work_bytes(4, 8, 2, 64) <= tok.attend_work_bytes(5, 8, 2, 64)
+
+
+def _in_a_row(env, cache, lens, group=1, **other):
+    """An _Attend whose requests have the cache's blocks one after another."""
+    a = _Attend(env, lens, group, cache, spare=0, **other)
+    a.table.fill_(-1)
+    at = 0
+    for r, m in enumerate(lens):
+        need = -(-m // cache.bs)
+        a.table[r, :need] = env[0].arange(at, at + need, dtype=env[0].int32, device="cuda")
+        at += need
+    assert at <= cache.n_blocks
+    return a
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_weights_keep_their_bits(env, kind):
+    # Values that the weights make cancel: what is left of out is far below its terms, so that a weight's error
+    # shows.  A token of score 0 and value 0, then four of scores in -1 .. 0, each of whose values takes away
+    # what the ones before leave.
+    torch = env[0]
+    n, heads, dim = 40, 8, 64
+    c = _Cache(env, kind, n, 5, heads, dim)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    s = -torch.randint(1, 128, (n, 5, heads), generator=g, device="cuda").double() / 128
+    s[:, 0] = 0
+    c.k.zero_()
+    c.k[..., 0] = s
+    w = s.exp()[..., None]
+    v = torch.zeros(n, 5, heads, dim, dtype=torch.float64, device="cuda")
+    v[:, 1] = 1 + torch.rand(n, heads, dim, generator=g, device="cuda").to(c.dtype).double()
+    v[:, 1] = v[:, 1].to(c.dtype).double()
+    for t in range(2, 5):
+        v[:, t] = (-(w * v).sum(1) / w[:, t]).to(c.dtype).double()
+    c.v.copy_(v)
+    a = _in_a_row(env, c, [5] * n, scale=1.0)
+    a.q.zero_()
+    a.q[..., 0] = 1
+    a.run()
+    out, lse, size = a.want()
+    # A score is exact; its product with log2(e) and the reference's are off by 2 roundings of at most 1.45 each,
+    # their difference by one more: 2^-21.2 in all, times ln 2.  The exponential: 2^-22.  A weight's parts: 2^-22.
+    # Sums of 5 tokens' products in 2 or 3 parts: a product of matrices adds each part to within 2^-22 of its
+    # terms, 2^-20.4.  The sum of weights and the quotient: 2^-22 of out, which is small.
+    half = torch.finfo(c.dtype).eps / 2
+    tol = size * 2.0**-19 + out.abs() * half * (1 + 2.0**-8) + 2.0**-25
+    assert float(out.abs().max()) < float(size.min()) * 2.0**-15
+    assert bool(((a.out[:n].double() - out).abs() <= tol).all()), float(((a.out[:n].double() - out).abs() / size).max()) * 2.0**19
+    assert bool(((a.lse[:n].double() - lse).abs() <= 2.0**-19).all())
