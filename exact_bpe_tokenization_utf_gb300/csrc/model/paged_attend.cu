@@ -42,8 +42,8 @@ constexpr int STEP = 16;                // tokens of a warp's step
 constexpr int TILE = STEP * WARPS;      // tokens of a CTA's step, the unit that pieces are cut at
 constexpr uint32_t START = 2;           // what the start of a request and head counts, in tiles
 constexpr uint32_t MOST_REQUESTS = 1u << 20, MOST_GROUP = 64;
-// A weight's exponent is relative to a reference that is replaced once a score lies
-// more than this above it (in powers of 2): weights stay below 2^8.
+// A weight's exponent is relative to a reference, BIAS below the largest score when it was
+// taken, that is replaced once a score lies more than this above that one (in powers of 2).
 constexpr float SLACK = 8.f;
 
 // Kernels are made for widths of 64, 128 and 256; others take the next one's, with zeros
@@ -101,11 +101,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The products of a type, and a weight as PARTS numbers of the type that add up to it:
-// three of bf16 hold its 24 bits, two of f16 22 of them.
+// The products of a type, and a weight as PARTS numbers of the type: three of bf16 add up
+// to its 24 bits.  f16 holds no number below 2^-24: weights are taken 2^BIAS times, so that
+// the largest one lies near the type's upper end, and what rounding to f16 left 2^11 times
+// in sums of its own.  Together they are off by at most 2^-23 of the weight or 2^-43 of the
+// largest one.  (As two f16 numbers in one sum, without either, weights were off by 2^-25 of
+// the largest one: a token that took nearly the whole weight hid all others.)
 template <class T> struct Mma;
 template <> struct Mma<__nv_bfloat16> {
   static constexpr int PARTS = 3;
+  static constexpr float BIAS = 0.f;
   static __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -124,9 +129,15 @@ template <> struct Mma<__nv_bfloat16> {
       y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
     }
   }
+  // c += a times the weights whose parts are w[.][0] and w[.][1]
+  static __device__ __forceinline__ void add(float* c, const uint32_t* a, const uint32_t (*w)[2]) {
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) mma(c, a, w[p][0], w[p][1]);
+  }
 };
 template <> struct Mma<__half> {
   static constexpr int PARTS = 2;
+  static constexpr float BIAS = 7.f;   // (with SLACK weights are at most 2^15)
   static __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -139,7 +150,14 @@ template <> struct Mma<__half> {
   static __device__ __forceinline__ void split(float x, float y, uint32_t* part) {
     part[0] = pack(x, y);
     const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&part[0]));
-    part[1] = pack(x - back.x, y - back.y);
+    part[1] = pack((x - back.x) * 2048.f, (y - back.y) * 2048.f);
+  }
+  static __device__ __forceinline__ void add(float* c, const uint32_t* a, const uint32_t (*w)[2]) {
+    float rest[4] = {0.f, 0.f, 0.f, 0.f};
+    mma(c, a, w[0][0], w[0][1]);
+    mma(rest, a, w[1][0], w[1][1]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = fmaf(rest[e], 1.f / 2048.f, c[e]);
   }
 };
 
@@ -353,10 +371,10 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[nt][e] = (e < 2 ? has0 : has8) ? s[nt][e] * c.scale_log2 : -INFINITY;
-          above |= s[nt][e] > ref[nt][e & 1] + SLACK;
+          above |= s[nt][e] - ref[nt][e & 1] > SLACK + Mma<T>::BIAS;
         }
       if (__any_sync(ALL, above)) {
-        // a new reference: the largest score so far of each query head (its 8 lanes agree)
+        // a new reference, from the largest score so far of each query head (its 8 lanes agree)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -365,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
             m = fmaxf(m, __shfl_xor_sync(ALL, m, 4));
             m = fmaxf(m, __shfl_xor_sync(ALL, m, 8));
             m = fmaxf(m, __shfl_xor_sync(ALL, m, 16));
-            m = fmaxf(m, ref[nt][e]);
+            m = fmaxf(m - Mma<T>::BIAS, ref[nt][e]);
             const float f = ex2(ref[nt][e] - m);
             ref[nt][e] = m;
             sum[nt][e] *= f;
@@ -398,10 +416,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
         const uint32_t row = (lane & 7u) + (lane >> 4) * 8, chunk = 2 * i + (lane >> 3 & 1u);
         ldmatrix_trans(a, vs + row * S::ROW + (chunk ^ (row & 7u)) * 16);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) Mma<T>::mma(o[nt][i], a, w[nt][p][0], w[nt][p][1]);
-        }
+        for (int nt = 0; nt < NT; ++nt) Mma<T>::add(o[nt][i], a, w[nt]);
       }
     }
 

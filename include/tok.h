@@ -589,8 +589,9 @@ int tok_paged_store(tok_handle* h, const tok_kv_cache* c, const tok_store_args* 
  * Query head j reads key head j / (heads / kv_heads).  With
  *   s(p) = scale * (q[k][j] . key(p))   for max(0, L - window) <= p < L (window 0: all),
  *   out[k][j] = sum of exp(s(p)) value(p) / sum of exp(s(p)),   lse[k][j] = log sum of exp(s(p))
- * Sums and the softmax are in 32 bits, out is rounded once.  The values of bf16
- * are multiplied by weights of 24 bits, those of f16 by two f16 numbers each.  A table
+ * Sums and the softmax are in 32 bits, out is rounded once.  The weights that the
+ * values are multiplied by keep 24 bits for bf16 and 22 for f16 (there, 2^-43 of the
+ * largest one at the least).  A table
  * entry outside 0 .. n_blocks - 1 hides its block's tokens; their memory is not
  * read.  A request without a token to read has out 0 and lse -inf.
  */

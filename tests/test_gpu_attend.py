@@ -453,3 +453,27 @@ def test_weights_keep_their_bits(env, kind):
     assert float(out.abs().max()) < float(size.min()) * 2.0**-15
     assert bool(((a.out[:n].double() - out).abs() <= tol).all()), float(((a.out[:n].double() - out).abs() / size).max()) * 2.0**19
     assert bool(((a.lse[:n].double() - lse).abs() <= 2.0**-19).all())
+
+
+@pytest.mark.parametrize("depth", [9.0, 12.0, 14.0, 16.0, 17.6, 20.0, 26.0])
+@pytest.mark.parametrize("kind", KINDS)
+def test_small_weights_count(env, kind, depth):
+    # A first token that takes nearly the whole weight and whose value is 0: out is what the others' small weights
+    # make of theirs.  So many requests that a CTA has most of a request's tokens beside that one.
+    torch, pkg, tok = env
+    n, m, dim = 330, 4096, 64
+    c = _Cache(env, kind, m // 16, 16, 2, dim, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    c.k.zero_()
+    c.k[..., 0] = (-depth + (torch.rand(m // 16, 16, 2, generator=g, device="cuda") - 0.5) / 2).to(c.dtype)
+    c.v[:, :, 1] = 1   # (one key head's values have no sign to cancel by)
+    c.k[0, 0], c.v[0, 0] = 0, 0
+    a = _in_a_row(env, c, [m], scale=1.0)
+    a.q.zero_()
+    a.q[..., 0] = 1
+    out, lse, size = a.want()
+    many = _Attend(env, [m] * n, 1, c, scale=1.0)
+    many.table[:, :a.table.shape[1]] = a.table
+    many.q.copy_(a.q.expand(n, -1, -1))
+    many.want = lambda: tuple(t.expand(n, *t.shape[1:]) for t in (out, lse, size))
+    many.check()
