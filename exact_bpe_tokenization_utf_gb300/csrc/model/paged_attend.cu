@@ -215,6 +215,46 @@ template <class T, int D> struct Loader {
   }
 };
 
+// a + v f for a part v of an output, however small f is: an infinity or a NaN stays what it is
+__device__ __forceinline__ float plus(float a, float v, float f) { return fabsf(v) < INFINITY ? fmaf(v, f, a) : a + v; }
+
+// Where the values hold an infinity, the products of matrices give a NaN: weights and their
+// rests may be 0, or of both signs.  Every weight is above 0, so what such a column's
+// output is follows from the values alone: the warp passes over those of its tokens (at p,
+// a step's 16 by the lanes) once more and sets that column for all of its query heads.
+template <class T, int D>
+__device__ __forceinline__ void set_infinities(const Loader<T, D>& in, long long p, uint32_t steps, float* out, uint32_t pitch,
+                                               const float* tot, uint32_t heads) {
+  constexpr uint32_t INF = std::is_same_v<T, __half> ? 0x7c00u : 0x7f80u;
+  const uint32_t lane = threadIdx.x & 31u;
+  uint32_t seen = 0;   // of each of the lane's columns, two side by side in every 64: 1 for inf, 2 for -inf, both for a NaN
+  for (uint32_t step = 0; step < steps; ++step, p += TILE) {
+    const long long at = in.place(p);
+    for (int r = 0; r < STEP; ++r) {
+      const long long from = __shfl_sync(ALL, at, r);
+      if (from < 0) continue;
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) {
+        const uint32_t d = k * 64 + lane * 2;
+        if (d >= in.c.head_dim) continue;
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const T*>(in.c.v) + from + d);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t u = e ? w >> 16 : w & 0xffffu;
+          if ((u & INF) == INF) seen |= ((u & 0x7fffu) != INF ? 3u : u >> 15 ? 2u : 1u) << (4 * k + 2 * e);
+        }
+      }
+    }
+  }
+  for (int c = 0; c < D / 32; ++c) {
+    const uint32_t what = seen >> (2 * c) & 3u;
+    if (!what) continue;
+    for (uint32_t j = 0; j < heads; ++j)
+      if (tot[j] == tot[j])   // (a NaN among the scores is a NaN everywhere)
+        out[j * pitch + c / 2 * 64 + lane * 2 + (c & 1)] = what == 3 ? NAN : what == 2 ? -INFINITY : INFINITY;
+  }
+}
+
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c) {
   extern __shared__ __align__(128) uint8_t mem[];
@@ -425,6 +465,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
     __syncwarp();
     constexpr int PITCH = D + 4;
     float* my = reinterpret_cast<float*>(mem + warp * S::WARP_BYTES);
+    float finite = 0.f;   // a NaN once a number is not
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -442,8 +483,14 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
         for (int i = 0; i < D / 16; ++i) {
           my[j * PITCH + i * 16 + g] = o[nt][i][e];
           my[j * PITCH + i * 16 + g + 8] = o[nt][i][e + 2];
+          finite = fmaf(o[nt][i][e], 0.f, finite);
+          finite = fmaf(o[nt][i][e + 2], 0.f, finite);
         }
       }
+    if (__any_sync(ALL, finite != 0.f)) {
+      __syncwarp();
+      set_infinities(in, p0 + warp * STEP + (lane & 15u), tiles_here, my, PITCH, s_tot[warp], heads);
+    }
     __syncthreads();
     const bool whole = tile0 == 0 && tile1 == tiles;
     // a part that the CTA before began is its first; one that the next CTA ends its second
@@ -458,8 +505,8 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
       for (int w = 0; w < WARPS; ++w) {
         const float f = ex2(s_ref[w][j] - m);
         const float2 v = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(mem + w * S::WARP_BYTES) + j * PITCH + d);
-        x = fmaf(v.x, f, x);
-        y = fmaf(v.y, f, y);
+        x = plus(x, v.x, f);
+        y = plus(y, v.y, f);
         tot = fmaf(s_tot[w][j], f, tot);
       }
       if (whole) {
@@ -517,8 +564,8 @@ __global__ void __launch_bounds__(THREADS) k_attend_join(AttendCall c) {
       const size_t at = place(k0 + k);
       const float2 v = *reinterpret_cast<const float2*>(c.outs + at * D + d);
       const float f = s_f[k];
-      x = fmaf(v.x, f, x);
-      y = fmaf(v.y, f, y);
+      x = plus(x, v.x, f);
+      y = plus(y, v.y, f);
       tot = fmaf(c.sums[at * 2 + 1], f, tot);
     }
   }

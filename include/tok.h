@@ -591,7 +591,9 @@ int tok_paged_store(tok_handle* h, const tok_kv_cache* c, const tok_store_args* 
  *   out[k][j] = sum of exp(s(p)) value(p) / sum of exp(s(p)),   lse[k][j] = log sum of exp(s(p))
  * Sums and the softmax are in 32 bits, out is rounded once.  The weights that the
  * values are multiplied by keep 24 bits for bf16 and 22 for f16 (there, 2^-43 of the
- * largest one at the least).  A table
+ * largest one at the least).  A weight counts as above 0 however small it is: an
+ * infinity among the values of the tokens read is out's, a NaN or two infinities
+ * of both signs are a NaN.  A table
  * entry outside 0 .. n_blocks - 1 hides its block's tokens; their memory is not
  * read.  A request without a token to read has out 0 and lse -inf.
  */

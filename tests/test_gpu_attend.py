@@ -477,3 +477,48 @@ def test_small_weights_count(env, kind, depth):
     many.q.copy_(a.q.expand(n, -1, -1))
     many.want = lambda: tuple(t.expand(n, *t.shape[1:]) for t in (out, lse, size))
     many.check()
+
+
+def _put(c, a, r, p, head, d, x):
+    c.v[a.table[r, p // c.bs].long(), p % c.bs, head, d] = x
+
+
+@pytest.mark.parametrize("q_size", [1.0, 40.0])
+@pytest.mark.parametrize("dim,group", [(64, 8), (128, 16), (256, 3), (40, 1)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_infinities_among_the_values(env, kind, dim, group, q_size):
+    # every weight is above 0, however small: an infinity is out's, two of both signs and a NaN make a NaN
+    torch = env[0]
+    inf = float("inf")
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        lens = [1, 1, 2, 40, 17, 333, 0, 20011, 1000]
+        c = _Cache(env, kind, 1500, 16, 2, dim, layout="head" if seed % 2 else "token", seed=seed)
+        a = _in_a_row(env, c, lens, group=group, seed=seed, q_size=q_size)
+        a.window = 700 if seed == 3 else 0
+        out, lse, size = a.want()
+        for r, m in enumerate(lens):
+            for _ in range(12 if m else 0):
+                p, h, d, x = int(rng.integers(m)), int(rng.integers(2)), int(rng.integers(dim)), float(rng.choice([inf, -inf, inf, -inf, np.nan]))
+                _put(c, a, r, p, h, d, x)
+        # (what the queries read, as the caches have it now: later ones replaced some)
+        group_of = a.heads // c.heads
+        special = torch.zeros_like(out)
+        for r, m in enumerate(lens):
+            p = torch.arange(max(0, m - a.window) if a.window else 0, m, device="cuda")
+            v = c.v[a.table[r, p // c.bs].long(), p % c.bs].double()
+            both = torch.where(torch.isfinite(v), 0.0, v).sum(0)          # inf, -inf, NaN or 0 for each key head and column
+            special[r] = both.repeat_interleave(group_of, 0)
+        a.run()
+        got = a.out[:a.n].double()
+        odd = special != 0   # (a NaN too)
+        assert bool(odd.any())
+        assert bool(torch.equal(torch.isnan(got), torch.isnan(special)))
+        assert bool((got[odd] == special[odd])[~torch.isnan(special[odd])].all())
+        assert bool(torch.isfinite(got[~odd]).all())
+        if q_size == 1:
+            # the others as ever
+            off = max(1.0, float(a.q.double().abs().sum(2).max()) * float(c.k.double().abs().max()) * a.scale) * (dim + 4) * 2.0**-24 + 2.0**-13
+            tol = torch.where(odd, 0.0, size * off * 2 + out.abs() * torch.finfo(c.dtype).eps / 2 * (1 + 2.0**-8) + 2.0**-25)
+            assert bool(((torch.where(odd, 0.0, got) - torch.where(odd, 0.0, out)).abs() <= tol).all())
+            assert bool(torch.isfinite(a.lse[:a.n][lse > -inf]).all())
