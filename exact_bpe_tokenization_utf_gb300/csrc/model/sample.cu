@@ -181,6 +181,7 @@ template <int BIN_SHIFT> struct Shared {
   double t_ln_m;                                     // T ln(min_p), for the threshold
   uint32_t listed;
   Command cmd;
+  int brief;                                         // apart from cmd, which the first CTA may set again before all have read it
   uint32_t found;
   unsigned long long answer_mass;
   uint32_t answer_cnt, answer_key;
@@ -457,11 +458,11 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
       Command next{};
       next.by_bin = (int)b;
       next.op = sh.upto[b] <= LIST ? OP_GATHER : OP_BINS;
-      __syncthreads();
-      if (tid < c.ranks) cluster.map_shared_rank(&sh, tid)->cmd = next;
+      if (tid < c.ranks) cluster.map_shared_rank(&sh, tid)->brief = next.op == OP_GATHER;
+      if (tid == 0) sh.cmd = next;
     }
     cluster.sync();
-    brief = sh.cmd.op == OP_GATHER;
+    brief = sh.brief;
     if (!brief)
       for (uint32_t i = tid; i < BINS; i += THREADS) sh.cnt[i] = 0;
     __syncthreads();

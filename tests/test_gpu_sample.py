@@ -204,6 +204,20 @@ def test_rows_that_masks_left(env, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,n", [(1, 100257), (3, 100257), (200, 5003), (6, 20011), (40, 70001)])
+def test_min_p_that_keeps_nothing(env, rows, n, kind):
+    # rows of one CTA and of many; 16-bit rows by counts and, with scores from 2^11 on, the general way
+    x = _scores(rows + n, rows, n)
+    for lift in (0.0, 3000.0):
+        for min_p in (1 + 2.0**-23, 1.5, np.inf):
+            for rules in (dict(), dict(top_k=50), dict(top_p=0.9), dict(temperature=0.0), dict(temperature=40.0, top_k=n // 2)):
+                r = _Rows(env, x + lift, kind, min_p=min_p, **rules)
+                r.check()
+                assert (r.pick[:-1] == -1).all() and (r.kept[:-1] == 0).all() and (r.logprob[:-1] == -np.inf).all()
+    _Rows(env, x, kind, min_p=np.where(np.arange(rows) % 3, 0.01, 1.5)).check()
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_scores_next_to_zero(env, kind):
     x = _scores(3, 6, 5003, spread=1e-9)
     x[1] = _scores(4, 1, 5003)[0]
