@@ -355,10 +355,11 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   };
   // a bin of the same width without the care that weights take: off by one at most (but
   // for the last ones), and it never falls where x falls either
-  const float bin_scale = (float)(65536 >> BIN_SHIFT) * r.c_hi;
+  // (by half the scores: the difference of two at the type's ends is not finite)
+  const float bin_scale = (float)(131072 >> BIN_SHIFT) * r.c_hi, half_max = 0.5f * r.x_max;
   auto rough_bin = [&](float x) {
     if (r.only_max) return x == r.x_max ? 0u : (uint32_t)BINS - 1u;
-    return (uint32_t)min((int)((r.x_max - x) * bin_scale), BINS - 1);
+    return (uint32_t)min((int)(fmaf(x, -0.5f, half_max) * bin_scale), BINS - 1);
   };
   // the row's bins: each CTA adds a share of them, for the first one
   auto add_up = [&](bool sub, bool weights) {

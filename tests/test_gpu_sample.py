@@ -217,6 +217,18 @@ def test_min_p_that_keeps_nothing(env, rows, n, kind):
     _Rows(env, x, kind, min_p=np.where(np.arange(rows) % 3, 0.01, 1.5)).check()
 
 
+@pytest.mark.parametrize("temperature", [1e37, 5e37])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_scores_at_both_ends_of_the_type(env, kind, temperature):
+    # differences that are not finite, at temperatures that give them weight
+    rng = np.random.default_rng(3)
+    x = (rng.random((8, 20011)) * 2 - 1) * 3.3e38
+    x[1] = rng.choice([-3.3e38, 3.3e38], 20011)
+    x[2, 1000:] = -3.3e38
+    for rules in (dict(), dict(top_p=0.9), dict(top_k=5000), dict(top_k=15000, top_p=0.99), dict(min_p=1e-3)):
+        _Rows(env, x, kind, temperature=temperature, **rules).check()
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_scores_next_to_zero(env, kind):
     x = _scores(3, 6, 5003, spread=1e-9)
