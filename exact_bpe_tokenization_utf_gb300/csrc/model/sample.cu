@@ -72,29 +72,40 @@ __device__ const Powers g_powers = make_powers();
 
 // a row's temperature and maximum, for weights
 struct Rule {
-  float c_hi, c_lo;     // log2(e) / T
-  float p_max, e_max;   // the largest score's c x, in two parts
-  float x_max;
+  float shrink;         // scores are taken times it, so that differences are finite and c is not too small:
+                        // 1/2, or 2^-64 for temperatures from 2^64 on
+  float c_hi, c_lo;     // log2(e) / T, for those
+  float top;            // the largest score, so taken
+  float x_max;          // and as it is
   bool only_max;        // no other weight is above 0
 };
 
-__device__ __forceinline__ void times_c(const Rule& r, float x, float& p, float& e) {
-  p = __fmul_rn(x, r.c_hi);   // (not to be joined with the subtraction after it)
-  e = fmaf(x, r.c_hi, -p);
-  e = fmaf(x, r.c_lo, e);
+// all but top and x_max
+__device__ __forceinline__ void set_temperature(Rule& r, float temp) {
+  r.shrink = temp >= 0x1p64f ? 0x1p-64f : 0.5f;
+  r.only_max = temp < 0x1p-100f;
+  const double t = r.only_max ? 1.0 : fmin((double)temp, 3e38), k = 1.4426950408889634074 / (t * r.shrink);
+  r.c_hi = (float)k;
+  r.c_lo = (float)(k - (double)(float)k);
+}
+__device__ __forceinline__ void set_largest(Rule& r, float x) {
+  r.x_max = x;
+  r.top = x * r.shrink;
 }
 
-// log2 w in two parts: hi rounded to 32 bits (it never rises where x falls), and the rest
+// log2 w in two parts: hi rounded to 32 bits, and the rest.  The difference to the largest
+// score comes first, exactly in two parts: the product is off by 2^-46 of log2 w, however
+// far from 0 the scores lie.  hi never rises where x falls (but by its last place, where
+// two scores differ by less than 2^-46 of their difference to the largest).
 __device__ __forceinline__ void log2_weight(const Rule& r, float x, float& hi, float& lo) {
-  float p, e;
-  times_c(r, x, p, e);
-  const float d = p - r.p_max;                       // exact with err
-  const float back = d - p;
-  const float err = (p - (d - back)) + (-r.p_max - back);
-  e = (e - r.e_max) + err;
-  hi = d + e;
-  lo = e - (hi - d);
-  if (r.only_max || !(d > -1e4f)) {
+  const float y = __fmul_rn(x, r.shrink), d = y - r.top, back = d - y;
+  const float err = (y - (d - back)) + (-r.top - back);
+  const float p = __fmul_rn(d, r.c_hi);   // (not to be joined with the sums after it)
+  float e = fmaf(d, r.c_hi, -p);
+  e = fmaf(d, r.c_lo, fmaf(err, r.c_hi, e));
+  hi = p + e;
+  lo = e - (hi - p);
+  if (r.only_max || !(p > -1e4f)) {
     hi = x == r.x_max ? 0.f : -1e4f;
     lo = 0.f;
   }
@@ -311,10 +322,8 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   for (int o = 16; o; o >>= 1) most = max_nan(most, __shfl_xor_sync(ALL, most, o));
   if (lane == 0) sh.scan_c[warp] = __float_as_uint(most);
   if (tid == 32) {
-    const double t = temp >= 0x1p-100f ? fmin((double)temp, 3e38) : 1.0, k = 1.4426950408889634074 / t;
-    sh.rule.c_hi = (float)k;
-    sh.rule.c_lo = (float)(k - (double)(float)k);
-    sh.t_ln_m = min_p > 0.f ? t * log((double)min_p) : 0.0;
+    set_temperature(sh.rule, temp);
+    sh.t_ln_m = min_p > 0.f ? fmin((double)temp, 3e38) * log((double)min_p) : 0.0;
   }
   __syncthreads();
   most = __uint_as_float(sh.scan_c[lane % WARPS]);
@@ -333,10 +342,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
     return;
   }
   Rule r = sh.rule;
-  r.x_max = most;
-  r.p_max = r.e_max = 0.f;
-  times_c(r, most, r.p_max, r.e_max);
-  r.only_max = temp < 0x1p-100f || !(fabsf(r.p_max) < INFINITY);
+  set_largest(r, most);
   const float least = least_of(r, temp, min_p, sh.t_ln_m);
   auto bin_of = [](int k) { return min((uint32_t)-k >> BIN_SHIFT, (uint32_t)BINS - 1u); };
   // what a token of the row is counted as; false: it is not kept
@@ -355,11 +361,10 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   };
   // a bin of the same width without the care that weights take: off by one at most (but
   // for the last ones), and it never falls where x falls either
-  // (by half the scores: the difference of two at the type's ends is not finite)
-  const float bin_scale = (float)(131072 >> BIN_SHIFT) * r.c_hi, half_max = 0.5f * r.x_max;
+  const float bin_scale = (float)(65536 >> BIN_SHIFT) * r.c_hi;
   auto rough_bin = [&](float x) {
     if (r.only_max) return x == r.x_max ? 0u : (uint32_t)BINS - 1u;
-    return (uint32_t)min((int)(fmaf(x, -0.5f, half_max) * bin_scale), BINS - 1);
+    return (uint32_t)min((int)(fmaf(x, -r.shrink, r.top) * bin_scale), BINS - 1);
   };
   // the row's bins: each CTA adds a share of them, for the first one
   auto add_up = [&](bool sub, bool weights) {
@@ -898,10 +903,8 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
     sh.fine[i] = g_powers.b[i];
   }
   if (tid == 32) {
-    const double t = temp >= 0x1p-100f ? fmin((double)temp, 3e38) : 1.0, k = 1.4426950408889634074 / t;
-    sh.rule.c_hi = (float)k;
-    sh.rule.c_lo = (float)(k - (double)(float)k);
-    sh.t_ln_m = min_p > 0.f ? t * log((double)min_p) : 0.0;
+    set_temperature(sh.rule, temp);
+    sh.t_ln_m = min_p > 0.f ? fmin((double)temp, 3e38) * log((double)min_p) : 0.0;
   }
   if (tid == 0) {
     sh.best = ALL;
@@ -1032,9 +1035,7 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
     return true;
   }
   Rule r = sh.rule;
-  r.x_max = C::score(best);
-  times_c(r, r.x_max, r.p_max, r.e_max);
-  r.only_max = temp < 0x1p-100f || !(fabsf(r.p_max) < INFINITY);
+  set_largest(r, C::score(best));
   const float least = least_of(r, temp, min_p, sh.t_ln_m);
   const int top_k = c.a.d_top_k ? c.a.d_top_k[row] : 0;
   if (far) {

@@ -217,7 +217,7 @@ def test_min_p_that_keeps_nothing(env, rows, n, kind):
     _Rows(env, x, kind, min_p=np.where(np.arange(rows) % 3, 0.01, 1.5)).check()
 
 
-@pytest.mark.parametrize("temperature", [1e37, 5e37])
+@pytest.mark.parametrize("temperature", [1e37, 5e37, 3e38])
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_scores_at_both_ends_of_the_type(env, kind, temperature):
     # differences that are not finite, at temperatures that give them weight
@@ -227,6 +227,40 @@ def test_scores_at_both_ends_of_the_type(env, kind, temperature):
     x[2, 1000:] = -3.3e38
     for rules in (dict(), dict(top_p=0.9), dict(top_k=5000), dict(top_k=15000, top_p=0.99), dict(min_p=1e-3)):
         _Rows(env, x, kind, temperature=temperature, **rules).check()
+
+
+def _borders(kind, most, temperature, seed, steps):
+    """Rows of two scores near `most` and a temperature and top-p for each, such that top_p times both weights lies
+    between 2^-35.9 and 2^-32 of the first weight's: what is kept is 1 where it lies below it, else 2."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 40
+    rng = np.random.default_rng(seed)
+    place = np.spacing({"f32": np.float32, "f16": np.float16}[kind](abs(most) * 0.999))
+    rows = []
+    while len(rows) < 60:
+        t = np.float32(temperature * (0.7 + 0.6 * rng.random()))
+        m = float(np.floor(most / place) * place)
+        d = float(rng.integers(1, steps)) * float(place)
+        w = (Decimal(-d) / Decimal(float(t))).exp()
+        p = np.float32(1 / (1 + w))
+        off = abs(Decimal(float(p)) * (1 + w) - 1)
+        if Decimal(2) ** Decimal("-35.9") < off < Decimal(2) ** -32 and p < 1:
+            rows.append((m, m - d, t, p, 1 if Decimal(float(p)) * (1 + w) < 1 else 2))
+    return rows
+
+
+@pytest.mark.parametrize("kind,most,temperature,steps", [("f32", 1.5e7, 1.0, 20), ("f32", 1e6, 1.0, 200), ("f32", 1e5, 1.0, 300), ("f32", 1000.0, 0.1, 1500),
+                                                         ("f32", 30.0, 1e-3, 1000), ("f32", -7e4, 2.0, 500), ("f32", 3e30, 1e25, 60),
+                                                         ("f16", 50.0, 0.02, 6), ("f16", 2000.0, 0.9, 5)])
+def test_borders_far_from_zero(env, kind, most, temperature, steps):
+    # weights are good to 2^-36 of their size, wherever the scores lie: borders farther away are met
+    rows = _borders(kind, most, temperature, 1, steps)
+    x = np.array([r[:2] for r in rows])
+    r = _Rows(env, x, kind, temperature=[r[2] for r in rows], top_p=[r[3] for r in rows], random=0.0)
+    r.run()
+    assert (r.x.double().cpu().numpy() == x).all()
+    assert (r.pick[:-1] == 0).all()
+    assert r.kept[:-1].tolist() == [r[4] for r in rows]
 
 
 @pytest.mark.parametrize("kind", KINDS)
