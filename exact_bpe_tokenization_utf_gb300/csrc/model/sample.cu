@@ -84,7 +84,7 @@ struct Rule {
 __device__ __forceinline__ void set_temperature(Rule& r, float temp) {
   r.shrink = temp >= 0x1p64f ? 0x1p-64f : 0.5f;
   r.only_max = temp < 0x1p-100f;
-  const double t = r.only_max ? 1.0 : fmin((double)temp, 3e38), k = 1.4426950408889634074 / (t * r.shrink);
+  const double k = 1.4426950408889634074 / (r.only_max ? 1.0 : (double)temp * r.shrink);   // (0 for an infinite one: all weights are 1)
   r.c_hi = (float)k;
   r.c_lo = (float)(k - (double)(float)k);
 }
@@ -139,6 +139,9 @@ __device__ __forceinline__ uint32_t key_of(float x) {   // whole numbers of the 
 }
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
+__device__ __forceinline__ double t_ln(float temp, float min_p) {
+  return !(min_p > 0.f) ? 0.0 : temp < INFINITY ? (double)temp * log((double)min_p) : -INFINITY;
+}
 // scores below this are not kept: M + T ln(min_p) (T = 0: M)
 __device__ __forceinline__ float least_of(const Rule& r, float temp, float min_p, double t_ln_m) {
   if (!(min_p > 0.f)) return -INFINITY;
@@ -323,7 +326,7 @@ __device__ __forceinline__ void choose(const SampleCall& c, uint8_t* mem) {
   if (lane == 0) sh.scan_c[warp] = __float_as_uint(most);
   if (tid == 32) {
     set_temperature(sh.rule, temp);
-    sh.t_ln_m = min_p > 0.f ? fmin((double)temp, 3e38) * log((double)min_p) : 0.0;
+    sh.t_ln_m = t_ln(temp, min_p);
   }
   __syncthreads();
   most = __uint_as_float(sh.scan_c[lane % WARPS]);
@@ -904,7 +907,7 @@ __device__ __forceinline__ bool choose_counted(const SampleCall& c, uint8_t* mem
   }
   if (tid == 32) {
     set_temperature(sh.rule, temp);
-    sh.t_ln_m = min_p > 0.f ? fmin((double)temp, 3e38) * log((double)min_p) : 0.0;
+    sh.t_ln_m = t_ln(temp, min_p);
   }
   if (tid == 0) {
     sh.best = ALL;

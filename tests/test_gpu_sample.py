@@ -263,6 +263,17 @@ def test_borders_far_from_zero(env, kind, most, temperature, steps):
     assert r.kept[:-1].tolist() == [r[4] for r in rows]
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_an_infinite_temperature_at_both_ends_of_the_type(env, kind):
+    # every weight is 1, whatever the differences
+    rng = np.random.default_rng(4)
+    x = (rng.random((6, 20011)) * 2 - 1) * 3.3e38
+    x[1, 1000:] = -3.3e38
+    x[2, 5:] = -np.inf
+    for rules in (dict(), dict(top_p=0.9), dict(top_k=700), dict(top_k=15000, top_p=0.5), dict(min_p=1.0), dict(min_p=0.5, top_p=0.3)):
+        _Rows(env, x, kind, temperature=np.inf, **rules).check()
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_scores_next_to_zero(env, kind):
     x = _scores(3, 6, 5003, spread=1e-9)
