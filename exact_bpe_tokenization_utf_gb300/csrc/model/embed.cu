@@ -407,14 +407,7 @@ __device__ __forceinline__ void write_row(const SumCall& c, uint32_t v, uint32_t
     Eight<TW> y;
     if (add) {
       Eight<TW> old;
-#pragma unroll
-      for (int i = 0; i < Eight<TW>::WORDS / 4; ++i) {
-        const uint4 q = reinterpret_cast<const uint4*>(to + col)[i];
-        old.w[4 * i] = q.x;
-        old.w[4 * i + 1] = q.y;
-        old.w[4 * i + 2] = q.z;
-        old.w[4 * i + 3] = q.w;
-      }
+      old.load(to + col);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         y.put_pair(i, fmaf(s[2 * i], c.scale, old.get(2 * i)), fmaf(s[2 * i + 1], c.scale, old.get(2 * i + 1)));

@@ -25,10 +25,10 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 template <class T> struct Eight {
   static constexpr int WORDS = sizeof(T) * 2;
   uint32_t w[WORDS];
-  __device__ __forceinline__ void load(const T* p) {
+  __device__ __forceinline__ void load(const T* p) {   // what the kernel writes, too
 #pragma unroll
     for (int i = 0; i < WORDS / 4; ++i) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      const uint4 q = reinterpret_cast<const uint4*>(p)[i];
       w[4 * i] = q.x;
       w[4 * i + 1] = q.y;
       w[4 * i + 2] = q.z;
