@@ -601,7 +601,7 @@ typedef struct {
   const void* d_q;        /* request k, head j: from k * q_stride + j * q_head_stride on, in the cache's type */
   int64_t q_stride;
   int64_t q_head_stride;
-  void* d_out;            /* the same with its strides; must not overlap the cache */
+  void* d_out;            /* the same with its strides; may be d_q itself, must not overlap it or the cache otherwise */
   int64_t out_stride;
   int64_t out_head_stride;
   float* d_lse;           /* n rows of heads, back to back; NULL: not wanted */

@@ -522,3 +522,40 @@ def test_infinities_among_the_values(env, kind, dim, group, q_size):
             tol = torch.where(odd, 0.0, size * off * 2 + out.abs() * torch.finfo(c.dtype).eps / 2 * (1 + 2.0**-8) + 2.0**-25)
             assert bool(((torch.where(odd, 0.0, got) - torch.where(odd, 0.0, out)).abs() <= tol).all())
             assert bool(torch.isfinite(a.lse[:a.n][lse > -inf]).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim,kv,group", [(64, 2, 4), (128, 2, 8), (80, 3, 5), (256, 1, 12), (64, 1, 20)])
+def test_queries_and_outputs_with_strides(env, kind, dim, kv, group):
+    # queries as slices of the rows of one product for queries, keys and values; outputs in wider rows, head by
+    # head, and over the queries themselves
+    torch = env[0]
+    lens = [100, 1, 0, 5000, 64, 333]
+    n, heads = len(lens), kv * group
+    c = _Cache(env, kind, 400, 16, kv, dim)
+    a = _Attend(env, lens, group, c)
+    a.check()
+    want, want_lse = a.out.clone(), a.lse.clone()
+    wide = torch.full((n, heads + 2 * kv, dim + 8), float("nan"), dtype=c.dtype, device="cuda")
+    wide[:, :heads, :dim] = a.q
+    q = dict(d_q=wide.data_ptr(), q_stride=wide.stride(0), q_head_stride=wide.stride(1))
+
+    def store(*size):
+        return torch.full(size, 9.0, dtype=c.dtype, device="cuda")
+
+    rows = store(n + 1, heads + 3, dim + 16)
+    a.run(**q, d_out=rows[:, 1:].data_ptr(), out_stride=rows.stride(0), out_head_stride=rows.stride(1))
+    assert torch.equal(rows[:n, 1:heads + 1, :dim], want[:n])
+    rows[:n, 1:heads + 1, :dim] = 9
+    assert bool((rows == 9).all())
+    by_head = store(heads, n + 1, dim)
+    a.lse.fill_(7)
+    a.run(**q, d_out=by_head.data_ptr(), out_stride=by_head.stride(1), out_head_stride=by_head.stride(0))
+    assert torch.equal(by_head[:, :n].transpose(0, 1), want[:n]) and bool((by_head[:, n] == 9).all())
+    assert torch.equal(a.lse, want_lse)
+    backwards = store(n, heads, dim)   # (strides below 0 are strides, too)
+    a.run(**q, d_out=backwards[n - 1].data_ptr(), out_stride=-backwards.stride(0), out_head_stride=dim)
+    assert torch.equal(backwards.flip(0), want[:n])
+    over = a.q.clone()
+    a.run(d_q=over.data_ptr(), d_out=over.data_ptr())
+    assert torch.equal(over, want[:n])
