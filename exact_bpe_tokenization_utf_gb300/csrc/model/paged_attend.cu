@@ -42,8 +42,8 @@ constexpr int STEP = 16;                // tokens of a warp's step
 constexpr int TILE = STEP * WARPS;      // tokens of a CTA's step, the unit that pieces are cut at
 constexpr uint32_t START = 2;           // what the start of a request and head counts, in tiles
 constexpr uint32_t MOST_REQUESTS = 1u << 20, MOST_GROUP = 64;
-// A weight's exponent is relative to a reference, BIAS below the largest score when it was
-// taken, that is replaced once a score lies more than this above that one (in powers of 2).
+// A weight's exponent is relative to a reference that is replaced once a score lies
+// more than this above it (in powers of 2): weights stay below 2^8.
 constexpr float SLACK = 8.f;
 
 // Kernels are made for widths of 64, 128 and 256; others take the next one's, with zeros
@@ -102,15 +102,17 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // The products of a type, and a weight as PARTS numbers of the type: three of bf16 add up
-// to its 24 bits.  f16 holds no number below 2^-24: weights are taken 2^BIAS times, so that
-// the largest one lies near the type's upper end, and what rounding to f16 left 2^11 times
-// in sums of its own.  Together they are off by at most 2^-23 of the weight or 2^-43 of the
-// largest one.  (As two f16 numbers in one sum, without either, weights were off by 2^-25 of
-// the largest one: a token that took nearly the whole weight hid all others.)
+// to its 24 bits.  Weights are taken UNIT times.  bf16 holds values near the 32-bit numbers'
+// end: with weights of 2^-32 at most, sums over 2^31 tokens stay finite.  f16 holds no
+// number below 2^-24: there the largest weight lies near the type's upper end, and what
+// rounding to f16 left is taken 2^11 times, in sums of its own.  Together they are off by at
+// most 2^-23 of the weight or 2^-43 of the largest one.  (As two f16 numbers in one sum,
+// without either, weights were off by 2^-25 of the largest one: a token that took nearly the
+// whole weight hid all others.)
 template <class T> struct Mma;
 template <> struct Mma<__nv_bfloat16> {
   static constexpr int PARTS = 3;
-  static constexpr float BIAS = 0.f;
+  static constexpr float UNIT = 0x1p-40f;   // (SLACK: 2^-32 at most)
   static __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -137,7 +139,7 @@ template <> struct Mma<__nv_bfloat16> {
 };
 template <> struct Mma<__half> {
   static constexpr int PARTS = 2;
-  static constexpr float BIAS = 7.f;   // (with SLACK weights are at most 2^15)
+  static constexpr float UNIT = 0x1p7f;     // (2^15 at most)
   static __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -411,10 +413,10 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[nt][e] = (e < 2 ? has0 : has8) ? s[nt][e] * c.scale_log2 : -INFINITY;
-          above |= s[nt][e] - ref[nt][e & 1] > SLACK + Mma<T>::BIAS;
+          above |= s[nt][e] - ref[nt][e & 1] > SLACK;
         }
       if (__any_sync(ALL, above)) {
-        // a new reference, from the largest score so far of each query head (its 8 lanes agree)
+        // a new reference: the largest score so far of each query head (its 8 lanes agree)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
             m = fmaxf(m, __shfl_xor_sync(ALL, m, 4));
             m = fmaxf(m, __shfl_xor_sync(ALL, m, 8));
             m = fmaxf(m, __shfl_xor_sync(ALL, m, 16));
-            m = fmaxf(m - Mma<T>::BIAS, ref[nt][e]);
+            m = fmaxf(m, ref[nt][e]);
             const float f = ex2(ref[nt][e] - m);
             ref[nt][e] = m;
             sum[nt][e] *= f;
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float x = ex2(s[nt][2 * e] - ref[nt][0]), y = ex2(s[nt][2 * e + 1] - ref[nt][1]);
+          const float x = ex2(s[nt][2 * e] - ref[nt][0]) * Mma<T>::UNIT, y = ex2(s[nt][2 * e + 1] - ref[nt][1]) * Mma<T>::UNIT;
           sum[nt][0] += x;
           sum[nt][1] += y;
           uint32_t part[PARTS];
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D>::CTAS) k_attend(AttendCall c
           T* to = static_cast<T*>(c.out) + (long long)r_now * c.out_stride + (long long)(j0 + j) * c.out_head_stride + d;
           *reinterpret_cast<uint32_t*>(to) = Mma<T>::pack(x * inv, y * inv);
         }
-        if (d == 0 && c.lse) c.lse[(size_t)r_now * c.heads + j0 + j] = tot == 0.f ? -INFINITY : (m + log2f(tot)) * LN2;
+        if (d == 0 && c.lse) c.lse[(size_t)r_now * c.heads + j0 + j] = tot == 0.f ? -INFINITY : (m + log2f(tot * (1.f / Mma<T>::UNIT))) * LN2;
       } else {
         *reinterpret_cast<float2*>(c.outs + (part_at * 16 + j) * D + d) = make_float2(x, y);
         if (d == 0) *reinterpret_cast<float2*>(c.sums + (part_at * 16 + j) * 2) = make_float2(m, tot);
@@ -584,7 +586,7 @@ __global__ void __launch_bounds__(THREADS) k_attend_join(AttendCall c) {
     T* to = static_cast<T*>(c.out) + (long long)r * c.out_stride + (long long)(j0 + j) * c.out_head_stride + d;
     *reinterpret_cast<uint32_t*>(to) = Mma<T>::pack(x * inv, y * inv);
   }
-  if (d == 0 && c.lse) c.lse[(size_t)r * c.heads + j0 + j] = tot == 0.f ? -INFINITY : (m + log2f(tot)) * LN2;
+  if (d == 0 && c.lse) c.lse[(size_t)r * c.heads + j0 + j] = tot == 0.f ? -INFINITY : (m + log2f(tot * (1.f / Mma<T>::UNIT))) * LN2;
 }
 
 struct StoreCall {

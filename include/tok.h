@@ -585,7 +585,7 @@ int tok_paged_store(tok_handle* h, const tok_kv_cache* c, const tok_store_args* 
 /* tok_paged_attend -- the attention of one new token of each request over the
  * request's tokens in the cache.  Request k has L = seq_len[k] of them (the new
  * one among them, as tok_paged_assign's d_seq_len counts; below 0: 0, beyond
- * the table's row: what the row holds), token p in block table[k][p / block_size].
+ * the table's row: what the row holds, 2^31 - 1 at most), token p in block table[k][p / block_size].
  * Query head j reads key head j / (heads / kv_heads).  With
  *   s(p) = scale * (q[k][j] . key(p))   for max(0, L - window) <= p < L (window 0: all),
  *   out[k][j] = sum of exp(s(p)) value(p) / sum of exp(s(p)),   lse[k][j] = log sum of exp(s(p))

@@ -559,3 +559,26 @@ def test_queries_and_outputs_with_strides(env, kind, dim, kv, group):
     over = a.q.clone()
     a.run(d_q=over.data_ptr(), d_out=over.data_ptr())
     assert torch.equal(over, want[:n])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_values_at_the_types_end(env, kind):
+    # a mean of finite values is finite, and not above them
+    torch = env[0]
+    for dim, group in ((64, 8), (128, 12), (256, 2)):
+        c = _Cache(env, kind, 1400, 16, 2, dim, seed=dim)
+        most = torch.finfo(c.dtype).max
+        c.v[:, :, 0] = most
+        c.v[:, :, 1] = torch.where(c.v[:, :, 1] < 0, -most, most)
+        lens = [1, 2, 40, 333, 20011]
+        for q_size in (1.0, 20.0):
+            a = _in_a_row(env, c, lens, group=group, seed=dim, q_size=q_size)
+            a.run()
+            got, half = a.out[:len(lens)].double(), torch.finfo(c.dtype).eps / 2
+            assert bool(torch.isfinite(got).all())
+            assert bool((got[:, :group] == most).all())
+            if q_size == 1:
+                out, lse, size = a.want()
+                off = max(1.0, float(a.q.double().abs().sum(2).max()) * float(c.k.double().abs().max()) * a.scale) * (dim + 4) * 2.0**-24 + 2.0**-13
+                assert bool(((got - out).abs() <= size * off * 2 + out.abs() * half * (1 + 2.0**-8)).all())
+                assert bool(((a.lse[:len(lens)].double() - lse).abs() <= off + lse.abs() * 2.0**-22).all())
