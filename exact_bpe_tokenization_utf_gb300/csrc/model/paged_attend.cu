@@ -21,11 +21,12 @@
 // groups of eight fill it; S^T = K Q^T and O^T = V^T P^T both read the cache's rows
 // as they lie (ldmatrix, transposed for the values), and P^T comes from S^T by
 // movmatrix.  The matrix work is a small part of the time that the bytes take: at
-// group 8 and width 128, 32 instructions (bf16; f16: 24) of 2,048 multiply-adds for 8 KB.
+// group 8 and width 128, 32 instructions (bf16; f16: 24, and 32 sums) of 2,048
+// multiply-adds for 8 KB.
 //
 // Measured on a GB300 (6.7 TB/s of plain copying): 256 requests of up to 4,801 tokens, 8
-// key heads of 128, group 8, in 390 us (6.5 TB/s); 64 requests of 0 to 16,381 tokens in 81
-// us (5.5); one of 32,749 in 36 us (3.7): of these 2 are the way to the first copies, 24
+// key heads of 128, group 8, in 397 us (6.4 TB/s); 64 requests of 0 to 16,381 tokens in 82
+// us (5.4); one of 32,749 in 35 us (3.8): of these 2 are the way to the first copies, 24
 // the bytes, 4 the warps' and CTAs' joins, the rest the second kernel, which the first lets
 // start early.  Without the starts' share in the pieces the 64 requests took 133 us.
 #include "types.cuh"
@@ -603,8 +604,9 @@ struct StoreCall {
 };
 
 // A copy of 2 * row units a head and token; a thread takes one of the keys and one of
-// the values.  Bound by the bytes: 16,381 tokens of 8 heads of 128 in 19 us (7.1 TB/s, the
-// writes in part still in L2).
+// the values.  Bound by the bytes: 16,381 tokens of 8 heads of 128 in 24.6 us (5.5 TB/s; 18.5
+// where one call is repeated, whose bytes stay in L2 in part).  64 tokens: a launch, 1.7 us
+// in a graph, 6.3 a call through the binding.
 __global__ void __launch_bounds__(256) k_store(StoreCall c) {
   const uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const uint32_t per = c.kv_heads * c.row;

@@ -1327,7 +1327,13 @@ __global__ void __launch_bounds__(Places<T>::THREADS, 1024 / Places<T>::THREADS)
 // More CTAs for a row while all of them run at once (fit: on an SM) and each keeps `few`
 // scores: adding up bins over a cluster costs more than it gains from there.  us with 1,
 // 2, 4 and 8 CTAs for a row of bf16 (16,384 scores): 64 rows of 50,257 27, 23, 25, 32; 512
-// of 100,257 70, 78, 119, 192; one of 100,257 27, 25, 23, 21; 150 39, 33, 47, 70.
+// of 100,257 70, 78, 119, 192; one of 100,257 27, 25, 23, 21; 150 39, 33, 47, 70.  Of f16 (16,384): one
+// row of 50,257 33, 35, 36, 35; 64 33, 37, 74, 155; 150 35, 72, 157, 317; of 100,257 from 2 on
+// (counts of 16 bits take 63,000 scores) one 37, 38, 36; 512 253, 510, 1,091.  Of f32 (4,096), with
+// 16 CTAs last: one row of 100,257 with top-p 108, 65, 43, 33, 31; 16 147, 93, 62, 48, 70; 64 166, 103,
+// 78, 95, 190; 150 163, 125, 144, 197; 512 388, 358, 416, 615 (`most` is 65,536: at least 2 there,
+// where 300 rows take 227, 233); of 50,257 300 124, 146, 179; of 8,192 one 23, 21, 19, 21; 64 39, 36, 37,
+// 60; 300 47, 61, 99.
 void split(const tok_handle* h, uint32_t fit, uint32_t most, uint32_t few, SampleCall& c) {
   const uint32_t V = c.a.n_logits;
   uint32_t n = 1;

@@ -520,8 +520,10 @@ uint64_t tok_embed_work_bytes(uint64_t n, uint32_t n_rows, uint32_t dim);
  * first token at which the running sum of w exceeds random[b] times the whole
  * sum (random below 0 or NaN: 0; from 1 on: 1 - 2^-24), kept[b] the list's length, logprob[b] = log(w(pick) / the sum).
  * The weights are formed to within 2^-36 of their size, in steps of 2^-43 of the
- * largest one, and summed exactly: a border of top_p or random is met unless it
- * lies closer than that, and results are the same bits each time.  A NaN in min_p or top_p is no rule.
+ * largest one, and summed exactly: a border of top_p or random is met unless a
+ * sum lies closer to it than these make of it (2^-36 of the sum, and 2^-44 of the
+ * largest weight for each of its tokens: one below that counts as 0), and results
+ * are the same bits each time.  A NaN in min_p or top_p is no rule.
  * A row in which nothing is above -inf, with a score of NaN or +inf, or with a
  * temperature below 0 or NaN has pick -1, kept 0 and logprob -inf.
  */
